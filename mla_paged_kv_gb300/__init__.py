@@ -434,3 +434,12 @@ def packed_sparse_decode(q, packed, topk, topk_length=None, softmax_scale=None, 
     if check:
         check_status(status, "mla_sparse_fp8_packed_decode_fwd")
     return out, lse
+
+
+# ---------------------------------------------------------------- operators around the decode
+
+from . import serving as _serving  # noqa: E402  (uses the names above)
+from .serving import *  # noqa: E402,F401,F403
+
+_SIGS.update(_serving.SERVING_SIGS)
+__all__ += _serving.__all__

@@ -11,6 +11,7 @@
 
 #include "mla_paged_kv.h"
 #include "common.cuh"
+#include "serving.cuh"
 
 namespace mla {
 cudaError_t launch_sched(const int32_t*, int, int, int, int32_t*, int32_t*, int, cudaStream_t);
@@ -415,6 +416,27 @@ int fp8_record_splits(const void* d_q, const void* d_kv, const int32_t* d_block_
 
 }  // namespace
 
+namespace mla {
+
+int device_ready(int* sms) {
+  const DeviceInfo& d = device_info();
+  if (d.status == MLA_OK) *sms = d.sms;
+  return d.status;
+}
+
+int encode_map16(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                 const cuuint32_t* box) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return MLA_ERR_CUDA;
+  const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, static_cast<cuuint32_t>(rank), const_cast<void*>(base),
+                        dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MLA_OK : MLA_ERR_INVALID_ARG;
+}
+
+}  // namespace mla
+
 extern "C" {
 
 const char* mla_status_string(int status) {
@@ -425,6 +447,7 @@ const char* mla_status_string(int status) {
     case MLA_ERR_CUDA: return "MLA_ERR_CUDA: a CUDA runtime call failed";
     case MLA_ERR_TIMEOUT: return "MLA_ERR_TIMEOUT: a device pipeline wait ran out of time";
     case MLA_ERR_BAD_INDEX: return "MLA_ERR_BAD_INDEX: block-table entry or sparse index outside the pool";
+    case MLA_ERR_NO_PAGES: return "MLA_ERR_NO_PAGES: no free pages left in the pool";
     default: return "unknown mla status";
   }
 }

@@ -1,0 +1,269 @@
+// C ABI of the serving operators (mla_serving.h): argument checks, tensor
+// maps and launches.  No device memory is allocated here.
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+#include "mla_serving.h"
+#include "common.cuh"
+#include "serving.cuh"
+
+using namespace mla;
+
+namespace {
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+cudaStream_t to_stream(mla_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
+int launched(cudaError_t e) { return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA; }
+
+constexpr long long kMaxInt = (1LL << 31) - 1;
+constexpr int kMaxRowPages = 1 << 18;  // pages of one block-table row: positions and sums stay in 32 bits
+
+// Checks common to the calls that take a page pool's bookkeeping.
+int page_state(int32_t* refcount, int num_pages, int32_t* table, int rows, int max_pages, int32_t* seqlens,
+               int32_t* status, PageState* s) {
+  if (!refcount || !table || !seqlens || !status) return MLA_ERR_INVALID_ARG;
+  if (num_pages < 1 || rows < 1 || max_pages < 1) return MLA_ERR_INVALID_ARG;
+  if (!aligned(refcount, 4) || !aligned(table, 4) || !aligned(seqlens, 4) || !aligned(status, 4))
+    return MLA_ERR_INVALID_ARG;
+  if (rows > kMaxPageRows || max_pages > kMaxRowPages) return MLA_ERR_UNSUPPORTED;
+  if (num_pages > (1 << 30)) return MLA_ERR_UNSUPPORTED;
+  *s = PageState{refcount, num_pages, table, rows, max_pages, seqlens, status};
+  return MLA_OK;
+}
+
+int check_list(const int32_t* a, const int32_t* b, int n) {
+  if (n < 0 || (n > 0 && (!a || !b)) || !aligned(a, 4) || !aligned(b, 4)) return MLA_ERR_INVALID_ARG;
+  return n > kMaxPageList ? MLA_ERR_UNSUPPORTED : MLA_OK;
+}
+
+int prompt_device() {
+  constexpr int kMaxDevices = 64;
+  static bool done[kMaxDevices] = {};
+  static std::mutex mu;
+  int sms = 0, dev = -1;
+  const int rc = device_ready(&sms);
+  if (rc != MLA_OK) return rc;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MLA_ERR_CUDA;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!done[dev]) {
+    if (prompt_setup() != cudaSuccess) {
+      cudaGetLastError();
+      return MLA_ERR_CUDA;
+    }
+    done[dev] = true;
+  }
+  return MLA_OK;
+}
+
+// [total, heads, dim] of 16-bit elements, viewed as (dim, heads, total); one
+// box = 64 dims of 128 rows of one head.
+int head_map(CUtensorMap* m, const void* base, long long total, int heads, int dim, long long token_stride,
+             long long head_stride) {
+  // a stride that no second index uses may be anything: take a legal one
+  if (heads == 1) head_stride = dim;
+  if (total == 1) token_stride = static_cast<long long>(heads) * head_stride;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(total)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_stride) * 2, static_cast<cuuint64_t>(token_stride) * 2};
+  const cuuint32_t box[3] = {64, 1, 128};
+  return encode_map16(m, base, 3, dims, strides, box);
+}
+
+// Strides of a [total, heads, dim] tensor: multiples of 8 elements, no
+// smaller than a row, within what a tensor map takes.
+bool good_strides(long long total, int heads, int dim, long long ts, long long hs) {
+  const long long most = 1LL << 38;
+  if (heads > 1 && (hs < dim || hs % 8 != 0 || hs > most)) return false;
+  return total <= 1 || (ts >= dim && ts % 8 == 0 && ts <= most);
+}
+
+}  // namespace
+
+extern "C" {
+
+int mla_cache_append(const void* d_c, long long c_stride, const void* d_r, long long r_stride, int in_dtype,
+                     int total_tokens, const int32_t* d_cu_seqlens, const int32_t* d_cache_seqlens, int batch,
+                     const int32_t* d_block_table, int max_pages, void* d_cache, int cache_dtype, int num_pages,
+                     const void* d_norm_weight, float norm_eps, const float* d_cos_sin, int max_pos,
+                     int rope_interleaved, const int32_t* d_refcount, int32_t* d_status, mla_stream_t stream) {
+  if (!d_cache_seqlens || !d_block_table || !d_cache || !d_status) return MLA_ERR_INVALID_ARG;
+  if (total_tokens < 0 || batch < 1 || max_pages < 1 || num_pages < 1) return MLA_ERR_INVALID_ARG;
+  if (total_tokens > 0 && (!d_c || !d_r)) return MLA_ERR_INVALID_ARG;
+  if (in_dtype != MLA_DTYPE_BF16 && in_dtype != MLA_DTYPE_FP16) return MLA_ERR_INVALID_ARG;
+  if (cache_dtype != in_dtype && cache_dtype != MLA_DTYPE_FP8_RECORD) return MLA_ERR_INVALID_ARG;
+  if (!d_cu_seqlens && total_tokens % batch != 0) return MLA_ERR_INVALID_ARG;
+  if (c_stride < 0 || r_stride < 0 || c_stride % 8 != 0 || r_stride % 8 != 0) return MLA_ERR_INVALID_ARG;
+  if (d_norm_weight && !(std::isfinite(norm_eps) && norm_eps >= 0.f)) return MLA_ERR_INVALID_ARG;
+  if (d_cos_sin && max_pos < 1) return MLA_ERR_INVALID_ARG;
+  if (!aligned(d_c, 16) || !aligned(d_r, 16) || !aligned(d_cache, 16) || !aligned(d_norm_weight, 16) ||
+      !aligned(d_cos_sin, 16) || !aligned(d_cu_seqlens, 4) || !aligned(d_cache_seqlens, 4) ||
+      !aligned(d_block_table, 4) || !aligned(d_refcount, 4) || !aligned(d_status, 4))
+    return MLA_ERR_INVALID_ARG;
+  if (max_pages > kMaxRowPages || num_pages > (1 << 30)) return MLA_ERR_UNSUPPORTED;
+  int sms = 0;
+  const int rc = device_ready(&sms);
+  if (rc != MLA_OK) return rc;
+  if (total_tokens == 0) return MLA_OK;
+  AppendParams p{};
+  p.c = static_cast<const uint16_t*>(d_c);
+  p.c_stride = c_stride;
+  p.r = static_cast<const uint16_t*>(d_r);
+  p.r_stride = r_stride;
+  p.total = total_tokens;
+  p.batch = batch;
+  p.cu = d_cu_seqlens;
+  p.seqlens = d_cache_seqlens;
+  p.table = d_block_table;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  p.cache = d_cache;
+  p.weight = static_cast<const uint16_t*>(d_norm_weight);
+  p.eps = norm_eps;
+  p.cos_sin = d_cos_sin;
+  p.max_pos = max_pos;
+  p.interleaved = rope_interleaved ? 1 : 0;
+  p.refcount = d_refcount;
+  p.status = d_status;
+  return launched(
+      launch_append(p, in_dtype == MLA_DTYPE_FP16, cache_dtype == MLA_DTYPE_FP8_RECORD, to_stream(stream)));
+}
+
+int mla_cache_grow(int32_t* d_refcount, int num_pages, int32_t* d_block_table, int rows, int max_pages,
+                   int32_t* d_seqlens, const int32_t* d_rows, const int32_t* d_new_tokens, int n, int32_t* d_status,
+                   mla_stream_t stream) {
+  PageState s;
+  int sms = 0, rc = page_state(d_refcount, num_pages, d_block_table, rows, max_pages, d_seqlens, d_status, &s);
+  if (rc == MLA_OK) rc = check_list(d_rows, d_new_tokens, n);
+  if (rc == MLA_OK) rc = device_ready(&sms);
+  if (rc != MLA_OK || n == 0) return rc;
+  return launched(launch_grow(s, d_rows, d_new_tokens, n, to_stream(stream)));
+}
+
+int mla_cache_fork(int32_t* d_refcount, int num_pages, int32_t* d_block_table, int rows, int max_pages,
+                   int32_t* d_seqlens, const int32_t* d_parents, const int32_t* d_children, int n, int32_t* d_pairs,
+                   int32_t* d_status, mla_stream_t stream) {
+  PageState s;
+  int sms = 0, rc = page_state(d_refcount, num_pages, d_block_table, rows, max_pages, d_seqlens, d_status, &s);
+  if (rc == MLA_OK) rc = check_list(d_parents, d_children, n);
+  if (rc == MLA_OK && ((n > 0 && !d_pairs) || !aligned(d_pairs, 8))) rc = MLA_ERR_INVALID_ARG;
+  if (rc == MLA_OK) rc = device_ready(&sms);
+  if (rc != MLA_OK || n == 0) return rc;
+  return launched(launch_fork(s, d_parents, d_children, n, d_pairs, to_stream(stream)));
+}
+
+int mla_cache_free(int32_t* d_refcount, int num_pages, int32_t* d_block_table, int rows, int max_pages,
+                   int32_t* d_seqlens, const int32_t* d_rows, int n, int32_t* d_status, mla_stream_t stream) {
+  PageState s;
+  int sms = 0, rc = page_state(d_refcount, num_pages, d_block_table, rows, max_pages, d_seqlens, d_status, &s);
+  if (rc == MLA_OK) rc = check_list(d_rows, d_rows, n);
+  if (rc == MLA_OK) rc = device_ready(&sms);
+  if (rc != MLA_OK || n == 0) return rc;
+  return launched(launch_free(s, d_rows, n, to_stream(stream)));
+}
+
+size_t mla_cache_compact_workspace_bytes(int num_pages) {
+  return num_pages < 1 || num_pages > (1 << 30) ? 0 : compact_workspace_bytes(num_pages);
+}
+
+int mla_cache_compact(int32_t* d_refcount, int num_pages, int32_t* d_block_table, int rows, int max_pages,
+                      const int32_t* d_seqlens, int32_t* d_pairs, int32_t* d_count, void* d_workspace,
+                      size_t workspace_bytes, int32_t* d_status, mla_stream_t stream) {
+  PageState s;
+  int sms = 0, rc = page_state(d_refcount, num_pages, d_block_table, rows, max_pages,
+                               const_cast<int32_t*>(d_seqlens), d_status, &s);
+  if (rc != MLA_OK) return rc;
+  if (!d_count || !d_workspace || (num_pages > 1 && !d_pairs)) return MLA_ERR_INVALID_ARG;
+  if (!aligned(d_pairs, 8) || !aligned(d_count, 4) || !aligned(d_workspace, 16)) return MLA_ERR_INVALID_ARG;
+  if (workspace_bytes < compact_workspace_bytes(num_pages)) return MLA_ERR_INVALID_ARG;
+  rc = device_ready(&sms);
+  if (rc != MLA_OK) return rc;
+  return launched(launch_compact(s, d_pairs, d_count, d_workspace, to_stream(stream)));
+}
+
+int mla_cache_copy_pages(void* d_pool, int layers, long long layer_stride, int num_pages, long long page_bytes,
+                         const int32_t* d_pairs, const int32_t* d_count, int n, int32_t* d_status,
+                         mla_stream_t stream) {
+  if (!d_pool || !d_status || n < 0 || (n > 0 && !d_pairs)) return MLA_ERR_INVALID_ARG;
+  if (layers < 1 || num_pages < 1 || page_bytes < 16 || page_bytes % 16 != 0 || layer_stride % 16 != 0)
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned(d_pool, 16) || !aligned(d_pairs, 8) || !aligned(d_count, 4) || !aligned(d_status, 4))
+    return MLA_ERR_INVALID_ARG;
+  if (page_bytes > (1LL << 30) || num_pages > (1 << 30) || layers > (1 << 16)) return MLA_ERR_UNSUPPORTED;
+  if (layers > 1 && layer_stride < page_bytes * num_pages) return MLA_ERR_INVALID_ARG;
+  int sms = 0;
+  const int rc = device_ready(&sms);
+  if (rc != MLA_OK || n == 0) return rc;
+  return launched(launch_copy_pages(d_pool, layers, layer_stride, num_pages, page_bytes, d_pairs, d_count, n,
+                                    d_status, sms, to_stream(stream)));
+}
+
+size_t mla_prompt_plan_bytes(int batch, int total_q) {
+  return batch < 1 || total_q < 0 ? 0 : prompt_plan_bytes(batch, total_q);
+}
+
+int mla_prompt_get_plan(const int32_t* d_cu_seqlens_q, const int32_t* d_cu_seqlens_k, int batch, int total_q,
+                        int total_k, int causal, void* d_plan, size_t plan_bytes, int32_t* d_status,
+                        mla_stream_t stream) {
+  if (!d_cu_seqlens_q || !d_plan || !d_status || batch < 1 || total_q < 0 || total_k < 0) return MLA_ERR_INVALID_ARG;
+  if (!d_cu_seqlens_k && total_k != total_q) return MLA_ERR_INVALID_ARG;
+  if (!aligned(d_cu_seqlens_q, 4) || !aligned(d_cu_seqlens_k, 4) || !aligned(d_plan, 16) || !aligned(d_status, 4))
+    return MLA_ERR_INVALID_ARG;
+  if (total_q > (1 << 30) || total_k > (1 << 30) || batch > (1 << 20)) return MLA_ERR_UNSUPPORTED;
+  if (plan_bytes < prompt_plan_bytes(batch, total_q)) return MLA_ERR_INVALID_ARG;
+  int sms = 0;
+  const int rc = device_ready(&sms);
+  if (rc != MLA_OK) return rc;
+  return launched(launch_prompt_plan(d_cu_seqlens_q, d_cu_seqlens_k ? d_cu_seqlens_k : d_cu_seqlens_q, batch, total_q,
+                                     total_k, causal ? 1 : 0, d_plan, d_status, to_stream(stream)));
+}
+
+int mla_prompt_attention_fwd(const void* d_q, long long q_token_stride, long long q_head_stride, const void* d_k,
+                             long long k_token_stride, long long k_head_stride, const void* d_v,
+                             long long v_token_stride, long long v_head_stride, int dtype, int total_q, int total_k,
+                             int batch, int h_q, int h_kv, int d_qk, float softmax_scale, const void* d_plan,
+                             size_t plan_bytes, void* d_out, float* d_lse, int32_t* d_status, mla_stream_t stream) {
+  if (!d_plan || !d_status || batch < 1 || total_q < 0 || total_k < 0 || h_q < 1 || h_kv < 1 || h_q % h_kv != 0)
+    return MLA_ERR_INVALID_ARG;
+  if (total_q > 0 && (!d_q || !d_out || !d_lse)) return MLA_ERR_INVALID_ARG;
+  if (total_k > 0 && (!d_k || !d_v)) return MLA_ERR_INVALID_ARG;
+  if (dtype != MLA_DTYPE_BF16 && dtype != MLA_DTYPE_FP16) return MLA_ERR_INVALID_ARG;
+  if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.f)) return MLA_ERR_INVALID_ARG;
+  if (!aligned(d_q, 16) || !aligned(d_k, 16) || !aligned(d_v, 16) || !aligned(d_plan, 16) || !aligned(d_out, 16) ||
+      !aligned(d_lse, 4) || !aligned(d_status, 4))
+    return MLA_ERR_INVALID_ARG;
+  if (!good_strides(total_q, h_q, d_qk, q_token_stride, q_head_stride) ||
+      !good_strides(total_k, h_kv, d_qk, k_token_stride, k_head_stride) ||
+      !good_strides(total_k, h_kv, 128, v_token_stride, v_head_stride))
+    return MLA_ERR_INVALID_ARG;
+  if (d_qk != 192 && d_qk != 128) return MLA_ERR_UNSUPPORTED;
+  if (total_q > (1 << 30) || total_k > (1 << 30) || batch > (1 << 20)) return MLA_ERR_UNSUPPORTED;
+  if (plan_bytes < prompt_plan_bytes(batch, total_q)) return MLA_ERR_INVALID_ARG;
+  const int tiles = prompt_plan_tiles(batch, total_q);
+  if (static_cast<long long>(tiles) * h_q > kMaxInt) return MLA_ERR_UNSUPPORTED;
+  const int rc0 = prompt_device();
+  if (rc0 != MLA_OK || total_q == 0) return rc0;
+  PromptParams p{};
+  p.plan = static_cast<const int32_t*>(d_plan);
+  p.max_tiles = tiles;
+  p.h_q = h_q;
+  p.group = h_q / h_kv;
+  p.total_q = total_q;
+  p.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * 1.4426950408889634);
+  p.out = d_out;
+  p.lse = d_lse;
+  p.status = d_status;
+  CUtensorMap qm, km, vm;
+  int rc = head_map(&qm, d_q, total_q, h_q, d_qk, q_token_stride, q_head_stride);
+  // without any key no CTA loads K or V: any valid map serves
+  if (rc == MLA_OK)
+    rc = total_k > 0 ? head_map(&km, d_k, total_k, h_kv, d_qk, k_token_stride, k_head_stride)
+                     : head_map(&km, d_q, total_q, h_q, d_qk, q_token_stride, q_head_stride);
+  if (rc == MLA_OK)
+    rc = total_k > 0 ? head_map(&vm, d_v, total_k, h_kv, 128, v_token_stride, v_head_stride)
+                     : head_map(&vm, d_q, total_q, h_q, d_qk, q_token_stride, q_head_stride);
+  if (rc != MLA_OK) return rc;
+  return launched(launch_prompt(qm, km, vm, p, dtype == MLA_DTYPE_FP16, d_qk, to_stream(stream)));
+}
+
+}  // extern "C"

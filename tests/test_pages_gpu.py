@@ -1,0 +1,257 @@
+"""Page operations against plain lists of whole numbers: exact."""
+
+import random
+
+import numpy as np
+import pytest
+import torch
+
+import mla_paged_kv_gb300 as mla
+from oracle import serving_oracle as so
+
+pytestmark = pytest.mark.gpu
+
+BAD_INDEX, NO_PAGES = 5, 6
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+class State:
+    """A random pool on the GPU and its restatement."""
+
+    def __init__(self, rows, max_len, pages, seed, empty_rows=0, width=None):
+        rng = random.Random(seed)
+        lens = [rng.randint(0, max_len) for _ in range(rows)] + [0] * empty_rows
+        width = width or -(-max_len // 64) + 3
+        perm = list(range(pages))
+        rng.shuffle(perm)
+        table = np.full((rows + empty_rows, width), -1, dtype=np.int32)
+        ref = np.zeros(pages, dtype=np.int32)
+        for r, n in enumerate(lens):
+            for j in range(-(-n // 64)):
+                table[r, j] = perm.pop()
+                ref[table[r, j]] = 1
+        self.ref, self.table, self.lens = i32(ref), torch.from_numpy(table).cuda(), i32(lens)
+        self.host = so.Pool(ref, table, lens)
+        self.status = i32([0])
+
+    def same(self):
+        assert self.ref.tolist() == self.host.ref
+        assert self.lens.tolist() == self.host.lens
+        assert self.table.tolist() == self.host.table
+        code = int(self.status)
+        assert (code != 0) == (self.host.bad or self.host.empty)
+        if code:
+            assert (code == BAD_INDEX and self.host.bad) or (code == NO_PAGES and self.host.empty)
+
+    def grow(self, rows, new):
+        self.host.grow(rows, new)
+        mla.cache_grow(self.ref, self.table, self.lens, i32(rows), i32(new), status=self.status)
+        self.same()
+
+    def fork(self, parents, children):
+        want = self.host.fork(parents, children)
+        got = mla.cache_fork(self.ref, self.table, self.lens, i32(parents), i32(children), status=self.status)
+        assert [tuple(p) for p in got.tolist()] == want
+        self.same()
+
+    def free(self, rows):
+        self.host.free(rows)
+        mla.cache_free(self.ref, self.table, self.lens, i32(rows), status=self.status)
+        self.same()
+
+    def compact(self):
+        want = self.host.compact()
+        pairs, count = mla.cache_compact(self.ref, self.table, self.lens, status=self.status)
+        got = [tuple(p) for p in pairs.tolist()]
+        assert int(count) == len(want) and got[:len(want)] == want
+        assert all(p == (-1, -1) for p in got[len(want):])
+        self.same()
+
+
+@pytest.mark.parametrize("pages", [64, 1023, 8192, 8193, 20000])
+def test_grow_takes_the_lowest_free_pages(pages):
+    s = State(9, 250, pages, seed=pages)
+    s.grow([3, 0, 8], [64, 1, 130])
+    s.grow([5], [0])
+    s.grow(list(range(9)), [7 * i for i in range(9)])
+
+
+def test_grow_many_rows():
+    s = State(3000, 64, 9000, seed=1, width=5)
+    s.grow(list(range(0, 3000, 2)), [i % 140 for i in range(1500)])
+    s.grow(list(range(3000)), [1] * 3000)
+
+
+def test_grow_until_the_pool_is_empty():
+    s = State(6, 100, 20, seed=2, width=30)
+    free = s.host.ref.count(0)
+    s.grow([0], [64 * (free - 1)])
+    assert not s.host.empty
+    # the first needs none, the second more than is left, the third none, the fourth one
+    s.grow([1, 2, 3, 4], [0, 64 * 5, 0, 64])
+    assert s.host.empty and s.host.ref.count(0) >= 1
+
+
+@pytest.mark.parametrize("rows,new", [([0, 1, 0], [5, 5, 5]), ([-1, 2], [5, 5]), ([7, 2], [5, 5]), ([1, 2], [-1, 5]),
+                                      ([1, 2], [10 ** 6, 5]), ([1, 2], [2 ** 31 - 1, 5])])
+def test_grow_refuses_bad_entries_only(rows, new):
+    s = State(4, 200, 100, seed=3)
+    s.grow(rows, new)
+    assert s.host.bad
+
+
+def test_fork_shares_full_pages_and_copies_the_tail():
+    s = State(5, 400, 200, seed=4, empty_rows=9)
+    s.fork([0, 1, 1, 1, 4], [5, 6, 7, 8, 9])
+    s.fork([5, 2], [10, 11])          # a fork of a fork
+    s.grow([5, 6, 7], [1, 64, 100])
+    s.free([1, 6])
+    s.fork([7], [1])                  # into a freed row
+    s.free(list(range(14)))
+    assert not any(s.host.ref)
+
+
+@pytest.mark.parametrize("length", [0, 1, 63, 64, 65, 128])
+def test_fork_lengths(length):
+    s = State(1, 0, 10, seed=5, empty_rows=3, width=4)
+    s.grow([0], [length])
+    s.fork([0, 0], [1, 3])
+
+
+@pytest.mark.parametrize("parents,children", [([0, 0], [4, 4]), ([0, 4], [4, 5]), ([0, 1], [1, 4]), ([0, 0], [0, 4]),
+                                              ([-1, 0], [4, 5]), ([9, 0], [4, 5]), ([0, 0], [6, 5]),
+                                              ([0, 0], [-2, 5])])
+def test_fork_refuses_bad_entries_only(parents, children):
+    s = State(4, 200, 100, seed=6, empty_rows=2)
+    s.grow([0, 1], [65, 65])  # neither is empty
+    s.fork(parents, children)
+    assert s.host.bad
+
+
+def test_fork_without_pages():
+    s = State(1, 0, 5, seed=7, empty_rows=6, width=8)
+    s.grow([0], [100])
+    s.fork([0] * 5, [1, 2, 3, 4, 5])
+    assert s.host.empty and s.host.lens == [100, 100, 100, 100, 0, 0, 0]
+
+
+def test_free_twice_and_bad_rows():
+    s = State(4, 200, 60, seed=8)
+    s.free([1, 1, 1])
+    assert not s.host.bad
+    s.free([1])
+    s.free([7, 0, -1])
+    assert s.host.bad
+
+
+def test_free_reports_pages_that_are_free_already():
+    s = State(2, 200, 30, seed=9, empty_rows=1)
+    s.host.lens[2], s.host.table[2][0] = 40, s.host.ref.index(0)
+    s.lens, s.table = i32(s.host.lens), torch.tensor(s.host.table, dtype=torch.int32, device="cuda")
+    s.free([2])
+    assert s.host.bad
+
+
+@pytest.mark.parametrize("pages,rows,max_len", [(1, 0, 0), (2, 1, 64), (3, 2, 64), (100, 6, 300), (4096, 40, 900),
+                                                (4097, 200, 900), (13000, 400, 1500)])
+def test_compact(pages, rows, max_len):
+    s = State(max(rows, 1), max_len, pages, seed=pages)
+    if rows > 3:
+        s.free([0])
+        s.fork([1, 2], [0] + ([] if rows < 4 else [0]))  # the second is refused: same child
+        s.status.zero_()
+        s.host.bad = False
+    s.compact()
+    live = [c for c in s.host.ref if c]
+    assert s.host.ref[:len(live)] == live
+    s.compact()  # nothing left to move
+
+
+def test_compact_full_and_empty_pools():
+    s = State(1, 0, 50, seed=11)
+    s.compact()
+    s.grow([0], [64 * 3])
+    s.compact()
+    s = State(1, 64 * 50, 50, seed=12, width=60)
+    s.grow([0], [64 * s.host.ref.count(0)])
+    s.compact()
+
+
+def test_compact_reports_entries_that_name_free_pages():
+    s = State(3, 200, 40, seed=13)
+    s.host.lens[0] = s.host.lens[0] // 64 * 64 + 1  # its last entry: a free page, or none
+    row = s.host.table[0]
+    row[(s.host.lens[0] - 1) // 64] = -1
+    s.lens, s.table = i32(s.host.lens), torch.tensor(s.host.table, dtype=torch.int32, device="cuda")
+    s.compact()
+    assert s.host.bad
+
+
+# ------------------------------------------------------------------ copy
+
+
+def pool_of(shape, dtype, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    if dtype == torch.uint8:
+        return torch.randint(0, 256, shape, dtype=dtype, device="cuda", generator=g)
+    return torch.randn(shape, device="cuda", generator=g).to(dtype)
+
+
+def check_copy(pool, pairs, layered, count=None):
+    want = pool.clone()
+    flat = want if layered else want[None]
+    used = pairs if count is None else pairs[:count]
+    done, bad = so.copy_pairs(used, flat.shape[1])
+    before = flat.clone()
+    for a, b in done:
+        flat[:, b] = before[:, a]
+    status = i32([0])
+    mla.cache_copy_pages(pool, i32(pairs).reshape(-1, 2), None if count is None else i32([count]), layered, status)
+    assert torch.equal(pool, want)
+    assert int(status) == (BAD_INDEX if bad else 0)
+
+
+@pytest.mark.parametrize("shape,dtype,layered", [
+    ((40, 64, 576), torch.bfloat16, False), ((40, 64, 656), torch.uint8, False), ((3, 40, 64, 656), torch.uint8, True),
+    ((2, 40, 64, 576), torch.float16, True), ((40, 64, 2, 576), torch.bfloat16, False), ((5, 40, 8), torch.float32, True)])
+def test_copy_pages(shape, dtype, layered):
+    pool = pool_of(shape, dtype, 1)
+    check_copy(pool, [(0, 39), (3, 5), (-1, -1), (3, 6), (7, 7), (30, 1)], layered)
+
+
+def test_copy_layers_with_a_gap():
+    whole = pool_of((3, 21, 64, 576), torch.bfloat16, 2)
+    keep = whole[:, 20].clone()
+    check_copy(whole[:, :20], [(1, 2), (3, 4)], True)
+    assert torch.equal(whole[:, 20], keep)
+
+
+@pytest.mark.parametrize("pairs", [[(0, 1), (2, 1)], [(0, 1), (1, 2)], [(0, 1), (1, 0)], [(0, 40)], [(-1, 3), (4, 5)],
+                                   [(5, -7), (4, 6)], [(1, 1), (0, 1)], [(0, 1), (0, 1), (0, 2)]])
+def test_copy_refuses_what_would_depend_on_order(pairs):
+    check_copy(pool_of((2, 40, 64, 16), torch.bfloat16, 3), pairs, True)
+
+
+@pytest.mark.parametrize("count", [0, 1, 5, 99])
+def test_copy_count_on_the_device(count):
+    check_copy(pool_of((60, 64, 16), torch.bfloat16, 4), [(i, 30 + i) for i in range(8)], False, count)
+
+
+def test_copy_many_pairs():
+    n = 3000
+    order = torch.randperm(2 * n, generator=torch.Generator().manual_seed(5)).tolist()
+    check_copy(pool_of((2, 2 * n, 64, 4), torch.float16, 6), list(zip(order[:n], order[n:])), True)
+
+
+def test_copy_past_32_bits():
+    pages = (1 << 32) // (64 * 1152) + 40
+    pool = torch.zeros(pages, 64, 576, dtype=torch.bfloat16, device="cuda")
+    pool[pages - 1] = 3
+    mla.cache_copy_pages(pool, i32([[pages - 1, pages - 2], [pages - 1, 2]]))
+    assert torch.all(pool[pages - 2] == 3) and torch.all(pool[2] == 3)
+    pool[pages - 2:] = 0
+    pool[2] = 0
+    assert not pool.any()
