@@ -17,7 +17,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libmla_paged_kv.so")
 SOURCES = ["api.cu", "sched.cu", "combine.cu", "decode_dense.cu", "decode_sparse.cu", "static_ws.cu",
-           "append.cu", "pages.cu", "prompt.cu", "serving_api.cu"]
+           "append.cu", "pages.cu", "prompt.cu", "shared_prefix.cu",
+           "serving_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

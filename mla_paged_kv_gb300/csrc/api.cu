@@ -104,7 +104,7 @@ const DeviceInfo& device_info() {
   for (int stall = 0; stall < 2; ++stall)
     attr_ok = attr_ok && cudaFuncSetAttribute(sparse_kernel_ptr(stall), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                               sparse_smem_bytes()) == cudaSuccess;
-  for (int kind = 0; kind < 5; ++kind)
+  for (int kind = 0; kind < 7; ++kind)
     attr_ok = attr_ok && cudaFuncSetAttribute(dense_kernel_ptr(kind), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                               dense_smem_bytes()) == cudaSuccess;
   attr_ok = attr_ok && cudaFuncSetAttribute(combine_stream_kernel_ptr(), cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -417,6 +417,43 @@ int fp8_record_splits(const void* d_q, const void* d_kv, const int32_t* d_block_
 }  // namespace
 
 namespace mla {
+
+// The shared-prefix launch of the dense kernel: n_units units of 128 rows.
+int launch_shared(const SharedLaunch& c, cudaStream_t stream) {
+  CUtensorMap qm, km, sm, rm;
+  int rc = encode_q_map(&qm, c.q, c.total_rows);
+  if (rc == MLA_OK) rc = encode_kv_map(&km, c.kv, c.num_pages, 1, 4);
+  if (rc == MLA_OK) rc = encode_kv_map(&sm, c.kv, c.num_pages, 1, 5);
+  if (rc == MLA_OK) rc = encode_kv_map(&rm, c.kv, c.num_pages, 1, 1);
+  if (rc != MLA_OK) return rc;
+  DecodeParams p{};
+  p.lengths = c.lengths;
+  p.n_units = c.n_units;
+  p.rows = MLA_ROWS_PER_BLOCK;
+  p.row_blocks = 1;
+  p.h_q = c.h_q;
+  p.s_q = c.s_q;
+  p.h_kv = 1;
+  p.group_heads = c.h_q;
+  p.blocks_per_group = 1;
+  p.scale_log2 = c.scale_log2;
+  p.block_table = c.block_table;
+  p.num_pages = c.num_pages;
+  p.units = c.units;
+  p.sched = c.sched;
+  p.split_offset = c.split_offset;
+  p.num_parts = c.num_parts;
+  p.o_accum = c.o_accum;
+  p.lse_accum = c.lse_accum;
+  p.out_type = MLA_DTYPE_FP32;
+  p.status = c.status;
+  return launch_dense(qm, km, sm, rm, p, c.num_parts, c.half ? 6 : 5, stream) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+cudaError_t launch_plan(const int32_t* lengths, int n_units, int num_parts, int32_t* sched, int32_t* split_offset,
+                        cudaStream_t stream) {
+  return launch_sched(lengths, 0, n_units, num_parts, sched, split_offset, 0, stream);
+}
 
 int device_ready(int* sms) {
   const DeviceInfo& d = device_info();

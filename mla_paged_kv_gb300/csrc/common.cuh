@@ -22,6 +22,18 @@ __host__ __device__ __forceinline__ int ceil_div_i(int a, int b) { return (a + b
 
 __device__ __forceinline__ int num_tiles(int len) { return len > 0 ? ceil_div_i(len, kTile) : 0; }
 
+// One unit of a shared-prefix plan: up to 128 consecutive query rows and the
+// run of keys they all read (a 128-row block over the shared pages, or a
+// block of one request's rows over the pages behind them).
+struct SharedUnit {
+  int row0;       // first query row, of batch * s_q * h_q
+  int rows;       // query rows
+  int rel;        // row0's place among its request's rows (causal), or -1: every key is visible
+  int table_off;  // its first page's entry, from the block table's start
+  int avail;      // entries of the block-table row from there on
+};
+constexpr int kUnitInts = 8;
+
 // Everything the split-KV attention kernels read besides the tensor maps.
 struct DecodeParams {
   // keys per unit (dense: cache_seqlens, sparse: topk_length or NULL)
@@ -55,6 +67,9 @@ struct DecodeParams {
   // block-table row b / unit_request_div (s_q when a unit is one query token
   // of a request, 1 when it is the whole request)
   int unit_request_div;
+  // shared-prefix plan (dense kernel, kShared): what each unit is, kUnitInts
+  // int32 each (SharedUnit); rows = 128, a unit's rows being its own count
+  const int32_t* units;
   // schedule
   const int32_t* sched;
   const int32_t* split_offset;

@@ -255,14 +255,25 @@ __device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity
   return __all_sync(0xffffffffu, mbar_wait<true>(bar, parity, abort_flag, limit_ns));
 }
 
+__device__ __forceinline__ SharedUnit load_unit(const DecodeParams& p, int u) {
+  const int32_t* e = p.units + u * kUnitInts;
+  return SharedUnit{e[0], e[1], e[2], e[3], e[4]};
+}
+
 // Page ids of 32 consecutive pages of unit c.b starting at `base`, one per lane
 // (0 past the partition's range; ids outside the pool are reported and read
 // as page 0, whose keys the softmax then masks).
+template <bool kShared>
 __device__ __forceinline__ int load_page_window(const DecodeParams& p, const Cursor& c, int base, int lane) {
   const int kk = base + lane;
   int pg = 0;
   if (kk < c.hi) {
-    pg = kk < p.max_pages ? p.block_table[static_cast<size_t>(c.b) * p.max_pages + kk] : -1;
+    if constexpr (kShared) {
+      const SharedUnit su = load_unit(p, c.b);
+      pg = kk < su.avail ? p.block_table[su.table_off + kk] : -1;
+    } else {
+      pg = kk < p.max_pages ? p.block_table[static_cast<size_t>(c.b) * p.max_pages + kk] : -1;
+    }
     if (pg < 0 || pg >= p.num_pages) {
       report(p.status, MLA_ERR_BAD_INDEX);
       pg = -1;
@@ -361,7 +372,11 @@ __device__ __forceinline__ float ref_alpha(float r_old, float r_new) {
 // kHalf: Q and KV are fp16 (else bf16).  The three maps view the 16-bit
 // pool with boxes of 4, 5 and 1 consecutive 64-dim slices (kv_map, sc_map,
 // rope_map).
-template <bool kHalf, bool kQV, bool kStall>
+// kShared: units come from a shared-prefix plan (p.units): 128-row blocks of
+// all requests' queries over the pages they share, and each request's own
+// rows over the rest; one row block a unit, always split partials (128 rows a
+// slot), merged across both kinds of units by the shared-prefix combine.
+template <bool kHalf, bool kQV, bool kStall, bool kShared = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     dense_decode_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kv_map,
                         const __grid_constant__ CUtensorMap sc_map, const __grid_constant__ CUtensorMap rope_map,
@@ -480,7 +495,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (c.b != cur_b || c.k - page_base >= 32) {
           cur_b = c.b;
           page_base = c.k;
-          page_reg = load_page_window(p, c, page_base, lane);
+          page_reg = load_page_window<kShared>(p, c, page_base, lane);
         }
         const int page_raw = __shfl_sync(0xffffffffu, page_reg, c.k - page_base);
         const int page = max(page_raw, 0);  // a page outside the pool (-1) reads page 0
@@ -561,7 +576,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // box j of unit b into dst; into L2 only when bar is null
       auto q_box = [&](int b, int j, uint8_t* dst, uint64_t* bar) {
         if (p.h_kv == 1) {
-          const int row0 = b * p.rows + rb * kRowsPerBlock;
+          const int row0 = kShared ? p.units[b * kUnitInts] : b * p.rows + rb * kRowsPerBlock;
           if (bar)
             tma_load_2d(dst, &q_map, bar, 64 * j, row0, pol_q);
           else
@@ -620,7 +635,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       auto q_box = [&](int b, int j, uint64_t* bar) {
         uint8_t* dst = sQ + (j % kQSmemBoxes) * kQBoxBytes;
         if (p.h_kv == 1) {
-          const int row0 = b * p.rows + rb * kRowsPerBlock;
+          const int row0 = kShared ? p.units[b * kUnitInts] : b * p.rows + rb * kRowsPerBlock;
           if (bar)
             tma_load_2d(dst, &q_map, bar, 64 * j, row0, pol_q);
           else
@@ -869,8 +884,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t taddr = tmem + lane_base;
     const uint32_t swz = static_cast<uint32_t>(r & 7);
     int qrow, tok;
-    const bool row_ok = block_row(p, grp, rb, r, qrow, tok);
+    bool row_ok = kShared || block_row(p, grp, rb, r, qrow, tok);
     if (!row_ok) tok = 0;
+    SharedUnit su{};
     const float c_log2 = p.scale_log2;
     // the peer's buffers and barriers this warp sends to
     const uint32_t peer_p = mapa_shared(smem_u32(sPRecv + warp * kWarpPBytes), peer);
@@ -895,11 +911,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (first) {
         r_cur = -INFINITY;
         l_own = 0.f;
+        if constexpr (kShared) {
+          su = load_unit(p, c.b);
+          qrow = r;
+          row_ok = r < su.rows;
+          tok = row_ok && su.rel >= 0 ? (su.rel + r) / p.h_q : p.s_q - 1;
+        }
       }
       float alpha;
       if (mine) {
         // ---- own tile: scores, reference, P
-        const int jmax = p.causal ? (c.L - p.s_q + tok) : (c.L - 1);  // last visible key
+        // last visible key (kShared: tok = s_q - 1 where every key is visible)
+        const int jmax = kShared || p.causal ? (c.L - p.s_q + tok) : (c.L - 1);
         const int vis = jmax - c.k * kT;                                // keys 0..vis of this tile are visible
         uint64_t keep = (vis >= kT - 1 ? ~0ull : (vis < 0 ? 0ull : (~0ull >> (kT - 1 - vis))));
         ok = warp_wait(&bars[S_FULL], own_i & 1, abort_flag, kWaitNs);
@@ -1064,7 +1087,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int nsplit = p.split_offset[b_here + 1] - s_begin;
       const int slot = s_begin + ((b_here == P.b0) ? P.s0 : 0);
       const float inv_l = l_sum > 0.f ? 1.f / l_sum : 0.f;
-      const bool direct = (nsplit == 1);
+      const bool direct = !kShared && nsplit == 1;
       const bool bf16_out = direct && p.out_type != MLA_DTYPE_FP32;  // a 16-bit output (bf16 or fp16)
       const bool fp16_out = p.out_type == MLA_DTYPE_FP16;
       // O half -> global through that buffer: each thread stages its row's
@@ -1105,7 +1128,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int flat = tid + 128 * i;
           const int rr = flat >> 3, cc = flat & 7;
           int rg, rtok;
-          if (!block_row(p, grp, rb, rr, rg, rtok)) continue;
+          if constexpr (kShared) {
+            rg = rr;
+            if (rr >= su.rows) continue;
+          } else if (!block_row(p, grp, rb, rr, rg, rtok)) {
+            continue;
+          }
           const uint4 val =
               *reinterpret_cast<const uint4*>(stage + rr * 128 + ((static_cast<uint32_t>(cc ^ (rr & 7))) << 4));
           const size_t e = (base_row + rg) * kDv + 256u * rank + static_cast<size_t>(ch) * chunk_cols;
@@ -1157,7 +1185,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 int dense_smem_bytes() { return dn::kSmemBytes; }
 // kind 0: bf16, 1: fp16, 2: bf16 with the V-ring Q stage, 3: fp16 with it,
 // 4: the bf16 stall-test instance (its first own tile's K slot is never
-// loaded, so a wait runs out and the kernel reports MLA_ERR_TIMEOUT)
+// loaded, so a wait runs out and the kernel reports MLA_ERR_TIMEOUT),
+// 5, 6: bf16, fp16 under a shared-prefix plan
 int dense_threads(int) { return dn::kThreads; }
 const void* dense_kernel_ptr(int kind) {
   switch (kind) {
@@ -1165,6 +1194,8 @@ const void* dense_kernel_ptr(int kind) {
     case 2: return reinterpret_cast<const void*>(&dn::dense_decode_kernel<false, true, false>);
     case 3: return reinterpret_cast<const void*>(&dn::dense_decode_kernel<true, true, false>);
     case 4: return reinterpret_cast<const void*>(&dn::dense_decode_kernel<false, false, true>);
+    case 5: return reinterpret_cast<const void*>(&dn::dense_decode_kernel<false, false, false, true>);
+    case 6: return reinterpret_cast<const void*>(&dn::dense_decode_kernel<true, false, false, true>);
     default: return reinterpret_cast<const void*>(&dn::dense_decode_kernel<false, false, false>);
   }
 }
@@ -1188,6 +1219,14 @@ cudaError_t launch_dense(const CUtensorMap& q_map, const CUtensorMap& kv_map, co
       break;
     case 4:
       dn::dense_decode_kernel<false, false, true>
+          <<<grid, dn::kThreads, dn::kSmemBytes, stream>>>(q_map, kv_map, sc_map, rope_map, p);
+      break;
+    case 5:
+      dn::dense_decode_kernel<false, false, false, true>
+          <<<grid, dn::kThreads, dn::kSmemBytes, stream>>>(q_map, kv_map, sc_map, rope_map, p);
+      break;
+    case 6:
+      dn::dense_decode_kernel<true, false, false, true>
           <<<grid, dn::kThreads, dn::kSmemBytes, stream>>>(q_map, kv_map, sc_map, rope_map, p);
       break;
     default:

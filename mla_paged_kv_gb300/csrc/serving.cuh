@@ -15,6 +15,31 @@ int device_ready(int* sms);
 int encode_map16(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
                  const cuuint32_t* box);
 
+// The dense decode kernel over the units of a shared-prefix plan, and the
+// scheduler over unit lengths (both with the decode's own code).
+struct SharedLaunch {
+  const void* q;
+  const void* kv;
+  long long total_rows;  // batch * s_q * h_q
+  int num_pages, n_units, s_q, h_q, num_parts;
+  bool half;
+  float scale_log2;
+  const int32_t *block_table, *units, *lengths, *sched, *split_offset;
+  float *o_accum, *lse_accum;  // [slots][128][512], [slots][128]
+  int32_t* status;
+};
+int launch_shared(const SharedLaunch& c, cudaStream_t stream);
+cudaError_t launch_plan(const int32_t* lengths, int n_units, int num_parts, int32_t* sched, int32_t* split_offset,
+                        cudaStream_t stream);
+
+cudaError_t launch_shared_units(const int32_t* block_table, int max_pages, const int32_t* seqlens, int batch,
+                                int s_q, int h_q, int causal, int share, int32_t* units, int32_t* lengths,
+                                cudaStream_t st);
+cudaError_t launch_shared_combine(const float* o_accum, const float* lse_accum, const int32_t* split_offset,
+                                  int batch, int rows, int share, void* out, int out_type, float* lse, int sms,
+                                  cudaStream_t st);
+constexpr int kMaxSharedParts = 1024;  // partitions of a shared-prefix plan
+
 struct AppendParams {
   const uint16_t* c;
   long long c_stride;

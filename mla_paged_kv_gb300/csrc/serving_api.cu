@@ -78,6 +78,39 @@ bool good_strides(long long total, int heads, int dim, long long ts, long long h
   return total <= 1 || (ts >= dim && ts % 8 == 0 && ts <= most);
 }
 
+// Sizes of a shared-prefix batch, and where its plan's and workspace's parts
+// lie (each from a 256-byte boundary).
+struct SharedSizes {
+  int share;      // 1: a prefix is attended together
+  int units;      // at most: prefix blocks, then the requests' own
+  long long rows;  // batch * s_q * h_q
+  size_t lengths_off, offset_off, sched_off, plan_bytes;
+  size_t lse_off, ws_bytes;
+};
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+int shared_sizes(int batch, int s_q, int h_q, int num_parts, SharedSizes* z) {
+  if (batch < 1 || s_q < 1 || h_q < 1 || num_parts < 1) return MLA_ERR_INVALID_ARG;
+  const long long per_request = static_cast<long long>(s_q) * h_q;
+  z->rows = per_request * batch;
+  if (per_request > (1 << 20) || batch > 65535 || z->rows > kMaxInt || num_parts > kMaxSharedParts)
+    return MLA_ERR_UNSUPPORTED;
+  const long long own = batch * ((per_request + MLA_ROWS_PER_BLOCK - 1) / MLA_ROWS_PER_BLOCK);
+  const long long front = (z->rows + MLA_ROWS_PER_BLOCK - 1) / MLA_ROWS_PER_BLOCK;
+  z->share = front < own;
+  const long long units = own + (z->share ? front : 0);
+  z->units = static_cast<int>(units);
+  z->lengths_off = up256(static_cast<size_t>(units) * kUnitInts * 4);
+  z->offset_off = z->lengths_off + up256(static_cast<size_t>(units) * 4);
+  z->sched_off = z->offset_off + up256(static_cast<size_t>(units + 1) * 4);
+  z->plan_bytes = z->sched_off + up256(static_cast<size_t>(num_parts) * MLA_SCHED_INTS * 4);
+  const size_t slots = static_cast<size_t>(units) + num_parts;
+  z->lse_off = slots * MLA_ROWS_PER_BLOCK * MLA_D_V * 4;
+  z->ws_bytes = z->lse_off + slots * MLA_ROWS_PER_BLOCK * 4;
+  return MLA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -264,6 +297,92 @@ int mla_prompt_attention_fwd(const void* d_q, long long q_token_stride, long lon
                      : head_map(&vm, d_q, total_q, h_q, d_qk, q_token_stride, q_head_stride);
   if (rc != MLA_OK) return rc;
   return launched(launch_prompt(qm, km, vm, p, dtype == MLA_DTYPE_FP16, d_qk, to_stream(stream)));
+}
+
+size_t mla_shared_prefix_plan_bytes(int batch, int s_q, int h_q, int num_parts) {
+  SharedSizes z;
+  return shared_sizes(batch, s_q, h_q, num_parts, &z) == MLA_OK ? z.plan_bytes : 0;
+}
+
+size_t mla_shared_prefix_workspace_bytes(int batch, int s_q, int h_q, int num_parts) {
+  SharedSizes z;
+  return shared_sizes(batch, s_q, h_q, num_parts, &z) == MLA_OK ? z.ws_bytes : 0;
+}
+
+int mla_shared_prefix_get_plan(const int32_t* d_block_table, int max_pages, const int32_t* d_cache_seqlens, int batch,
+                               int s_q, int h_q, int causal, int num_parts, void* d_plan, size_t plan_bytes,
+                               mla_stream_t stream) {
+  if (!d_block_table || !d_cache_seqlens || !d_plan || max_pages < 1) return MLA_ERR_INVALID_ARG;
+  if (!aligned(d_block_table, 4) || !aligned(d_cache_seqlens, 4) || !aligned(d_plan, 16)) return MLA_ERR_INVALID_ARG;
+  SharedSizes z;
+  int rc = shared_sizes(batch, s_q, h_q, num_parts, &z);
+  if (rc != MLA_OK) return rc;
+  if (max_pages > kMaxRowPages || static_cast<long long>(batch) * max_pages > kMaxInt) return MLA_ERR_UNSUPPORTED;
+  if (plan_bytes < z.plan_bytes) return MLA_ERR_INVALID_ARG;
+  int sms = 0;
+  rc = device_ready(&sms);
+  if (rc != MLA_OK) return rc;
+  char* plan = static_cast<char*>(d_plan);
+  int32_t* lengths = reinterpret_cast<int32_t*>(plan + z.lengths_off);
+  const cudaStream_t st = to_stream(stream);
+  rc = launched(launch_shared_units(d_block_table, max_pages, d_cache_seqlens, batch, s_q, h_q, causal ? 1 : 0,
+                                    z.share, reinterpret_cast<int32_t*>(plan), lengths, st));
+  if (rc != MLA_OK) return rc;
+  return launched(launch_plan(lengths, z.units, num_parts, reinterpret_cast<int32_t*>(plan + z.sched_off),
+                              reinterpret_cast<int32_t*>(plan + z.offset_off), st));
+}
+
+int mla_shared_prefix_decode_fwd(const void* d_q, const void* d_kv, const int32_t* d_block_table, int max_pages,
+                                 int num_pages, int batch, int s_q, int h_q, int dtype, float softmax_scale,
+                                 const void* d_plan, size_t plan_bytes, int num_parts, void* d_workspace,
+                                 size_t workspace_bytes, void* d_out, int out_type, float* d_lse, int32_t* d_status,
+                                 mla_stream_t stream) {
+  if (!d_q || !d_kv || !d_block_table || !d_plan || !d_workspace || !d_out || !d_lse || !d_status)
+    return MLA_ERR_INVALID_ARG;
+  if (max_pages < 1 || num_pages < 1) return MLA_ERR_INVALID_ARG;
+  if (dtype != MLA_DTYPE_BF16 && dtype != MLA_DTYPE_FP16)
+    return dtype == MLA_DTYPE_FP8_RECORD ? MLA_ERR_UNSUPPORTED : MLA_ERR_INVALID_ARG;
+  if (out_type != MLA_DTYPE_BF16 && out_type != MLA_DTYPE_FP32 && out_type != MLA_DTYPE_FP16)
+    return MLA_ERR_INVALID_ARG;
+  if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.f)) return MLA_ERR_INVALID_ARG;
+  if (!aligned(d_q, 16) || !aligned(d_kv, 16) || !aligned(d_plan, 16) || !aligned(d_workspace, 16) ||
+      !aligned(d_out, 16) || !aligned(d_block_table, 4) || !aligned(d_lse, 4) || !aligned(d_status, 4))
+    return MLA_ERR_INVALID_ARG;
+  SharedSizes z;
+  int rc = shared_sizes(batch, s_q, h_q, num_parts, &z);
+  if (rc != MLA_OK) return rc;
+  if (max_pages > kMaxRowPages || static_cast<long long>(batch) * max_pages > kMaxInt ||
+      static_cast<long long>(num_pages) * MLA_PAGE_SIZE > kMaxInt + 1)
+    return MLA_ERR_UNSUPPORTED;
+  if (plan_bytes < z.plan_bytes || workspace_bytes < z.ws_bytes) return MLA_ERR_INVALID_ARG;
+  int sms = 0;
+  rc = device_ready(&sms);
+  if (rc != MLA_OK) return rc;
+  const char* plan = static_cast<const char*>(d_plan);
+  SharedLaunch c{};
+  c.q = d_q;
+  c.kv = d_kv;
+  c.total_rows = z.rows;
+  c.num_pages = num_pages;
+  c.n_units = z.units;
+  c.s_q = s_q;
+  c.h_q = h_q;
+  c.num_parts = num_parts;
+  c.half = dtype == MLA_DTYPE_FP16;
+  c.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * 1.4426950408889634);
+  c.block_table = d_block_table;
+  c.units = reinterpret_cast<const int32_t*>(plan);
+  c.lengths = reinterpret_cast<const int32_t*>(plan + z.lengths_off);
+  c.split_offset = reinterpret_cast<const int32_t*>(plan + z.offset_off);
+  c.sched = reinterpret_cast<const int32_t*>(plan + z.sched_off);
+  c.o_accum = static_cast<float*>(d_workspace);
+  c.lse_accum = reinterpret_cast<float*>(static_cast<char*>(d_workspace) + z.lse_off);
+  c.status = d_status;
+  const cudaStream_t st = to_stream(stream);
+  rc = launch_shared(c, st);
+  if (rc != MLA_OK) return rc;
+  return launched(launch_shared_combine(c.o_accum, c.lse_accum, c.split_offset, batch, s_q * h_q, z.share, d_out,
+                                        out_type, d_lse, sms, st));
 }
 
 }  // extern "C"

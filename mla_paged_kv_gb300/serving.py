@@ -4,8 +4,8 @@ pages, and attention over the prompts that fill it (see include/mla_serving.h).
 Functions named ``mla_*`` mirror the C entry points: they check torch tensors
 and marshal them into pointers, sizes and a CUDA stream.  The helpers
 (``cache_append``, ``cache_grow``, ``cache_fork``, ``cache_free``,
-``cache_compact``, ``cache_copy_pages``, ``plan_prompt``, ``prompt_attention``)
-allocate outputs.  A helper without ``status`` reads the device status after
+``cache_compact``, ``cache_copy_pages``, ``plan_prompt``, ``prompt_attention``,
+``plan_shared_prefix``, ``shared_prefix_decode``) allocate outputs.  A helper without ``status`` reads the device status after
 its call (which waits for the GPU) and raises ``MlaError``; with ``status`` (an
 int32 tensor the caller zeroed) it does not wait, and the caller looks at the
 word when it wants to.
@@ -22,7 +22,8 @@ import math
 
 import torch
 
-from . import (DTYPE_FP8_RECORD, _DTYPE_CODE, _F, _I, _P, _SZ, _check, _ptr, _stream, check_status, load_library)
+from . import (DTYPE_FP8_RECORD, _DTYPE_CODE, _F, _I, _P, _SZ, _check, _ptr, _stream, check_status, load_library,
+               mla_num_parts)
 
 _LL = ctypes.c_longlong
 
@@ -39,12 +40,17 @@ SERVING_SIGS = {
     "mla_prompt_get_plan": (_I, [_P, _P, _I, _I, _I, _I, _P, _SZ, _P, _P]),
     "mla_prompt_attention_fwd": (_I, [_P, _LL, _LL, _P, _LL, _LL, _P, _LL, _LL, _I, _I, _I, _I, _I, _I, _I, _F, _P,
                                       _SZ, _P, _P, _P, _P]),
+    "mla_shared_prefix_plan_bytes": (_SZ, [_I, _I, _I, _I]),
+    "mla_shared_prefix_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
+    "mla_shared_prefix_get_plan": (_I, [_P, _I, _P, _I, _I, _I, _I, _I, _P, _SZ, _P]),
+    "mla_shared_prefix_decode_fwd": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P, _SZ, _I, _P, _SZ, _P, _I, _P,
+                                          _P, _P]),
 }
 SERVING_SYMBOLS = tuple(SERVING_SIGS)
 
 __all__ = [n for n in SERVING_SYMBOLS] + [
     "SERVING_SYMBOLS", "cache_append", "cache_grow", "cache_fork", "cache_free", "cache_compact", "cache_copy_pages",
-    "PromptPlan", "plan_prompt", "prompt_attention",
+    "PromptPlan", "plan_prompt", "prompt_attention", "SharedPrefixPlan", "plan_shared_prefix", "shared_prefix_decode",
 ]
 
 
@@ -372,4 +378,103 @@ def prompt_attention(q, k, v, cu_seqlens_q, cu_seqlens_k=None, causal=True, soft
     mla_prompt_attention_fwd(q, k, v, pl, out, lse, st, softmax_scale)
     if status is None:
         check_status(st, "mla_prompt_attention_fwd")
+    return out, lse
+
+
+# ------------------------------------------------------------ shared prefix
+
+
+class SharedPrefixPlan:
+    """The units and split plan of a batch that shares a prefix, and its split
+    workspace: reused by every layer of that batch, one call at a time."""
+
+    def __init__(self, plan, batch, s_q, h_q, num_parts, causal, workspace):
+        self.plan = plan
+        self.batch = batch
+        self.s_q = s_q
+        self.h_q = h_q
+        self.num_parts = num_parts
+        self.causal = causal
+        self.workspace = workspace
+
+
+def mla_shared_prefix_plan_bytes(batch: int, s_q: int, h_q: int, num_parts: int) -> int:
+    return int(load_library().mla_shared_prefix_plan_bytes(int(batch), int(s_q), int(h_q), int(num_parts)))
+
+
+def mla_shared_prefix_workspace_bytes(batch: int, s_q: int, h_q: int, num_parts: int) -> int:
+    return int(load_library().mla_shared_prefix_workspace_bytes(int(batch), int(s_q), int(h_q), int(num_parts)))
+
+
+def mla_shared_prefix_get_plan(block_table, cache_seqlens, s_q, h_q, causal, num_parts, plan, stream=None):
+    _plain(block_table, torch.int32, "block_table", 2)
+    _plain(cache_seqlens, torch.int32, "cache_seqlens", 1)
+    if cache_seqlens.shape[0] != block_table.shape[0]:
+        raise ValueError("block_table / cache_seqlens batch mismatch")
+    _plain(plan, torch.uint8, "plan", 1)
+    _same_device(block_table, cache_seqlens, plan)
+    _check(load_library().mla_shared_prefix_get_plan(
+        block_table.data_ptr(), block_table.shape[1], cache_seqlens.data_ptr(), block_table.shape[0], int(s_q),
+        int(h_q), 1 if causal else 0, int(num_parts), plan.data_ptr(), plan.numel(), _stream(stream)),
+        "mla_shared_prefix_get_plan")
+
+
+def mla_shared_prefix_decode_fwd(q, kv, block_table, pl, out, lse, status, softmax_scale=1.0 / 24.0, stream=None):
+    """q [B, s_q, h_q, 576] and kv [pages, 64, 576], both bf16 or both fp16; pl a
+    SharedPrefixPlan of this block table; out [B, s_q, h_q, 512] bf16, fp16 or
+    fp32, lse fp32 [B, s_q, h_q]."""
+    if q.dtype not in (torch.bfloat16, torch.float16) or kv.dtype != q.dtype:
+        raise TypeError("q and kv must be both bf16 or both fp16")
+    _plain(q, q.dtype, "q", 4)
+    _plain(kv, q.dtype, "kv", 3)
+    _plain(block_table, torch.int32, "block_table", 2)
+    if out.dtype not in _DTYPE_CODE:
+        raise TypeError("out must be bf16, fp16 or fp32")
+    _plain(out, out.dtype, "out", 4)
+    _plain(lse, torch.float32, "lse", 3)
+    B, s_q, h_q, d = q.shape
+    if d != 576 or tuple(kv.shape[1:]) != (64, 576):
+        raise ValueError("q must be [B, s_q, h_q, 576] and kv [pages, 64, 576]")
+    if tuple(out.shape) != (B, s_q, h_q, 512) or tuple(lse.shape) != (B, s_q, h_q):
+        raise ValueError("out must be [B, s_q, h_q, 512] and lse [B, s_q, h_q]")
+    if block_table.shape[0] != B or (pl.batch, pl.s_q, pl.h_q) != (B, s_q, h_q):
+        raise ValueError("the plan or block table was made for another batch")
+    _plain(status, torch.int32, "status", 1)
+    _same_device(q, kv, block_table, pl.plan, pl.workspace, out, lse, status)
+    _check(load_library().mla_shared_prefix_decode_fwd(
+        q.data_ptr(), kv.data_ptr(), block_table.data_ptr(), block_table.shape[1], kv.shape[0], B, s_q, h_q,
+        _DTYPE_CODE[q.dtype], softmax_scale, pl.plan.data_ptr(), pl.plan.numel(), pl.num_parts,
+        pl.workspace.data_ptr(), pl.workspace.numel(), out.data_ptr(), _DTYPE_CODE[out.dtype], lse.data_ptr(),
+        status.data_ptr(), _stream(stream)), "mla_shared_prefix_decode_fwd")
+
+
+def plan_shared_prefix(block_table, cache_seqlens, s_q, h_q, causal=False, num_parts=None):
+    """The plan of a batch: finds the pages that all requests start with."""
+    B = block_table.shape[0]
+    parts = mla_num_parts(128) if num_parts is None else int(num_parts)
+    size = mla_shared_prefix_plan_bytes(B, s_q, h_q, parts)
+    if size == 0:
+        raise ValueError("batch, s_q, h_q or num_parts out of range")
+    plan = torch.empty(size, dtype=torch.uint8, device=block_table.device)
+    ws = torch.empty(mla_shared_prefix_workspace_bytes(B, s_q, h_q, parts), dtype=torch.uint8,
+                     device=block_table.device)
+    mla_shared_prefix_get_plan(block_table, cache_seqlens, s_q, h_q, causal, parts, plan)
+    return SharedPrefixPlan(plan, B, s_q, h_q, parts, bool(causal), ws)
+
+
+def shared_prefix_decode(q, kv, block_table, cache_seqlens, causal=False, softmax_scale=None, out_fp32=False,
+                         pl=None, status=None):
+    """Dense decode that attends the pages all requests share once; returns (out, lse)."""
+    B, s_q, h_q, _ = q.shape
+    if pl is None:
+        pl = plan_shared_prefix(block_table, cache_seqlens, s_q, h_q, causal)
+    elif pl.causal != bool(causal):
+        raise ValueError("the plan was made with another causal setting")
+    out = torch.empty(B, s_q, h_q, 512, dtype=torch.float32 if out_fp32 else q.dtype, device=q.device)
+    lse = torch.empty(B, s_q, h_q, dtype=torch.float32, device=q.device)
+    st = _status(status, q)
+    mla_shared_prefix_decode_fwd(q, kv, block_table, pl, out, lse, st,
+                                 1.0 / 24.0 if softmax_scale is None else softmax_scale)
+    if status is None:
+        check_status(st, "mla_shared_prefix_decode_fwd")
     return out, lse

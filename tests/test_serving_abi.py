@@ -108,6 +108,37 @@ def test_prompt_refusals(change, want):
     assert mla.load_library().mla_prompt_attention_fwd(*{**PROMPT, **change}.values()) == want
 
 
+SPLAN = dict(table=P, width=4, lens=P, batch=2, s_q=1, h_q=16, causal=0, parts=4, plan=P, bytes=1 << 16, stream=N)
+SDEC = dict(q=P, kv=P, table=P, width=4, pages=8, batch=2, s_q=1, h_q=16, dt=0, scale=0.1, plan=P, pbytes=1 << 16,
+            parts=4, ws=P, wbytes=1 << 24, out=P, ot=0, lse=P, status=P, stream=N)
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(table=N), INVALID), (dict(lens=N), INVALID), (dict(plan=N), INVALID), (dict(batch=0), INVALID),
+    (dict(s_q=0), INVALID), (dict(width=0), INVALID), (dict(parts=0), INVALID), (dict(parts=1025), UNSUPPORTED),
+    (dict(batch=65536), UNSUPPORTED), (dict(bytes=64), INVALID), (dict(width=1 << 18, batch=1 << 14), UNSUPPORTED),
+    (dict(s_q=1 << 17), UNSUPPORTED)])
+def test_shared_plan_refusals(change, want):
+    assert mla.load_library().mla_shared_prefix_get_plan(*{**SPLAN, **change}.values()) == want
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(q=N), INVALID), (dict(kv=N), INVALID), (dict(table=N), INVALID), (dict(plan=N), INVALID),
+    (dict(ws=N), INVALID), (dict(out=N), INVALID), (dict(lse=N), INVALID), (dict(status=N), INVALID),
+    (dict(dt=1), INVALID), (dict(dt=3), UNSUPPORTED), (dict(ot=3), INVALID), (dict(scale=-1.0), INVALID),
+    (dict(pbytes=64), INVALID), (dict(wbytes=64), INVALID), (dict(pages=0), INVALID), (dict(q=ODD), INVALID)])
+def test_shared_decode_refusals(change, want):
+    assert mla.load_library().mla_shared_prefix_decode_fwd(*{**SDEC, **change}.values()) == want
+
+
+def test_shared_prefix_sizes():
+    # 64 requests of 16 rows: 8 prefix blocks and 64 own ones; (units + parts) slots of 128 rows
+    assert mla.mla_shared_prefix_workspace_bytes(64, 1, 16, 76) == (72 + 76) * 128 * 513 * 4
+    # rows that fill their blocks: no prefix blocks
+    assert mla.mla_shared_prefix_workspace_bytes(64, 1, 128, 76) == (64 + 76) * 128 * 513 * 4
+    assert mla.mla_shared_prefix_plan_bytes(0, 1, 16, 76) == 0
+
+
 def test_python_refuses_wrong_tensors():
     c, r = torch.zeros(4, 512, dtype=torch.bfloat16), torch.zeros(4, 64, dtype=torch.bfloat16)
     table, lens = torch.zeros(2, 4, dtype=torch.int32), torch.full((2,), 2, dtype=torch.int32)

@@ -1,0 +1,194 @@
+"""Decode over a shared prefix against the 64-bit oracle of the plain decode
+(the same keys in the same order, so the same result), under the decode's own
+bars (tests/parity.py)."""
+
+import numpy as np
+import pytest
+import torch
+
+import mla_paged_kv_gb300 as mla
+from oracle import mla_oracle as orc
+from tests.parity import compare
+
+pytestmark = pytest.mark.gpu
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+class Case:
+    def __init__(self, head, tails, s_q, h_q, causal=False, dtype=torch.bfloat16, seed=0, amp=1.0, poison=True):
+        """head: shared pages; tails: each request's keys behind them."""
+        g = torch.Generator().manual_seed(seed)
+        B = len(tails)
+        width = head + max(-(-t // 64) for t in tails) + 1
+        pages = head + sum(-(-t // 64) for t in tails) + 2
+        perm = torch.randperm(pages, generator=g).tolist()
+        front = [perm.pop() for _ in range(head)]
+        self.table = np.full((B, width), -1, dtype=np.int32)
+        for b, t in enumerate(tails):
+            self.table[b, :head] = front
+            for j in range(-(-t // 64)):
+                self.table[b, head + j] = perm.pop()
+        self.lens = [head * 64 + t for t in tails]
+        self.kv = torch.randn(pages, 64, 576, generator=g).to(dtype)
+        for b, n in enumerate(self.lens):  # finite poison behind the last key
+            if poison and n % 64:
+                self.kv[self.table[b, n // 64], n % 64:] = 1000.0
+        self.q = (amp * torch.randn(B, s_q, h_q, 576, generator=g)).to(dtype)
+        self.causal, self.s_q, self.h_q = causal, s_q, h_q
+
+    def want(self):
+        return orc.dense_decode(self.q.double().numpy(), self.kv.float().numpy(), self.table,
+                                np.array(self.lens, dtype=np.int32), self.causal, 1 / 24)
+
+    def run(self, num_parts=None, out_fp32=False):
+        table, lens = torch.from_numpy(self.table).cuda(), i32(self.lens)
+        pl = mla.plan_shared_prefix(table, lens, self.s_q, self.h_q, self.causal, num_parts)
+        pl.workspace.fill_(0xFF)  # NaN partials: nothing of an earlier call is read
+        return mla.shared_prefix_decode(self.q.cuda(), self.kv.cuda(), table, lens, self.causal, out_fp32=out_fp32,
+                                        pl=pl)
+
+    def check(self, **kw):
+        out, lse = self.run(**kw)
+        compare(out, lse, *self.want())
+        return out, lse
+
+
+@pytest.mark.parametrize("head", [1, 2, 17])
+@pytest.mark.parametrize("tails", [[1, 64], [65, 3, 130, 64, 1], [0, 5, 0]])
+@pytest.mark.parametrize("h_q", [16, 64, 128])
+def test_prefix_and_tails(head, tails, h_q):
+    Case(head, tails, 1, h_q, seed=head).check()
+
+
+@pytest.mark.parametrize("s_q,h_q,causal", [(2, 16, True), (2, 128, True), (3, 40, True), (2, 40, False),
+                                            (1, 1, False), (5, 7, True), (1, 129, False), (2, 100, True)])
+def test_rows_per_request(s_q, h_q, causal):
+    Case(5, [s_q, 64, 100, 70, 3 + s_q, 200, 65], s_q, h_q, causal, seed=s_q).check()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("out_fp32", [False, True])
+def test_types(dtype, out_fp32):
+    out, _ = Case(9, [30, 90, 128], 1, 32, dtype=dtype, seed=4).check(out_fp32=out_fp32)
+    assert out.dtype == (torch.float32 if out_fp32 else dtype)
+
+
+@pytest.mark.parametrize("num_parts", [1, 2, 7, 300])
+def test_split_counts(num_parts):
+    Case(40, [10, 700, 64, 1], 1, 16, seed=5).check(num_parts=num_parts)
+
+
+def test_peaky_scores():
+    Case(20, [30, 300, 64], 1, 16, seed=6, amp=8.0).check()
+
+
+def test_no_common_page():
+    c = Case(3, [64, 100, 5], 1, 16, seed=7)
+    c.table[1, 0], c.table[1, 1] = c.table[1, 1], c.table[1, 0]
+    c.check()
+
+
+def test_requests_part_inside_the_prefix():
+    """Tables that agree in their first 5, 3 and 7 pages: 3 are shared."""
+    c = Case(7, [64, 100, 5, 300], 1, 16, seed=8)
+    c.table[2, 3:7] = c.table[2, 3:7][::-1].copy()
+    c.table[3, 5] = c.table[3, 6]
+    c.check()
+
+
+@pytest.mark.parametrize("causal", [False, True])
+def test_a_request_that_ends_inside_the_prefix(causal):
+    """Only whole pages that every query of every request sees are shared."""
+    c = Case(6, [64, 100, 5], 2, 16, causal, seed=9)
+    for n in (3 * 64, 3 * 64 + 1, 3 * 64 - 1, 65, 64, 2, 1):
+        c.lens[1] = n
+        c.check()
+
+
+def test_an_empty_request():
+    c = Case(6, [64, 100, 5], 1, 16, seed=10)
+    c.lens[1] = 0
+    out, lse = c.check()
+    assert not out[1].any() and torch.isneginf(lse[1]).all()
+
+
+def test_one_request_and_many():
+    Case(12, [77], 1, 16, seed=11).check()
+    Case(2, [(i * 13) % 90 for i in range(150)], 1, 8, seed=12).check()
+    Case(2, [(i * 13) % 90 + 1 for i in range(40)], 1, 128, seed=12).check()
+
+
+def test_same_as_the_decode_of_each_request():
+    c = Case(30, [64, 100, 5, 300], 1, 16, seed=13, poison=False)
+    out, lse = c.run(out_fp32=True)
+    table, lens = torch.from_numpy(c.table).cuda(), i32(c.lens)
+    o2, l2 = mla.decode(c.q.cuda(), c.kv.cuda(), table, lens, out_fp32=True)
+    # both round the weights to bf16 against references up to 2^8 apart: 2 * 2^-8 of weights of sum 1
+    assert torch.all((out - o2).abs() <= 2.0 ** -6 * c.kv[..., :512].float().abs().max())
+    assert torch.all((lse - l2).abs() <= 1e-4)
+
+
+@pytest.mark.parametrize("where", ["prefix", "tail"])
+def test_bad_page_is_masked_and_reported(where):
+    c = Case(4, [64, 100, 130], 1, 16, seed=14)
+    if where == "prefix":
+        c.table[:, 2] = 10 ** 6
+    else:
+        c.table[2, 5] = -1
+    table, lens = torch.from_numpy(c.table).cuda(), i32(c.lens)
+    with pytest.raises(mla.MlaError) as e:
+        mla.shared_prefix_decode(c.q.cuda(), c.kv.cuda(), table, lens)
+    assert e.value.code == 5
+    st = i32([0])
+    out, lse = mla.shared_prefix_decode(c.q.cuda(), c.kv.cuda(), table, lens, status=st)
+    compare(out, lse, *c.want())
+    assert int(st) == 5
+
+
+def test_refusals():
+    c = Case(4, [64, 100], 1, 16, seed=15)
+    q, kv, table, lens = c.q.cuda(), c.kv.cuda(), torch.from_numpy(c.table).cuda(), i32(c.lens)
+    pl = mla.plan_shared_prefix(table, lens, 1, 16)
+    for bad in (dict(q=q.half()), dict(kv=kv.view(torch.uint8)), dict(table=table[:1]), dict(q=q[:, :, :8]),
+                dict(causal=True), dict(lens=None, q=q[..., :512])):
+        a = {**dict(q=q, kv=kv, table=table, causal=False), **{k: v for k, v in bad.items() if k != "lens"}}
+        with pytest.raises((TypeError, ValueError)):
+            mla.shared_prefix_decode(a["q"], a["kv"], a["table"], lens, a["causal"], pl=pl)
+    with pytest.raises(ValueError):
+        mla.plan_shared_prefix(table, lens, 1, 16, num_parts=1025)
+    with pytest.raises(ValueError):
+        mla.plan_shared_prefix(table, lens[:1], 1, 16)
+    pl.workspace = pl.workspace[:1024]
+    with pytest.raises(mla.MlaError):
+        mla.shared_prefix_decode(q, kv, table, lens, pl=pl)
+
+
+def test_graph_replays_with_new_lengths():
+    """Plan and decode captured together: the table and lengths may change between replays."""
+    c = Case(10, [64, 100, 5, 300], 1, 16, seed=16)
+    q, kv, table, lens = c.q.cuda(), c.kv.cuda(), torch.from_numpy(c.table).cuda(), i32(c.lens)
+    pl = mla.plan_shared_prefix(table, lens, 1, 16)
+    st = i32([0])
+    out, lse = mla.shared_prefix_decode(q, kv, table, lens, pl=pl, status=st)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mla.mla_shared_prefix_get_plan(table, lens, 1, 16, False, pl.num_parts, pl.plan)
+        mla.mla_shared_prefix_decode_fwd(q, kv, table, pl, out, lse, st)
+    for lengths in (c.lens, [600, 640, 641, 704], [64, 130, 70, 65], [10, 0, 3, 2]):
+        c.lens = lengths
+        lens.copy_(i32(lengths))
+        out.fill_(float("nan"))
+        graph.replay()
+        compare(out, lse, *c.want())
+    assert int(st) == 0
+
+
+def test_same_bits_every_time():
+    c = Case(64, [500, 100, 5, 300, 64, 9], 1, 16, seed=17)
+    first = c.run()
+    for _ in range(3):
+        again = c.run()
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
