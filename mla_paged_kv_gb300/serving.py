@@ -22,10 +22,10 @@ import math
 
 import torch
 
-from . import (DTYPE_FP8_RECORD, _DTYPE_CODE, _F, _I, _P, _SZ, _check, _ptr, _stream, check_status, load_library,
-               mla_num_parts)
+from . import (DTYPE_FP8_RECORD, _DTYPE_CODE, _F, _I, _P, _SZ, _check, check_status, load_library, mla_num_parts)
 
 _LL = ctypes.c_longlong
+_DTYPE_CODE16 = {d: _DTYPE_CODE[d] for d in (torch.bfloat16, torch.float16)}
 
 SERVING_SIGS = {
     "mla_cache_append": (_I, [_P, _LL, _P, _LL, _I, _I, _P, _P, _I, _P, _I, _P, _I, _I, _P, _F, _P, _I, _I, _P, _P,
@@ -54,42 +54,55 @@ __all__ = [n for n in SERVING_SYMBOLS] + [
 ]
 
 
-def _same_device(first, *rest):
-    """Checks that every tensor is on `first`'s CUDA device and that it is current."""
-    dev = first.device
-    if dev.type != "cuda":
-        raise ValueError("tensors must be on a CUDA device")
-    for t in rest:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {dev}, the current device is cuda:{torch.cuda.current_device()}")
-
-
-def _plain(t, dtype, name, dims):
+def _refuse(t, dtype, dims, dev, name):
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != dims or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with {dims} dims, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be on cuda:{dev}, is on {t.device}")
 
 
-def _rows16(t, dtype, width, name):
-    """A [n, width] tensor of 16-bit values with contiguous rows; its row stride."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 2 or t.shape[1] != width or t.stride(1) != 1:
-        raise ValueError(f"{name} must be [tokens, {width}] with contiguous rows")
-    return t.stride(0) if t.shape[0] > 1 else width
+def _p(t, dtype, dims, dev, name):
+    """Address of a contiguous tensor of that type and rank on that device.  (A
+    launch-bound call spends most of its time in checks like this: few attribute
+    reads, and the wording of a refusal apart.)"""
+    if t.dtype is dtype and t.dim() == dims and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, dtype, dims, dev, name)
+
+
+def _q(stream, dev):
+    """The stream's handle (the given one, or the current one) for tensors on
+    CUDA device dev, which must be the current device."""
+    if dev < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors are on cuda:{dev}, the current device is cuda:{torch._C._cuda_getDevice()}")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _status(status, like):
-    if status is None:
-        return torch.zeros(1, dtype=torch.int32, device=like.device)
-    _plain(status, torch.int32, "status", 1)
-    return status
+    return torch.zeros(1, dtype=torch.int32, device=like.device) if status is None else status
+
+
+_INT32, _FP32, _UINT8 = torch.int32, torch.float32, torch.uint8
 
 
 # ------------------------------------------------------------------ append
+
+
+def _row_stride(t, dtype, width, dev, name):
+    """Row stride of a [tokens, width] tensor with contiguous rows."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    stride = t.stride()
+    if len(stride) != 2 or t.shape[1] != width or stride[1] != 1:
+        raise ValueError(f"{name} must be [tokens, {width}] with contiguous rows")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, is on {t.device}")
+    if stride[0] % 8 and t.shape[0] > 1:
+        raise ValueError(f"the row stride of {name} must be a multiple of 8 elements")
+    return stride[0] if t.shape[0] > 1 else width
 
 
 def mla_cache_append(c, r, cache, block_table, cache_seqlens, status, cu_seqlens=None, norm_weight=None,
@@ -97,48 +110,53 @@ def mla_cache_append(c, r, cache, block_table, cache_seqlens, status, cu_seqlens
     """New tokens' latent rows c [tokens, 512] and RoPE rows r [tokens, 64]
     (bf16 or fp16, row strides free) into a paged cache: 16-bit
     [pages, 64, 576] of the same type, or FP8 records uint8 [pages, 64, 656]."""
-    if c.dtype not in (torch.bfloat16, torch.float16):
+    dt = c.dtype
+    code = _DTYPE_CODE16.get(dt)
+    if code is None:
         raise TypeError("c must be bf16 or fp16")
-    cs, rs = _rows16(c, c.dtype, 512, "c"), _rows16(r, c.dtype, 64, "r")
-    if r.shape[0] != c.shape[0]:
+    dev = c.get_device()
+    cs, rs = _row_stride(c, dt, 512, dev, "c"), _row_stride(r, dt, 64, dev, "r")
+    tokens = c.shape[0]
+    if r.shape[0] != tokens:
         raise ValueError("c and r must have the same number of tokens")
-    if cs % 8 or rs % 8:
-        raise ValueError("row strides of c and r must be multiples of 8 elements")
-    fp8 = cache.dtype == torch.uint8
-    _plain(cache, torch.uint8 if fp8 else c.dtype, "cache", 3)
-    if cache.shape[1] != 64 or cache.shape[2] != (656 if fp8 else 576):
+    fp8 = cache.dtype is _UINT8
+    cache_ptr = _p(cache, _UINT8 if fp8 else dt, 3, dev, "cache")
+    pages, page, width = cache.shape
+    if page != 64 or width != (656 if fp8 else 576):
         raise ValueError("cache must be [pages, 64, 576] (16-bit) or [pages, 64, 656] (uint8 records)")
-    _plain(block_table, torch.int32, "block_table", 2)
-    _plain(cache_seqlens, torch.int32, "cache_seqlens", 1)
-    batch = block_table.shape[0]
+    table_ptr, lens_ptr = _p(block_table, _INT32, 2, dev, "block_table"), _p(cache_seqlens, _INT32, 1, dev,
+                                                                             "cache_seqlens")
+    batch, max_pages = block_table.shape
     if cache_seqlens.shape[0] != batch:
         raise ValueError("block_table / cache_seqlens batch mismatch")
+    cu_ptr = weight_ptr = cos_ptr = ref_ptr = None
+    max_pos = 0
     if cu_seqlens is not None:
-        _plain(cu_seqlens, torch.int32, "cu_seqlens", 1)
+        cu_ptr = _p(cu_seqlens, _INT32, 1, dev, "cu_seqlens")
         if cu_seqlens.shape[0] != batch + 1:
             raise ValueError("cu_seqlens must have batch + 1 entries")
-    elif batch == 0 or c.shape[0] % batch:
+    elif batch == 0 or tokens % batch:
         raise ValueError("without cu_seqlens every request has tokens / batch tokens")
     if norm_weight is not None:
-        _plain(norm_weight, c.dtype, "norm_weight", 1)
+        weight_ptr = _p(norm_weight, dt, 1, dev, "norm_weight")
         if norm_weight.shape[0] != 512:
             raise ValueError("norm_weight must have 512 entries")
     if cos_sin is not None:
-        _plain(cos_sin, torch.float32, "cos_sin", 2)
-        if cos_sin.shape[1] != 64:
+        cos_ptr = _p(cos_sin, _FP32, 2, dev, "cos_sin")
+        max_pos, width = cos_sin.shape
+        if width != 64:
             raise ValueError("cos_sin must be [positions, 64]: 32 cosines, 32 sines")
     if refcount is not None:
-        _plain(refcount, torch.int32, "refcount", 1)
-        if refcount.shape[0] != cache.shape[0]:
+        ref_ptr = _p(refcount, _INT32, 1, dev, "refcount")
+        if refcount.shape[0] != pages:
             raise ValueError("refcount must have one entry a page")
-    _plain(status, torch.int32, "status", 1)
-    _same_device(c, r, cache, block_table, cache_seqlens, cu_seqlens, norm_weight, cos_sin, refcount, status)
-    _check(load_library().mla_cache_append(
-        c.data_ptr(), cs, r.data_ptr(), rs, _DTYPE_CODE[c.dtype], c.shape[0], _ptr(cu_seqlens),
-        cache_seqlens.data_ptr(), batch, block_table.data_ptr(), block_table.shape[1], cache.data_ptr(),
-        DTYPE_FP8_RECORD if fp8 else _DTYPE_CODE[c.dtype], cache.shape[0], _ptr(norm_weight), norm_eps,
-        _ptr(cos_sin), 0 if cos_sin is None else cos_sin.shape[0], 1 if rope_interleaved else 0, _ptr(refcount),
-        status.data_ptr(), _stream(stream)), "mla_cache_append")
+    st_ptr = _p(status, _INT32, 1, dev, "status")
+    rc = load_library().mla_cache_append(
+        c.data_ptr(), cs, r.data_ptr(), rs, code, tokens, cu_ptr, lens_ptr, batch, table_ptr, max_pages, cache_ptr,
+        DTYPE_FP8_RECORD if fp8 else code, pages, weight_ptr, norm_eps, cos_ptr, max_pos,
+        1 if rope_interleaved else 0, ref_ptr, st_ptr, _q(stream, dev))
+    if rc:
+        _check(rc, "mla_cache_append")
 
 
 def cache_append(c, r, cache, block_table, cache_seqlens, cu_seqlens=None, norm_weight=None, norm_eps=1e-6,
@@ -154,42 +172,48 @@ def cache_append(c, r, cache, block_table, cache_seqlens, cu_seqlens=None, norm_
 # ------------------------------------------------------------------ pages
 
 
-def _pages(refcount, block_table, seqlens, status, *lists):
-    _plain(refcount, torch.int32, "refcount", 1)
-    _plain(block_table, torch.int32, "block_table", 2)
-    _plain(seqlens, torch.int32, "seqlens", 1)
-    if seqlens.shape[0] != block_table.shape[0]:
+def _pages(refcount, block_table, seqlens, dev):
+    args = (_p(refcount, _INT32, 1, dev, "refcount"), refcount.shape[0],
+            _p(block_table, _INT32, 2, dev, "block_table"), *block_table.shape, _p(seqlens, _INT32, 1, dev, "seqlens"))
+    if seqlens.shape[0] != args[3]:
         raise ValueError("block_table / seqlens row mismatch")
-    for t in lists:
-        _plain(t, torch.int32, "list", 1)
-        if t.shape[0] != lists[0].shape[0]:
-            raise ValueError("lists of different lengths")
-    _plain(status, torch.int32, "status", 1)
-    _same_device(refcount, block_table, seqlens, status, *lists)
-    return (refcount.data_ptr(), refcount.shape[0], block_table.data_ptr(), block_table.shape[0],
-            block_table.shape[1], seqlens.data_ptr())
+    return args
 
 
 def mla_cache_grow(refcount, block_table, seqlens, rows, new_tokens, status, stream=None):
-    args = _pages(refcount, block_table, seqlens, status, rows, new_tokens)
-    _check(load_library().mla_cache_grow(*args, rows.data_ptr(), new_tokens.data_ptr(), rows.shape[0],
-                                         status.data_ptr(), _stream(stream)), "mla_cache_grow")
+    dev = refcount.get_device()
+    args = _pages(refcount, block_table, seqlens, dev)
+    rows_ptr, new_ptr = _p(rows, _INT32, 1, dev, "rows"), _p(new_tokens, _INT32, 1, dev, "new_tokens")
+    n = rows.shape[0]
+    if new_tokens.shape[0] != n:
+        raise ValueError("rows and new_tokens must have the same length")
+    rc = load_library().mla_cache_grow(*args, rows_ptr, new_ptr, n, _p(status, _INT32, 1, dev, "status"),
+                                       _q(stream, dev))
+    if rc:
+        _check(rc, "mla_cache_grow")
 
 
 def mla_cache_fork(refcount, block_table, seqlens, parents, children, pairs, status, stream=None):
-    args = _pages(refcount, block_table, seqlens, status, parents, children)
-    _plain(pairs, torch.int32, "pairs", 2)
-    if tuple(pairs.shape) != (parents.shape[0], 2):
-        raise ValueError("pairs must be [n, 2]")
-    _same_device(refcount, pairs)
-    _check(load_library().mla_cache_fork(*args, parents.data_ptr(), children.data_ptr(), parents.shape[0],
-                                         pairs.data_ptr(), status.data_ptr(), _stream(stream)), "mla_cache_fork")
+    dev = refcount.get_device()
+    args = _pages(refcount, block_table, seqlens, dev)
+    par_ptr, chi_ptr = _p(parents, _INT32, 1, dev, "parents"), _p(children, _INT32, 1, dev, "children")
+    pairs_ptr = _p(pairs, _INT32, 2, dev, "pairs")
+    n = parents.shape[0]
+    if children.shape[0] != n or pairs.shape != (n, 2):
+        raise ValueError("parents and children must have the same length n, and pairs be [n, 2]")
+    rc = load_library().mla_cache_fork(*args, par_ptr, chi_ptr, n, pairs_ptr, _p(status, _INT32, 1, dev, "status"),
+                                       _q(stream, dev))
+    if rc:
+        _check(rc, "mla_cache_fork")
 
 
 def mla_cache_free(refcount, block_table, seqlens, rows, status, stream=None):
-    args = _pages(refcount, block_table, seqlens, status, rows)
-    _check(load_library().mla_cache_free(*args, rows.data_ptr(), rows.shape[0], status.data_ptr(), _stream(stream)),
-           "mla_cache_free")
+    dev = refcount.get_device()
+    args = _pages(refcount, block_table, seqlens, dev)
+    rc = load_library().mla_cache_free(*args, _p(rows, _INT32, 1, dev, "rows"), rows.shape[0],
+                                       _p(status, _INT32, 1, dev, "status"), _q(stream, dev))
+    if rc:
+        _check(rc, "mla_cache_free")
 
 
 def mla_cache_compact_workspace_bytes(num_pages: int) -> int:
@@ -197,42 +221,46 @@ def mla_cache_compact_workspace_bytes(num_pages: int) -> int:
 
 
 def mla_cache_compact(refcount, block_table, seqlens, pairs, count, workspace, status, stream=None):
-    args = _pages(refcount, block_table, seqlens, status)
-    _plain(pairs, torch.int32, "pairs", 2)
-    _plain(count, torch.int32, "count", 1)
-    _plain(workspace, torch.uint8, "workspace", 1)
-    if pairs.shape[0] < refcount.shape[0] // 2 or pairs.shape[1] != 2 or count.shape[0] < 1:
+    dev = refcount.get_device()
+    args = _pages(refcount, block_table, seqlens, dev)
+    pairs_ptr, count_ptr = _p(pairs, _INT32, 2, dev, "pairs"), _p(count, _INT32, 1, dev, "count")
+    ws_ptr = _p(workspace, _UINT8, 1, dev, "workspace")
+    if pairs.shape[0] < args[1] // 2 or pairs.shape[1] != 2 or count.shape[0] < 1:
         raise ValueError("pairs must be [num_pages // 2, 2] and count have one entry")
-    _same_device(refcount, pairs, count, workspace)
-    _check(load_library().mla_cache_compact(*args, pairs.data_ptr(), count.data_ptr(), workspace.data_ptr(),
-                                            workspace.numel(), status.data_ptr(), _stream(stream)),
-           "mla_cache_compact")
+    rc = load_library().mla_cache_compact(*args, pairs_ptr, count_ptr, ws_ptr, workspace.shape[0],
+                                          _p(status, _INT32, 1, dev, "status"), _q(stream, dev))
+    if rc:
+        _check(rc, "mla_cache_compact")
 
 
 def mla_cache_copy_pages(pool, pairs, status, count=None, layered=False, stream=None):
     """pool: [pages, ...], or with layered [layers, pages, ...]; any type, pages
     contiguous and one after another; layers may be any distance apart."""
+    dev = pool.get_device()
+    shape, strides, size = pool.shape, pool.stride(), pool.element_size()
     lead = 2 if layered else 1
-    if pool.dim() < lead + 1:
+    if len(shape) < lead + 1:
         raise ValueError("pool must be [pages, ...] or, layered, [layers, pages, ...]")
-    first = pool[0] if layered else pool
-    if not first.is_contiguous():
+    layers, layer_stride = (shape[0], strides[0] * size) if layered else (1, 0)
+    page = 1
+    for n, step in zip(reversed(shape[lead:]), reversed(strides[lead:])):
+        if n != 1 and step != page:
+            raise ValueError("the pages of a layer must be contiguous")
+        page *= n
+    if shape[lead - 1] > 1 and strides[lead - 1] != page:
         raise ValueError("the pages of a layer must be contiguous")
-    _plain(pairs, torch.int32, "pairs", 2)
+    page *= size
+    if page % 16 or (layers > 1 and layer_stride % 16):
+        raise ValueError("pages and layers must be multiples of 16 bytes")
+    pairs_ptr = _p(pairs, _INT32, 2, dev, "pairs")
     if pairs.shape[1] != 2:
         raise ValueError("pairs must be [n, 2]")
-    if count is not None:
-        _plain(count, torch.int32, "count", 1)
-    _plain(status, torch.int32, "status", 1)
-    _same_device(pool, pairs, count, status)
-    size = pool.element_size()
-    layers = pool.shape[0] if layered else 1
-    page_bytes = first.stride(0) * size if first.shape[0] > 1 else first[0].numel() * size
-    if page_bytes % 16 or (layers > 1 and pool.stride(0) * size % 16):
-        raise ValueError("pages and layers must be multiples of 16 bytes")
-    _check(load_library().mla_cache_copy_pages(
-        pool.data_ptr(), layers, pool.stride(0) * size if layers > 1 else 0, first.shape[0], page_bytes,
-        pairs.data_ptr(), _ptr(count), pairs.shape[0], status.data_ptr(), _stream(stream)), "mla_cache_copy_pages")
+    rc = load_library().mla_cache_copy_pages(
+        pool.data_ptr(), layers, layer_stride if layers > 1 else 0, shape[lead - 1], page, pairs_ptr,
+        None if count is None else _p(count, _INT32, 1, dev, "count"), pairs.shape[0],
+        _p(status, _INT32, 1, dev, "status"), _q(stream, dev))
+    if rc:
+        _check(rc, "mla_cache_copy_pages")
 
 
 def cache_grow(refcount, block_table, seqlens, rows, new_tokens, status=None):
@@ -302,17 +330,15 @@ def mla_prompt_plan_bytes(batch: int, total_q: int) -> int:
 
 
 def mla_prompt_get_plan(cu_seqlens_q, cu_seqlens_k, total_q, total_k, causal, plan, status, stream=None):
-    _plain(cu_seqlens_q, torch.int32, "cu_seqlens_q", 1)
+    dev = cu_seqlens_q.get_device()
+    cu_q, cu_k = _p(cu_seqlens_q, _INT32, 1, dev, "cu_seqlens_q"), None
     if cu_seqlens_k is not None:
-        _plain(cu_seqlens_k, torch.int32, "cu_seqlens_k", 1)
+        cu_k = _p(cu_seqlens_k, _INT32, 1, dev, "cu_seqlens_k")
         if cu_seqlens_k.shape != cu_seqlens_q.shape:
             raise ValueError("cu_seqlens_q and cu_seqlens_k must have the same length")
-    _plain(plan, torch.uint8, "plan", 1)
-    _plain(status, torch.int32, "status", 1)
-    _same_device(cu_seqlens_q, cu_seqlens_k, plan, status)
     _check(load_library().mla_prompt_get_plan(
-        cu_seqlens_q.data_ptr(), _ptr(cu_seqlens_k), cu_seqlens_q.shape[0] - 1, int(total_q), int(total_k),
-        1 if causal else 0, plan.data_ptr(), plan.numel(), status.data_ptr(), _stream(stream)),
+        cu_q, cu_k, cu_seqlens_q.shape[0] - 1, int(total_q), int(total_k), 1 if causal else 0,
+        _p(plan, _UINT8, 1, dev, "plan"), plan.shape[0], _p(status, _INT32, 1, dev, "status"), _q(stream, dev)),
         "mla_prompt_get_plan")
 
 
@@ -320,31 +346,37 @@ def mla_prompt_attention_fwd(q, k, v, pl, out, lse, status, softmax_scale=None, 
     """q [total_q, h_q, 192 or 128], k [total_k, h_kv, same], v [total_k, h_kv,
     128], bf16 or fp16, last dimension contiguous, other strides multiples of 8;
     pl a PromptPlan; out [total_q, h_q, 128] of q's type, lse fp32 [total_q, h_q]."""
-    if q.dtype not in (torch.bfloat16, torch.float16) or k.dtype != q.dtype or v.dtype != q.dtype:
+    dt = q.dtype
+    code = _DTYPE_CODE16.get(dt)
+    if code is None or k.dtype is not dt or v.dtype is not dt:
         raise TypeError("q, k and v must be all bf16 or all fp16")
-    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+    qs, ks, vs = q.stride(), k.stride(), v.stride()
+    if len(qs) != 3 or len(ks) != 3 or len(vs) != 3:
         raise ValueError("q, k and v must be [tokens, heads, dim]")
     total_q, h_q, d = q.shape
-    total_k, h_kv = k.shape[:2]
-    if d not in (128, 192) or k.shape[2] != d or tuple(v.shape) != (total_k, h_kv, 128):
+    total_k, h_kv, dk = k.shape
+    if d not in (128, 192) or dk != d or v.shape != (total_k, h_kv, 128):
         raise ValueError("q and k must have 128 or 192 dims, v 128, k and v the same tokens and heads")
     if h_kv < 1 or h_q % h_kv:
         raise ValueError("the key heads must divide the query heads")
-    if q.stride(2) != 1 or k.stride(2) != 1 or v.stride(2) != 1:
+    if qs[2] != 1 or ks[2] != 1 or vs[2] != 1:
         raise ValueError("the last dimension of q, k and v must be contiguous")
     if pl.total_q != total_q or pl.total_k != total_k:
         raise ValueError("the plan was made for other token counts")
-    _plain(out, q.dtype, "out", 3)
-    _plain(lse, torch.float32, "lse", 2)
-    if tuple(out.shape) != (total_q, h_q, 128) or tuple(lse.shape) != (total_q, h_q):
+    dev = q.get_device()
+    if k.get_device() != dev or v.get_device() != dev:
+        raise ValueError("q, k and v must be on one device")
+    out_ptr, lse_ptr = _p(out, dt, 3, dev, "out"), _p(lse, _FP32, 2, dev, "lse")
+    if out.shape != (total_q, h_q, 128) or lse.shape != (total_q, h_q):
         raise ValueError("out must be [total_q, h_q, 128] and lse [total_q, h_q]")
-    _plain(status, torch.int32, "status", 1)
-    _same_device(q, k, v, pl.plan, out, lse, status)
-    _check(load_library().mla_prompt_attention_fwd(
-        q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
-        v.stride(1), _DTYPE_CODE[q.dtype], total_q, total_k, pl.batch, h_q, h_kv, d,
-        1.0 / math.sqrt(d) if softmax_scale is None else softmax_scale, pl.plan.data_ptr(), pl.plan.numel(),
-        out.data_ptr(), lse.data_ptr(), status.data_ptr(), _stream(stream)), "mla_prompt_attention_fwd")
+    plan = pl.plan
+    rc = load_library().mla_prompt_attention_fwd(
+        q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], code, total_q, total_k,
+        pl.batch, h_q, h_kv, d, 1.0 / math.sqrt(d) if softmax_scale is None else softmax_scale,
+        _p(plan, _UINT8, 1, dev, "plan"), plan.shape[0], out_ptr, lse_ptr, _p(status, _INT32, 1, dev, "status"),
+        _q(stream, dev))
+    if rc:
+        _check(rc, "mla_prompt_attention_fwd")
 
 
 def plan_prompt(cu_seqlens_q, cu_seqlens_k=None, total_q=None, total_k=None, causal=True, status=None):
@@ -388,9 +420,10 @@ class SharedPrefixPlan:
     """The units and split plan of a batch that shares a prefix, and its split
     workspace: reused by every layer of that batch, one call at a time."""
 
-    def __init__(self, plan, batch, s_q, h_q, num_parts, causal, workspace):
+    def __init__(self, plan, batch, max_pages, s_q, h_q, num_parts, causal, workspace):
         self.plan = plan
         self.batch = batch
+        self.max_pages = max_pages
         self.s_q = s_q
         self.h_q = h_q
         self.num_parts = num_parts
@@ -407,50 +440,52 @@ def mla_shared_prefix_workspace_bytes(batch: int, s_q: int, h_q: int, num_parts:
 
 
 def mla_shared_prefix_get_plan(block_table, cache_seqlens, s_q, h_q, causal, num_parts, plan, stream=None):
-    _plain(block_table, torch.int32, "block_table", 2)
-    _plain(cache_seqlens, torch.int32, "cache_seqlens", 1)
-    if cache_seqlens.shape[0] != block_table.shape[0]:
+    dev = block_table.get_device()
+    table_ptr = _p(block_table, _INT32, 2, dev, "block_table")
+    lens_ptr = _p(cache_seqlens, _INT32, 1, dev, "cache_seqlens")
+    batch, max_pages = block_table.shape
+    if cache_seqlens.shape[0] != batch:
         raise ValueError("block_table / cache_seqlens batch mismatch")
-    _plain(plan, torch.uint8, "plan", 1)
-    _same_device(block_table, cache_seqlens, plan)
     _check(load_library().mla_shared_prefix_get_plan(
-        block_table.data_ptr(), block_table.shape[1], cache_seqlens.data_ptr(), block_table.shape[0], int(s_q),
-        int(h_q), 1 if causal else 0, int(num_parts), plan.data_ptr(), plan.numel(), _stream(stream)),
-        "mla_shared_prefix_get_plan")
+        table_ptr, max_pages, lens_ptr, batch, int(s_q), int(h_q), 1 if causal else 0, int(num_parts),
+        _p(plan, _UINT8, 1, dev, "plan"), plan.shape[0], _q(stream, dev)), "mla_shared_prefix_get_plan")
 
 
 def mla_shared_prefix_decode_fwd(q, kv, block_table, pl, out, lse, status, softmax_scale=1.0 / 24.0, stream=None):
     """q [B, s_q, h_q, 576] and kv [pages, 64, 576], both bf16 or both fp16; pl a
     SharedPrefixPlan of this block table; out [B, s_q, h_q, 512] bf16, fp16 or
     fp32, lse fp32 [B, s_q, h_q]."""
-    if q.dtype not in (torch.bfloat16, torch.float16) or kv.dtype != q.dtype:
+    dt = q.dtype
+    code, out_code = _DTYPE_CODE16.get(dt), _DTYPE_CODE.get(out.dtype)
+    if code is None or kv.dtype is not dt:
         raise TypeError("q and kv must be both bf16 or both fp16")
-    _plain(q, q.dtype, "q", 4)
-    _plain(kv, q.dtype, "kv", 3)
-    _plain(block_table, torch.int32, "block_table", 2)
-    if out.dtype not in _DTYPE_CODE:
+    if out_code is None:
         raise TypeError("out must be bf16, fp16 or fp32")
-    _plain(out, out.dtype, "out", 4)
-    _plain(lse, torch.float32, "lse", 3)
+    dev = q.get_device()
+    q_ptr, kv_ptr = _p(q, dt, 4, dev, "q"), _p(kv, dt, 3, dev, "kv")
+    table_ptr = _p(block_table, _INT32, 2, dev, "block_table")
+    out_ptr, lse_ptr = _p(out, out.dtype, 4, dev, "out"), _p(lse, _FP32, 3, dev, "lse")
     B, s_q, h_q, d = q.shape
-    if d != 576 or tuple(kv.shape[1:]) != (64, 576):
+    pages, page, width = kv.shape
+    if d != 576 or page != 64 or width != 576:
         raise ValueError("q must be [B, s_q, h_q, 576] and kv [pages, 64, 576]")
-    if tuple(out.shape) != (B, s_q, h_q, 512) or tuple(lse.shape) != (B, s_q, h_q):
+    if out.shape != (B, s_q, h_q, 512) or lse.shape != (B, s_q, h_q):
         raise ValueError("out must be [B, s_q, h_q, 512] and lse [B, s_q, h_q]")
-    if block_table.shape[0] != B or (pl.batch, pl.s_q, pl.h_q) != (B, s_q, h_q):
+    batch, max_pages = block_table.shape
+    if batch != B or pl.batch != B or pl.s_q != s_q or pl.h_q != h_q or pl.max_pages != max_pages:
         raise ValueError("the plan or block table was made for another batch")
-    _plain(status, torch.int32, "status", 1)
-    _same_device(q, kv, block_table, pl.plan, pl.workspace, out, lse, status)
-    _check(load_library().mla_shared_prefix_decode_fwd(
-        q.data_ptr(), kv.data_ptr(), block_table.data_ptr(), block_table.shape[1], kv.shape[0], B, s_q, h_q,
-        _DTYPE_CODE[q.dtype], softmax_scale, pl.plan.data_ptr(), pl.plan.numel(), pl.num_parts,
-        pl.workspace.data_ptr(), pl.workspace.numel(), out.data_ptr(), _DTYPE_CODE[out.dtype], lse.data_ptr(),
-        status.data_ptr(), _stream(stream)), "mla_shared_prefix_decode_fwd")
+    plan, ws = pl.plan, pl.workspace
+    rc = load_library().mla_shared_prefix_decode_fwd(
+        q_ptr, kv_ptr, table_ptr, max_pages, pages, B, s_q, h_q, code, softmax_scale,
+        _p(plan, _UINT8, 1, dev, "plan"), plan.shape[0], pl.num_parts, _p(ws, _UINT8, 1, dev, "workspace"),
+        ws.shape[0], out_ptr, out_code, lse_ptr, _p(status, _INT32, 1, dev, "status"), _q(stream, dev))
+    if rc:
+        _check(rc, "mla_shared_prefix_decode_fwd")
 
 
 def plan_shared_prefix(block_table, cache_seqlens, s_q, h_q, causal=False, num_parts=None):
     """The plan of a batch: finds the pages that all requests start with."""
-    B = block_table.shape[0]
+    B, max_pages = block_table.shape
     parts = mla_num_parts(128) if num_parts is None else int(num_parts)
     size = mla_shared_prefix_plan_bytes(B, s_q, h_q, parts)
     if size == 0:
@@ -459,7 +494,7 @@ def plan_shared_prefix(block_table, cache_seqlens, s_q, h_q, causal=False, num_p
     ws = torch.empty(mla_shared_prefix_workspace_bytes(B, s_q, h_q, parts), dtype=torch.uint8,
                      device=block_table.device)
     mla_shared_prefix_get_plan(block_table, cache_seqlens, s_q, h_q, causal, parts, plan)
-    return SharedPrefixPlan(plan, B, s_q, h_q, parts, bool(causal), ws)
+    return SharedPrefixPlan(plan, B, max_pages, s_q, h_q, parts, bool(causal), ws)
 
 
 def shared_prefix_decode(q, kv, block_table, cache_seqlens, causal=False, softmax_scale=None, out_fp32=False,
