@@ -136,10 +136,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                   const __grid_constant__ CUtensorMap v_map, const PromptParams p) {
   using L = Layout<kQBoxes>;
-  // tiles longest first within a head, heads one after another: the CTAs that
-  // run together read few heads' keys, and the last ones to start are short
-  const int head = blockIdx.x / p.max_tiles;
-  const int item = blockIdx.x - head * p.max_tiles;
+  // tiles longest first, every head of a tile before the next one: the last CTAs
+  // to start are the short ones of all heads
+  const int item = blockIdx.x / p.h_q;
+  const int head = blockIdx.x - item * p.h_q;
   if (item >= p.plan[0]) return;
   const int causal = p.plan[1];
   const int4* e = reinterpret_cast<const int4*>(p.plan + kTileInts * (item + 1));
@@ -265,18 +265,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == kWarpMma) {
     // ------------------------------------------------------------ MMAs
-    if (lane == 0 && n > 0) {
+    // the whole warp runs this loop (see umma_f16_warp); its control flow and
+    // every operand are the same in all lanes
+    if (n > 0) {
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       constexpr uint32_t idesc_qk = idesc_16bit_f32(128, kBN, false, kHalf);
       constexpr uint32_t idesc_pv = idesc_16bit_f32(128, 128, true, kHalf);
       const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024);
       const uint64_t k_desc = sdesc_sw128(smem_u32(sRing), 16, 1024);
-      bool ok = mbar_wait(&bars[Q_FULL], 0, abort_flag);
+      auto wait = [&](int bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait(&bars[bar], parity, abort_flag));
+      };
+      bool ok = wait(Q_FULL, 0);
       uint32_t use = 0;  // ring boxes waited for
       uint32_t k_at = 0, v_at = 0;
       auto wait_boxes = [&](int count) {
         const uint32_t at = use;
         for (int i = 0; i < count && ok; ++i, ++use)
-          ok = mbar_wait(&bars[R_FULL + use % kRing], (use / kRing) & 1, abort_flag);
+          ok = wait(R_FULL + use % kRing, (use / kRing) & 1);
         return at;
       };
       for (int j = 0; j <= n && ok; ++j) {
@@ -285,13 +291,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int h = 0; h < 2 && ok; ++h) {
           const int nh = h ? n1 : n0;
-          const uint32_t s_col = tmem + 128u * h, o_col = tmem + 256u + 128u * h;
+          const uint32_t s_col = tm + 128u * h, o_col = tm + 256u + 128u * h;
           if (j >= 1 && j - 1 < nh) {
             if (!have_v) {
               v_at = wait_boxes(kVBoxes);
               have_v = true;
             }
-            if (ok) ok = mbar_wait(&bars[P_FULL + h], (j - 1) & 1, abort_flag);
+            if (ok) ok = wait(P_FULL + h, (j - 1) & 1);
             if (!ok) break;
             tc_fence_after();
             // V as the MN-major B operand: dims 0-63 in one box, 64-127 in the
@@ -302,9 +308,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                             (wrap ? kRing - 1 : 1) * kBoxBytes, 1024);
 #pragma unroll
             for (int kk = 0; kk < kBN / 16; ++kk)
-              umma_f16_ts(o_col, s_col + 8u * kk, vd + static_cast<uint64_t>((kk * 2048) >> 4), idesc_pv,
+              umma_f16_ts_warp(o_col, s_col + 8u * kk, vd + static_cast<uint64_t>((kk * 2048) >> 4), idesc_pv,
                           (j == 1 && kk == 0) ? 0u : 1u);
-            if (j == nh) umma_commit(&bars[O_FULL + h]);
+            if (j == nh) umma_commit_warp(&bars[O_FULL + h]);
           }
           if (j < nh) {
             if (!have_k) {
@@ -319,21 +325,21 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint64_t qd = q_desc + static_cast<uint64_t>(((h * kQBoxes + s) * kBoxBytes) >> 4);
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                umma_f16(s_col, qd + static_cast<uint64_t>((kk * 32) >> 4), kd + static_cast<uint64_t>((kk * 32) >> 4),
+                umma_f16_warp(s_col, qd + static_cast<uint64_t>((kk * 32) >> 4), kd + static_cast<uint64_t>((kk * 32) >> 4),
                          idesc_qk, (s == 0 && kk == 0) ? 0u : 1u);
             }
-            umma_commit(&bars[S_FULL + h]);
+            umma_commit_warp(&bars[S_FULL + h]);
           }
         }
         if (!ok) break;
         if (have_v)
-          for (int b = 0; b < kVBoxes; ++b) umma_commit(&bars[R_EMPTY + (v_at + b) % kRing]);
+          for (int b = 0; b < kVBoxes; ++b) umma_commit_warp(&bars[R_EMPTY + (v_at + b) % kRing]);
         if (have_k)
-          for (int s = 0; s < kQBoxes; ++s) umma_commit(&bars[R_EMPTY + (k_at + s) % kRing]);
+          for (int s = 0; s < kQBoxes; ++s) umma_commit_warp(&bars[R_EMPTY + (k_at + s) % kRing]);
       }
-      if (!ok) fail(abort_flag, p.status);
+      if (!ok && lane == 0) fail(abort_flag, p.status);
       // every MMA is done with shared memory and TMEM before this CTA ends
-      umma_commit(&bars[DRAIN]);
+      umma_commit_warp(&bars[DRAIN]);
       mbar_wait(&bars[DRAIN], 0, nullptr);
     }
     __syncwarp();
