@@ -4,21 +4,21 @@
 //   s_ij = scale q_i . k_j,  out_i = sum_j e^(s_ij - r_i) v_j / l_i,
 //   l_i = sum_j e^(s_ij - r_i),  lse_i = r_i + ln l_i,  j <= i + Lk - Lq
 //
-// One CTA per (query head, 256-query tile): two 128-row halves, each with its
-// own scores, softmax warps and accumulator, take turns on the tensor cores, so
-// that one half's exponentials run while the other half's products do.  128
-// keys at a time:
+// A worker takes (query head, query tile) items from the plan's list, longest
+// first.  A tile has two halves, each with its own scores, softmax warps and
+// accumulator, that take turns on the tensor cores: one half's exponentials
+// run while the other half's products do.  128 keys at a time:
 //   * TMEM (512 columns): scores of both halves (2 x 128), outputs (2 x 128).
 //     A half's weights P overwrite its scores as packed 16-bit pairs and are the
 //     A operand of P V from there, so P never touches shared memory.
-//   * Shared memory: Q of both halves (6 boxes of 128 rows x 64 dims, 96 KB) and
-//     a ring of eight 16 KB boxes through which K (3 boxes) and V (2) stream in
-//     the order they are used, K0 V0 K1 V1 ...
-//   * One thread issues every MMA in the order
+//   * Shared memory: Q of both halves, and a ring of K and of V stages.
+//   * One warp issues every MMA in the order
 //       PV0(j-1) QK0(j)  PV1(j-1) QK1(j)
 //     The tensor pipe runs them in order, so S(j) being ready means PV(j-1) of
 //     that half is done: its P may be overwritten, and its O rescaled, without a
 //     wait of their own.  Two barriers a half remain: scores ready, weights ready.
+//     The same order lets the next item's first products follow the last ones of
+//     this item while its output is still being written.
 //   * The softmax reference r is raised only when a row's maximum grows by more
 //     than 2^8 (then O is rescaled in TMEM, rarely); weights stay below 2^8, so
 //     sums stay far from overflow.  Statistics are fp32; P is rounded to the
@@ -27,9 +27,15 @@
 //   * Keys past the sequence's end in its last tile belong to another sequence
 //     (or to nothing): their scores are masked and their V rows are zeroed in
 //     shared memory, since 0 x NaN would not be 0.
-// The tensor work a tile of 128 keys costs one half is 128 x 128 x (192 + 128)
-// multiply-adds = 640 cycles at 8192 a cycle; its 16384 exponentials take about
-// 512 at 32 a cycle.
+// A worker is a pair of CTAs for long prompts (kPair): cta_group::2 MMAs over
+// 256 rows a half, 128 in each CTA, with K and V split between the two shared
+// memories (K by keys, V by dims).  One CTA alone has room for 1.6 key tiles
+// beside its 96 KB of Q, too few to cover the latency of the loads (2.15 us a
+// tile against 1.61 with the loads taken out); half a tile each gives the pair
+// three.  A prompt of 256 queries or fewer would leave half a pair idle: those
+// run on single CTAs with two 128-row halves.
+// The bound is the tensor pipe: 128 x 128 x (192 + 128) multiply-adds a half and
+// key tile are 1280 cycles at 4096 a cycle.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -40,36 +46,53 @@
 namespace mla {
 namespace pr {
 
-constexpr int kBM = 128;                  // query rows of a half
-constexpr int kBN = 128;                  // keys of a tile
-constexpr int kTileQ = 2 * kBM;
-constexpr int kBoxBytes = 128 * 128;      // 128 rows x 64 16-bit values
-constexpr int kRing = 8;
-constexpr int kVBoxes = 2;
+constexpr int kBM = 128;              // query rows of a half in one CTA
+constexpr int kBN = 128;              // keys of a tile
+constexpr int kBoxBytes = 128 * 128;  // 128 rows x 64 16-bit values
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;  // three warpgroups: two of softmax warps, one for the loads and the MMAs
 constexpr int kWarpMma = 8, kWarpLoad = 9;
+// Registers: 384 threads start with 168 each; the third warpgroup gives 80 of
+// its own to the softmax threads, which hold a row of 128 scores
+// (2 x 128 x 208 + 128 x 88 = 384 x 168).
+constexpr int kRegsSoftmax = 208, kRegsOther = 88;
+constexpr int kMaxStages = 5;
 
 enum : int {
   Q_FULL = 0,
-  R_FULL = 1,               // +slot: a ring box has landed
-  R_EMPTY = R_FULL + kRing,  // +slot: its MMAs are done
-  S_FULL = R_EMPTY + kRing,  // +half: scores ready, and P V of the tile before done
-  P_FULL = S_FULL + 2,       // +half: weights written (128 arrivals)
-  O_FULL = P_FULL + 2,       // +half: the last P V is done
-  TAIL = O_FULL + 2,         // the last V tile, before its rows past the end are zeroed
-  DRAIN,                     // every MMA issued is done
+  Q_EMPTY,                        // the item's last Q K^T is done: Q may be loaded over
+  K_FULL,                         // +stage
+  K_EMPTY = K_FULL + kMaxStages,  // +stage: its MMAs are done
+  V_FULL = K_EMPTY + kMaxStages,
+  V_EMPTY = V_FULL + kMaxStages,
+  S_FULL = V_EMPTY + kMaxStages,  // +half: scores ready, and P V of the tile before done
+  P_FULL = S_FULL + 2,            // +half: weights written (one arrival per softmax warp)
+  O_FULL = P_FULL + 2,            // +half: the item's last P V is done
+  TAIL = O_FULL + 2,              // the last V tile, before its rows past the end are zeroed
+  DRAIN,                          // every MMA issued is done
   kNumBars
 };
 
-template <int kQBoxes>
+// Shared memory of one CTA: Q (2 halves x kQBoxes boxes), then K stages (the
+// CTA's keys x kQBoxes 64-dim slices), then V stages (128 keys x the CTA's dims).
+template <int kQBoxes, bool kPair>
 struct Layout {
-  static constexpr int kOffRing = 2 * kQBoxes * kBoxBytes;
-  static constexpr int kOffBar = kOffRing + kRing * kBoxBytes;
+  static constexpr int kHalfRows = kPair ? 256 : 128;          // query rows of a half
+  static constexpr int kKeys = kPair ? 64 : 128;               // keys of a tile in this CTA's K stage
+  static constexpr int kVBoxes = kPair ? 1 : 2;                // 64-dim boxes of its V stage
+  static constexpr int kKBoxBytes = kKeys * 128;
+  static constexpr int kKBytes = kQBoxes * kKBoxBytes;
+  static constexpr int kVBytes = kVBoxes * kBoxBytes;
+  static constexpr int kKStages = kPair ? (kQBoxes == 3 ? 3 : 5) : (kQBoxes == 3 ? 2 : 3);
+  static constexpr int kVStages = kPair ? (kQBoxes == 3 ? 3 : 5) : (kQBoxes == 3 ? 1 : 2);
+  static constexpr int kOffK = 2 * kQBoxes * kBoxBytes;
+  static constexpr int kOffV = kOffK + kKStages * kKBytes;
+  static constexpr int kOffBar = kOffV + kVStages * kVBytes;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kBytes = kOffMisc + 16 + 1024;  // slack to align the base to 1024 B
+  static_assert(kBytes <= 232448, "shared memory budget");
+  static_assert(kKStages <= kMaxStages && kVStages <= kMaxStages, "barriers");
 };
-static_assert(Layout<3>::kBytes <= 232448, "shared memory budget");
 
 constexpr uint32_t kTmemCols = 512;
 constexpr float kTau = 8.0f;
@@ -78,7 +101,7 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // Plan: a header {tiles, causal}, then the tiles, kTileInts int32 each.
 struct Tile {
   int q0;    // first query row of the tile in the packed q
-  int rows;  // queries of the sequence from q0 on (at most 256 matter)
+  int rows;  // queries of the sequence from q0 on (the first two halves' worth matter)
   int k0;    // first key row of the sequence
   int lk;    // keys of the sequence
   int vis;   // keys that the tile's first query sees
@@ -119,11 +142,36 @@ __device__ __forceinline__ void tmem_ld32_max(uint32_t taddr, float* f, float& m
 
 // 128-key tiles that half h of a tile has to visit: keys its last valid row
 // sees, at most the sequence's; 0 for a half without rows.
-__device__ __forceinline__ int half_tiles(const Tile& t, int h, int causal) {
-  const int rows = min(t.rows - h * kBM, kBM);
+__device__ __forceinline__ int half_tiles(const Tile& t, int h, int half_rows, int causal) {
+  const int rows = min(t.rows - h * half_rows, half_rows);
   if (rows <= 0) return 0;
-  const int keys = causal ? min(t.lk, t.vis + h * kBM + rows - 1) : t.lk;
+  const int keys = causal ? min(t.lk, t.vis + h * half_rows + rows - 1) : t.lk;
   return keys > 0 ? (keys + kBN - 1) / kBN : 0;
+}
+
+// The items of one worker, the same in every role: item `round` is number
+// round * workers + worker of the list, counted backwards in every other round,
+// so that the sums of a descending list come out nearly equal.  An item is one
+// tile of the plan and one query head, all heads of a tile in a row.
+struct Items {
+  int round, at, total;  // at: the current item's number
+  int causal;
+};
+
+__device__ __forceinline__ Items first_item(const PromptParams& p, int worker) {
+  return Items{0, worker, p.plan[0] * p.h_q, p.plan[1]};
+}
+
+__device__ __forceinline__ void next_item(Items& it, int worker, int workers) {
+  ++it.round;
+  it.at = it.round * workers + ((it.round & 1) ? workers - 1 - worker : worker);
+}
+
+__device__ __forceinline__ Tile load_tile(const PromptParams& p, const Items& it) {
+  if (it.at >= it.total) return Tile{0, 0, 0, 0, 0};
+  const int4* e = reinterpret_cast<const int4*>(p.plan + kTileInts * (it.at / p.h_q + 1));
+  const int4 a = e[0];
+  return Tile{a.x, a.y, a.z, a.w, e[1].x};
 }
 
 __device__ __forceinline__ void fail(volatile int* abort_flag, int32_t* status) {
@@ -131,45 +179,42 @@ __device__ __forceinline__ void fail(volatile int* abort_flag, int32_t* status) 
   report(status, MLA_ERR_TIMEOUT);
 }
 
-template <bool kHalf, int kQBoxes>
+template <bool kHalf, int kQBoxes, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                   const __grid_constant__ CUtensorMap v_map, const PromptParams p) {
-  using L = Layout<kQBoxes>;
-  // tiles longest first, every head of a tile before the next one: the last CTAs
-  // to start are the short ones of all heads
-  const int item = blockIdx.x / p.h_q;
-  const int head = blockIdx.x - item * p.h_q;
-  if (item >= p.plan[0]) return;
-  const int causal = p.plan[1];
-  const int4* e = reinterpret_cast<const int4*>(p.plan + kTileInts * (item + 1));
-  const int4 e0 = e[0];
-  const Tile t{e0.x, e0.y, e0.z, e0.w, e[1].x};
+  using L = Layout<kQBoxes, kPair>;
+  const uint32_t rank = kPair ? cluster_ctarank() : 0u;
+  const int worker = kPair ? blockIdx.x >> 1 : blockIdx.x;
+  const int workers = kPair ? gridDim.x >> 1 : gridDim.x;
 
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
   uint8_t* sQ = smem;
-  uint8_t* sRing = smem + L::kOffRing;
+  uint8_t* sK = smem + L::kOffK;
+  uint8_t* sV = smem + L::kOffV;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffMisc + 4);
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5, lane = tid & 31;
-  const int n0 = half_tiles(t, 0, causal), n1 = half_tiles(t, 1, causal);
-  const int n = max(n0, n1);
 
   if (tid == 0) {
     *abort_flag = 0;
-    mbar_init(&bars[Q_FULL], 1);
-    for (int i = 0; i < kRing; ++i) {
-      mbar_init(&bars[R_FULL + i], 1);
-      mbar_init(&bars[R_EMPTY + i], 1);
+    constexpr uint32_t kCtas = kPair ? 2 : 1;  // loaders that fill a stage, each its part
+    mbar_init(&bars[Q_FULL], kCtas);
+    mbar_init(&bars[Q_EMPTY], 1);
+    for (int i = 0; i < kMaxStages; ++i) {
+      mbar_init(&bars[K_FULL + i], kCtas);
+      mbar_init(&bars[K_EMPTY + i], 1);
+      mbar_init(&bars[V_FULL + i], kCtas);
+      mbar_init(&bars[V_EMPTY + i], 1);
     }
     for (int h = 0; h < 2; ++h) {
       mbar_init(&bars[S_FULL + h], 1);
-      mbar_init(&bars[P_FULL + h], 128);
+      mbar_init(&bars[P_FULL + h], 4 * kCtas);
       mbar_init(&bars[O_FULL + h], 1);
     }
     mbar_init(&bars[TAIL], 1);
@@ -177,8 +222,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init_cluster();
   }
   if (warp == kWarpMma) {
-    tmem_alloc(tmem_slot, kTmemCols);
-    tmem_relinquish();
+    if constexpr (kPair) {
+      tmem2_alloc(tmem_slot, kTmemCols);
+      tmem2_relinquish();
+    } else {
+      tmem_alloc(tmem_slot, kTmemCols);
+      tmem_relinquish();
+    }
   }
   if (warp == kWarpLoad && lane == 0) {
     prefetch_tmap(&q_map);
@@ -188,248 +238,320 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if constexpr (kPair) {  // the other CTA's barriers are ready before anything arrives there
+    cluster_arrive();
+    cluster_wait();
+  }
   const uint32_t tmem = *tmem_slot;
+  Items it = first_item(p, worker);
 
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
   if (warp == kWarpLoad) {
     // ------------------------------------------------------------ loads
-    const int kvh = head / p.group;
     bool ok = true;
-    uint32_t fill = 0;  // ring boxes issued
-    const int halves = t.rows > kBM ? 2 : 1;
-    bool q_issued = false;
-    if (lane == 0 && n > 0) {
-      const uint64_t pol = policy_evict_first();
-      mbar_arrive_expect_tx(&bars[Q_FULL], halves * kQBoxes * kBoxBytes);
-      for (int h = 0; h < halves; ++h)
-        for (int s = 0; s < kQBoxes; ++s)
-          tma_load_3d(sQ + (h * kQBoxes + s) * kBoxBytes, &q_map, &bars[Q_FULL], 64 * s, head, t.q0 + h * kBM, pol);
-      q_issued = true;
-    }
-    const uint64_t pol_kv = policy_evict_last();
-    // one box into the next slot; the tail's boxes complete on their own barrier
-    auto box = [&](const CUtensorMap* map, int col, int row, bool tail) {
-      const int s = static_cast<int>(fill % kRing);
-      const uint32_t round = fill / kRing;
-      if (round >= 1) ok = mbar_wait(&bars[R_EMPTY + s], (round - 1) & 1, abort_flag);
-      if (!ok) return;
-      uint64_t* bar = tail ? &bars[TAIL] : &bars[R_FULL + s];
-      if (!tail) mbar_arrive_expect_tx(bar, kBoxBytes);
-      tma_load_3d(sRing + s * kBoxBytes, map, bar, col, kvh, row, pol_kv);
-      ++fill;
+    uint32_t kn = 0, vn = 0, qn = 0, tails = 0;  // stages and items loaded so far
+    const uint64_t pol_q = policy_evict_first(), pol_kv = policy_evict_last();
+    // The barriers that count loads are the even CTA's: its MMA warp waits for
+    // both CTAs' parts there.
+    const uint32_t bar0 = kPair ? mapa_shared(smem_u32(bars), 0) : smem_u32(bars);
+    auto expect = [&](int bar, uint32_t bytes) {
+      if constexpr (kPair)
+        mbar_arrive_expect_tx_remote(bar0 + 8 * bar, bytes);
+      else
+        mbar_arrive_expect_tx(&bars[bar], bytes);
     };
-    bool tail_issued = false;
-    for (int j = 0; j < n && ok; ++j) {
-      const bool tail = (j + 1) * kBN > t.lk;  // the sequence ends inside this tile
-      if (lane == 0) {
-        for (int s = 0; s < kQBoxes && ok; ++s) box(&k_map, 64 * s, t.k0 + j * kBN, false);
-        if (tail && ok) {
-          mbar_arrive_expect_tx(&bars[TAIL], kVBoxes * kBoxBytes);
-          tail_issued = true;
+    auto load = [&](uint8_t* dst, const CUtensorMap* map, int bar, int c0, int c1, int c2, uint64_t pol) {
+      if constexpr (kPair)
+        tma_load_3d_pair(dst, map, bar0 + 8 * bar, c0, c1, c2, pol);
+      else
+        tma_load_3d(dst, map, &bars[bar], c0, c1, c2, pol);
+    };
+    for (; it.at < it.total && ok; next_item(it, worker, workers)) {
+      const Tile t = load_tile(p, it);
+      const int head = it.at % p.h_q, kvh = head / p.group;
+      const int n = max(half_tiles(t, 0, L::kHalfRows, it.causal), half_tiles(t, 1, L::kHalfRows, it.causal));
+      for (int j = 0; j < n && ok; ++j) {
+        const bool tail = (j + 1) * kBN > t.lk;  // the sequence ends inside this tile
+        uint8_t* vdst = nullptr;
+        int vbar = 0;
+        if (lane == 0) {
+          const int ks = static_cast<int>(kn % L::kKStages), kr = static_cast<int>(kn / L::kKStages);
+          if (kr >= 1) ok = mbar_wait(&bars[K_EMPTY + ks], (kr - 1) & 1, abort_flag);
+          if (ok) {
+            expect(K_FULL + ks, L::kKBytes);
+            for (int s = 0; s < kQBoxes; ++s)
+              load(sK + ks * L::kKBytes + s * L::kKBoxBytes, &k_map, K_FULL + ks, 64 * s, kvh,
+                   t.k0 + j * kBN + static_cast<int>(rank) * L::kKeys, pol_kv);
+          }
+          if (j == 0 && ok) {
+            // both halves' boxes, also those past the sequence's last query (their rows are not stored)
+            if (qn >= 1) ok = mbar_wait(&bars[Q_EMPTY], (qn - 1) & 1, abort_flag);
+            if (ok) {
+              const int halves = t.rows > L::kHalfRows ? 2 : 1;
+              expect(Q_FULL, halves * kQBoxes * kBoxBytes);
+              for (int h = 0; h < halves; ++h)
+                for (int s = 0; s < kQBoxes; ++s)
+                  load(sQ + (h * kQBoxes + s) * kBoxBytes, &q_map, Q_FULL, 64 * s, head,
+                       t.q0 + h * L::kHalfRows + static_cast<int>(rank) * kBM, pol_q);
+            }
+          }
         }
-        // where the two V boxes wrap around the ring, dims 0-63 take slot 0, so
-        // that they come first in shared memory too
-        const int swap = fill % kRing == kRing - 1 ? 1 : 0;
-        for (int s = 0; s < kVBoxes && ok; ++s) box(&v_map, 64 * (s ^ swap), t.k0 + j * kBN, tail);
-      }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      fill = __shfl_sync(0xffffffffu, fill, 0);
-      if (tail && ok) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars[TAIL], 0, abort_flag));
-        if (ok) {
+        const int vs = static_cast<int>(vn % L::kVStages), vr = static_cast<int>(vn / L::kVStages);
+        vdst = sV + vs * L::kVBytes;
+        vbar = V_FULL + vs;
+        if (lane == 0 && ok) {
+          if (vr >= 1) ok = mbar_wait(&bars[V_EMPTY + vs], (vr - 1) & 1, abort_flag);
+          if (ok) {
+            if (tail)
+              mbar_arrive_expect_tx(&bars[TAIL], L::kVBytes);
+            else
+              expect(vbar, L::kVBytes);
+            for (int b = 0; b < L::kVBoxes; ++b) {
+              const int col = 64 * (kPair ? static_cast<int>(rank) : b);
+              if (tail)  // onto this CTA's own barrier
+                tma_load_3d(vdst + b * kBoxBytes, &v_map, &bars[TAIL], col, kvh, t.k0 + j * kBN, pol_kv);
+              else
+                load(vdst + b * kBoxBytes, &v_map, vbar, col, kvh, t.k0 + j * kBN, pol_kv);
+            }
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        ++kn;
+        ++vn;
+        if (tail) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars[TAIL], tails & 1, abort_flag));
+          ++tails;
+          if (!ok) break;
           const int keep = t.lk - j * kBN;  // rows of this tile that are the sequence's
-          for (int b = 0; b < kVBoxes; ++b) {
-            const int s = static_cast<int>((fill - kVBoxes + b) % kRing);
-            uint4* dst = reinterpret_cast<uint4*>(sRing + s * kBoxBytes + keep * 128);
+          for (int b = 0; b < L::kVBoxes; ++b) {
+            uint4* dst = reinterpret_cast<uint4*>(vdst + b * kBoxBytes + keep * 128);
             for (int i = lane; i < (kBN - keep) * 8; i += 32) dst[i] = make_uint4(0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0)
-            for (int b = 0; b < kVBoxes; ++b)
-              mbar_arrive(&bars[R_FULL + static_cast<int>((fill - kVBoxes + b) % kRing)]);
+          if (lane == 0) {
+            if constexpr (kPair)
+              mbar_arrive_remote(bar0 + 8 * vbar);
+            else
+              mbar_arrive(&bars[vbar]);
+          }
         }
       }
+      if (n > 0) ++qn;
     }
-    if (lane == 0) {
-      if (!ok) fail(abort_flag, p.status);
-      // no TMA write may land after this CTA exits
-      if (q_issued) mbar_wait(&bars[Q_FULL], 0, nullptr);
-      if (!ok) {
-        if (tail_issued) mbar_wait(&bars[TAIL], 0, nullptr);
-        for (uint32_t s = 0; s < kRing && s < fill; ++s) {
-          const uint32_t last = (fill - 1 - s) / kRing;  // the slot's last round
-          mbar_wait(&bars[R_FULL + s], last & 1, nullptr, 1000000);
-        }
+    if (!ok && lane == 0) {
+      fail(abort_flag, p.status);
+      // copies in flight land (bounded) before this CTA may end
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 1000000ull) {
       }
     }
     __syncwarp();
   } else if (warp == kWarpMma) {
     // ------------------------------------------------------------ MMAs
-    // the whole warp runs this loop (see umma_f16_warp); its control flow and
-    // every operand are the same in all lanes
-    if (n > 0) {
+    // The even CTA's warp issues for the pair.  The whole warp runs this loop
+    // (see umma_f16_warp); its control flow and operands are the same in all lanes.
+    if (rank == 0) {
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-      constexpr uint32_t idesc_qk = idesc_16bit_f32(128, kBN, false, kHalf);
-      constexpr uint32_t idesc_pv = idesc_16bit_f32(128, 128, true, kHalf);
+      constexpr uint32_t kM = kPair ? 256 : 128;
+      constexpr uint32_t idesc_qk = idesc_16bit_f32(kM, kBN, false, kHalf);
+      constexpr uint32_t idesc_pv = idesc_16bit_f32(kM, 128, true, kHalf);
       const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024);
-      const uint64_t k_desc = sdesc_sw128(smem_u32(sRing), 16, 1024);
+      const uint64_t k_desc = sdesc_sw128(smem_u32(sK), 16, 1024);
+      const uint64_t v_desc = sdesc_sw128(smem_u32(sV), kBoxBytes, 1024);  // MN-major
       auto wait = [&](int bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait(&bars[bar], parity, abort_flag));
+        return __all_sync(0xffffffffu, mbar_wait<kPair>(&bars[bar], parity, abort_flag));
       };
-      bool ok = wait(Q_FULL, 0);
-      uint32_t use = 0;  // ring boxes waited for
-      uint32_t k_at = 0, v_at = 0;
-      auto wait_boxes = [&](int count) {
-        const uint32_t at = use;
-        for (int i = 0; i < count && ok; ++i, ++use)
-          ok = wait(R_FULL + use % kRing, (use / kRing) & 1);
-        return at;
+      auto commit = [&](int bar) {
+        if constexpr (kPair)
+          umma2_commit_warp(&bars[bar]);
+        else
+          umma_commit_warp(&bars[bar]);
       };
-      for (int j = 0; j <= n && ok; ++j) {
-        // boxes in load order: V(j-1) before K(j)
-        bool have_v = false, have_k = false;
-#pragma unroll 1
-        for (int h = 0; h < 2 && ok; ++h) {
-          const int nh = h ? n1 : n0;
-          const uint32_t s_col = tm + 128u * h, o_col = tm + 256u + 128u * h;
-          if (j >= 1 && j - 1 < nh) {
-            if (!have_v) {
-              v_at = wait_boxes(kVBoxes);
+      bool ok = true;
+      uint32_t kn = 0, vn = 0, qn = 0, tiles[2] = {0, 0};
+      for (; it.at < it.total && ok; next_item(it, worker, workers)) {
+        const Tile t = load_tile(p, it);
+        const int n0 = half_tiles(t, 0, L::kHalfRows, it.causal), n1 = half_tiles(t, 1, L::kHalfRows, it.causal);
+        const int n = max(n0, n1);
+        if (n == 0) continue;
+        for (int j = 0; j <= n && ok; ++j) {
+          bool have_v = false, have_k = false;
+          const int ks = static_cast<int>(kn % L::kKStages);
+          const int vs = static_cast<int>(vn % L::kVStages);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int nh = h ? n1 : n0;
+            const uint32_t s_col = tm + 128u * h, o_col = tm + 256u + 128u * h;
+            if (ok && j >= 1 && j - 1 < nh) {
+              if (!have_v) ok = wait(V_FULL + vs, (vn / L::kVStages) & 1);
               have_v = true;
-            }
-            if (ok) ok = wait(P_FULL + h, (j - 1) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            // V as the MN-major B operand: dims 0-63 in one box, 64-127 in the
-            // next, or (where the ring wraps) seven boxes further on
-            const uint32_t s0 = v_at % kRing;
-            const bool wrap = s0 == kRing - 1;
-            const uint64_t vd = sdesc_sw128(smem_u32(sRing + (wrap ? 0u : s0) * kBoxBytes),
-                                            (wrap ? kRing - 1 : 1) * kBoxBytes, 1024);
+              if (ok) ok = wait(P_FULL + h, (tiles[h] - 1) & 1);
+              if (ok) {
+                tc_fence_after();
+                const uint64_t vd = v_desc + static_cast<uint64_t>((vs * L::kVBytes) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < kBN / 16; ++kk)
-              umma_f16_ts_warp(o_col, s_col + 8u * kk, vd + static_cast<uint64_t>((kk * 2048) >> 4), idesc_pv,
-                          (j == 1 && kk == 0) ? 0u : 1u);
-            if (j == nh) umma_commit_warp(&bars[O_FULL + h]);
-          }
-          if (j < nh) {
-            if (!have_k) {
-              k_at = wait_boxes(kQBoxes);
+                for (int kk = 0; kk < kBN / 16; ++kk) {
+                  const uint32_t acc = (j == 1 && kk == 0) ? 0u : 1u;
+                  if constexpr (kPair)
+                    umma2_f16_ts_warp(o_col, s_col + 8u * kk, vd + static_cast<uint64_t>((kk * 2048) >> 4), idesc_pv,
+                                      acc);
+                  else
+                    umma_f16_ts_warp(o_col, s_col + 8u * kk, vd + static_cast<uint64_t>((kk * 2048) >> 4), idesc_pv,
+                                     acc);
+                }
+                if (j == nh) commit(O_FULL + h);
+                if (h == 1 || j - 1 >= n1) commit(V_EMPTY + vs);  // read for the last time
+              }
+            }
+            if (ok && j < nh) {
+              if (!have_k) {
+                if (j == 0) ok = wait(Q_FULL, qn & 1);
+                if (ok) ok = wait(K_FULL + ks, (kn / L::kKStages) & 1);
+              }
               have_k = true;
-            }
-            if (!ok) break;
-            tc_fence_after();
+              if (ok) {
+                tc_fence_after();
+                const uint64_t kd0 = k_desc + static_cast<uint64_t>((ks * L::kKBytes) >> 4);
 #pragma unroll
-            for (int s = 0; s < kQBoxes; ++s) {
-              const uint64_t kd = k_desc + static_cast<uint64_t>((((k_at + s) % kRing) * kBoxBytes) >> 4);
-              const uint64_t qd = q_desc + static_cast<uint64_t>(((h * kQBoxes + s) * kBoxBytes) >> 4);
+                for (int s = 0; s < kQBoxes; ++s) {
+                  const uint64_t kd = kd0 + static_cast<uint64_t>((s * L::kKBoxBytes) >> 4);
+                  const uint64_t qd = q_desc + static_cast<uint64_t>(((h * kQBoxes + s) * kBoxBytes) >> 4);
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                umma_f16_warp(s_col, qd + static_cast<uint64_t>((kk * 32) >> 4), kd + static_cast<uint64_t>((kk * 32) >> 4),
-                         idesc_qk, (s == 0 && kk == 0) ? 0u : 1u);
+                  for (int kk = 0; kk < 4; ++kk) {
+                    const uint32_t acc = (s == 0 && kk == 0) ? 0u : 1u;
+                    if constexpr (kPair)
+                      umma2_f16_warp(s_col, qd + static_cast<uint64_t>((kk * 32) >> 4),
+                                     kd + static_cast<uint64_t>((kk * 32) >> 4), idesc_qk, acc);
+                    else
+                      umma_f16_warp(s_col, qd + static_cast<uint64_t>((kk * 32) >> 4),
+                                    kd + static_cast<uint64_t>((kk * 32) >> 4), idesc_qk, acc);
+                  }
+                }
+                commit(S_FULL + h);
+                ++tiles[h];
+                if (h == 1 || j >= n1) {
+                  commit(K_EMPTY + ks);
+                  if (j == n - 1) commit(Q_EMPTY);
+                }
+              }
             }
-            umma_commit_warp(&bars[S_FULL + h]);
           }
+          if (j >= 1) ++vn;
+          if (j < n) ++kn;
         }
-        if (!ok) break;
-        if (have_v)
-          for (int b = 0; b < kVBoxes; ++b) umma_commit_warp(&bars[R_EMPTY + (v_at + b) % kRing]);
-        if (have_k)
-          for (int s = 0; s < kQBoxes; ++s) umma_commit_warp(&bars[R_EMPTY + (k_at + s) % kRing]);
+        ++qn;
       }
       if (!ok && lane == 0) fail(abort_flag, p.status);
       // every MMA is done with shared memory and TMEM before this CTA ends
-      umma_commit_warp(&bars[DRAIN]);
-      mbar_wait(&bars[DRAIN], 0, nullptr);
+      commit(DRAIN);
+      mbar_wait<kPair>(&bars[DRAIN], 0, nullptr);
     }
     __syncwarp();
+  }
   } else {
     // ------------------------------------------------------------ softmax + epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int h = warp >> 2;
-    const int r = tid & 127;  // row of the half == TMEM lane
-    const int row = h * kBM + r;
-    const int nh = h ? n1 : n0;
     const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t s_addr = tmem + lane_base + 128u * h;
     const uint32_t o_addr = tmem + lane_base + 256u + 128u * h;
-    const bool row_ok = row < t.rows;
-    const int limit = causal ? min(t.lk, t.vis + row) : t.lk;  // keys this row sees
+    // this thread's row of every tile (TMEM lane tid % 128 of this CTA)
+    const int row = h * L::kHalfRows + static_cast<int>(rank) * kBM + (tid & 127);
+    const uint32_t p_full = kPair ? mapa_shared(smem_u32(&bars[P_FULL + h]), 0) : smem_u32(&bars[P_FULL + h]);
     const float c_log2 = p.scale_log2;
-    float ref = -INFINITY, l = 0.f;
     bool ok = true;
-    for (int j = 0; j < nh; ++j) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&bars[S_FULL + h], j & 1, abort_flag));
-      if (!ok) break;
-      tc_fence_after();
-      float s[kBN];
-      float mx[4];
+    uint32_t tiles = 0, items = 0;
+    Tile t = load_tile(p, it);
+    while (it.at < it.total) {
+      const int nh = half_tiles(t, h, L::kHalfRows, it.causal);
+      const int limit = it.causal ? min(t.lk, t.vis + row) : t.lk;  // keys this row sees
+      float ref = -INFINITY, l = 0.f;
+      for (int j = 0; j < nh; ++j, ++tiles) {
+        ok = __all_sync(0xffffffffu, mbar_wait<kPair>(&bars[S_FULL + h], tiles & 1, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        float s[kBN];
+        float mx[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32_max(s_addr + 32u * c, s + 32 * c, mx[c]);
-      tmem_wait_ld();
-      float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      const int seen = limit - j * kBN;
-      if (__any_sync(0xffffffffu, seen < kBN)) {
-        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        for (int c = 0; c < 4; ++c) tmem_ld32_max(s_addr + 32u * c, s + 32 * c, mx[c]);
+        tmem_wait_ld();
+        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const int seen = limit - j * kBN;
+        if (__any_sync(0xffffffffu, seen < kBN)) {
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < kBN; ++i) {
-          s[i] = i < seen ? s[i] : -INFINITY;
-          m4[i & 3] = fmaxf(m4[i & 3], s[i]);
+          for (int i = 0; i < kBN; ++i) {
+            s[i] = i < seen ? s[i] : -INFINITY;
+            m4[i & 3] = fmaxf(m4[i & 3], s[i]);
+          }
+          top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         }
-        top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-      }
-      const float mt = top * c_log2;
-      const float r_new = mt > ref + kTau ? mt : ref;
-      const float alpha = r_new == ref ? 1.f : ex2(ref - r_new);
-      // P V of the tile before is done (see above): O may be rescaled here
-      if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+        const float mt = top * c_log2;
+        const float r_new = mt > ref + kTau ? mt : ref;
+        const float alpha = r_new == ref ? 1.f : ex2(ref - r_new);
+        // P V of the tile before is done (see above): O may be rescaled here
+        if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
-        for (uint32_t c0 = 0; c0 < 128; c0 += 16) {
-          uint32_t v[16];
-          tmem_ld16(o_addr + c0, v);
-          tmem_wait_ld();
+          for (uint32_t c0 = 0; c0 < 128; c0 += 16) {
+            uint32_t v[16];
+            tmem_ld16(o_addr + c0, v);
+            tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
-          tmem_st16(o_addr + c0, v);
+            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
+            tmem_st16(o_addr + c0, v);
+          }
+        }
+        ref = r_new;
+        const float mref = ref == -INFINITY ? 0.f : ref;
+        float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float2 cl = make_float2(c_log2, c_log2), nr = make_float2(-mref, -mref);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 x = __ffma2_rn(make_float2(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), cl, nr);
+            const float p0 = ex2(x.x), p1 = ex2(x.y);
+            pk[i] = pack2<kHalf>(p0, p1);
+            ls[i & 1] = __fadd2_rn(ls[i & 1], make_float2(p0, p1));
+          }
+          tmem_st16(s_addr + 16u * c, pk);
+        }
+        l = l * alpha + ((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y));
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (kPair)
+            mbar_arrive_remote(p_full);
+          else
+            mbar_arrive(&bars[P_FULL + h]);
         }
       }
-      ref = r_new;
-      const float mref = ref == -INFINITY ? 0.f : ref;
-      float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      const float2 cl = make_float2(c_log2, c_log2), nr = make_float2(-mref, -mref);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 x = __ffma2_rn(make_float2(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), cl, nr);
-          const float p0 = ex2(x.x), p1 = ex2(x.y);
-          pk[i] = pack2<kHalf>(p0, p1);
-          ls[i & 1] = __fadd2_rn(ls[i & 1], make_float2(p0, p1));
-        }
-        tmem_st16(s_addr + 16u * c, pk);
+      if (!ok) break;
+      // the next item's tile is on its way during this one's epilogue
+      const int head = it.at % p.h_q;
+      next_item(it, worker, workers);
+      const Tile t_next = load_tile(p, it);
+      if (nh > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait<kPair>(&bars[O_FULL + h], items & 1, abort_flag));
+        if (!ok) break;
+        ++items;
+        tc_fence_after();
       }
-      l = l * alpha + ((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y));
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(&bars[P_FULL + h]);
-    }
-    if (ok && nh > 0) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&bars[O_FULL + h], 0, abort_flag));
-      tc_fence_after();
-    }
-    if (ok) {
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const size_t orow = static_cast<size_t>(t.q0 + row) * p.h_q + head;
       uint16_t* out = static_cast<uint16_t*>(p.out) + orow * 128;
+      const bool row_ok = row < t.rows;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         uint32_t v[32];
         if (nh > 0) {
           tmem_ld32(o_addr + 32u * c, v);
           tmem_wait_ld();
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0u;
         }
         if (row_ok) {
 #pragma unroll
@@ -437,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              // a row without keys has l = 0 and an untouched or zero sum: 0 by selection
+              // a row that sees no key: 0 by selection, whatever the accumulator holds
               const float a = __uint_as_float(v[8 * q + 2 * i]) * inv, b = __uint_as_float(v[8 * q + 2 * i + 1]) * inv;
               w[i] = limit > 0 ? pack2<kHalf>(a, b) : 0u;
             }
@@ -446,17 +568,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (row_ok) p.lse[orow] = limit > 0 ? (ref + __log2f(l)) * kLn2 : -INFINITY;
-    } else if (lane == 0) {
-      fail(abort_flag, p.status);
+      // O has been read: the next item's first P V waits for this warp's P
+      tc_fence_before();
+      t = t_next;
     }
+    if (!ok && lane == 0) fail(abort_flag, p.status);
   }
 
   // ------------------------------------------------------------ teardown
   tc_fence_before();
   __syncthreads();
+  if constexpr (kPair) {  // the other CTA loads, arrives and multiplies here no more
+    cluster_arrive();
+    cluster_wait();
+  }
   if (warp == kWarpMma) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    if constexpr (kPair)
+      tmem2_dealloc(tmem, kTmemCols);
+    else
+      tmem_dealloc(tmem, kTmemCols);
+  }
+  if constexpr (kPair) {  // neither CTA ends while the other gives TMEM back
+    cluster_arrive();
+    cluster_wait();
   }
 }
 
@@ -483,7 +618,7 @@ __device__ __forceinline__ bool seq_bounds(const int32_t* cu, int b, int total, 
 // first.  The order within a bin is by chance; no result depends on it.
 __global__ void __launch_bounds__(kPlanThreads)
     prompt_plan_kernel(const int32_t* cu_q, const int32_t* cu_k, int batch, int total_q, int total_k, int causal,
-                       int max_tiles, int32_t* plan, int32_t* status) {
+                       int tile_q, int max_tiles, int32_t* plan, int32_t* status) {
   __shared__ int bin[kBins];
   __shared__ int warp_sum[32];
   __shared__ int longest, broken;
@@ -504,10 +639,10 @@ __global__ void __launch_bounds__(kPlanThreads)
         lq = 0;
         broken = 1;
       }
-      for (int m = lane; m * kTileQ < lq; m += 32) {
-        const int row0 = m * kTileQ;
+      for (int m = lane; m * tile_q < lq; m += 32) {
+        const int row0 = m * tile_q;
         const Tile t{q0 + row0, lq - row0, k0, lk, lk - lq + row0 + 1};
-        f(t, max(half_tiles(t, 0, causal), half_tiles(t, 1, causal)));
+        f(t, max(half_tiles(t, 0, tile_q / 2, causal), half_tiles(t, 1, tile_q / 2, causal)));
       }
     }
   };
@@ -548,7 +683,13 @@ static_assert(kBins == kPlanThreads, "one bin a thread");
 
 }  // namespace pr
 
-int prompt_plan_tiles(int batch, int total_q) { return total_q / pr::kTileQ + batch; }
+// Pairs of CTAs on 512-query tiles where prompts are longer than one CTA's 256
+// queries on average, else CTAs on 256.
+bool prompt_pairs(int batch, int total_q) { return total_q / batch > 256; }
+namespace {
+int prompt_tile_q(int batch, int total_q) { return prompt_pairs(batch, total_q) ? 512 : 256; }
+}  // namespace
+int prompt_plan_tiles(int batch, int total_q) { return total_q / prompt_tile_q(batch, total_q) + batch; }
 size_t prompt_plan_bytes(int batch, int total_q) {
   return static_cast<size_t>(prompt_plan_tiles(batch, total_q) + 1) * pr::kTileInts * 4;
 }
@@ -556,41 +697,60 @@ size_t prompt_plan_bytes(int batch, int total_q) {
 cudaError_t launch_prompt_plan(const int32_t* cu_q, const int32_t* cu_k, int batch, int total_q, int total_k,
                                int causal, void* plan, int32_t* status, cudaStream_t st) {
   pr::prompt_plan_kernel<<<1, pr::kPlanThreads, 0, st>>>(cu_q, cu_k, batch, total_q, total_k, causal,
+                                                         prompt_tile_q(batch, total_q),
                                                          prompt_plan_tiles(batch, total_q),
                                                          static_cast<int32_t*>(plan), status);
   return cudaGetLastError();
 }
 
+namespace {
+
+using PromptKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, PromptParams);
+
+PromptKernel prompt_kernel_of(bool half, int d_qk, bool pair) {
+  if (d_qk == 192) {
+    if (half) return pair ? pr::prompt_kernel<true, 3, true> : pr::prompt_kernel<true, 3, false>;
+    return pair ? pr::prompt_kernel<false, 3, true> : pr::prompt_kernel<false, 3, false>;
+  }
+  if (half) return pair ? pr::prompt_kernel<true, 2, true> : pr::prompt_kernel<true, 2, false>;
+  return pair ? pr::prompt_kernel<false, 2, true> : pr::prompt_kernel<false, 2, false>;
+}
+
+int prompt_smem(int d_qk, bool pair) {
+  return d_qk == 192 ? (pair ? pr::Layout<3, true>::kBytes : pr::Layout<3, false>::kBytes)
+                     : (pair ? pr::Layout<2, true>::kBytes : pr::Layout<2, false>::kBytes);
+}
+
+}  // namespace
+
 cudaError_t prompt_setup() {
-  cudaError_t e;
-  if ((e = cudaFuncSetAttribute(pr::prompt_kernel<false, 3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                pr::Layout<3>::kBytes)) != cudaSuccess)
-    return e;
-  if ((e = cudaFuncSetAttribute(pr::prompt_kernel<true, 3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                pr::Layout<3>::kBytes)) != cudaSuccess)
-    return e;
-  if ((e = cudaFuncSetAttribute(pr::prompt_kernel<false, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                pr::Layout<2>::kBytes)) != cudaSuccess)
-    return e;
-  return cudaFuncSetAttribute(pr::prompt_kernel<true, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              pr::Layout<2>::kBytes);
+  for (int v = 0; v < 8; ++v) {
+    const int d_qk = v & 1 ? 192 : 128;
+    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(prompt_kernel_of(v & 2, d_qk, v & 4)),
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, prompt_smem(d_qk, v & 4));
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t launch_prompt(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PromptParams& p,
-                          bool half, int d_qk, cudaStream_t st) {
-  const int grid = p.max_tiles * p.h_q;
-  if (d_qk == 192) {
-    if (half)
-      pr::prompt_kernel<true, 3><<<grid, pr::kThreads, pr::Layout<3>::kBytes, st>>>(q, k, v, p);
-    else
-      pr::prompt_kernel<false, 3><<<grid, pr::kThreads, pr::Layout<3>::kBytes, st>>>(q, k, v, p);
-  } else {
-    if (half)
-      pr::prompt_kernel<true, 2><<<grid, pr::kThreads, pr::Layout<2>::kBytes, st>>>(q, k, v, p);
-    else
-      pr::prompt_kernel<false, 2><<<grid, pr::kThreads, pr::Layout<2>::kBytes, st>>>(q, k, v, p);
-  }
-  return cudaGetLastError();
+                          bool half, int d_qk, bool pair, int sms, cudaStream_t st) {
+  const int ctas = pair ? 2 : 1;
+  const long long items = static_cast<long long>(p.max_tiles) * p.h_q;
+  const int workers = static_cast<int>(items < sms / ctas ? items : sms / ctas);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(workers * ctas), 1, 1);
+  cfg.blockDim = dim3(pr::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = prompt_smem(d_qk, pair);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prompt_kernel_of(half, d_qk, pair), q, k, v, p);
 }
 
 }  // namespace mla

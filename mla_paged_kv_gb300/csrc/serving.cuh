@@ -92,11 +92,12 @@ struct PromptParams {
   int32_t* status;
 };
 size_t prompt_plan_bytes(int batch, int total_q);
+bool prompt_pairs(int batch, int total_q);  // CTA pairs on 512 queries (else CTAs on 256)
 int prompt_plan_tiles(int batch, int total_q);
 cudaError_t launch_prompt_plan(const int32_t* cu_q, const int32_t* cu_k, int batch, int total_q, int total_k,
                                int causal, void* plan, int32_t* status, cudaStream_t st);
 cudaError_t prompt_setup();  // once per device: shared-memory opt-in
 cudaError_t launch_prompt(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PromptParams& p,
-                          bool half, int d_qk, cudaStream_t st);
+                          bool half, int d_qk, bool pair, int sms, cudaStream_t st);
 
 }  // namespace mla

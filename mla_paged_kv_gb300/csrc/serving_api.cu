@@ -37,12 +37,12 @@ int check_list(const int32_t* a, const int32_t* b, int n) {
   return n > kMaxPageList ? MLA_ERR_UNSUPPORTED : MLA_OK;
 }
 
-int prompt_device() {
+int prompt_device(int* sms) {
   constexpr int kMaxDevices = 64;
   static bool done[kMaxDevices] = {};
   static std::mutex mu;
-  int sms = 0, dev = -1;
-  const int rc = device_ready(&sms);
+  int dev = -1;
+  const int rc = device_ready(sms);
   if (rc != MLA_OK) return rc;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MLA_ERR_CUDA;
   std::lock_guard<std::mutex> lock(mu);
@@ -57,16 +57,16 @@ int prompt_device() {
 }
 
 // [total, heads, dim] of 16-bit elements, viewed as (dim, heads, total); one
-// box = 64 dims of 128 rows of one head.
+// box = 64 dims of `rows` rows of one head.
 int head_map(CUtensorMap* m, const void* base, long long total, int heads, int dim, long long token_stride,
-             long long head_stride) {
+             long long head_stride, unsigned rows) {
   // a stride that no second index uses may be anything: take a legal one
   if (heads == 1) head_stride = dim;
   if (total == 1) token_stride = static_cast<long long>(heads) * head_stride;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads),
                               static_cast<cuuint64_t>(total)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_stride) * 2, static_cast<cuuint64_t>(token_stride) * 2};
-  const cuuint32_t box[3] = {64, 1, 128};
+  const cuuint32_t box[3] = {64, 1, rows};
   return encode_map16(m, base, 3, dims, strides, box);
 }
 
@@ -273,8 +273,9 @@ int mla_prompt_attention_fwd(const void* d_q, long long q_token_stride, long lon
   if (total_q > (1 << 30) || total_k > (1 << 30) || batch > (1 << 20)) return MLA_ERR_UNSUPPORTED;
   if (plan_bytes < prompt_plan_bytes(batch, total_q)) return MLA_ERR_INVALID_ARG;
   const int tiles = prompt_plan_tiles(batch, total_q);
-  if (static_cast<long long>(tiles) * h_q > kMaxInt) return MLA_ERR_UNSUPPORTED;
-  const int rc0 = prompt_device();
+  if (static_cast<long long>(tiles) * h_q > (1 << 30)) return MLA_ERR_UNSUPPORTED;
+  int sms = 0;
+  const int rc0 = prompt_device(&sms);
   if (rc0 != MLA_OK || total_q == 0) return rc0;
   PromptParams p{};
   p.plan = static_cast<const int32_t*>(d_plan);
@@ -286,17 +287,18 @@ int mla_prompt_attention_fwd(const void* d_q, long long q_token_stride, long lon
   p.out = d_out;
   p.lse = d_lse;
   p.status = d_status;
+  const bool pair = prompt_pairs(batch, total_q);
   CUtensorMap qm, km, vm;
-  int rc = head_map(&qm, d_q, total_q, h_q, d_qk, q_token_stride, q_head_stride);
-  // without any key no CTA loads K or V: any valid map serves
-  if (rc == MLA_OK)
-    rc = total_k > 0 ? head_map(&km, d_k, total_k, h_kv, d_qk, k_token_stride, k_head_stride)
-                     : head_map(&km, d_q, total_q, h_q, d_qk, q_token_stride, q_head_stride);
-  if (rc == MLA_OK)
-    rc = total_k > 0 ? head_map(&vm, d_v, total_k, h_kv, 128, v_token_stride, v_head_stride)
-                     : head_map(&vm, d_q, total_q, h_q, d_qk, q_token_stride, q_head_stride);
+  int rc = head_map(&qm, d_q, total_q, h_q, d_qk, q_token_stride, q_head_stride, 128);
+  if (total_k == 0) {  // no CTA loads K or V: any valid map serves
+    km = vm = qm;
+  } else {
+    // a pair's CTAs load 64 keys each, and all 128 for their half of V's dims
+    if (rc == MLA_OK) rc = head_map(&km, d_k, total_k, h_kv, d_qk, k_token_stride, k_head_stride, pair ? 64 : 128);
+    if (rc == MLA_OK) rc = head_map(&vm, d_v, total_k, h_kv, 128, v_token_stride, v_head_stride, 128);
+  }
   if (rc != MLA_OK) return rc;
-  return launched(launch_prompt(qm, km, vm, p, dtype == MLA_DTYPE_FP16, d_qk, to_stream(stream)));
+  return launched(launch_prompt(qm, km, vm, p, dtype == MLA_DTYPE_FP16, d_qk, pair, sms, to_stream(stream)));
 }
 
 size_t mla_shared_prefix_plan_bytes(int batch, int s_q, int h_q, int num_parts) {
