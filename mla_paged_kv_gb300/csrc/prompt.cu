@@ -50,12 +50,10 @@ constexpr int kBM = 128;              // query rows of a half in one CTA
 constexpr int kBN = 128;              // keys of a tile
 constexpr int kBoxBytes = 128 * 128;  // 128 rows x 64 16-bit values
 
-constexpr int kThreads = 384;  // three warpgroups: two of softmax warps, one for the loads and the MMAs
-constexpr int kWarpMma = 8, kWarpLoad = 9;
-// Registers: 384 threads start with 168 each; the third warpgroup gives 80 of
-// its own to the softmax threads, which hold a row of 128 scores
-// (2 x 128 x 208 + 128 x 88 = 384 x 168).
-constexpr int kRegsSoftmax = 208, kRegsOther = 88;
+// 16 softmax warps: two for each 32 rows of a half, 64 of the 128 keys each;
+// then the MMA warp, the warps that load K and Q and that load V, and a spare.
+constexpr int kThreads = 640;
+constexpr int kWarpMma = 16, kWarpK = 17, kWarpV = 18;
 constexpr int kMaxStages = 5;
 
 enum : int {
@@ -89,7 +87,8 @@ struct Layout {
   static constexpr int kOffV = kOffK + kKStages * kKBytes;
   static constexpr int kOffBar = kOffV + kVStages * kVBytes;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kBytes = kOffMisc + 16 + 1024;  // slack to align the base to 1024 B
+  static constexpr int kOffRow = kOffMisc + 16;                // one float per half, key half and row
+  static constexpr int kBytes = kOffRow + 2 * 2 * kBM * 4;
   static_assert(kBytes <= 232448, "shared memory budget");
   static_assert(kKStages <= kMaxStages && kVStages <= kMaxStages, "barriers");
 };
@@ -188,15 +187,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int worker = kPair ? blockIdx.x >> 1 : blockIdx.x;
   const int workers = kPair ? gridDim.x >> 1 : gridDim.x;
 
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw_addr = smem_u32(smem_raw);
-  uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  extern __shared__ __align__(1024) uint8_t smem[];  // swizzle atoms need 1024-byte alignment
   uint8_t* sQ = smem;
   uint8_t* sK = smem + L::kOffK;
   uint8_t* sV = smem + L::kOffV;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffMisc + 4);
+  float* sRow = reinterpret_cast<float*>(smem + L::kOffRow);
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5, lane = tid & 31;
@@ -214,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int h = 0; h < 2; ++h) {
       mbar_init(&bars[S_FULL + h], 1);
-      mbar_init(&bars[P_FULL + h], 4 * kCtas);
+      mbar_init(&bars[P_FULL + h], 8 * kCtas);
       mbar_init(&bars[O_FULL + h], 1);
     }
     mbar_init(&bars[TAIL], 1);
@@ -230,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_relinquish();
     }
   }
-  if (warp == kWarpLoad && lane == 0) {
+  if (warp == kWarpK && lane == 0) {
     prefetch_tmap(&q_map);
     prefetch_tmap(&k_map);
     prefetch_tmap(&v_map);
@@ -245,101 +243,91 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   Items it = first_item(p, worker);
 
-  if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-  if (warp == kWarpLoad) {
-    // ------------------------------------------------------------ loads
+
+  if (warp == kWarpK || warp == kWarpV) {
+    // ------------------------------------------------------------ loads: K and Q, or V
+    const bool is_k = warp == kWarpK;
     bool ok = true;
-    uint32_t kn = 0, vn = 0, qn = 0, tails = 0;  // stages and items loaded so far
+    uint32_t n_loaded = 0, items = 0, tails = 0;  // stages of this warp's ring, items, tail tiles so far
     const uint64_t pol_q = policy_evict_first(), pol_kv = policy_evict_last();
     // The barriers that count loads are the even CTA's: its MMA warp waits for
     // both CTAs' parts there.
     const uint32_t bar0 = kPair ? mapa_shared(smem_u32(bars), 0) : smem_u32(bars);
     auto expect = [&](int bar, uint32_t bytes) {
       if constexpr (kPair)
-        mbar_arrive_expect_tx_remote(bar0 + 8 * bar, bytes);
+        mbar_arrive_expect_tx_remote_relaxed(bar0 + 8 * bar, bytes);
       else
         mbar_arrive_expect_tx(&bars[bar], bytes);
     };
-    auto load = [&](uint8_t* dst, const CUtensorMap* map, int bar, int c0, int c1, int c2, uint64_t pol) {
+    // rows from `row` on of slices from `slice` on of one head
+    auto load = [&](uint8_t* dst, const CUtensorMap* map, int bar, int row, int slice, int hd, uint64_t pol) {
       if constexpr (kPair)
-        tma_load_3d_pair(dst, map, bar0 + 8 * bar, c0, c1, c2, pol);
+        tma_load_4d_pair(dst, map, bar0 + 8 * bar, 0, row, slice, hd, pol);
       else
-        tma_load_3d(dst, map, &bars[bar], c0, c1, c2, pol);
+        tma_load_4d(dst, map, &bars[bar], 0, row, slice, hd, pol);
     };
     for (; it.at < it.total && ok; next_item(it, worker, workers)) {
       const Tile t = load_tile(p, it);
       const int head = it.at % p.h_q, kvh = head / p.group;
       const int n = max(half_tiles(t, 0, L::kHalfRows, it.causal), half_tiles(t, 1, L::kHalfRows, it.causal));
-      for (int j = 0; j < n && ok; ++j) {
-        const bool tail = (j + 1) * kBN > t.lk;  // the sequence ends inside this tile
-        uint8_t* vdst = nullptr;
-        int vbar = 0;
-        if (lane == 0) {
-          const int ks = static_cast<int>(kn % L::kKStages), kr = static_cast<int>(kn / L::kKStages);
-          if (kr >= 1) ok = mbar_wait(&bars[K_EMPTY + ks], (kr - 1) & 1, abort_flag);
-          if (ok) {
-            expect(K_FULL + ks, L::kKBytes);
-            for (int s = 0; s < kQBoxes; ++s)
-              load(sK + ks * L::kKBytes + s * L::kKBoxBytes, &k_map, K_FULL + ks, 64 * s, kvh,
-                   t.k0 + j * kBN + static_cast<int>(rank) * L::kKeys, pol_kv);
-          }
-          if (j == 0 && ok) {
-            // both halves' boxes, also those past the sequence's last query (their rows are not stored)
-            if (qn >= 1) ok = mbar_wait(&bars[Q_EMPTY], (qn - 1) & 1, abort_flag);
+      if (is_k) {
+        if (lane == 0)
+          for (int j = 0; j < n && ok; ++j, ++n_loaded) {
+            const int s = static_cast<int>(n_loaded % L::kKStages), r = static_cast<int>(n_loaded / L::kKStages);
+            if (r >= 1) ok = mbar_wait(&bars[K_EMPTY + s], (r - 1) & 1, abort_flag);
             if (ok) {
-              const int halves = t.rows > L::kHalfRows ? 2 : 1;
-              expect(Q_FULL, halves * kQBoxes * kBoxBytes);
-              for (int h = 0; h < halves; ++h)
-                for (int s = 0; s < kQBoxes; ++s)
-                  load(sQ + (h * kQBoxes + s) * kBoxBytes, &q_map, Q_FULL, 64 * s, head,
-                       t.q0 + h * L::kHalfRows + static_cast<int>(rank) * kBM, pol_q);
+              expect(K_FULL + s, L::kKBytes);
+              load(sK + s * L::kKBytes, &k_map, K_FULL + s, t.k0 + j * kBN + static_cast<int>(rank) * L::kKeys, 0, kvh,
+                   pol_kv);
+            }
+            if (j == 0 && ok) {
+              if (items >= 1) ok = mbar_wait(&bars[Q_EMPTY], (items - 1) & 1, abort_flag);
+              if (ok) {
+                const int halves = t.rows > L::kHalfRows ? 2 : 1;
+                expect(Q_FULL, halves * kQBoxes * kBoxBytes);
+                for (int h = 0; h < halves; ++h)  // rows past the sequence's last query are not stored
+                  load(sQ + h * kQBoxes * kBoxBytes, &q_map, Q_FULL,
+                       t.q0 + h * L::kHalfRows + static_cast<int>(rank) * kBM, 0, head, pol_q);
+              }
             }
           }
-        }
-        const int vs = static_cast<int>(vn % L::kVStages), vr = static_cast<int>(vn / L::kVStages);
-        vdst = sV + vs * L::kVBytes;
-        vbar = V_FULL + vs;
-        if (lane == 0 && ok) {
-          if (vr >= 1) ok = mbar_wait(&bars[V_EMPTY + vs], (vr - 1) & 1, abort_flag);
-          if (ok) {
-            if (tail)
-              mbar_arrive_expect_tx(&bars[TAIL], L::kVBytes);
-            else
-              expect(vbar, L::kVBytes);
-            for (int b = 0; b < L::kVBoxes; ++b) {
-              const int col = 64 * (kPair ? static_cast<int>(rank) : b);
-              if (tail)  // onto this CTA's own barrier
-                tma_load_3d(vdst + b * kBoxBytes, &v_map, &bars[TAIL], col, kvh, t.k0 + j * kBN, pol_kv);
-              else
-                load(vdst + b * kBoxBytes, &v_map, vbar, col, kvh, t.k0 + j * kBN, pol_kv);
-            }
-          }
-        }
         ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
-        ++kn;
-        ++vn;
-        if (tail) {
+        if (n > 0) ++items;
+      } else {
+        for (int j = 0; j < n && ok; ++j, ++n_loaded) {
+          const bool tail = (j + 1) * kBN > t.lk;  // the sequence ends inside this tile
+          const int s = static_cast<int>(n_loaded % L::kVStages), r = static_cast<int>(n_loaded / L::kVStages);
+          uint8_t* dst = sV + s * L::kVBytes;
+          if (lane == 0) {
+            if (r >= 1) ok = mbar_wait(&bars[V_EMPTY + s], (r - 1) & 1, abort_flag);
+            if (ok && tail) {  // onto this CTA's own barrier
+              mbar_arrive_expect_tx(&bars[TAIL], L::kVBytes);
+              tma_load_4d(dst, &v_map, &bars[TAIL], 0, t.k0 + j * kBN, kPair ? static_cast<int>(rank) : 0, kvh, pol_kv);
+            } else if (ok) {
+              expect(V_FULL + s, L::kVBytes);
+              load(dst, &v_map, V_FULL + s, t.k0 + j * kBN, kPair ? static_cast<int>(rank) : 0, kvh, pol_kv);
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok || !tail) continue;
           ok = __all_sync(0xffffffffu, mbar_wait(&bars[TAIL], tails & 1, abort_flag));
           ++tails;
-          if (!ok) break;
+          if (!ok) continue;
           const int keep = t.lk - j * kBN;  // rows of this tile that are the sequence's
           for (int b = 0; b < L::kVBoxes; ++b) {
-            uint4* dst = reinterpret_cast<uint4*>(vdst + b * kBoxBytes + keep * 128);
-            for (int i = lane; i < (kBN - keep) * 8; i += 32) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+            uint4* z = reinterpret_cast<uint4*>(dst + b * kBoxBytes + keep * 128);
+            for (int i = lane; i < (kBN - keep) * 8; i += 32) z[i] = make_uint4(0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
             if constexpr (kPair)
-              mbar_arrive_remote(bar0 + 8 * vbar);
+              mbar_arrive_remote(bar0 + 8 * (V_FULL + s));
             else
-              mbar_arrive(&bars[vbar]);
+              mbar_arrive(&bars[V_FULL + s]);
           }
         }
       }
-      if (n > 0) ++qn;
     }
     if (!ok && lane == 0) {
       fail(abort_flag, p.status);
@@ -362,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t k_desc = sdesc_sw128(smem_u32(sK), 16, 1024);
       const uint64_t v_desc = sdesc_sw128(smem_u32(sV), kBoxBytes, 1024);  // MN-major
       auto wait = [&](int bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait<kPair>(&bars[bar], parity, abort_flag));
+        return __all_sync(0xffffffffu, mbar_wait(&bars[bar], parity, abort_flag));
       };
       auto commit = [&](int bar) {
         if constexpr (kPair)
@@ -371,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma_commit_warp(&bars[bar]);
       };
       bool ok = true;
-      uint32_t kn = 0, vn = 0, qn = 0, tiles[2] = {0, 0};
+      uint32_t kn = 0, vn = 0, qn = 0, tiles0 = 0, tiles1 = 0;  // stages, items, key tiles of each half
       for (; it.at < it.total && ok; next_item(it, worker, workers)) {
         const Tile t = load_tile(p, it);
         const int n0 = half_tiles(t, 0, L::kHalfRows, it.causal), n1 = half_tiles(t, 1, L::kHalfRows, it.causal);
@@ -381,14 +369,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           bool have_v = false, have_k = false;
           const int ks = static_cast<int>(kn % L::kKStages);
           const int vs = static_cast<int>(vn % L::kVStages);
-#pragma unroll
+#pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             const int nh = h ? n1 : n0;
             const uint32_t s_col = tm + 128u * h, o_col = tm + 256u + 128u * h;
             if (ok && j >= 1 && j - 1 < nh) {
               if (!have_v) ok = wait(V_FULL + vs, (vn / L::kVStages) & 1);
               have_v = true;
-              if (ok) ok = wait(P_FULL + h, (tiles[h] - 1) & 1);
+              if (ok) ok = wait(P_FULL + h, ((h ? tiles1 : tiles0) - 1) & 1);
               if (ok) {
                 tc_fence_after();
                 const uint64_t vd = v_desc + static_cast<uint64_t>((vs * L::kVBytes) >> 4);
@@ -431,7 +419,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                   }
                 }
                 commit(S_FULL + h);
-                ++tiles[h];
+                if (h)
+                  ++tiles1;
+                else
+                  ++tiles0;
                 if (h == 1 || j >= n1) {
                   commit(K_EMPTY + ks);
                   if (j == n - 1) commit(Q_EMPTY);
@@ -447,55 +438,86 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok && lane == 0) fail(abort_flag, p.status);
       // every MMA is done with shared memory and TMEM before this CTA ends
       commit(DRAIN);
-      mbar_wait<kPair>(&bars[DRAIN], 0, nullptr);
+      mbar_wait(&bars[DRAIN], 0, nullptr);
     }
     __syncwarp();
-  }
-  } else {
+  } else if (warp < kWarpMma) {
     // ------------------------------------------------------------ softmax + epilogue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    const int h = warp >> 2;
+    const int h = warp >> 3, part = (warp >> 2) & 1;  // half, and which 64 of the 128 keys (and output dims)
+    const int r = tid & 127;                          // row of the half in this CTA == TMEM lane
     const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint32_t s_addr = tmem + lane_base + 128u * h;
-    const uint32_t o_addr = tmem + lane_base + 256u + 128u * h;
-    // this thread's row of every tile (TMEM lane tid % 128 of this CTA)
-    const int row = h * L::kHalfRows + static_cast<int>(rank) * kBM + (tid & 127);
+    const uint32_t s_addr = tmem + lane_base + 128u * h + 64u * part;
+    const uint32_t p_addr = tmem + lane_base + 128u * h + 32u * part;
+    const uint32_t o_addr = tmem + lane_base + 256u + 128u * h + 64u * part;
+    const int row = h * L::kHalfRows + static_cast<int>(rank) * kBM + r;  // of a tile
+    // the other warp of these 32 rows: one float each way, behind a barrier of the two
+    float* mine = sRow + (2 * h + part) * kBM + r;
+    const float* other = sRow + (2 * h + (part ^ 1)) * kBM + r;
+    const uint32_t row_bar = 1 + 4 * h + (warp & 3);
     const uint32_t p_full = kPair ? mapa_shared(smem_u32(&bars[P_FULL + h]), 0) : smem_u32(&bars[P_FULL + h]);
     const float c_log2 = p.scale_log2;
     bool ok = true;
     uint32_t tiles = 0, items = 0;
-    Tile t = load_tile(p, it);
+    // key tiles of this half, and keys this row sees.  (All that the loop below
+    // keeps of the tile: the rest is read again after it, which costs nothing
+    // beside the wait for the last P V, and the registers do not go round.)
+    int nh, limit;
+    auto enter = [&](const Tile& t) {
+      nh = half_tiles(t, h, L::kHalfRows, it.causal);
+      limit = it.causal ? min(t.lk, t.vis + row) : t.lk;
+    };
+    enter(load_tile(p, it));
     while (it.at < it.total) {
-      const int nh = half_tiles(t, h, L::kHalfRows, it.causal);
-      const int limit = it.causal ? min(t.lk, t.vis + row) : t.lk;  // keys this row sees
       float ref = -INFINITY, l = 0.f;
       for (int j = 0; j < nh; ++j, ++tiles) {
-        ok = __all_sync(0xffffffffu, mbar_wait<kPair>(&bars[S_FULL + h], tiles & 1, abort_flag));
-        if (!ok) break;
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars[S_FULL + h], tiles & 1, abort_flag));
         tc_fence_after();
-        float s[kBN];
-        float mx[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32_max(s_addr + 32u * c, s + 32 * c, mx[c]);
+        float s[64];
+        float m0, m1;
+        tmem_ld32_max(s_addr, s, m0);
+        tmem_ld32_max(s_addr + 32u, s + 32, m1);
         tmem_wait_ld();
-        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        const int seen = limit - j * kBN;
-        if (__any_sync(0xffffffffu, seen < kBN)) {
+        float top = fmaxf(m0, m1);
+        const int seen = limit - j * kBN - 64 * part;
+        if (__any_sync(0xffffffffu, seen < 64)) {
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 0; i < kBN; ++i) {
+          for (int i = 0; i < 64; ++i) {
             s[i] = i < seen ? s[i] : -INFINITY;
             m4[i & 3] = fmaxf(m4[i & 3], s[i]);
           }
           top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         }
-        const float mt = top * c_log2;
+        // the row's maximum over both warps.  (The other warp's word is read
+        // before its next write: that needs S(j+1), which needs this warp's P.)
+        *mine = top;
+        // (a warp that gave up waiting takes the other one along)
+        ok = !named_bar_or(row_bar, 64, !ok);
+        if (!ok) break;
+        const float mt = fmaxf(top, *other) * c_log2;
         const float r_new = mt > ref + kTau ? mt : ref;
         const float alpha = r_new == ref ? 1.f : ex2(ref - r_new);
-        // P V of the tile before is done (see above): O may be rescaled here
+        ref = r_new;
+        const float mref = ref == -INFINITY ? 0.f : ref;
+        float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float2 cl = make_float2(c_log2, c_log2), nr = make_float2(-mref, -mref);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float2 x = __ffma2_rn(make_float2(s[16 * c + 2 * i], s[16 * c + 2 * i + 1]), cl, nr);
+            const float p0 = ex2(x.x), p1 = ex2(x.y);
+            pk[i] = pack2<kHalf>(p0, p1);
+            ls[i & 1] = __fadd2_rn(ls[i & 1], make_float2(p0, p1));
+          }
+          tmem_st8(p_addr + 8u * c, pk);
+        }
+        // P V of the tile before is done (see above): O may be rescaled here (after the
+        // scores have been used up: fewer registers)
         if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
-          for (uint32_t c0 = 0; c0 < 128; c0 += 16) {
+          for (uint32_t c0 = 0; c0 < 64; c0 += 16) {
             uint32_t v[16];
             tmem_ld16(o_addr + c0, v);
             tmem_wait_ld();
@@ -504,58 +526,46 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st16(o_addr + c0, v);
           }
         }
-        ref = r_new;
-        const float mref = ref == -INFINITY ? 0.f : ref;
-        float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        const float2 cl = make_float2(c_log2, c_log2), nr = make_float2(-mref, -mref);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 x = __ffma2_rn(make_float2(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), cl, nr);
-            const float p0 = ex2(x.x), p1 = ex2(x.y);
-            pk[i] = pack2<kHalf>(p0, p1);
-            ls[i & 1] = __fadd2_rn(ls[i & 1], make_float2(p0, p1));
-          }
-          tmem_st16(s_addr + 16u * c, pk);
-        }
         l = l * alpha + ((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y));
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
           if constexpr (kPair)
-            mbar_arrive_remote(p_full);
+            mbar_arrive_remote_relaxed(p_full);
           else
             mbar_arrive(&bars[P_FULL + h]);
         }
       }
       if (!ok) break;
-      // the next item's tile is on its way during this one's epilogue
+      const Tile t = load_tile(p, it);
       const int head = it.at % p.h_q;
       next_item(it, worker, workers);
       const Tile t_next = load_tile(p, it);
       if (nh > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait<kPair>(&bars[O_FULL + h], items & 1, abort_flag));
-        if (!ok) break;
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars[O_FULL + h], items & 1, abort_flag));
         ++items;
         tc_fence_after();
+        // the row's sum over both warps, in an order that both share
+        *mine = l;
+        ok = !named_bar_or(row_bar, 64, !ok);
+        if (!ok) break;
+        const float l2 = *other;
+        l = part == 0 ? l + l2 : l2 + l;
+        named_bar_sync(row_bar, 64);  // read before the next item's first maximum is written
       }
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const size_t orow = static_cast<size_t>(t.q0 + row) * p.h_q + head;
-      uint16_t* out = static_cast<uint16_t*>(p.out) + orow * 128;
+      uint16_t* out = static_cast<uint16_t*>(p.out) + orow * 128 + 64 * part;
       const bool row_ok = row < t.rows;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
-        uint32_t v[32];
-        if (nh > 0) {
-          tmem_ld32(o_addr + 32u * c, v);
-          tmem_wait_ld();
-        }
+        uint32_t v[16];
+        tmem_ld16(o_addr + 16u * c, v);
+        tmem_wait_ld();
         if (row_ok) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < 2; ++q) {
             uint32_t w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -563,14 +573,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float a = __uint_as_float(v[8 * q + 2 * i]) * inv, b = __uint_as_float(v[8 * q + 2 * i + 1]) * inv;
               w[i] = limit > 0 ? pack2<kHalf>(a, b) : 0u;
             }
-            *reinterpret_cast<uint4*>(out + 32 * c + 8 * q) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(out + 16 * c + 8 * q) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
       }
-      if (row_ok) p.lse[orow] = limit > 0 ? (ref + __log2f(l)) * kLn2 : -INFINITY;
+      if (row_ok && part == 0) p.lse[orow] = limit > 0 ? (ref + __log2f(l)) * kLn2 : -INFINITY;
       // O has been read: the next item's first P V waits for this warp's P
       tc_fence_before();
-      t = t_next;
+      enter(t_next);
     }
     if (!ok && lane == 0) fail(abort_flag, p.status);
   }

@@ -56,18 +56,21 @@ int prompt_device(int* sms) {
   return MLA_OK;
 }
 
-// [total, heads, dim] of 16-bit elements, viewed as (dim, heads, total); one
-// box = 64 dims of `rows` rows of one head.
+// [total, heads, dim] of 16-bit elements, viewed as (64 dims of a slice, total,
+// slices, heads), innermost first; one box = `slices` consecutive 64-dim slices
+// of `rows` rows of one head, which lands slice after slice, each `rows` rows of
+// 128 swizzled bytes, by one TMA instruction.
 int head_map(CUtensorMap* m, const void* base, long long total, int heads, int dim, long long token_stride,
-             long long head_stride, unsigned rows) {
+             long long head_stride, unsigned rows, unsigned slices) {
   // a stride that no second index uses may be anything: take a legal one
   if (heads == 1) head_stride = dim;
   if (total == 1) token_stride = static_cast<long long>(heads) * head_stride;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads),
-                              static_cast<cuuint64_t>(total)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_stride) * 2, static_cast<cuuint64_t>(token_stride) * 2};
-  const cuuint32_t box[3] = {64, 1, rows};
-  return encode_map16(m, base, 3, dims, strides, box);
+  const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(total), static_cast<cuuint64_t>(dim / 64),
+                              static_cast<cuuint64_t>(heads)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(token_stride) * 2, 128,
+                                 static_cast<cuuint64_t>(head_stride) * 2};
+  const cuuint32_t box[4] = {64, rows, slices, 1};
+  return encode_map16(m, base, 4, dims, strides, box);
 }
 
 // Strides of a [total, heads, dim] tensor: multiples of 8 elements, no
@@ -289,13 +292,15 @@ int mla_prompt_attention_fwd(const void* d_q, long long q_token_stride, long lon
   p.status = d_status;
   const bool pair = prompt_pairs(batch, total_q);
   CUtensorMap qm, km, vm;
-  int rc = head_map(&qm, d_q, total_q, h_q, d_qk, q_token_stride, q_head_stride, 128);
+  int rc = head_map(&qm, d_q, total_q, h_q, d_qk, q_token_stride, q_head_stride, 128, d_qk / 64);
   if (total_k == 0) {  // no CTA loads K or V: any valid map serves
     km = vm = qm;
   } else {
     // a pair's CTAs load 64 keys each, and all 128 for their half of V's dims
-    if (rc == MLA_OK) rc = head_map(&km, d_k, total_k, h_kv, d_qk, k_token_stride, k_head_stride, pair ? 64 : 128);
-    if (rc == MLA_OK) rc = head_map(&vm, d_v, total_k, h_kv, 128, v_token_stride, v_head_stride, 128);
+    if (rc == MLA_OK)
+      rc = head_map(&km, d_k, total_k, h_kv, d_qk, k_token_stride, k_head_stride, pair ? 64 : 128, d_qk / 64);
+    if (rc == MLA_OK)
+      rc = head_map(&vm, d_v, total_k, h_kv, 128, v_token_stride, v_head_stride, 128, pair ? 1 : 2);
   }
   if (rc != MLA_OK) return rc;
   return launched(launch_prompt(qm, km, vm, p, dtype == MLA_DTYPE_FP16, d_qk, pair, sms, to_stream(stream)));
