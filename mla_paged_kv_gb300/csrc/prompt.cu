@@ -51,15 +51,15 @@ constexpr int kBN = 128;              // keys of a tile
 constexpr int kBoxBytes = 128 * 128;  // 128 rows x 64 16-bit values
 
 // 16 softmax warps: two for each 32 rows of a half, 64 of the 128 keys each;
-// then the MMA warp, the warps that load K and Q and that load V, and a spare.
+// then the MMA warp, and the warps that load K, V and Q.
 constexpr int kThreads = 640;
-constexpr int kWarpMma = 16, kWarpK = 17, kWarpV = 18;
+constexpr int kWarpMma = 16, kWarpK = 17, kWarpV = 18, kWarpQ = 19;
 constexpr int kMaxStages = 5;
 
 enum : int {
-  Q_FULL = 0,
-  Q_EMPTY,                        // the item's last Q K^T is done: Q may be loaded over
-  K_FULL,                         // +stage
+  Q_FULL = 0,                     // +half
+  Q_EMPTY = Q_FULL + 2,           // +half: the item's last Q K^T is done: Q may be loaded over
+  K_FULL = Q_EMPTY + 2,           // +stage
   K_EMPTY = K_FULL + kMaxStages,  // +stage: its MMAs are done
   V_FULL = K_EMPTY + kMaxStages,
   V_EMPTY = V_FULL + kMaxStages,
@@ -202,8 +202,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     *abort_flag = 0;
     constexpr uint32_t kCtas = kPair ? 2 : 1;  // loaders that fill a stage, each its part
-    mbar_init(&bars[Q_FULL], kCtas);
-    mbar_init(&bars[Q_EMPTY], 1);
     for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(&bars[K_FULL + i], kCtas);
       mbar_init(&bars[K_EMPTY + i], 1);
@@ -211,6 +209,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars[V_EMPTY + i], 1);
     }
     for (int h = 0; h < 2; ++h) {
+      mbar_init(&bars[Q_FULL + h], kCtas);
+      mbar_init(&bars[Q_EMPTY + h], 1);
       mbar_init(&bars[S_FULL + h], 1);
       mbar_init(&bars[P_FULL + h], 8 * kCtas);
       mbar_init(&bars[O_FULL + h], 1);
@@ -244,11 +244,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   Items it = first_item(p, worker);
 
 
-  if (warp == kWarpK || warp == kWarpV) {
-    // ------------------------------------------------------------ loads: K and Q, or V
-    const bool is_k = warp == kWarpK;
+  if (warp > kWarpMma) {
+    // ------------------------------------------------------------ loads: K, V or Q
     bool ok = true;
-    uint32_t n_loaded = 0, items = 0, tails = 0;  // stages of this warp's ring, items, tail tiles so far
+    uint32_t n_loaded = 0, q0n = 0, q1n = 0, tails = 0;  // stages, Q halves and tail tiles loaded so far
     const uint64_t pol_q = policy_evict_first(), pol_kv = policy_evict_last();
     // The barriers that count loads are the even CTA's: its MMA warp waits for
     // both CTAs' parts there.
@@ -269,8 +268,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (; it.at < it.total && ok; next_item(it, worker, workers)) {
       const Tile t = load_tile(p, it);
       const int head = it.at % p.h_q, kvh = head / p.group;
-      const int n = max(half_tiles(t, 0, L::kHalfRows, it.causal), half_tiles(t, 1, L::kHalfRows, it.causal));
-      if (is_k) {
+      const int n0 = half_tiles(t, 0, L::kHalfRows, it.causal), n1 = half_tiles(t, 1, L::kHalfRows, it.causal);
+      const int n = max(n0, n1);
+      if (warp == kWarpQ) {
+        // a half's rows as soon as its last Q K^T of the item before is done
+        // (rows past the sequence's last query come along and are not stored)
+        if (lane == 0)
+          for (int h = 0; h < 2 && ok; ++h) {
+            if ((h ? n1 : n0) == 0) continue;
+            const uint32_t before = h ? q1n++ : q0n++;
+            if (before >= 1) ok = mbar_wait(&bars[Q_EMPTY + h], (before - 1) & 1, abort_flag);
+            if (!ok) break;
+            expect(Q_FULL + h, kQBoxes * kBoxBytes);
+            load(sQ + h * kQBoxes * kBoxBytes, &q_map, Q_FULL + h,
+                 t.q0 + h * L::kHalfRows + static_cast<int>(rank) * kBM, 0, head, pol_q);
+          }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+      } else if (warp == kWarpK) {
         if (lane == 0)
           for (int j = 0; j < n && ok; ++j, ++n_loaded) {
             const int s = static_cast<int>(n_loaded % L::kKStages), r = static_cast<int>(n_loaded / L::kKStages);
@@ -280,19 +294,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               load(sK + s * L::kKBytes, &k_map, K_FULL + s, t.k0 + j * kBN + static_cast<int>(rank) * L::kKeys, 0, kvh,
                    pol_kv);
             }
-            if (j == 0 && ok) {
-              if (items >= 1) ok = mbar_wait(&bars[Q_EMPTY], (items - 1) & 1, abort_flag);
-              if (ok) {
-                const int halves = t.rows > L::kHalfRows ? 2 : 1;
-                expect(Q_FULL, halves * kQBoxes * kBoxBytes);
-                for (int h = 0; h < halves; ++h)  // rows past the sequence's last query are not stored
-                  load(sQ + h * kQBoxes * kBoxBytes, &q_map, Q_FULL,
-                       t.q0 + h * L::kHalfRows + static_cast<int>(rank) * kBM, 0, head, pol_q);
-              }
-            }
           }
         ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (n > 0) ++items;
       } else {
         for (int j = 0; j < n && ok; ++j, ++n_loaded) {
           const bool tail = (j + 1) * kBN > t.lk;  // the sequence ends inside this tile
@@ -352,88 +355,102 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto wait = [&](int bar, uint32_t parity) {
         return __all_sync(0xffffffffu, mbar_wait(&bars[bar], parity, abort_flag));
       };
+      // a stage of V may hold rows that threads of the other CTA zeroed
+      auto wait_v = [&](int bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait<kPair>(&bars[bar], parity, abort_flag));
+      };
       auto commit = [&](int bar) {
         if constexpr (kPair)
           umma2_commit_warp(&bars[bar]);
         else
           umma_commit_warp(&bars[bar]);
       };
+      // One step a key tile, through all items: P V of the tile before, then
+      // Q K^T of this one, half by half.  At an item's end the tile before is
+      // its last one and this one the next item's first.
       bool ok = true;
-      uint32_t kn = 0, vn = 0, qn = 0, tiles0 = 0, tiles1 = 0;  // stages, items, key tiles of each half
-      for (; it.at < it.total && ok; next_item(it, worker, workers)) {
-        const Tile t = load_tile(p, it);
-        const int n0 = half_tiles(t, 0, L::kHalfRows, it.causal), n1 = half_tiles(t, 1, L::kHalfRows, it.causal);
-        const int n = max(n0, n1);
-        if (n == 0) continue;
-        for (int j = 0; j <= n && ok; ++j) {
-          bool have_v = false, have_k = false;
-          const int ks = static_cast<int>(kn % L::kKStages);
-          const int vs = static_cast<int>(vn % L::kVStages);
+      uint32_t kn = 0, vn = 0, q0n = 0, q1n = 0, tiles0 = 0, tiles1 = 0;  // stages, Q halves, tiles of each half so far
+      int n0 = 0, n1 = 0, j = 0;        // this item's key tiles, and this one
+      int pn0 = 0, pn1 = 0, pj = 0;     // the same of the tile before
+      Tile next = load_tile(p, it);
+      // on to the next item with keys; n0 = n1 = 0 past the last one
+      auto enter = [&]() {
+        n0 = n1 = j = 0;
+        while (it.at < it.total && max(n0, n1) == 0) {
+          n0 = half_tiles(next, 0, L::kHalfRows, it.causal);
+          n1 = half_tiles(next, 1, L::kHalfRows, it.causal);
+          next_item(it, worker, workers);
+          next = load_tile(p, it);  // not needed before this item's end
+        }
+      };
+      enter();
+      while (ok && (max(n0, n1) > 0 || max(pn0, pn1) > 0)) {
+        bool have_v = false, have_k = false;
+        const int ks = static_cast<int>(kn % L::kKStages);
+        const int vs = static_cast<int>(vn % L::kVStages);
 #pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            const int nh = h ? n1 : n0;
-            const uint32_t s_col = tm + 128u * h, o_col = tm + 256u + 128u * h;
-            if (ok && j >= 1 && j - 1 < nh) {
-              if (!have_v) ok = wait(V_FULL + vs, (vn / L::kVStages) & 1);
-              have_v = true;
-              if (ok) ok = wait(P_FULL + h, ((h ? tiles1 : tiles0) - 1) & 1);
-              if (ok) {
-                tc_fence_after();
-                const uint64_t vd = v_desc + static_cast<uint64_t>((vs * L::kVBytes) >> 4);
+        for (int h = 0; h < 2; ++h) {
+          const int nh = h ? n1 : n0, pnh = h ? pn1 : pn0;
+          const uint32_t s_col = tm + 128u * h, o_col = tm + 256u + 128u * h;
+          if (ok && pj < pnh) {
+            if (!have_v) ok = wait_v(V_FULL + vs, (vn / L::kVStages) & 1);
+            have_v = true;
+            if (ok) ok = wait(P_FULL + h, ((h ? tiles1 : tiles0) - 1) & 1);
+            if (ok) {
+              tc_fence_after();
+              const uint64_t vd = v_desc + static_cast<uint64_t>((vs * L::kVBytes) >> 4);
 #pragma unroll
-                for (int kk = 0; kk < kBN / 16; ++kk) {
-                  const uint32_t acc = (j == 1 && kk == 0) ? 0u : 1u;
-                  if constexpr (kPair)
-                    umma2_f16_ts_warp(o_col, s_col + 8u * kk, vd + static_cast<uint64_t>((kk * 2048) >> 4), idesc_pv,
-                                      acc);
-                  else
-                    umma_f16_ts_warp(o_col, s_col + 8u * kk, vd + static_cast<uint64_t>((kk * 2048) >> 4), idesc_pv,
-                                     acc);
-                }
-                if (j == nh) commit(O_FULL + h);
-                if (h == 1 || j - 1 >= n1) commit(V_EMPTY + vs);  // read for the last time
-              }
-            }
-            if (ok && j < nh) {
-              if (!have_k) {
-                if (j == 0) ok = wait(Q_FULL, qn & 1);
-                if (ok) ok = wait(K_FULL + ks, (kn / L::kKStages) & 1);
-              }
-              have_k = true;
-              if (ok) {
-                tc_fence_after();
-                const uint64_t kd0 = k_desc + static_cast<uint64_t>((ks * L::kKBytes) >> 4);
-#pragma unroll
-                for (int s = 0; s < kQBoxes; ++s) {
-                  const uint64_t kd = kd0 + static_cast<uint64_t>((s * L::kKBoxBytes) >> 4);
-                  const uint64_t qd = q_desc + static_cast<uint64_t>(((h * kQBoxes + s) * kBoxBytes) >> 4);
-#pragma unroll
-                  for (int kk = 0; kk < 4; ++kk) {
-                    const uint32_t acc = (s == 0 && kk == 0) ? 0u : 1u;
-                    if constexpr (kPair)
-                      umma2_f16_warp(s_col, qd + static_cast<uint64_t>((kk * 32) >> 4),
-                                     kd + static_cast<uint64_t>((kk * 32) >> 4), idesc_qk, acc);
-                    else
-                      umma_f16_warp(s_col, qd + static_cast<uint64_t>((kk * 32) >> 4),
-                                    kd + static_cast<uint64_t>((kk * 32) >> 4), idesc_qk, acc);
-                  }
-                }
-                commit(S_FULL + h);
-                if (h)
-                  ++tiles1;
+              for (int kk = 0; kk < kBN / 16; ++kk) {
+                const uint32_t acc = (pj == 0 && kk == 0) ? 0u : 1u;
+                if constexpr (kPair)
+                  umma2_f16_ts_warp(o_col, s_col + 8u * kk, vd + static_cast<uint64_t>((kk * 2048) >> 4), idesc_pv, acc);
                 else
-                  ++tiles0;
-                if (h == 1 || j >= n1) {
-                  commit(K_EMPTY + ks);
-                  if (j == n - 1) commit(Q_EMPTY);
-                }
+                  umma_f16_ts_warp(o_col, s_col + 8u * kk, vd + static_cast<uint64_t>((kk * 2048) >> 4), idesc_pv, acc);
               }
+              if (pj == pnh - 1) commit(O_FULL + h);
+              if (h == 1 || pj >= pn1) commit(V_EMPTY + vs);  // read for the last time
             }
           }
-          if (j >= 1) ++vn;
-          if (j < n) ++kn;
+          if (ok && j < nh) {
+            if (j == 0) ok = wait(Q_FULL + h, (h ? q1n++ : q0n++) & 1);
+            if (ok && !have_k) ok = wait(K_FULL + ks, (kn / L::kKStages) & 1);
+            have_k = true;
+            if (ok) {
+              tc_fence_after();
+              const uint64_t kd0 = k_desc + static_cast<uint64_t>((ks * L::kKBytes) >> 4);
+#pragma unroll
+              for (int s = 0; s < kQBoxes; ++s) {
+                const uint64_t kd = kd0 + static_cast<uint64_t>((s * L::kKBoxBytes) >> 4);
+                const uint64_t qd = q_desc + static_cast<uint64_t>(((h * kQBoxes + s) * kBoxBytes) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                  const uint32_t acc = (s == 0 && kk == 0) ? 0u : 1u;
+                  if constexpr (kPair)
+                    umma2_f16_warp(s_col, qd + static_cast<uint64_t>((kk * 32) >> 4),
+                                   kd + static_cast<uint64_t>((kk * 32) >> 4), idesc_qk, acc);
+                  else
+                    umma_f16_warp(s_col, qd + static_cast<uint64_t>((kk * 32) >> 4),
+                                  kd + static_cast<uint64_t>((kk * 32) >> 4), idesc_qk, acc);
+                }
+              }
+              commit(S_FULL + h);
+              if (h)
+                ++tiles1;
+              else
+                ++tiles0;
+              if (j == nh - 1) commit(Q_EMPTY + h);
+              if (h == 1 || j >= n1) commit(K_EMPTY + ks);
+            }
+          }
         }
-        ++qn;
+        if (max(pn0, pn1) > 0) ++vn;
+        pn0 = n0;
+        pn1 = n1;
+        pj = j;
+        if (max(n0, n1) > 0) {
+          ++kn;
+          if (++j == max(n0, n1)) enter();
+        }
       }
       if (!ok && lane == 0) fail(abort_flag, p.status);
       // every MMA is done with shared memory and TMEM before this CTA ends
