@@ -184,14 +184,15 @@ int mla_prompt_attention_fwd(const void* d_q, long long q_token_stride, long lon
  * entries that all requests have in common, in whole pages that every query of
  * every request sees; it may be none.  It is made once for a batch and read
  * by every layer, while the block table and lengths stay as they were.
- * A prefix is only attended together where that takes fewer 128-row blocks
- * than attending it request by request, that is where
- * ceil(batch * s_q * h_q / 128) < batch * ceil(s_q * h_q / 128); with s_q * h_q a
- * multiple of 128 the rows fill their blocks either way, and the shared pages
- * are one copy in L2.
- *   num_parts from mla_num_parts(MLA_ROWS_PER_BLOCK, 0); at most 1024
+ * The prefix is attended together only where that takes fewer 128-row blocks
+ * than attending it request by request:
+ * ceil(batch * s_q * h_q / 128) < batch * ceil(s_q * h_q / 128).  With s_q * h_q a
+ * multiple of 128 every request fills its blocks alone, the shared pages are
+ * one copy in L2 either way, and the call is mla_decode_fwd.
+ *   num_parts from mla_shared_prefix_num_parts; at most 1024
  * Other arguments as for mla_decode_fwd.  batch * s_q * h_q and
  * batch * max_pages stay below 2^31; s_q * h_q <= 2^20, batch <= 65535. */
+int mla_shared_prefix_num_parts(int batch, int s_q, int h_q); /* >= 1, or a negative mla_status_t */
 size_t mla_shared_prefix_plan_bytes(int batch, int s_q, int h_q, int num_parts);
 size_t mla_shared_prefix_workspace_bytes(int batch, int s_q, int h_q, int num_parts);
 int mla_shared_prefix_get_plan(const int32_t* d_block_table, int max_pages, const int32_t* d_cache_seqlens, int batch,
@@ -199,15 +200,14 @@ int mla_shared_prefix_get_plan(const int32_t* d_block_table, int max_pages, cons
                                mla_stream_t stream);
 
 /*   d_plan      from mla_shared_prefix_get_plan for the same block table,
- *               batch, s_q, h_q and num_parts; it holds the lengths and the
- *               causal flag
+ *               batch, s_q, h_q, causal and num_parts; it holds the lengths
  *   d_workspace >= mla_shared_prefix_workspace_bytes(batch, s_q, h_q, num_parts)
  * A block-table entry outside the pool masks its 64 keys and is reported, as
  * in mla_decode_fwd.  Slots of a page behind a request's last key must hold
  * finite values (they meet a weight of 0). */
 int mla_shared_prefix_decode_fwd(const void* d_q, const void* d_kv, const int32_t* d_block_table, int max_pages,
-                                 int num_pages, int batch, int s_q, int h_q, int dtype, float softmax_scale,
-                                 const void* d_plan, size_t plan_bytes, int num_parts, void* d_workspace,
+                                 int num_pages, int batch, int s_q, int h_q, int dtype, int causal,
+                                 float softmax_scale, const void* d_plan, size_t plan_bytes, int num_parts, void* d_workspace,
                                  size_t workspace_bytes, void* d_out, int out_type, float* d_lse, int32_t* d_status,
                                  mla_stream_t stream);
 

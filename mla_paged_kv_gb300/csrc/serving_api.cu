@@ -102,12 +102,16 @@ int shared_sizes(int batch, int s_q, int h_q, int num_parts, SharedSizes* z) {
   const long long own = batch * ((per_request + MLA_ROWS_PER_BLOCK - 1) / MLA_ROWS_PER_BLOCK);
   const long long front = (z->rows + MLA_ROWS_PER_BLOCK - 1) / MLA_ROWS_PER_BLOCK;
   z->share = front < own;
-  const long long units = own + (z->share ? front : 0);
+  const long long units = z->share ? own + front : batch;
   z->units = static_cast<int>(units);
   z->lengths_off = up256(static_cast<size_t>(units) * kUnitInts * 4);
   z->offset_off = z->lengths_off + up256(static_cast<size_t>(units) * 4);
   z->sched_off = z->offset_off + up256(static_cast<size_t>(units + 1) * 4);
   z->plan_bytes = z->sched_off + up256(static_cast<size_t>(num_parts) * MLA_SCHED_INTS * 4);
+  if (!z->share) {  // the plan and the workspace of the plain decode
+    z->ws_bytes = mla_workspace_bytes(batch, static_cast<int>(per_request), num_parts);
+    return MLA_OK;
+  }
   const size_t slots = static_cast<size_t>(units) + num_parts;
   z->lse_off = slots * MLA_ROWS_PER_BLOCK * MLA_D_V * 4;
   z->ws_bytes = z->lse_off + slots * MLA_ROWS_PER_BLOCK * 4;
@@ -306,6 +310,14 @@ int mla_prompt_attention_fwd(const void* d_q, long long q_token_stride, long lon
   return launched(launch_prompt(qm, km, vm, p, dtype == MLA_DTYPE_FP16, d_qk, pair, sms, to_stream(stream)));
 }
 
+int mla_shared_prefix_num_parts(int batch, int s_q, int h_q) {
+  SharedSizes z;
+  const int rc = shared_sizes(batch, s_q, h_q, 1, &z);
+  if (rc != MLA_OK) return -rc;
+  const int parts = mla_num_parts(z.share ? MLA_ROWS_PER_BLOCK : s_q * h_q, 0);
+  return parts > kMaxSharedParts ? kMaxSharedParts : parts;
+}
+
 size_t mla_shared_prefix_plan_bytes(int batch, int s_q, int h_q, int num_parts) {
   SharedSizes z;
   return shared_sizes(batch, s_q, h_q, num_parts, &z) == MLA_OK ? z.plan_bytes : 0;
@@ -332,15 +344,18 @@ int mla_shared_prefix_get_plan(const int32_t* d_block_table, int max_pages, cons
   char* plan = static_cast<char*>(d_plan);
   int32_t* lengths = reinterpret_cast<int32_t*>(plan + z.lengths_off);
   const cudaStream_t st = to_stream(stream);
-  rc = launched(launch_shared_units(d_block_table, max_pages, d_cache_seqlens, batch, s_q, h_q, causal ? 1 : 0,
-                                    z.share, reinterpret_cast<int32_t*>(plan), lengths, st));
+  rc = z.share ? launched(launch_shared_units(d_block_table, max_pages, d_cache_seqlens, batch, s_q, h_q,
+                                              causal ? 1 : 0, reinterpret_cast<int32_t*>(plan), lengths, st))
+               : launched(cudaMemcpyAsync(lengths, d_cache_seqlens, static_cast<size_t>(batch) * 4,
+                                          cudaMemcpyDeviceToDevice, st));
   if (rc != MLA_OK) return rc;
   return launched(launch_plan(lengths, z.units, num_parts, reinterpret_cast<int32_t*>(plan + z.sched_off),
                               reinterpret_cast<int32_t*>(plan + z.offset_off), st));
 }
 
 int mla_shared_prefix_decode_fwd(const void* d_q, const void* d_kv, const int32_t* d_block_table, int max_pages,
-                                 int num_pages, int batch, int s_q, int h_q, int dtype, float softmax_scale,
+                                 int num_pages, int batch, int s_q, int h_q, int dtype, int causal,
+                                 float softmax_scale,
                                  const void* d_plan, size_t plan_bytes, int num_parts, void* d_workspace,
                                  size_t workspace_bytes, void* d_out, int out_type, float* d_lse, int32_t* d_status,
                                  mla_stream_t stream) {
@@ -366,6 +381,12 @@ int mla_shared_prefix_decode_fwd(const void* d_q, const void* d_kv, const int32_
   rc = device_ready(&sms);
   if (rc != MLA_OK) return rc;
   const char* plan = static_cast<const char*>(d_plan);
+  if (!z.share)
+    return mla_decode_fwd(d_q, d_kv, d_block_table, max_pages, num_pages,
+                          reinterpret_cast<const int32_t*>(plan + z.lengths_off), batch, s_q, h_q, 1, dtype, causal,
+                          softmax_scale, reinterpret_cast<const int32_t*>(plan + z.sched_off),
+                          reinterpret_cast<const int32_t*>(plan + z.offset_off), num_parts, d_workspace,
+                          workspace_bytes, d_out, out_type, d_lse, d_status, stream);
   SharedLaunch c{};
   c.q = d_q;
   c.kv = d_kv;
@@ -388,8 +409,8 @@ int mla_shared_prefix_decode_fwd(const void* d_q, const void* d_kv, const int32_
   const cudaStream_t st = to_stream(stream);
   rc = launch_shared(c, st);
   if (rc != MLA_OK) return rc;
-  return launched(launch_shared_combine(c.o_accum, c.lse_accum, c.split_offset, batch, s_q * h_q, z.share, d_out,
-                                        out_type, d_lse, sms, st));
+  return launched(launch_shared_combine(c.o_accum, c.lse_accum, c.split_offset, batch, s_q * h_q, d_out, out_type,
+                                        d_lse, sms, st));
 }
 
 }  // extern "C"

@@ -25,27 +25,25 @@ constexpr int kRB = kRowsPerBlock;
 // over the rest.  One block; made once for a batch.
 __global__ void __launch_bounds__(1024)
     shared_units_kernel(const int32_t* table, int max_pages, const int32_t* seqlens, int batch, int s_q, int h_q,
-                        int causal, int share, int32_t* units, int32_t* lengths) {
+                        int causal, int32_t* units, int32_t* lengths) {
   __shared__ int common;
-  if (threadIdx.x == 0) common = share ? max_pages : 0;
+  if (threadIdx.x == 0) common = max_pages;
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (share) {
-    for (int b = threadIdx.x; b < batch; b += 1024) {
-      const int seen = max(seqlens[b], 0) - (causal ? s_q - 1 : 0);  // keys the first query sees
-      atomicMin(&common, max(seen, 0) / kTile);
-    }
-    __syncthreads();
-    for (int b = 1 + warp; b < batch; b += 32) {
-      const int32_t* row = table + static_cast<long long>(b) * max_pages;
-      const int most = *reinterpret_cast<volatile int*>(&common);
-      for (int c0 = 0; c0 < most; c0 += 32) {
-        const int c = c0 + lane;
-        const unsigned diff = __ballot_sync(0xffffffffu, c < most && row[c] != table[c]);
-        if (diff) {
-          if (lane == 0) atomicMin(&common, c0 + __ffs(diff) - 1);
-          break;
-        }
+  for (int b = threadIdx.x; b < batch; b += 1024) {
+    const int seen = max(seqlens[b], 0) - (causal ? s_q - 1 : 0);  // keys the first query sees
+    atomicMin(&common, max(seen, 0) / kTile);
+  }
+  __syncthreads();
+  for (int b = 1 + warp; b < batch; b += 32) {
+    const int32_t* row = table + static_cast<long long>(b) * max_pages;
+    const int most = *reinterpret_cast<volatile int*>(&common);
+    for (int c0 = 0; c0 < most; c0 += 32) {
+      const int c = c0 + lane;
+      const unsigned diff = __ballot_sync(0xffffffffu, c < most && row[c] != table[c]);
+      if (diff) {
+        if (lane == 0) atomicMin(&common, c0 + __ffs(diff) - 1);
+        break;
       }
     }
   }
@@ -53,7 +51,7 @@ __global__ void __launch_bounds__(1024)
   const int shared = common;
   const int rows = s_q * h_q;
   const long long total = static_cast<long long>(batch) * rows;
-  const int front = share ? static_cast<int>((total + kRB - 1) / kRB) : 0, per = ceil_div_i(rows, kRB);
+  const int front = static_cast<int>((total + kRB - 1) / kRB), per = ceil_div_i(rows, kRB);
   for (int u = threadIdx.x; u < front + batch * per; u += 1024) {
     int4* e = reinterpret_cast<int4*>(units + u * kUnitInts);
     if (u < front) {
@@ -89,113 +87,175 @@ __device__ __forceinline__ void store4(void* out, int out_type, size_t elem, flo
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + elem) = w;
 }
 
-// One block per query row; kGroups groups of 128 threads take every kGroups-th
-// split (four columns a thread), merged through shared memory.  Bound by the
-// partials' bytes where there are many rows (kGroups = 1), by the latency of
-// dozens of splits where there are few (kGroups = 8).
-template <int kGroups>
-__global__ void __launch_bounds__(128 * kGroups)
-    shared_combine_kernel(const float* __restrict__ o_accum, const float* __restrict__ lse_accum,
-                          const int32_t* __restrict__ split_offset, int batch, int rows, int share,
-                          void* __restrict__ out, int out_type, float* __restrict__ lse) {
-  constexpr int kBatch = 4;
-  __shared__ float weight[2 * kMaxSharedParts];
-  __shared__ float red[kGroups * 4 + 1];
-  __shared__ float4 part[kGroups > 1 ? kGroups - 1 : 1][128];
-  const long long g = blockIdx.x;  // query row of batch * rows
+// What a row merges: the splits of its prefix unit, then those of its own unit.
+struct RowSplits {
+  int p0, np, o0, n;  // prefix: slots p0 .. p0 + np - 1; own: o0 .. o0 + n - np - 1
+  int pr, orow;       // the row within either unit
+
+  // Row of split i among all slots' 128 rows.
+  __device__ __forceinline__ size_t at(int i) const {
+    return i < np ? static_cast<size_t>(p0 + i) * kRB + pr : static_cast<size_t>(o0 + i - np) * kRB + orow;
+  }
+};
+
+__device__ __forceinline__ RowSplits row_splits(const int32_t* split_offset, int batch, int rows, long long g) {
   const int b = static_cast<int>(g / rows), r = static_cast<int>(g - static_cast<long long>(b) * rows);
-  const int front = share ? static_cast<int>((static_cast<long long>(batch) * rows + kRB - 1) / kRB) : 0;
+  const int front = static_cast<int>((static_cast<long long>(batch) * rows + kRB - 1) / kRB);
   const int own = front + b * ceil_div_i(rows, kRB) + r / kRB;
   const int pre = static_cast<int>(g / kRB);
-  // the plan is complete long before: its offsets are read before the wait
-  const int p0 = share ? split_offset[pre] : 0;
-  const int np = share ? split_offset[pre + 1] - p0 : 0;
-  const int o0 = split_offset[own];
-  const int n = np + split_offset[own + 1] - o0;
-  const int pr = static_cast<int>(g % kRB), orow = r % kRB;
-  // row of split i: its slot's 128 rows, then the unit's row
-  auto slot_row = [&](int i) {
-    return i < np ? static_cast<size_t>(p0 + i) * kRB + pr : static_cast<size_t>(o0 + i - np) * kRB + orow;
-  };
-  pdl_wait_prior_grid();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  float m = -INFINITY;
-  for (int i = tid; i < n; i += 128 * kGroups) {
-    const float l = lse_accum[slot_row(i)];
-    weight[i] = l;
-    m = fmaxf(m, l);
+  RowSplits s;
+  s.p0 = split_offset[pre];
+  s.np = split_offset[pre + 1] - s.p0;
+  s.o0 = split_offset[own];
+  s.n = s.np + split_offset[own + 1] - s.o0;
+  s.pr = static_cast<int>(g % kRB);
+  s.orow = r % kRB;
+  return s;
+}
+
+__device__ __forceinline__ void add4(float4& acc, float w, const float4& v) {
+  if (w != 0.f) {  // an empty split weighs 0 whatever its partial holds
+    acc.x = fmaf(w, v.x, acc.x);
+    acc.y = fmaf(w, v.y, acc.y);
+    acc.z = fmaf(w, v.z, acc.z);
+    acc.w = fmaf(w, v.w, acc.w);
   }
+}
+
+// Many rows: a warp merges 128 columns of a row (four a lane).  The lanes hold
+// the splits' LSEs, 32 at a time; the partials of eight splits are in flight at
+// once.  No shared memory, so the blocks are resident beside the attention
+// kernel's CTAs and start as it ends.  Bound by the partials' bytes.
+__global__ void __launch_bounds__(128)
+    shared_combine_rows_kernel(const float* __restrict__ o_accum, const float* __restrict__ lse_accum,
+                               const int32_t* __restrict__ split_offset, int batch, int rows, void* __restrict__ out,
+                               int out_type, float* __restrict__ lse) {
+  constexpr int kBatch = 8;
+  const long long g = blockIdx.x;
+  const int lane = threadIdx.x & 31, col = 4 * threadIdx.x;
+  const RowSplits s = row_splits(split_offset, batch, rows, g);  // the plan's: read before the wait
+  pdl_wait_prior_grid();
+  const float l0 = lane < s.n ? lse_accum[s.at(lane)] : -INFINITY;
+  float m = l0;
+  for (int i = 32 + lane; i < s.n; i += 32) m = fmaxf(m, lse_accum[s.at(i)]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) red[warp] = m;
-  __syncthreads();
-  m = red[0];
-#pragma unroll
-  for (int w = 1; w < 4 * kGroups; ++w) m = fmaxf(m, red[w]);
-  // the sum in split order, the same in every thread
-  float z = 0.f;
-  for (int i = 0; i < n; ++i) {
-    const float l = weight[i];
-    z += l == -INFINITY ? 0.f : expf(l - m);
-  }
-  const float inv_z = z > 0.f ? 1.f / z : 0.f;
-  const int col = 4 * (tid & 127), grp = tid >> 7;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](int i, const float4& v) {
-    const float l = weight[i];
-    const float w = l == -INFINITY ? 0.f : expf(l - m) * inv_z;
-    if (w != 0.f) {  // an empty split weighs 0 whatever its partial holds
-      acc.x = fmaf(w, v.x, acc.x);
-      acc.y = fmaf(w, v.y, acc.y);
-      acc.z = fmaf(w, v.z, acc.z);
-      acc.w = fmaf(w, v.w, acc.w);
-    }
-  };
-  int i = grp;
-  for (; i + (kBatch - 1) * kGroups < n; i += kBatch * kGroups) {
-    float4 v[kBatch];
+  float z = 0.f;
+  for (int c0 = 0; c0 < s.n; c0 += 32) {
+    const int cnt = min(32, s.n - c0);
+    float l = l0;
+    if (c0 > 0) l = lane < cnt ? lse_accum[s.at(c0 + lane)] : -INFINITY;
+    const float w = l == -INFINITY ? 0.f : expf(l - m);
+    z += w;
+    for (int j = 0; j < cnt; j += kBatch) {
+      float4 v[kBatch];
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k)
-      v[k] = __ldg(reinterpret_cast<const float4*>(o_accum + slot_row(i + k * kGroups) * kDv + col));
+      for (int k = 0; k < kBatch; ++k)
+        v[k] = j + k < cnt ? __ldg(reinterpret_cast<const float4*>(o_accum + s.at(c0 + j + k) * kDv + col))
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) add(i + k * kGroups, v[k]);
-  }
-  for (; i < n; i += kGroups) add(i, __ldg(reinterpret_cast<const float4*>(o_accum + slot_row(i) * kDv + col)));
-  if constexpr (kGroups > 1) {
-    if (grp > 0) part[grp - 1][tid & 127] = acc;
-    __syncthreads();
-    if (grp > 0) return;
-#pragma unroll
-    for (int k = 0; k < kGroups - 1; ++k) {
-      const float4 v = part[k][tid];
-      acc.x += v.x;
-      acc.y += v.y;
-      acc.z += v.z;
-      acc.w += v.w;
+      for (int k = 0; k < kBatch; ++k) add4(acc, __shfl_sync(0xffffffffu, w, (j + k) & 31), v[k]);
     }
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+  const float inv = z > 0.f ? 1.f / z : 0.f;
+  acc.x *= inv;
+  acc.y *= inv;
+  acc.z *= inv;
+  acc.w *= inv;
   store4(out, out_type, static_cast<size_t>(g) * kDv + col, acc);
-  if (tid == 0) lse[g] = z > 0.f ? m + logf(z) : -INFINITY;
+  if (threadIdx.x == 0) lse[g] = z > 0.f ? m + logf(z) : -INFINITY;
+}
+
+// Few rows: a block per row, eight warps to each 128 columns, every eighth
+// split each; merged through shared memory.  Bound by the latency of dozens of
+// splits.
+constexpr int kGroups = 8;
+__global__ void __launch_bounds__(128 * kGroups)
+    shared_combine_splits_kernel(const float* __restrict__ o_accum, const float* __restrict__ lse_accum,
+                                 const int32_t* __restrict__ split_offset, int batch, int rows,
+                                 void* __restrict__ out, int out_type, float* __restrict__ lse) {
+  constexpr int kBatch = 4;
+  __shared__ float part_m[kGroups][4], part_z[kGroups][4];
+  __shared__ float4 part[kGroups][128];
+  const long long g = blockIdx.x;
+  const int grp = threadIdx.x >> 7, tid = threadIdx.x & 127, quarter = tid >> 5;
+  const int col = 4 * tid;
+  const RowSplits s = row_splits(split_offset, batch, rows, g);
+  pdl_wait_prior_grid();
+  float m = -INFINITY, z = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = grp; i < s.n; i += kBatch * kGroups) {
+    float4 v[kBatch];
+    float l[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int si = i + k * kGroups;
+      l[k] = si < s.n ? lse_accum[s.at(si)] : -INFINITY;
+      v[k] = si < s.n ? __ldg(reinterpret_cast<const float4*>(o_accum + s.at(si) * kDv + col))
+                      : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float mb = m;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) mb = fmaxf(mb, l[k]);
+    if (mb == -INFINITY) continue;  // nothing but empty splits so far
+    const float r = m == -INFINITY ? 0.f : expf(m - mb);
+    z *= r;
+    acc.x *= r;
+    acc.y *= r;
+    acc.z *= r;
+    acc.w *= r;
+    m = mb;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const float w = l[k] == -INFINITY ? 0.f : expf(l[k] - m);
+      z += w;
+      add4(acc, w, v[k]);
+    }
+  }
+  part[grp][tid] = acc;
+  if ((tid & 31) == 0) {
+    part_m[grp][quarter] = m;
+    part_z[grp][quarter] = z;
+  }
+  __syncthreads();
+  if (grp > 0) return;
+  float top = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < kGroups; ++k) top = fmaxf(top, part_m[k][quarter]);
+  float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+  float total = 0.f;
+#pragma unroll
+  for (int k = 0; k < kGroups; ++k) {
+    const float mk = part_m[k][quarter];
+    const float r = mk == -INFINITY ? 0.f : expf(mk - top);
+    total = fmaf(part_z[k][quarter], r, total);
+    add4(t, r, part[k][tid]);
+  }
+  const float inv = total > 0.f ? 1.f / total : 0.f;
+  store4(out, out_type, static_cast<size_t>(g) * kDv + col, make_float4(t.x * inv, t.y * inv, t.z * inv, t.w * inv));
+  if (tid == 0) lse[g] = total > 0.f ? top + logf(total) : -INFINITY;
 }
 
 }  // namespace
 
 cudaError_t launch_shared_units(const int32_t* block_table, int max_pages, const int32_t* seqlens, int batch,
-                                int s_q, int h_q, int causal, int share, int32_t* units, int32_t* lengths,
+                                int s_q, int h_q, int causal, int32_t* units, int32_t* lengths,
                                 cudaStream_t st) {
-  shared_units_kernel<<<1, 1024, 0, st>>>(block_table, max_pages, seqlens, batch, s_q, h_q, causal, share, units,
-                                          lengths);
+  shared_units_kernel<<<1, 1024, 0, st>>>(block_table, max_pages, seqlens, batch, s_q, h_q, causal, units, lengths);
   return cudaGetLastError();
 }
 
 cudaError_t launch_shared_combine(const float* o_accum, const float* lse_accum, const int32_t* split_offset,
-                                  int batch, int rows, int share, void* out, int out_type, float* lse, int sms,
+                                  int batch, int rows, void* out, int out_type, float* lse, int sms,
                                   cudaStream_t st) {
   const long long total = static_cast<long long>(batch) * rows;
   const bool few = total < 4ll * sms;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(total), 1, 1);
-  cfg.blockDim = dim3(few ? 1024 : 128, 1, 1);
+  cfg.blockDim = dim3(few ? 128 * kGroups : 128, 1, 1);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -203,9 +263,9 @@ cudaError_t launch_shared_combine(const float* o_accum, const float* lse_accum, 
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (few)
-    return cudaLaunchKernelEx(&cfg, shared_combine_kernel<8>, o_accum, lse_accum, split_offset, batch, rows, share,
-                              out, out_type, lse);
-  return cudaLaunchKernelEx(&cfg, shared_combine_kernel<1>, o_accum, lse_accum, split_offset, batch, rows, share, out,
+    return cudaLaunchKernelEx(&cfg, shared_combine_splits_kernel, o_accum, lse_accum, split_offset, batch, rows, out,
+                              out_type, lse);
+  return cudaLaunchKernelEx(&cfg, shared_combine_rows_kernel, o_accum, lse_accum, split_offset, batch, rows, out,
                             out_type, lse);
 }
 

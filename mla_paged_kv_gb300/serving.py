@@ -22,7 +22,7 @@ import math
 
 import torch
 
-from . import (DTYPE_FP8_RECORD, _DTYPE_CODE, _F, _I, _P, _SZ, _check, check_status, load_library, mla_num_parts)
+from . import (DTYPE_FP8_RECORD, _DTYPE_CODE, _F, _I, _P, _SZ, _check, check_status, load_library, MlaError)
 
 _LL = ctypes.c_longlong
 _DTYPE_CODE16 = {d: _DTYPE_CODE[d] for d in (torch.bfloat16, torch.float16)}
@@ -40,11 +40,12 @@ SERVING_SIGS = {
     "mla_prompt_get_plan": (_I, [_P, _P, _I, _I, _I, _I, _P, _SZ, _P, _P]),
     "mla_prompt_attention_fwd": (_I, [_P, _LL, _LL, _P, _LL, _LL, _P, _LL, _LL, _I, _I, _I, _I, _I, _I, _I, _F, _P,
                                       _SZ, _P, _P, _P, _P]),
+    "mla_shared_prefix_num_parts": (_I, [_I, _I, _I]),
     "mla_shared_prefix_plan_bytes": (_SZ, [_I, _I, _I, _I]),
     "mla_shared_prefix_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
     "mla_shared_prefix_get_plan": (_I, [_P, _I, _P, _I, _I, _I, _I, _I, _P, _SZ, _P]),
-    "mla_shared_prefix_decode_fwd": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P, _SZ, _I, _P, _SZ, _P, _I, _P,
-                                          _P, _P]),
+    "mla_shared_prefix_decode_fwd": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _SZ, _I, _P, _SZ, _P, _I,
+                                          _P, _P, _P]),
 }
 SERVING_SYMBOLS = tuple(SERVING_SIGS)
 
@@ -431,6 +432,13 @@ class SharedPrefixPlan:
         self.workspace = workspace
 
 
+def mla_shared_prefix_num_parts(batch: int, s_q: int, h_q: int) -> int:
+    n = load_library().mla_shared_prefix_num_parts(int(batch), int(s_q), int(h_q))
+    if n < 1:
+        raise MlaError(-n, "mla_shared_prefix_num_parts")
+    return n
+
+
 def mla_shared_prefix_plan_bytes(batch: int, s_q: int, h_q: int, num_parts: int) -> int:
     return int(load_library().mla_shared_prefix_plan_bytes(int(batch), int(s_q), int(h_q), int(num_parts)))
 
@@ -476,7 +484,7 @@ def mla_shared_prefix_decode_fwd(q, kv, block_table, pl, out, lse, status, softm
         raise ValueError("the plan or block table was made for another batch")
     plan, ws = pl.plan, pl.workspace
     rc = load_library().mla_shared_prefix_decode_fwd(
-        q_ptr, kv_ptr, table_ptr, max_pages, pages, B, s_q, h_q, code, softmax_scale,
+        q_ptr, kv_ptr, table_ptr, max_pages, pages, B, s_q, h_q, code, 1 if pl.causal else 0, softmax_scale,
         _p(plan, _UINT8, 1, dev, "plan"), plan.shape[0], pl.num_parts, _p(ws, _UINT8, 1, dev, "workspace"),
         ws.shape[0], out_ptr, out_code, lse_ptr, _p(status, _INT32, 1, dev, "status"), _q(stream, dev))
     if rc:
@@ -486,7 +494,7 @@ def mla_shared_prefix_decode_fwd(q, kv, block_table, pl, out, lse, status, softm
 def plan_shared_prefix(block_table, cache_seqlens, s_q, h_q, causal=False, num_parts=None):
     """The plan of a batch: finds the pages that all requests start with."""
     B, max_pages = block_table.shape
-    parts = mla_num_parts(128) if num_parts is None else int(num_parts)
+    parts = mla_shared_prefix_num_parts(B, s_q, h_q) if num_parts is None else int(num_parts)
     size = mla_shared_prefix_plan_bytes(B, s_q, h_q, parts)
     if size == 0:
         raise ValueError("batch, s_q, h_q or num_parts out of range")

@@ -109,7 +109,7 @@ def test_prompt_refusals(change, want):
 
 
 SPLAN = dict(table=P, width=4, lens=P, batch=2, s_q=1, h_q=16, causal=0, parts=4, plan=P, bytes=1 << 16, stream=N)
-SDEC = dict(q=P, kv=P, table=P, width=4, pages=8, batch=2, s_q=1, h_q=16, dt=0, scale=0.1, plan=P, pbytes=1 << 16,
+SDEC = dict(q=P, kv=P, table=P, width=4, pages=8, batch=2, s_q=1, h_q=16, dt=0, causal=0, scale=0.1, plan=P, pbytes=1 << 16,
             parts=4, ws=P, wbytes=1 << 24, out=P, ot=0, lse=P, status=P, stream=N)
 
 
@@ -134,8 +134,9 @@ def test_shared_decode_refusals(change, want):
 def test_shared_prefix_sizes():
     # 64 requests of 16 rows: 8 prefix blocks and 64 own ones; (units + parts) slots of 128 rows
     assert mla.mla_shared_prefix_workspace_bytes(64, 1, 16, 76) == (72 + 76) * 128 * 513 * 4
-    # rows that fill their blocks: no prefix blocks
-    assert mla.mla_shared_prefix_workspace_bytes(64, 1, 128, 76) == (64 + 76) * 128 * 513 * 4
+    # rows that fill their blocks: the plain decode and its workspace
+    assert mla.mla_shared_prefix_workspace_bytes(64, 1, 128, 76) == mla.mla_workspace_bytes(64, 128, 76)
+    assert mla.mla_shared_prefix_workspace_bytes(1, 1, 16, 5) == mla.mla_workspace_bytes(1, 16, 5)
     assert mla.mla_shared_prefix_plan_bytes(0, 1, 16, 76) == 0
 
 
