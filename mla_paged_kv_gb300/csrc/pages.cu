@@ -160,37 +160,35 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(const PageState s, const
     const int len = grown(s, sm, rows, add, i, old_len);
     return len < 0 ? 0 : pages_of(len) - pages_of(old_len);
   });
+  // where the k-th new page goes
+  auto entry_at = [&](int i, int k) {
+    const int r = rows[i];
+    return s.table + static_cast<long long>(r) * s.max_pages + pages_of(s.seqlens[r]) + (k - sm.first[i]);
+  };
   const int want = sm.first[n];
   const int found = scan_free(sm, s.refcount, s.num_pages, want, [&](int k, int page) {
-    const int i = entry_of(sm, n, k);
-    const int r = rows[i];
-    s.table[static_cast<long long>(r) * s.max_pages + pages_of(s.seqlens[r]) + (k - sm.first[i])] = page;
+    *entry_at(entry_of(sm, n, k), k) = page;
+    s.refcount[page] = 1;
   });
-  // counts and lengths; an entry past the last free page gives back its entries
-  const int lane = threadIdx.x & 31;
-  for (int i = threadIdx.x >> 5; i < n; i += kThreads / 32) {
+  if (found < want) {  // the pool ran out: entries past its last page give theirs back
+    for (int k = threadIdx.x; k < found; k += kThreads) {
+      const int i = entry_of(sm, n, k);
+      if (sm.first[i + 1] <= found) continue;
+      int32_t* e = entry_at(i, k);
+      s.refcount[*e] = 0;
+      *e = -1;
+    }
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < n; i += kThreads) {
     int old_len;
     const int len = grown(s, sm, rows, add, i, old_len);
-    if (len < 0) {
-      if (lane == 0) report(s.status, MLA_ERR_BAD_INDEX);
-      continue;
-    }
-    const int need = sm.first[i + 1] - sm.first[i];
-    const bool served = need == 0 || sm.first[i + 1] <= found;
-    int32_t* entry = s.table + static_cast<long long>(rows[i]) * s.max_pages + pages_of(old_len);
-    for (int j = lane; j < need; j += 32) {
-      if (served)
-        s.refcount[entry[j]] = 1;
-      else if (sm.first[i] + j < found)
-        entry[j] = -1;
-    }
-    __syncwarp();
-    if (lane == 0) {
-      if (served)
-        s.seqlens[rows[i]] = len;
-      else
-        report(s.status, MLA_ERR_NO_PAGES);
-    }
+    if (len < 0)
+      report(s.status, MLA_ERR_BAD_INDEX);
+    else if (sm.first[i + 1] > found && sm.first[i + 1] > sm.first[i])
+      report(s.status, MLA_ERR_NO_PAGES);
+    else
+      s.seqlens[rows[i]] = len;
   }
 }
 

@@ -58,7 +58,7 @@ struct AppendParams {
   const int32_t* refcount;
   int32_t* status;
 };
-cudaError_t launch_append(const AppendParams& p, bool half, bool fp8, cudaStream_t stream);
+cudaError_t launch_append(const AppendParams& p, bool half, bool fp8, int sms, cudaStream_t stream);
 
 // The bookkeeping of a page pool.
 struct PageState {

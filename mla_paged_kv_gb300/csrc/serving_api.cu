@@ -166,7 +166,7 @@ int mla_cache_append(const void* d_c, long long c_stride, const void* d_r, long 
   p.refcount = d_refcount;
   p.status = d_status;
   return launched(
-      launch_append(p, in_dtype == MLA_DTYPE_FP16, cache_dtype == MLA_DTYPE_FP8_RECORD, to_stream(stream)));
+      launch_append(p, in_dtype == MLA_DTYPE_FP16, cache_dtype == MLA_DTYPE_FP8_RECORD, sms, to_stream(stream)));
 }
 
 int mla_cache_grow(int32_t* d_refcount, int num_pages, int32_t* d_block_table, int rows, int max_pages,
