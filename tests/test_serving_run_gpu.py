@@ -1,0 +1,169 @@
+"""The serving operators together, as a program uses them: prompts are attended
+and appended, one is forked into samples, the samples grow token by token and
+decode over their shared prefix, some end, the pool is compacted, and the rest
+go on."""
+
+import numpy as np
+import pytest
+import torch
+
+import mla_paged_kv_gb300 as mla
+from oracle import mla_oracle as orc
+from oracle import serving_oracle as so
+from tests.parity import compare
+
+pytestmark = pytest.mark.gpu
+
+H, LAYERS, PAGES, ROWS, WIDTH = 16, 2, 96, 12, 12
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+class Program:
+    """A pool of `LAYERS` layers with its bookkeeping, and random layers' outputs."""
+
+    def __init__(self, fp8, seed):
+        self.g = torch.Generator(device="cuda").manual_seed(seed)
+        self.fp8 = fp8
+        shape = (LAYERS, PAGES, 64, 656 if fp8 else 576)
+        self.pool = torch.zeros(shape, dtype=torch.uint8 if fp8 else torch.bfloat16, device="cuda")
+        self.ref = torch.zeros(PAGES, dtype=torch.int32, device="cuda")
+        self.table = torch.full((ROWS, WIDTH), -1, dtype=torch.int32, device="cuda")
+        self.lens = torch.zeros(ROWS, dtype=torch.int32, device="cuda")
+        self.weight = (1 + 0.1 * self.rand(512)).to(torch.bfloat16)
+        ang = torch.arange(WIDTH * 64)[:, None] * 10000.0 ** (-torch.arange(32) / 32.0)[None]
+        self.cos_sin = torch.cat([ang.cos(), ang.sin()], 1).float().cuda()
+        self.status = i32([0])
+        self.count = torch.zeros(PAGES, dtype=torch.int64)
+
+    def rand(self, *s):
+        return torch.randn(*s, device="cuda", generator=self.g)
+
+    def append(self, rows, new):
+        """New tokens of `rows` in every layer; rows must have grown."""
+        idx = torch.tensor(rows, device="cuda")
+        cu = None if len(set(new)) == 1 else i32([0] + list(np.cumsum(new)))
+        for layer in range(LAYERS):
+            kv_a = self.rand(sum(new), 576).to(torch.bfloat16)
+            mla.cache_append(kv_a[:, :512], kv_a[:, 512:], self.pool[layer], self.table[idx], self.lens[idx],
+                             cu_seqlens=cu, norm_weight=self.weight, cos_sin=self.cos_sin, rope_interleaved=True,
+                             refcount=self.ref, status=self.status)
+
+    def oracle(self, q, rows, layer):
+        table, lens = self.table[rows].cpu().numpy(), self.lens[rows].cpu().numpy()
+        kv = self.pool[layer].cpu()
+        kv = kv.numpy() if self.fp8 else kv.float().numpy()
+        fn = orc.dense_fp8_decode if self.fp8 else orc.dense_decode
+        return fn(q.double().cpu().numpy(), kv, table, lens, False, 1 / 24)[:2]
+
+    def decode(self, rows, check=True):
+        idx = torch.tensor(rows, device="cuda")
+        table, lens = self.table[idx], self.lens[idx]
+        outs = []
+        pl = None if self.fp8 else mla.plan_shared_prefix(table, lens, 1, H)
+        for layer in range(LAYERS):
+            q = torch.randn(len(rows), 1, H, 576, device="cuda",
+                            generator=torch.Generator(device="cuda").manual_seed(layer)).to(torch.bfloat16)
+            if self.fp8:
+                out, lse = mla.decode(q, self.pool[layer], table, lens)
+            else:
+                out, lse = mla.shared_prefix_decode(q, self.pool[layer], table, lens, pl=pl, status=self.status)
+            if check:
+                compare(out, lse, *self.oracle(q, idx, layer))
+            outs.append((out, lse))
+        return outs
+
+    def audit(self):
+        """Every count equals the number of entries that name the page."""
+        used = torch.zeros(PAGES, dtype=torch.int32)
+        for r, n in enumerate(self.lens.tolist()):
+            for p in self.table[r, :-(-n // 64)].tolist():
+                used[p] += 1
+        assert torch.equal(used, self.ref.cpu())
+        assert int(self.status) == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_prompts_samples_and_compaction(fp8):
+    p = Program(fp8, seed=21 + fp8)
+    prompts = [300, 77]
+    # prompts: attention over the expanded heads, then their latent rows into the cache
+    q, k, v = (p.rand(sum(prompts), 4, d).to(torch.bfloat16) for d in (192, 192, 128))
+    cu = [0, 300, 377]
+    out, lse = mla.prompt_attention(q, k, v, i32(cu), status=p.status)
+    want, wlse, mix, _ = so.prompt_attention(q.double().cpu().numpy(), k.double().cpu().numpy(),
+                                             v.double().cpu().numpy(), cu, cu, True, 192 ** -0.5)
+    assert np.all(np.abs(out.double().cpu().numpy() - want) <= 2.0 ** -7 * mix + 2.0 ** -8 * np.abs(want))
+    mla.cache_grow(p.ref, p.table, p.lens, i32([0, 1]), i32(prompts), status=p.status)
+    p.append([0, 1], prompts)
+    p.audit()
+    # six samples of the first prompt
+    samples = [2, 3, 4, 5, 6, 7]
+    pairs = mla.cache_fork(p.ref, p.table, p.lens, i32([0] * 6), i32(samples), status=p.status)
+    mla.cache_copy_pages(p.pool, pairs, layered=True, status=p.status)
+    p.audit()
+    for _ in range(3):
+        mla.cache_grow(p.ref, p.table, p.lens, i32(samples), i32([1] * 6), status=p.status)
+        p.append(samples, [1] * 6)
+        p.decode(samples)
+    # a chunk of different lengths for each, past a page
+    mla.cache_grow(p.ref, p.table, p.lens, i32(samples), i32([30, 1, 64, 9, 100, 17]), status=p.status)
+    p.append(samples, [30, 1, 64, 9, 100, 17])
+    p.audit()
+    # some end; the pool is compacted; the others read the same keys from other pages
+    mla.cache_free(p.ref, p.table, p.lens, i32([0, 3, 6]), status=p.status)
+    stay = [2, 4, 5, 7]
+    before = p.decode(stay)
+    moves, count = mla.cache_compact(p.ref, p.table, p.lens, status=p.status)
+    mla.cache_copy_pages(p.pool, moves, count=count, layered=True, status=p.status)
+    p.audit()
+    live = int((p.ref > 0).sum())
+    assert int(count) > 0 and not p.ref[live:].any()
+    for (o1, l1), (o2, l2) in zip(before, p.decode(stay)):
+        assert torch.equal(o1, o2) and torch.equal(l1, l2)
+    # the pages of the shared prompt are still shared: appending into one is refused
+    st = i32([0])
+    kv = p.rand(1, 576).to(torch.bfloat16)
+    snapshot = p.pool.clone()
+    mla.cache_append(kv[:, :512], kv[:, 512:], p.pool[0], p.table[2:3], i32([64]), refcount=p.ref, status=st)
+    assert int(st) == 5 and torch.equal(snapshot, p.pool)
+    mla.cache_free(p.ref, p.table, p.lens, i32(list(range(8))), status=p.status)
+    p.audit()
+    assert not p.ref.any()
+
+
+def test_a_decode_step_as_one_graph():
+    """Grow, append, plan and decode of a step captured once and replayed: all sizes live on the device."""
+    p = Program(False, seed=33)
+    mla.cache_grow(p.ref, p.table, p.lens, i32([0]), i32([200]), status=p.status)
+    p.append([0], [200])
+    samples = [1, 2, 3, 4]
+    mla.cache_copy_pages(p.pool, mla.cache_fork(p.ref, p.table, p.lens, i32([0] * 4), i32(samples), status=p.status),
+                         layered=True, status=p.status)
+    rows, one = i32(samples), i32([1] * 4)
+    kv = p.rand(4, 576).to(torch.bfloat16)
+    q = p.rand(4, 1, H, 576).to(torch.bfloat16)
+    table, lens = p.table[1:5], p.lens[1:5]
+    pl = mla.plan_shared_prefix(table, lens, 1, H)
+    out = torch.empty(4, 1, H, 512, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(4, 1, H, device="cuda")
+
+    def step():
+        mla.mla_cache_grow(p.ref, p.table, p.lens, rows, one, p.status)
+        mla.mla_cache_append(kv[:, :512], kv[:, 512:], p.pool[0], table, lens, p.status, cos_sin=p.cos_sin,
+                             refcount=p.ref)
+        mla.mla_shared_prefix_get_plan(table, lens, 1, H, False, pl.num_parts, pl.plan)
+        mla.mla_shared_prefix_decode_fwd(q, p.pool[0], table, pl, out, lse, p.status)
+
+    step()  # (first use of every kernel outside the capture)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for n in range(202, 270):
+        graph.replay()
+        if n in (202, 230, 256, 257, 269):
+            assert p.lens[1:5].tolist() == [n] * 4
+            compare(out, lse, *p.oracle(q, torch.tensor(samples, device="cuda"), 0))
+    p.audit()
