@@ -175,8 +175,8 @@ int mla_prompt_attention_fwd(const void* d_q, long long q_token_stride, long lon
 
 /* ------------------------------------------------------------ shared prefix */
 
-/* Dense decode (mla_decode_fwd, one latent KV head, bf16 or fp16) for a batch
- * whose requests start with the same pages, as after mla_cache_fork: the
+/* Dense decode (mla_decode_fwd with one latent KV head: a bf16 or fp16 cache, or
+ * FP8 records with a bf16 query) for a batch whose requests start with the same pages, as after mla_cache_fork: the
  * shared pages are attended once for all requests' queries, 128 rows at a
  * time, and merged with each request's own pages.
  *

@@ -27,7 +27,7 @@ const void* dense_kernel_ptr(int kind);
 cudaError_t launch_sparse(const CUtensorMap&, const DecodeParams&, int, int, cudaStream_t);
 int sparse_smem_bytes();
 int sparse_threads();
-const void* sparse_kernel_ptr(int stall);
+const void* sparse_kernel_ptr(int kind);
 cudaError_t launch_unpack(const uint8_t*, int, const int32_t*, int, float*, int32_t*, cudaStream_t);
 cudaError_t launch_pack(const uint8_t*, int, const int32_t*, int, const int32_t*, int, uint8_t*, uint64_t*,
                         int32_t*, int, cudaStream_t);
@@ -101,8 +101,8 @@ const DeviceInfo& device_info() {
     return d;
   }
   bool attr_ok = true;
-  for (int stall = 0; stall < 2; ++stall)
-    attr_ok = attr_ok && cudaFuncSetAttribute(sparse_kernel_ptr(stall), cudaFuncAttributeMaxDynamicSharedMemorySize,
+  for (int kind = 0; kind < 3; ++kind)
+    attr_ok = attr_ok && cudaFuncSetAttribute(sparse_kernel_ptr(kind), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                               sparse_smem_bytes()) == cudaSuccess;
   for (int kind = 0; kind < 7; ++kind)
     attr_ok = attr_ok && cudaFuncSetAttribute(dense_kernel_ptr(kind), cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -418,14 +418,9 @@ int fp8_record_splits(const void* d_q, const void* d_kv, const int32_t* d_block_
 
 namespace mla {
 
-// The shared-prefix launch of the dense kernel: n_units units of 128 rows.
+// The shared-prefix launch of a decode kernel (the dense one, or for FP8
+// records the sparse one): n_units units of up to 128 rows.
 int launch_shared(const SharedLaunch& c, cudaStream_t stream) {
-  CUtensorMap qm, km, sm, rm;
-  int rc = encode_q_map(&qm, c.q, c.total_rows);
-  if (rc == MLA_OK) rc = encode_kv_map(&km, c.kv, c.num_pages, 1, 4);
-  if (rc == MLA_OK) rc = encode_kv_map(&sm, c.kv, c.num_pages, 1, 5);
-  if (rc == MLA_OK) rc = encode_kv_map(&rm, c.kv, c.num_pages, 1, 1);
-  if (rc != MLA_OK) return rc;
   DecodeParams p{};
   p.lengths = c.lengths;
   p.n_units = c.n_units;
@@ -447,7 +442,21 @@ int launch_shared(const SharedLaunch& c, cudaStream_t stream) {
   p.lse_accum = c.lse_accum;
   p.out_type = MLA_DTYPE_FP32;
   p.status = c.status;
-  return launch_dense(qm, km, sm, rm, p, c.num_parts, c.half ? 6 : 5, stream) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  CUtensorMap qm, km, sm, rm;
+  int rc = encode_q_map(&qm, c.q, c.total_rows);
+  if (rc != MLA_OK) return rc;
+  if (c.dtype == MLA_DTYPE_FP8_RECORD) {
+    p.kv8 = static_cast<const uint8_t*>(c.kv);
+    p.topk = c.max_pages * MLA_PAGE_SIZE;
+    p.unit_request_div = 1;
+    return launch_sparse(qm, p, c.num_parts, 2, stream) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  }
+  rc = encode_kv_map(&km, c.kv, c.num_pages, 1, 4);
+  if (rc == MLA_OK) rc = encode_kv_map(&sm, c.kv, c.num_pages, 1, 5);
+  if (rc == MLA_OK) rc = encode_kv_map(&rm, c.kv, c.num_pages, 1, 1);
+  if (rc != MLA_OK) return rc;
+  const int kind = c.dtype == MLA_DTYPE_FP16 ? 6 : 5;
+  return launch_dense(qm, km, sm, rm, p, c.num_parts, kind, stream) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 cudaError_t launch_plan(const int32_t* lengths, int n_units, int num_parts, int32_t* sched, int32_t* split_offset,

@@ -67,8 +67,8 @@ struct DecodeParams {
   // block-table row b / unit_request_div (s_q when a unit is one query token
   // of a request, 1 when it is the whole request)
   int unit_request_div;
-  // shared-prefix plan (dense kernel, kShared): what each unit is, kUnitInts
-  // int32 each (SharedUnit); rows = 128, a unit's rows being its own count
+  // shared-prefix plan (kShared instances): what each unit is, kUnitInts int32
+  // each (SharedUnit); rows = 128, a unit's rows being its own count
   const int32_t* units;
   // schedule
   const int32_t* sched;
@@ -82,5 +82,10 @@ struct DecodeParams {
   float* lse;               // [n_units, rows]
   int32_t* status;
 };
+
+__device__ __forceinline__ SharedUnit load_unit(const DecodeParams& p, int u) {
+  const int32_t* e = p.units + u * kUnitInts;
+  return SharedUnit{e[0], e[1], e[2], e[3], e[4]};
+}
 
 }  // namespace mla

@@ -255,11 +255,6 @@ __device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity
   return __all_sync(0xffffffffu, mbar_wait<true>(bar, parity, abort_flag, limit_ns));
 }
 
-__device__ __forceinline__ SharedUnit load_unit(const DecodeParams& p, int u) {
-  const int32_t* e = p.units + u * kUnitInts;
-  return SharedUnit{e[0], e[1], e[2], e[3], e[4]};
-}
-
 // Page ids of 32 consecutive pages of unit c.b starting at `base`, one per lane
 // (0 past the partition's range; ids outside the pool are reported and read
 // as page 0, whose keys the softmax then masks).

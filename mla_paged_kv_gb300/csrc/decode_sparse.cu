@@ -257,8 +257,16 @@ __device__ __forceinline__ uint4 codes_to_bf16(uint2 codes) {
 // Dense FP8 cache: every token is a key; slot t of unit b is record t % 64
 // of page block_table[b / unit_request_div][t / 64] (a unit is a whole
 // request); a page outside the pool comes back as -2 (reported, masked).
+// kShared: the unit's own run of block-table entries.
+template <bool kShared>
 __device__ __forceinline__ int load_slot(const DecodeParams& p, int b, int t, int L) {
   if (t >= L) return -1;
+  if constexpr (kShared) {
+    const SharedUnit su = load_unit(p, b);
+    const int pg = t / kT;
+    const int page = pg < su.avail ? __ldg(p.block_table + su.table_off + pg) : -1;
+    return (page < 0 || page >= p.num_pages) ? -2 : page * kT + (t - pg * kT);
+  }
   if (p.block_table != nullptr) {
     const int pg = t / kT;
     const int page =
@@ -325,7 +333,10 @@ __device__ __forceinline__ void issue_pv(uint32_t tmem, uint64_t p_desc0, uint64
   }
 }
 
-template <bool kStall>
+// kShared: units of a shared-prefix plan over a cache of FP8 records (128-row
+// blocks of all requests' queries over the pages they share, and each request's
+// own rows over the rest); one row block a unit, always split partials.
+template <bool kStall, bool kShared = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     sparse_decode_kernel(const __grid_constant__ CUtensorMap q_map, const DecodeParams p) {
   constexpr uint64_t kWaitNs = kStall ? kDecodeStallWaitNs : MLA_WAIT_LIMIT_NS;
@@ -416,7 +427,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (u >= 1) ok = mbar_wait(&bars[Q_EMPTY], (u - 1) & 1, abort_flag, kWaitNs);
         if (ok) {
           mbar_arrive_expect_tx(&bars[Q_FULL], n_boxes * kQBoxBytes);
-          const int row0 = b * p.rows + rb * kRowsPerBlock;
+          const int row0 = kShared ? p.units[b * kUnitInts] : b * p.rows + rb * kRowsPerBlock;
           for (int lb = 0; lb < n_boxes; ++lb)
             tma_load_2d(sQ + lb * kQBoxBytes, &q_map, &bars[Q_FULL], box_dim(rank, lb), row0, pol_q);
           ++q_issued;
@@ -463,8 +474,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       };
       // slot entries are loaded two tiles ahead of their records, so that no
       // tile waits for an index load
-      int entry = ptid < kT ? load_slot(p, b, lo * kT + ptid, L) : -1;
-      int entry_n = (ptid < kT && lo + 1 < hi) ? load_slot(p, b, (lo + 1) * kT + ptid, L) : -1;
+      int entry = ptid < kT ? load_slot<kShared>(p, b, lo * kT + ptid, L) : -1;
+      int entry_n = (ptid < kT && lo + 1 < hi) ? load_slot<kShared>(p, b, (lo + 1) * kT + ptid, L) : -1;
       publish_indices(entry, t);
       issue_loads(t, raw, sc);
       for (int k = lo; ok && k < hi; ++k, ++t) {
@@ -473,7 +484,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         float sc_n[2];
         if (k + 1 < hi) {
           publish_indices(entry_n, t + 1);
-          entry_n = (ptid < kT && k + 2 < hi) ? load_slot(p, b, (k + 2) * kT + ptid, L) : -1;
+          entry_n = (ptid < kT && k + 2 < hi) ? load_slot<kShared>(p, b, (k + 2) * kT + ptid, L) : -1;
           issue_loads(t + 1, raw_n, sc_n);
         }
         bool failed = false;
@@ -654,11 +665,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int lo, hi;
       unit_tiles(P, b, nt, lo, hi);
       if (hi <= lo) continue;
+      const SharedUnit su = kShared ? load_unit(p, b) : SharedUnit{};
+      const int unit_rows = kShared ? su.rows : p.rows;
       const int row = rb * kRowsPerBlock + r;
-      const bool row_ok = row < p.rows;
+      const bool row_ok = row < unit_rows;
       // last key this row sees: with the causal mask, query token i of a
       // request with L keys ends at key L - s_q + i (rows are token-major)
-      const int row_last = p.causal ? L - p.s_q + row / p.h_q : L - 1;
+      const bool causal = kShared ? su.rel >= 0 : p.causal != 0;
+      const int row_last = causal ? L - p.s_q + (kShared ? su.rel + row : row) / p.h_q : L - 1;
       // running max (log2 units), the same in both threads of a row, and
       // this thread's part of the fp32 row sum
       float m_used = -INFINITY, l_part = 0.f;
@@ -886,7 +900,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const float inv_l = l_sum > 0.f ? 1.f / l_norm : 0.f;
       const size_t orow = static_cast<size_t>(b) * p.rows + row;
       const size_t arow = static_cast<size_t>(slot) * p.rows + row;
-      const bool direct = (nsplit == 1);
+      const bool direct = !kShared && nsplit == 1;
       const bool out16 = direct && p.out_type != MLA_DTYPE_FP32;
       const bool half = p.out_type == MLA_DTYPE_FP16;
       // Through a 4 KB stage per warp (its own rows' bytes of the P buffer,
@@ -937,7 +951,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = lane; i < 32 * pieces; i += 32) {
           const int rl = i / pieces, pc = i - rl * pieces;
           const int row_g = row_base + rl;
-          if (row_g < p.rows) {
+          if (row_g < unit_rows) {
             const uint4 val = reinterpret_cast<const uint4*>(stage + rl * 128)[pc ^ (rl & 7)];
             if (out16) {
               uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
@@ -1146,16 +1160,20 @@ __global__ void __launch_bounds__(256) unpack_kernel(const uint8_t* __restrict__
 
 int sparse_smem_bytes() { return sp::kSmemBytes; }
 int sparse_threads() { return sp::kThreads; }
-// stall 1: the test instance whose first tile's scores are never computed
-const void* sparse_kernel_ptr(int stall) {
-  return stall ? reinterpret_cast<const void*>(&sp::sparse_decode_kernel<true>)
-               : reinterpret_cast<const void*>(&sp::sparse_decode_kernel<false>);
+// kind 1: the test instance whose first tile's scores are never computed;
+// 2: under a shared-prefix plan
+const void* sparse_kernel_ptr(int kind) {
+  return kind == 2   ? reinterpret_cast<const void*>(&sp::sparse_decode_kernel<false, true>)
+         : kind == 1 ? reinterpret_cast<const void*>(&sp::sparse_decode_kernel<true>)
+                     : reinterpret_cast<const void*>(&sp::sparse_decode_kernel<false>);
 }
 
-cudaError_t launch_sparse(const CUtensorMap& q_map, const DecodeParams& p, int num_parts, int stall,
+cudaError_t launch_sparse(const CUtensorMap& q_map, const DecodeParams& p, int num_parts, int kind,
                           cudaStream_t stream) {
   const dim3 grid(2 * num_parts * p.row_blocks);
-  if (stall)
+  if (kind == 2)
+    sp::sparse_decode_kernel<false, true><<<grid, sp::kThreads, sp::kSmemBytes, stream>>>(q_map, p);
+  else if (kind == 1)
     sp::sparse_decode_kernel<true><<<grid, sp::kThreads, sp::kSmemBytes, stream>>>(q_map, p);
   else
     sp::sparse_decode_kernel<false><<<grid, sp::kThreads, sp::kSmemBytes, stream>>>(q_map, p);

@@ -15,14 +15,14 @@ int device_ready(int* sms);
 int encode_map16(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
                  const cuuint32_t* box);
 
-// The dense decode kernel over the units of a shared-prefix plan, and the
-// scheduler over unit lengths (both with the decode's own code).
+// The decode kernels over the units of a shared-prefix plan, and the scheduler
+// over unit lengths (both with the decode's own code).
 struct SharedLaunch {
   const void* q;
   const void* kv;
   long long total_rows;  // batch * s_q * h_q
-  int num_pages, n_units, s_q, h_q, num_parts;
-  bool half;
+  int num_pages, max_pages, n_units, s_q, h_q, num_parts;
+  int dtype;  // MLA_DTYPE_BF16, _FP16 or _FP8_RECORD
   float scale_log2;
   const int32_t *block_table, *units, *lengths, *sched, *split_offset;
   float *o_accum, *lse_accum;  // [slots][128][512], [slots][128]

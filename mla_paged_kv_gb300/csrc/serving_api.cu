@@ -362,8 +362,8 @@ int mla_shared_prefix_decode_fwd(const void* d_q, const void* d_kv, const int32_
   if (!d_q || !d_kv || !d_block_table || !d_plan || !d_workspace || !d_out || !d_lse || !d_status)
     return MLA_ERR_INVALID_ARG;
   if (max_pages < 1 || num_pages < 1) return MLA_ERR_INVALID_ARG;
-  if (dtype != MLA_DTYPE_BF16 && dtype != MLA_DTYPE_FP16)
-    return dtype == MLA_DTYPE_FP8_RECORD ? MLA_ERR_UNSUPPORTED : MLA_ERR_INVALID_ARG;
+  if (dtype != MLA_DTYPE_BF16 && dtype != MLA_DTYPE_FP16 && dtype != MLA_DTYPE_FP8_RECORD)
+    return MLA_ERR_INVALID_ARG;
   if (out_type != MLA_DTYPE_BF16 && out_type != MLA_DTYPE_FP32 && out_type != MLA_DTYPE_FP16)
     return MLA_ERR_INVALID_ARG;
   if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.f)) return MLA_ERR_INVALID_ARG;
@@ -374,7 +374,7 @@ int mla_shared_prefix_decode_fwd(const void* d_q, const void* d_kv, const int32_
   int rc = shared_sizes(batch, s_q, h_q, num_parts, &z);
   if (rc != MLA_OK) return rc;
   if (max_pages > kMaxRowPages || static_cast<long long>(batch) * max_pages > kMaxInt ||
-      static_cast<long long>(num_pages) * MLA_PAGE_SIZE > kMaxInt + 1)
+      static_cast<long long>(num_pages) * MLA_PAGE_SIZE > kMaxInt)
     return MLA_ERR_UNSUPPORTED;
   if (plan_bytes < z.plan_bytes || workspace_bytes < z.ws_bytes) return MLA_ERR_INVALID_ARG;
   int sms = 0;
@@ -396,7 +396,8 @@ int mla_shared_prefix_decode_fwd(const void* d_q, const void* d_kv, const int32_
   c.s_q = s_q;
   c.h_q = h_q;
   c.num_parts = num_parts;
-  c.half = dtype == MLA_DTYPE_FP16;
+  c.max_pages = max_pages;
+  c.dtype = dtype;
   c.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * 1.4426950408889634);
   c.block_table = d_block_table;
   c.units = reinterpret_cast<const int32_t*>(plan);

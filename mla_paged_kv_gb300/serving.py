@@ -460,23 +460,25 @@ def mla_shared_prefix_get_plan(block_table, cache_seqlens, s_q, h_q, causal, num
 
 
 def mla_shared_prefix_decode_fwd(q, kv, block_table, pl, out, lse, status, softmax_scale=1.0 / 24.0, stream=None):
-    """q [B, s_q, h_q, 576] and kv [pages, 64, 576], both bf16 or both fp16; pl a
-    SharedPrefixPlan of this block table; out [B, s_q, h_q, 512] bf16, fp16 or
-    fp32, lse fp32 [B, s_q, h_q]."""
+    """q [B, s_q, h_q, 576] and kv [pages, 64, 576], both bf16 or both fp16, or a
+    bf16 q over FP8 records (uint8 [pages, 64, 656]); pl a SharedPrefixPlan of
+    this block table; out [B, s_q, h_q, 512] bf16, fp16 or fp32, lse fp32
+    [B, s_q, h_q]."""
     dt = q.dtype
     code, out_code = _DTYPE_CODE16.get(dt), _DTYPE_CODE.get(out.dtype)
-    if code is None or kv.dtype is not dt:
-        raise TypeError("q and kv must be both bf16 or both fp16")
+    fp8 = kv.dtype is _UINT8
+    if code is None or (kv.dtype is not dt and not (fp8 and dt is torch.bfloat16)):
+        raise TypeError("q and kv must be both bf16 or both fp16, or a bf16 q over FP8 records")
     if out_code is None:
         raise TypeError("out must be bf16, fp16 or fp32")
     dev = q.get_device()
-    q_ptr, kv_ptr = _p(q, dt, 4, dev, "q"), _p(kv, dt, 3, dev, "kv")
+    q_ptr, kv_ptr = _p(q, dt, 4, dev, "q"), _p(kv, kv.dtype, 3, dev, "kv")
     table_ptr = _p(block_table, _INT32, 2, dev, "block_table")
     out_ptr, lse_ptr = _p(out, out.dtype, 4, dev, "out"), _p(lse, _FP32, 3, dev, "lse")
     B, s_q, h_q, d = q.shape
     pages, page, width = kv.shape
-    if d != 576 or page != 64 or width != 576:
-        raise ValueError("q must be [B, s_q, h_q, 576] and kv [pages, 64, 576]")
+    if d != 576 or page != 64 or width != (656 if fp8 else 576):
+        raise ValueError("q must be [B, s_q, h_q, 576] and kv [pages, 64, 576] or records [pages, 64, 656]")
     if out.shape != (B, s_q, h_q, 512) or lse.shape != (B, s_q, h_q):
         raise ValueError("out must be [B, s_q, h_q, 512] and lse [B, s_q, h_q]")
     batch, max_pages = block_table.shape
@@ -484,7 +486,7 @@ def mla_shared_prefix_decode_fwd(q, kv, block_table, pl, out, lse, status, softm
         raise ValueError("the plan or block table was made for another batch")
     plan, ws = pl.plan, pl.workspace
     rc = load_library().mla_shared_prefix_decode_fwd(
-        q_ptr, kv_ptr, table_ptr, max_pages, pages, B, s_q, h_q, code, 1 if pl.causal else 0, softmax_scale,
+        q_ptr, kv_ptr, table_ptr, max_pages, pages, B, s_q, h_q, DTYPE_FP8_RECORD if fp8 else code, 1 if pl.causal else 0, softmax_scale,
         _p(plan, _UINT8, 1, dev, "plan"), plan.shape[0], pl.num_parts, _p(ws, _UINT8, 1, dev, "workspace"),
         ws.shape[0], out_ptr, out_code, lse_ptr, _p(status, _INT32, 1, dev, "status"), _q(stream, dev))
     if rc:

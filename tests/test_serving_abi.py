@@ -125,7 +125,7 @@ def test_shared_plan_refusals(change, want):
 @pytest.mark.parametrize("change,want", [
     (dict(q=N), INVALID), (dict(kv=N), INVALID), (dict(table=N), INVALID), (dict(plan=N), INVALID),
     (dict(ws=N), INVALID), (dict(out=N), INVALID), (dict(lse=N), INVALID), (dict(status=N), INVALID),
-    (dict(dt=1), INVALID), (dict(dt=3), UNSUPPORTED), (dict(ot=3), INVALID), (dict(scale=-1.0), INVALID),
+    (dict(dt=1), INVALID), (dict(dt=4), INVALID), (dict(ot=3), INVALID), (dict(scale=-1.0), INVALID),
     (dict(pbytes=64), INVALID), (dict(wbytes=64), INVALID), (dict(pages=0), INVALID), (dict(q=ODD), INVALID)])
 def test_shared_decode_refusals(change, want):
     assert mla.load_library().mla_shared_prefix_decode_fwd(*{**SDEC, **change}.values()) == want

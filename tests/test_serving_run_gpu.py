@@ -62,14 +62,11 @@ class Program:
         idx = torch.tensor(rows, device="cuda")
         table, lens = self.table[idx], self.lens[idx]
         outs = []
-        pl = None if self.fp8 else mla.plan_shared_prefix(table, lens, 1, H)
+        pl = mla.plan_shared_prefix(table, lens, 1, H)
         for layer in range(LAYERS):
             q = torch.randn(len(rows), 1, H, 576, device="cuda",
                             generator=torch.Generator(device="cuda").manual_seed(layer)).to(torch.bfloat16)
-            if self.fp8:
-                out, lse = mla.decode(q, self.pool[layer], table, lens)
-            else:
-                out, lse = mla.shared_prefix_decode(q, self.pool[layer], table, lens, pl=pl, status=self.status)
+            out, lse = mla.shared_prefix_decode(q, self.pool[layer], table, lens, pl=pl, status=self.status)
             if check:
                 compare(out, lse, *self.oracle(q, idx, layer))
             outs.append((out, lse))

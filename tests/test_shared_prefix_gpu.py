@@ -18,7 +18,8 @@ def i32(v):
 
 
 class Case:
-    def __init__(self, head, tails, s_q, h_q, causal=False, dtype=torch.bfloat16, seed=0, amp=1.0, poison=True):
+    def __init__(self, head, tails, s_q, h_q, causal=False, dtype=torch.bfloat16, seed=0, amp=1.0, poison=True,
+                 fp8=False):
         """head: shared pages; tails: each request's keys behind them."""
         g = torch.Generator().manual_seed(seed)
         B = len(tails)
@@ -36,10 +37,23 @@ class Case:
         for b, n in enumerate(self.lens):  # finite poison behind the last key
             if poison and n % 64:
                 self.kv[self.table[b, n // 64], n % 64:] = 1000.0
+        if fp8:  # the same rows as records: 128-element groups, scale = max / 448
+            x = self.kv.float().reshape(pages * 64, 576)
+            rec = torch.empty(pages * 64, 656, dtype=torch.uint8)
+            top = x[:, :512].reshape(-1, 4, 128).abs().amax(2)
+            scale = torch.where(top > 0, top / 448, torch.ones_like(top))
+            rec[:, :512] = (x[:, :512].reshape(-1, 4, 128) / scale[..., None]).clamp(-448, 448).to(
+                torch.float8_e4m3fn).view(torch.uint8).reshape(-1, 512)
+            rec[:, 512:528] = scale.contiguous().view(torch.uint8)
+            rec[:, 528:] = x[:, 512:].to(torch.bfloat16).contiguous().view(torch.uint8)
+            self.kv = rec.reshape(pages, 64, 656)
         self.q = (amp * torch.randn(B, s_q, h_q, 576, generator=g)).to(dtype)
         self.causal, self.s_q, self.h_q = causal, s_q, h_q
 
     def want(self):
+        if self.kv.dtype == torch.uint8:
+            return orc.dense_fp8_decode(self.q.double().numpy(), self.kv.numpy(), self.table,
+                                        np.array(self.lens, dtype=np.int32), self.causal, 1 / 24)[:2]
         return orc.dense_decode(self.q.double().numpy(), self.kv.float().numpy(), self.table,
                                 np.array(self.lens, dtype=np.int32), self.causal, 1 / 24)
 
@@ -74,6 +88,23 @@ def test_rows_per_request(s_q, h_q, causal):
 def test_types(dtype, out_fp32):
     out, _ = Case(9, [30, 90, 128], 1, 32, dtype=dtype, seed=4).check(out_fp32=out_fp32)
     assert out.dtype == (torch.float32 if out_fp32 else dtype)
+
+
+@pytest.mark.parametrize("head,tails,s_q,h_q,causal", [
+    (1, [1, 64], 1, 16, False), (9, [65, 3, 130, 64, 1], 1, 16, False), (17, [0, 5, 0], 1, 64, False),
+    (5, [2, 64, 100, 70, 5, 200, 65], 2, 16, True), (5, [3, 64, 100, 70], 3, 40, True), (5, [5, 7], 1, 128, False),
+    (40, [10, 700, 64, 1], 1, 16, False), (30, [64] * 50, 1, 8, False)])
+@pytest.mark.parametrize("out_fp32", [False, True])
+def test_fp8_records(head, tails, s_q, h_q, causal, out_fp32):
+    Case(head, tails, s_q, h_q, causal, seed=head, fp8=True).check(out_fp32=out_fp32)
+
+
+def test_fp8_records_peaky_and_cut():
+    Case(20, [30, 300, 64], 1, 16, seed=6, amp=8.0, fp8=True).check()
+    c = Case(6, [64, 100, 5], 2, 16, True, seed=9, fp8=True)
+    for n in (3 * 64, 3 * 64 + 1, 65, 2, 1, 0):
+        c.lens[1] = n
+        c.check()
 
 
 @pytest.mark.parametrize("num_parts", [1, 2, 7, 300])
@@ -131,9 +162,10 @@ def test_same_as_the_decode_of_each_request():
     assert torch.all((lse - l2).abs() <= 1e-4)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("where", ["prefix", "tail"])
-def test_bad_page_is_masked_and_reported(where):
-    c = Case(4, [64, 100, 130], 1, 16, seed=14)
+def test_bad_page_is_masked_and_reported(where, fp8):
+    c = Case(4, [64, 100, 130], 1, 16, seed=14, fp8=fp8)
     if where == "prefix":
         c.table[:, 2] = 10 ** 6
     else:
@@ -152,7 +184,7 @@ def test_refusals():
     c = Case(4, [64, 100], 1, 16, seed=15)
     q, kv, table, lens = c.q.cuda(), c.kv.cuda(), torch.from_numpy(c.table).cuda(), i32(c.lens)
     pl = mla.plan_shared_prefix(table, lens, 1, 16)
-    for bad in (dict(q=q.half()), dict(kv=kv.view(torch.uint8)), dict(table=table[:1]), dict(q=q[:, :, :8]),
+    for bad in (dict(q=q.half()), dict(kv=kv.float()), dict(table=table[:1]), dict(q=q[:, :, :8]),
                 dict(causal=True), dict(lens=None, q=q[..., :512])):
         a = {**dict(q=q, kv=kv, table=table, causal=False), **{k: v for k, v in bad.items() if k != "lens"}}
         with pytest.raises((TypeError, ValueError)):
