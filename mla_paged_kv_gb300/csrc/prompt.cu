@@ -148,22 +148,42 @@ __device__ __forceinline__ int half_tiles(const Tile& t, int h, int half_rows, i
   return keys > 0 ? (keys + kBN - 1) / kBN : 0;
 }
 
-// The items of one worker, the same in every role: item `round` is number
-// round * workers + worker of the list, counted backwards in every other round,
-// so that the sums of a descending list come out nearly equal.  An item is one
-// tile of the plan and one query head, all heads of a tile in a row.
+// The items of one worker, the same in every role.  An item is one tile of the
+// plan and one query head, all heads of a tile in a row in the list.  In round r
+// a worker gets number r * workers + worker of the list, counted backwards in
+// every other round, so that the sums of the descending list come out nearly
+// equal.  It runs them 32 rounds at a time in the order of their heads: the
+// workers then read the keys of few heads at a time, which stay in L2.  (In the
+// list's order a ragged batch read its keys 2.3 times from HBM.)
 struct Items {
-  int round, at, total;  // at: the current item's number
-  int causal;
+  int at, total;  // the current item's number; `total`: no more
+  int base;       // first of the 32 rounds
+  uint32_t key;   // head and round of the current one, + 1
 };
 
-__device__ __forceinline__ Items first_item(const PromptParams& p, int worker) {
-  return Items{0, worker, p.plan[0] * p.h_q, p.plan[1]};
+__device__ __forceinline__ int item_of_round(int round, int worker, int workers) {
+  return round * workers + ((round & 1) ? workers - 1 - worker : worker);
 }
 
-__device__ __forceinline__ void next_item(Items& it, int worker, int workers) {
-  ++it.round;
-  it.at = it.round * workers + ((it.round & 1) ? workers - 1 - worker : worker);
+// By a whole warp: lane i looks at round base + i.
+__device__ __forceinline__ void next_item(Items& it, int worker, int workers, int heads) {
+  const int lane = threadIdx.x & 31;
+  while (true) {
+    const int at = item_of_round(it.base + lane, worker, workers);
+    const uint32_t key = (static_cast<uint32_t>(at % heads) << 5 | static_cast<uint32_t>(lane)) + 1u;
+    const uint32_t mine = at < it.total && key > it.key ? key : ~0u;
+    if (__any_sync(0xffffffffu, mine != ~0u)) {
+      it.key = __shfl_sync(0xffffffffu, __reduce_min_sync(0xffffffffu, mine), 0);
+      it.at = item_of_round(it.base + static_cast<int>((it.key - 1u) & 31u), worker, workers);
+      return;
+    }
+    it.base += 32;
+    it.key = 0;
+    if (it.base * workers >= it.total) {
+      it.at = it.total;
+      return;
+    }
+  }
 }
 
 __device__ __forceinline__ Tile load_tile(const PromptParams& p, const Items& it) {
@@ -197,7 +217,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* sRow = reinterpret_cast<float*>(smem + L::kOffRow);
 
   const int tid = threadIdx.x;
-  const int warp = tid >> 5, lane = tid & 31;
+  // The warp's number by a shuffle: the compiler then knows that a warp takes one
+  // role, keeps that role's code convergent and its MMA operands in uniform
+  // registers (16384-token prompt: 771 us without, 704 with).
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   if (tid == 0) {
     *abort_flag = 0;
@@ -241,7 +264,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_wait();
   }
   const uint32_t tmem = *tmem_slot;
-  Items it = first_item(p, worker);
+  const int causal = p.plan[1];
+  Items it{0, p.plan[0] * p.h_q, 0, 0};
+  next_item(it, worker, workers, p.h_q);
 
 
   if (warp > kWarpMma) {
@@ -265,10 +290,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       else
         tma_load_4d(dst, map, &bars[bar], 0, row, slice, hd, pol);
     };
-    for (; it.at < it.total && ok; next_item(it, worker, workers)) {
+    for (; it.at < it.total && ok; next_item(it, worker, workers, p.h_q)) {
       const Tile t = load_tile(p, it);
       const int head = it.at % p.h_q, kvh = head / p.group;
-      const int n0 = half_tiles(t, 0, L::kHalfRows, it.causal), n1 = half_tiles(t, 1, L::kHalfRows, it.causal);
+      const int n0 = half_tiles(t, 0, L::kHalfRows, causal), n1 = half_tiles(t, 1, L::kHalfRows, causal);
       const int n = max(n0, n1);
       if (warp == kWarpQ) {
         // a half's rows as soon as its last Q K^T of the item before is done
@@ -377,9 +402,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto enter = [&]() {
         n0 = n1 = j = 0;
         while (it.at < it.total && max(n0, n1) == 0) {
-          n0 = half_tiles(next, 0, L::kHalfRows, it.causal);
-          n1 = half_tiles(next, 1, L::kHalfRows, it.causal);
-          next_item(it, worker, workers);
+          n0 = __shfl_sync(0xffffffffu, half_tiles(next, 0, L::kHalfRows, causal), 0);
+          n1 = __shfl_sync(0xffffffffu, half_tiles(next, 1, L::kHalfRows, causal), 0);
+          next_item(it, worker, workers, p.h_q);
           next = load_tile(p, it);  // not needed before this item's end
         }
       };
@@ -480,8 +505,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // beside the wait for the last P V, and the registers do not go round.)
     int nh, limit;
     auto enter = [&](const Tile& t) {
-      nh = half_tiles(t, h, L::kHalfRows, it.causal);
-      limit = it.causal ? min(t.lk, t.vis + row) : t.lk;
+      nh = half_tiles(t, h, L::kHalfRows, causal);
+      limit = causal ? min(t.lk, t.vis + row) : t.lk;
     };
     enter(load_tile(p, it));
     while (it.at < it.total) {
@@ -562,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       const Tile t = load_tile(p, it);
       const int head = it.at % p.h_q;
-      next_item(it, worker, workers);
+      next_item(it, worker, workers, p.h_q);
       const Tile t_next = load_tile(p, it);
       if (nh > 0) {
         ok = __all_sync(0xffffffffu, mbar_wait(&bars[O_FULL + h], items & 1, abort_flag));
