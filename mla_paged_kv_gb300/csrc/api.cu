@@ -104,7 +104,7 @@ const DeviceInfo& device_info() {
   for (int kind = 0; kind < 3; ++kind)
     attr_ok = attr_ok && cudaFuncSetAttribute(sparse_kernel_ptr(kind), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                               sparse_smem_bytes()) == cudaSuccess;
-  for (int kind = 0; kind < 7; ++kind)
+  for (int kind = 0; kind < 9; ++kind)
     attr_ok = attr_ok && cudaFuncSetAttribute(dense_kernel_ptr(kind), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                               dense_smem_bytes()) == cudaSuccess;
   attr_ok = attr_ok && cudaFuncSetAttribute(combine_stream_kernel_ptr(), cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -457,6 +457,31 @@ int launch_shared(const SharedLaunch& c, cudaStream_t stream) {
   if (rc != MLA_OK) return rc;
   const int kind = c.dtype == MLA_DTYPE_FP16 ? 6 : 5;
   return launch_dense(qm, km, sm, rm, p, c.num_parts, kind, stream) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+// mla_decode_fwd for a shared-prefix call whose requests fill their row blocks
+// alone: 16-bit caches with few partitions a request take the kWarp instance.
+int decode_full_blocks(const void* q, const void* kv, const int32_t* block_table, int max_pages, int num_pages,
+                       const int32_t* lengths, int batch, int s_q, int h_q, int dtype, int causal, float scale,
+                       const int32_t* sched, const int32_t* split_offset, int num_parts, void* ws, size_t ws_bytes,
+                       void* out, int out_type, float* lse, int32_t* status, cudaStream_t stream) {
+  DecodeParams p;
+  CUtensorMap qm, km, sm, rm;
+  if (dtype != MLA_DTYPE_FP8_RECORD) {
+    const int rc = dense_prepare(q, kv, block_table, max_pages, num_pages, lengths, batch, s_q, h_q, 1, dtype, causal,
+                                 scale, sched, split_offset, num_parts, ws, ws_bytes, out, out_type, lse, status, &p,
+                                 &qm, &km, &sm, &rm);
+    if (rc != MLA_OK) return rc;
+    if (!p.q_vring) {
+      const int kind = dtype == MLA_DTYPE_FP16 ? 8 : 7;
+      if (launch_dense(qm, km, sm, rm, p, num_parts, kind, stream) != cudaSuccess) return MLA_ERR_CUDA;
+      return mla_combine(ws, ws_bytes, split_offset, batch, s_q * h_q, num_parts, out, out_type, lse, status,
+                         reinterpret_cast<mla_stream_t>(stream));
+    }
+  }
+  return mla_decode_fwd(q, kv, block_table, max_pages, num_pages, lengths, batch, s_q, h_q, 1, dtype, causal, scale,
+                        sched, split_offset, num_parts, ws, ws_bytes, out, out_type, lse, status,
+                        reinterpret_cast<mla_stream_t>(stream));
 }
 
 cudaError_t launch_plan(const int32_t* lengths, int n_units, int num_parts, int32_t* sched, int32_t* split_offset,

@@ -277,39 +277,95 @@ __device__ __forceinline__ int load_page_window(const DecodeParams& p, const Cur
   return pg;
 }
 
+// Tell the peer that its mailbox has been read.  The word has been loaded and
+// used, so there is nothing left to order; a release at cluster scope (the form
+// of the other instances) holds the softmax warp until all its stores have
+// reached the cluster.
+template <bool kRelaxed>
+__device__ __forceinline__ void free_mailbox(uint32_t remote_bar) {
+  if constexpr (kRelaxed)
+    mbar_arrive_remote_relaxed(remote_bar);
+  else
+    mbar_arrive_remote(remote_bar);
+}
+
+// Whether a polling issuer (a converged warp) has to give up: no progress for
+// the wait budget, or another role gave up.  The clock is read only once in 256
+// idle passes.
+__device__ __forceinline__ bool stuck(bool progressed, uint32_t& idle, uint64_t& t_last,
+                                      const volatile int* abort_flag) {
+  if (progressed) {
+    idle = 0;
+    return false;
+  }
+  if ((++idle & 255u) != 0) return false;
+  const uint64_t now = globaltimer_ns();
+  if (idle == 256u) t_last = now;
+  return __any_sync(0xffffffffu, *abort_flag != 0 || now - t_last > MLA_WAIT_LIMIT_NS);
+}
+
+// The two issuers run on one lane, or (kWarp) on a converged warp that elects
+// the lane that issues: see umma_f16_warp.
+template <bool kWarp>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  if constexpr (kWarp)
+    umma_f16_warp(d, a, b, idesc, acc);
+  else
+    umma_f16(d, a, b, idesc, acc);
+}
+template <bool kWarp>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  if constexpr (kWarp)
+    umma_f16_ts_warp(d, a, b, idesc, acc);
+  else
+    umma_f16_ts(d, a, b, idesc, acc);
+}
+template <bool kWarp>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if constexpr (kWarp)
+    umma_commit_warp(bar);
+  else
+    umma_commit(bar);
+}
+template <bool kWarp>
+__device__ __forceinline__ bool test(uint64_t* bar, uint32_t parity) {
+  const bool done = mbar_test_wait(bar, parity);
+  return kWarp ? __all_sync(0xffffffffu, done) : done;
+}
+
 // Q K^T over one 64-dim box kG (4 K-steps).  The A operand (Q) comes from TMEM
 // for kG < 6, else from shared memory; B is the box in the K slot or V ring.
-template <bool kHalf, int kG>
+template <bool kHalf, int kG, bool kWarp>
 __device__ __forceinline__ void qk_box(uint32_t d, uint32_t tmem, uint64_t q_desc0, uint64_t b_desc, bool first) {
   constexpr uint32_t idesc = idesc_16bit_f32(128, kT, false, kHalf);
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const uint64_t b = b_desc + static_cast<uint64_t>((k * 32) >> 4);
     if constexpr (kG < kQTmemBoxes)
-      umma_f16_ts(d, tmem + kTmemQ + 32 * kG + 8 * k, b, idesc, (first && k == 0) ? 0u : 1u);
+      mma_ts<kWarp>(d, tmem + kTmemQ + 32 * kG + 8 * k, b, idesc, (first && k == 0) ? 0u : 1u);
     else
-      umma_f16(d, q_desc0 + static_cast<uint64_t>(((kG - kQTmemBoxes) * kQBoxBytes + k * 32) >> 4), b, idesc,
+      mma<kWarp>(d, q_desc0 + static_cast<uint64_t>(((kG - kQTmemBoxes) * kQBoxBytes + k * 32) >> 4), b, idesc,
                (first && k == 0) ? 0u : 1u);
   }
 }
 
 // Q K^T over this rank's K-slot boxes (first part of the score tile).
-template <bool kHalf, int kRank>
+template <bool kHalf, int kRank, bool kWarp>
 __device__ __forceinline__ void issue_qk_k(uint32_t d, uint32_t tmem, uint64_t q_desc0, uint64_t kslot) {
-  qk_box<kHalf, k_box<kRank>(0)>(d, tmem, q_desc0, kslot + ((0 * kBoxBytes) >> 4), true);
-  qk_box<kHalf, k_box<kRank>(1)>(d, tmem, q_desc0, kslot + ((1 * kBoxBytes) >> 4), false);
-  qk_box<kHalf, k_box<kRank>(2)>(d, tmem, q_desc0, kslot + ((2 * kBoxBytes) >> 4), false);
-  qk_box<kHalf, k_box<kRank>(3)>(d, tmem, q_desc0, kslot + ((3 * kBoxBytes) >> 4), false);
-  qk_box<kHalf, k_box<kRank>(4)>(d, tmem, q_desc0, kslot + ((4 * kBoxBytes) >> 4), false);
+  qk_box<kHalf, k_box<kRank>(0), kWarp>(d, tmem, q_desc0, kslot + ((0 * kBoxBytes) >> 4), true);
+  qk_box<kHalf, k_box<kRank>(1), kWarp>(d, tmem, q_desc0, kslot + ((1 * kBoxBytes) >> 4), false);
+  qk_box<kHalf, k_box<kRank>(2), kWarp>(d, tmem, q_desc0, kslot + ((2 * kBoxBytes) >> 4), false);
+  qk_box<kHalf, k_box<kRank>(3), kWarp>(d, tmem, q_desc0, kslot + ((3 * kBoxBytes) >> 4), false);
+  qk_box<kHalf, k_box<kRank>(4), kWarp>(d, tmem, q_desc0, kslot + ((4 * kBoxBytes) >> 4), false);
 }
 
 // Q K^T over this rank's V-ring boxes (second part of the score tile).
-template <bool kHalf, int kRank>
+template <bool kHalf, int kRank, bool kWarp>
 __device__ __forceinline__ void issue_qk_v(uint32_t d, uint32_t tmem, uint64_t q_desc0, uint64_t vslot) {
-  qk_box<kHalf, 4 * kRank + 0>(d, tmem, q_desc0, vslot + ((0 * kBoxBytes) >> 4), false);
-  qk_box<kHalf, 4 * kRank + 1>(d, tmem, q_desc0, vslot + ((1 * kBoxBytes) >> 4), false);
-  qk_box<kHalf, 4 * kRank + 2>(d, tmem, q_desc0, vslot + ((2 * kBoxBytes) >> 4), false);
-  qk_box<kHalf, 4 * kRank + 3>(d, tmem, q_desc0, vslot + ((3 * kBoxBytes) >> 4), false);
+  qk_box<kHalf, 4 * kRank + 0, kWarp>(d, tmem, q_desc0, vslot + ((0 * kBoxBytes) >> 4), false);
+  qk_box<kHalf, 4 * kRank + 1, kWarp>(d, tmem, q_desc0, vslot + ((1 * kBoxBytes) >> 4), false);
+  qk_box<kHalf, 4 * kRank + 2, kWarp>(d, tmem, q_desc0, vslot + ((2 * kBoxBytes) >> 4), false);
+  qk_box<kHalf, 4 * kRank + 3, kWarp>(d, tmem, q_desc0, vslot + ((3 * kBoxBytes) >> 4), false);
 }
 
 // Two fp32 -> one packed pair of 16-bit floats (round to nearest even).
@@ -371,7 +427,11 @@ __device__ __forceinline__ float ref_alpha(float r_old, float r_new) {
 // all requests' queries over the pages they share, and each request's own
 // rows over the rest; one row block a unit, always split partials (128 rows a
 // slot), merged across both kinds of units by the shared-prefix combine.
-template <bool kHalf, bool kQV, bool kStall, bool kShared = false>
+// kWarp: roles dispatched by a warp-uniform index and MMAs issued by converged
+// warps, their operands in uniform registers; mailboxes freed by relaxed
+// arrivals.  The same operations on the same values.  (64 x 16 heads, 16384
+// shared keys: 46.4 us against 54.4.)
+template <bool kHalf, bool kQV, bool kStall, bool kShared = false, bool kWarp = kShared>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     dense_decode_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kv_map,
                         const __grid_constant__ CUtensorMap sc_map, const __grid_constant__ CUtensorMap rope_map,
@@ -394,7 +454,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   volatile int* sBad = reinterpret_cast<volatile int*>(smem + kOffMisc + 8);  // [2]: own tile's page outside the pool
 
   const int tid = threadIdx.x;
-  const int warp = tid >> 5, lane = tid & 31;
+  // (kWarp: by a shuffle, so that the compiler knows that a warp takes one role)
+  const int warp = kWarp ? __shfl_sync(0xffffffffu, tid >> 5, 0) : tid >> 5, lane = tid & 31;
   // Q rows staged per box: 128 (h_kv = 1) or the group's block_tokens tokens
   const uint32_t q_box_bytes =
       (p.h_kv == 1 ? kRowsPerBlock : p.group_heads * p.block_tokens) * 128u;
@@ -675,7 +736,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // P V of every tile in order, from the own or the received P; issued by a
     // thread of its own so that a ready P V enters the tensor pipe without
     // waiting for a Q K^T block to finish issuing.
-    if (lane == 0) {
+    if (kWarp || lane == 0) {
+      const uint32_t tmem_u = kWarp ? __shfl_sync(0xffffffffu, tmem, 0) : tmem;
       const uint32_t idesc_pv = idesc_16bit_f32(128, 256, true, kHalf);
       const uint64_t vv_desc0 = sdesc_sw128(smem_u32(sV), kBoxBytes, 1024);  // V boxes as MN-major B of P V
       const uint64_t pown_desc = sdesc_sw128(smem_u32(sPOwn), 16, 1024);
@@ -686,45 +748,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t pv_own = 0, pv_recv = 0;
       bool ok = true;
       uint64_t t_last = globaltimer_ns();
+      uint32_t idle = 0;
       while (cv.valid) {
         bool progressed = false;
         {
           const bool mine = (cv.t & 1u) == rank;
           const bool first = cursor_first(cv);
           const int vs = static_cast<int>(cv.t % kVSlots);
-          bool ready = mine ? mbar_test_wait(&bars[OWN_GO], pv_own & 1)
-                            : (mbar_test_wait(&bars[RECV_GO], pv_recv & 1) &&
-                               mbar_test_wait(&bars[RECV_FULL], pv_recv & 1));
-          ready = ready && mbar_test_wait(&bars[V_FULL + vs], (cv.t / kVSlots) & 1);
-          if (ready && first && cv.u >= 1) ready = mbar_test_wait(&bars[O_FREE], (cv.u - 1) & 1);
+          bool ready = mine ? test<kWarp>(&bars[OWN_GO], pv_own & 1)
+                            : (test<kWarp>(&bars[RECV_GO], pv_recv & 1) &&
+                               test<kWarp>(&bars[RECV_FULL], pv_recv & 1));
+          ready = ready && test<kWarp>(&bars[V_FULL + vs], (cv.t / kVSlots) & 1);
+          if (ready && first && cv.u >= 1) ready = test<kWarp>(&bars[O_FREE], (cv.u - 1) & 1);
           if (ready) {
             MLA_TRACE(3, cv.t);
             // armed for the next received P (it cannot be sent before this P V is done)
-            if (!mine) mbar_arrive_expect_tx(&bars[RECV_FULL], kPBytes);
+            if (!mine && (!kWarp || lane == 0)) mbar_arrive_expect_tx(&bars[RECV_FULL], kPBytes);
             tc_fence_after();
             const uint64_t a0 = mine ? pown_desc : precv_desc;
             const uint64_t b0 = vv_desc0 + static_cast<uint64_t>((vs * kVSlotBytes) >> 4);
 #pragma unroll
             for (int kk = 0; kk < kT / 16; ++kk)
-              umma_f16(tmem + kTmemO, a0 + static_cast<uint64_t>((kk * 32) >> 4),
+              mma<kWarp>(tmem_u + kTmemO, a0 + static_cast<uint64_t>((kk * 32) >> 4),
                        b0 + static_cast<uint64_t>((kk * 2048) >> 4), idesc_pv, (first && kk == 0) ? 0u : 1u);
-            umma_commit(&bars[V_EMPTY + vs]);
-            umma_commit(&bars[PV_DONE + (cv.t & 1)]);
+            commit<kWarp>(&bars[V_EMPTY + vs]);
+            commit<kWarp>(&bars[PV_DONE + (cv.t & 1)]);
             if (mine) {
-              umma_commit(&bars[OWN_FREE]);
+              commit<kWarp>(&bars[OWN_FREE]);
               ++pv_own;
             } else {
               // the peer may refill our receive buffer (and reuse its own copy of that P)
-              umma_commit_multicast(&bars[OWN_FREE], peer_mask);
+              if constexpr (kWarp)
+                umma_commit_multicast_warp(&bars[OWN_FREE], peer_mask);
+              else
+                umma_commit_multicast(&bars[OWN_FREE], peer_mask);
               ++pv_recv;
             }
-            if (cursor_last(cv)) umma_commit(&bars[O_FULL]);
+            if (cursor_last(cv)) commit<kWarp>(&bars[O_FULL]);
             MLA_TRACE(16, cv.t);
             cursor_next(p, P, cv);
             progressed = true;
           }
         }
-        if (progressed) {
+        if constexpr (kWarp) {
+          if (stuck(progressed, idle, t_last, abort_flag)) {
+            ok = false;
+            break;
+          }
+        } else if (progressed) {
           t_last = globaltimer_ns();
         } else if (*abort_flag || globaltimer_ns() - t_last > kWaitNs) {
           ok = false;
@@ -732,16 +803,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) {
-        set_abort(abort_flag, p.status, MLA_ERR_TIMEOUT);
+        if (!kWarp || lane == 0) set_abort(abort_flag, p.status, MLA_ERR_TIMEOUT);
         // a P the peer already sent may still be landing in our receive buffer
         mbar_wait<true>(&bars[RECV_FULL], pv_recv & 1, nullptr, kWaitNs);
       }
-      umma_commit(&bars[DRAIN]);
+      commit<kWarp>(&bars[DRAIN]);
     }
     __syncwarp();
   } else if (warp == kWarpMma) {
     // ------------------------------------------------------------ Q K^T issuer
-    if (lane == 0) {
+    if (kWarp || lane == 0) {
+      const uint32_t tmem_u = kWarp ? __shfl_sync(0xffffffffu, tmem, 0) : tmem;
       const uint64_t q_desc0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
       const uint64_t k_desc0 = sdesc_sw128(smem_u32(sK), 16, 1024);
       const uint64_t vk_desc0 = sdesc_sw128(smem_u32(sV), 16, 1024);        // V boxes as K-major B of Q K^T
@@ -758,6 +830,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t qb_seen = 0;     // Q boxes seen landed (nine per unit, in order)
       bool ok = true;
       uint64_t t_last = globaltimer_ns();
+      uint32_t idle = 0;
       // cq onto the next own tile, releasing the Q of every unit it leaves;
       // returns false if it has to stop at a unit end whose Q has not arrived
       auto advance_q = [&]() -> bool {
@@ -768,7 +841,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // leaving this tile; at the unit's end, Q of the unit is released
             if (cursor_last(cq)) {
               if (qb_seen < 9u * static_cast<uint32_t>(cq.u + 1)) return false;
-              umma_commit(&bars[Q_EMPTY]);
+              commit<kWarp>(&bars[Q_EMPTY]);
             }
             cursor_next(p, P, cq);
             q_phase = 0;
@@ -786,14 +859,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // completion of this box's slot barrier: three per unit, except one
         // (boxes 6-8) for a first unit staged in the V ring
         const uint32_t idx = !kQV ? 3u * uq + j / 3u : (uq == 0 ? 0u : 1u + 3u * (uq - 1u) + j / 3u);
-        if (!mbar_test_wait(&bars[QB_FULL + sl], idx & 1u)) return false;
+        if (!test<kWarp>(&bars[QB_FULL + sl], idx & 1u)) return false;
         if (j < 6u) {
           tc_fence_after();
 #pragma unroll
           for (uint32_t k = 0; k < 4; ++k)
-            tmem_cp_128x256b(tmem + kTmemQ + 32u * j + 8u * k,
-                             q_desc0 + static_cast<uint64_t>((sl * kQBoxBytes + k * 32u) >> 4));
-          umma_commit(&bars[QB_EMPTY + sl]);
+            if constexpr (kWarp)
+              tmem_cp_128x256b_warp(tmem_u + kTmemQ + 32u * j + 8u * k,
+                                    q_desc0 + static_cast<uint64_t>((sl * kQBoxBytes + k * 32u) >> 4));
+            else
+              tmem_cp_128x256b(tmem + kTmemQ + 32u * j + 8u * k,
+                               q_desc0 + static_cast<uint64_t>((sl * kQBoxBytes + k * 32u) >> 4));
+          commit<kWarp>(&bars[QB_EMPTY + sl]);
         }
         ++qb_seen;
         return true;
@@ -811,7 +888,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (uint32_t k = 0; k < 4; ++k)
               tmem_cp_128x256b(tmem + kTmemQ + 32u * jj + 8u * k,
                                vq_desc0 + static_cast<uint64_t>((jj * kQBoxBytes + k * 32u) >> 4));
-          umma_commit(&bars[VQ_EMPTY]);
+          commit<kWarp>(&bars[VQ_EMPTY]);
           qb_seen = 6;
         }
       }
@@ -822,17 +899,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (q_phase == 0) {
             const int ks = static_cast<int>(a_own % kKSlots);
             bool ready = qb_seen >= 9u * static_cast<uint32_t>(cq.u + 1);
-            ready = ready && mbar_test_wait(&bars[K_FULL + ks], (a_own / kKSlots) & 1);
-            if (ready && a_own >= 1) ready = mbar_test_wait(&bars[S_FREE], (a_own - 1) & 1);
+            ready = ready && test<kWarp>(&bars[K_FULL + ks], (a_own / kKSlots) & 1);
+            if (ready && a_own >= 1) ready = test<kWarp>(&bars[S_FREE], (a_own - 1) & 1);
             if (ready) {
               MLA_TRACE(1, cq.t);
               tc_fence_after();
               const uint64_t kslot = k_desc0 + static_cast<uint64_t>((ks * kKSlotBytes) >> 4);
               if (rank == 0)
-                issue_qk_k<kHalf, 0>(tmem + kTmemS, tmem, q_desc0, kslot);
+                issue_qk_k<kHalf, 0, kWarp>(tmem_u + kTmemS, tmem_u, q_desc0, kslot);
               else
-                issue_qk_k<kHalf, 1>(tmem + kTmemS, tmem, q_desc0, kslot);
-              umma_commit(&bars[K_EMPTY + ks]);
+                issue_qk_k<kHalf, 1, kWarp>(tmem_u + kTmemS, tmem_u, q_desc0, kslot);
+              commit<kWarp>(&bars[K_EMPTY + ks]);
               MLA_TRACE(17, cq.t);
               ++a_own;
               q_phase = 1;
@@ -840,15 +917,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           } else {
             const int vs = static_cast<int>(cq.t % kVSlots);
-            if (mbar_test_wait(&bars[V_FULL + vs], (cq.t / kVSlots) & 1)) {
+            if (test<kWarp>(&bars[V_FULL + vs], (cq.t / kVSlots) & 1)) {
               MLA_TRACE(8, cq.t);
               tc_fence_after();
               const uint64_t vslot = vk_desc0 + static_cast<uint64_t>((vs * kVSlotBytes) >> 4);
               if (rank == 0)
-                issue_qk_v<kHalf, 0>(tmem + kTmemS, tmem, q_desc0, vslot);
+                issue_qk_v<kHalf, 0, kWarp>(tmem_u + kTmemS, tmem_u, q_desc0, vslot);
               else
-                issue_qk_v<kHalf, 1>(tmem + kTmemS, tmem, q_desc0, vslot);
-              umma_commit(&bars[S_FULL]);
+                issue_qk_v<kHalf, 1, kWarp>(tmem_u + kTmemS, tmem_u, q_desc0, vslot);
+              commit<kWarp>(&bars[S_FULL]);
               MLA_TRACE(2, cq.t);
               q_phase = 2;
               advance_q();
@@ -856,7 +933,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (progressed) {
+        if constexpr (kWarp) {
+          if (stuck(progressed, idle, t_last, abort_flag)) {
+            ok = false;
+            break;
+          }
+        } else if (progressed) {
           t_last = globaltimer_ns();
         } else {
           // spin: a sleeping issuer reacts to a ready job far later than the job takes
@@ -866,9 +948,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (!ok) set_abort(abort_flag, p.status, MLA_ERR_TIMEOUT);
+      if (!ok && (!kWarp || lane == 0)) set_abort(abort_flag, p.status, MLA_ERR_TIMEOUT);
       // every MMA (of both issuers) has completed before TMEM is released
-      umma_commit(&bars[DRAIN]);
+      commit<kWarp>(&bars[DRAIN]);
       mbar_wait(&bars[DRAIN], 0, nullptr, kWaitNs);
     }
     __syncwarp();
@@ -1023,7 +1105,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // read (and use, so the load has completed) before the mailbox is released
         const float m_in = __shfl_sync(0xffffffffu, sRefIn[r], lane);
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(peer_r_free);
+        if (lane == 0) free_mailbox<kWarp>(peer_r_free);
         if (tid == 0) MLA_TRACE(10, t);
         const float r_t = (m_in > r_cur + kTau) ? m_in : r_cur;
         alpha = ref_alpha(r_cur, r_t);
@@ -1069,7 +1151,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (tid == 0) mbar_arrive_expect_tx(&bars[L_FULL], kVecBytes);
       const float l_peer = __shfl_sync(0xffffffffu, sLIn[r], lane);
       __syncwarp();
-      if (lane == 0) mbar_arrive_remote(peer_l_free);
+      if (lane == 0) free_mailbox<kWarp>(peer_l_free);
       const float l_sum = l_own + l_peer;  // the same fp32 sum on both ranks
       ++units;
       // ---- epilogue of this (unit, split)
@@ -1181,7 +1263,7 @@ int dense_smem_bytes() { return dn::kSmemBytes; }
 // kind 0: bf16, 1: fp16, 2: bf16 with the V-ring Q stage, 3: fp16 with it,
 // 4: the bf16 stall-test instance (its first own tile's K slot is never
 // loaded, so a wait runs out and the kernel reports MLA_ERR_TIMEOUT),
-// 5, 6: bf16, fp16 under a shared-prefix plan
+// 5, 6: bf16, fp16 under a shared-prefix plan, 7, 8: bf16, fp16, kWarp
 int dense_threads(int) { return dn::kThreads; }
 const void* dense_kernel_ptr(int kind) {
   switch (kind) {
@@ -1191,6 +1273,8 @@ const void* dense_kernel_ptr(int kind) {
     case 4: return reinterpret_cast<const void*>(&dn::dense_decode_kernel<false, false, true>);
     case 5: return reinterpret_cast<const void*>(&dn::dense_decode_kernel<false, false, false, true>);
     case 6: return reinterpret_cast<const void*>(&dn::dense_decode_kernel<true, false, false, true>);
+    case 7: return reinterpret_cast<const void*>(&dn::dense_decode_kernel<false, false, false, false, true>);
+    case 8: return reinterpret_cast<const void*>(&dn::dense_decode_kernel<true, false, false, false, true>);
     default: return reinterpret_cast<const void*>(&dn::dense_decode_kernel<false, false, false>);
   }
 }
@@ -1222,6 +1306,14 @@ cudaError_t launch_dense(const CUtensorMap& q_map, const CUtensorMap& kv_map, co
       break;
     case 6:
       dn::dense_decode_kernel<true, false, false, true>
+          <<<grid, dn::kThreads, dn::kSmemBytes, stream>>>(q_map, kv_map, sc_map, rope_map, p);
+      break;
+    case 7:
+      dn::dense_decode_kernel<false, false, false, false, true>
+          <<<grid, dn::kThreads, dn::kSmemBytes, stream>>>(q_map, kv_map, sc_map, rope_map, p);
+      break;
+    case 8:
+      dn::dense_decode_kernel<true, false, false, false, true>
           <<<grid, dn::kThreads, dn::kSmemBytes, stream>>>(q_map, kv_map, sc_map, rope_map, p);
       break;
     default:

@@ -439,6 +439,17 @@ __device__ __forceinline__ void umma_commit_warp(uint64_t* bar) {
       : "memory");
 }
 
+// umma_commit_multicast by the elected lane of a converged warp.
+__device__ __forceinline__ void umma_commit_multicast_warp(uint64_t* bar, uint16_t cta_mask) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+          smem_u32(bar)),
+      "h"(cta_mask)
+      : "memory");
+}
+
 // The pair forms (cta_group::2, issued by the even CTA of a pair): M = 256, each
 // CTA's 128 rows of A and D in its own shared memory or TMEM, B's N split
 // between the two shared memories, all at the same offsets.
@@ -512,6 +523,15 @@ __device__ __forceinline__ void mbar_arrive_expect_tx_remote_relaxed(uint32_t ba
 // its next tcgen05.commit.
 __device__ __forceinline__ void tmem_cp_128x256b(uint32_t t_addr, uint64_t s_desc) {
   asm volatile("tcgen05.cp.cta_group::1.128x256b [%0], %1;" ::"r"(t_addr), "l"(s_desc) : "memory");
+}
+
+__device__ __forceinline__ void tmem_cp_128x256b_warp(uint32_t t_addr, uint64_t s_desc) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.cp.cta_group::1.128x256b [%0], %1;\n\t}" ::"r"(t_addr),
+      "l"(s_desc)
+      : "memory");
 }
 
 // Arrive (once) on a CTA-local mbarrier when all previously issued MMAs of

@@ -29,6 +29,10 @@ struct SharedLaunch {
   int32_t* status;
 };
 int launch_shared(const SharedLaunch& c, cudaStream_t stream);
+int decode_full_blocks(const void* q, const void* kv, const int32_t* block_table, int max_pages, int num_pages,
+                       const int32_t* lengths, int batch, int s_q, int h_q, int dtype, int causal, float scale,
+                       const int32_t* sched, const int32_t* split_offset, int num_parts, void* ws, size_t ws_bytes,
+                       void* out, int out_type, float* lse, int32_t* status, cudaStream_t stream);
 cudaError_t launch_plan(const int32_t* lengths, int n_units, int num_parts, int32_t* sched, int32_t* split_offset,
                         cudaStream_t stream);
 

@@ -382,11 +382,11 @@ int mla_shared_prefix_decode_fwd(const void* d_q, const void* d_kv, const int32_
   if (rc != MLA_OK) return rc;
   const char* plan = static_cast<const char*>(d_plan);
   if (!z.share)
-    return mla_decode_fwd(d_q, d_kv, d_block_table, max_pages, num_pages,
-                          reinterpret_cast<const int32_t*>(plan + z.lengths_off), batch, s_q, h_q, 1, dtype, causal,
-                          softmax_scale, reinterpret_cast<const int32_t*>(plan + z.sched_off),
-                          reinterpret_cast<const int32_t*>(plan + z.offset_off), num_parts, d_workspace,
-                          workspace_bytes, d_out, out_type, d_lse, d_status, stream);
+    return decode_full_blocks(d_q, d_kv, d_block_table, max_pages, num_pages,
+                              reinterpret_cast<const int32_t*>(plan + z.lengths_off), batch, s_q, h_q, dtype, causal,
+                              softmax_scale, reinterpret_cast<const int32_t*>(plan + z.sched_off),
+                              reinterpret_cast<const int32_t*>(plan + z.offset_off), num_parts, d_workspace,
+                              workspace_bytes, d_out, out_type, d_lse, d_status, to_stream(stream));
   SharedLaunch c{};
   c.q = d_q;
   c.kv = d_kv;
