@@ -27,15 +27,28 @@
 //   * Keys past the sequence's end in its last tile belong to another sequence
 //     (or to nothing): their scores are masked and their V rows are zeroed in
 //     shared memory, since 0 x NaN would not be 0.
+//   * A softmax warp has 32 rows and 64 of the 128 keys, so that the chain from
+//     scores to weights is half as long; the two warps of a row exchange their
+//     maxima through one word each.
 // A worker is a pair of CTAs for long prompts (kPair): cta_group::2 MMAs over
 // 256 rows a half, 128 in each CTA, with K and V split between the two shared
 // memories (K by keys, V by dims).  One CTA alone has room for 1.6 key tiles
-// beside its 96 KB of Q, too few to cover the latency of the loads (2.15 us a
-// tile against 1.61 with the loads taken out); half a tile each gives the pair
-// three.  A prompt of 256 queries or fewer would leave half a pair idle: those
-// run on single CTAs with two 128-row halves.
-// The bound is the tensor pipe: 128 x 128 x (192 + 128) multiply-adds a half and
-// key tile are 1280 cycles at 4096 a cycle.
+// beside its 96 KB of Q, too few to cover the latency of the loads; half a tile
+// each gives the pair three.  Shorter prompts would leave half a pair idle: those
+// run on single CTAs with two 128-row halves (see prompt_pairs).
+//
+// Bound: the tensor pipe.  128 x 128 x (192 + 128) multiply-adds a half and key
+// tile are 1280 cycles at 4096 a cycle, 2560 a step of both halves, 1.24 us at
+// 2.06 GHz.  Measured (bf16, 192 dims): 1.52 us a step where all pairs have one
+// item (1.98 PFLOP/s), 688 us for a causal prompt of 16384 tokens x 16 heads (2.0
+// PFLOP/s; 780 us back to back, under the power limit), 102 us for 8192 x 8,
+// 168 us for 32 prompts of 1024 x 16 (their 670 MB are 100 us of HBM).  An item's
+// change costs about 1.3 us a worker.
+// Steps that made it (16384 x 16): one thread issuing MMAs from divergent code
+// 1137 us, a converged warp 953 (an MMA's operand moves cost a lone thread 110
+// cycles), pairs 912, weights announced by relaxed cluster arrivals 779 (a release
+// waits for earlier stores to reach the cluster: 1700 cycles), stores exchanged
+// among lanes 770, the roles' dispatch made warp-uniform 688.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -222,6 +235,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   // registers (16384-token prompt: 771 us without, 704 with).
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
+  if ((smem_u32(smem) & 1023u) != 0u) {  // not what was asked for (all CTAs alike)
+    if (tid == 0) report(p.status, MLA_ERR_UNSUPPORTED);
+    return;
+  }
   if (tid == 0) {
     *abort_flag = 0;
     constexpr uint32_t kCtas = kPair ? 2 : 1;  // loaders that fill a stage, each its part
@@ -267,7 +284,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int causal = p.plan[1];
   Items it{0, p.plan[0] * p.h_q, 0, 0};
   next_item(it, worker, workers, p.h_q);
-
 
   if (warp > kWarpMma) {
     // ------------------------------------------------------------ loads: K, V or Q
@@ -778,7 +794,10 @@ static_assert(kBins == kPlanThreads, "one bin a thread");
 }  // namespace pr
 
 // Pairs of CTAs on 512-query tiles where prompts are longer than one CTA's 256
-// queries on average, else CTAs on 256.
+// queries on average, else CTAs on 256.  Causal batches x 16 heads, pairs against
+// single CTAs: 128 x 200 tokens 136 and 98 us, 128 x 256 137 and 110, 128 x 300 173
+// and 194, 128 x 384 187 and 211, 64 x 512 123 and 139; 64 x 700, whose second tile
+// is a third full, 250 and 238.
 bool prompt_pairs(int batch, int total_q) { return total_q / batch > 256; }
 namespace {
 int prompt_tile_q(int batch, int total_q) { return prompt_pairs(batch, total_q) ? 512 : 256; }
