@@ -124,7 +124,8 @@ int mla_cache_compact(int32_t* d_refcount, int num_pages, int32_t* d_block_table
 /* Copy whole pages inside a pool, for every layer: page d_pairs[i].x to page
  * d_pairs[i].y, i < n (or i < min(n, *d_count) with d_count).
  *   d_pool        layers x [num_pages, page_bytes], layer_stride bytes apart
- *                 (>= num_pages * page_bytes; both multiples of 16)
+ *                 (>= num_pages * page_bytes; both multiples of 16); pages of
+ *                 at most 16 MB, at most 4096 layers and 2^24 pairs
  * (-1, -1) is skipped, and so is a pair of equal pages.  A pair with a page
  * outside the pool, with a target that an earlier pair also has, or with a
  * target that another pair reads is skipped and reported

@@ -140,7 +140,7 @@ int mla_cache_append(const void* d_c, long long c_stride, const void* d_r, long 
       !aligned(d_cos_sin, 16) || !aligned(d_cu_seqlens, 4) || !aligned(d_cache_seqlens, 4) ||
       !aligned(d_block_table, 4) || !aligned(d_refcount, 4) || !aligned(d_status, 4))
     return MLA_ERR_INVALID_ARG;
-  if (max_pages > kMaxRowPages || num_pages > (1 << 30)) return MLA_ERR_UNSUPPORTED;
+  if (max_pages > kMaxRowPages || num_pages > (1 << 30) || total_tokens > (1 << 30)) return MLA_ERR_UNSUPPORTED;
   int sms = 0;
   const int rc = device_ready(&sms);
   if (rc != MLA_OK) return rc;
@@ -229,7 +229,8 @@ int mla_cache_copy_pages(void* d_pool, int layers, long long layer_stride, int n
     return MLA_ERR_INVALID_ARG;
   if (!aligned(d_pool, 16) || !aligned(d_pairs, 8) || !aligned(d_count, 4) || !aligned(d_status, 4))
     return MLA_ERR_INVALID_ARG;
-  if (page_bytes > (1LL << 30) || num_pages > (1 << 30) || layers > (1 << 16)) return MLA_ERR_UNSUPPORTED;
+  if (page_bytes > (1LL << 24) || num_pages > (1 << 30) || layers > (1 << 12) || n > (1 << 24))
+    return MLA_ERR_UNSUPPORTED;
   if (layers > 1 && layer_stride < page_bytes * num_pages) return MLA_ERR_INVALID_ARG;
   int sms = 0;
   const int rc = device_ready(&sms);
@@ -346,8 +347,7 @@ int mla_shared_prefix_get_plan(const int32_t* d_block_table, int max_pages, cons
   const cudaStream_t st = to_stream(stream);
   rc = z.share ? launched(launch_shared_units(d_block_table, max_pages, d_cache_seqlens, batch, s_q, h_q,
                                               causal ? 1 : 0, reinterpret_cast<int32_t*>(plan), lengths, st))
-               : launched(cudaMemcpyAsync(lengths, d_cache_seqlens, static_cast<size_t>(batch) * 4,
-                                          cudaMemcpyDeviceToDevice, st));
+               : launched(launch_shared_lengths(d_cache_seqlens, batch, lengths, st));
   if (rc != MLA_OK) return rc;
   return launched(launch_plan(lengths, z.units, num_parts, reinterpret_cast<int32_t*>(plan + z.sched_off),
                               reinterpret_cast<int32_t*>(plan + z.offset_off), st));

@@ -69,6 +69,12 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
+// Where nothing is attended together the plan keeps the lengths as they are.
+__global__ void __launch_bounds__(256) shared_lengths_kernel(const int32_t* seqlens, int batch, int32_t* lengths) {
+  const int b = blockIdx.x * 256 + threadIdx.x;
+  if (b < batch) lengths[b] = seqlens[b];
+}
+
 __device__ __forceinline__ void store4(void* out, int out_type, size_t elem, float4 v) {
   if (out_type == MLA_DTYPE_FP32) {
     *reinterpret_cast<float4*>(static_cast<float*>(out) + elem) = v;
@@ -245,6 +251,11 @@ cudaError_t launch_shared_units(const int32_t* block_table, int max_pages, const
                                 int s_q, int h_q, int causal, int32_t* units, int32_t* lengths,
                                 cudaStream_t st) {
   shared_units_kernel<<<1, 1024, 0, st>>>(block_table, max_pages, seqlens, batch, s_q, h_q, causal, units, lengths);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_shared_lengths(const int32_t* seqlens, int batch, int32_t* lengths, cudaStream_t st) {
+  shared_lengths_kernel<<<ceil_div_i(batch, 256), 256, 0, st>>>(seqlens, batch, lengths);
   return cudaGetLastError();
 }
 

@@ -208,3 +208,30 @@ def test_slots_past_32_bits_of_bytes():
     cache[pages - 1, 63] = 0
     cache[pages - 2, 0] = 0
     assert not cache.any()
+
+
+@pytest.mark.parametrize("cu", [[0, 40, 10, 50], [5, 5, 5, 5], [60, 0, 20, 30], [-9, 3, 2, 1000], [7, -3, 90, 20]])
+def test_offsets_out_of_order_stay_inside_the_cache(cu):
+    """Offsets that decrease or leave the batch: some tokens land somewhere or nowhere, all of it inside the pool."""
+    pages = 8
+    table = torch.arange(6, dtype=torch.int32, device="cuda").reshape(3, 2)
+    whole = torch.zeros(pages + 4, 64, 576, dtype=torch.bfloat16, device="cuda")
+    a = torch.ones(50, 576, device="cuda").to(torch.bfloat16)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    mla.cache_append(a[:, :512], a[:, 512:], whole[2:2 + pages], table,
+                     torch.tensor([100, 64, 20], dtype=torch.int32, device="cuda"),
+                     cu_seqlens=torch.tensor(cu, dtype=torch.int32, device="cuda"), status=status)
+    assert int(status) in (0, 5)
+    assert not whole[:2].any() and not whole[2 + 6:].any()
+
+
+def test_one_row_for_every_token():
+    """A broadcast input (row stride 0) and a single token."""
+    a = torch.randn(1, 576, device="cuda").to(torch.bfloat16)
+    cache = torch.zeros(2, 64, 576, dtype=torch.bfloat16, device="cuda")
+    table = torch.tensor([[1]], dtype=torch.int32, device="cuda")
+    rows = a.expand(9, 576)
+    mla.cache_append(rows[:, :512], rows[:, 512:], cache, table, torch.tensor([20], dtype=torch.int32, device="cuda"))
+    assert torch.equal(cache[1, 11:20], rows) and not cache[0].any() and not cache[1, :11].any()
+    mla.cache_append(a[:, :512], a[:, 512:], cache, table, torch.tensor([1], dtype=torch.int32, device="cuda"))
+    assert torch.equal(cache[1, 0], a[0])

@@ -53,7 +53,8 @@ APPEND = dict(c=P, cs=576, r=P, rs=576, dt=0, total=4, cu=N, lens=P, batch=2, ta
     (dict(status=N), INVALID), (dict(dt=1), INVALID), (dict(cdt=2), INVALID), (dict(cs=577), INVALID),
     (dict(rs=-8), INVALID), (dict(total=-1), INVALID), (dict(total=5), INVALID), (dict(batch=0), INVALID),
     (dict(eps=float("nan")), INVALID), (dict(eps=-1.0), INVALID), (dict(maxpos=0), INVALID), (dict(c=ODD), INVALID),
-    (dict(cache=ctypes.c_void_p(4104)), INVALID), (dict(width=(1 << 18) + 1), UNSUPPORTED)])
+    (dict(cache=ctypes.c_void_p(4104)), INVALID), (dict(width=(1 << 18) + 1), UNSUPPORTED),
+    (dict(total=(1 << 30) + 2), UNSUPPORTED)])
 def test_append_refusals(change, want):
     assert mla.load_library().mla_cache_append(*{**APPEND, **change}.values()) == want
 
@@ -81,7 +82,8 @@ LIST = [(dict(n=-1), INVALID), (dict(n=4097), UNSUPPORTED)]
                              (dict(pool=N), INVALID), (dict(status=N), INVALID), (dict(pairs=N), INVALID),
                              (dict(n=-1), INVALID), (dict(page=1000), INVALID), (dict(stride=8 * 1024 - 16), INVALID),
                              (dict(stride=8 * 1024 + 8), INVALID), (dict(layers=0), INVALID),
-                             (dict(pool=ODD), INVALID), (dict(page=1 << 31), UNSUPPORTED)]])
+                             (dict(pool=ODD), INVALID),
+                             (dict(page=1 << 25, layers=1), UNSUPPORTED), (dict(n=1 << 25), UNSUPPORTED)]])
 def test_page_refusals(name, base, change, want):
     assert getattr(mla.load_library(), "mla_cache_" + name)(*{**base, **change}.values()) == want
 

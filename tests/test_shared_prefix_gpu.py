@@ -198,16 +198,17 @@ def test_refusals():
         mla.shared_prefix_decode(q, kv, table, lens, pl=pl)
 
 
-def test_graph_replays_with_new_lengths():
+@pytest.mark.parametrize("h_q,fp8", [(16, False), (128, False), (16, True), (128, True)])
+def test_graph_replays_with_new_lengths(h_q, fp8):
     """Plan and decode captured together: the table and lengths may change between replays."""
-    c = Case(10, [64, 100, 5, 300], 1, 16, seed=16)
+    c = Case(10, [64, 100, 5, 300], 1, h_q, seed=16, fp8=fp8)
     q, kv, table, lens = c.q.cuda(), c.kv.cuda(), torch.from_numpy(c.table).cuda(), i32(c.lens)
-    pl = mla.plan_shared_prefix(table, lens, 1, 16)
+    pl = mla.plan_shared_prefix(table, lens, 1, h_q)
     st = i32([0])
     out, lse = mla.shared_prefix_decode(q, kv, table, lens, pl=pl, status=st)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        mla.mla_shared_prefix_get_plan(table, lens, 1, 16, False, pl.num_parts, pl.plan)
+        mla.mla_shared_prefix_get_plan(table, lens, 1, h_q, False, pl.num_parts, pl.plan)
         mla.mla_shared_prefix_decode_fwd(q, kv, table, pl, out, lse, st)
     for lengths in (c.lens, [600, 640, 641, 704], [64, 130, 70, 65], [10, 0, 3, 2]):
         c.lens = lengths
@@ -224,3 +225,15 @@ def test_same_bits_every_time():
     for _ in range(3):
         again = c.run()
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def test_another_stream():
+    c = Case(12, [500, 100, 5], 1, 16, seed=18)
+    first = c.run()
+    q, kv, table, lens = c.q.cuda(), c.kv.cuda(), torch.from_numpy(c.table).cuda(), i32(c.lens)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        out, lse = mla.shared_prefix_decode(q, kv, table, lens)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
