@@ -177,14 +177,17 @@ int mla_prompt_attention_fwd(const void* d_q, long long q_token_stride, long lon
 /* ------------------------------------------------------------ shared prefix */
 
 /* Dense decode (mla_decode_fwd with one latent KV head: a bf16 or fp16 cache, or
- * FP8 records with a bf16 query) for a batch whose requests start with the same pages, as after mla_cache_fork: the
- * shared pages are attended once for all requests' queries, 128 rows at a
- * time, and merged with each request's own pages.
+ * FP8 records with a bf16 query) for a batch whose requests start with the same
+ * pages, as after mla_cache_fork: the shared pages are attended once for all
+ * requests' queries, 128 rows at a time, and merged with each request's own
+ * pages.
  *
  * The plan finds the shared pages itself: the longest run of block-table
- * entries that all requests have in common, in whole pages that every query of
- * every request sees; it may be none.  It is made once for a batch and read
- * by every layer, while the block table and lengths stay as they were.
+ * entries that the requests have in common, in whole pages that every query of
+ * each of them sees; it may be none.  Requests whose first query sees less
+ * than a page (empty slots of a padded batch) are attended by themselves and
+ * leave the others' prefix as it is.  The plan is made once for a batch and
+ * read by every layer, while the block table and lengths stay as they were.
  * The prefix is attended together only where that takes fewer 128-row blocks
  * than attending it request by request:
  * ceil(batch * s_q * h_q / 128) < batch * ceil(s_q * h_q / 128).  With s_q * h_q a
@@ -208,9 +211,27 @@ int mla_shared_prefix_get_plan(const int32_t* d_block_table, int max_pages, cons
  * finite values (they meet a weight of 0). */
 int mla_shared_prefix_decode_fwd(const void* d_q, const void* d_kv, const int32_t* d_block_table, int max_pages,
                                  int num_pages, int batch, int s_q, int h_q, int dtype, int causal,
-                                 float softmax_scale, const void* d_plan, size_t plan_bytes, int num_parts, void* d_workspace,
-                                 size_t workspace_bytes, void* d_out, int out_type, float* d_lse, int32_t* d_status,
-                                 mla_stream_t stream);
+                                 float softmax_scale, const void* d_plan, size_t plan_bytes, int num_parts,
+                                 void* d_workspace, size_t workspace_bytes, void* d_out, int out_type, float* d_lse,
+                                 int32_t* d_status, mla_stream_t stream);
+
+/* ---------------------------------------------------------------- one pointer */
+
+/* The calls above with their arguments, in order, as 8-byte words: pointers,
+ * sizes and integers as int64, floats as double.  For bindings whose
+ * foreign-call cost grows with the number of arguments (0.16 us each from
+ * Python on an Arm host, more than the call itself takes). */
+typedef enum {
+  MLA_CALL_APPEND = 0,
+  MLA_CALL_GROW = 1,
+  MLA_CALL_FORK = 2,
+  MLA_CALL_FREE = 3,
+  MLA_CALL_COMPACT = 4,
+  MLA_CALL_COPY_PAGES = 5,
+  MLA_CALL_PROMPT = 6,       /* mla_prompt_attention_fwd */
+  MLA_CALL_SHARED_PREFIX = 7 /* mla_shared_prefix_decode_fwd */
+} mla_call_t;
+int mla_serving_call(int op, const void* args, size_t bytes); /* bytes = 8 x the call's arguments */
 
 #ifdef __cplusplus
 }

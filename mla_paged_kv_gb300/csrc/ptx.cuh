@@ -120,41 +120,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
   }
 }
 
-// The same wait with the thread suspended in hardware until the phase
-// completes (or 20 us have passed) instead of polling: for kernels where
-// polling warps would take issue slots from computing ones.
-template <bool kCluster = false>
-__device__ __forceinline__ bool mbar_wait_suspended(uint64_t* bar, uint32_t parity, const volatile int* abort,
-                                                    uint64_t limit_ns = MLA_WAIT_LIMIT_NS) {
-  auto probe = [&]() {
-    uint32_t ok;
-    if constexpr (kCluster)
-      asm volatile(
-          "{\n\t.reg .pred P;\n\t"
-          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 P, [%1], %2, %3;\n\t"
-          "selp.u32 %0, 1, 0, P;\n\t}"
-          : "=r"(ok)
-          : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
-          : "memory");
-    else
-      asm volatile(
-          "{\n\t.reg .pred P;\n\t"
-          "mbarrier.try_wait.parity.shared::cta.b64 P, [%1], %2, %3;\n\t"
-          "selp.u32 %0, 1, 0, P;\n\t}"
-          : "=r"(ok)
-          : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
-          : "memory");
-    return ok != 0;
-  };
-  if (probe()) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (true) {
-    if (probe()) return true;
-    if (abort != nullptr && *abort) return false;
-    if (globaltimer_ns() - t0 > limit_ns) return false;
-  }
-}
-
 // ---------------------------------------------------------------- fences
 
 __device__ __forceinline__ void fence_proxy_async_smem() {

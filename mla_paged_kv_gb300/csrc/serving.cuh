@@ -40,9 +40,9 @@ cudaError_t launch_shared_units(const int32_t* block_table, int max_pages, const
                                 int s_q, int h_q, int causal, int32_t* units, int32_t* lengths,
                                 cudaStream_t st);
 cudaError_t launch_shared_lengths(const int32_t* seqlens, int batch, int32_t* lengths, cudaStream_t st);
-cudaError_t launch_shared_combine(const float* o_accum, const float* lse_accum, const int32_t* split_offset,
-                                  int batch, int rows, void* out, int out_type, float* lse, int sms,
-                                  cudaStream_t st);
+cudaError_t launch_shared_combine(const float* o_accum, const float* lse_accum, const int32_t* units,
+                                  const int32_t* split_offset, int batch, int rows, void* out, int out_type,
+                                  float* lse, int sms, cudaStream_t st);
 constexpr int kMaxSharedParts = 1024;  // partitions of a shared-prefix plan
 
 struct AppendParams {

@@ -2,6 +2,7 @@
 // maps and launches.  No device memory is allocated here.
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 #include <mutex>
 
 #include "mla_serving.h"
@@ -410,8 +411,54 @@ int mla_shared_prefix_decode_fwd(const void* d_q, const void* d_kv, const int32_
   const cudaStream_t st = to_stream(stream);
   rc = launch_shared(c, st);
   if (rc != MLA_OK) return rc;
-  return launched(launch_shared_combine(c.o_accum, c.lse_accum, c.split_offset, batch, s_q * h_q, d_out, out_type,
-                                        d_lse, sms, st));
+  return launched(launch_shared_combine(c.o_accum, c.lse_accum, c.units, c.split_offset, batch, s_q * h_q, d_out,
+                                        out_type, d_lse, sms, st));
+}
+
+int mla_serving_call(int op, const void* args, size_t bytes) {
+  constexpr size_t kWords[] = {22, 11, 12, 10, 12, 10, 23, 21};  // by mla_call_t
+  if (!args || op < 0 || op > MLA_CALL_SHARED_PREFIX || bytes != 8 * kWords[op]) return MLA_ERR_INVALID_ARG;
+  const char* a = static_cast<const char*>(args);
+  auto word = [&](int i) {
+    int64_t v;
+    std::memcpy(&v, a + 8 * i, 8);
+    return v;
+  };
+  auto I = [&](int i) { return static_cast<int>(word(i)); };
+  auto F = [&](int i) {
+    double v;
+    std::memcpy(&v, a + 8 * i, 8);
+    return static_cast<float>(v);
+  };
+  auto P = [&](int i) { return reinterpret_cast<void*>(word(i)); };
+  auto N = [&](int i) { return static_cast<int32_t*>(P(i)); };
+  auto R = [&](int i) { return static_cast<float*>(P(i)); };
+  auto S = [&](int i) { return static_cast<mla_stream_t>(P(i)); };
+  switch (op) {
+    case MLA_CALL_APPEND:
+      return mla_cache_append(P(0), word(1), P(2), word(3), I(4), I(5), N(6), N(7), I(8), N(9), I(10), P(11), I(12),
+                              I(13), P(14), F(15), R(16), I(17), I(18), N(19), N(20), S(21));
+    case MLA_CALL_GROW:
+      return mla_cache_grow(N(0), I(1), N(2), I(3), I(4), N(5), N(6), N(7), I(8), N(9), S(10));
+    case MLA_CALL_FORK:
+      return mla_cache_fork(N(0), I(1), N(2), I(3), I(4), N(5), N(6), N(7), I(8), N(9), N(10), S(11));
+    case MLA_CALL_FREE:
+      return mla_cache_free(N(0), I(1), N(2), I(3), I(4), N(5), N(6), I(7), N(8), S(9));
+    case MLA_CALL_COMPACT:
+      return mla_cache_compact(N(0), I(1), N(2), I(3), I(4), N(5), N(6), N(7), P(8), static_cast<size_t>(word(9)),
+                               N(10), S(11));
+    case MLA_CALL_COPY_PAGES:
+      return mla_cache_copy_pages(P(0), I(1), word(2), I(3), word(4), N(5), N(6), I(7), N(8), S(9));
+    case MLA_CALL_PROMPT:
+      return mla_prompt_attention_fwd(P(0), word(1), word(2), P(3), word(4), word(5), P(6), word(7), word(8), I(9),
+                                      I(10), I(11), I(12), I(13), I(14), I(15), F(16), P(17),
+                                      static_cast<size_t>(word(18)), P(19), R(20), N(21), S(22));
+    case MLA_CALL_SHARED_PREFIX:
+      return mla_shared_prefix_decode_fwd(P(0), P(1), N(2), I(3), I(4), I(5), I(6), I(7), I(8), I(9), F(10), P(11),
+                                          static_cast<size_t>(word(12)), I(13), P(14), static_cast<size_t>(word(15)),
+                                          P(16), I(17), R(18), N(19), S(20));
+    default: return MLA_ERR_INVALID_ARG;
+  }
 }
 
 }  // extern "C"

@@ -20,27 +20,45 @@ namespace {
 
 constexpr int kRB = kRowsPerBlock;
 
-// The pages every request starts with (the longest common run of block-table
-// entries, whole pages that every query sees), and the units over them and
-// over the rest.  One block; made once for a batch.
+// Ints of a unit's entry behind SharedUnit's: an own unit's, 1 where it holds
+// all of the request's keys.
+constexpr int kAlone = 5;
+
+// Keys that the first of a request's queries sees.  Less than a page shares
+// nothing: such a request (an empty slot of a padded batch, say) stands apart
+// and the others share without it.
+__device__ __forceinline__ int keys_seen(const int32_t* seqlens, int b, int s_q, int causal) {
+  return max(seqlens[b], 0) - (causal ? s_q - 1 : 0);
+}
+
+// The pages every request that sees one starts with (the longest common run of
+// block-table entries, whole pages that every query sees), and the units over
+// them and over the rest.  One block; made once for a batch.
 __global__ void __launch_bounds__(1024)
     shared_units_kernel(const int32_t* table, int max_pages, const int32_t* seqlens, int batch, int s_q, int h_q,
                         int causal, int32_t* units, int32_t* lengths) {
-  __shared__ int common;
-  if (threadIdx.x == 0) common = max_pages;
+  __shared__ int common, first;  // pages in common; the first request that takes part
+  if (threadIdx.x == 0) common = max_pages, first = batch;
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int b = threadIdx.x; b < batch; b += 1024) {
-    const int seen = max(seqlens[b], 0) - (causal ? s_q - 1 : 0);  // keys the first query sees
-    atomicMin(&common, max(seen, 0) / kTile);
+    const int seen = keys_seen(seqlens, b, s_q, causal);
+    if (seen >= kTile) {
+      atomicMin(&common, seen / kTile);
+      atomicMin(&first, b);
+    }
   }
   __syncthreads();
-  for (int b = 1 + warp; b < batch; b += 32) {
+  const bool none = first == batch;
+  const int ref = none ? 0 : first;
+  const int32_t* head = table + static_cast<long long>(ref) * max_pages;
+  for (int b = ref + 1 + warp; b < batch; b += 32) {
+    if (keys_seen(seqlens, b, s_q, causal) < kTile) continue;
     const int32_t* row = table + static_cast<long long>(b) * max_pages;
     const int most = *reinterpret_cast<volatile int*>(&common);
     for (int c0 = 0; c0 < most; c0 += 32) {
       const int c = c0 + lane;
-      const unsigned diff = __ballot_sync(0xffffffffu, c < most && row[c] != table[c]);
+      const unsigned diff = __ballot_sync(0xffffffffu, c < most && row[c] != head[c]);
       if (diff) {
         if (lane == 0) atomicMin(&common, c0 + __ffs(diff) - 1);
         break;
@@ -48,7 +66,7 @@ __global__ void __launch_bounds__(1024)
     }
   }
   __syncthreads();
-  const int shared = common;
+  const int shared = none ? 0 : common;
   const int rows = s_q * h_q;
   const long long total = static_cast<long long>(batch) * rows;
   const int front = static_cast<int>((total + kRB - 1) / kRB), per = ceil_div_i(rows, kRB);
@@ -56,15 +74,18 @@ __global__ void __launch_bounds__(1024)
     int4* e = reinterpret_cast<int4*>(units + u * kUnitInts);
     if (u < front) {
       const int row0 = u * kRB;
-      e[0] = make_int4(row0, static_cast<int>(min(total - row0, static_cast<long long>(kRB))), -1, 0);
+      e[0] = make_int4(row0, static_cast<int>(min(total - row0, static_cast<long long>(kRB))), -1,
+                       ref * max_pages);
       e[1] = make_int4(max_pages, 0, 0, 0);
       lengths[u] = shared * kTile;
     } else {
       const int b = (u - front) / per, blk = (u - front) - b * per;
       const int rel = blk * kRB;
-      e[0] = make_int4(b * rows + rel, min(rows - rel, kRB), causal ? rel : -1, b * max_pages + shared);
-      e[1] = make_int4(max_pages - shared, 0, 0, 0);
-      lengths[u] = max(seqlens[b], 0) - shared * kTile;
+      const bool alone = keys_seen(seqlens, b, s_q, causal) < kTile;
+      const int skip = alone ? 0 : shared;
+      e[0] = make_int4(b * rows + rel, min(rows - rel, kRB), causal ? rel : -1, b * max_pages + skip);
+      e[1] = make_int4(max_pages - skip, alone ? 1 : 0, 0, 0);
+      lengths[u] = max(seqlens[b], 0) - skip * kTile;
     }
   }
 }
@@ -93,7 +114,8 @@ __device__ __forceinline__ void store4(void* out, int out_type, size_t elem, flo
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + elem) = w;
 }
 
-// What a row merges: the splits of its prefix unit, then those of its own unit.
+// What a row merges: the splits of its prefix unit (if the request takes part in
+// it), then those of its own unit.
 struct RowSplits {
   int p0, np, o0, n;  // prefix: slots p0 .. p0 + np - 1; own: o0 .. o0 + n - np - 1
   int pr, orow;       // the row within either unit
@@ -104,14 +126,15 @@ struct RowSplits {
   }
 };
 
-__device__ __forceinline__ RowSplits row_splits(const int32_t* split_offset, int batch, int rows, long long g) {
+__device__ __forceinline__ RowSplits row_splits(const int32_t* units, const int32_t* split_offset, int batch,
+                                                int rows, long long g) {
   const int b = static_cast<int>(g / rows), r = static_cast<int>(g - static_cast<long long>(b) * rows);
   const int front = static_cast<int>((static_cast<long long>(batch) * rows + kRB - 1) / kRB);
   const int own = front + b * ceil_div_i(rows, kRB) + r / kRB;
   const int pre = static_cast<int>(g / kRB);
   RowSplits s;
   s.p0 = split_offset[pre];
-  s.np = split_offset[pre + 1] - s.p0;
+  s.np = units[own * kUnitInts + kAlone] ? 0 : split_offset[pre + 1] - s.p0;
   s.o0 = split_offset[own];
   s.n = s.np + split_offset[own + 1] - s.o0;
   s.pr = static_cast<int>(g % kRB);
@@ -134,12 +157,12 @@ __device__ __forceinline__ void add4(float4& acc, float w, const float4& v) {
 // kernel's CTAs and start as it ends.  Bound by the partials' bytes.
 __global__ void __launch_bounds__(128)
     shared_combine_rows_kernel(const float* __restrict__ o_accum, const float* __restrict__ lse_accum,
-                               const int32_t* __restrict__ split_offset, int batch, int rows, void* __restrict__ out,
-                               int out_type, float* __restrict__ lse) {
+                               const int32_t* __restrict__ units, const int32_t* __restrict__ split_offset, int batch,
+                               int rows, void* __restrict__ out, int out_type, float* __restrict__ lse) {
   constexpr int kBatch = 8;
   const long long g = blockIdx.x;
   const int lane = threadIdx.x & 31, col = 4 * threadIdx.x;
-  const RowSplits s = row_splits(split_offset, batch, rows, g);  // the plan's: read before the wait
+  const RowSplits s = row_splits(units, split_offset, batch, rows, g);  // the plan's: read before the wait
   pdl_wait_prior_grid();
   const float l0 = lane < s.n ? lse_accum[s.at(lane)] : -INFINITY;
   float m = l0;
@@ -181,15 +204,16 @@ __global__ void __launch_bounds__(128)
 constexpr int kGroups = 8;
 __global__ void __launch_bounds__(128 * kGroups)
     shared_combine_splits_kernel(const float* __restrict__ o_accum, const float* __restrict__ lse_accum,
-                                 const int32_t* __restrict__ split_offset, int batch, int rows,
-                                 void* __restrict__ out, int out_type, float* __restrict__ lse) {
+                                 const int32_t* __restrict__ units, const int32_t* __restrict__ split_offset,
+                                 int batch, int rows, void* __restrict__ out, int out_type,
+                                 float* __restrict__ lse) {
   constexpr int kBatch = 4;
   __shared__ float part_m[kGroups][4], part_z[kGroups][4];
   __shared__ float4 part[kGroups][128];
   const long long g = blockIdx.x;
   const int grp = threadIdx.x >> 7, tid = threadIdx.x & 127, quarter = tid >> 5;
   const int col = 4 * tid;
-  const RowSplits s = row_splits(split_offset, batch, rows, g);
+  const RowSplits s = row_splits(units, split_offset, batch, rows, g);
   pdl_wait_prior_grid();
   float m = -INFINITY, z = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -259,11 +283,16 @@ cudaError_t launch_shared_lengths(const int32_t* seqlens, int batch, int32_t* le
   return cudaGetLastError();
 }
 
-cudaError_t launch_shared_combine(const float* o_accum, const float* lse_accum, const int32_t* split_offset,
-                                  int batch, int rows, void* out, int out_type, float* lse, int sms,
-                                  cudaStream_t st) {
+cudaError_t launch_shared_combine(const float* o_accum, const float* lse_accum, const int32_t* units,
+                                  const int32_t* split_offset, int batch, int rows, void* out, int out_type,
+                                  float* lse, int sms, cudaStream_t st) {
   const long long total = static_cast<long long>(batch) * rows;
-  const bool few = total < 4ll * sms;
+  // A block of eight groups hides the latency of its splits, 128 threads a row
+  // leave more rows resident.  Whole calls with 16 heads, groups and rows, over
+  // 1024 / 16384 shared keys: 128 rows 14.3 and 18.9 / 20.6 and 36.3 us, 256 17.2
+  // and 18.0 / 26.1 and 30.1, 384 20.5 and 18.3 / 32.3 and 31.9, 1024 32.6 and
+  // 23.2 / 60.2 and 49.0.
+  const bool few = total <= 2ll * sms;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(total), 1, 1);
   cfg.blockDim = dim3(few ? 128 * kGroups : 128, 1, 1);
@@ -274,10 +303,10 @@ cudaError_t launch_shared_combine(const float* o_accum, const float* lse_accum, 
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (few)
-    return cudaLaunchKernelEx(&cfg, shared_combine_splits_kernel, o_accum, lse_accum, split_offset, batch, rows, out,
-                              out_type, lse);
-  return cudaLaunchKernelEx(&cfg, shared_combine_rows_kernel, o_accum, lse_accum, split_offset, batch, rows, out,
-                            out_type, lse);
+    return cudaLaunchKernelEx(&cfg, shared_combine_splits_kernel, o_accum, lse_accum, units, split_offset, batch, rows,
+                              out, out_type, lse);
+  return cudaLaunchKernelEx(&cfg, shared_combine_rows_kernel, o_accum, lse_accum, units, split_offset, batch, rows,
+                            out, out_type, lse);
 }
 
 }  // namespace mla

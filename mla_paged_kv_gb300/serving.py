@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+from struct import Struct
 
 import torch
 
@@ -46,6 +47,7 @@ SERVING_SIGS = {
     "mla_shared_prefix_get_plan": (_I, [_P, _I, _P, _I, _I, _I, _I, _I, _P, _SZ, _P]),
     "mla_shared_prefix_decode_fwd": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _SZ, _I, _P, _SZ, _P, _I,
                                           _P, _P, _P]),
+    "mla_serving_call": (_I, [_I, ctypes.c_char_p, _SZ]),
 }
 SERVING_SYMBOLS = tuple(SERVING_SIGS)
 
@@ -87,6 +89,29 @@ def _status(status, like):
 
 
 _INT32, _FP32, _UINT8 = torch.int32, torch.float32, torch.uint8
+
+# The calls of mla_serving_call (mla_call_t): number, packing of the argument
+# words, their bytes.
+def _words(op, layout):
+    s = Struct(layout)
+    return op, s.pack, s.size
+
+
+_APPEND, _GROW, _FORK, _FREE = _words(0, "15qd6q"), _words(1, "11q"), _words(2, "12q"), _words(3, "10q")
+_COMPACT, _COPY_PAGES, _PROMPT = _words(4, "12q"), _words(5, "10q"), _words(6, "16qd6q")
+_SHARED_PREFIX = _words(7, "10qd10q")
+
+
+def _call(op, name, *args):
+    rc = load_library().mla_serving_call(op[0], op[1](*args), op[2])
+    if rc:
+        _check(rc, name)
+
+
+def mla_serving_call(op, args):
+    """The packed form of the calls (bytes of 8-byte words), as the functions below use it."""
+    args = bytes(args)
+    _check(load_library().mla_serving_call(int(op), args, len(args)), "mla_serving_call")
 
 
 # ------------------------------------------------------------------ append
@@ -130,8 +155,7 @@ def mla_cache_append(c, r, cache, block_table, cache_seqlens, status, cu_seqlens
     batch, max_pages = block_table.shape
     if cache_seqlens.shape[0] != batch:
         raise ValueError("block_table / cache_seqlens batch mismatch")
-    cu_ptr = weight_ptr = cos_ptr = ref_ptr = None
-    max_pos = 0
+    cu_ptr = weight_ptr = cos_ptr = ref_ptr = max_pos = 0
     if cu_seqlens is not None:
         cu_ptr = _p(cu_seqlens, _INT32, 1, dev, "cu_seqlens")
         if cu_seqlens.shape[0] != batch + 1:
@@ -152,12 +176,11 @@ def mla_cache_append(c, r, cache, block_table, cache_seqlens, status, cu_seqlens
         if refcount.shape[0] != pages:
             raise ValueError("refcount must have one entry a page")
     st_ptr = _p(status, _INT32, 1, dev, "status")
-    rc = load_library().mla_cache_append(
-        c.data_ptr(), cs, r.data_ptr(), rs, code, tokens, cu_ptr, lens_ptr, batch, table_ptr, max_pages, cache_ptr,
+    _call(
+        _APPEND, "mla_cache_append", c.data_ptr(), cs, r.data_ptr(), rs, code, tokens, cu_ptr, lens_ptr, batch,
+        table_ptr, max_pages, cache_ptr,
         DTYPE_FP8_RECORD if fp8 else code, pages, weight_ptr, norm_eps, cos_ptr, max_pos,
         1 if rope_interleaved else 0, ref_ptr, st_ptr, _q(stream, dev))
-    if rc:
-        _check(rc, "mla_cache_append")
 
 
 def cache_append(c, r, cache, block_table, cache_seqlens, cu_seqlens=None, norm_weight=None, norm_eps=1e-6,
@@ -188,10 +211,8 @@ def mla_cache_grow(refcount, block_table, seqlens, rows, new_tokens, status, str
     n = rows.shape[0]
     if new_tokens.shape[0] != n:
         raise ValueError("rows and new_tokens must have the same length")
-    rc = load_library().mla_cache_grow(*args, rows_ptr, new_ptr, n, _p(status, _INT32, 1, dev, "status"),
-                                       _q(stream, dev))
-    if rc:
-        _check(rc, "mla_cache_grow")
+    _call(_GROW, "mla_cache_grow", *args, rows_ptr, new_ptr, n, _p(status, _INT32, 1, dev, "status"),
+          _q(stream, dev))
 
 
 def mla_cache_fork(refcount, block_table, seqlens, parents, children, pairs, status, stream=None):
@@ -202,19 +223,15 @@ def mla_cache_fork(refcount, block_table, seqlens, parents, children, pairs, sta
     n = parents.shape[0]
     if children.shape[0] != n or pairs.shape != (n, 2):
         raise ValueError("parents and children must have the same length n, and pairs be [n, 2]")
-    rc = load_library().mla_cache_fork(*args, par_ptr, chi_ptr, n, pairs_ptr, _p(status, _INT32, 1, dev, "status"),
-                                       _q(stream, dev))
-    if rc:
-        _check(rc, "mla_cache_fork")
+    _call(_FORK, "mla_cache_fork", *args, par_ptr, chi_ptr, n, pairs_ptr, _p(status, _INT32, 1, dev, "status"),
+          _q(stream, dev))
 
 
 def mla_cache_free(refcount, block_table, seqlens, rows, status, stream=None):
     dev = refcount.get_device()
     args = _pages(refcount, block_table, seqlens, dev)
-    rc = load_library().mla_cache_free(*args, _p(rows, _INT32, 1, dev, "rows"), rows.shape[0],
-                                       _p(status, _INT32, 1, dev, "status"), _q(stream, dev))
-    if rc:
-        _check(rc, "mla_cache_free")
+    _call(_FREE, "mla_cache_free", *args, _p(rows, _INT32, 1, dev, "rows"), rows.shape[0],
+          _p(status, _INT32, 1, dev, "status"), _q(stream, dev))
 
 
 def mla_cache_compact_workspace_bytes(num_pages: int) -> int:
@@ -228,10 +245,8 @@ def mla_cache_compact(refcount, block_table, seqlens, pairs, count, workspace, s
     ws_ptr = _p(workspace, _UINT8, 1, dev, "workspace")
     if pairs.shape[0] < args[1] // 2 or pairs.shape[1] != 2 or count.shape[0] < 1:
         raise ValueError("pairs must be [num_pages // 2, 2] and count have one entry")
-    rc = load_library().mla_cache_compact(*args, pairs_ptr, count_ptr, ws_ptr, workspace.shape[0],
-                                          _p(status, _INT32, 1, dev, "status"), _q(stream, dev))
-    if rc:
-        _check(rc, "mla_cache_compact")
+    _call(_COMPACT, "mla_cache_compact", *args, pairs_ptr, count_ptr, ws_ptr, workspace.shape[0],
+          _p(status, _INT32, 1, dev, "status"), _q(stream, dev))
 
 
 def mla_cache_copy_pages(pool, pairs, status, count=None, layered=False, stream=None):
@@ -256,12 +271,11 @@ def mla_cache_copy_pages(pool, pairs, status, count=None, layered=False, stream=
     pairs_ptr = _p(pairs, _INT32, 2, dev, "pairs")
     if pairs.shape[1] != 2:
         raise ValueError("pairs must be [n, 2]")
-    rc = load_library().mla_cache_copy_pages(
-        pool.data_ptr(), layers, layer_stride if layers > 1 else 0, shape[lead - 1], page, pairs_ptr,
-        None if count is None else _p(count, _INT32, 1, dev, "count"), pairs.shape[0],
+    _call(
+        _COPY_PAGES, "mla_cache_copy_pages", pool.data_ptr(), layers, layer_stride if layers > 1 else 0,
+        shape[lead - 1], page, pairs_ptr,
+        0 if count is None else _p(count, _INT32, 1, dev, "count"), pairs.shape[0],
         _p(status, _INT32, 1, dev, "status"), _q(stream, dev))
-    if rc:
-        _check(rc, "mla_cache_copy_pages")
 
 
 def cache_grow(refcount, block_table, seqlens, rows, new_tokens, status=None):
@@ -320,6 +334,7 @@ class PromptPlan:
 
     def __init__(self, plan, batch, total_q, total_k, causal):
         self.plan = plan
+        self.bytes = plan.numel()
         self.batch = batch
         self.total_q = total_q
         self.total_k = total_k
@@ -343,10 +358,8 @@ def mla_prompt_get_plan(cu_seqlens_q, cu_seqlens_k, total_q, total_k, causal, pl
         "mla_prompt_get_plan")
 
 
-def mla_prompt_attention_fwd(q, k, v, pl, out, lse, status, softmax_scale=None, stream=None):
-    """q [total_q, h_q, 192 or 128], k [total_k, h_kv, same], v [total_k, h_kv,
-    128], bf16 or fp16, last dimension contiguous, other strides multiples of 8;
-    pl a PromptPlan; out [total_q, h_q, 128] of q's type, lse fp32 [total_q, h_q]."""
+def _prompt(q, k, v, pl, softmax_scale, status, stream, out=None, lse=None):
+    """The checks and the call of mla_prompt_attention_fwd; allocates out and lse if not given."""
     dt = q.dtype
     code = _DTYPE_CODE16.get(dt)
     if code is None or k.dtype is not dt or v.dtype is not dt:
@@ -356,7 +369,7 @@ def mla_prompt_attention_fwd(q, k, v, pl, out, lse, status, softmax_scale=None, 
         raise ValueError("q, k and v must be [tokens, heads, dim]")
     total_q, h_q, d = q.shape
     total_k, h_kv, dk = k.shape
-    if d not in (128, 192) or dk != d or v.shape != (total_k, h_kv, 128):
+    if (d != 192 and d != 128) or dk != d or v.shape != (total_k, h_kv, 128):
         raise ValueError("q and k must have 128 or 192 dims, v 128, k and v the same tokens and heads")
     if h_kv < 1 or h_q % h_kv:
         raise ValueError("the key heads must divide the query heads")
@@ -367,17 +380,28 @@ def mla_prompt_attention_fwd(q, k, v, pl, out, lse, status, softmax_scale=None, 
     dev = q.get_device()
     if k.get_device() != dev or v.get_device() != dev:
         raise ValueError("q, k and v must be on one device")
-    out_ptr, lse_ptr = _p(out, dt, 3, dev, "out"), _p(lse, _FP32, 2, dev, "lse")
-    if out.shape != (total_q, h_q, 128) or lse.shape != (total_q, h_q):
-        raise ValueError("out must be [total_q, h_q, 128] and lse [total_q, h_q]")
-    plan = pl.plan
-    rc = load_library().mla_prompt_attention_fwd(
-        q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], code, total_q, total_k,
-        pl.batch, h_q, h_kv, d, 1.0 / math.sqrt(d) if softmax_scale is None else softmax_scale,
-        _p(plan, _UINT8, 1, dev, "plan"), plan.shape[0], out_ptr, lse_ptr, _p(status, _INT32, 1, dev, "status"),
-        _q(stream, dev))
-    if rc:
-        _check(rc, "mla_prompt_attention_fwd")
+    st = _p(status, _INT32, 1, dev, "status")
+    plan = _p(pl.plan, _UINT8, 1, dev, "plan")
+    queue = _q(stream, dev)
+    if out is None:
+        out = torch.empty((total_q, h_q, 128), dtype=dt, device=q.device)
+        lse = torch.empty((total_q, h_q), dtype=_FP32, device=q.device)
+        out_ptr, lse_ptr = out.data_ptr(), lse.data_ptr()
+    else:
+        out_ptr, lse_ptr = _p(out, dt, 3, dev, "out"), _p(lse, _FP32, 2, dev, "lse")
+        if out.shape != (total_q, h_q, 128) or lse.shape != (total_q, h_q):
+            raise ValueError("out must be [total_q, h_q, 128] and lse [total_q, h_q]")
+    _call(_PROMPT, "mla_prompt_attention_fwd", q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(),
+          vs[0], vs[1], code, total_q, total_k, pl.batch, h_q, h_kv, d,
+          1.0 / math.sqrt(d) if softmax_scale is None else softmax_scale, plan, pl.bytes, out_ptr, lse_ptr, st, queue)
+    return out, lse
+
+
+def mla_prompt_attention_fwd(q, k, v, pl, out, lse, status, softmax_scale=None, stream=None):
+    """q [total_q, h_q, 192 or 128], k [total_k, h_kv, same], v [total_k, h_kv,
+    128], bf16 or fp16, last dimension contiguous, other strides multiples of 8;
+    pl a PromptPlan; out [total_q, h_q, 128] of q's type, lse fp32 [total_q, h_q]."""
+    _prompt(q, k, v, pl, softmax_scale, status, stream, out, lse)
 
 
 def plan_prompt(cu_seqlens_q, cu_seqlens_k=None, total_q=None, total_k=None, causal=True, status=None):
@@ -405,10 +429,8 @@ def prompt_attention(q, k, v, cu_seqlens_q, cu_seqlens_k=None, causal=True, soft
         pl = plan_prompt(cu_seqlens_q, cu_seqlens_k, q.shape[0], k.shape[0], causal)
     elif pl.causal != bool(causal):
         raise ValueError("the plan was made with another causal setting")
-    out = torch.empty(q.shape[0], q.shape[1], 128, dtype=q.dtype, device=q.device)
-    lse = torch.empty(q.shape[0], q.shape[1], dtype=torch.float32, device=q.device)
     st = _status(status, q)
-    mla_prompt_attention_fwd(q, k, v, pl, out, lse, st, softmax_scale)
+    out, lse = _prompt(q, k, v, pl, softmax_scale, st, None)
     if status is None:
         check_status(st, "mla_prompt_attention_fwd")
     return out, lse
@@ -459,38 +481,49 @@ def mla_shared_prefix_get_plan(block_table, cache_seqlens, s_q, h_q, causal, num
         _p(plan, _UINT8, 1, dev, "plan"), plan.shape[0], _q(stream, dev)), "mla_shared_prefix_get_plan")
 
 
+def _shared_prefix(q, kv, block_table, pl, softmax_scale, status, stream, out=None, lse=None, out_dtype=None):
+    """The checks and the call of mla_shared_prefix_decode_fwd; allocates out and lse if not given."""
+    dt = q.dtype
+    code = _DTYPE_CODE16.get(dt)
+    fp8 = kv.dtype is _UINT8
+    if code is None or (kv.dtype is not dt and not (fp8 and dt is torch.bfloat16)):
+        raise TypeError("q and kv must be both bf16 or both fp16, or a bf16 q over FP8 records")
+    dev = q.get_device()
+    q_ptr, kv_ptr = _p(q, dt, 4, dev, "q"), _p(kv, kv.dtype, 3, dev, "kv")
+    table_ptr = _p(block_table, _INT32, 2, dev, "block_table")
+    B, s_q, h_q, d = q.shape
+    pages, page, width = kv.shape
+    if d != 576 or page != 64 or width != (656 if fp8 else 576):
+        raise ValueError("q must be [B, s_q, h_q, 576] and kv [pages, 64, 576] or records [pages, 64, 656]")
+    batch, max_pages = block_table.shape
+    if batch != B or pl.batch != B or pl.s_q != s_q or pl.h_q != h_q or pl.max_pages != max_pages:
+        raise ValueError("the plan or block table was made for another batch")
+    plan, ws, st = pl.plan, pl.workspace, _p(status, _INT32, 1, dev, "status")
+    plan_ptr, ws_ptr = _p(plan, _UINT8, 1, dev, "plan"), _p(ws, _UINT8, 1, dev, "workspace")
+    queue = _q(stream, dev)
+    if out is None:
+        out = torch.empty((B, s_q, h_q, 512), dtype=out_dtype, device=q.device)
+        lse = torch.empty((B, s_q, h_q), dtype=_FP32, device=q.device)
+        out_ptr, lse_ptr = out.data_ptr(), lse.data_ptr()
+    else:
+        out_dtype = out.dtype
+        if out_dtype not in _DTYPE_CODE:
+            raise TypeError("out must be bf16, fp16 or fp32")
+        out_ptr, lse_ptr = _p(out, out_dtype, 4, dev, "out"), _p(lse, _FP32, 3, dev, "lse")
+        if out.shape != (B, s_q, h_q, 512) or lse.shape != (B, s_q, h_q):
+            raise ValueError("out must be [B, s_q, h_q, 512] and lse [B, s_q, h_q]")
+    _call(_SHARED_PREFIX, "mla_shared_prefix_decode_fwd", q_ptr, kv_ptr, table_ptr, max_pages, pages, B, s_q, h_q,
+          DTYPE_FP8_RECORD if fp8 else code, 1 if pl.causal else 0, softmax_scale, plan_ptr, plan.shape[0],
+          pl.num_parts, ws_ptr, ws.shape[0], out_ptr, _DTYPE_CODE[out_dtype], lse_ptr, st, queue)
+    return out, lse
+
+
 def mla_shared_prefix_decode_fwd(q, kv, block_table, pl, out, lse, status, softmax_scale=1.0 / 24.0, stream=None):
     """q [B, s_q, h_q, 576] and kv [pages, 64, 576], both bf16 or both fp16, or a
     bf16 q over FP8 records (uint8 [pages, 64, 656]); pl a SharedPrefixPlan of
     this block table; out [B, s_q, h_q, 512] bf16, fp16 or fp32, lse fp32
     [B, s_q, h_q]."""
-    dt = q.dtype
-    code, out_code = _DTYPE_CODE16.get(dt), _DTYPE_CODE.get(out.dtype)
-    fp8 = kv.dtype is _UINT8
-    if code is None or (kv.dtype is not dt and not (fp8 and dt is torch.bfloat16)):
-        raise TypeError("q and kv must be both bf16 or both fp16, or a bf16 q over FP8 records")
-    if out_code is None:
-        raise TypeError("out must be bf16, fp16 or fp32")
-    dev = q.get_device()
-    q_ptr, kv_ptr = _p(q, dt, 4, dev, "q"), _p(kv, kv.dtype, 3, dev, "kv")
-    table_ptr = _p(block_table, _INT32, 2, dev, "block_table")
-    out_ptr, lse_ptr = _p(out, out.dtype, 4, dev, "out"), _p(lse, _FP32, 3, dev, "lse")
-    B, s_q, h_q, d = q.shape
-    pages, page, width = kv.shape
-    if d != 576 or page != 64 or width != (656 if fp8 else 576):
-        raise ValueError("q must be [B, s_q, h_q, 576] and kv [pages, 64, 576] or records [pages, 64, 656]")
-    if out.shape != (B, s_q, h_q, 512) or lse.shape != (B, s_q, h_q):
-        raise ValueError("out must be [B, s_q, h_q, 512] and lse [B, s_q, h_q]")
-    batch, max_pages = block_table.shape
-    if batch != B or pl.batch != B or pl.s_q != s_q or pl.h_q != h_q or pl.max_pages != max_pages:
-        raise ValueError("the plan or block table was made for another batch")
-    plan, ws = pl.plan, pl.workspace
-    rc = load_library().mla_shared_prefix_decode_fwd(
-        q_ptr, kv_ptr, table_ptr, max_pages, pages, B, s_q, h_q, DTYPE_FP8_RECORD if fp8 else code, 1 if pl.causal else 0, softmax_scale,
-        _p(plan, _UINT8, 1, dev, "plan"), plan.shape[0], pl.num_parts, _p(ws, _UINT8, 1, dev, "workspace"),
-        ws.shape[0], out_ptr, out_code, lse_ptr, _p(status, _INT32, 1, dev, "status"), _q(stream, dev))
-    if rc:
-        _check(rc, "mla_shared_prefix_decode_fwd")
+    _shared_prefix(q, kv, block_table, pl, softmax_scale, status, stream, out, lse)
 
 
 def plan_shared_prefix(block_table, cache_seqlens, s_q, h_q, causal=False, num_parts=None):
@@ -510,16 +543,13 @@ def plan_shared_prefix(block_table, cache_seqlens, s_q, h_q, causal=False, num_p
 def shared_prefix_decode(q, kv, block_table, cache_seqlens, causal=False, softmax_scale=None, out_fp32=False,
                          pl=None, status=None):
     """Dense decode that attends the pages all requests share once; returns (out, lse)."""
-    B, s_q, h_q, _ = q.shape
     if pl is None:
-        pl = plan_shared_prefix(block_table, cache_seqlens, s_q, h_q, causal)
+        pl = plan_shared_prefix(block_table, cache_seqlens, q.shape[1], q.shape[2], causal)
     elif pl.causal != bool(causal):
         raise ValueError("the plan was made with another causal setting")
-    out = torch.empty(B, s_q, h_q, 512, dtype=torch.float32 if out_fp32 else q.dtype, device=q.device)
-    lse = torch.empty(B, s_q, h_q, dtype=torch.float32, device=q.device)
     st = _status(status, q)
-    mla_shared_prefix_decode_fwd(q, kv, block_table, pl, out, lse, st,
-                                 1.0 / 24.0 if softmax_scale is None else softmax_scale)
+    out, lse = _shared_prefix(q, kv, block_table, pl, 1.0 / 24.0 if softmax_scale is None else softmax_scale, st, None,
+                              out_dtype=_FP32 if out_fp32 else q.dtype)
     if status is None:
         check_status(st, "mla_shared_prefix_decode_fwd")
     return out, lse

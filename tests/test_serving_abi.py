@@ -133,6 +133,35 @@ def test_shared_decode_refusals(change, want):
     assert mla.load_library().mla_shared_prefix_decode_fwd(*{**SDEC, **change}.values()) == want
 
 
+def test_packed_call():
+    """mla_serving_call takes the same arguments as 8-byte words, and refuses another number of them."""
+    lib = mla.load_library()
+    for op, base in enumerate((APPEND, GROW, FORK, FREE, COMPACT, COPY, PROMPT, SDEC)):
+        values = [v.value or 0 if isinstance(v, ctypes.c_void_p) else v for v in base.values()]
+        words = b"".join(np.float64(v).tobytes() if isinstance(v, float) else np.int64(v).tobytes() for v in values)
+        assert lib.mla_serving_call(op, words, len(words) - 8) == INVALID
+        assert lib.mla_serving_call(op, None, len(words)) == INVALID
+        # refused for the same reason as the call itself: one pointer or size at a time
+        for i, v in enumerate(values):
+            if isinstance(v, float) or v in (0, 4096):
+                continue
+            bad = words[:8 * i] + np.int64(-1).tobytes() + words[8 * i + 8:]
+            args = [x if j != i else -1 for j, x in enumerate(base.values())]
+            got = lib.mla_serving_call(op, bad, len(bad))
+            assert got == getattr(lib, NAMES[op])(*args)
+            if got == INVALID:
+                break
+        else:
+            raise AssertionError("no refusal compared")
+    assert lib.mla_serving_call(8, b"", 0) == INVALID and lib.mla_serving_call(-1, b"", 0) == INVALID
+    with pytest.raises(mla.MlaError):
+        mla.mla_serving_call(0, b"")
+
+
+NAMES = ["mla_cache_append", "mla_cache_grow", "mla_cache_fork", "mla_cache_free", "mla_cache_compact",
+         "mla_cache_copy_pages", "mla_prompt_attention_fwd", "mla_shared_prefix_decode_fwd"]
+
+
 def test_shared_prefix_sizes():
     # 64 requests of 16 rows: 8 prefix blocks and 64 own ones; (units + parts) slots of 128 rows
     assert mla.mla_shared_prefix_workspace_bytes(64, 1, 16, 76) == (72 + 76) * 128 * 513 * 4

@@ -146,6 +146,72 @@ def test_an_empty_request():
     assert not out[1].any() and torch.isneginf(lse[1]).all()
 
 
+@pytest.mark.parametrize("empty", [[0], [3], [0, 1, 4], [1, 2, 3, 4], [0, 1, 2, 3, 4]])
+@pytest.mark.parametrize("s_q,causal,fp8,few", [(1, False, False, 0), (2, True, False, 3), (2, True, True, 65),
+                                                (1, False, True, 63)])
+def test_short_slots_stand_apart(empty, s_q, causal, fp8, few):
+    """Requests that see less than a page leave the others' prefix alone: their rows of the table and of q
+    hold nothing, and no page of the others' prefix is read for them."""
+    c = Case(4, [64, 100, 5, 1, 200], s_q, 16, causal, seed=10, fp8=fp8)
+    spare = c.kv.shape[0] - 1
+    for b in empty:
+        c.lens[b] = min(few, 63 if not causal else 64)
+        c.table[b] = -1
+        c.table[b, 0] = spare
+        if c.lens[b] == 0:
+            c.q[b] = float("nan")
+    out, lse = c.run()
+    q = c.q
+    c.q = torch.where(torch.isnan(q), torch.zeros_like(q), q)
+    ref_out, ref_lse = c.want()
+    others = [b for b in range(5) if b not in empty]
+    if others:
+        compare(out, lse, ref_out, ref_lse, rows=others)
+    # The short slots' page may hold rows of 1000 (the poison), beyond what absolute bars are made for.  With
+    # M = sum p |v| >= |out|: weights and outputs rounded to bf16 are off by 2^-8 of M each, a sum over the
+    # rounded weights by as much again.  A score sums 576 products in fp32, 36 matrix steps and a handful of
+    # roundings, each off by 2^-24 of A = scale sum |q k| at most: d = 48 2^-24 max A, so the LSE is off by d
+    # and 2^-20 for its own sum, and weights by a factor of e^(2 d) at most.
+    for b in empty:
+        n = c.lens[b]
+        o, l = out[b].double().cpu().numpy(), lse[b].double().cpu().numpy()
+        if n == 0:
+            assert not o.any() and np.isneginf(l).all()
+            continue
+        kv = c.kv[spare, :n]
+        keys = np.stack([orc.decode_record(r) for r in kv.numpy()]) if fp8 else kv.double().numpy()
+        qs = c.q[b].double().numpy()
+        scores = np.einsum("shd,kd->shk", qs, keys) / 24
+        if causal:
+            for s in range(s_q):
+                scores[s, :, n - s_q + 1 + s:] = -np.inf
+        w = np.exp(scores - scores.max(2, keepdims=True))
+        w /= w.sum(2, keepdims=True)
+        mag = np.einsum("shk,kd->shd", w, np.abs(keys[:, :512]))
+        d = 48 * 2.0**-24 * (np.einsum("shd,kd->shk", np.abs(qs), np.abs(keys)).max() / 24)
+        assert np.abs(l - ref_lse[b]).max() <= d + 2.0**-20
+        assert (np.abs(o - ref_out[b]) <= (3 * 2.0**-8 + np.expm1(2 * d)) * mag).all()
+
+
+@pytest.mark.parametrize("empty", [[], [0], [2], [0, 3]])
+def test_plan_shares_without_empty_slots(empty):
+    """The plan's own units start behind the prefix, except those of the slots that stand apart."""
+    c = Case(4, [64, 100, 5, 1], 1, 16, seed=11)
+    for b in empty:
+        c.lens[b] = 0
+        c.table[b] = -1
+    pl = mla.plan_shared_prefix(torch.from_numpy(c.table).cuda(), i32(c.lens), 1, 16)
+    units = pl.plan[:5 * 32].view(torch.int32).reshape(5, 8).cpu().tolist()
+    lens = pl.plan[256:256 + 20].view(torch.int32).cpu().tolist()
+    width = c.table.shape[1]
+    first = next(b for b in range(4) if b not in empty)
+    assert units[0] == [0, 64, -1, first * width, width, 0, 0, 0] and lens[0] == 256
+    for b in range(4):
+        skip = 0 if b in empty else 4
+        assert units[1 + b][:6] == [16 * b, 16, -1, b * width + skip, width - skip, int(b in empty)]
+        assert lens[1 + b] == (0 if b in empty else c.lens[b] - 256)
+
+
 def test_one_request_and_many():
     Case(12, [77], 1, 16, seed=11).check()
     Case(2, [(i * 13) % 90 for i in range(150)], 1, 8, seed=12).check()
