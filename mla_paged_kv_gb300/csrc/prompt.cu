@@ -48,9 +48,11 @@
 // 1137 us, a converged warp 953 (an MMA's operand moves cost a lone thread 110
 // cycles), pairs 912, weights announced by relaxed cluster arrivals 779 (a release
 // waits for earlier stores to reach the cluster: 1700 cycles), stores exchanged
-// among lanes 770, the roles' dispatch made warp-uniform 688.
+// among lanes 770, the roles' dispatch made warp-uniform 688.  (Ragged batches: deal.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <algorithm>
 
 #include "common.cuh"
 #include "ptx.cuh"
@@ -86,6 +88,18 @@ enum : int {
 
 // Shared memory of one CTA: Q (2 halves x kQBoxes boxes), then K stages (the
 // CTA's keys x kQBoxes 64-dim slices), then V stages (128 keys x the CTA's dims).
+// Dealing out the last kRanked rounds of items (deal); in Q's place before the
+// first loads.
+constexpr int kRanked = 3;
+constexpr int kMaxWorkers = 80;
+constexpr int kLongTiles = 12;  // key tiles of an item of 20 us
+struct Deal {
+  uint32_t keys[2][kMaxWorkers];
+  uint32_t times[kRanked][kMaxWorkers];
+  uint8_t dealt[kRanked];
+};
+static_assert(kRanked == 3 && kMaxWorkers <= 255, "three bytes of a word");
+
 template <int kQBoxes, bool kPair>
 struct Layout {
   static constexpr int kHalfRows = kPair ? 256 : 128;          // query rows of a half
@@ -110,7 +124,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr float kTau = 8.0f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
-// Plan: a header {tiles, causal}, then the tiles, kTileInts int32 each.
+// Plan: a header {tiles, causal, deal by sums}, then the tiles, kTileInts int32 each.
 struct Tile {
   int q0;    // first query row of the tile in the packed q
   int rows;  // queries of the sequence from q0 on (the first two halves' worth matter)
@@ -163,31 +177,40 @@ __device__ __forceinline__ int half_tiles(const Tile& t, int h, int half_rows, i
 
 // The items of one worker, the same in every role.  An item is one tile of the
 // plan and one query head, all heads of a tile in a row in the list.  In round r
-// a worker gets number r * workers + worker of the list, counted backwards in
-// every other round, so that the sums of the descending list come out nearly
-// equal.  It runs them 32 rounds at a time in the order of their heads: the
-// workers then read the keys of few heads at a time, which stay in L2.  (In the
-// list's order a ragged batch read its keys 2.3 times from HBM.)
+// a worker gets one of the list's numbers r * workers .. (r + 1) * workers - 1:
+// counted backwards in every other round, and in the last rounds the longest of
+// them goes to the worker whose sum is smallest (deal).  It runs them 32 rounds
+// at a time in the order of their heads: the workers then read the keys of few
+// heads at a time, which stay in L2.  (In the list's order a ragged batch read
+// its keys 2.3 times from HBM.)
 struct Items {
-  int at, total;  // the current item's number; `total`: no more
-  int base;       // first of the 32 rounds
-  uint32_t key;   // head and round of the current one, + 1
+  int at, total;    // the current item's number; `total`: no more
+  int base;         // first of the 32 rounds
+  uint32_t key;     // head and round of the current one, + 1
+  int ranked;       // first round whose place is a byte of `dealt`
+  uint32_t dealt;
 };
 
-__device__ __forceinline__ int item_of_round(int round, int worker, int workers) {
-  return round * workers + ((round & 1) ? workers - 1 - worker : worker);
+__device__ __forceinline__ int place_in_round(int round, int worker, int workers) {
+  return (round & 1) ? workers - 1 - worker : worker;
+}
+
+__device__ __forceinline__ int item_of_round(const Items& it, int round, int worker, int workers) {
+  const int k = round - it.ranked;
+  const int place = k < 0 ? place_in_round(round, worker, workers) : static_cast<int>(it.dealt >> (8 * k & 31) & 255u);
+  return round * workers + place;
 }
 
 // By a whole warp: lane i looks at round base + i.
 __device__ __forceinline__ void next_item(Items& it, int worker, int workers, int heads) {
   const int lane = threadIdx.x & 31;
   while (true) {
-    const int at = item_of_round(it.base + lane, worker, workers);
+    const int at = item_of_round(it, it.base + lane, worker, workers);
     const uint32_t key = (static_cast<uint32_t>(at % heads) << 5 | static_cast<uint32_t>(lane)) + 1u;
     const uint32_t mine = at < it.total && key > it.key ? key : ~0u;
     if (__any_sync(0xffffffffu, mine != ~0u)) {
       it.key = __shfl_sync(0xffffffffu, __reduce_min_sync(0xffffffffu, mine), 0);
-      it.at = item_of_round(it.base + static_cast<int>((it.key - 1u) & 31u), worker, workers);
+      it.at = item_of_round(it, it.base + static_cast<int>((it.key - 1u) & 31u), worker, workers);
       return;
     }
     it.base += 32;
@@ -204,6 +227,66 @@ __device__ __forceinline__ Tile load_tile(const PromptParams& p, const Items& it
   const int4* e = reinterpret_cast<const int4*>(p.plan + kTileInts * (it.at / p.h_q + 1));
   const int4 a = e[0];
   return Tile{a.x, a.y, a.z, a.w, e[1].x};
+}
+
+// Time of an item in tenths of a microsecond, near enough to compare sums:
+// steps of both halves, of one, and the change of items.
+__device__ __forceinline__ uint32_t item_time(const int32_t* plan, int heads, int at, int total, int half_rows,
+                                              int causal) {
+  if (at >= total) return 0;
+  const int4* e = reinterpret_cast<const int4*>(plan + kTileInts * (at / heads + 1));
+  const int4 a = e[0];
+  const Tile t{a.x, a.y, a.z, a.w, e[1].x};
+  const int n0 = half_tiles(t, 0, half_rows, causal), n1 = half_tiles(t, 1, half_rows, causal);
+  return 15u * min(n0, n1) + 12u * abs(n0 - n1) + 13u;
+}
+
+// The worker's places in the last kRanked of at least as many rounds, a byte
+// each, worked out by every CTA alike (kG threads keep a worker's sum): within a
+// round the list descends, so the rank among the sums, smallest first, is the
+// place to take.  Going back and forth alone leaves the longest worker 2 to 12%
+// over the mean for ragged batches, this 1 to 4%, and it takes 2 to 3 us: 8 ragged
+// prompts up to 4000 tokens x 16 heads 242 -> 233 us, 8 others 128.5 -> 125, 3 x 128
+// heads 247 -> 242; but 32 of 1024 tokens 169 -> 172, 16 ragged ones up to 700 39 ->
+// 41.  So the plan asks for it where lengths differ and an item takes 20 us, and
+// pairs of CTAs alone do it (152 single workers rank in 6 us).  By all threads of
+// the CTA; a call, so that its registers cost the roles none.
+template <int kG>
+__device__ __noinline__ uint32_t deal(const int32_t* plan, int heads, int total, int rounds, int worker, int workers,
+                                      int half_rows, int causal, Deal* s) {
+  constexpr uint32_t kMost = (1u << 23) - 1;  // sums beyond 0.8 s count as equal
+  const int w = threadIdx.x / kG, sub = threadIdx.x % kG, from = rounds - kRanked;
+  const bool mine = w < workers;
+  uint32_t sum = 0;
+  if (mine) {
+    for (int k = sub; k < kRanked; k += kG)
+      s->times[k][w] = item_time(plan, heads, (from + k) * workers + w, total, half_rows, causal);
+#pragma unroll 2
+    for (int r = sub; r < from; r += kG)
+      sum = min(sum + item_time(plan, heads, r * workers + place_in_round(r, w, workers), total, half_rows, causal),
+                kMost);
+  }
+#pragma unroll
+  for (int o = 1; o < kG; o <<= 1) sum = min(sum + __shfl_xor_sync(0xffffffffu, sum, o), kMost);
+  for (int k = 0; k < kRanked; ++k) {
+    const uint32_t key = sum << 8 | static_cast<uint32_t>(w);
+    if (sub == 0) s->keys[k & 1][w] = mine ? key : ~0u;
+    __syncthreads();
+    int place = 0;
+#pragma unroll 10
+    for (int i = sub; i < kThreads / kG; i += kG) place += s->keys[k & 1][i] < key;
+#pragma unroll
+    for (int o = 1; o < kG; o <<= 1) place += __shfl_xor_sync(0xffffffffu, place, o);
+    if (mine) {
+      sum = min(sum + s->times[k][place], kMost);
+      if (w == worker && sub == 0) s->dealt[k] = static_cast<uint8_t>(place);
+    }
+  }
+  __syncthreads();
+  const uint32_t dealt = s->dealt[0] | s->dealt[1] << 8 | s->dealt[2] << 16;
+  fence_proxy_async_smem();  // the loads may write there next
+  __syncthreads();
+  return dealt;
 }
 
 __device__ __forceinline__ void fail(volatile int* abort_flag, int32_t* status) {
@@ -282,7 +365,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const uint32_t tmem = *tmem_slot;
   const int causal = p.plan[1];
-  Items it{0, p.plan[0] * p.h_q, 0, 0};
+  Items it{0, p.plan[0] * p.h_q, 0, 0, 1 << 30, 0};
+  if constexpr (kPair) {
+    const int rounds = (it.total + workers - 1) / workers;
+    if (p.plan[2] && rounds >= kRanked) {  // (two rounds back and forth are the same)
+      it.dealt = deal<kThreads / kMaxWorkers>(p.plan, p.h_q, it.total, rounds, worker, workers, L::kHalfRows, causal,
+                                              reinterpret_cast<Deal*>(sQ));
+      it.ranked = rounds - kRanked;
+    }
+  }
   next_item(it, worker, workers, p.h_q);
 
   if (warp > kWarpMma) {
@@ -731,14 +822,16 @@ __global__ void __launch_bounds__(kPlanThreads)
                        int tile_q, int max_tiles, int32_t* plan, int32_t* status) {
   __shared__ int bin[kBins];
   __shared__ int warp_sum[32];
-  __shared__ int longest, broken;
+  __shared__ int longest, broken, ragged;
   for (int i = threadIdx.x; i < kBins; i += kPlanThreads) bin[i] = 0;
   if (threadIdx.x == 0) {
     longest = 1;
     broken = 0;
+    ragged = 0;
   }
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int len_q = cu_q[1] - cu_q[0], len_k = cu_k[1] - cu_k[0];
   // warp per sequence, lanes over its tiles
   auto each = [&](auto f) {
     for (int b = warp; b < batch; b += kPlanThreads / 32) {
@@ -749,6 +842,7 @@ __global__ void __launch_bounds__(kPlanThreads)
         lq = 0;
         broken = 1;
       }
+      if (lq != len_q || lk != len_k) ragged = 1;
       for (int m = lane; m * tile_q < lq; m += 32) {
         const int row0 = m * tile_q;
         const Tile t{q0 + row0, lq - row0, k0, lk, lk - lq + row0 + 1};
@@ -778,6 +872,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     // offsets out of order could make sequences overlap: no tiles at all then
     plan[0] = broken ? 0 : base + inc;
     plan[1] = causal;
+    plan[2] = ragged && longest >= kLongTiles;
     if (broken) report(status, MLA_ERR_BAD_INDEX);
   }
   __syncthreads();
@@ -850,7 +945,8 @@ cudaError_t launch_prompt(const CUtensorMap& q, const CUtensorMap& k, const CUte
                           bool half, int d_qk, bool pair, int sms, cudaStream_t st) {
   const int ctas = pair ? 2 : 1;
   const long long items = static_cast<long long>(p.max_tiles) * p.h_q;
-  const int workers = static_cast<int>(items < sms / ctas ? items : sms / ctas);
+  const int most = pair ? std::min(sms / 2, pr::kMaxWorkers) : sms;
+  const int workers = static_cast<int>(items < most ? items : most);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(workers * ctas), 1, 1);
   cfg.blockDim = dim3(pr::kThreads, 1, 1);

@@ -88,6 +88,13 @@ def test_many_short_prompts():
     run(lens, lens, seed=5)
 
 
+@pytest.mark.parametrize("lens,h,causal", [([1800, 300, 1100, 1, 1700], 24, True), ([1700, 1600], 32, True),
+                                           ([200, 1600, 900, 1300], 40, False)])
+def test_long_ragged_prompts(lens, h, causal):
+    """Three to six rounds of items whose last ones are dealt out by the workers' sums; every row once."""
+    run(lens, lens, h=h, hkv=1, causal=causal, seed=len(lens))
+
+
 @pytest.mark.parametrize("lq,lk", [([1], [1000]), ([129], [1025]), ([300], [301]), ([5, 400], [133, 900])])
 def test_chunk_behind_earlier_keys(lq, lk):
     run(lq, lk, h=4, hkv=4, seed=lq[0])
