@@ -111,15 +111,15 @@ enum : int {
   QB_EMPTY = QB_FULL + kQSmemBoxes,  // +slot: the box in that slot has been copied into TMEM
   K_FULL = QB_EMPTY + kQSmemBoxes,   // +slot
   K_EMPTY = K_FULL + kKSlots,     // +slot
-  V_FULL = K_EMPTY + kKSlots,     // +slot
-  V_EMPTY = V_FULL + kVSlots,     // +slot
+  V_FULL = K_EMPTY + kKSlots,     // +v_full(tile): by slot and parity of the slot's load
+  V_EMPTY = V_FULL + 2 * kVSlots,  // +slot
   S_FULL = V_EMPTY + kVSlots,
   S_FREE,
   OWN_GO,     // softmax -> P V thread: P of an own tile written, O rescaled
   OWN_FREE,   // own P buffer reusable: own P V done + the peer's P V done (its multicast commit)
   RECV_FULL,  // the peer's P has landed (bulk-copy bytes); watched and re-armed by the P V thread
-  RECV_GO,    // softmax -> P V thread: received tile's reference applied (O rescaled if it changed)
-  R_FULL,     // raw-maximum mailbox filled (remote-store bytes)
+  RECV_GO,    // +(n&1), softmax -> P V thread: n-th received tile's reference applied (O rescaled if it changed)
+  R_FULL = RECV_GO + 2,     // raw-maximum mailbox filled (remote-store bytes)
   R_FREE,     // the peer has read our last references (one remote arrival per warp)
   L_FULL,     // row-sum mailbox filled (bulk-copy bytes)
   L_FREE,     // the peer has read our last row sums (one remote arrival per warp)
@@ -213,6 +213,15 @@ __device__ __forceinline__ void cursor_next(const DecodeParams& p, const Part& P
     cursor_seek(p, P, c, c.b + 1);
   }
 }
+
+// The V_FULL barrier of tile t and its phase.  Two a slot, by parity of the slot's
+// load: the Q K^T thread looks only at own tiles, and V of the slot's tile before
+// may still be in flight then, which with one barrier would read as "landed".
+// (V t-6 has landed: the P of own tile t-4 waited for P V t-6.)
+__device__ __forceinline__ int v_full(uint32_t t) {
+  return static_cast<int>(t % kVSlots + kVSlots * ((t / kVSlots) & 1u));
+}
+__device__ __forceinline__ uint32_t v_phase(uint32_t t) { return (t / kVSlots >> 1) & 1u; }
 
 // Global box held in slot position j of this rank's K slot: the other half's
 // value dims, then the RoPE box.
@@ -480,16 +489,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&bars[K_FULL + i], 1);
       mbar_init(&bars[K_EMPTY + i], 1);
     }
-    for (int i = 0; i < kVSlots; ++i) {
-      mbar_init(&bars[V_FULL + i], 1);
-      mbar_init(&bars[V_EMPTY + i], 1);
-    }
+    for (int i = 0; i < 2 * kVSlots; ++i) mbar_init(&bars[V_FULL + i], 1);
+    for (int i = 0; i < kVSlots; ++i) mbar_init(&bars[V_EMPTY + i], 1);
     mbar_init(&bars[S_FULL], 1);
     mbar_init(&bars[S_FREE], 128);
     mbar_init(&bars[OWN_GO], 128);
     mbar_init(&bars[OWN_FREE], 2);
     mbar_init(&bars[RECV_FULL], 1);
     mbar_init(&bars[RECV_GO], 128);
+    mbar_init(&bars[RECV_GO + 1], 128);
     mbar_init(&bars[R_FULL], 1);
     mbar_init(&bars[R_FREE], 4);
     mbar_init(&bars[L_FULL], 1);
@@ -542,7 +550,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int page_reg = 0, page_base = -1, cur_b = -1;
     cursor_init(p, P, c);
     bool ok = true;
-    uint32_t k_issued[kKSlots] = {}, v_issued[kVSlots] = {};
+    uint32_t k_issued[kKSlots] = {}, v_issued = 0;
     uint32_t own_k = 0;
     while (ok && c.valid) {
       const bool mine = (c.t & 1u) == rank;
@@ -593,9 +601,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (ok) {
               MLA_TRACE(7, c.t);
               uint8_t* dst = sV + s * kVSlotBytes;
-              mbar_arrive_expect_tx(&bars[V_FULL + s], kVSlotBytes);
-              tma_load_5d(dst, &kv_map, &bars[V_FULL + s], 0, 0, 4 * static_cast<int>(rank), grp, page, pol_kv);
-              ++v_issued[s];
+              const int full = v_full(c.t);
+              mbar_arrive_expect_tx(&bars[V_FULL + full], kVSlotBytes);
+              tma_load_5d(dst, &kv_map, &bars[V_FULL + full], 0, 0, 4 * static_cast<int>(rank), grp, page, pol_kv);
+              v_issued = c.t + 1;  // the V warp loads every tile
             }
           }
         }
@@ -609,8 +618,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // no TMA write may land after this CTA exits
       for (int s = 0; s < kKSlots; ++s)
         if (k_issued[s] > 0) mbar_wait(&bars[K_FULL + s], (k_issued[s] - 1) & 1, nullptr, kWaitNs);
-      for (int s = 0; s < kVSlots; ++s)
-        if (v_issued[s] > 0) mbar_wait(&bars[V_FULL + s], (v_issued[s] - 1) & 1, nullptr, kWaitNs);
+      for (uint32_t t = v_issued > kVSlots ? v_issued - kVSlots : 0; t < v_issued; ++t)
+        mbar_wait(&bars[V_FULL + v_full(t)], v_phase(t), nullptr, kWaitNs);
     }
     __syncwarp();
   } else if (warp == kWarpQ) {
@@ -756,9 +765,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const bool first = cursor_first(cv);
           const int vs = static_cast<int>(cv.t % kVSlots);
           bool ready = mine ? test<kWarp>(&bars[OWN_GO], pv_own & 1)
-                            : (test<kWarp>(&bars[RECV_GO], pv_recv & 1) &&
+                            : (test<kWarp>(&bars[RECV_GO + (pv_recv & 1)], (pv_recv >> 1) & 1) &&
                                test<kWarp>(&bars[RECV_FULL], pv_recv & 1));
-          ready = ready && test<kWarp>(&bars[V_FULL + vs], (cv.t / kVSlots) & 1);
+          ready = ready && test<kWarp>(&bars[V_FULL + v_full(cv.t)], v_phase(cv.t));
           if (ready && first && cv.u >= 1) ready = test<kWarp>(&bars[O_FREE], (cv.u - 1) & 1);
           if (ready) {
             MLA_TRACE(3, cv.t);
@@ -917,7 +926,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           } else {
             const int vs = static_cast<int>(cq.t % kVSlots);
-            if (test<kWarp>(&bars[V_FULL + vs], (cq.t / kVSlots) & 1)) {
+            if (test<kWarp>(&bars[V_FULL + v_full(cq.t)], v_phase(cq.t))) {
               MLA_TRACE(8, cq.t);
               tc_fence_after();
               const uint64_t vslot = vk_desc0 + static_cast<uint64_t>((vs * kVSlotBytes) >> 4);
@@ -1130,7 +1139,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (tid == 0) MLA_TRACE(12, t);
         ++own_i;
       } else {
-        mbar_arrive(&bars[RECV_GO]);
+        // (two barriers: a tile that rescales nothing waits for no P V, so this
+        // may run two received tiles ahead of the P V thread, which could no
+        // longer tell the phases of one; four it cannot: the P of own tile t+3
+        // waits for P V t+1)
+        mbar_arrive(&bars[RECV_GO + (recv_i & 1)]);
         if (tid == 0) MLA_TRACE(11, t);
         ++recv_i;
       }
