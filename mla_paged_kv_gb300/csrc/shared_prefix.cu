@@ -33,7 +33,9 @@ __device__ __forceinline__ int keys_seen(const int32_t* seqlens, int b, int s_q,
 
 // The pages every request that sees one starts with (the longest common run of
 // block-table entries, whole pages that every query sees), and the units over
-// them and over the rest.  One block; made once for a batch.
+// them and over the rest.  One block, made once for a batch; its time is the
+// latency of reading the tables (64 requests that share 2048 pages 9.8 us, with
+// one entry a lane in flight 29).
 __global__ void __launch_bounds__(1024)
     shared_units_kernel(const int32_t* table, int max_pages, const int32_t* seqlens, int batch, int s_q, int h_q,
                         int causal, int32_t* units, int32_t* lengths) {
@@ -41,6 +43,7 @@ __global__ void __launch_bounds__(1024)
   if (threadIdx.x == 0) common = max_pages, first = batch;
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kAhead = 8;  // entries a lane has in flight: the loop is their latency
   for (int b = threadIdx.x; b < batch; b += 1024) {
     const int seen = keys_seen(seqlens, b, s_q, causal);
     if (seen >= kTile) {
@@ -56,14 +59,21 @@ __global__ void __launch_bounds__(1024)
     if (keys_seen(seqlens, b, s_q, causal) < kTile) continue;
     const int32_t* row = table + static_cast<long long>(b) * max_pages;
     const int most = *reinterpret_cast<volatile int*>(&common);
-    for (int c0 = 0; c0 < most; c0 += 32) {
-      const int c = c0 + lane;
-      const unsigned diff = __ballot_sync(0xffffffffu, c < most && row[c] != head[c]);
-      if (diff) {
-        if (lane == 0) atomicMin(&common, c0 + __ffs(diff) - 1);
-        break;
+    int at = max_pages;  // the lane's first entry that differs
+    for (int c0 = 0; c0 < most && at == max_pages; c0 += 32 * kAhead) {
+      int a[kAhead], h[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int c = c0 + 32 * i + lane;
+        a[i] = c < most ? row[c] : 0;
+        h[i] = c < most ? head[c] : 0;
       }
+#pragma unroll
+      for (int i = kAhead - 1; i >= 0; --i)
+        if (a[i] != h[i]) at = c0 + 32 * i + lane;
+      at = __reduce_min_sync(0xffffffffu, at);
     }
+    if (lane == 0 && at < max_pages) atomicMin(&common, at);
   }
   __syncthreads();
   const int shared = none ? 0 : common;
