@@ -186,10 +186,17 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const AppendP
         for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[h][k]));
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float scale = top > 0.f ? top / 448.f : 1.f;
+        float scale = top / 448.f;
+        if (!(scale > 0.f)) scale = 1.f;  // (all zero, or below the smallest number times 448)
         // one division a group: c' * (1 / scale) is within 2^-23 of c' / scale,
-        // against the half step of 2^-4 that the code then rounds by
-        const float inv = 1.f / scale;
+        // against the half step of 2^-4 that the code then rounds by; tiny groups
+        // and their scale both by 2^64 before it, where 1 / scale would be infinite
+        float inv = 1.f / scale;
+        if (scale < 0x1p-64f) {
+          inv = 1.f / (scale * 0x1p64f);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[h][k] *= 0x1p64f;
+        }
         uint32_t w[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {

@@ -110,6 +110,19 @@ class Case:
         assert torch.all(rest == (0x5A if self.fp8 else 777.0)), "a slot of no token was written"
 
 
+@pytest.mark.parametrize("exponent", [-60, -64, -100, -120])
+def test_tiny_rows_into_records(exponent):
+    """Scales down to 2^-129, whose reciprocal is no fp32 number; groups of zeros beside them.  (The bars of
+    check() hold: a scale of 2^-129 is rounded by 2^-21 of itself.)"""
+    c = Case([5, 3], [2, 70], fp8=True, norm=False, seed=40)
+    lat = c.c * 2.0 ** exponent  # exact, but for values below bf16's smallest
+    lat[1, 128:256] = 0
+    lat[3, 5:] = 0
+    c.c = lat
+    c.host = (lat.double().numpy(), c.host[1])
+    c.check(c.run())
+
+
 @pytest.mark.parametrize("fp8,dtype", [(False, torch.bfloat16), (False, torch.float16), (True, torch.bfloat16),
                                        (True, torch.float16)])
 @pytest.mark.parametrize("interleaved", [False, True])
