@@ -246,6 +246,27 @@ def test_copy_many_pairs():
     check_copy(pool_of((2, 2 * n, 64, 4), torch.float16, 6), list(zip(order[:n], order[n:])), True)
 
 
+def test_copy_tens_of_thousands_of_pairs():
+    """Blocks that judge more pairs than one pass over the list takes; a few of them refused."""
+    n, pages = 50000, 100100
+    g = torch.Generator().manual_seed(7)
+    pairs = torch.randperm(pages, generator=g)[:2 * n].reshape(n, 2).int()
+    pairs[20000, 1] = pairs[31, 1]       # a target named before: the later pair is refused
+    pairs[49999] = pairs[77]             # the same pair again
+    pairs[12345, 1] = pairs[48000, 0]    # a target that another pair reads
+    pairs[33333, 1] = pages              # outside the pool
+    refused = torch.tensor([20000, 49999, 12345, 33333])
+    pool = torch.randint(0, 256, (pages, 16), dtype=torch.uint8, generator=g).cuda()
+    keep = torch.ones(n, dtype=torch.bool)
+    keep[refused] = False
+    done = pairs[keep].long().cuda()
+    want = pool.clone()
+    want[done[:, 1]] = pool[done[:, 0]]
+    status = i32([0])
+    mla.cache_copy_pages(pool, pairs.cuda(), status=status)
+    assert torch.equal(pool, want) and int(status) == BAD_INDEX
+
+
 def test_copy_past_32_bits():
     pages = (1 << 32) // (64 * 1152) + 40
     pool = torch.zeros(pages, 64, 576, dtype=torch.bfloat16, device="cuda")
