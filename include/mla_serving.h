@@ -188,11 +188,11 @@ int mla_prompt_attention_fwd(const void* d_q, long long q_token_stride, long lon
  * than a page (empty slots of a padded batch) are attended by themselves and
  * leave the others' prefix as it is.  The plan is made once for a batch and
  * read by every layer, while the block table and lengths stay as they were.
- * The prefix is attended together only where that takes fewer 128-row blocks
- * than attending it request by request:
- * ceil(batch * s_q * h_q / 128) < batch * ceil(s_q * h_q / 128).  With s_q * h_q a
- * multiple of 128 every request fills its blocks alone, the shared pages are
- * one copy in L2 either way, and the call is mla_decode_fwd.
+ * The prefix is attended together only where that takes at most 7/8 of the
+ * 128-row blocks that attending it request by request does:
+ * 8 ceil(batch * s_q * h_q / 128) <= 7 batch * ceil(s_q * h_q / 128).  Elsewhere
+ * (s_q * h_q a multiple of 128, say) every request fills its blocks alone, the
+ * shared pages are one copy in L2 either way, and the call is mla_decode_fwd.
  *   num_parts from mla_shared_prefix_num_parts; at most 1024
  * Other arguments as for mla_decode_fwd.  batch * s_q * h_q and
  * batch * max_pages stay below 2^31; s_q * h_q <= 2^20, batch <= 65535. */

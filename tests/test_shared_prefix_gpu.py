@@ -83,6 +83,13 @@ def test_rows_per_request(s_q, h_q, causal):
     Case(5, [s_q, 64, 100, 70, 3 + s_q, 200, 65], s_q, h_q, causal, seed=s_q).check()
 
 
+@pytest.mark.parametrize("h_q", [111, 112, 113, 120])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_around_the_rule_for_packing_rows(h_q, fp8):
+    """Eight requests: up to 112 heads their rows are packed, above each is attended alone."""
+    Case(6, [64, 100, 70, 3, 200, 65, 1, 0], 1, h_q, seed=h_q, fp8=fp8).check()
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("out_fp32", [False, True])
 def test_types(dtype, out_fp32):
