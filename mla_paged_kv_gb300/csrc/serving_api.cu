@@ -431,7 +431,10 @@ int mla_serving_call(int op, const void* args, size_t bytes) {
     std::memcpy(&v, a + 8 * i, 8);
     return v;
   };
-  auto I = [&](int i) { return static_cast<int>(word(i)); };
+  auto I = [&](int i) {  // beyond 32 bits: a number that every size and type refuses
+    const int64_t v = word(i);
+    return v == static_cast<int>(v) ? static_cast<int>(v) : INT32_MIN;
+  };
   auto F = [&](int i) {
     double v;
     std::memcpy(&v, a + 8 * i, 8);

@@ -153,6 +153,10 @@ def test_packed_call():
                 break
         else:
             raise AssertionError("no refusal compared")
+        for i, key in enumerate(base):  # a size that 32 bits would cut to a good one
+            if key in ("batch", "pages", "n", "rows", "width", "layers", "total", "tq", "tk", "hq", "h_q", "s_q"):
+                big = words[:8 * i] + np.int64((1 << 32) + 2).tobytes() + words[8 * i + 8:]
+                assert lib.mla_serving_call(op, big, len(big)) == INVALID, key
     assert lib.mla_serving_call(8, b"", 0) == INVALID and lib.mla_serving_call(-1, b"", 0) == INVALID
     with pytest.raises(mla.MlaError):
         mla.mla_serving_call(0, b"")
