@@ -164,3 +164,54 @@ def test_a_decode_step_as_one_graph():
             assert p.lens[1:5].tolist() == [n] * 4
             compare(out, lse, *p.oracle(q, torch.tensor(samples, device="cuda"), 0))
     p.audit()
+
+
+def test_two_streams_at_once():
+    """Every operator on two streams, each with its own tensors, plans and workspaces, as on one."""
+    g = torch.Generator().manual_seed(21)
+    lens = [300, 1, 700, 130]
+    cu = [0, 300, 301, 1001, 1131]
+
+    def state():
+        r = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).cuda()  # noqa: E731
+        s = dict(q=r(1131, 4, 192), k=r(1131, 4, 192), v=r(1131, 4, 128), row=r(1131, 576), cu=i32(cu))
+        s["table"] = torch.arange(48, dtype=torch.int32).reshape(4, 12).cuda()
+        s["lens"], s["cache"] = i32(lens), r(60, 64, 576)
+        s["shared"] = torch.arange(96, dtype=torch.int32).reshape(4, 24) % 60
+        s["shared"][:, :8] = torch.arange(8, dtype=torch.int32)
+        s["shared"] = s["shared"].cuda()
+        s["slens"], s["dq"], s["kv"] = i32([700, 1400, 600, 513]), r(4, 1, 16, 576), r(60, 64, 576)
+        s["ref"] = (torch.rand(60, generator=g) < 0.6).int().cuda()
+        s["pool"], s["status"] = r(2, 60, 64, 16), i32([0])
+        return s
+
+    def work(s):
+        out, lse = mla.prompt_attention(s["q"], s["k"], s["v"], s["cu"], s["cu"], status=s["status"])
+        cache = s["cache"].clone()
+        mla.cache_append(s["row"][:, :512], s["row"][:, 512:], cache, s["table"], s["lens"], cu_seqlens=s["cu"],
+                         status=s["status"])
+        dec, dlse = mla.shared_prefix_decode(s["dq"], s["kv"], s["shared"], s["slens"], status=s["status"])
+        ref, table, n, pool = s["ref"].clone(), torch.full_like(s["table"], -1), i32([0, 0, 0, 0]), s["pool"].clone()
+        mla.cache_grow(ref, table, n, i32([0, 2]), i32([100, 300]), status=s["status"])
+        pairs = mla.cache_fork(ref, table, n, i32([2]), i32([1]), status=s["status"])
+        mla.cache_copy_pages(pool, pairs, layered=True, status=s["status"])
+        mla.cache_free(ref, table, n, i32([0]), status=s["status"])
+        pairs, count = mla.cache_compact(ref, table, n, status=s["status"])
+        mla.cache_copy_pages(pool, pairs, count=count, layered=True, status=s["status"])
+        return [out, lse, cache, dec, dlse, ref, table, n, pool, pairs, count]
+
+    states = [state(), state()]
+    want = [work(s) for s in states]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in states]
+    for _ in range(5):
+        got = []
+        for _ in range(3):
+            got = []
+            for s, stream in zip(states, streams):
+                with torch.cuda.stream(stream):
+                    got.append(work(s))
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert [int(s["status"]) for s in states] == [0, 0]
