@@ -101,7 +101,7 @@ const DeviceInfo& device_info() {
     return d;
   }
   bool attr_ok = true;
-  for (int kind = 0; kind < 3; ++kind)
+  for (int kind = 0; kind < 4; ++kind)
     attr_ok = attr_ok && cudaFuncSetAttribute(sparse_kernel_ptr(kind), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                               sparse_smem_bytes()) == cudaSuccess;
   for (int kind = 0; kind < 9; ++kind)
@@ -310,7 +310,7 @@ struct SparseCall {
   float* lse = nullptr;
   int32_t* status = nullptr;
   mla_stream_t stream = nullptr;
-  int stall = 0;  // 1: the kernel's stall-test instance (mla_test_decode_timeout)
+  int kind = 0;  // the kernel's instance; 1: the stall-test one (mla_test_decode_timeout), 3: kWarp
 };
 
 int sparse_run(const SparseCall& c, bool combine) {
@@ -365,7 +365,7 @@ int sparse_run(const SparseCall& c, bool combine) {
   const int rc = encode_q_map(&qm, c.q, static_cast<long long>(c.n_units) * c.rows);
   if (rc != MLA_OK) return rc;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(c.stream);
-  if (launch_sparse(qm, p, c.num_parts, c.stall, s) != cudaSuccess) return MLA_ERR_CUDA;
+  if (launch_sparse(qm, p, c.num_parts, c.kind, s) != cudaSuccess) return MLA_ERR_CUDA;
   if (!combine) return MLA_OK;
   return mla_combine(c.ws, c.ws_bytes, c.split_offset, c.n_units, c.rows, c.num_parts, c.out, c.out_type, c.lse,
                      c.status, c.stream);
@@ -378,7 +378,7 @@ int fp8_record_splits(const void* d_q, const void* d_kv, const int32_t* d_block_
                       const int32_t* d_cache_seqlens, int batch, int s_q, int h_q, int h_kv, int causal,
                       float softmax_scale, const int32_t* d_sched, const int32_t* d_split_offset, int num_parts,
                       void* d_workspace, size_t workspace_bytes, void* d_out, int out_type, float* d_lse,
-                      int32_t* d_status, mla_stream_t stream, int stall) {
+                      int32_t* d_status, mla_stream_t stream, int kind) {
   if (!d_block_table || !d_cache_seqlens || max_pages < 1 || batch < 1 || s_q < 1 || h_q < 1)
     return MLA_ERR_INVALID_ARG;
   if (h_kv != 1) return MLA_ERR_UNSUPPORTED;
@@ -410,7 +410,7 @@ int fp8_record_splits(const void* d_q, const void* d_kv, const int32_t* d_block_
   c.lse = d_lse;
   c.status = d_status;
   c.stream = stream;
-  c.stall = stall;
+  c.kind = kind;
   return sparse_run(c, false);
 }
 
@@ -460,27 +460,29 @@ int launch_shared(const SharedLaunch& c, cudaStream_t stream) {
 }
 
 // mla_decode_fwd for a shared-prefix call whose requests (nearly) fill their row
-// blocks alone; 16-bit caches take the kWarp instance.  (16 requests x 128 heads,
-// 16884 keys: 71 us; the V-ring instance that mla_decode_fwd takes there 86.)
+// blocks alone, with the kWarp instances.  (16 requests x 128 heads, 16884 keys:
+// 71 us; the V-ring instance that mla_decode_fwd takes there 86.)
 int decode_full_blocks(const void* q, const void* kv, const int32_t* block_table, int max_pages, int num_pages,
                        const int32_t* lengths, int batch, int s_q, int h_q, int dtype, int causal, float scale,
                        const int32_t* sched, const int32_t* split_offset, int num_parts, void* ws, size_t ws_bytes,
                        void* out, int out_type, float* lse, int32_t* status, cudaStream_t stream) {
-  DecodeParams p;
-  CUtensorMap qm, km, sm, rm;
-  if (dtype != MLA_DTYPE_FP8_RECORD) {
+  if (dtype == MLA_DTYPE_FP8_RECORD) {
+    const int rc = fp8_record_splits(q, kv, block_table, max_pages, num_pages, lengths, batch, s_q, h_q, 1, causal,
+                                     scale, sched, split_offset, num_parts, ws, ws_bytes, out, out_type, lse, status,
+                                     reinterpret_cast<mla_stream_t>(stream), 3);
+    if (rc != MLA_OK) return rc;
+  } else {
+    DecodeParams p;
+    CUtensorMap qm, km, sm, rm;
     const int rc = dense_prepare(q, kv, block_table, max_pages, num_pages, lengths, batch, s_q, h_q, 1, dtype, causal,
                                  scale, sched, split_offset, num_parts, ws, ws_bytes, out, out_type, lse, status, &p,
                                  &qm, &km, &sm, &rm);
     if (rc != MLA_OK) return rc;
-    const int kind = dtype == MLA_DTYPE_FP16 ? 8 : 7;
-    if (launch_dense(qm, km, sm, rm, p, num_parts, kind, stream) != cudaSuccess) return MLA_ERR_CUDA;
-    return mla_combine(ws, ws_bytes, split_offset, batch, s_q * h_q, num_parts, out, out_type, lse, status,
-                       reinterpret_cast<mla_stream_t>(stream));
+    if (launch_dense(qm, km, sm, rm, p, num_parts, dtype == MLA_DTYPE_FP16 ? 8 : 7, stream) != cudaSuccess)
+      return MLA_ERR_CUDA;
   }
-  return mla_decode_fwd(q, kv, block_table, max_pages, num_pages, lengths, batch, s_q, h_q, 1, dtype, causal, scale,
-                        sched, split_offset, num_parts, ws, ws_bytes, out, out_type, lse, status,
-                        reinterpret_cast<mla_stream_t>(stream));
+  return mla_combine(ws, ws_bytes, split_offset, batch, s_q * h_q, num_parts, out, out_type, lse, status,
+                     reinterpret_cast<mla_stream_t>(stream));
 }
 
 cudaError_t launch_plan(const int32_t* lengths, int n_units, int num_parts, int32_t* sched, int32_t* split_offset,

@@ -302,7 +302,7 @@ __device__ __forceinline__ int box_dim(uint32_t rank, int lb) {
 // Group accumulator a reads boxes 2a, 2a+1 (8 K-steps of 16 dims); the RoPE
 // accumulator reads box 4 (4 K-steps).  Fully unrolled: the descriptor
 // offsets are compile-time constants.
-template <int kAcc>
+template <int kAcc, bool kWarp>
 __device__ __forceinline__ void issue_qk(uint32_t tmem, uint64_t q_desc0, uint64_t kv_desc_stage, uint32_t idesc) {
 #pragma unroll
   for (int a = 0; a < kAcc; ++a) {
@@ -312,13 +312,14 @@ __device__ __forceinline__ void issue_qk(uint32_t tmem, uint64_t q_desc0, uint64
       const int lb = a < 2 ? 2 * a + (ks >> 2) : 4;
       const uint32_t off_q = lb * kQBoxBytes + (ks & 3) * 32;
       const uint32_t off_k = lb * kBoxBytes + (ks & 3) * 32;
-      umma_f16(tmem + kTmemS + 64u * a, q_desc0 + (off_q >> 4), kv_desc_stage + (off_k >> 4), idesc,
-               ks > 0 ? 1u : 0u);
+      mma<kWarp>(tmem + kTmemS + 64u * a, q_desc0 + (off_q >> 4), kv_desc_stage + (off_k >> 4), idesc,
+                 ks > 0 ? 1u : 0u);
     }
   }
 }
 
 // O[:, 128g : 128g+128) += P_g (128 x 64 keys) x codes of boxes 2g, 2g+1.
+template <bool kWarp>
 __device__ __forceinline__ void issue_pv(uint32_t tmem, uint64_t p_desc0, uint64_t v_desc_stage, uint32_t idesc,
                                          bool first) {
 #pragma unroll
@@ -327,8 +328,8 @@ __device__ __forceinline__ void issue_pv(uint32_t tmem, uint64_t p_desc0, uint64
     for (int kk = 0; kk < kT / 16; ++kk) {
       const uint32_t off_p = g * kPGroupBytes + kk * 32;
       const uint32_t off_v = 2 * g * kBoxBytes + kk * 2048;
-      umma_f16(tmem + kTmemO + 128u * g, p_desc0 + (off_p >> 4), v_desc_stage + (off_v >> 4), idesc,
-               (first && kk == 0) ? 0u : 1u);
+      mma<kWarp>(tmem + kTmemO + 128u * g, p_desc0 + (off_p >> 4), v_desc_stage + (off_v >> 4), idesc,
+                 (first && kk == 0) ? 0u : 1u);
     }
   }
 }
@@ -336,7 +337,12 @@ __device__ __forceinline__ void issue_pv(uint32_t tmem, uint64_t p_desc0, uint64
 // kShared: units of a shared-prefix plan over a cache of FP8 records (128-row
 // blocks of all requests' queries over the pages they share, and each request's
 // own rows over the rest); one row block a unit, always split partials.
-template <bool kStall, bool kShared = false>
+// kWarp: roles dispatched by a warp-uniform index, MMAs issued by a converged
+// warp, their operands in uniform registers; mailboxes freed by relaxed arrivals
+// (they have been read, and nothing else is to be ordered).  The same operations
+// on the same values.  (64 x 16 heads, 16384 shared keys: 126 us against 145; 64 x 120
+// heads of 8692 keys, nothing shared: 360 against 420.)
+template <bool kStall, bool kShared = false, bool kWarp = kShared>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     sparse_decode_kernel(const __grid_constant__ CUtensorMap q_map, const DecodeParams p) {
   constexpr uint64_t kWaitNs = kStall ? kDecodeStallWaitNs : MLA_WAIT_LIMIT_NS;
@@ -355,7 +361,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
 
   const int tid = threadIdx.x;
-  const int warp = tid >> 5, lane = tid & 31;
+  // (kWarp: by a shuffle, so that the compiler knows that a warp takes one role)
+  const int warp = kWarp ? __shfl_sync(0xffffffffu, tid >> 5, 0) : tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_ctarank();
   const uint32_t peer = rank ^ 1u;
   const int cluster_id = blockIdx.x >> 1;
@@ -553,7 +560,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (ptid == 0 && q_issued > 0) mbar_wait(&bars[Q_FULL], (q_issued - 1) & 1, nullptr, kWaitNs);
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    if (kWarp || lane == 0) {
+      const uint32_t tmem_u = kWarp ? __shfl_sync(0xffffffffu, tmem, 0) : tmem;
       constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kT, false);
       constexpr uint32_t idesc_pv = idesc_bf16_f32(128, 128, true);
       const uint64_t q_desc0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
@@ -568,20 +576,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       cursor_init(p, P, cv);
       bool ok = true;
       uint64_t t_last = globaltimer_ns();
+      uint32_t idle = 0;
       while (cv.valid) {
         bool progressed = false;
         if (cv.t < cq.t) {
-          bool ready = mbar_test_wait(&bars[P_FULL], cv.t & 1);
+          bool ready = test<kWarp>(&bars[P_FULL], cv.t & 1);
           const bool first = cv.k == cv.lo, last = cv.k == cv.hi - 1;
-          if (ready && first && cv.u >= 1) ready = mbar_test_wait(&bars[O_FREE], (cv.u - 1) & 1);
+          if (ready && first && cv.u >= 1) ready = test<kWarp>(&bars[O_FREE], (cv.u - 1) & 1);
           if (ready) {
             tc_fence_after();
             const int st = cv.t & 1;
             MLA_TRACE(2, cv.t);
-            issue_pv(tmem, p_desc0, v_desc0 + static_cast<uint64_t>((st * kStageBytes) >> 4), idesc_pv, first);
-            umma_commit(&bars[P_FREE]);
-            umma_commit(&bars[KV_EMPTY + st]);
-            if (last) umma_commit(&bars[O_FULL]);
+            issue_pv<kWarp>(tmem_u, p_desc0, v_desc0 + static_cast<uint64_t>((st * kStageBytes) >> 4), idesc_pv, first);
+            commit<kWarp>(&bars[P_FREE]);
+            commit<kWarp>(&bars[KV_EMPTY + st]);
+            if (last) commit<kWarp>(&bars[O_FULL]);
             cursor_next(p, P, cv);
             progressed = true;
           }
@@ -589,9 +598,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (cq.valid) {
           const int st = cq.t & 1;
           bool ready = true;
-          if (cq.k == cq.lo) ready = mbar_test_wait(&bars[Q_FULL], cq.u & 1);
-          ready = ready && mbar_test_wait(&bars[KV_FULL + st], (cq.t >> 1) & 1);
-          if (ready && cq.t >= 1) ready = mbar_test_wait(&bars[S_FREE], (cq.t - 1) & 1);
+          if (cq.k == cq.lo) ready = test<kWarp>(&bars[Q_FULL], cq.u & 1);
+          ready = ready && test<kWarp>(&bars[KV_FULL + st], (cq.t >> 1) & 1);
+          if (ready && cq.t >= 1) ready = test<kWarp>(&bars[S_FREE], (cq.t - 1) & 1);
           if (ready) {
             tc_fence_after();
             MLA_TRACE(3, cq.t);
@@ -600,17 +609,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // (the softmax's wait for them runs out)
             if (!(kStall && cq.t == 0)) {
               if (rank == 0)
-                issue_qk<3>(tmem, q_desc0, kvs, idesc_qk);
+                issue_qk<3, kWarp>(tmem_u, q_desc0, kvs, idesc_qk);
               else
-                issue_qk<2>(tmem, q_desc0, kvs, idesc_qk);
-              umma_commit(&bars[S_FULL]);
+                issue_qk<2, kWarp>(tmem_u, q_desc0, kvs, idesc_qk);
+              commit<kWarp>(&bars[S_FULL]);
             }
-            if (cq.k == cq.hi - 1) umma_commit(&bars[Q_EMPTY]);
+            if (cq.k == cq.hi - 1) commit<kWarp>(&bars[Q_EMPTY]);
             cursor_next(p, P, cq);
             progressed = true;
           }
         }
-        if (progressed) {
+        if constexpr (kWarp) {
+          if (stuck(progressed, idle, t_last, abort_flag)) {
+            ok = false;
+            break;
+          }
+        } else if (progressed) {
           t_last = globaltimer_ns();
         } else {
           if (*abort_flag || globaltimer_ns() - t_last > kWaitNs) {
@@ -620,9 +634,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           __nanosleep(32);
         }
       }
-      if (!ok) set_abort(abort_flag, p.status, MLA_ERR_TIMEOUT);
+      if (!ok && (!kWarp || lane == 0)) set_abort(abort_flag, p.status, MLA_ERR_TIMEOUT);
       // every MMA has completed before TMEM is released
-      umma_commit(&bars[DRAIN]);
+      commit<kWarp>(&bars[DRAIN]);
       mbar_wait(&bars[DRAIN], 0, nullptr, kWaitNs);
     }
     __syncwarp();
@@ -781,7 +795,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // both warps have read the mailbox: arm it for the next tile, free it for the peer
         if (sender) {
           mbar_arrive_expect_tx(&bars[X_FULL + q], 2 * 32 * 128);
-          mbar_arrive_remote(xfree_remote);
+          if constexpr (kWarp)
+            mbar_arrive_remote_relaxed(xfree_remote);
+          else
+            mbar_arrive_remote(xfree_remote);
         }
         // ---- phase 3: the row's tile max, reference, exponentials, P
         tc_fence_after();
@@ -1161,9 +1178,10 @@ __global__ void __launch_bounds__(256) unpack_kernel(const uint8_t* __restrict__
 int sparse_smem_bytes() { return sp::kSmemBytes; }
 int sparse_threads() { return sp::kThreads; }
 // kind 1: the test instance whose first tile's scores are never computed;
-// 2: under a shared-prefix plan
+// 2: under a shared-prefix plan; 3: kWarp
 const void* sparse_kernel_ptr(int kind) {
-  return kind == 2   ? reinterpret_cast<const void*>(&sp::sparse_decode_kernel<false, true>)
+  return kind == 3   ? reinterpret_cast<const void*>(&sp::sparse_decode_kernel<false, false, true>)
+         : kind == 2   ? reinterpret_cast<const void*>(&sp::sparse_decode_kernel<false, true>)
          : kind == 1 ? reinterpret_cast<const void*>(&sp::sparse_decode_kernel<true>)
                      : reinterpret_cast<const void*>(&sp::sparse_decode_kernel<false>);
 }
@@ -1171,7 +1189,9 @@ const void* sparse_kernel_ptr(int kind) {
 cudaError_t launch_sparse(const CUtensorMap& q_map, const DecodeParams& p, int num_parts, int kind,
                           cudaStream_t stream) {
   const dim3 grid(2 * num_parts * p.row_blocks);
-  if (kind == 2)
+  if (kind == 3)
+    sp::sparse_decode_kernel<false, false, true><<<grid, sp::kThreads, sp::kSmemBytes, stream>>>(q_map, p);
+  else if (kind == 2)
     sp::sparse_decode_kernel<false, true><<<grid, sp::kThreads, sp::kSmemBytes, stream>>>(q_map, p);
   else if (kind == 1)
     sp::sparse_decode_kernel<true><<<grid, sp::kThreads, sp::kSmemBytes, stream>>>(q_map, p);

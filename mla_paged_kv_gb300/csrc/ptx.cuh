@@ -618,4 +618,50 @@ __device__ __forceinline__ void pdl_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// ---------------------------------------------------------------- issuers
+
+// Whether a polling issuer (a converged warp) has to give up: no progress for
+// the wait budget, or another role gave up.  The clock is read only once in 256
+// idle passes.
+__device__ __forceinline__ bool stuck(bool progressed, uint32_t& idle, uint64_t& t_last,
+                                      const volatile int* abort_flag) {
+  if (progressed) {
+    idle = 0;
+    return false;
+  }
+  if ((++idle & 255u) != 0) return false;
+  const uint64_t now = globaltimer_ns();
+  if (idle == 256u) t_last = now;
+  return __any_sync(0xffffffffu, *abort_flag != 0 || now - t_last > MLA_WAIT_LIMIT_NS);
+}
+
+// The two issuers run on one lane, or (kWarp) on a converged warp that elects
+// the lane that issues: see umma_f16_warp.
+template <bool kWarp>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  if constexpr (kWarp)
+    umma_f16_warp(d, a, b, idesc, acc);
+  else
+    umma_f16(d, a, b, idesc, acc);
+}
+template <bool kWarp>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  if constexpr (kWarp)
+    umma_f16_ts_warp(d, a, b, idesc, acc);
+  else
+    umma_f16_ts(d, a, b, idesc, acc);
+}
+template <bool kWarp>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if constexpr (kWarp)
+    umma_commit_warp(bar);
+  else
+    umma_commit(bar);
+}
+template <bool kWarp>
+__device__ __forceinline__ bool test(uint64_t* bar, uint32_t parity) {
+  const bool done = mbar_test_wait(bar, parity);
+  return kWarp ? __all_sync(0xffffffffu, done) : done;
+}
+
 }  // namespace mla

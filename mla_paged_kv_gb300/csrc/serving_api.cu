@@ -107,8 +107,8 @@ int shared_sizes(int batch, int s_q, int h_q, int num_parts, SharedSizes* z) {
   // (64 requests unless said, 8192 shared and 500 own keys, bf16): 96 heads 111 and
   // 125 us, 104 116 and 128, 112 126 and 127, 120 136 and 131; 32 requests x 2 x 100
   // heads, 4096 keys 72 and 75, 2 x 112 80 and 76.  (A prefix of 1024 keys and 96
-  // heads loses: 42 and 39; 64 heads 33.5 and 36.)  FP8 records: 96 heads 337 and
-  // 417 us, 112 390 and 418, 120 413 and 419.
+  // heads loses: 42 and 39; 64 heads 33.5 and 36.)  FP8 records: 96 heads 290 and
+  // 358 us, 112 334 and 358, 120 355 and 360.
   z->share = front * 8 <= own * 7;
   const long long units = z->share ? own + front : batch;
   z->units = static_cast<int>(units);
