@@ -103,8 +103,9 @@ int mla_cache_fork(int32_t* d_refcount, int num_pages, int32_t* d_block_table, i
                    int32_t* d_status, mla_stream_t stream);
 
 /* Free rows: the counts of a row's pages go down (a page whose count is
- * already 0 is left there and reported, MLA_ERR_BAD_INDEX), its entries
- * become -1 and its length 0.  A row listed twice is freed once. */
+ * already 0 is left there and reported, MLA_ERR_BAD_INDEX, as an entry that
+ * names none is), its entries become -1 and its length 0.  A row listed twice
+ * is freed once. */
 int mla_cache_free(int32_t* d_refcount, int num_pages, int32_t* d_block_table, int rows, int max_pages,
                    int32_t* d_seqlens, const int32_t* d_rows, int n, int32_t* d_status, mla_stream_t stream);
 

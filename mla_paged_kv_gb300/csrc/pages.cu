@@ -265,21 +265,22 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const PageState s, const
 // ------------------------------------------------------------------ free
 
 // One warp per listed row.  The row's length is taken by an exchange, so a
-// row listed twice is freed once, whichever entry gets there.
+// row listed twice is freed once, whichever entry gets there; a length out of
+// range is no call's to take, and stays.
 __global__ void __launch_bounds__(128) free_kernel(const PageState s, const int32_t* rows, int n) {
   const int lane = threadIdx.x & 31;
   const int i = blockIdx.x * 4 + (threadIdx.x >> 5);
   if (i >= n) return;
   const int r = rows[i];
-  if (r < 0 || r >= s.rows) {
+  int len = -1;
+  if (r >= 0 && r < s.rows && lane == 0) {
+    len = *const_cast<volatile int32_t*>(&s.seqlens[r]);
+    len = len < 0 || len > static_cast<long long>(s.max_pages) * kTile ? -1 : atomicExch(&s.seqlens[r], 0);
+  }
+  len = __shfl_sync(0xffffffffu, len, 0);
+  if (len < 0) {
     if (lane == 0) report(s.status, MLA_ERR_BAD_INDEX);
     return;
-  }
-  int len = lane == 0 ? atomicExch(&s.seqlens[r], 0) : 0;
-  len = __shfl_sync(0xffffffffu, len, 0);
-  if (len < 0 || len > static_cast<long long>(s.max_pages) * kTile) {
-    if (lane == 0) report(s.status, MLA_ERR_BAD_INDEX);
-    len = len < 0 ? 0 : s.max_pages * kTile;
   }
   int32_t* entry = s.table + static_cast<long long>(r) * s.max_pages;
   for (int j = lane; j < pages_of(len); j += 32) {

@@ -122,7 +122,7 @@ class Pool:
 
     def free(self, rows):
         for r in rows:
-            if not 0 <= r < len(self.table):
+            if not 0 <= r < len(self.table) or not 0 <= self.lens[r] <= len(self.table[r]) * PAGE:
                 self.bad = True
                 continue
             for j in range(_pages(self.lens[r])):

@@ -276,3 +276,15 @@ def test_copy_past_32_bits():
     pool[pages - 2:] = 0
     pool[2] = 0
     assert not pool.any()
+
+
+@pytest.mark.parametrize("length", [-1, -2 ** 31, 7 * 64 + 1, 10 ** 6, 2 ** 31 - 1])
+def test_free_leaves_a_row_whose_length_is_out_of_range(length):
+    """Such an entry is reported and its row left as it was; entries behind a length are not read."""
+    s = State(3, 200, 60, seed=20)
+    assert len(s.host.table[0]) == 7
+    s.host.lens[1] = length
+    s.host.table[1][5:] = s.host.table[0][:1] + s.host.table[2][:1]  # stale: pages of the other rows
+    s.lens, s.table = i32(s.host.lens), i32(s.host.table)
+    s.free([1, 0, 1])
+    assert s.host.bad and s.host.lens[1] == length and s.host.lens[0] == 0
