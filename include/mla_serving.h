@@ -96,7 +96,8 @@ int mla_cache_grow(int32_t* d_refcount, int num_pages, int32_t* d_block_table, i
  * filled last page is replaced by a fresh page, and d_pairs[i] = (parent's
  * page, fresh page) for mla_cache_copy_pages, else (-1, -1).  A parent may
  * appear any number of times; an entry whose child is listed twice or is not
- * empty, or whose parent is a child in this call, is refused.
+ * empty, or whose parent is a child in this call or names a page outside the
+ * pool or a free one, is refused.
  *   d_pairs int32 [n, 2] out */
 int mla_cache_fork(int32_t* d_refcount, int num_pages, int32_t* d_block_table, int rows, int max_pages,
                    int32_t* d_seqlens, const int32_t* d_parents, const int32_t* d_children, int n, int32_t* d_pairs,

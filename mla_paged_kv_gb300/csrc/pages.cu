@@ -54,6 +54,7 @@ struct AllocSmem {
   int first[kMaxPageList + 1];             // pages wanted before entry i; [n] = all
   uint32_t seen[kMaxPageRows / 32];        // rows listed
   uint32_t twice[kMaxPageRows / 32];       // rows listed more than once
+  uint32_t broken[kMaxPageList / 32];      // fork: entries whose parent names a page that is not in use
   int scan[33];
 };
 
@@ -194,9 +195,10 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(const PageState s, const
 
 // ------------------------------------------------------------------ fork
 
-// Length of entry i's parent, or -1 if the entry cannot be served.
-__device__ __forceinline__ int forked(const PageState& s, const AllocSmem& sm, const int32_t* parents,
-                                      const int32_t* children, int i) {
+// Length of entry i's parent, or -1 if the entry cannot be served (its parent's
+// pages apart).
+__device__ __forceinline__ int parent_len(const PageState& s, const AllocSmem& sm, const int32_t* parents,
+                                          const int32_t* children, int i) {
   const int pr = parents[i], ch = children[i];
   if (pr < 0 || pr >= s.rows || ch < 0 || ch >= s.rows) return -1;
   if (bit(sm.twice, ch) || bit(sm.seen, pr)) return -1;
@@ -205,10 +207,30 @@ __device__ __forceinline__ int forked(const PageState& s, const AllocSmem& sm, c
   return len < 0 || len > static_cast<long long>(s.max_pages) * kTile ? -1 : len;
 }
 
+__device__ __forceinline__ int forked(const PageState& s, const AllocSmem& sm, const int32_t* parents,
+                                      const int32_t* children, int i) {
+  return bit(sm.broken, i) ? -1 : parent_len(s, sm, parents, children, i);
+}
+
 __global__ void __launch_bounds__(kThreads) fork_kernel(const PageState s, const int32_t* parents,
                                                          const int32_t* children, int n, int2* pairs) {
   __shared__ AllocSmem sm;
+  const int lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < kMaxPageList / 32; i += kThreads) sm.broken[i] = 0u;
   mark_rows(sm, children, n, s.rows);
+  // a parent that names a page outside the pool or a free one: refused as a whole,
+  // before any page is handed out
+  for (int i = threadIdx.x >> 5; i < n; i += kThreads / 32) {
+    const int pages = pages_of(max(parent_len(s, sm, parents, children, i), 0));
+    const int32_t* from = s.table + static_cast<long long>(parents[i]) * s.max_pages;
+    bool bad = false;
+    for (int j = lane; j < pages; j += 32) {
+      const int page = from[j];
+      bad |= page < 0 || page >= s.num_pages || s.refcount[page] <= 0;
+    }
+    if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&sm.broken[i >> 5], 1u << (i & 31));
+  }
+  __syncthreads();
   scan_wants(sm, n, [&](int i) {
     const int len = forked(s, sm, parents, children, i);
     return len > 0 && (len & 63) != 0 ? 1 : 0;
@@ -216,7 +238,6 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const PageState s, const
   const int want = sm.first[n];
   const int found = scan_free(sm, s.refcount, s.num_pages, want,
                               [&](int k, int page) { pairs[entry_of(sm, n, k)] = make_int2(-1, page); });
-  const int lane = threadIdx.x & 31;
   // every entry is judged before any length changes (a child's length is read by its own entry only,
   // a parent's never written)
   for (int i = threadIdx.x >> 5; i < n; i += kThreads / 32) {
@@ -238,12 +259,7 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const PageState s, const
       int page = -1;
       if (j < full) {
         page = from[j];
-        if (page < 0 || page >= s.num_pages) {
-          report(s.status, MLA_ERR_BAD_INDEX);
-          page = -1;
-        } else {
-          atomicAdd(&s.refcount[page], 1);
-        }
+        atomicAdd(&s.refcount[page], 1);
       } else if (j == full && tail) {
         page = pairs[i].y;
       }

@@ -91,10 +91,11 @@ class Pool:
 
     def fork(self, parents, children):
         free, at, width = self._free(), 0, len(self.table[0])
-        pairs, lens0 = [], list(self.lens)
+        pairs, lens0, ref0 = [], list(self.lens), list(self.ref)
         for p, c in zip(parents, children):
             ok = 0 <= p < len(self.table) and 0 <= c < len(self.table) and list(children).count(c) == 1 and \
-                p not in list(children) and lens0[c] == 0 and 0 <= lens0[p] <= width * PAGE
+                p not in list(children) and lens0[c] == 0 and 0 <= lens0[p] <= width * PAGE and \
+                all(0 <= q < len(ref0) and ref0[q] > 0 for q in self.table[p][:_pages(lens0[p])])
             pairs.append((-1, -1))
             if not ok:
                 self.bad = True
@@ -106,12 +107,8 @@ class Pool:
                 continue
             row = [-1] * width
             for j in range(full):
-                q = self.table[p][j]
-                if 0 <= q < len(self.ref):
-                    row[j] = q
-                    self.ref[q] += 1
-                else:
-                    self.bad = True
+                row[j] = self.table[p][j]
+                self.ref[row[j]] += 1
             if tail:
                 row[full] = free[at - 1]
                 self.ref[free[at - 1]] = 1

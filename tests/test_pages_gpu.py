@@ -288,3 +288,17 @@ def test_free_leaves_a_row_whose_length_is_out_of_range(length):
     s.lens, s.table = i32(s.host.lens), i32(s.host.table)
     s.free([1, 0, 1])
     assert s.host.bad and s.host.lens[1] == length and s.host.lens[0] == 0
+
+
+@pytest.mark.parametrize("page", [-1, 40, 10 ** 6, "free"])
+@pytest.mark.parametrize("where", [0, 1, 3])  # full pages, the partly filled last one
+def test_fork_refuses_a_parent_with_a_bad_page(where, page):
+    """A parent that names a page outside the pool, or a free one, forks into nothing; the other entries are
+    served, with the lowest free pages."""
+    s = State(2, 0, 40, seed=21, empty_rows=5, width=6)
+    s.grow([0, 1], [200, 150])
+    s.host.table[0][where] = s.host.ref.index(0) if page == "free" else page
+    s.table = i32(s.host.table)
+    s.fork([0, 1, 0, 1], [3, 4, 5, 6])
+    assert s.host.bad and s.host.lens == [200, 150, 0, 0, 150, 0, 150]
+    assert s.host.table[3] == s.host.table[5] == [-1] * 6
