@@ -248,3 +248,50 @@ def test_one_row_for_every_token():
     assert torch.equal(cache[1, 11:20], rows) and not cache[0].any() and not cache[1, :11].any()
     mla.cache_append(a[:, :512], a[:, 512:], cache, table, torch.tensor([1], dtype=torch.int32, device="cuda"))
     assert torch.equal(cache[1, 0], a[0])
+
+
+@pytest.mark.parametrize("exponent", [0, -40, -90, 30])
+def test_codes_are_the_quotients_rounded(exponent):
+    """codes = E4M3(c' / scale), the quotient in fp32, bit for bit; among the rows are quotients at ties, where a
+    product with the reciprocal of the scale rounds to the other neighbour."""
+    tops = [m / 128.0 for m in range(128, 256)]
+    finite = torch.arange(0x7f80, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).float()
+    rows, g = [], torch.Generator().manual_seed(41)
+
+    def code(v):
+        return v.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+
+    for top in tops:
+        scale = torch.tensor(top) / 448
+        x = finite[(finite <= top) & (finite > 0)]
+        tie = x[code(x / scale) != code(x * (1 / scale))]
+        fill = torch.randn(128, generator=g).clamp(-top, top).to(torch.bfloat16).float()
+        fill[0] = top
+        fill[1:1 + min(len(tie), 120)] = tie[:120]
+        rows.append(fill)
+    lat = (torch.stack(rows).reshape(32, 512) * 2.0 ** exponent).to(torch.bfloat16)
+    c = Case([32], [40], fp8=True, norm=False, rope=False, seed=42)
+    c.c, c.host = lat, (lat.double().numpy(), c.host[1])
+    cache = c.run()
+    c.check(cache)
+    x = lat.float().reshape(32, 4, 128)
+    scale = x.abs().amax(2) / 448
+    want = code(x / scale[..., None])
+    assert (want != code(x * (1 / scale)[..., None])).sum() > 50
+    at, _ = so.append_targets(c.cu, c.lens, c.table, c.pages)
+    got = torch.stack([cache[p, r].cpu() for p, r, _ in (at[t] for t in range(32))])
+    assert torch.equal(got[:, :512].reshape(32, 4, 128), want)
+    assert torch.equal(got[:, 512:528].contiguous().view(torch.float32), scale)
+
+
+def test_infinity_takes_its_group():
+    """A scale of infinity: finite values over it are zeros, infinities no number; other groups as ever."""
+    c = Case([2], [0], fp8=True, seed=43, norm=False, rope=False)
+    c.c[0, 130] = float("inf")
+    c.c[0, 140] = -3e38
+    cache = c.run()
+    row = cache[int(c.table[0, 0]), 0].cpu()
+    codes, scale = so.e4m3_value(row[:512].numpy()), row[512:528].clone().view(torch.float32).numpy()
+    assert np.isinf(scale[1]) and np.isfinite(scale[[0, 2, 3]]).all()
+    assert np.isnan(codes[130]) and not np.delete(codes[128:256], 2).any()
+    assert np.isfinite(np.delete(codes, 130)).all() and codes[:128].any() and codes[256:].any()
