@@ -425,11 +425,11 @@ def plan_prompt(cu_seqlens_q, cu_seqlens_k=None, total_q=None, total_k=None, cau
 def prompt_attention(q, k, v, cu_seqlens_q, cu_seqlens_k=None, causal=True, softmax_scale=None, pl=None,
                      status=None):
     """Attention over packed prompts; returns (out, lse)."""
+    st = _status(status, q)
     if pl is None:
-        pl = plan_prompt(cu_seqlens_q, cu_seqlens_k, q.shape[0], k.shape[0], causal)
+        pl = plan_prompt(cu_seqlens_q, cu_seqlens_k, q.shape[0], k.shape[0], causal, st)
     elif pl.causal != bool(causal):
         raise ValueError("the plan was made with another causal setting")
-    st = _status(status, q)
     out, lse = _prompt(q, k, v, pl, softmax_scale, st, None)
     if status is None:
         check_status(st, "mla_prompt_attention_fwd")

@@ -216,3 +216,26 @@ def test_same_result_every_time_and_in_a_graph():
         graph.replay()
         assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
     assert int(st) == 0
+
+
+def test_without_a_plan_the_status_is_the_callers():
+    """With a status word nothing waits: offsets that no plan can be made of set it (and give no output), and
+    plan and attention can be captured together."""
+    q, k, v, cu, _ = make([300, 20], [300, 20], 2, 1, 192, torch.bfloat16, 16)
+    q, k, v = q.cuda(), k.cuda(), v.cuda()
+    st = i32([0])
+    mla.prompt_attention(q, k, v, i32([0, 330, 320]), status=st)
+    assert int(st) == 5
+    with pytest.raises(mla.MlaError) as e:
+        mla.prompt_attention(q, k, v, i32([0, 330, 320]))
+    assert e.value.code == 5
+    want = mla.prompt_attention(q, k, v, i32(cu))
+    st, offsets = i32([0]), i32(cu)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = mla.prompt_attention(q, k, v, offsets, status=st)
+    graph.replay()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1]) and int(st) == 0
+    offsets.copy_(i32([0, 20, 320]))
+    graph.replay()
+    assert torch.equal(out[:20], mla.prompt_attention(q, k, v, i32([0, 20, 320]))[0][:20]) and int(st) == 0
