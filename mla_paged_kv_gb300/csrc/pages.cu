@@ -417,82 +417,141 @@ __global__ void __launch_bounds__(256) compact_apply_kernel(const PageState s, C
 
 // ------------------------------------------------------------------ copy
 
-constexpr int kCopyThreads = 256;
-constexpr int kCopyVec = 4;  // 16-byte loads a thread has in flight
+constexpr int kCopyThreads = 256;  // threads that copy a chunk together
+constexpr int kCopyVec = 4;        // 16-byte loads a thread has in flight
 constexpr int kCopyChunk = kCopyThreads * kCopyVec * 16;
-constexpr int kJudged = 32;
+// Lists of up to kLongList pairs: blocks of 256 threads that judge 2^7 pairs a
+// pass.  Longer ones: a block of 1024 an SM, 2^12 pairs, so that an eighth of the
+// blocks reads the list, and seldom twice.  (72 KB pages, short form and long: 16
+// pairs of 4 layers 5.4 and 5.9 us, 337 of 8 layers 67 and 69, 4096 of one 103 and 103,
+// 16384 392 and 390, 65536 1640 and 1526.  16-byte pages in the long form: 2^20 pairs 3.7
+// ms, 2^22 39, 2^24 543.)
+constexpr int kShortPairs = 7, kLongPairs = 12;
+constexpr int kLongGroups = 4, kLongList = 8192;
+
+// The targets of the pairs a block is judging, by open addressing: page
+// key[i] (-1: none) and the first pair of the whole list that has it as its
+// target, or -1 once a pair that reads it is met.
+template <int kLogPairs>
+struct Judge {
+  static constexpr int kPairs = 1 << kLogPairs;  // judged in one pass over the list
+  static constexpr int kSlots = 2 * kPairs;      // at most half of them taken: a search ends at a free one
+  int key[kSlots];
+  int first[kSlots];
+  int2 pair[kPairs];
+
+  static __device__ __forceinline__ int slot_of(int page) {
+    return static_cast<int>(static_cast<uint32_t>(page) * 2654435761u >> (31 - kLogPairs));
+  }
+
+  // The place of a page, or -1.
+  __device__ __forceinline__ int find(int page) const {
+    for (int i = slot_of(page);; i = (i + 1) & (kSlots - 1)) {
+      const int k = key[i];
+      if (k == page) return i;
+      if (k < 0) return -1;
+    }
+  }
+
+  // Read pairs from .. to - 1 (at most kPairs) and judge their targets against
+  // the list, by the whole block.
+  __device__ __forceinline__ void fill(const int2* pairs, int n, int from, int to) {
+    const int threads = blockDim.x;
+    __syncthreads();  // the pairs before are done with
+    for (int i = threadIdx.x; i < kSlots; i += threads) {
+      key[i] = -1;
+      first[i] = INT32_MAX;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < to - from; i += threads) {
+      const int2 m = pairs[from + i];
+      pair[i] = m;
+      if (m.y < 0) continue;
+      for (int k = slot_of(m.y);; k = (k + 1) & (kSlots - 1)) {
+        const int was = atomicCAS(&key[k], -1, m.y);
+        if (was == -1 || was == m.y) break;
+      }
+    }
+    __syncthreads();
+    constexpr int kAhead = 4;
+    for (int j0 = threadIdx.x; j0 < n; j0 += threads * kAhead) {
+      int2 o[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int j = j0 + i * threads;
+        o[i] = j < n ? pairs[j] : make_int2(-1, -1);
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int target = o[i].y < 0 ? -1 : find(o[i].y);
+        if (target >= 0) atomicMin(&first[target], j0 + i * threads);
+        const int source = o[i].x < 0 || o[i].x == o[i].y ? -1 : find(o[i].x);
+        if (source >= 0) atomicMin(&first[source], -1);
+      }
+    }
+    __syncthreads();
+  }
+};
 
 // Bound by HBM: each page is read and written once.  The blocks take equal
 // runs of (pair, layer, 16 KB chunk) items in that order, so that a block
-// judges a pair against the list once for all its layers and chunks, up to
-// kJudged pairs in one pass over the list.  (8 layers of 337 pages moved: 60 us, 0.99
-// of a plain copy.  One layer of 4096 pages 106 us, 16384 470, 65536 2.9 ms, where the
-// passes cost as much as the copy; with a pass a pair 103 us, 543 us and 7.2 ms.)
-__global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(uint8_t* pool, int layers, long long layer_stride,
-                                                                   int num_pages, long long page_bytes,
-                                                                   const int2* pairs, const int32_t* count, int n,
-                                                                   int32_t* status) {
+// judges a pair against the list once for all its layers and chunks, many
+// pairs in one pass over the list (two look-ups a pair of it).  kGroups groups
+// of 256 threads copy a chunk each.
+template <int kGroups, int kLogPairs>
+__global__ void __launch_bounds__(kCopyThreads* kGroups, kGroups == 1 ? 5 : 1)
+    copy_pages_kernel(uint8_t* pool, int layers, long long layer_stride, int num_pages, long long page_bytes,
+                      const int2* pairs, const int32_t* count, int n, int32_t* status) {
   if (count != nullptr) n = max(0, min(n, *count));
   const long long chunks = (page_bytes + kCopyChunk - 1) / kCopyChunk;
   const long long per_pair = chunks * layers;
   const long long items = per_pair * n;
   const long long lo = items * blockIdx.x / gridDim.x, hi = items * (blockIdx.x + 1) / gridDim.x;
-  const int last = static_cast<int>((hi - 1) / per_pair);  // this block's last pair (lo < hi)
-  __shared__ int2 judged[kJudged];
-  __shared__ unsigned refused;
-  int cur = -1, base = 0, end = 0;  // pairs base .. end - 1 are judged
-  bool go = false;
-  int2 m = make_int2(-1, -1);
-  for (long long it = lo; it < hi; ++it) {
-    const int pair = static_cast<int>(it / per_pair);
-    if (pair != cur) {
-      cur = pair;
-      if (pair >= end) {
-        base = pair;
-        end = min(last + 1, pair + kJudged);
-        __syncthreads();
-        if (static_cast<int>(threadIdx.x) < end - base) judged[threadIdx.x] = pairs[base + threadIdx.x];
-        if (threadIdx.x == 0) refused = 0u;
-        __syncthreads();
-        unsigned mine = 0u;
-#pragma unroll 4
-        for (int j = threadIdx.x; j < n; j += kCopyThreads) {
-          const int2 o = pairs[j];
-          for (int i = 0; i < end - base; ++i)
-            if (j != base + i &&
-                ((o.y == judged[i].y && j < base + i) || (o.x == judged[i].y && o.x != o.y)))
-              mine |= 1u << i;
+  if (lo >= hi) return;
+  const int last = static_cast<int>((hi - 1) / per_pair);  // this block's last pair
+  const int tid = threadIdx.x % kCopyThreads, group = threadIdx.x / kCopyThreads;
+  extern __shared__ __align__(16) uint8_t copy_smem[];
+  Judge<kLogPairs>& judge = *reinterpret_cast<Judge<kLogPairs>*>(copy_smem);
+  for (int from = static_cast<int>(lo / per_pair), to; from <= last; from = to) {
+    to = min(last + 1, from + judge.kPairs);
+    judge.fill(pairs, n, from, to);
+    const long long end = min(hi, to * per_pair);
+    int cur = -1;
+    bool go = false;
+    int2 m = make_int2(-1, -1);
+    for (long long it = max(lo, from * per_pair) + group; it < end;) {
+      const int pair = static_cast<int>(it / per_pair);
+      if (pair != cur) {
+        cur = pair;
+        m = judge.pair[pair - from];
+        go = !(m.x < 0 && m.y < 0) && m.x != m.y;
+        if (go && (m.x < 0 || m.y < 0 || m.x >= num_pages || m.y >= num_pages ||
+                   judge.first[judge.find(m.y)] < pair)) {
+          if (tid == 0) report(status, MLA_ERR_BAD_INDEX);
+          go = false;
         }
-        mine = __reduce_or_sync(0xffffffffu, mine);
-        if ((threadIdx.x & 31) == 0 && mine) atomicOr(&refused, mine);
-        __syncthreads();
       }
-      m = judged[pair - base];
-      go = !(m.x < 0 && m.y < 0) && m.x != m.y;
-      if (go && (m.x < 0 || m.y < 0 || m.x >= num_pages || m.y >= num_pages || (refused >> (pair - base) & 1u))) {
-        if (threadIdx.x == 0) report(status, MLA_ERR_BAD_INDEX);
-        go = false;
+      if (!go) {  // this group's first item of the next pair
+        it += ((pair + 1) * per_pair - it + kGroups - 1) / kGroups * kGroups;
+        continue;
       }
-    }
-    if (!go) {  // to the next pair
-      it = min(hi, static_cast<long long>(cur + 1) * per_pair) - 1;
-      continue;
-    }
-    const long long rest = it - static_cast<long long>(pair) * per_pair;
-    const long long layer = rest / chunks, chunk = rest - layer * chunks;
-    uint8_t* base = pool + layer * layer_stride;
-    const uint8_t* src = base + m.x * page_bytes;
-    uint8_t* dst = base + m.y * page_bytes;
-    uint4 v[kCopyVec];
+      const long long rest = it - pair * per_pair;
+      const long long layer = rest / chunks, chunk = rest - layer * chunks;
+      uint8_t* base = pool + layer * layer_stride;
+      const uint8_t* src = base + m.x * page_bytes;
+      uint8_t* dst = base + m.y * page_bytes;
+      uint4 v[kCopyVec];
 #pragma unroll
-    for (int i = 0; i < kCopyVec; ++i) {
-      const long long off = chunk * kCopyChunk + (i * kCopyThreads + static_cast<int>(threadIdx.x)) * 16ll;
-      if (off < page_bytes) v[i] = __ldcs(reinterpret_cast<const uint4*>(src + off));
-    }
+      for (int i = 0; i < kCopyVec; ++i) {
+        const long long off = chunk * kCopyChunk + (i * kCopyThreads + tid) * 16ll;
+        if (off < page_bytes) v[i] = __ldcs(reinterpret_cast<const uint4*>(src + off));
+      }
 #pragma unroll
-    for (int i = 0; i < kCopyVec; ++i) {
-      const long long off = chunk * kCopyChunk + (i * kCopyThreads + static_cast<int>(threadIdx.x)) * 16ll;
-      if (off < page_bytes) __stcs(reinterpret_cast<uint4*>(dst + off), v[i]);
+      for (int i = 0; i < kCopyVec; ++i) {
+        const long long off = chunk * kCopyChunk + (i * kCopyThreads + tid) * 16ll;
+        if (off < page_bytes) __stcs(reinterpret_cast<uint4*>(dst + off), v[i]);
+      }
+      it += kGroups;
     }
   }
 }
@@ -539,14 +598,26 @@ cudaError_t launch_compact(const PageState& s, int32_t* pairs, int32_t* count, v
   return cudaGetLastError();
 }
 
+cudaError_t copy_pages_setup() {
+  return cudaFuncSetAttribute(reinterpret_cast<const void*>(copy_pages_kernel<kLongGroups, kLongPairs>),
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Judge<kLongPairs>));
+}
+
 cudaError_t launch_copy_pages(void* pool, int layers, long long layer_stride, int num_pages, long long page_bytes,
                               const int32_t* pairs, const int32_t* count, int n, int32_t* status, int sms,
                               cudaStream_t st) {
   const long long items = (page_bytes + kCopyChunk - 1) / kCopyChunk * layers * n;
-  const long long most = 8ll * sms;  // 8 resident blocks of 256 threads an SM
-  copy_pages_kernel<<<static_cast<int>(items < most ? items : most), kCopyThreads, 0, st>>>(
-      static_cast<uint8_t*>(pool), layers, layer_stride, num_pages, page_bytes,
-      reinterpret_cast<const int2*>(pairs), count, n, status);
+  const bool many = n > kLongList;
+  const long long most = many ? sms : 8ll * sms;  // as many blocks as are resident
+  const int blocks = static_cast<int>(items < most ? items : most);
+  uint8_t* base = static_cast<uint8_t*>(pool);
+  const int2* list = reinterpret_cast<const int2*>(pairs);
+  if (many)
+    copy_pages_kernel<kLongGroups, kLongPairs><<<blocks, kCopyThreads * kLongGroups, sizeof(Judge<kLongPairs>), st>>>(
+        base, layers, layer_stride, num_pages, page_bytes, list, count, n, status);
+  else
+    copy_pages_kernel<1, kShortPairs><<<blocks, kCopyThreads, sizeof(Judge<kShortPairs>), st>>>(
+        base, layers, layer_stride, num_pages, page_bytes, list, count, n, status);
   return cudaGetLastError();
 }
 

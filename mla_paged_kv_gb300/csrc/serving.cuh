@@ -82,6 +82,7 @@ cudaError_t launch_fork(const PageState& s, const int32_t* parents, const int32_
 cudaError_t launch_free(const PageState& s, const int32_t* rows, int n, cudaStream_t st);
 size_t compact_workspace_bytes(int num_pages);
 cudaError_t launch_compact(const PageState& s, int32_t* pairs, int32_t* count, void* ws, cudaStream_t st);
+cudaError_t copy_pages_setup();  // once per device: shared-memory opt-in
 cudaError_t launch_copy_pages(void* pool, int layers, long long layer_stride, int num_pages, long long page_bytes,
                               const int32_t* pairs, const int32_t* count, int n, int32_t* status, int sms,
                               cudaStream_t st);

@@ -38,7 +38,8 @@ int check_list(const int32_t* a, const int32_t* b, int n) {
   return n > kMaxPageList ? MLA_ERR_UNSUPPORTED : MLA_OK;
 }
 
-int prompt_device(int* sms) {
+// device_ready, and this file's kernels set up for the current device (once).
+int serving_device(int* sms) {
   constexpr int kMaxDevices = 64;
   static bool done[kMaxDevices] = {};
   static std::mutex mu;
@@ -48,7 +49,7 @@ int prompt_device(int* sms) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MLA_ERR_CUDA;
   std::lock_guard<std::mutex> lock(mu);
   if (!done[dev]) {
-    if (prompt_setup() != cudaSuccess) {
+    if (prompt_setup() != cudaSuccess || copy_pages_setup() != cudaSuccess) {
       cudaGetLastError();
       return MLA_ERR_CUDA;
     }
@@ -241,7 +242,7 @@ int mla_cache_copy_pages(void* d_pool, int layers, long long layer_stride, int n
     return MLA_ERR_UNSUPPORTED;
   if (layers > 1 && layer_stride < page_bytes * num_pages) return MLA_ERR_INVALID_ARG;
   int sms = 0;
-  const int rc = device_ready(&sms);
+  const int rc = serving_device(&sms);
   if (rc != MLA_OK || n == 0) return rc;
   return launched(launch_copy_pages(d_pool, layers, layer_stride, num_pages, page_bytes, d_pairs, d_count, n,
                                     d_status, sms, to_stream(stream)));
@@ -291,7 +292,7 @@ int mla_prompt_attention_fwd(const void* d_q, long long q_token_stride, long lon
   const int tiles = prompt_plan_tiles(batch, total_q);
   if (static_cast<long long>(tiles) * h_q > (1 << 30)) return MLA_ERR_UNSUPPORTED;
   int sms = 0;
-  const int rc0 = prompt_device(&sms);
+  const int rc0 = serving_device(&sms);
   if (rc0 != MLA_OK || total_q == 0) return rc0;
   PromptParams p{};
   p.plan = static_cast<const int32_t*>(d_plan);

@@ -302,3 +302,49 @@ def test_fork_refuses_a_parent_with_a_bad_page(where, page):
     s.fork([0, 1, 0, 1], [3, 4, 5, 6])
     assert s.host.bad and s.host.lens == [200, 150, 0, 0, 150, 0, 150]
     assert s.host.table[3] == s.host.table[5] == [-1] * 6
+
+
+def test_copy_long_list():
+    """Hundreds of thousands of pairs, thousands of them refused: a target named before, a target that another
+    pair reads, the same pair again, pages outside the pool."""
+    n, pages = 300000, 700001
+    g = torch.Generator().manual_seed(8)
+    pairs = torch.randperm(pages, generator=g)[:2 * n].reshape(n, 2).int()
+    at = torch.randperm(n, generator=g)
+    pairs[at[:2000], 1] = pairs[at[5000:7000], 1]    # the later of two is refused
+    pairs[at[2000:4000], 1] = pairs[at[7000:9000], 0]
+    pairs[at[4000:4100]] = pairs[at[9000:9100]]
+    pairs[at[4100:4200], 1] = pages + 5
+    pairs[at[4200:4300], 0] = -3
+    pairs[at[4300:4400]] = -1
+    pairs[at[4400:4500], 0] = pairs[at[4400:4500], 1]  # a page onto itself: skipped, but it is the first of its target
+    x, y = pairs[:, 0].numpy().astype(np.int64), pairs[:, 1].numpy().astype(np.int64)
+    first = np.full(pages + 6, n)
+    np.minimum.at(first, y[y >= 0], np.nonzero(y >= 0)[0])
+    read = np.zeros(pages + 6, dtype=bool)
+    read[x[(x >= 0) & (x != y)]] = True
+    skip = ((x < 0) & (y < 0)) | (x == y)
+    good = (x >= 0) & (y >= 0) & (x < pages) & (y < pages)
+    good &= (first[np.maximum(y, 0)] == np.arange(n)) & ~read[np.maximum(y, 0)]
+    done = torch.from_numpy(np.nonzero(good & ~skip)[0])
+    assert 4000 < int((~good & ~skip).sum()) < 10000
+    pool = torch.randint(0, 256, (pages, 32), dtype=torch.uint8, generator=g).cuda()
+    want = pool.clone()
+    want[pairs[done, 1].long().cuda()] = pool[pairs[done, 0].long().cuda()]
+    status = i32([0])
+    mla.cache_copy_pages(pool, pairs.cuda(), status=status)
+    assert torch.equal(pool, want) and int(status) == BAD_INDEX
+
+
+def test_copy_judges_targets_that_fall_together():
+    """Targets at regular distances (the places of a judging table fill unevenly), each once, and read by none."""
+    for step in (1, 2, 64, 1024, 2048, 4096):
+        n = 3000
+        pages = n * step + n
+        pairs = torch.stack([torch.arange(n) + n * step, torch.arange(n) * step], 1).int()
+        pool = torch.randint(0, 256, (pages, 16), dtype=torch.uint8, device="cuda")
+        want = pool.clone()
+        want[pairs[:, 1].long().cuda()] = pool[pairs[:, 0].long().cuda()]
+        status = i32([0])
+        mla.cache_copy_pages(pool, pairs.cuda(), status=status)
+        assert torch.equal(pool, want) and int(status) == 0
