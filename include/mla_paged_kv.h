@@ -54,7 +54,8 @@ typedef enum {
   MLA_ERR_CUDA = 3,        /* a CUDA runtime call failed (launch, attribute query) */
   MLA_ERR_TIMEOUT = 4,     /* device: a pipeline wait exceeded its time budget */
   MLA_ERR_BAD_INDEX = 5,   /* device: block-table entry or sparse index outside the pool */
-  MLA_ERR_NO_PAGES = 6     /* device: the page pool ran out (mla_serving.h) */
+  MLA_ERR_NO_PAGES = 6,    /* device: the page pool ran out (mla_serving.h) */
+  MLA_ERR_STALE_PLAN = 7   /* device: the plan was made for other lengths (mla_serving.h) */
 } mla_status_t;
 
 /* Element types of query, cache and output tensors.  The values keep the

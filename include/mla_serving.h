@@ -217,6 +217,18 @@ int mla_shared_prefix_decode_fwd(const void* d_q, const void* d_kv, const int32_
                                  void* d_workspace, size_t workspace_bytes, void* d_out, int out_type, float* d_lse,
                                  int32_t* d_status, mla_stream_t stream);
 
+/* The same call for a program that holds the lengths: d_cache_seqlens int32
+ * [batch] is compared with the plan on the device, and MLA_ERR_STALE_PLAN is
+ * reported where a request's length is another than the plan's, or its entry of
+ * the last shared page is another page than the others'.  The results are those
+ * of the plan either way. */
+int mla_shared_prefix_decode_checked_fwd(const void* d_q, const void* d_kv, const int32_t* d_block_table,
+                                         int max_pages, int num_pages, int batch, int s_q, int h_q, int dtype,
+                                         int causal, float softmax_scale, const int32_t* d_cache_seqlens,
+                                         const void* d_plan, size_t plan_bytes, int num_parts, void* d_workspace,
+                                         size_t workspace_bytes, void* d_out, int out_type, float* d_lse,
+                                         int32_t* d_status, mla_stream_t stream);
+
 /* ---------------------------------------------------------------- one pointer */
 
 /* The calls above with their arguments, in order, as 8-byte words: pointers,
@@ -231,7 +243,8 @@ typedef enum {
   MLA_CALL_COMPACT = 4,
   MLA_CALL_COPY_PAGES = 5,
   MLA_CALL_PROMPT = 6,       /* mla_prompt_attention_fwd */
-  MLA_CALL_SHARED_PREFIX = 7 /* mla_shared_prefix_decode_fwd */
+  MLA_CALL_SHARED_PREFIX = 7, /* mla_shared_prefix_decode_fwd */
+  MLA_CALL_SHARED_PREFIX_CHECKED = 8
 } mla_call_t;
 int mla_serving_call(int op, const void* args, size_t bytes); /* bytes = 8 x the call's arguments */
 

@@ -311,6 +311,7 @@ struct SparseCall {
   int32_t* status = nullptr;
   mla_stream_t stream = nullptr;
   int kind = 0;  // the kernel's instance; 1: the stall-test one (mla_test_decode_timeout), 3: kWarp
+  const int32_t* live = nullptr;  // kind 3: see DecodeParams
 };
 
 int sparse_run(const SparseCall& c, bool combine) {
@@ -361,6 +362,8 @@ int sparse_run(const SparseCall& c, bool combine) {
   p.out_type = c.out_type;
   p.lse = c.lse;
   p.status = c.status;
+  p.live = c.live;
+  p.live_n = c.n_units;
   CUtensorMap qm;
   const int rc = encode_q_map(&qm, c.q, static_cast<long long>(c.n_units) * c.rows);
   if (rc != MLA_OK) return rc;
@@ -378,7 +381,7 @@ int fp8_record_splits(const void* d_q, const void* d_kv, const int32_t* d_block_
                       const int32_t* d_cache_seqlens, int batch, int s_q, int h_q, int h_kv, int causal,
                       float softmax_scale, const int32_t* d_sched, const int32_t* d_split_offset, int num_parts,
                       void* d_workspace, size_t workspace_bytes, void* d_out, int out_type, float* d_lse,
-                      int32_t* d_status, mla_stream_t stream, int kind) {
+                      int32_t* d_status, mla_stream_t stream, int kind, const int32_t* live = nullptr) {
   if (!d_block_table || !d_cache_seqlens || max_pages < 1 || batch < 1 || s_q < 1 || h_q < 1)
     return MLA_ERR_INVALID_ARG;
   if (h_kv != 1) return MLA_ERR_UNSUPPORTED;
@@ -411,6 +414,7 @@ int fp8_record_splits(const void* d_q, const void* d_kv, const int32_t* d_block_
   c.status = d_status;
   c.stream = stream;
   c.kind = kind;
+  c.live = live;
   return sparse_run(c, false);
 }
 
@@ -433,8 +437,13 @@ int launch_shared(const SharedLaunch& c, cudaStream_t stream) {
   p.blocks_per_group = 1;
   p.scale_log2 = c.scale_log2;
   p.block_table = c.block_table;
+  p.max_pages = c.max_pages;
   p.num_pages = c.num_pages;
   p.units = c.units;
+  p.live = c.live;
+  p.live_n = c.batch;
+  p.live_per = ceil_div_i(c.s_q * c.h_q, MLA_ROWS_PER_BLOCK);
+  p.live_u0 = c.n_units - c.batch * p.live_per;
   p.sched = c.sched;
   p.split_offset = c.split_offset;
   p.num_parts = c.num_parts;
@@ -463,13 +472,13 @@ int launch_shared(const SharedLaunch& c, cudaStream_t stream) {
 // blocks alone, with the kWarp instances.  (16 requests x 128 heads, 16884 keys:
 // 71 us; the V-ring instance that mla_decode_fwd takes there 86.)
 int decode_full_blocks(const void* q, const void* kv, const int32_t* block_table, int max_pages, int num_pages,
-                       const int32_t* lengths, int batch, int s_q, int h_q, int dtype, int causal, float scale,
-                       const int32_t* sched, const int32_t* split_offset, int num_parts, void* ws, size_t ws_bytes,
+                       const int32_t* lengths, const int32_t* live, int batch, int s_q, int h_q, int dtype,
+                       int causal, float scale, const int32_t* sched, const int32_t* split_offset, int num_parts, void* ws, size_t ws_bytes,
                        void* out, int out_type, float* lse, int32_t* status, cudaStream_t stream) {
   if (dtype == MLA_DTYPE_FP8_RECORD) {
     const int rc = fp8_record_splits(q, kv, block_table, max_pages, num_pages, lengths, batch, s_q, h_q, 1, causal,
                                      scale, sched, split_offset, num_parts, ws, ws_bytes, out, out_type, lse, status,
-                                     reinterpret_cast<mla_stream_t>(stream), 3);
+                                     reinterpret_cast<mla_stream_t>(stream), 3, live);
     if (rc != MLA_OK) return rc;
   } else {
     DecodeParams p;
@@ -478,6 +487,8 @@ int decode_full_blocks(const void* q, const void* kv, const int32_t* block_table
                                  scale, sched, split_offset, num_parts, ws, ws_bytes, out, out_type, lse, status, &p,
                                  &qm, &km, &sm, &rm);
     if (rc != MLA_OK) return rc;
+    p.live = live;
+    p.live_n = batch;
     if (launch_dense(qm, km, sm, rm, p, num_parts, dtype == MLA_DTYPE_FP16 ? 8 : 7, stream) != cudaSuccess)
       return MLA_ERR_CUDA;
   }
@@ -520,6 +531,7 @@ const char* mla_status_string(int status) {
     case MLA_ERR_TIMEOUT: return "MLA_ERR_TIMEOUT: a device pipeline wait ran out of time";
     case MLA_ERR_BAD_INDEX: return "MLA_ERR_BAD_INDEX: block-table entry or sparse index outside the pool";
     case MLA_ERR_NO_PAGES: return "MLA_ERR_NO_PAGES: no free pages left in the pool";
+    case MLA_ERR_STALE_PLAN: return "MLA_ERR_STALE_PLAN: the plan was made for other lengths";
     default: return "unknown mla status";
   }
 }

@@ -70,6 +70,11 @@ struct DecodeParams {
   // shared-prefix plan (kShared instances): what each unit is, kUnitInts int32
   // each (SharedUnit); rows = 128, a unit's rows being its own count
   const int32_t* units;
+  // kWarp instances: the caller's lengths [live_n], to be compared with those of
+  // the plan (check_plan), or NULL; under a shared-prefix plan request b's first
+  // own unit is live_u0 + b * live_per
+  const int32_t* live;
+  int live_n, live_u0, live_per;
   // schedule
   const int32_t* sched;
   const int32_t* split_offset;
@@ -86,6 +91,29 @@ struct DecodeParams {
 __device__ __forceinline__ SharedUnit load_unit(const DecodeParams& p, int u) {
   const int32_t* e = p.units + u * kUnitInts;
   return SharedUnit{e[0], e[1], e[2], e[3], e[4]};
+}
+
+// Whether the plan is that of the caller's lengths (and, under a shared prefix,
+// each request that takes part still ends it on the page that they share), by
+// warps that have loaded their last tile; the call's results are those of the
+// plan either way.  (In the softmax warps, before their first tile, it took 3% of
+// the kernel.)
+template <bool kShared>
+__device__ __forceinline__ void check_plan(const DecodeParams& p, int thread, int threads) {
+  if (p.live == nullptr) return;
+  for (int b = thread; b < p.live_n; b += threads) {
+    bool same;
+    if constexpr (kShared) {
+      const int u = p.live_u0 + b * p.live_per;
+      const SharedUnit su = load_unit(p, u), front = load_unit(p, 0);
+      const int skip = su.table_off - b * p.max_pages;  // shared pages
+      same = p.lengths[u] + skip * kTile == max(p.live[b], 0) &&
+             (skip == 0 || p.block_table[su.table_off - 1] == p.block_table[front.table_off + skip - 1]);
+    } else {
+      same = p.lengths[b] == p.live[b];
+    }
+    if (!same) report(p.status, MLA_ERR_STALE_PLAN);
+  }
 }
 
 }  // namespace mla

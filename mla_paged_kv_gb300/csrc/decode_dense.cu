@@ -696,6 +696,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (qb_issued[sl] > 0) mbar_wait(&bars[QB_FULL + sl], (qb_issued[sl] - 1) & 1, nullptr, kWaitNs);
     }
     __syncwarp();
+    if constexpr (kWarp) check_plan<kShared>(p, blockIdx.x * 32 + lane, gridDim.x * 32);
   } else if (warp == kWarpPV) {
     // ------------------------------------------------------------ P V issuer
     // P V of every tile in order, from the own or the received P; issued by a

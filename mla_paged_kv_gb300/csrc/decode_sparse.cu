@@ -558,6 +558,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (!ok) set_abort(abort_flag, p.status, MLA_ERR_TIMEOUT);
     // no TMA write may land after this CTA exits
     if (ptid == 0 && q_issued > 0) mbar_wait(&bars[Q_FULL], (q_issued - 1) & 1, nullptr, kWaitNs);
+    if constexpr (kWarp) {
+      constexpr int kN = 32 * kProducerWarps;
+      check_plan<kShared>(p, blockIdx.x * kN + ptid, gridDim.x * kN);
+    }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
     if (kWarp || lane == 0) {

@@ -21,7 +21,8 @@ struct SharedLaunch {
   const void* q;
   const void* kv;
   long long total_rows;  // batch * s_q * h_q
-  int num_pages, max_pages, n_units, s_q, h_q, num_parts;
+  const int32_t* live;   // the caller's lengths, to be compared with the plan's, or NULL
+  int batch, num_pages, max_pages, n_units, s_q, h_q, num_parts;
   int dtype;  // MLA_DTYPE_BF16, _FP16 or _FP8_RECORD
   float scale_log2;
   const int32_t *block_table, *units, *lengths, *sched, *split_offset;
@@ -30,9 +31,10 @@ struct SharedLaunch {
 };
 int launch_shared(const SharedLaunch& c, cudaStream_t stream);
 int decode_full_blocks(const void* q, const void* kv, const int32_t* block_table, int max_pages, int num_pages,
-                       const int32_t* lengths, int batch, int s_q, int h_q, int dtype, int causal, float scale,
-                       const int32_t* sched, const int32_t* split_offset, int num_parts, void* ws, size_t ws_bytes,
-                       void* out, int out_type, float* lse, int32_t* status, cudaStream_t stream);
+                       const int32_t* lengths, const int32_t* live, int batch, int s_q, int h_q, int dtype,
+                       int causal, float scale, const int32_t* sched, const int32_t* split_offset, int num_parts,
+                       void* ws, size_t ws_bytes, void* out, int out_type, float* lse, int32_t* status,
+                       cudaStream_t stream);
 cudaError_t launch_plan(const int32_t* lengths, int n_units, int num_parts, int32_t* sched, int32_t* split_offset,
                         cudaStream_t stream);
 
@@ -92,6 +94,8 @@ struct PromptParams {
   int max_tiles;        // tiles the plan has room for
   int h_q, group;       // query heads, query heads per key head
   int total_q;
+  int batch;
+  const int32_t *cu_q, *cu_k;  // the caller's offsets, to be compared with the plan's, or NULL
   float scale_log2;
   void* out;            // [total_q, h_q, 128]
   float* lse;           // [total_q, h_q]

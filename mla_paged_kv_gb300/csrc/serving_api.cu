@@ -127,6 +127,68 @@ int shared_sizes(int batch, int s_q, int h_q, int num_parts, SharedSizes* z) {
   return MLA_OK;
 }
 
+// mla_shared_prefix_decode_fwd, with lengths to be compared with the plan's or NULL.
+int shared_decode(const void* d_q, const void* d_kv, const int32_t* d_block_table, int max_pages, int num_pages,
+                  int batch, int s_q, int h_q, int dtype, int causal, float softmax_scale, const int32_t* live,
+                  const void* d_plan, size_t plan_bytes, int num_parts, void* d_workspace, size_t workspace_bytes,
+                  void* d_out, int out_type, float* d_lse, int32_t* d_status, mla_stream_t stream) {
+  if (!d_q || !d_kv || !d_block_table || !d_plan || !d_workspace || !d_out || !d_lse || !d_status)
+    return MLA_ERR_INVALID_ARG;
+  if (max_pages < 1 || num_pages < 1) return MLA_ERR_INVALID_ARG;
+  if (dtype != MLA_DTYPE_BF16 && dtype != MLA_DTYPE_FP16 && dtype != MLA_DTYPE_FP8_RECORD)
+    return MLA_ERR_INVALID_ARG;
+  if (out_type != MLA_DTYPE_BF16 && out_type != MLA_DTYPE_FP32 && out_type != MLA_DTYPE_FP16)
+    return MLA_ERR_INVALID_ARG;
+  if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.f)) return MLA_ERR_INVALID_ARG;
+  if (!aligned(d_q, 16) || !aligned(d_kv, 16) || !aligned(d_plan, 16) || !aligned(d_workspace, 16) ||
+      !aligned(d_out, 16) || !aligned(d_block_table, 4) || !aligned(d_lse, 4) || !aligned(live, 4) || !aligned(d_status, 4))
+    return MLA_ERR_INVALID_ARG;
+  SharedSizes z;
+  int rc = shared_sizes(batch, s_q, h_q, num_parts, &z);
+  if (rc != MLA_OK) return rc;
+  if (max_pages > kMaxRowPages || static_cast<long long>(batch) * max_pages > kMaxInt ||
+      static_cast<long long>(num_pages) * MLA_PAGE_SIZE > kMaxInt)
+    return MLA_ERR_UNSUPPORTED;
+  if (plan_bytes < z.plan_bytes || workspace_bytes < z.ws_bytes) return MLA_ERR_INVALID_ARG;
+  int sms = 0;
+  rc = device_ready(&sms);
+  if (rc != MLA_OK) return rc;
+  const char* plan = static_cast<const char*>(d_plan);
+  if (!z.share)
+    return decode_full_blocks(d_q, d_kv, d_block_table, max_pages, num_pages,
+                              reinterpret_cast<const int32_t*>(plan + z.lengths_off), live, batch, s_q, h_q, dtype, causal,
+                              softmax_scale, reinterpret_cast<const int32_t*>(plan + z.sched_off),
+                              reinterpret_cast<const int32_t*>(plan + z.offset_off), num_parts, d_workspace,
+                              workspace_bytes, d_out, out_type, d_lse, d_status, to_stream(stream));
+  SharedLaunch c{};
+  c.q = d_q;
+  c.kv = d_kv;
+  c.total_rows = z.rows;
+  c.live = live;
+  c.batch = batch;
+  c.num_pages = num_pages;
+  c.n_units = z.units;
+  c.s_q = s_q;
+  c.h_q = h_q;
+  c.num_parts = num_parts;
+  c.max_pages = max_pages;
+  c.dtype = dtype;
+  c.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * 1.4426950408889634);
+  c.block_table = d_block_table;
+  c.units = reinterpret_cast<const int32_t*>(plan);
+  c.lengths = reinterpret_cast<const int32_t*>(plan + z.lengths_off);
+  c.split_offset = reinterpret_cast<const int32_t*>(plan + z.offset_off);
+  c.sched = reinterpret_cast<const int32_t*>(plan + z.sched_off);
+  c.o_accum = static_cast<float*>(d_workspace);
+  c.lse_accum = reinterpret_cast<float*>(static_cast<char*>(d_workspace) + z.lse_off);
+  c.status = d_status;
+  const cudaStream_t st = to_stream(stream);
+  rc = launch_shared(c, st);
+  if (rc != MLA_OK) return rc;
+  return launched(launch_shared_combine(c.o_accum, c.lse_accum, c.units, c.split_offset, batch, s_q * h_q, d_out,
+                                        out_type, d_lse, sms, st));
+}
+
 }  // namespace
 
 extern "C" {
@@ -364,68 +426,29 @@ int mla_shared_prefix_get_plan(const int32_t* d_block_table, int max_pages, cons
 
 int mla_shared_prefix_decode_fwd(const void* d_q, const void* d_kv, const int32_t* d_block_table, int max_pages,
                                  int num_pages, int batch, int s_q, int h_q, int dtype, int causal,
-                                 float softmax_scale,
-                                 const void* d_plan, size_t plan_bytes, int num_parts, void* d_workspace,
-                                 size_t workspace_bytes, void* d_out, int out_type, float* d_lse, int32_t* d_status,
-                                 mla_stream_t stream) {
-  if (!d_q || !d_kv || !d_block_table || !d_plan || !d_workspace || !d_out || !d_lse || !d_status)
-    return MLA_ERR_INVALID_ARG;
-  if (max_pages < 1 || num_pages < 1) return MLA_ERR_INVALID_ARG;
-  if (dtype != MLA_DTYPE_BF16 && dtype != MLA_DTYPE_FP16 && dtype != MLA_DTYPE_FP8_RECORD)
-    return MLA_ERR_INVALID_ARG;
-  if (out_type != MLA_DTYPE_BF16 && out_type != MLA_DTYPE_FP32 && out_type != MLA_DTYPE_FP16)
-    return MLA_ERR_INVALID_ARG;
-  if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.f)) return MLA_ERR_INVALID_ARG;
-  if (!aligned(d_q, 16) || !aligned(d_kv, 16) || !aligned(d_plan, 16) || !aligned(d_workspace, 16) ||
-      !aligned(d_out, 16) || !aligned(d_block_table, 4) || !aligned(d_lse, 4) || !aligned(d_status, 4))
-    return MLA_ERR_INVALID_ARG;
-  SharedSizes z;
-  int rc = shared_sizes(batch, s_q, h_q, num_parts, &z);
-  if (rc != MLA_OK) return rc;
-  if (max_pages > kMaxRowPages || static_cast<long long>(batch) * max_pages > kMaxInt ||
-      static_cast<long long>(num_pages) * MLA_PAGE_SIZE > kMaxInt)
-    return MLA_ERR_UNSUPPORTED;
-  if (plan_bytes < z.plan_bytes || workspace_bytes < z.ws_bytes) return MLA_ERR_INVALID_ARG;
-  int sms = 0;
-  rc = device_ready(&sms);
-  if (rc != MLA_OK) return rc;
-  const char* plan = static_cast<const char*>(d_plan);
-  if (!z.share)
-    return decode_full_blocks(d_q, d_kv, d_block_table, max_pages, num_pages,
-                              reinterpret_cast<const int32_t*>(plan + z.lengths_off), batch, s_q, h_q, dtype, causal,
-                              softmax_scale, reinterpret_cast<const int32_t*>(plan + z.sched_off),
-                              reinterpret_cast<const int32_t*>(plan + z.offset_off), num_parts, d_workspace,
-                              workspace_bytes, d_out, out_type, d_lse, d_status, to_stream(stream));
-  SharedLaunch c{};
-  c.q = d_q;
-  c.kv = d_kv;
-  c.total_rows = z.rows;
-  c.num_pages = num_pages;
-  c.n_units = z.units;
-  c.s_q = s_q;
-  c.h_q = h_q;
-  c.num_parts = num_parts;
-  c.max_pages = max_pages;
-  c.dtype = dtype;
-  c.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * 1.4426950408889634);
-  c.block_table = d_block_table;
-  c.units = reinterpret_cast<const int32_t*>(plan);
-  c.lengths = reinterpret_cast<const int32_t*>(plan + z.lengths_off);
-  c.split_offset = reinterpret_cast<const int32_t*>(plan + z.offset_off);
-  c.sched = reinterpret_cast<const int32_t*>(plan + z.sched_off);
-  c.o_accum = static_cast<float*>(d_workspace);
-  c.lse_accum = reinterpret_cast<float*>(static_cast<char*>(d_workspace) + z.lse_off);
-  c.status = d_status;
-  const cudaStream_t st = to_stream(stream);
-  rc = launch_shared(c, st);
-  if (rc != MLA_OK) return rc;
-  return launched(launch_shared_combine(c.o_accum, c.lse_accum, c.units, c.split_offset, batch, s_q * h_q, d_out,
-                                        out_type, d_lse, sms, st));
+                                 float softmax_scale, const void* d_plan, size_t plan_bytes, int num_parts,
+                                 void* d_workspace, size_t workspace_bytes, void* d_out, int out_type, float* d_lse,
+                                 int32_t* d_status, mla_stream_t stream) {
+  return shared_decode(d_q, d_kv, d_block_table, max_pages, num_pages, batch, s_q, h_q, dtype, causal, softmax_scale,
+                       nullptr, d_plan, plan_bytes, num_parts, d_workspace, workspace_bytes, d_out, out_type, d_lse,
+                       d_status, stream);
+}
+
+int mla_shared_prefix_decode_checked_fwd(const void* d_q, const void* d_kv, const int32_t* d_block_table,
+                                         int max_pages, int num_pages, int batch, int s_q, int h_q, int dtype,
+                                         int causal, float softmax_scale, const int32_t* d_cache_seqlens,
+                                         const void* d_plan, size_t plan_bytes, int num_parts, void* d_workspace,
+                                         size_t workspace_bytes, void* d_out, int out_type, float* d_lse,
+                                         int32_t* d_status, mla_stream_t stream) {
+  if (!d_cache_seqlens) return MLA_ERR_INVALID_ARG;
+  return shared_decode(d_q, d_kv, d_block_table, max_pages, num_pages, batch, s_q, h_q, dtype, causal, softmax_scale,
+                       d_cache_seqlens, d_plan, plan_bytes, num_parts, d_workspace, workspace_bytes, d_out, out_type,
+                       d_lse, d_status, stream);
 }
 
 int mla_serving_call(int op, const void* args, size_t bytes) {
-  constexpr size_t kWords[] = {22, 11, 12, 10, 12, 10, 23, 21};  // by mla_call_t
-  if (!args || op < 0 || op > MLA_CALL_SHARED_PREFIX || bytes != 8 * kWords[op]) return MLA_ERR_INVALID_ARG;
+  constexpr size_t kWords[] = {22, 11, 12, 10, 12, 10, 23, 21, 22};  // by mla_call_t
+  if (!args || op < 0 || op > MLA_CALL_SHARED_PREFIX_CHECKED || bytes != 8 * kWords[op]) return MLA_ERR_INVALID_ARG;
   const char* a = static_cast<const char*>(args);
   auto word = [&](int i) {
     int64_t v;
@@ -468,6 +491,10 @@ int mla_serving_call(int op, const void* args, size_t bytes) {
       return mla_shared_prefix_decode_fwd(P(0), P(1), N(2), I(3), I(4), I(5), I(6), I(7), I(8), I(9), F(10), P(11),
                                           static_cast<size_t>(word(12)), I(13), P(14), static_cast<size_t>(word(15)),
                                           P(16), I(17), R(18), N(19), S(20));
+    case MLA_CALL_SHARED_PREFIX_CHECKED:
+      return mla_shared_prefix_decode_checked_fwd(P(0), P(1), N(2), I(3), I(4), I(5), I(6), I(7), I(8), I(9), F(10),
+                                                  N(11), P(12), static_cast<size_t>(word(13)), I(14), P(15),
+                                                  static_cast<size_t>(word(16)), P(17), I(18), R(19), N(20), S(21));
     default: return MLA_ERR_INVALID_ARG;
   }
 }

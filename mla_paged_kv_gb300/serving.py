@@ -47,6 +47,8 @@ SERVING_SIGS = {
     "mla_shared_prefix_get_plan": (_I, [_P, _I, _P, _I, _I, _I, _I, _I, _P, _SZ, _P]),
     "mla_shared_prefix_decode_fwd": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _SZ, _I, _P, _SZ, _P, _I,
                                           _P, _P, _P]),
+    "mla_shared_prefix_decode_checked_fwd": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _SZ, _I, _P, _SZ,
+                                                  _P, _I, _P, _P, _P]),
     "mla_serving_call": (_I, [_I, ctypes.c_char_p, _SZ]),
 }
 SERVING_SYMBOLS = tuple(SERVING_SIGS)
@@ -99,7 +101,7 @@ def _words(op, layout):
 
 _APPEND, _GROW, _FORK, _FREE = _words(0, "15qd6q"), _words(1, "11q"), _words(2, "12q"), _words(3, "10q")
 _COMPACT, _COPY_PAGES, _PROMPT = _words(4, "12q"), _words(5, "10q"), _words(6, "16qd6q")
-_SHARED_PREFIX = _words(7, "10qd10q")
+_SHARED_PREFIX, _SHARED_PREFIX_CHECKED = _words(7, "10qd10q"), _words(8, "10qd11q")
 
 
 def _call(op, name, *args):
@@ -481,8 +483,10 @@ def mla_shared_prefix_get_plan(block_table, cache_seqlens, s_q, h_q, causal, num
         _p(plan, _UINT8, 1, dev, "plan"), plan.shape[0], _q(stream, dev)), "mla_shared_prefix_get_plan")
 
 
-def _shared_prefix(q, kv, block_table, pl, softmax_scale, status, stream, out=None, lse=None, out_dtype=None):
-    """The checks and the call of mla_shared_prefix_decode_fwd; allocates out and lse if not given."""
+def _shared_prefix(q, kv, block_table, pl, softmax_scale, status, stream, out=None, lse=None, out_dtype=None,
+                   cache_seqlens=None):
+    """The checks and the call of mla_shared_prefix_decode_fwd (with lengths, _checked_fwd); allocates out and lse
+    if not given."""
     dt = q.dtype
     code = _DTYPE_CODE16.get(dt)
     fp8 = kv.dtype is _UINT8
@@ -512,9 +516,17 @@ def _shared_prefix(q, kv, block_table, pl, softmax_scale, status, stream, out=No
         out_ptr, lse_ptr = _p(out, out_dtype, 4, dev, "out"), _p(lse, _FP32, 3, dev, "lse")
         if out.shape != (B, s_q, h_q, 512) or lse.shape != (B, s_q, h_q):
             raise ValueError("out must be [B, s_q, h_q, 512] and lse [B, s_q, h_q]")
-    _call(_SHARED_PREFIX, "mla_shared_prefix_decode_fwd", q_ptr, kv_ptr, table_ptr, max_pages, pages, B, s_q, h_q,
-          DTYPE_FP8_RECORD if fp8 else code, 1 if pl.causal else 0, softmax_scale, plan_ptr, plan.shape[0],
-          pl.num_parts, ws_ptr, ws.shape[0], out_ptr, _DTYPE_CODE[out_dtype], lse_ptr, st, queue)
+    if cache_seqlens is None:
+        _call(_SHARED_PREFIX, "mla_shared_prefix_decode_fwd", q_ptr, kv_ptr, table_ptr, max_pages, pages, B, s_q, h_q,
+              DTYPE_FP8_RECORD if fp8 else code, 1 if pl.causal else 0, softmax_scale, plan_ptr, plan.shape[0],
+              pl.num_parts, ws_ptr, ws.shape[0], out_ptr, _DTYPE_CODE[out_dtype], lse_ptr, st, queue)
+        return out, lse
+    lens_ptr = _p(cache_seqlens, _INT32, 1, dev, "cache_seqlens")
+    if cache_seqlens.shape[0] != B:
+        raise ValueError("block_table / cache_seqlens batch mismatch")
+    _call(_SHARED_PREFIX_CHECKED, "mla_shared_prefix_decode_checked_fwd", q_ptr, kv_ptr, table_ptr, max_pages, pages,
+          B, s_q, h_q, DTYPE_FP8_RECORD if fp8 else code, 1 if pl.causal else 0, softmax_scale, lens_ptr, plan_ptr,
+          plan.shape[0], pl.num_parts, ws_ptr, ws.shape[0], out_ptr, _DTYPE_CODE[out_dtype], lse_ptr, st, queue)
     return out, lse
 
 
@@ -524,6 +536,13 @@ def mla_shared_prefix_decode_fwd(q, kv, block_table, pl, out, lse, status, softm
     this block table; out [B, s_q, h_q, 512] bf16, fp16 or fp32, lse fp32
     [B, s_q, h_q]."""
     _shared_prefix(q, kv, block_table, pl, softmax_scale, status, stream, out, lse)
+
+
+def mla_shared_prefix_decode_checked_fwd(q, kv, block_table, cache_seqlens, pl, out, lse, status,
+                                         softmax_scale=1.0 / 24.0, stream=None):
+    """mla_shared_prefix_decode_fwd that also compares the lengths [B] with the plan's on the device: another
+    length, or a request that no longer ends its shared pages on the shared one, is MLA_ERR_STALE_PLAN in status."""
+    _shared_prefix(q, kv, block_table, pl, softmax_scale, status, stream, out, lse, cache_seqlens=cache_seqlens)
 
 
 def plan_shared_prefix(block_table, cache_seqlens, s_q, h_q, causal=False, num_parts=None):
@@ -542,14 +561,20 @@ def plan_shared_prefix(block_table, cache_seqlens, s_q, h_q, causal=False, num_p
 
 def shared_prefix_decode(q, kv, block_table, cache_seqlens, causal=False, softmax_scale=None, out_fp32=False,
                          pl=None, status=None):
-    """Dense decode that attends the pages all requests share once; returns (out, lse)."""
+    """Dense decode that attends the pages all requests share once; returns (out, lse).
+
+    A plan holds the lengths it was made for.  With pl they are compared with cache_seqlens on the device, and a
+    plan of other lengths (rows that have grown since, say) is MLA_ERR_STALE_PLAN."""
+    lens = None  # a plan made here is that of the lengths
     if pl is None:
         pl = plan_shared_prefix(block_table, cache_seqlens, q.shape[1], q.shape[2], causal)
     elif pl.causal != bool(causal):
         raise ValueError("the plan was made with another causal setting")
+    else:
+        lens = cache_seqlens
     st = _status(status, q)
     out, lse = _shared_prefix(q, kv, block_table, pl, 1.0 / 24.0 if softmax_scale is None else softmax_scale, st, None,
-                              out_dtype=_FP32 if out_fp32 else q.dtype)
+                              out_dtype=_FP32 if out_fp32 else q.dtype, cache_seqlens=lens)
     if status is None:
         check_status(st, "mla_shared_prefix_decode_fwd")
     return out, lse

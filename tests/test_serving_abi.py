@@ -238,3 +238,37 @@ def test_prompt_oracle_against_torch_attention():
             q[qs].transpose(0, 1), k[ks].transpose(0, 1).expand(2, -1, -1), v[ks].transpose(0, 1).expand(2, -1, -1),
             attn_mask=mask, scale=0.1)
         np.testing.assert_allclose(out[qs], want.transpose(0, 1).numpy(), rtol=0, atol=1e-12)
+
+
+# ---------------------------------------------------------------- calls that compare their plan
+
+
+def checked(base, names, at):
+    """The arguments of a call with further pointers before `at`."""
+    out = {}
+    for k, v in base.items():
+        if k == at:
+            out.update({n: P for n in names})
+        out[k] = v
+    return out
+
+
+CHECKED = [(8, "mla_shared_prefix_decode_checked_fwd", checked(SDEC, ["lens"], "plan"), "lens")]
+
+
+@pytest.mark.parametrize("op,name,base,own", CHECKED)
+def test_checked_calls_refuse_as_the_plain_ones(op, name, base, own):
+    lib = mla.load_library()
+    for change in ({own: N}, {own: ODD}, dict(q=N), dict(plan=N), dict(status=N), dict(batch=0), dict(scale=-1.0)):
+        args = {**base, **change}
+        assert getattr(lib, name)(*args.values()) == INVALID
+        values = [v.value or 0 if isinstance(v, ctypes.c_void_p) else v for v in args.values()]
+        words = b"".join(np.float64(v).tobytes() if isinstance(v, float) else np.int64(v).tobytes() for v in values)
+        assert lib.mla_serving_call(op, words, len(words)) == INVALID
+        assert lib.mla_serving_call(op, words, len(words) - 8) == INVALID
+    assert lib.mla_serving_call(CHECKED[-1][0] + 1, b"", 0) == INVALID
+
+
+def test_status_words_have_names():
+    for code, name in ((6, "MLA_ERR_NO_PAGES"), (7, "MLA_ERR_STALE_PLAN")):
+        assert mla.mla_status_string(code).startswith(name)

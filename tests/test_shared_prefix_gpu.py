@@ -346,3 +346,64 @@ def test_thousands_of_calls(b, h_q, head, fp8):
         if i % 50 == 49:
             assert int(status) == 0
     assert bad.tolist() == [0, 0]
+
+
+STALE_PLAN = 7
+
+
+@pytest.mark.parametrize("h_q,fp8,dtype", [(16, False, torch.bfloat16), (16, False, torch.float16),
+                                           (128, False, torch.bfloat16), (128, False, torch.float16),
+                                           (16, True, torch.bfloat16), (128, True, torch.bfloat16)])
+def test_a_plan_of_other_lengths_is_reported(h_q, fp8, dtype):
+    """A plan holds its lengths: with others, longer, shorter or newly empty or live, the call says so (and
+    answers by the plan); with the same ones it is silent."""
+    c = Case(4, [64, 100, 5, 0, 200], 1, h_q, seed=19, fp8=fp8, dtype=dtype)
+    c.lens[3] = 0
+    q, kv, table, lens = c.q.cuda(), c.kv.cuda(), torch.from_numpy(c.table).cuda(), i32(c.lens)
+    pl = mla.plan_shared_prefix(table, lens, 1, h_q)
+    st = i32([0])
+    want = mla.shared_prefix_decode(q, kv, table, lens, pl=pl, status=st)
+    assert int(st) == 0
+    for b, n in ((0, c.lens[0] + 1), (1, c.lens[1] - 1), (2, 0), (3, 1), (4, c.lens[4] + 640), (4, 64)):
+        other = list(c.lens)
+        other[b] = n
+        with pytest.raises(mla.MlaError) as e:
+            mla.shared_prefix_decode(q, kv, table, i32(other), pl=pl)
+        assert e.value.code == STALE_PLAN
+        st = i32([0])
+        out, lse = mla.shared_prefix_decode(q, kv, table, i32(other), pl=pl, status=st)
+        assert int(st) == STALE_PLAN and torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    # rows that grow in place, as mla_cache_grow lets them
+    lens[1] += 1
+    with pytest.raises(mla.MlaError):
+        mla.shared_prefix_decode(q, kv, table, lens, pl=pl)
+    mla.shared_prefix_decode(q, kv, table, lens)  # a plan of its own: fine
+    lens[1] -= 1
+    mla.shared_prefix_decode(q, kv, table, lens, pl=pl)
+    if h_q == 16:  # another request of the same length took the slot: it does not start with the prefix
+        table[1, :4] = table[1, 4]
+        with pytest.raises(mla.MlaError) as e:
+            mla.shared_prefix_decode(q, kv, table, lens, pl=pl)
+        assert e.value.code == STALE_PLAN
+
+
+def test_lengths_of_a_given_plan_are_checked_tensors():
+    c = Case(4, [64, 100], 1, 16, seed=20)
+    q, kv, table, lens = c.q.cuda(), c.kv.cuda(), torch.from_numpy(c.table).cuda(), i32(c.lens)
+    pl = mla.plan_shared_prefix(table, lens, 1, 16)
+    for bad, error in ((lens.long(), TypeError), (lens[:1], ValueError), (lens.cpu(), ValueError)):
+        with pytest.raises(error):
+            mla.shared_prefix_decode(q, kv, table, bad, pl=pl)
+
+
+def test_many_lengths_are_all_compared():
+    """More requests than one CTA has threads: the last one's length."""
+    c = Case(1, [(i * 13) % 90 for i in range(2000)], 1, 2, seed=21)
+    q, kv, table, lens = c.q.cuda(), c.kv.cuda(), torch.from_numpy(c.table).cuda(), i32(c.lens)
+    pl = mla.plan_shared_prefix(table, lens, 1, 2)
+    st = i32([0])
+    mla.shared_prefix_decode(q, kv, table, lens, pl=pl, status=st)
+    assert int(st) == 0
+    lens[1999] += 1
+    mla.shared_prefix_decode(q, kv, table, lens, pl=pl, status=st)
+    assert int(st) == STALE_PLAN
