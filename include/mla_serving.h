@@ -176,6 +176,18 @@ int mla_prompt_attention_fwd(const void* d_q, long long q_token_stride, long lon
                              int batch, int h_q, int h_kv, int d_qk, float softmax_scale, const void* d_plan,
                              size_t plan_bytes, void* d_out, float* d_lse, int32_t* d_status, mla_stream_t stream);
 
+/* The same call for a program that holds the offsets: d_cu_seqlens_q and
+ * d_cu_seqlens_k (NULL: the same) are compared with the plan on the device, and
+ * MLA_ERR_STALE_PLAN is reported where one is another than the plan was made
+ * for.  The results are those of the plan either way. */
+int mla_prompt_attention_checked_fwd(const void* d_q, long long q_token_stride, long long q_head_stride,
+                                     const void* d_k, long long k_token_stride, long long k_head_stride,
+                                     const void* d_v, long long v_token_stride, long long v_head_stride, int dtype,
+                                     int total_q, int total_k, int batch, int h_q, int h_kv, int d_qk,
+                                     float softmax_scale, const int32_t* d_cu_seqlens_q,
+                                     const int32_t* d_cu_seqlens_k, const void* d_plan, size_t plan_bytes,
+                                     void* d_out, float* d_lse, int32_t* d_status, mla_stream_t stream);
+
 /* ------------------------------------------------------------ shared prefix */
 
 /* Dense decode (mla_decode_fwd with one latent KV head: a bf16 or fp16 cache, or
@@ -244,7 +256,8 @@ typedef enum {
   MLA_CALL_COPY_PAGES = 5,
   MLA_CALL_PROMPT = 6,       /* mla_prompt_attention_fwd */
   MLA_CALL_SHARED_PREFIX = 7, /* mla_shared_prefix_decode_fwd */
-  MLA_CALL_SHARED_PREFIX_CHECKED = 8
+  MLA_CALL_SHARED_PREFIX_CHECKED = 8,
+  MLA_CALL_PROMPT_CHECKED = 9
 } mla_call_t;
 int mla_serving_call(int op, const void* args, size_t bytes); /* bytes = 8 x the call's arguments */
 

@@ -124,7 +124,9 @@ constexpr uint32_t kTmemCols = 512;
 constexpr float kTau = 8.0f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
-// Plan: a header {tiles, causal, deal by sums}, then the tiles, kTileInts int32 each.
+// Plan: a header {tiles, causal, deal by sums}, then the tiles, kTileInts int32
+// each, then the offsets it was made for: batch + 1 of the queries, as many of
+// the keys.
 struct Tile {
   int q0;    // first query row of the tile in the packed q
   int rows;  // queries of the sequence from q0 on (the first two halves' worth matter)
@@ -287,6 +289,15 @@ __device__ __noinline__ uint32_t deal(const int32_t* plan, int heads, int total,
   fence_proxy_async_smem();  // the loads may write there next
   __syncthreads();
   return dealt;
+}
+
+// Whether the plan is that of the caller's offsets, by warps that have loaded
+// their last tile; the call's results are those of the plan either way.
+__device__ __forceinline__ void check_plan(const PromptParams& p) {
+  if (p.cu_q == nullptr) return;
+  const int32_t* made = p.plan + kTileInts * (p.max_tiles + 1);
+  for (int i = blockIdx.x * 32 + (threadIdx.x & 31); i <= p.batch; i += gridDim.x * 32)
+    if (made[i] != p.cu_q[i] || made[p.batch + 1 + i] != p.cu_k[i]) report(p.status, MLA_ERR_STALE_PLAN);
 }
 
 __device__ __forceinline__ void fail(volatile int* abort_flag, int32_t* status) {
@@ -464,6 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    if (warp == kWarpV) check_plan(p);
     if (!ok && lane == 0) {
       fail(abort_flag, p.status);
       // copies in flight land (bounded) before this CTA may end
@@ -831,6 +843,11 @@ __global__ void __launch_bounds__(kPlanThreads)
   }
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int32_t* made = plan + kTileInts * (max_tiles + 1);
+  for (int i = threadIdx.x; i <= batch; i += kPlanThreads) {
+    made[i] = cu_q[i];
+    made[batch + 1 + i] = cu_k[i];
+  }
   const int len_q = cu_q[1] - cu_q[0], len_k = cu_k[1] - cu_k[0];
   // warp per sequence, lanes over its tiles
   auto each = [&](auto f) {
@@ -899,7 +916,8 @@ int prompt_tile_q(int batch, int total_q) { return prompt_pairs(batch, total_q) 
 }  // namespace
 int prompt_plan_tiles(int batch, int total_q) { return total_q / prompt_tile_q(batch, total_q) + batch; }
 size_t prompt_plan_bytes(int batch, int total_q) {
-  return static_cast<size_t>(prompt_plan_tiles(batch, total_q) + 1) * pr::kTileInts * 4;
+  return static_cast<size_t>(prompt_plan_tiles(batch, total_q) + 1) * pr::kTileInts * 4 +
+         2 * (static_cast<size_t>(batch) + 1) * 4;
 }
 
 cudaError_t launch_prompt_plan(const int32_t* cu_q, const int32_t* cu_k, int batch, int total_q, int total_k,

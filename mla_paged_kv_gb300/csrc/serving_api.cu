@@ -127,6 +127,62 @@ int shared_sizes(int batch, int s_q, int h_q, int num_parts, SharedSizes* z) {
   return MLA_OK;
 }
 
+// mla_prompt_attention_fwd, with offsets to be compared with the plan's or NULL.
+int prompt_attention(const void* d_q, long long q_token_stride, long long q_head_stride, const void* d_k,
+                     long long k_token_stride, long long k_head_stride, const void* d_v, long long v_token_stride,
+                     long long v_head_stride, int dtype, int total_q, int total_k, int batch, int h_q, int h_kv,
+                     int d_qk, float softmax_scale, const int32_t* cu_q, const int32_t* cu_k, const void* d_plan,
+                     size_t plan_bytes, void* d_out, float* d_lse, int32_t* d_status, mla_stream_t stream) {
+  if (!d_plan || !d_status || batch < 1 || total_q < 0 || total_k < 0 || h_q < 1 || h_kv < 1 || h_q % h_kv != 0)
+    return MLA_ERR_INVALID_ARG;
+  if (total_q > 0 && (!d_q || !d_out || !d_lse)) return MLA_ERR_INVALID_ARG;
+  if (total_k > 0 && (!d_k || !d_v)) return MLA_ERR_INVALID_ARG;
+  if (dtype != MLA_DTYPE_BF16 && dtype != MLA_DTYPE_FP16) return MLA_ERR_INVALID_ARG;
+  if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.f)) return MLA_ERR_INVALID_ARG;
+  if (!aligned(d_q, 16) || !aligned(d_k, 16) || !aligned(d_v, 16) || !aligned(d_plan, 16) || !aligned(d_out, 16) ||
+      !aligned(d_lse, 4) || !aligned(cu_q, 4) || !aligned(cu_k, 4) || !aligned(d_status, 4))
+    return MLA_ERR_INVALID_ARG;
+  if (!good_strides(total_q, h_q, d_qk, q_token_stride, q_head_stride) ||
+      !good_strides(total_k, h_kv, d_qk, k_token_stride, k_head_stride) ||
+      !good_strides(total_k, h_kv, 128, v_token_stride, v_head_stride))
+    return MLA_ERR_INVALID_ARG;
+  if (d_qk != 192 && d_qk != 128) return MLA_ERR_UNSUPPORTED;
+  if (total_q > (1 << 30) || total_k > (1 << 30) || batch > (1 << 20)) return MLA_ERR_UNSUPPORTED;
+  if (plan_bytes < prompt_plan_bytes(batch, total_q)) return MLA_ERR_INVALID_ARG;
+  const int tiles = prompt_plan_tiles(batch, total_q);
+  if (static_cast<long long>(tiles) * h_q > (1 << 30)) return MLA_ERR_UNSUPPORTED;
+  int sms = 0;
+  const int rc0 = serving_device(&sms);
+  if (rc0 != MLA_OK || total_q == 0) return rc0;
+  PromptParams p{};
+  p.plan = static_cast<const int32_t*>(d_plan);
+  p.max_tiles = tiles;
+  p.h_q = h_q;
+  p.group = h_q / h_kv;
+  p.total_q = total_q;
+  p.batch = batch;
+  p.cu_q = cu_q;
+  p.cu_k = cu_k;
+  p.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * 1.4426950408889634);
+  p.out = d_out;
+  p.lse = d_lse;
+  p.status = d_status;
+  const bool pair = prompt_pairs(batch, total_q);
+  CUtensorMap qm, km, vm;
+  int rc = head_map(&qm, d_q, total_q, h_q, d_qk, q_token_stride, q_head_stride, 128, d_qk / 64);
+  if (total_k == 0) {  // no CTA loads K or V: any valid map serves
+    km = vm = qm;
+  } else {
+    // a pair's CTAs load 64 keys each, and all 128 for their half of V's dims
+    if (rc == MLA_OK)
+      rc = head_map(&km, d_k, total_k, h_kv, d_qk, k_token_stride, k_head_stride, pair ? 64 : 128, d_qk / 64);
+    if (rc == MLA_OK)
+      rc = head_map(&vm, d_v, total_k, h_kv, 128, v_token_stride, v_head_stride, 128, pair ? 1 : 2);
+  }
+  if (rc != MLA_OK) return rc;
+  return launched(launch_prompt(qm, km, vm, p, dtype == MLA_DTYPE_FP16, d_qk, pair, sms, to_stream(stream)));
+}
+
 // mla_shared_prefix_decode_fwd, with lengths to be compared with the plan's or NULL.
 int shared_decode(const void* d_q, const void* d_kv, const int32_t* d_block_table, int max_pages, int num_pages,
                   int batch, int s_q, int h_q, int dtype, int causal, float softmax_scale, const int32_t* live,
@@ -335,51 +391,23 @@ int mla_prompt_attention_fwd(const void* d_q, long long q_token_stride, long lon
                              long long v_token_stride, long long v_head_stride, int dtype, int total_q, int total_k,
                              int batch, int h_q, int h_kv, int d_qk, float softmax_scale, const void* d_plan,
                              size_t plan_bytes, void* d_out, float* d_lse, int32_t* d_status, mla_stream_t stream) {
-  if (!d_plan || !d_status || batch < 1 || total_q < 0 || total_k < 0 || h_q < 1 || h_kv < 1 || h_q % h_kv != 0)
-    return MLA_ERR_INVALID_ARG;
-  if (total_q > 0 && (!d_q || !d_out || !d_lse)) return MLA_ERR_INVALID_ARG;
-  if (total_k > 0 && (!d_k || !d_v)) return MLA_ERR_INVALID_ARG;
-  if (dtype != MLA_DTYPE_BF16 && dtype != MLA_DTYPE_FP16) return MLA_ERR_INVALID_ARG;
-  if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.f)) return MLA_ERR_INVALID_ARG;
-  if (!aligned(d_q, 16) || !aligned(d_k, 16) || !aligned(d_v, 16) || !aligned(d_plan, 16) || !aligned(d_out, 16) ||
-      !aligned(d_lse, 4) || !aligned(d_status, 4))
-    return MLA_ERR_INVALID_ARG;
-  if (!good_strides(total_q, h_q, d_qk, q_token_stride, q_head_stride) ||
-      !good_strides(total_k, h_kv, d_qk, k_token_stride, k_head_stride) ||
-      !good_strides(total_k, h_kv, 128, v_token_stride, v_head_stride))
-    return MLA_ERR_INVALID_ARG;
-  if (d_qk != 192 && d_qk != 128) return MLA_ERR_UNSUPPORTED;
-  if (total_q > (1 << 30) || total_k > (1 << 30) || batch > (1 << 20)) return MLA_ERR_UNSUPPORTED;
-  if (plan_bytes < prompt_plan_bytes(batch, total_q)) return MLA_ERR_INVALID_ARG;
-  const int tiles = prompt_plan_tiles(batch, total_q);
-  if (static_cast<long long>(tiles) * h_q > (1 << 30)) return MLA_ERR_UNSUPPORTED;
-  int sms = 0;
-  const int rc0 = serving_device(&sms);
-  if (rc0 != MLA_OK || total_q == 0) return rc0;
-  PromptParams p{};
-  p.plan = static_cast<const int32_t*>(d_plan);
-  p.max_tiles = tiles;
-  p.h_q = h_q;
-  p.group = h_q / h_kv;
-  p.total_q = total_q;
-  p.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * 1.4426950408889634);
-  p.out = d_out;
-  p.lse = d_lse;
-  p.status = d_status;
-  const bool pair = prompt_pairs(batch, total_q);
-  CUtensorMap qm, km, vm;
-  int rc = head_map(&qm, d_q, total_q, h_q, d_qk, q_token_stride, q_head_stride, 128, d_qk / 64);
-  if (total_k == 0) {  // no CTA loads K or V: any valid map serves
-    km = vm = qm;
-  } else {
-    // a pair's CTAs load 64 keys each, and all 128 for their half of V's dims
-    if (rc == MLA_OK)
-      rc = head_map(&km, d_k, total_k, h_kv, d_qk, k_token_stride, k_head_stride, pair ? 64 : 128, d_qk / 64);
-    if (rc == MLA_OK)
-      rc = head_map(&vm, d_v, total_k, h_kv, 128, v_token_stride, v_head_stride, 128, pair ? 1 : 2);
-  }
-  if (rc != MLA_OK) return rc;
-  return launched(launch_prompt(qm, km, vm, p, dtype == MLA_DTYPE_FP16, d_qk, pair, sms, to_stream(stream)));
+  return prompt_attention(d_q, q_token_stride, q_head_stride, d_k, k_token_stride, k_head_stride, d_v, v_token_stride,
+                          v_head_stride, dtype, total_q, total_k, batch, h_q, h_kv, d_qk, softmax_scale, nullptr,
+                          nullptr, d_plan, plan_bytes, d_out, d_lse, d_status, stream);
+}
+
+int mla_prompt_attention_checked_fwd(const void* d_q, long long q_token_stride, long long q_head_stride,
+                                     const void* d_k, long long k_token_stride, long long k_head_stride,
+                                     const void* d_v, long long v_token_stride, long long v_head_stride, int dtype,
+                                     int total_q, int total_k, int batch, int h_q, int h_kv, int d_qk,
+                                     float softmax_scale, const int32_t* d_cu_seqlens_q,
+                                     const int32_t* d_cu_seqlens_k, const void* d_plan, size_t plan_bytes,
+                                     void* d_out, float* d_lse, int32_t* d_status, mla_stream_t stream) {
+  if (!d_cu_seqlens_q || (!d_cu_seqlens_k && total_k != total_q)) return MLA_ERR_INVALID_ARG;
+  return prompt_attention(d_q, q_token_stride, q_head_stride, d_k, k_token_stride, k_head_stride, d_v, v_token_stride,
+                          v_head_stride, dtype, total_q, total_k, batch, h_q, h_kv, d_qk, softmax_scale,
+                          d_cu_seqlens_q, d_cu_seqlens_k ? d_cu_seqlens_k : d_cu_seqlens_q, d_plan, plan_bytes, d_out,
+                          d_lse, d_status, stream);
 }
 
 int mla_shared_prefix_num_parts(int batch, int s_q, int h_q) {
@@ -447,8 +475,8 @@ int mla_shared_prefix_decode_checked_fwd(const void* d_q, const void* d_kv, cons
 }
 
 int mla_serving_call(int op, const void* args, size_t bytes) {
-  constexpr size_t kWords[] = {22, 11, 12, 10, 12, 10, 23, 21, 22};  // by mla_call_t
-  if (!args || op < 0 || op > MLA_CALL_SHARED_PREFIX_CHECKED || bytes != 8 * kWords[op]) return MLA_ERR_INVALID_ARG;
+  constexpr size_t kWords[] = {22, 11, 12, 10, 12, 10, 23, 21, 22, 25};  // by mla_call_t
+  if (!args || op < 0 || op > MLA_CALL_PROMPT_CHECKED || bytes != 8 * kWords[op]) return MLA_ERR_INVALID_ARG;
   const char* a = static_cast<const char*>(args);
   auto word = [&](int i) {
     int64_t v;
@@ -495,6 +523,10 @@ int mla_serving_call(int op, const void* args, size_t bytes) {
       return mla_shared_prefix_decode_checked_fwd(P(0), P(1), N(2), I(3), I(4), I(5), I(6), I(7), I(8), I(9), F(10),
                                                   N(11), P(12), static_cast<size_t>(word(13)), I(14), P(15),
                                                   static_cast<size_t>(word(16)), P(17), I(18), R(19), N(20), S(21));
+    case MLA_CALL_PROMPT_CHECKED:
+      return mla_prompt_attention_checked_fwd(P(0), word(1), word(2), P(3), word(4), word(5), P(6), word(7), word(8),
+                                              I(9), I(10), I(11), I(12), I(13), I(14), I(15), F(16), N(17), N(18),
+                                              P(19), static_cast<size_t>(word(20)), P(21), R(22), N(23), S(24));
     default: return MLA_ERR_INVALID_ARG;
   }
 }

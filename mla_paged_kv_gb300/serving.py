@@ -41,6 +41,8 @@ SERVING_SIGS = {
     "mla_prompt_get_plan": (_I, [_P, _P, _I, _I, _I, _I, _P, _SZ, _P, _P]),
     "mla_prompt_attention_fwd": (_I, [_P, _LL, _LL, _P, _LL, _LL, _P, _LL, _LL, _I, _I, _I, _I, _I, _I, _I, _F, _P,
                                       _SZ, _P, _P, _P, _P]),
+    "mla_prompt_attention_checked_fwd": (_I, [_P, _LL, _LL, _P, _LL, _LL, _P, _LL, _LL, _I, _I, _I, _I, _I, _I, _I,
+                                              _F, _P, _P, _P, _SZ, _P, _P, _P, _P]),
     "mla_shared_prefix_num_parts": (_I, [_I, _I, _I]),
     "mla_shared_prefix_plan_bytes": (_SZ, [_I, _I, _I, _I]),
     "mla_shared_prefix_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
@@ -102,6 +104,7 @@ def _words(op, layout):
 _APPEND, _GROW, _FORK, _FREE = _words(0, "15qd6q"), _words(1, "11q"), _words(2, "12q"), _words(3, "10q")
 _COMPACT, _COPY_PAGES, _PROMPT = _words(4, "12q"), _words(5, "10q"), _words(6, "16qd6q")
 _SHARED_PREFIX, _SHARED_PREFIX_CHECKED = _words(7, "10qd10q"), _words(8, "10qd11q")
+_PROMPT_CHECKED = _words(9, "16qd8q")
 
 
 def _call(op, name, *args):
@@ -360,8 +363,9 @@ def mla_prompt_get_plan(cu_seqlens_q, cu_seqlens_k, total_q, total_k, causal, pl
         "mla_prompt_get_plan")
 
 
-def _prompt(q, k, v, pl, softmax_scale, status, stream, out=None, lse=None):
-    """The checks and the call of mla_prompt_attention_fwd; allocates out and lse if not given."""
+def _prompt(q, k, v, pl, softmax_scale, status, stream, out=None, lse=None, cu_seqlens_q=None, cu_seqlens_k=None):
+    """The checks and the call of mla_prompt_attention_fwd (with offsets, _checked_fwd); allocates out and lse if
+    not given."""
     dt = q.dtype
     code = _DTYPE_CODE16.get(dt)
     if code is None or k.dtype is not dt or v.dtype is not dt:
@@ -393,9 +397,21 @@ def _prompt(q, k, v, pl, softmax_scale, status, stream, out=None, lse=None):
         out_ptr, lse_ptr = _p(out, dt, 3, dev, "out"), _p(lse, _FP32, 2, dev, "lse")
         if out.shape != (total_q, h_q, 128) or lse.shape != (total_q, h_q):
             raise ValueError("out must be [total_q, h_q, 128] and lse [total_q, h_q]")
-    _call(_PROMPT, "mla_prompt_attention_fwd", q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(),
-          vs[0], vs[1], code, total_q, total_k, pl.batch, h_q, h_kv, d,
-          1.0 / math.sqrt(d) if softmax_scale is None else softmax_scale, plan, pl.bytes, out_ptr, lse_ptr, st, queue)
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(d)
+    if cu_seqlens_q is None:
+        _call(_PROMPT, "mla_prompt_attention_fwd", q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1],
+              v.data_ptr(), vs[0], vs[1], code, total_q, total_k, pl.batch, h_q, h_kv, d, softmax_scale, plan,
+              pl.bytes, out_ptr, lse_ptr, st, queue)
+        return out, lse
+    cu_q, cu_k = _p(cu_seqlens_q, _INT32, 1, dev, "cu_seqlens_q"), 0
+    if cu_seqlens_k is not None:
+        cu_k = _p(cu_seqlens_k, _INT32, 1, dev, "cu_seqlens_k")
+    if cu_seqlens_q.shape[0] != pl.batch + 1 or (cu_k and cu_seqlens_k.shape[0] != pl.batch + 1):
+        raise ValueError("the plan was made for another batch")
+    _call(_PROMPT_CHECKED, "mla_prompt_attention_checked_fwd", q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1],
+          v.data_ptr(), vs[0], vs[1], code, total_q, total_k, pl.batch, h_q, h_kv, d, softmax_scale, cu_q, cu_k, plan,
+          pl.bytes, out_ptr, lse_ptr, st, queue)
     return out, lse
 
 
@@ -404,6 +420,13 @@ def mla_prompt_attention_fwd(q, k, v, pl, out, lse, status, softmax_scale=None, 
     128], bf16 or fp16, last dimension contiguous, other strides multiples of 8;
     pl a PromptPlan; out [total_q, h_q, 128] of q's type, lse fp32 [total_q, h_q]."""
     _prompt(q, k, v, pl, softmax_scale, status, stream, out, lse)
+
+
+def mla_prompt_attention_checked_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, pl, out, lse, status, softmax_scale=None,
+                                     stream=None):
+    """mla_prompt_attention_fwd that also compares the offsets [batch + 1] (cu_seqlens_k None: the same) with the
+    plan's on the device: others are MLA_ERR_STALE_PLAN in status."""
+    _prompt(q, k, v, pl, softmax_scale, status, stream, out, lse, cu_seqlens_q, cu_seqlens_k)
 
 
 def plan_prompt(cu_seqlens_q, cu_seqlens_k=None, total_q=None, total_k=None, causal=True, status=None):
@@ -426,13 +449,17 @@ def plan_prompt(cu_seqlens_q, cu_seqlens_k=None, total_q=None, total_k=None, cau
 
 def prompt_attention(q, k, v, cu_seqlens_q, cu_seqlens_k=None, causal=True, softmax_scale=None, pl=None,
                      status=None):
-    """Attention over packed prompts; returns (out, lse)."""
+    """Attention over packed prompts; returns (out, lse).
+
+    A plan holds the offsets it was made for.  With pl they are compared with cu_seqlens_q and cu_seqlens_k on the
+    device, and a plan of others is MLA_ERR_STALE_PLAN."""
     st = _status(status, q)
-    if pl is None:
+    if pl is None:  # a plan made here is that of the offsets
         pl = plan_prompt(cu_seqlens_q, cu_seqlens_k, q.shape[0], k.shape[0], causal, st)
+        cu_seqlens_q = cu_seqlens_k = None
     elif pl.causal != bool(causal):
         raise ValueError("the plan was made with another causal setting")
-    out, lse = _prompt(q, k, v, pl, softmax_scale, st, None)
+    out, lse = _prompt(q, k, v, pl, softmax_scale, st, None, cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k)
     if status is None:
         check_status(st, "mla_prompt_attention_fwd")
     return out, lse

@@ -239,3 +239,28 @@ def test_without_a_plan_the_status_is_the_callers():
     offsets.copy_(i32([0, 20, 320]))
     graph.replay()
     assert torch.equal(out[:20], mla.prompt_attention(q, k, v, i32([0, 20, 320]))[0][:20]) and int(st) == 0
+
+
+@pytest.mark.parametrize("lq,lk", [([300, 20, 0, 5], None), ([700, 900], [700, 1000]), ([3] * 6000, None)])
+def test_a_plan_of_other_offsets_is_reported(lq, lk):
+    """A plan holds its offsets: with others that end in the same place the call says so (and answers by the
+    plan); with the same ones it is silent."""
+    q, k, v, cu_q, cu_k = make(lq, lk or lq, 2, 1, 192, torch.bfloat16, 17)
+    q, k, v = q.cuda(), k.cuda(), v.cuda()
+    dev_q, dev_k = i32(cu_q), i32(cu_k) if lk else None
+    pl = mla.plan_prompt(dev_q, dev_k, q.shape[0], k.shape[0])
+    want = mla.prompt_attention(q, k, v, dev_q, dev_k, pl=pl)
+    for which, at in (("q", 1), ("q", len(lq) - 1), ("k", 1)):
+        if which == "k" and lk is None:
+            continue
+        a, b = dev_q.clone(), None if dev_k is None else dev_k.clone()
+        (a if which == "q" else b)[at] += 1
+        with pytest.raises(mla.MlaError) as e:
+            mla.prompt_attention(q, k, v, a, b, pl=pl)
+        assert e.value.code == 7
+        st = i32([0])
+        out, lse = mla.prompt_attention(q, k, v, a, b, pl=pl, status=st)
+        assert int(st) == 7 and torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    for bad, error in ((dev_q.long(), TypeError), (dev_q[1:], ValueError), (dev_q.cpu(), ValueError)):
+        with pytest.raises(error):
+            mla.prompt_attention(q, k, v, bad, dev_k, pl=pl)

@@ -253,7 +253,8 @@ def checked(base, names, at):
     return out
 
 
-CHECKED = [(8, "mla_shared_prefix_decode_checked_fwd", checked(SDEC, ["lens"], "plan"), "lens")]
+CHECKED = [(8, "mla_shared_prefix_decode_checked_fwd", checked(SDEC, ["lens"], "plan"), "lens"),
+           (9, "mla_prompt_attention_checked_fwd", checked(PROMPT, ["cuq", "cuk"], "plan"), "cuq")]
 
 
 @pytest.mark.parametrize("op,name,base,own", CHECKED)
