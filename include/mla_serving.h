@@ -200,7 +200,8 @@ int mla_prompt_attention_checked_fwd(const void* d_q, long long q_token_stride, 
  * entries that the requests have in common, in whole pages that every query of
  * each of them sees; it may be none.  Requests whose first query sees less
  * than a page (empty slots of a padded batch) are attended by themselves and
- * leave the others' prefix as it is.  The plan is made once for a batch and
+ * leave the others' prefix as it is; a request that none is left to share with
+ * shares nothing.  The plan is made once for a batch and
  * read by every layer, while the block table and lengths stay as they were.
  * The prefix is attended together only where that takes at most 7/8 of the
  * 128-row blocks that attending it request by request does:

@@ -33,14 +33,16 @@ __device__ __forceinline__ int keys_seen(const int32_t* seqlens, int b, int s_q,
 
 // The pages every request that sees one starts with (the longest common run of
 // block-table entries, whole pages that every query sees), and the units over
-// them and over the rest.  One block, made once for a batch; its time is the
+// them and over the rest.  A single request shares with none, and a row block
+// whose requests all stand apart (the empty slots at the end of a padded batch)
+// has no keys.  One block, made once for a batch; its time is the
 // latency of reading the tables (64 requests that share 2048 pages 9.8 us, with
 // one entry a lane in flight 29).
 __global__ void __launch_bounds__(1024)
     shared_units_kernel(const int32_t* table, int max_pages, const int32_t* seqlens, int batch, int s_q, int h_q,
                         int causal, int32_t* units, int32_t* lengths) {
-  __shared__ int common, first;  // pages in common; the first request that takes part
-  if (threadIdx.x == 0) common = max_pages, first = batch;
+  __shared__ int common, first, last;  // pages in common; the first and the last request that take part
+  if (threadIdx.x == 0) common = max_pages, first = batch, last = -1;
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kAhead = 8;  // entries a lane has in flight: the loop is their latency
@@ -49,6 +51,7 @@ __global__ void __launch_bounds__(1024)
     if (seen >= kTile) {
       atomicMin(&common, seen / kTile);
       atomicMin(&first, b);
+      atomicMax(&last, b);
     }
   }
   __syncthreads();
@@ -76,7 +79,7 @@ __global__ void __launch_bounds__(1024)
     if (lane == 0 && at < max_pages) atomicMin(&common, at);
   }
   __syncthreads();
-  const int shared = none ? 0 : common;
+  const int shared = first < last ? common : 0;
   const int rows = s_q * h_q;
   const long long total = static_cast<long long>(batch) * rows;
   const int front = static_cast<int>((total + kRB - 1) / kRB), per = ceil_div_i(rows, kRB);
@@ -87,7 +90,10 @@ __global__ void __launch_bounds__(1024)
       e[0] = make_int4(row0, static_cast<int>(min(total - row0, static_cast<long long>(kRB))), -1,
                        ref * max_pages);
       e[1] = make_int4(max_pages, 0, 0, 0);
-      lengths[u] = shared * kTile;
+      int b = row0 / rows;
+      const int end = static_cast<int>((min(total, static_cast<long long>(row0) + kRB) - 1) / rows);
+      while (b < end && keys_seen(seqlens, b, s_q, causal) < kTile) ++b;
+      lengths[u] = keys_seen(seqlens, b, s_q, causal) < kTile ? 0 : shared * kTile;
     } else {
       const int b = (u - front) / per, blk = (u - front) - b * per;
       const int rel = blk * kRB;

@@ -407,3 +407,27 @@ def test_many_lengths_are_all_compared():
     lens[1999] += 1
     mla.shared_prefix_decode(q, kv, table, lens, pl=pl, status=st)
     assert int(st) == STALE_PLAN
+
+
+@pytest.mark.parametrize("live", [[0], [63], [0, 1], [5, 60], [0, 1, 2, 3, 4, 5, 6, 7, 8], [9, 40, 41]])
+@pytest.mark.parametrize("s_q,fp8", [(1, False), (2, False), (1, True)])
+def test_padded_batch_attends_the_prefix_for_its_live_rows_alone(live, s_q, fp8):
+    """64 slots of 16 heads, few of them live: only row blocks with a request that takes part have the prefix's
+    keys, and a single one has all its keys to itself."""
+    c = Case(5, [64 + 3 * b for b in range(64)], s_q, 16, s_q > 1, seed=22, fp8=fp8)
+    for b in range(64):
+        if b not in live:
+            c.lens[b] = 0
+            c.table[b] = -1
+    c.check()
+    rows, width = 16 * s_q, c.table.shape[1]
+    front = 64 * rows // 128
+    pl = mla.plan_shared_prefix(torch.from_numpy(c.table).cuda(), i32(c.lens), s_q, 16, s_q > 1)
+    units = pl.plan[:(front + 64) * 32].view(torch.int32).reshape(-1, 8).cpu().tolist()
+    at = -(-(front + 64) * 32 // 256) * 256
+    keys = pl.plan[at:at + (front + 64) * 4].view(torch.int32).cpu().tolist()
+    blocks = {b * rows // 128 for b in live} if len(live) > 1 else set()
+    assert keys[:front] == [5 * 64 if u in blocks else 0 for u in range(front)]
+    for b in range(64):
+        skip = 5 if b in live and len(live) > 1 else 0
+        assert units[front + b][3] == b * width + skip and keys[front + b] == c.lens[b] - 64 * skip
