@@ -264,3 +264,58 @@ def test_a_plan_of_other_offsets_is_reported(lq, lk):
     for bad, error in ((dev_q.long(), TypeError), (dev_q[1:], ValueError), (dev_q.cpu(), ValueError)):
         with pytest.raises(error):
             mla.prompt_attention(q, k, v, bad, dev_k, pl=pl)
+
+
+# Batches of more than 256 queries a prompt run on pairs of CTAs, in instances of their own by type and dims.
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [128, 192])
+@pytest.mark.parametrize("lq,lk,causal", [([600, 1, 333], [600, 5, 400], True), ([600, 1, 333], [600, 5, 400], False),
+                                          ([513], [2500], True), ([700, 900], [300, 1000], True),
+                                          ([700, 900, 257], [300, 0, 257], False)])
+def test_pairs_types_and_dims(dtype, d, lq, lk, causal):
+    """Ragged ends, long key rings, queries that see no key (a whole first half of a tile among them), no keys."""
+    run(lq, lk, h=4, hkv=2, d=d, dtype=dtype, causal=causal, seed=d + len(lq))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [128, 192])
+@pytest.mark.parametrize("h,hkv", [(3, 3), (8, 1), (12, 4)])
+def test_pairs_head_groups(dtype, d, h, hkv):
+    run([500, 270], [500, 470], h=h, hkv=hkv, d=d, dtype=dtype, seed=h)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [128, 192])
+def test_pairs_strided_inputs(dtype, d):
+    """Slices of one fused projection, and head-major storage; NaN and infinities between and behind."""
+    g = torch.Generator().manual_seed(18)
+    n, h, cu = 1000, 2, [3, 420, 960]
+    fused = torch.randn(n, h, 2 * d + 128, generator=g).to(dtype)
+    fused[:3] = float("nan")
+    fused[960:] = float("inf")
+    cut = lambda x: (x[..., :d], x[..., d:2 * d], x[..., 2 * d:])  # noqa: E731
+    dev = cut(fused.cuda())
+    pl = mla.plan_prompt(i32(cu), None, n)
+    results = []
+    for q, k, v in (dev, [t.transpose(0, 1).contiguous().transpose(0, 1) for t in dev]):
+        out = torch.full((n, h, 128), 5.0, dtype=dtype, device="cuda")
+        lse, st = torch.full((n, h), 5.0, device="cuda"), i32([0])
+        mla.mla_prompt_attention_fwd(q, k, v, pl, out, lse, st)
+        assert int(st) == 0
+        results.append((out, lse))
+    clean = cut(torch.where(torch.isfinite(fused), fused, torch.zeros_like(fused)))
+    check(*results[0], *clean, cu, cu, True, 1 / math.sqrt(d), fill=5.0)
+    assert torch.equal(results[0][0], results[1][0]) and torch.equal(results[0][1], results[1][1])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [128, 192])
+def test_pairs_rescale_the_output(dtype, d):
+    q, k, v, cu, _ = make([900], [900], 2, 1, d, dtype, 11)
+    k = (k.float() * 0.02 + torch.linspace(0, 3, 900)[:, None, None] * q[:1, :1].float()).to(dtype)
+    q = (q.float() * 0.1 + q[:1, :1].float()).to(dtype)
+    out, lse = mla.prompt_attention(q.cuda(), k.cuda(), v.cuda(), i32(cu), None, True, 0.2)
+    check(out, lse, q, k, v, cu, cu, True, 0.2)
+    run([600], [600], d=d, dtype=dtype, seed=12, amp=8.0)
