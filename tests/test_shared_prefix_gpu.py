@@ -431,3 +431,53 @@ def test_padded_batch_attends_the_prefix_for_its_live_rows_alone(live, s_q, fp8)
     for b in range(64):
         skip = 5 if b in live and len(live) > 1 else 0
         assert units[front + b][3] == b * width + skip and keys[front + b] == c.lens[b] - 64 * skip
+
+
+def bound_of(c, out_dtype):
+    """want, lse and what they may be off by, element by element.  Weights of type `dtype` are rounded once, half a
+    step u of each (2^-8 bf16, 2^-11 fp16; FP8 records: bf16, and the sum is that of the rounded ones, once more), so
+    the output moves by u M, M = sum w |v|; the output's own rounding is a half step of it.  A score is 576 products in
+    fp32, off by 576 2^-23 A, A = max scale |q|.|k|; the exponentials and the merge of the splits add 2^-20.  fp16
+    weights below the smallest normal are off by 2^-25 each, of a sum of 1 at least."""
+    u = 2.0 ** -11 if c.q.dtype == torch.float16 else 2.0 ** -8
+    fp8 = c.kv.dtype == torch.uint8
+    want, lse = c.want()
+    want, lse = np.asarray(want, dtype=np.float64), np.asarray(lse, dtype=np.float64)
+    mix, reach, tiny = np.zeros_like(want), np.zeros_like(lse), np.zeros_like(want)
+    for b, n in enumerate(c.lens):
+        pages = c.kv[c.table[b, :-(-n // 64)]].reshape(-1, c.kv.shape[2])[:n]
+        keys = np.stack([orc.decode_record(r) for r in pages.numpy()]) if fp8 else pages.double().numpy()
+        q = c.q[b].double().numpy()
+        s = np.einsum("shd,kd->shk", q, keys) / 24
+        if c.causal:
+            for i in range(c.s_q):
+                s[i, :, max(n - c.s_q + 1 + i, 0):] = -np.inf
+        w = np.exp(s - lse[b][..., None])
+        mix[b] = np.einsum("shk,kd->shd", w, np.abs(keys[:, :512]))
+        if c.q.dtype == torch.float16:
+            tiny[b] = 2.0 ** -25 * np.abs(keys[:, :512]).sum(0)
+        reach[b] = (np.einsum("shd,kd->shk", np.abs(q), np.abs(keys)) / 24).max(2)
+    score = 576 * 2.0 ** -23 * reach
+    own = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}[out_dtype]
+    tiny += 2.0 ** -25 if out_dtype == torch.float16 else 0.0
+    return want, lse, ((2 if fp8 else 1) * u + 2 * score + 2.0 ** -20)[..., None] * mix + own * np.abs(want) + tiny, \
+        score + 2.0 ** -20 + 2.0 ** -23 * np.abs(lse)
+
+
+@pytest.mark.parametrize("h_q", [16, 104, 128])  # rows packed twice, requests alone
+@pytest.mark.parametrize("dtype,fp8", [(torch.bfloat16, False), (torch.float16, False), (torch.bfloat16, True)])
+@pytest.mark.parametrize("out_fp32", [False, True])
+@pytest.mark.parametrize("s_q,causal", [(1, False), (2, True)])
+def test_every_instance_within_its_roundings(h_q, dtype, fp8, out_fp32, s_q, causal):
+    """Every kernel of the call against the bound of its own arithmetic, a fraction of the outputs' spread."""
+    c = Case(9, [64, 100, 5, 300, 33, 64, 2, 190], s_q, h_q, causal, dtype=dtype, seed=23 + s_q, poison=False, fp8=fp8)
+    out, lse = c.run(out_fp32=out_fp32)
+    want, wlse, tol, ltol = bound_of(c, out.dtype)
+    assert np.median(tol) < want.std() / 4
+    o, l = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert np.all(np.abs(o - want) <= tol), np.max(np.abs(o - want) / tol)
+    assert np.all(np.abs(l - wlse) <= ltol), np.max(np.abs(l - wlse) / ltol)
+    if not fp8 and not causal:  # and so the plain decode of each request
+        o2, l2 = mla.decode(c.q.cuda(), c.kv.cuda(), torch.from_numpy(c.table).cuda(), i32(c.lens), out_fp32=out_fp32)
+        assert np.all(np.abs(o2.double().cpu().numpy() - o) <= 2 * tol)
+        assert np.all(np.abs(l2.double().cpu().numpy() - l) <= 2 * ltol)
