@@ -215,3 +215,115 @@ def test_two_streams_at_once():
         for a, b in zip(want, got):
             assert all(torch.equal(x, y) for x, y in zip(a, b))
     assert [int(s["status"]) for s in states] == [0, 0]
+
+
+def test_two_graphs_at_once():
+    """Every operator captured into a graph of its own tensors, plans and workspaces, twice; the two replayed
+    back to back on two streams, round after round without a wait, give what each gives alone."""
+    g = torch.Generator().manual_seed(22)
+    lens, slens = [300, 1, 700, 130], [700, 1400, 600, 513]
+    cu = [0, 300, 301, 1001, 1131]
+
+    def state():
+        r = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).cuda()  # noqa: E731
+        s = dict(q=r(1131, 4, 192), k=r(1131, 4, 192), v=r(1131, 4, 128), row=r(1131, 576), cu=i32(cu))
+        s["table"] = torch.arange(48, dtype=torch.int32).reshape(4, 12).cuda()
+        s["lens"], s["cache"] = i32(lens), r(60, 64, 576)
+        shared = torch.arange(96, dtype=torch.int32).reshape(4, 24) % 60
+        shared[:, :8] = torch.arange(8, dtype=torch.int32)
+        s["shared"], s["slens"], s["kv"] = shared.cuda(), i32(slens), r(60, 64, 576)
+        s["dq"], s["dq128"] = r(4, 1, 16, 576), r(4, 1, 128, 576)
+        s["ref0"], s["zero"] = (torch.rand(60, generator=g) < 0.6).int().cuda(), i32([0, 0, 0, 0])
+        s["none"], s["pool0"], s["status"] = torch.full_like(s["table"], -1), r(2, 60, 64, 16), i32([0])
+        for name, v in (("grow", [0, 2]), ("new", [100, 300]), ("parent", [2]), ("child", [1]), ("gone", [0])):
+            s[name] = i32(v)
+        return s
+
+    def work(s):
+        st = s["status"]
+        out = [*mla.prompt_attention(s["q"], s["k"], s["v"], s["cu"], status=st)]
+        cache = s["cache"].clone()
+        mla.cache_append(s["row"][:, :512], s["row"][:, 512:], cache, s["table"], s["lens"], cu_seqlens=s["cu"],
+                         status=st)
+        out += [*mla.shared_prefix_decode(s["dq"], s["kv"], s["shared"], s["slens"], status=st),
+                *mla.shared_prefix_decode(s["dq128"], s["kv"], s["shared"], s["slens"], status=st)]
+        ref, table, n, pool = (s[k].clone() for k in ("ref0", "none", "zero", "pool0"))
+        mla.cache_grow(ref, table, n, s["grow"], s["new"], status=st)
+        mla.cache_copy_pages(pool, mla.cache_fork(ref, table, n, s["parent"], s["child"], status=st), layered=True,
+                             status=st)
+        mla.cache_free(ref, table, n, s["gone"], status=st)
+        pairs, count = mla.cache_compact(ref, table, n, status=st)
+        mla.cache_copy_pages(pool, pairs, count=count, layered=True, status=st)
+        return out + [cache, ref, table, n, pool, pairs, count]
+
+    states = [state(), state()]
+    want = [[t.clone() for t in work(s)] for s in states]
+    torch.cuda.synchronize()
+    graphs, got = [], []
+    for s in states:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got.append(work(s))
+        graphs.append(graph)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in states]
+    marks = [[torch.cuda.Event(enable_timing=True) for _ in range(2)] for _ in states]
+    for _ in range(3):
+        for stream, (begin, _) in zip(streams, marks):
+            begin.record(stream)
+        for _ in range(40):
+            for graph, stream in zip(graphs, streams):
+                with torch.cuda.stream(stream):
+                    graph.replay()
+        for stream, (_, end) in zip(streams, marks):
+            end.record(stream)
+        torch.cuda.synchronize()
+        # both were at work for most of the time of either
+        alone = max(b.elapsed_time(e) for b, e in marks)
+        assert min(marks[0][0].elapsed_time(marks[1][1]), marks[1][0].elapsed_time(marks[0][1])) > 0.5 * alone
+        for a, b in zip(want, got):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert [int(s["status"]) for s in states] == [0, 0]
+
+
+@pytest.mark.parametrize("s_q", [1, 3])
+def test_decode_continues_the_prompts_attention(s_q):
+    """The last queries of prompts, once by prompt attention over expanded heads and once by the decode over the
+    appended latent rows: with the same scale the same attention.  The expansions select latent dims (head h: dims
+    (37 h + i) % 512 for keys, (53 h + 11 + i) % 512 for values), so both see the same numbers.
+
+    Each side is off by the rounding of its weights and its output, u = 2^-8 of M = sum w |v| and of the value, and
+    by its scores, a sum of 576 products at most in fp32: d = 576 2^-23 max scale |q|.|k|, twice that on weights."""
+    H, lens, scale = 16, [130, 77, 300, 64], 192 ** -0.5
+    g = torch.Generator().manual_seed(5)
+    total = sum(lens)
+    cu = [0] + [int(x) for x in np.cumsum(lens)]
+    lat, rope = (torch.randn(total, n, generator=g).to(torch.bfloat16) for n in (512, 64))
+    q = torch.randn(total, H, 192, generator=g).to(torch.bfloat16)
+    kdim = torch.stack([(37 * h + torch.arange(128)) % 512 for h in range(H)])
+    vdim = torch.stack([(53 * h + 11 + torch.arange(128)) % 512 for h in range(H)])
+    k = torch.cat([lat[:, kdim], rope[:, None].expand(-1, H, -1)], 2)
+    v = lat[:, vdim]
+    out, lse = mla.prompt_attention(q.cuda(), k.cuda(), v.cuda(), i32(cu), softmax_scale=scale)
+    # into pages, and the last s_q queries of each with their heads absorbed
+    cache = torch.zeros(12, 64, 576, dtype=torch.bfloat16, device="cuda")
+    table = torch.tensor([[0, 1, 2, -1, -1], [3, 4, -1, -1, -1], [5, 6, 7, 8, 9], [10, -1, -1, -1, -1]],
+                         dtype=torch.int32, device="cuda")
+    mla.cache_append(lat.cuda(), rope.cuda(), cache, table, i32(lens), cu_seqlens=i32(cu))
+    last = torch.tensor([[e - s_q + i for i in range(s_q)] for e in cu[1:]])
+    absorbed = torch.zeros(len(lens), s_q, H, 576, dtype=torch.bfloat16)
+    absorbed[..., :512].scatter_(3, kdim.expand(len(lens), s_q, H, 128), q[last][..., :128])
+    absorbed[..., 512:] = q[last][..., 128:]
+    _, _, mix, reach = so.prompt_attention(q.double().numpy(), k.double().numpy(), v.double().numpy(), cu, cu, True,
+                                           scale)
+    want, wlse = out.double().cpu()[last].numpy(), lse.double().cpu()[last].numpy()
+    d = 576 * 2.0 ** -23 * reach[last]
+    tol = 2 * ((2.0 ** -8 + 2 * d + 2.0 ** -20)[..., None] * mix[last] + 2.0 ** -8 * (np.abs(want) + 2.0 ** -8))
+    pick = vdim.expand(len(lens), s_q, H, 128)
+    for name, fn in (("decode", mla.decode), ("shared", mla.shared_prefix_decode)):
+        o, l = fn(absorbed.cuda(), cache, table, i32(lens), causal=True, softmax_scale=scale)
+        assert np.all(np.abs(o.double().cpu().gather(3, pick).numpy() - want) <= tol), name
+        assert np.all(np.abs(l.double().cpu().numpy() - wlse) <= 2 * (d + 2.0 ** -20 + 2.0 ** -23 * np.abs(wlse)))
+    # with the decode's default, 1 / sqrt(576), it is another attention
+    o, _ = mla.decode(absorbed.cuda(), cache, table, i32(lens), causal=True)
+    assert not np.all(np.abs(o.double().cpu().gather(3, pick).numpy() - want) <= tol)
