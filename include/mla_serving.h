@@ -242,6 +242,28 @@ int mla_shared_prefix_decode_checked_fwd(const void* d_q, const void* d_kv, cons
                                          size_t workspace_bytes, void* d_out, int out_type, float* d_lse,
                                          int32_t* d_status, mla_stream_t stream);
 
+/* -------------------------------------------------------------- test hooks */
+
+/* The timeout and unwind paths of the two attention kernels above, as
+ * mla_test_decode_timeout does for the plain decode: the arguments and checks of
+ * mla_prompt_attention_fwd (bf16 with 192 dims) and of
+ * mla_shared_prefix_decode_fwd (bf16, or FP8 records), else MLA_ERR_UNSUPPORTED.
+ * Instances whose waits have a 200 us budget and whose first tile is never
+ * loaded (FP8 records: whose first scores are never computed): the wait for it
+ * runs out, MLA_ERR_TIMEOUT is reported, every role leaves its loop, copies and
+ * products in flight end, tensor memory is given back, and the grid ends.  The
+ * context and the stream stay usable; outputs and workspace are unspecified. */
+int mla_test_prompt_timeout(const void* d_q, long long q_token_stride, long long q_head_stride, const void* d_k,
+                            long long k_token_stride, long long k_head_stride, const void* d_v,
+                            long long v_token_stride, long long v_head_stride, int dtype, int total_q, int total_k,
+                            int batch, int h_q, int h_kv, int d_qk, float softmax_scale, const void* d_plan,
+                            size_t plan_bytes, void* d_out, float* d_lse, int32_t* d_status, mla_stream_t stream);
+int mla_test_shared_prefix_timeout(const void* d_q, const void* d_kv, const int32_t* d_block_table, int max_pages,
+                                   int num_pages, int batch, int s_q, int h_q, int dtype, int causal,
+                                   float softmax_scale, const void* d_plan, size_t plan_bytes, int num_parts,
+                                   void* d_workspace, size_t workspace_bytes, void* d_out, int out_type, float* d_lse,
+                                   int32_t* d_status, mla_stream_t stream);
+
 /* ---------------------------------------------------------------- one pointer */
 
 /* The calls above with their arguments, in order, as 8-byte words: pointers,

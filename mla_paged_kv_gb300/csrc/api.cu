@@ -101,10 +101,10 @@ const DeviceInfo& device_info() {
     return d;
   }
   bool attr_ok = true;
-  for (int kind = 0; kind < 4; ++kind)
+  for (int kind = 0; kind < 6; ++kind)
     attr_ok = attr_ok && cudaFuncSetAttribute(sparse_kernel_ptr(kind), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                               sparse_smem_bytes()) == cudaSuccess;
-  for (int kind = 0; kind < 9; ++kind)
+  for (int kind = 0; kind < 11; ++kind)
     attr_ok = attr_ok && cudaFuncSetAttribute(dense_kernel_ptr(kind), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                               dense_smem_bytes()) == cudaSuccess;
   attr_ok = attr_ok && cudaFuncSetAttribute(combine_stream_kernel_ptr(), cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -310,7 +310,7 @@ struct SparseCall {
   float* lse = nullptr;
   int32_t* status = nullptr;
   mla_stream_t stream = nullptr;
-  int kind = 0;  // the kernel's instance; 1: the stall-test one (mla_test_decode_timeout), 3: kWarp
+  int kind = 0;  // the kernel's instance (sparse_kernel_ptr)
   const int32_t* live = nullptr;  // kind 3: see DecodeParams
 };
 
@@ -458,13 +458,13 @@ int launch_shared(const SharedLaunch& c, cudaStream_t stream) {
     p.kv8 = static_cast<const uint8_t*>(c.kv);
     p.topk = c.max_pages * MLA_PAGE_SIZE;
     p.unit_request_div = 1;
-    return launch_sparse(qm, p, c.num_parts, 2, stream) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+    return launch_sparse(qm, p, c.num_parts, c.stall ? 4 : 2, stream) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
   }
   rc = encode_kv_map(&km, c.kv, c.num_pages, 1, 4);
   if (rc == MLA_OK) rc = encode_kv_map(&sm, c.kv, c.num_pages, 1, 5);
   if (rc == MLA_OK) rc = encode_kv_map(&rm, c.kv, c.num_pages, 1, 1);
   if (rc != MLA_OK) return rc;
-  const int kind = c.dtype == MLA_DTYPE_FP16 ? 6 : 5;
+  const int kind = c.stall ? 9 : c.dtype == MLA_DTYPE_FP16 ? 6 : 5;
   return launch_dense(qm, km, sm, rm, p, c.num_parts, kind, stream) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
@@ -474,11 +474,11 @@ int launch_shared(const SharedLaunch& c, cudaStream_t stream) {
 int decode_full_blocks(const void* q, const void* kv, const int32_t* block_table, int max_pages, int num_pages,
                        const int32_t* lengths, const int32_t* live, int batch, int s_q, int h_q, int dtype,
                        int causal, float scale, const int32_t* sched, const int32_t* split_offset, int num_parts, void* ws, size_t ws_bytes,
-                       void* out, int out_type, float* lse, int32_t* status, cudaStream_t stream) {
+                       void* out, int out_type, float* lse, int32_t* status, int stall, cudaStream_t stream) {
   if (dtype == MLA_DTYPE_FP8_RECORD) {
     const int rc = fp8_record_splits(q, kv, block_table, max_pages, num_pages, lengths, batch, s_q, h_q, 1, causal,
                                      scale, sched, split_offset, num_parts, ws, ws_bytes, out, out_type, lse, status,
-                                     reinterpret_cast<mla_stream_t>(stream), 3, live);
+                                     reinterpret_cast<mla_stream_t>(stream), stall ? 5 : 3, live);
     if (rc != MLA_OK) return rc;
   } else {
     DecodeParams p;
@@ -489,8 +489,8 @@ int decode_full_blocks(const void* q, const void* kv, const int32_t* block_table
     if (rc != MLA_OK) return rc;
     p.live = live;
     p.live_n = batch;
-    if (launch_dense(qm, km, sm, rm, p, num_parts, dtype == MLA_DTYPE_FP16 ? 8 : 7, stream) != cudaSuccess)
-      return MLA_ERR_CUDA;
+    const int kind = stall ? 10 : dtype == MLA_DTYPE_FP16 ? 8 : 7;
+    if (launch_dense(qm, km, sm, rm, p, num_parts, kind, stream) != cudaSuccess) return MLA_ERR_CUDA;
   }
   return mla_combine(ws, ws_bytes, split_offset, batch, s_q * h_q, num_parts, out, out_type, lse, status,
                      reinterpret_cast<mla_stream_t>(stream));

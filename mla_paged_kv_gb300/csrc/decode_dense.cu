@@ -757,7 +757,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
         if constexpr (kWarp) {
-          if (stuck(progressed, idle, t_last, abort_flag)) {
+          if (stuck(progressed, idle, t_last, abort_flag, kWaitNs)) {
             ok = false;
             break;
           }
@@ -900,7 +900,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
         if constexpr (kWarp) {
-          if (stuck(progressed, idle, t_last, abort_flag)) {
+          if (stuck(progressed, idle, t_last, abort_flag, kWaitNs)) {
             ok = false;
             break;
           }
@@ -1233,7 +1233,8 @@ int dense_smem_bytes() { return dn::kSmemBytes; }
 // kind 0: bf16, 1: fp16, 2: bf16 with the V-ring Q stage, 3: fp16 with it,
 // 4: the bf16 stall-test instance (its first own tile's K slot is never
 // loaded, so a wait runs out and the kernel reports MLA_ERR_TIMEOUT),
-// 5, 6: bf16, fp16 under a shared-prefix plan, 7, 8: bf16, fp16, kWarp
+// 5, 6: bf16, fp16 under a shared-prefix plan, 7, 8: bf16, fp16, kWarp,
+// 9, 10: stall-test instances of 5 and 7
 int dense_threads(int) { return dn::kThreads; }
 const void* dense_kernel_ptr(int kind) {
   switch (kind) {
@@ -1245,6 +1246,8 @@ const void* dense_kernel_ptr(int kind) {
     case 6: return reinterpret_cast<const void*>(&dn::dense_decode_kernel<true, false, false, true>);
     case 7: return reinterpret_cast<const void*>(&dn::dense_decode_kernel<false, false, false, false, true>);
     case 8: return reinterpret_cast<const void*>(&dn::dense_decode_kernel<true, false, false, false, true>);
+    case 9: return reinterpret_cast<const void*>(&dn::dense_decode_kernel<false, false, true, true>);
+    case 10: return reinterpret_cast<const void*>(&dn::dense_decode_kernel<false, false, true, false, true>);
     default: return reinterpret_cast<const void*>(&dn::dense_decode_kernel<false, false, false>);
   }
 }
@@ -1284,6 +1287,14 @@ cudaError_t launch_dense(const CUtensorMap& q_map, const CUtensorMap& kv_map, co
       break;
     case 8:
       dn::dense_decode_kernel<true, false, false, false, true>
+          <<<grid, dn::kThreads, dn::kSmemBytes, stream>>>(q_map, kv_map, sc_map, rope_map, p);
+      break;
+    case 9:
+      dn::dense_decode_kernel<false, false, true, true>
+          <<<grid, dn::kThreads, dn::kSmemBytes, stream>>>(q_map, kv_map, sc_map, rope_map, p);
+      break;
+    case 10:
+      dn::dense_decode_kernel<false, false, true, false, true>
           <<<grid, dn::kThreads, dn::kSmemBytes, stream>>>(q_map, kv_map, sc_map, rope_map, p);
       break;
     default:

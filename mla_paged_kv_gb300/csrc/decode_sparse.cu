@@ -624,7 +624,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
         if constexpr (kWarp) {
-          if (stuck(progressed, idle, t_last, abort_flag)) {
+          if (stuck(progressed, idle, t_last, abort_flag, kWaitNs)) {
             ok = false;
             break;
           }
@@ -1182,18 +1182,26 @@ __global__ void __launch_bounds__(256) unpack_kernel(const uint8_t* __restrict__
 int sparse_smem_bytes() { return sp::kSmemBytes; }
 int sparse_threads() { return sp::kThreads; }
 // kind 1: the test instance whose first tile's scores are never computed;
-// 2: under a shared-prefix plan; 3: kWarp
+// 2: under a shared-prefix plan; 3: kWarp; 4, 5: stall-test instances of 2 and 3
 const void* sparse_kernel_ptr(int kind) {
-  return kind == 3   ? reinterpret_cast<const void*>(&sp::sparse_decode_kernel<false, false, true>)
-         : kind == 2   ? reinterpret_cast<const void*>(&sp::sparse_decode_kernel<false, true>)
-         : kind == 1 ? reinterpret_cast<const void*>(&sp::sparse_decode_kernel<true>)
-                     : reinterpret_cast<const void*>(&sp::sparse_decode_kernel<false>);
+  switch (kind) {
+    case 1: return reinterpret_cast<const void*>(&sp::sparse_decode_kernel<true>);
+    case 2: return reinterpret_cast<const void*>(&sp::sparse_decode_kernel<false, true>);
+    case 3: return reinterpret_cast<const void*>(&sp::sparse_decode_kernel<false, false, true>);
+    case 4: return reinterpret_cast<const void*>(&sp::sparse_decode_kernel<true, true>);
+    case 5: return reinterpret_cast<const void*>(&sp::sparse_decode_kernel<true, false, true>);
+    default: return reinterpret_cast<const void*>(&sp::sparse_decode_kernel<false>);
+  }
 }
 
 cudaError_t launch_sparse(const CUtensorMap& q_map, const DecodeParams& p, int num_parts, int kind,
                           cudaStream_t stream) {
   const dim3 grid(2 * num_parts * p.row_blocks);
-  if (kind == 3)
+  if (kind == 5)
+    sp::sparse_decode_kernel<true, false, true><<<grid, sp::kThreads, sp::kSmemBytes, stream>>>(q_map, p);
+  else if (kind == 4)
+    sp::sparse_decode_kernel<true, true><<<grid, sp::kThreads, sp::kSmemBytes, stream>>>(q_map, p);
+  else if (kind == 3)
     sp::sparse_decode_kernel<false, false, true><<<grid, sp::kThreads, sp::kSmemBytes, stream>>>(q_map, p);
   else if (kind == 2)
     sp::sparse_decode_kernel<false, true><<<grid, sp::kThreads, sp::kSmemBytes, stream>>>(q_map, p);

@@ -305,11 +305,16 @@ __device__ __forceinline__ void fail(volatile int* abort_flag, int32_t* status) 
   report(status, MLA_ERR_TIMEOUT);
 }
 
-template <bool kHalf, int kQBoxes, bool kPair>
+// Wait budget of the stall-test instances (kStall), whose first K stage is never
+// loaded; the others keep the 2 s budget of every wait.
+constexpr uint64_t kStallWaitNs = 200000;  // 200 us
+
+template <bool kHalf, int kQBoxes, bool kPair, bool kStall = false>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                   const __grid_constant__ CUtensorMap v_map, const PromptParams p) {
   using L = Layout<kQBoxes, kPair>;
+  constexpr uint64_t kWaitNs = kStall ? kStallWaitNs : MLA_WAIT_LIMIT_NS;
   const uint32_t rank = kPair ? cluster_ctarank() : 0u;
   const int worker = kPair ? blockIdx.x >> 1 : blockIdx.x;
   const int workers = kPair ? gridDim.x >> 1 : gridDim.x;
@@ -420,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int h = 0; h < 2 && ok; ++h) {
             if ((h ? n1 : n0) == 0) continue;
             const uint32_t before = h ? q1n++ : q0n++;
-            if (before >= 1) ok = mbar_wait(&bars[Q_EMPTY + h], (before - 1) & 1, abort_flag);
+            if (before >= 1) ok = mbar_wait(&bars[Q_EMPTY + h], (before - 1) & 1, abort_flag, kWaitNs);
             if (!ok) break;
             expect(Q_FULL + h, kQBoxes * kBoxBytes);
             load(sQ + h * kQBoxes * kBoxBytes, &q_map, Q_FULL + h,
@@ -431,8 +436,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0)
           for (int j = 0; j < n && ok; ++j, ++n_loaded) {
             const int s = static_cast<int>(n_loaded % L::kKStages), r = static_cast<int>(n_loaded / L::kKStages);
-            if (r >= 1) ok = mbar_wait(&bars[K_EMPTY + s], (r - 1) & 1, abort_flag);
-            if (ok) {
+            if (r >= 1) ok = mbar_wait(&bars[K_EMPTY + s], (r - 1) & 1, abort_flag, kWaitNs);
+            if (ok && !(kStall && rank == 0 && n_loaded == 0)) {
               expect(K_FULL + s, L::kKBytes);
               load(sK + s * L::kKBytes, &k_map, K_FULL + s, t.k0 + j * kBN + static_cast<int>(rank) * L::kKeys, 0, kvh,
                    pol_kv);
@@ -445,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int s = static_cast<int>(n_loaded % L::kVStages), r = static_cast<int>(n_loaded / L::kVStages);
           uint8_t* dst = sV + s * L::kVBytes;
           if (lane == 0) {
-            if (r >= 1) ok = mbar_wait(&bars[V_EMPTY + s], (r - 1) & 1, abort_flag);
+            if (r >= 1) ok = mbar_wait(&bars[V_EMPTY + s], (r - 1) & 1, abort_flag, kWaitNs);
             if (ok && tail) {  // onto this CTA's own barrier
               mbar_arrive_expect_tx(&bars[TAIL], L::kVBytes);
               tma_load_4d(dst, &v_map, &bars[TAIL], 0, t.k0 + j * kBN, kPair ? static_cast<int>(rank) : 0, kvh, pol_kv);
@@ -456,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           ok = __shfl_sync(0xffffffffu, ok, 0);
           if (!ok || !tail) continue;
-          ok = __all_sync(0xffffffffu, mbar_wait(&bars[TAIL], tails & 1, abort_flag));
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars[TAIL], tails & 1, abort_flag, kWaitNs));
           ++tails;
           if (!ok) continue;
           const int keep = t.lk - j * kBN;  // rows of this tile that are the sequence's
@@ -497,11 +502,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t k_desc = sdesc_sw128(smem_u32(sK), 16, 1024);
       const uint64_t v_desc = sdesc_sw128(smem_u32(sV), kBoxBytes, 1024);  // MN-major
       auto wait = [&](int bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait(&bars[bar], parity, abort_flag));
+        return __all_sync(0xffffffffu, mbar_wait(&bars[bar], parity, abort_flag, kWaitNs));
       };
       // a stage of V may hold rows that threads of the other CTA zeroed
       auto wait_v = [&](int bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait<kPair>(&bars[bar], parity, abort_flag));
+        return __all_sync(0xffffffffu, mbar_wait<kPair>(&bars[bar], parity, abort_flag, kWaitNs));
       };
       auto commit = [&](int bar) {
         if constexpr (kPair)
@@ -599,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok && lane == 0) fail(abort_flag, p.status);
       // every MMA is done with shared memory and TMEM before this CTA ends
       commit(DRAIN);
-      mbar_wait(&bars[DRAIN], 0, nullptr);
+      mbar_wait(&bars[DRAIN], 0, nullptr, kWaitNs);
     }
     __syncwarp();
   } else if (warp < kWarpMma) {
@@ -631,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (it.at < it.total) {
       float ref = -INFINITY, l = 0.f;
       for (int j = 0; j < nh; ++j, ++tiles) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars[S_FULL + h], tiles & 1, abort_flag));
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars[S_FULL + h], tiles & 1, abort_flag, kWaitNs));
         tc_fence_after();
         float s[64];
         float m0, m1;
@@ -709,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       next_item(it, worker, workers, p.h_q);
       const Tile t_next = load_tile(p, it);
       if (nh > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars[O_FULL + h], items & 1, abort_flag));
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars[O_FULL + h], items & 1, abort_flag, kWaitNs));
         ++items;
         tc_fence_after();
         // the row's sum over both warps, in an order that both share
@@ -933,7 +938,8 @@ namespace {
 
 using PromptKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, PromptParams);
 
-PromptKernel prompt_kernel_of(bool half, int d_qk, bool pair) {
+PromptKernel prompt_kernel_of(bool half, int d_qk, bool pair, bool stall = false) {
+  if (stall) return pair ? pr::prompt_kernel<false, 3, true, true> : pr::prompt_kernel<false, 3, false, true>;
   if (d_qk == 192) {
     if (half) return pair ? pr::prompt_kernel<true, 3, true> : pr::prompt_kernel<true, 3, false>;
     return pair ? pr::prompt_kernel<false, 3, true> : pr::prompt_kernel<false, 3, false>;
@@ -950,17 +956,18 @@ int prompt_smem(int d_qk, bool pair) {
 }  // namespace
 
 cudaError_t prompt_setup() {
-  for (int v = 0; v < 8; ++v) {
-    const int d_qk = v & 1 ? 192 : 128;
-    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(prompt_kernel_of(v & 2, d_qk, v & 4)),
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, prompt_smem(d_qk, v & 4));
+  for (int v = 0; v < 10; ++v) {
+    const bool stall = v >= 8, pair = stall ? v & 1 : v & 4;
+    const int d_qk = stall || (v & 1) ? 192 : 128;
+    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(prompt_kernel_of(v & 2, d_qk, pair, stall)),
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, prompt_smem(d_qk, pair));
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
 
 cudaError_t launch_prompt(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PromptParams& p,
-                          bool half, int d_qk, bool pair, int sms, cudaStream_t st) {
+                          bool half, int d_qk, bool pair, bool stall, int sms, cudaStream_t st) {
   const int ctas = pair ? 2 : 1;
   const long long items = static_cast<long long>(p.max_tiles) * p.h_q;
   const int most = pair ? std::min(sms / 2, pr::kMaxWorkers) : sms;
@@ -977,7 +984,7 @@ cudaError_t launch_prompt(const CUtensorMap& q, const CUtensorMap& k, const CUte
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prompt_kernel_of(half, d_qk, pair), q, k, v, p);
+  return cudaLaunchKernelEx(&cfg, prompt_kernel_of(half, d_qk, pair, stall), q, k, v, p);
 }
 
 }  // namespace mla

@@ -624,7 +624,7 @@ __device__ __forceinline__ void pdl_launch_dependents() {
 // the wait budget, or another role gave up.  The clock is read only once in 256
 // idle passes.
 __device__ __forceinline__ bool stuck(bool progressed, uint32_t& idle, uint64_t& t_last,
-                                      const volatile int* abort_flag) {
+                                      const volatile int* abort_flag, uint64_t limit_ns) {
   if (progressed) {
     idle = 0;
     return false;
@@ -632,7 +632,7 @@ __device__ __forceinline__ bool stuck(bool progressed, uint32_t& idle, uint64_t&
   if ((++idle & 255u) != 0) return false;
   const uint64_t now = globaltimer_ns();
   if (idle == 256u) t_last = now;
-  return __any_sync(0xffffffffu, *abort_flag != 0 || now - t_last > MLA_WAIT_LIMIT_NS);
+  return __any_sync(0xffffffffu, *abort_flag != 0 || now - t_last > limit_ns);
 }
 
 // The two issuers run on one lane, or (kWarp) on a converged warp that elects

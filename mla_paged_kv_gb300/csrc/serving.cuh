@@ -28,12 +28,13 @@ struct SharedLaunch {
   const int32_t *block_table, *units, *lengths, *sched, *split_offset;
   float *o_accum, *lse_accum;  // [slots][128][512], [slots][128]
   int32_t* status;
+  int stall;  // 1: the stall-test instances
 };
 int launch_shared(const SharedLaunch& c, cudaStream_t stream);
 int decode_full_blocks(const void* q, const void* kv, const int32_t* block_table, int max_pages, int num_pages,
                        const int32_t* lengths, const int32_t* live, int batch, int s_q, int h_q, int dtype,
                        int causal, float scale, const int32_t* sched, const int32_t* split_offset, int num_parts,
-                       void* ws, size_t ws_bytes, void* out, int out_type, float* lse, int32_t* status,
+                       void* ws, size_t ws_bytes, void* out, int out_type, float* lse, int32_t* status, int stall,
                        cudaStream_t stream);
 cudaError_t launch_plan(const int32_t* lengths, int n_units, int num_parts, int32_t* sched, int32_t* split_offset,
                         cudaStream_t stream);
@@ -108,6 +109,6 @@ cudaError_t launch_prompt_plan(const int32_t* cu_q, const int32_t* cu_k, int bat
                                int causal, void* plan, int32_t* status, cudaStream_t st);
 cudaError_t prompt_setup();  // once per device: shared-memory opt-in
 cudaError_t launch_prompt(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PromptParams& p,
-                          bool half, int d_qk, bool pair, int sms, cudaStream_t st);
+                          bool half, int d_qk, bool pair, bool stall, int sms, cudaStream_t st);
 
 }  // namespace mla

@@ -132,7 +132,8 @@ int prompt_attention(const void* d_q, long long q_token_stride, long long q_head
                      long long k_token_stride, long long k_head_stride, const void* d_v, long long v_token_stride,
                      long long v_head_stride, int dtype, int total_q, int total_k, int batch, int h_q, int h_kv,
                      int d_qk, float softmax_scale, const int32_t* cu_q, const int32_t* cu_k, const void* d_plan,
-                     size_t plan_bytes, void* d_out, float* d_lse, int32_t* d_status, mla_stream_t stream) {
+                     size_t plan_bytes, void* d_out, float* d_lse, int32_t* d_status, bool stall,
+                     mla_stream_t stream) {
   if (!d_plan || !d_status || batch < 1 || total_q < 0 || total_k < 0 || h_q < 1 || h_kv < 1 || h_q % h_kv != 0)
     return MLA_ERR_INVALID_ARG;
   if (total_q > 0 && (!d_q || !d_out || !d_lse)) return MLA_ERR_INVALID_ARG;
@@ -180,14 +181,14 @@ int prompt_attention(const void* d_q, long long q_token_stride, long long q_head
       rc = head_map(&vm, d_v, total_k, h_kv, 128, v_token_stride, v_head_stride, 128, pair ? 1 : 2);
   }
   if (rc != MLA_OK) return rc;
-  return launched(launch_prompt(qm, km, vm, p, dtype == MLA_DTYPE_FP16, d_qk, pair, sms, to_stream(stream)));
+  return launched(launch_prompt(qm, km, vm, p, dtype == MLA_DTYPE_FP16, d_qk, pair, stall, sms, to_stream(stream)));
 }
 
 // mla_shared_prefix_decode_fwd, with lengths to be compared with the plan's or NULL.
 int shared_decode(const void* d_q, const void* d_kv, const int32_t* d_block_table, int max_pages, int num_pages,
                   int batch, int s_q, int h_q, int dtype, int causal, float softmax_scale, const int32_t* live,
                   const void* d_plan, size_t plan_bytes, int num_parts, void* d_workspace, size_t workspace_bytes,
-                  void* d_out, int out_type, float* d_lse, int32_t* d_status, mla_stream_t stream) {
+                  void* d_out, int out_type, float* d_lse, int32_t* d_status, int stall, mla_stream_t stream) {
   if (!d_q || !d_kv || !d_block_table || !d_plan || !d_workspace || !d_out || !d_lse || !d_status)
     return MLA_ERR_INVALID_ARG;
   if (max_pages < 1 || num_pages < 1) return MLA_ERR_INVALID_ARG;
@@ -215,7 +216,7 @@ int shared_decode(const void* d_q, const void* d_kv, const int32_t* d_block_tabl
                               reinterpret_cast<const int32_t*>(plan + z.lengths_off), live, batch, s_q, h_q, dtype, causal,
                               softmax_scale, reinterpret_cast<const int32_t*>(plan + z.sched_off),
                               reinterpret_cast<const int32_t*>(plan + z.offset_off), num_parts, d_workspace,
-                              workspace_bytes, d_out, out_type, d_lse, d_status, to_stream(stream));
+                              workspace_bytes, d_out, out_type, d_lse, d_status, stall, to_stream(stream));
   SharedLaunch c{};
   c.q = d_q;
   c.kv = d_kv;
@@ -238,6 +239,7 @@ int shared_decode(const void* d_q, const void* d_kv, const int32_t* d_block_tabl
   c.o_accum = static_cast<float*>(d_workspace);
   c.lse_accum = reinterpret_cast<float*>(static_cast<char*>(d_workspace) + z.lse_off);
   c.status = d_status;
+  c.stall = stall;
   const cudaStream_t st = to_stream(stream);
   rc = launch_shared(c, st);
   if (rc != MLA_OK) return rc;
@@ -393,7 +395,7 @@ int mla_prompt_attention_fwd(const void* d_q, long long q_token_stride, long lon
                              size_t plan_bytes, void* d_out, float* d_lse, int32_t* d_status, mla_stream_t stream) {
   return prompt_attention(d_q, q_token_stride, q_head_stride, d_k, k_token_stride, k_head_stride, d_v, v_token_stride,
                           v_head_stride, dtype, total_q, total_k, batch, h_q, h_kv, d_qk, softmax_scale, nullptr,
-                          nullptr, d_plan, plan_bytes, d_out, d_lse, d_status, stream);
+                          nullptr, d_plan, plan_bytes, d_out, d_lse, d_status, false, stream);
 }
 
 int mla_prompt_attention_checked_fwd(const void* d_q, long long q_token_stride, long long q_head_stride,
@@ -407,7 +409,18 @@ int mla_prompt_attention_checked_fwd(const void* d_q, long long q_token_stride, 
   return prompt_attention(d_q, q_token_stride, q_head_stride, d_k, k_token_stride, k_head_stride, d_v, v_token_stride,
                           v_head_stride, dtype, total_q, total_k, batch, h_q, h_kv, d_qk, softmax_scale,
                           d_cu_seqlens_q, d_cu_seqlens_k ? d_cu_seqlens_k : d_cu_seqlens_q, d_plan, plan_bytes, d_out,
-                          d_lse, d_status, stream);
+                          d_lse, d_status, false, stream);
+}
+
+int mla_test_prompt_timeout(const void* d_q, long long q_token_stride, long long q_head_stride, const void* d_k,
+                            long long k_token_stride, long long k_head_stride, const void* d_v,
+                            long long v_token_stride, long long v_head_stride, int dtype, int total_q, int total_k,
+                            int batch, int h_q, int h_kv, int d_qk, float softmax_scale, const void* d_plan,
+                            size_t plan_bytes, void* d_out, float* d_lse, int32_t* d_status, mla_stream_t stream) {
+  if (dtype != MLA_DTYPE_BF16 || d_qk != 192) return MLA_ERR_UNSUPPORTED;
+  return prompt_attention(d_q, q_token_stride, q_head_stride, d_k, k_token_stride, k_head_stride, d_v, v_token_stride,
+                          v_head_stride, dtype, total_q, total_k, batch, h_q, h_kv, d_qk, softmax_scale, nullptr,
+                          nullptr, d_plan, plan_bytes, d_out, d_lse, d_status, true, stream);
 }
 
 int mla_shared_prefix_num_parts(int batch, int s_q, int h_q) {
@@ -459,7 +472,7 @@ int mla_shared_prefix_decode_fwd(const void* d_q, const void* d_kv, const int32_
                                  int32_t* d_status, mla_stream_t stream) {
   return shared_decode(d_q, d_kv, d_block_table, max_pages, num_pages, batch, s_q, h_q, dtype, causal, softmax_scale,
                        nullptr, d_plan, plan_bytes, num_parts, d_workspace, workspace_bytes, d_out, out_type, d_lse,
-                       d_status, stream);
+                       d_status, 0, stream);
 }
 
 int mla_shared_prefix_decode_checked_fwd(const void* d_q, const void* d_kv, const int32_t* d_block_table,
@@ -471,7 +484,18 @@ int mla_shared_prefix_decode_checked_fwd(const void* d_q, const void* d_kv, cons
   if (!d_cache_seqlens) return MLA_ERR_INVALID_ARG;
   return shared_decode(d_q, d_kv, d_block_table, max_pages, num_pages, batch, s_q, h_q, dtype, causal, softmax_scale,
                        d_cache_seqlens, d_plan, plan_bytes, num_parts, d_workspace, workspace_bytes, d_out, out_type,
-                       d_lse, d_status, stream);
+                       d_lse, d_status, 0, stream);
+}
+
+int mla_test_shared_prefix_timeout(const void* d_q, const void* d_kv, const int32_t* d_block_table, int max_pages,
+                                   int num_pages, int batch, int s_q, int h_q, int dtype, int causal,
+                                   float softmax_scale, const void* d_plan, size_t plan_bytes, int num_parts,
+                                   void* d_workspace, size_t workspace_bytes, void* d_out, int out_type, float* d_lse,
+                                   int32_t* d_status, mla_stream_t stream) {
+  if (dtype == MLA_DTYPE_FP16) return MLA_ERR_UNSUPPORTED;
+  return shared_decode(d_q, d_kv, d_block_table, max_pages, num_pages, batch, s_q, h_q, dtype, causal, softmax_scale,
+                       nullptr, d_plan, plan_bytes, num_parts, d_workspace, workspace_bytes, d_out, out_type, d_lse,
+                       d_status, 1, stream);
 }
 
 int mla_serving_call(int op, const void* args, size_t bytes) {

@@ -53,6 +53,9 @@ SERVING_SIGS = {
                                                   _P, _I, _P, _P, _P]),
     "mla_serving_call": (_I, [_I, ctypes.c_char_p, _SZ]),
 }
+for _hook, _of in (("mla_test_prompt_timeout", "mla_prompt_attention_fwd"),
+                   ("mla_test_shared_prefix_timeout", "mla_shared_prefix_decode_fwd")):
+    SERVING_SIGS[_hook] = SERVING_SIGS[_of]
 SERVING_SYMBOLS = tuple(SERVING_SIGS)
 
 __all__ = [n for n in SERVING_SYMBOLS] + [
@@ -363,9 +366,10 @@ def mla_prompt_get_plan(cu_seqlens_q, cu_seqlens_k, total_q, total_k, causal, pl
         "mla_prompt_get_plan")
 
 
-def _prompt(q, k, v, pl, softmax_scale, status, stream, out=None, lse=None, cu_seqlens_q=None, cu_seqlens_k=None):
-    """The checks and the call of mla_prompt_attention_fwd (with offsets, _checked_fwd); allocates out and lse if
-    not given."""
+def _prompt(q, k, v, pl, softmax_scale, status, stream, out=None, lse=None, cu_seqlens_q=None, cu_seqlens_k=None,
+            hook=False):
+    """The checks and the call of mla_prompt_attention_fwd (with offsets, _checked_fwd; hook:
+    mla_test_prompt_timeout); allocates out and lse if not given."""
     dt = q.dtype
     code = _DTYPE_CODE16.get(dt)
     if code is None or k.dtype is not dt or v.dtype is not dt:
@@ -400,9 +404,12 @@ def _prompt(q, k, v, pl, softmax_scale, status, stream, out=None, lse=None, cu_s
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(d)
     if cu_seqlens_q is None:
-        _call(_PROMPT, "mla_prompt_attention_fwd", q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1],
-              v.data_ptr(), vs[0], vs[1], code, total_q, total_k, pl.batch, h_q, h_kv, d, softmax_scale, plan,
-              pl.bytes, out_ptr, lse_ptr, st, queue)
+        args = (q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], code, total_q,
+                total_k, pl.batch, h_q, h_kv, d, softmax_scale, plan, pl.bytes, out_ptr, lse_ptr, st, queue)
+        if hook:
+            _check(load_library().mla_test_prompt_timeout(*args), "mla_test_prompt_timeout")
+        else:
+            _call(_PROMPT, "mla_prompt_attention_fwd", *args)
         return out, lse
     cu_q, cu_k = _p(cu_seqlens_q, _INT32, 1, dev, "cu_seqlens_q"), 0
     if cu_seqlens_k is not None:
@@ -427,6 +434,11 @@ def mla_prompt_attention_checked_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, pl, ou
     """mla_prompt_attention_fwd that also compares the offsets [batch + 1] (cu_seqlens_k None: the same) with the
     plan's on the device: others are MLA_ERR_STALE_PLAN in status."""
     _prompt(q, k, v, pl, softmax_scale, status, stream, out, lse, cu_seqlens_q, cu_seqlens_k)
+
+
+def mla_test_prompt_timeout(q, k, v, pl, out, lse, status, softmax_scale=None, stream=None):
+    """Test hook: mla_prompt_attention_fwd whose first key tile is never loaded (status: MLA_ERR_TIMEOUT)."""
+    _prompt(q, k, v, pl, softmax_scale, status, stream, out, lse, hook=True)
 
 
 def plan_prompt(cu_seqlens_q, cu_seqlens_k=None, total_q=None, total_k=None, causal=True, status=None):
@@ -511,9 +523,9 @@ def mla_shared_prefix_get_plan(block_table, cache_seqlens, s_q, h_q, causal, num
 
 
 def _shared_prefix(q, kv, block_table, pl, softmax_scale, status, stream, out=None, lse=None, out_dtype=None,
-                   cache_seqlens=None):
-    """The checks and the call of mla_shared_prefix_decode_fwd (with lengths, _checked_fwd); allocates out and lse
-    if not given."""
+                   cache_seqlens=None, hook=False):
+    """The checks and the call of mla_shared_prefix_decode_fwd (with lengths, _checked_fwd; hook:
+    mla_test_shared_prefix_timeout); allocates out and lse if not given."""
     dt = q.dtype
     code = _DTYPE_CODE16.get(dt)
     fp8 = kv.dtype is _UINT8
@@ -544,9 +556,13 @@ def _shared_prefix(q, kv, block_table, pl, softmax_scale, status, stream, out=No
         if out.shape != (B, s_q, h_q, 512) or lse.shape != (B, s_q, h_q):
             raise ValueError("out must be [B, s_q, h_q, 512] and lse [B, s_q, h_q]")
     if cache_seqlens is None:
-        _call(_SHARED_PREFIX, "mla_shared_prefix_decode_fwd", q_ptr, kv_ptr, table_ptr, max_pages, pages, B, s_q, h_q,
-              DTYPE_FP8_RECORD if fp8 else code, 1 if pl.causal else 0, softmax_scale, plan_ptr, plan.shape[0],
-              pl.num_parts, ws_ptr, ws.shape[0], out_ptr, _DTYPE_CODE[out_dtype], lse_ptr, st, queue)
+        args = (q_ptr, kv_ptr, table_ptr, max_pages, pages, B, s_q, h_q, DTYPE_FP8_RECORD if fp8 else code,
+                1 if pl.causal else 0, softmax_scale, plan_ptr, plan.shape[0], pl.num_parts, ws_ptr, ws.shape[0],
+                out_ptr, _DTYPE_CODE[out_dtype], lse_ptr, st, queue)
+        if hook:
+            _check(load_library().mla_test_shared_prefix_timeout(*args), "mla_test_shared_prefix_timeout")
+        else:
+            _call(_SHARED_PREFIX, "mla_shared_prefix_decode_fwd", *args)
         return out, lse
     lens_ptr = _p(cache_seqlens, _INT32, 1, dev, "cache_seqlens")
     if cache_seqlens.shape[0] != B:
@@ -570,6 +586,11 @@ def mla_shared_prefix_decode_checked_fwd(q, kv, block_table, cache_seqlens, pl, 
     """mla_shared_prefix_decode_fwd that also compares the lengths [B] with the plan's on the device: another
     length, or a request that no longer ends its shared pages on the shared one, is MLA_ERR_STALE_PLAN in status."""
     _shared_prefix(q, kv, block_table, pl, softmax_scale, status, stream, out, lse, cache_seqlens=cache_seqlens)
+
+
+def mla_test_shared_prefix_timeout(q, kv, block_table, pl, out, lse, status, softmax_scale=1.0 / 24.0, stream=None):
+    """Test hook: mla_shared_prefix_decode_fwd whose first tile never comes (status: MLA_ERR_TIMEOUT)."""
+    _shared_prefix(q, kv, block_table, pl, softmax_scale, status, stream, out, lse, hook=True)
 
 
 def plan_shared_prefix(block_table, cache_seqlens, s_q, h_q, causal=False, num_parts=None):
