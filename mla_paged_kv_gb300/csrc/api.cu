@@ -20,11 +20,11 @@ cudaError_t launch_combine(const float*, const float*, const int32_t*, int, int,
 const void* combine_stream_kernel_ptr();
 int combine_stream_smem_bytes();
 cudaError_t launch_dense(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
-                         const DecodeParams&, int, int, cudaStream_t);
+                         const DecodeParams&, int, int, cudaStream_t, const LiveLengths& live = {});
 int dense_smem_bytes();
 int dense_threads(int kind);
 const void* dense_kernel_ptr(int kind);
-cudaError_t launch_sparse(const CUtensorMap&, const DecodeParams&, int, int, cudaStream_t);
+cudaError_t launch_sparse(const CUtensorMap&, const DecodeParams&, int, int, cudaStream_t, const LiveLengths& live = {});
 int sparse_smem_bytes();
 int sparse_threads();
 const void* sparse_kernel_ptr(int kind);
@@ -311,7 +311,7 @@ struct SparseCall {
   int32_t* status = nullptr;
   mla_stream_t stream = nullptr;
   int kind = 0;  // the kernel's instance (sparse_kernel_ptr)
-  const int32_t* live = nullptr;  // kind 3: see DecodeParams
+  const int32_t* live = nullptr;  // kWarp kinds: see LiveLengths
 };
 
 int sparse_run(const SparseCall& c, bool combine) {
@@ -362,13 +362,11 @@ int sparse_run(const SparseCall& c, bool combine) {
   p.out_type = c.out_type;
   p.lse = c.lse;
   p.status = c.status;
-  p.live = c.live;
-  p.live_n = c.n_units;
   CUtensorMap qm;
   const int rc = encode_q_map(&qm, c.q, static_cast<long long>(c.n_units) * c.rows);
   if (rc != MLA_OK) return rc;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(c.stream);
-  if (launch_sparse(qm, p, c.num_parts, c.kind, s) != cudaSuccess) return MLA_ERR_CUDA;
+  if (launch_sparse(qm, p, c.num_parts, c.kind, s, LiveLengths{c.live, c.n_units}) != cudaSuccess) return MLA_ERR_CUDA;
   if (!combine) return MLA_OK;
   return mla_combine(c.ws, c.ws_bytes, c.split_offset, c.n_units, c.rows, c.num_parts, c.out, c.out_type, c.lse,
                      c.status, c.stream);
@@ -440,10 +438,8 @@ int launch_shared(const SharedLaunch& c, cudaStream_t stream) {
   p.max_pages = c.max_pages;
   p.num_pages = c.num_pages;
   p.units = c.units;
-  p.live = c.live;
-  p.live_n = c.batch;
-  p.live_per = ceil_div_i(c.s_q * c.h_q, MLA_ROWS_PER_BLOCK);
-  p.live_u0 = c.n_units - c.batch * p.live_per;
+  const int per = ceil_div_i(c.s_q * c.h_q, MLA_ROWS_PER_BLOCK);
+  const LiveLengths live{c.live, c.batch, c.n_units - c.batch * per, per};
   p.sched = c.sched;
   p.split_offset = c.split_offset;
   p.num_parts = c.num_parts;
@@ -458,14 +454,14 @@ int launch_shared(const SharedLaunch& c, cudaStream_t stream) {
     p.kv8 = static_cast<const uint8_t*>(c.kv);
     p.topk = c.max_pages * MLA_PAGE_SIZE;
     p.unit_request_div = 1;
-    return launch_sparse(qm, p, c.num_parts, c.stall ? 4 : 2, stream) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+    return launch_sparse(qm, p, c.num_parts, c.stall ? 4 : 2, stream, live) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
   }
   rc = encode_kv_map(&km, c.kv, c.num_pages, 1, 4);
   if (rc == MLA_OK) rc = encode_kv_map(&sm, c.kv, c.num_pages, 1, 5);
   if (rc == MLA_OK) rc = encode_kv_map(&rm, c.kv, c.num_pages, 1, 1);
   if (rc != MLA_OK) return rc;
   const int kind = c.stall ? 9 : c.dtype == MLA_DTYPE_FP16 ? 6 : 5;
-  return launch_dense(qm, km, sm, rm, p, c.num_parts, kind, stream) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  return launch_dense(qm, km, sm, rm, p, c.num_parts, kind, stream, live) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 // mla_decode_fwd for a shared-prefix call whose requests (nearly) fill their row
@@ -487,10 +483,9 @@ int decode_full_blocks(const void* q, const void* kv, const int32_t* block_table
                                  scale, sched, split_offset, num_parts, ws, ws_bytes, out, out_type, lse, status, &p,
                                  &qm, &km, &sm, &rm);
     if (rc != MLA_OK) return rc;
-    p.live = live;
-    p.live_n = batch;
     const int kind = stall ? 10 : dtype == MLA_DTYPE_FP16 ? 8 : 7;
-    if (launch_dense(qm, km, sm, rm, p, num_parts, kind, stream) != cudaSuccess) return MLA_ERR_CUDA;
+    if (launch_dense(qm, km, sm, rm, p, num_parts, kind, stream, LiveLengths{live, batch}) != cudaSuccess)
+      return MLA_ERR_CUDA;
   }
   return mla_combine(ws, ws_bytes, split_offset, batch, s_q * h_q, num_parts, out, out_type, lse, status,
                      reinterpret_cast<mla_stream_t>(stream));

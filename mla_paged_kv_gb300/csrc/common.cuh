@@ -70,11 +70,6 @@ struct DecodeParams {
   // shared-prefix plan (kShared instances): what each unit is, kUnitInts int32
   // each (SharedUnit); rows = 128, a unit's rows being its own count
   const int32_t* units;
-  // kWarp instances: the caller's lengths [live_n], to be compared with those of
-  // the plan (check_plan), or NULL; under a shared-prefix plan request b's first
-  // own unit is live_u0 + b * live_per
-  const int32_t* live;
-  int live_n, live_u0, live_per;
   // schedule
   const int32_t* sched;
   const int32_t* split_offset;
@@ -88,6 +83,25 @@ struct DecodeParams {
   int32_t* status;
 };
 
+// The kWarp instances' further parameters: the caller's lengths [n], to be
+// compared with those of the plan (check_plan), or NULL; under a shared-prefix
+// plan request b's first own unit is first + b * per.
+struct LiveLengths {
+  const int32_t* lengths = nullptr;
+  int n = 0, first = 0, per = 0;
+};
+struct WarpParams : DecodeParams {
+  LiveLengths live;
+};
+template <bool kWarp>
+struct KernelParams {
+  using type = DecodeParams;
+};
+template <>
+struct KernelParams<true> {
+  using type = WarpParams;
+};
+
 __device__ __forceinline__ SharedUnit load_unit(const DecodeParams& p, int u) {
   const int32_t* e = p.units + u * kUnitInts;
   return SharedUnit{e[0], e[1], e[2], e[3], e[4]};
@@ -99,18 +113,19 @@ __device__ __forceinline__ SharedUnit load_unit(const DecodeParams& p, int u) {
 // plan either way.  (In the softmax warps, before their first tile, it took 3% of
 // the kernel.)
 template <bool kShared>
-__device__ __forceinline__ void check_plan(const DecodeParams& p, int thread, int threads) {
-  if (p.live == nullptr) return;
-  for (int b = thread; b < p.live_n; b += threads) {
+__device__ __forceinline__ void check_plan(const WarpParams& p, int thread, int threads) {
+  const LiveLengths& live = p.live;
+  if (live.lengths == nullptr) return;
+  for (int b = thread; b < live.n; b += threads) {
     bool same;
     if constexpr (kShared) {
-      const int u = p.live_u0 + b * p.live_per;
+      const int u = live.first + b * live.per;
       const SharedUnit su = load_unit(p, u), front = load_unit(p, 0);
       const int skip = su.table_off - b * p.max_pages;  // shared pages
-      same = p.lengths[u] + skip * kTile == max(p.live[b], 0) &&
+      same = p.lengths[u] + skip * kTile == max(live.lengths[b], 0) &&
              (skip == 0 || p.block_table[su.table_off - 1] == p.block_table[front.table_off + skip - 1]);
     } else {
-      same = p.lengths[b] == p.live[b];
+      same = p.lengths[b] == live.lengths[b];
     }
     if (!same) report(p.status, MLA_ERR_STALE_PLAN);
   }

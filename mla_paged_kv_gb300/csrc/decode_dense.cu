@@ -400,7 +400,7 @@ template <bool kHalf, bool kQV, bool kStall, bool kShared = false, bool kWarp = 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     dense_decode_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kv_map,
                         const __grid_constant__ CUtensorMap sc_map, const __grid_constant__ CUtensorMap rope_map,
-                        const DecodeParams p) {
+                        const typename KernelParams<kWarp>::type p) {
   constexpr uint64_t kWaitNs = kStall ? kStallWaitNs : MLA_WAIT_LIMIT_NS;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -1108,6 +1108,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       cursor_next(p, P, c);
       if (!last) continue;
       // ---- row sum of the unit: ours + the peer's, both relative to r_cur
+      // From here to the barriers of the epilogue the four warps wait for the same
+      // phases, whatever role gave up meanwhile (their own budget ends a wait): one
+      // that left by itself would leave the others at a barrier for good.
       if (units >= 1) {
         ok = warp_wait_cluster(&bars[L_FREE], (units - 1) & 1, abort_flag, kWaitNs);
         if (!ok) break;
@@ -1254,7 +1257,8 @@ const void* dense_kernel_ptr(int kind) {
 
 cudaError_t launch_dense(const CUtensorMap& q_map, const CUtensorMap& kv_map, const CUtensorMap& sc_map,
                          const CUtensorMap& rope_map, const DecodeParams& p, int num_parts, int kind,
-                         cudaStream_t stream) {
+                         cudaStream_t stream, const LiveLengths& live) {
+  const WarpParams w{p, live};
   const dim3 grid(2 * num_parts * p.row_blocks);
   switch (kind) {
     case 1:
@@ -1275,27 +1279,27 @@ cudaError_t launch_dense(const CUtensorMap& q_map, const CUtensorMap& kv_map, co
       break;
     case 5:
       dn::dense_decode_kernel<false, false, false, true>
-          <<<grid, dn::kThreads, dn::kSmemBytes, stream>>>(q_map, kv_map, sc_map, rope_map, p);
+          <<<grid, dn::kThreads, dn::kSmemBytes, stream>>>(q_map, kv_map, sc_map, rope_map, w);
       break;
     case 6:
       dn::dense_decode_kernel<true, false, false, true>
-          <<<grid, dn::kThreads, dn::kSmemBytes, stream>>>(q_map, kv_map, sc_map, rope_map, p);
+          <<<grid, dn::kThreads, dn::kSmemBytes, stream>>>(q_map, kv_map, sc_map, rope_map, w);
       break;
     case 7:
       dn::dense_decode_kernel<false, false, false, false, true>
-          <<<grid, dn::kThreads, dn::kSmemBytes, stream>>>(q_map, kv_map, sc_map, rope_map, p);
+          <<<grid, dn::kThreads, dn::kSmemBytes, stream>>>(q_map, kv_map, sc_map, rope_map, w);
       break;
     case 8:
       dn::dense_decode_kernel<true, false, false, false, true>
-          <<<grid, dn::kThreads, dn::kSmemBytes, stream>>>(q_map, kv_map, sc_map, rope_map, p);
+          <<<grid, dn::kThreads, dn::kSmemBytes, stream>>>(q_map, kv_map, sc_map, rope_map, w);
       break;
     case 9:
       dn::dense_decode_kernel<false, false, true, true>
-          <<<grid, dn::kThreads, dn::kSmemBytes, stream>>>(q_map, kv_map, sc_map, rope_map, p);
+          <<<grid, dn::kThreads, dn::kSmemBytes, stream>>>(q_map, kv_map, sc_map, rope_map, w);
       break;
     case 10:
       dn::dense_decode_kernel<false, false, true, false, true>
-          <<<grid, dn::kThreads, dn::kSmemBytes, stream>>>(q_map, kv_map, sc_map, rope_map, p);
+          <<<grid, dn::kThreads, dn::kSmemBytes, stream>>>(q_map, kv_map, sc_map, rope_map, w);
       break;
     default:
       dn::dense_decode_kernel<false, false, false>

@@ -344,7 +344,8 @@ __device__ __forceinline__ void issue_pv(uint32_t tmem, uint64_t p_desc0, uint64
 // heads of 8692 keys, nothing shared: 360 against 420.)
 template <bool kStall, bool kShared = false, bool kWarp = kShared>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    sparse_decode_kernel(const __grid_constant__ CUtensorMap q_map, const DecodeParams p) {
+    sparse_decode_kernel(const __grid_constant__ CUtensorMap q_map,
+                         const typename KernelParams<kWarp>::type p) {
   constexpr uint64_t kWaitNs = kStall ? kDecodeStallWaitNs : MLA_WAIT_LIMIT_NS;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -1195,16 +1196,17 @@ const void* sparse_kernel_ptr(int kind) {
 }
 
 cudaError_t launch_sparse(const CUtensorMap& q_map, const DecodeParams& p, int num_parts, int kind,
-                          cudaStream_t stream) {
+                          cudaStream_t stream, const LiveLengths& live) {
+  const WarpParams w{p, live};
   const dim3 grid(2 * num_parts * p.row_blocks);
   if (kind == 5)
-    sp::sparse_decode_kernel<true, false, true><<<grid, sp::kThreads, sp::kSmemBytes, stream>>>(q_map, p);
+    sp::sparse_decode_kernel<true, false, true><<<grid, sp::kThreads, sp::kSmemBytes, stream>>>(q_map, w);
   else if (kind == 4)
-    sp::sparse_decode_kernel<true, true><<<grid, sp::kThreads, sp::kSmemBytes, stream>>>(q_map, p);
+    sp::sparse_decode_kernel<true, true><<<grid, sp::kThreads, sp::kSmemBytes, stream>>>(q_map, w);
   else if (kind == 3)
-    sp::sparse_decode_kernel<false, false, true><<<grid, sp::kThreads, sp::kSmemBytes, stream>>>(q_map, p);
+    sp::sparse_decode_kernel<false, false, true><<<grid, sp::kThreads, sp::kSmemBytes, stream>>>(q_map, w);
   else if (kind == 2)
-    sp::sparse_decode_kernel<false, true><<<grid, sp::kThreads, sp::kSmemBytes, stream>>>(q_map, p);
+    sp::sparse_decode_kernel<false, true><<<grid, sp::kThreads, sp::kSmemBytes, stream>>>(q_map, w);
   else if (kind == 1)
     sp::sparse_decode_kernel<true><<<grid, sp::kThreads, sp::kSmemBytes, stream>>>(q_map, p);
   else
