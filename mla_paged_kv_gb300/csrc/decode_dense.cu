@@ -1112,14 +1112,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // phases, whatever role gave up meanwhile (their own budget ends a wait): one
       // that left by itself would leave the others at a barrier for good.
       if (units >= 1) {
-        ok = warp_wait_cluster(&bars[L_FREE], (units - 1) & 1, abort_flag, kWaitNs);
+        ok = warp_wait_cluster(&bars[L_FREE], (units - 1) & 1, nullptr, kWaitNs);
         if (!ok) break;
       }
       sLOut[r] = l_own;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) bulk_copy_to_cluster(peer_l, smem_u32(sLOut + 32 * warp), 32 * 4, peer_l_full);
-      ok = warp_wait_cluster(&bars[L_FULL], units & 1, abort_flag, kWaitNs);
+      ok = warp_wait_cluster(&bars[L_FULL], units & 1, nullptr, kWaitNs);
       if (!ok) break;
       if (tid == 0) mbar_arrive_expect_tx(&bars[L_FULL], kVecBytes);
       const float l_peer = __shfl_sync(0xffffffffu, sLIn[r], lane);
@@ -1129,8 +1129,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ++units;
       // ---- epilogue of this (unit, split)
       // staging buffer: the own P buffer, free once both P V of our last own tile are done
-      ok = warp_wait(&bars[O_FULL], u_here & 1, abort_flag, kWaitNs);
-      if (ok && own_i >= 1) ok = warp_wait_cluster(&bars[OWN_FREE], (own_i - 1) & 1, abort_flag, kWaitNs);
+      ok = warp_wait(&bars[O_FULL], u_here & 1, nullptr, kWaitNs);
+      if (ok && own_i >= 1) ok = warp_wait_cluster(&bars[OWN_FREE], (own_i - 1) & 1, nullptr, kWaitNs);
       if (!ok) break;
       tc_fence_after();
       const int s_begin = p.split_offset[b_here];
