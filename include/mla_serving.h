@@ -42,7 +42,7 @@ extern "C" {
  * A 16-bit cache takes [c', r'] (576 values of its type).  A cache of FP8
  * records (MLA_DTYPE_FP8_RECORD) takes, for each 128-element group of c',
  * scale = max|c'| / 448 (1 for a group of zeros) and codes = E4M3(c' / scale)
- * (nearest even, saturating), and r' in bf16.
+ * (the fp32 quotient, nearest even, saturating), and r' in bf16.
  *
  *   d_c            [total_tokens] rows of 512, `in_dtype`, c_stride elements
  *                  apart (a multiple of 8)
@@ -148,8 +148,10 @@ int mla_cache_copy_pages(void* d_pool, int layers, long long layer_stride, int n
  * Bytes of the plan of a batch. */
 size_t mla_prompt_plan_bytes(int batch, int total_q);
 
-/* The plan: the list of 256-query tiles of all sequences, longest first; made
- * once for a batch and read by every layer.
+/* The plan: the list of query tiles of all sequences, longest first, and the
+ * offsets it was made for; made once for a batch and read by every layer.
+ * Tiles have 512 queries where total_q / batch > 256, else 256: a plan is of
+ * exactly its batch, total_q, total_k and offsets.
  *   d_cu_seqlens_q, d_cu_seqlens_k int32 [batch + 1], not decreasing (NULL k:
  *   the same as q); sequence b has queries cu_q[b] .. cu_q[b+1] - 1 and keys
  *   cu_k[b] .. cu_k[b+1] - 1.  With an offset that decreases or lies outside
@@ -166,8 +168,10 @@ int mla_prompt_get_plan(const int32_t* d_cu_seqlens_q, const int32_t* d_cu_seqle
  *   h_kv divides h_q; query head h reads key head h / (h_q / h_kv)
  *   d_plan from mla_prompt_get_plan with the same batch, total_q, total_k and causal
  *   d_out [total_q, h_q, 128] of `dtype`, d_lse fp32 [total_q, h_q], contiguous
- * Softmax weights are rounded to `dtype` for the product with v; statistics
- * and sums are fp32.  Values of a sequence must be finite where a query of
+ * Softmax weights are rounded to `dtype` for the product with v and divided by
+ * the sum of the unrounded ones; statistics and sums are fp32.  softmax_scale is
+ * the model's: heads expanded from a latent cache are scaled for their 192 dims,
+ * and the decode of their absorbed form takes the same scale.  Values of a sequence must be finite where a query of
  * the same 128-key tile could reach them; rows of other sequences, and rows
  * past the last one, may hold anything. */
 int mla_prompt_attention_fwd(const void* d_q, long long q_token_stride, long long q_head_stride, const void* d_k,
@@ -208,6 +212,9 @@ int mla_prompt_attention_checked_fwd(const void* d_q, long long q_token_stride, 
  * 8 ceil(batch * s_q * h_q / 128) <= 7 batch * ceil(s_q * h_q / 128).  Elsewhere
  * (s_q * h_q a multiple of 128, say) every request fills its blocks alone, the
  * shared pages are one copy in L2 either way, and the call is mla_decode_fwd.
+ * As in mla_decode_fwd, a 16-bit cache's softmax weights are rounded to its type
+ * for the product with the values and divided by the sum of the unrounded ones;
+ * over FP8 records the sum is that of the rounded ones.
  *   num_parts from mla_shared_prefix_num_parts; at most 1024
  * Other arguments as for mla_decode_fwd.  batch * s_q * h_q and
  * batch * max_pages stay below 2^31; s_q * h_q <= 2^20, batch <= 65535. */
@@ -219,7 +226,8 @@ int mla_shared_prefix_get_plan(const int32_t* d_block_table, int max_pages, cons
                                mla_stream_t stream);
 
 /*   d_plan      from mla_shared_prefix_get_plan for the same block table,
- *               batch, s_q, h_q, causal and num_parts; it holds the lengths
+ *               batch, s_q, h_q, causal and num_parts; it holds the lengths: a
+ *               plan of others is answered by (see the checked call below)
  *   d_workspace >= mla_shared_prefix_workspace_bytes(batch, s_q, h_q, num_parts)
  * A block-table entry outside the pool masks its 64 keys and is reported, as
  * in mla_decode_fwd.  Slots of a page behind a request's last key must hold

@@ -6,8 +6,8 @@
 //   record: scale_g = max|c'_g| / 448, code = e4m3(c' / scale_g), bf16 r'
 //
 // Memory bound: a token reads 1152 bytes (and 256 of its angles) and writes
-// 1152 or 656.  One warp per token: lane l holds columns 8l .. 8l+7 of each
-// half of the latent row, so that every load and store of the row is one
+// 1152 or 656.  A warp holds a token (two, one after the other, in larger calls):
+// lane l has columns 8l .. 8l+7 of each half of the latent row, so that every load and store of the row is one
 // contiguous run over the warp (16 bytes a lane; 8 for codes) and a 128-column
 // group is 16 lanes of one half, whose maximum takes four shuffles.
 #include <cuda_bf16.h>
@@ -193,7 +193,8 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const AppendP
         // difference exact in an FMA (P. Markstein, IBM J. Res. Dev. 34, 1990), by
         // 2^-46 of the quotient before its rounding: at the ties of E4M3, where q alone
         // takes the other neighbour now and then, it is the quotient.  (24577
-        // tokens: 12.7 us, with q alone 11.9, with sixteen divisions a lane 15.1.)  Tiny groups and
+        // tokens back to back in L2: 12.7 us, with q alone 11.9, with sixteen
+        // divisions a lane 15.1; from HBM 13.1 either of the first two.)  Tiny groups and
         // their scale both by 2^64 before it, where 1 / scale would be infinite; a
         // scale of infinity divides to zeros.
         float den = scale;

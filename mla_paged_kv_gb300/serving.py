@@ -5,10 +5,15 @@ Functions named ``mla_*`` mirror the C entry points: they check torch tensors
 and marshal them into pointers, sizes and a CUDA stream.  The helpers
 (``cache_append``, ``cache_grow``, ``cache_fork``, ``cache_free``,
 ``cache_compact``, ``cache_copy_pages``, ``plan_prompt``, ``prompt_attention``,
-``plan_shared_prefix``, ``shared_prefix_decode``) allocate outputs.  A helper without ``status`` reads the device status after
-its call (which waits for the GPU) and raises ``MlaError``; with ``status`` (an
-int32 tensor the caller zeroed) it does not wait, and the caller looks at the
-word when it wants to.
+``plan_shared_prefix``, ``shared_prefix_decode``) allocate outputs.  A helper
+without ``status`` reads the device status after its call (which waits for the
+GPU) and raises ``MlaError``; with ``status`` (an int32 tensor the caller zeroed)
+it does not wait, and the caller looks at the word when it wants to.
+
+Softmax scales default to the width of the heads a call is given:
+1 / sqrt(192 or 128) in prompt attention, 1 / sqrt(576) in the decodes.  A model
+whose prompt heads are expanded from the latent rows that it decodes over has one
+scale, that of its prompt heads: give it to both.
 
 Every tensor of a call lives on one device, which must be the current one;
 tensors used on a stream other than the one they were made on follow torch's
@@ -461,7 +466,7 @@ def plan_prompt(cu_seqlens_q, cu_seqlens_k=None, total_q=None, total_k=None, cau
 
 def prompt_attention(q, k, v, cu_seqlens_q, cu_seqlens_k=None, causal=True, softmax_scale=None, pl=None,
                      status=None):
-    """Attention over packed prompts; returns (out, lse).
+    """Attention over packed prompts; returns (out, lse).  softmax_scale defaults to 1 / sqrt(dims of q).
 
     A plan holds the offsets it was made for.  With pl they are compared with cu_seqlens_q and cu_seqlens_k on the
     device, and a plan of others is MLA_ERR_STALE_PLAN."""
@@ -609,7 +614,8 @@ def plan_shared_prefix(block_table, cache_seqlens, s_q, h_q, causal=False, num_p
 
 def shared_prefix_decode(q, kv, block_table, cache_seqlens, causal=False, softmax_scale=None, out_fp32=False,
                          pl=None, status=None):
-    """Dense decode that attends the pages all requests share once; returns (out, lse).
+    """Dense decode that attends the pages all requests share once; returns (out, lse).  softmax_scale defaults to
+    1 / sqrt(576), as decode's does: a model with prompt heads of 192 dims gives 192 ** -0.5.
 
     A plan holds the lengths it was made for.  With pl they are compared with cache_seqlens on the device, and a
     plan of other lengths (rows that have grown since, say) is MLA_ERR_STALE_PLAN."""
