@@ -51,6 +51,13 @@ __device__ __forceinline__ void acc4(float4& a, float w, const float4& v) {
   }
 }
 
+// A grid launched early whose blocks all left at once would end before the
+// attention kernel does, and what follows in the stream waits for this grid
+// alone: the first block stays until that kernel is done.
+__device__ __forceinline__ void first_block_waits() {
+  if (blockIdx.x == 0 && blockIdx.y == 0) pdl_wait_prior_grid();
+}
+
 // Many rows (enough to fill the GPU several times over), few splits each:
 // a warp merges a whole 512-column row (kVec = 4 float4 per lane per split;
 // a block = 4 rows).  Its blocks hold no shared memory, so they stay
@@ -75,7 +82,10 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
   if (row >= rows) return;
   const int s0 = split_offset[unit];
   const int n = split_offset[unit + 1] - s0;
-  if (n == 1) return;  // written directly by the attention kernel
+  if (n == 1) {  // written directly by the attention kernel
+    first_block_waits();
+    return;
+  }
   pdl_wait_prior_grid();
   const size_t orow = static_cast<size_t>(unit) * rows + row;
   const size_t col = lane * 4;
@@ -180,7 +190,10 @@ __global__ void __launch_bounds__(kSubsets * 32)
   if (row >= rows) return;  // uniform over the block
   const int s0 = split_offset[unit];  // from the plan: read before the wait
   const int n = split_offset[unit + 1] - s0;
-  if (n == 1) return;  // written directly by the attention kernel
+  if (n == 1) {  // written directly by the attention kernel
+    first_block_waits();
+    return;
+  }
   pdl_wait_prior_grid();
   const size_t orow = static_cast<size_t>(unit) * rows + row;
   const size_t col = static_cast<size_t>(quarter) * 128 + lane * 4;

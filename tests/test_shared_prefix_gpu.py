@@ -481,3 +481,46 @@ def test_every_instance_within_its_roundings(h_q, dtype, fp8, out_fp32, s_q, cau
         o2, l2 = mla.decode(c.q.cuda(), c.kv.cuda(), torch.from_numpy(c.table).cuda(), i32(c.lens), out_fp32=out_fp32)
         assert np.all(np.abs(o2.double().cpu().numpy() - o) <= 2 * tol)
         assert np.all(np.abs(l2.double().cpu().numpy() - l) <= 2 * ltol)
+
+
+@pytest.mark.parametrize("call", ["decode", "shared"])
+def test_whole_units_in_one_graph_with_what_follows(call):
+    """One partition: every unit is written by the attention kernel itself and the combine has nothing to do, but
+    what follows in the graph (a copy of the output, the next plan in the same buffers) still finds it done."""
+    c = Case(2, [64 * (i % 7) + 1 for i in range(70)], 1, 128, seed=24, poison=False)
+    q, kv, table, lens = c.q.cuda(), c.kv.cuda(), torch.from_numpy(c.table).cuda(), i32(c.lens)
+    other = i32([70 + 3 * (i % 40) for i in range(70)])
+    st, n = i32([0]), torch.empty_like(lens)
+    if call == "shared":
+        pl = mla.plan_shared_prefix(table, lens, 1, 128, num_parts=1)
+    else:
+        pl = mla.plan(lens, 70, 128, num_parts=1)
+    out = torch.empty(70, 1, 128, 512, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(70, 1, 128, device="cuda")
+
+    def step(lengths):
+        n.copy_(lengths)
+        if call == "shared":
+            mla.mla_shared_prefix_get_plan(table, n, 1, 128, False, 1, pl.plan)
+            mla.mla_shared_prefix_decode_fwd(q, kv, table, pl, out, lse, st)
+        else:
+            mla.mla_get_metadata(n, 70, 1, pl.sched, pl.split_offset)
+            mla.mla_decode_fwd(q, kv, table, n, pl.sched, pl.split_offset, 1, pl.workspace, out, lse, st)
+        return out.clone(), lse.clone()
+
+    want = []
+    for lengths in (lens, other):
+        want.append(step(lengths))
+        torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [step(lens), step(other), step(lens)]
+    for _ in range(5):
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        for (o, l), (wo, wl) in zip(got, [want[0], want[1], want[0]]):
+            assert torch.equal(o, wo) and torch.equal(l, wl)
+    c.lens = other.tolist()
+    compare(*want[1], *c.want())
+    assert int(st) == 0
