@@ -117,7 +117,8 @@ size_t mla_cache_compact_workspace_bytes(int num_pages);
  * n, the lowest first on both sides.  Counts and tables are rewritten;
  * d_pairs[k] = (old page, new page) for k < *d_count, (-1, -1) after that.  No
  * page is both a source and a target.  A table entry inside a row's length
- * that names a free page or none at all is left and reported.
+ * that names a free page or none at all is left and reported; so is a length out
+ * of range, whose row is taken as far as the table goes (negative: not at all).
  *   d_pairs int32 [num_pages / 2, 2] out, d_count int32 [1] out */
 int mla_cache_compact(int32_t* d_refcount, int num_pages, int32_t* d_block_table, int rows, int max_pages,
                       const int32_t* d_seqlens, int32_t* d_pairs, int32_t* d_count, void* d_workspace,

@@ -405,6 +405,7 @@ __global__ void __launch_bounds__(256) compact_apply_kernel(const PageState s, C
     const int r = static_cast<int>(e / s.max_pages);
     const int col = static_cast<int>(e - static_cast<long long>(r) * s.max_pages);
     const int len = s.seqlens[r];
+    if (col == 0 && (len < 0 || len > static_cast<long long>(s.max_pages) * kTile)) report(s.status, MLA_ERR_BAD_INDEX);
     if (len <= 0 || col >= pages_of(len)) continue;
     const int page = s.table[e];
     const int to = page >= 0 && page < s.num_pages ? ws.rank[page] : kFree;

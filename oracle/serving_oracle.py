@@ -137,7 +137,9 @@ class Pool:
         live = [c != 0 for c in self.ref]
         to = dict(zip(src, dst))
         for r, row in enumerate(self.table):
-            for j in range(_pages(max(self.lens[r], 0))):
+            if not 0 <= self.lens[r] <= len(row) * PAGE:
+                self.bad = True
+            for j in range(min(_pages(max(self.lens[r], 0)), len(row))):
                 if not 0 <= row[j] < len(self.ref) or not live[row[j]]:
                     self.bad = True
                 else:

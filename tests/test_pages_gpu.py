@@ -348,3 +348,24 @@ def test_copy_judges_targets_that_fall_together():
         status = i32([0])
         mla.cache_copy_pages(pool, pairs.cuda(), status=status)
         assert torch.equal(pool, want) and int(status) == 0
+
+
+@pytest.mark.parametrize("length", [-5, 7 * 64 + 1, 2 ** 31 - 1])
+def test_compact_reports_a_length_out_of_range(length):
+    s = State(3, 200, 40, seed=25)
+    s.grow([1], [7 * 64 - s.host.lens[1]])  # a row of all its pages
+    s.host.lens[1] = length
+    s.lens = i32(s.host.lens)
+    s.compact()
+    assert s.host.bad
+
+
+def test_largest_lists_and_tables():
+    """65536 rows and lists of 4096 entries, the most that a call takes."""
+    rng = random.Random(26)
+    s = State(4096, 190, 24000, seed=26, empty_rows=61440, width=4)
+    some = rng.sample(range(4096), 4096)
+    s.grow(some, [rng.randint(0, 70) if s.host.lens[r] < 186 else 0 for r in some])
+    s.fork([rng.randrange(4096) for _ in range(4096)], rng.sample(range(4096, 65536), 4096))
+    s.free(rng.sample(range(65536), 4096))
+    s.compact()
