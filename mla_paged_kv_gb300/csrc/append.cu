@@ -6,10 +6,11 @@
 //   record: scale_g = max|c'_g| / 448, code = e4m3(c' / scale_g), bf16 r'
 //
 // Memory bound: a token reads 1152 bytes (and 256 of its angles) and writes
-// 1152 or 656.  A warp holds a token (two, one after the other, in larger calls):
-// lane l has columns 8l .. 8l+7 of each half of the latent row, so that every load and store of the row is one
-// contiguous run over the warp (16 bytes a lane; 8 for codes) and a 128-column
-// group is 16 lanes of one half, whose maximum takes four shuffles.
+// 1152 or 656.  A warp holds a token (two, one after the other, in larger
+// calls): lane l has columns 8l .. 8l+7 of each half of the latent row, so that
+// every load and store of the row is one contiguous run over the warp (16 bytes
+// a lane; 8 for codes) and a 128-column group is 16 lanes of one half, whose
+// maximum takes four shuffles.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
