@@ -251,6 +251,146 @@ int mla_shared_prefix_decode_checked_fwd(const void* d_q, const void* d_kv, cons
                                          size_t workspace_bytes, void* d_out, int out_type, float* d_lse,
                                          int32_t* d_status, mla_stream_t stream);
 
+/* ------------------------------------------------------------------ rotary */
+
+/* How the frequencies of rotary positions are scaled for contexts longer than
+ * the one a model was trained on (`original` positions), by `factor` (s):
+ *   f_i = base^(-2i / dim), i < dim / 2;  turns_i = original f_i / 2 pi
+ *   NONE        f_i
+ *   LINEAR      f_i / s  (position interpolation)
+ *   NTK         of base s^(dim / (dim - 2)) base
+ *   YARN        w f_i / s + (1 - w) f_i, w = clamp((i - a) / max(b - a, 0.001), 0, 1) with
+ *               a = max(floor(c(high)), 0), b = min(ceil(c(low)), dim - 1),
+ *               c(t) = dim ln(original / 2 pi t) / (2 ln base); the table's values
+ *               are multiplied by 0.1 ln s + 1
+ *   WAVELENGTH  (1 - w) f_i / s + w f_i, w = clamp((turns_i - low) / (high - low), 0, 1)
+ * low and high are numbers of turns over the original context. */
+typedef enum {
+  MLA_ROPE_NONE = 0,
+  MLA_ROPE_LINEAR = 1,
+  MLA_ROPE_NTK = 2,
+  MLA_ROPE_YARN = 3,
+  MLA_ROPE_WAVELENGTH = 4
+} mla_rope_scaling_t;
+
+/* The frequencies h_freq[dim / 2] (radians a position) and the magnitude of a
+ * table, both in host memory.  dim a multiple of 8, at most 256; base > 1;
+ * factor >= 1 and original > 0 where they are used; 0 < low < high (YARN and
+ * WAVELENGTH). */
+int mla_rope_frequencies(int dim, double base, int scaling, double factor, double original, double low, double high,
+                         double* h_freq, double* h_magnitude);
+
+/* The table of positions first_pos .. first_pos + positions - 1:
+ *   d_cos_sin[p] = magnitude (cos p f_0 .. cos p f_(dim/2-1), sin p f_0 ..)
+ * fp32 [positions, dim], 16-byte aligned, as mla_cache_append (dim 64) and
+ * mla_rope_heads read it.  h_freq in host memory, 0 <= f <= 2^10, read before the
+ * call returns.  Angles are exact to 2^-52 of themselves at any position below
+ * 2^31 (first_pos + positions is at most that), and values to a few ulp. */
+int mla_rope_table(const double* h_freq, int dim, double magnitude, long long first_pos, int positions,
+                   float* d_cos_sin, mla_stream_t stream);
+
+/* Rotate part of each head of new tokens' queries (x) and keys (k, or none), each
+ * head optionally RMS-normalised first, in one pass:
+ *   y = x rsqrt(mean(x^2) + norm_eps) w   over the head's dims (with weights, else x)
+ *   dims rope_offset .. rope_offset + rope_dim - 1 of y turned by the angle of the
+ *   token's position, pairs as in mla_cache_append: (y[i], y[i + rope_dim/2]), or
+ *   (y[2i], y[2i+1]) with rope_interleaved; (a, b) -> (a cos - b sin, b cos + a sin)
+ * All arithmetic is fp32; each stored value is rounded once.  A token's position
+ * is d_positions[t], or, with d_positions NULL, that of mla_cache_append:
+ * cache_seqlens[b] - (cu[b+1] - t) for cu[b] <= t < cu[b+1] (d_cu_seqlens NULL:
+ * total_tokens / batch tokens for each request, which must divide); tokens
+ * outside [cu[0], cu[batch]) are ignored.  A token whose position is negative or
+ * past max_pos is not written, MLA_ERR_BAD_INDEX.  Without d_cos_sin (rope_dim 0)
+ * heads are only normalised, and all of d_positions, d_cu_seqlens and
+ * d_cache_seqlens are NULL.
+ *   d_x, d_k   [total_tokens, heads, dim] of `dtype` (MLA_DTYPE_BF16 or _FP16);
+ *              strides in elements, multiples of 8, the last dimension contiguous
+ *   d_out, d_k_out  the same shapes, strides of their own; may be d_x and d_k
+ *              themselves with the same strides (dims that are not changed are
+ *              then not moved), else must not overlap any input
+ *   dim        a multiple of 8, at most 1024; rope_dim a multiple of 16, at most
+ *              256; rope_offset a multiple of 8
+ *   d_x_weight, d_k_weight  [dim] of `dtype`, or NULL: no norm of that side
+ *   k_heads    0: no keys (their pointers NULL)
+ *   d_cos_sin  fp32 [max_pos, rope_dim]: cosines, then sines */
+int mla_rope_heads(const void* d_x, long long x_token_stride, long long x_head_stride, void* d_out,
+                   long long out_token_stride, long long out_head_stride, int heads, const void* d_x_weight,
+                   const void* d_k, long long k_token_stride, long long k_head_stride, void* d_k_out,
+                   long long k_out_token_stride, long long k_out_head_stride, int k_heads, const void* d_k_weight,
+                   int dim, int dtype, int total_tokens, int rope_dim, int rope_offset, int rope_interleaved,
+                   float norm_eps, const int32_t* d_positions, const int32_t* d_cu_seqlens,
+                   const int32_t* d_cache_seqlens, int batch, const float* d_cos_sin, int max_pos, int32_t* d_status,
+                   mla_stream_t stream);
+
+/* ------------------------------------------------------------------ gather */
+
+/* Rows of a paged cache as packed rows (to be expanded into the heads of
+ * mla_prompt_attention_fwd, say): row t of the output, cu[b] <= t < cu[b+1],
+ * is the cache's row of request b at position d_starts[b] + t - cu[b] (d_starts
+ * NULL: 0).  Rows outside [cu[0], cu[batch]) are left as they were.
+ *   d_cache  [num_pages, 64, 576] bf16 or fp16, copied; or FP8 records
+ *            [num_pages, 64, 656], whose codes times scales are rounded to bf16
+ *            once (the RoPE part is bf16 already)
+ *   d_out    [total_rows] rows of 576 of the cache's type (records: bf16),
+ *            out_stride elements apart (a multiple of 8, at least 576); must not
+ *            overlap the cache
+ *   d_cu_seqlens int32 [batch + 1], not decreasing; d_starts int32 [batch]
+ * A row whose position is negative or past max_pages * 64, or whose page is
+ * outside the pool, is not written; MLA_ERR_BAD_INDEX. */
+int mla_cache_gather(const void* d_cache, int cache_dtype, int num_pages, const int32_t* d_block_table, int max_pages,
+                     const int32_t* d_cu_seqlens, const int32_t* d_starts, int batch, int total_rows, void* d_out,
+                     long long out_stride, int32_t* d_status, mla_stream_t stream);
+
+/* ------------------------------------------------------------------- chunk */
+
+/* Attention of ragged chunks of new tokens over a paged latent cache, all of a
+ * batch in one call: drafts to verify, prompts taken in chunks, single tokens
+ * beside them.  Token i of request b's n_b = cu[b+1] - cu[b] tokens sees the
+ * request's keys 0 .. cache_seqlens[b] - 1 (the new tokens among them, as after
+ * mla_cache_append), with causal those up to cache_seqlens[b] - n_b + i:
+ *   out = sum_j softmax_j(scale q . k_j) k_j[:512],  lse = ln sum_j exp(scale q . k_j)
+ * A query that sees no key gets out = 0, lse = -inf.  Rows of the outputs outside
+ * every chunk are left as they were.  Softmax weights are rounded to the cache's
+ * type for the product with the values and divided by the sum of the unrounded
+ * ones; statistics and sums are fp32.
+ *
+ * num_parts: pairs of CTAs that share the work; mla_chunk_num_parts gives as many
+ * as the device runs at once (>= 1, or a negative mla_status_t).  At most 1024. */
+int mla_chunk_num_parts(void);
+size_t mla_chunk_plan_bytes(int batch, int total_q, int h_q, int num_parts); /* 0: sizes out of range */
+size_t mla_chunk_workspace_bytes(int num_parts);
+
+/* The plan: blocks of 128 query rows with the keys they see, cut into num_parts
+ * runs of equal cost, and the offsets and lengths it was made for; made once for
+ * a batch and read by every layer.  total_q * h_q < 2^31, batch <= 2^20.
+ *   d_cu_seqlens_q int32 [batch + 1], not decreasing, within [0, total_q];
+ *   d_cache_seqlens int32 [batch], at most 2^24 (negative: no keys).  With an
+ *   offset or length out of range the plan is empty: MLA_ERR_BAD_INDEX, and a
+ *   call with it writes nothing. */
+int mla_chunk_get_plan(const int32_t* d_cu_seqlens_q, const int32_t* d_cache_seqlens, int batch, int total_q, int h_q,
+                       int causal, int num_parts, void* d_plan, size_t plan_bytes, int32_t* d_status,
+                       mla_stream_t stream);
+
+/*   d_q           [total_q, h_q, 576] of `dtype` (MLA_DTYPE_BF16 or _FP16)
+ *   d_kv          [num_pages, 64, 576] of `dtype`
+ *   d_block_table int32 [batch, max_pages]
+ *   d_plan        from mla_chunk_get_plan with the same batch, total_q, h_q and
+ *                 num_parts
+ *   d_cu_seqlens_q, d_cache_seqlens  compared with the plan's on the device:
+ *                 MLA_ERR_STALE_PLAN where one is another than the plan was made
+ *                 for; the results are those of the plan.  NULL: not compared
+ *   d_workspace   >= mla_chunk_workspace_bytes(num_parts)
+ *   d_out         [total_q, h_q, 512] of out_type (bf16, fp16 or fp32), d_lse fp32
+ *                 [total_q, h_q]
+ * A block-table entry outside the pool (or past max_pages) masks its 64 keys and
+ * is reported, MLA_ERR_BAD_INDEX.  Slots of a page behind a request's last key may
+ * hold anything; keys that any of its queries sees must be finite for all of them. */
+int mla_chunk_attention_fwd(const void* d_q, const void* d_kv, const int32_t* d_block_table, int max_pages,
+                            int num_pages, int batch, int total_q, int h_q, int dtype, float softmax_scale,
+                            const int32_t* d_cu_seqlens_q, const int32_t* d_cache_seqlens, const void* d_plan,
+                            size_t plan_bytes, int num_parts, void* d_workspace, size_t workspace_bytes, void* d_out,
+                            int out_type, float* d_lse, int32_t* d_status, mla_stream_t stream);
+
 /* -------------------------------------------------------------- test hooks */
 
 /* The timeout and unwind paths of the two attention kernels above, as
@@ -272,6 +412,12 @@ int mla_test_shared_prefix_timeout(const void* d_q, const void* d_kv, const int3
                                    float softmax_scale, const void* d_plan, size_t plan_bytes, int num_parts,
                                    void* d_workspace, size_t workspace_bytes, void* d_out, int out_type, float* d_lse,
                                    int32_t* d_status, mla_stream_t stream);
+/* The same of mla_chunk_attention_fwd (bf16): its first K stage is never loaded. */
+int mla_test_chunk_timeout(const void* d_q, const void* d_kv, const int32_t* d_block_table, int max_pages,
+                           int num_pages, int batch, int total_q, int h_q, int dtype, float softmax_scale,
+                           const int32_t* d_cu_seqlens_q, const int32_t* d_cache_seqlens, const void* d_plan,
+                           size_t plan_bytes, int num_parts, void* d_workspace, size_t workspace_bytes, void* d_out,
+                           int out_type, float* d_lse, int32_t* d_status, mla_stream_t stream);
 
 /* ---------------------------------------------------------------- one pointer */
 
@@ -289,7 +435,10 @@ typedef enum {
   MLA_CALL_PROMPT = 6,       /* mla_prompt_attention_fwd */
   MLA_CALL_SHARED_PREFIX = 7, /* mla_shared_prefix_decode_fwd */
   MLA_CALL_SHARED_PREFIX_CHECKED = 8,
-  MLA_CALL_PROMPT_CHECKED = 9
+  MLA_CALL_PROMPT_CHECKED = 9,
+  MLA_CALL_ROPE_HEADS = 10,
+  MLA_CALL_GATHER = 11,
+  MLA_CALL_CHUNK = 12
 } mla_call_t;
 int mla_serving_call(int op, const void* args, size_t bytes); /* bytes = 8 x the call's arguments */
 

@@ -441,5 +441,8 @@ def packed_sparse_decode(q, packed, topk, topk_length=None, softmax_scale=None, 
 from . import serving as _serving  # noqa: E402  (uses the names above)
 from .serving import *  # noqa: E402,F401,F403
 
+from . import chunks as _chunks  # noqa: E402
+from .chunks import *  # noqa: E402,F401,F403
+
 _SIGS.update(_serving.SERVING_SIGS)
-__all__ += _serving.__all__
+__all__ += _serving.__all__ + _chunks.__all__

@@ -17,7 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libmla_paged_kv.so")
 SOURCES = ["api.cu", "sched.cu", "combine.cu", "decode_dense.cu", "decode_sparse.cu", "static_ws.cu",
-           "append.cu", "pages.cu", "prompt.cu", "shared_prefix.cu",
+           "append.cu", "pages.cu", "prompt.cu", "shared_prefix.cu", "rope.cu", "gather.cu", "chunk.cu",
            "serving_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

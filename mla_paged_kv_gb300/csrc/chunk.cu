@@ -1,0 +1,943 @@
+// Attention of ragged chunks of new tokens over a paged latent cache: q of 576
+// dims for every token and head, one latent key row of 576 for all heads, its
+// first 512 dims the value; request b's queries see its keys up to their own
+// position (causal, aligned at the end) or all of them.
+//
+//   s_ij = scale q_i . k_j,  out_i = sum_j e^(s_ij - r_i) k_j[:512] / l_i,
+//   l_i = sum_j e^(s_ij - r_i),  lse_i = r_i + ln l_i
+//
+// Units.  A request's queries are rows, token-major; 128 rows and the keys that
+// the last of them sees are a unit.  The plan cuts the units' 128-key tiles into
+// one run for each pair of CTAs, all of the same cost; a unit that a cut divides
+// leaves partial sums, which the combine merges, every other one its output.
+//
+// The pair splits the rows, not the values: CTA c has rows 64 c .. 64 c + 63, and
+// every product is a cta_group::2 MMA of M = 128, whose accumulator holds a CTA's
+// 64 rows in 128 lanes: columns [0, N/2) in lanes 0 .. 63, [N/2, N) in lanes 64
+// .. 127 (and which runs at the full rate, 4090 multiply-adds a cycle and SM, at
+// N = 128 and 256).  A row's scores, weights and output never leave its CTA, so
+// nothing is exchanged between the two but barrier arrivals:
+//   * Q K^T: N = 128 keys, two pages; CTA c loads page 2 j + c, all 576 dims.
+//   * P V: N = 256 dims, twice; CTA c loads dims 256 c .. 256 c + 255 of both
+//     pages.  (The half of them that are in its key page too cannot serve: an MMA
+//     reads both CTAs' operands at one offset, and they lie at different ones.)
+//   * TMEM: O 64 x 512 as 256 columns, two score buffers of 64.
+//   * Shared memory: Q 72 KB, K in three stages of three 64-dim slices, V in two
+//     stages of a page, P 16 KB.
+//   * One warp issues  Q K^T (t+1)  P V (t):  the softmax of tile t+1 runs under
+//     P V (t) and Q K^T (t+2), that of t under Q K^T (t+1).
+//   * Four threads hold a row's 128 scores, 32 each, and share their maxima in
+//     shared memory.  The reference r is raised only when the maximum grows by
+//     more than 2^8 (then O is rescaled, rarely).  Weights are rounded to the
+//     cache's type for P V and divided by the sum of the unrounded ones.
+//   * Rows of a page behind the unit's last key may hold anything: their scores
+//     are masked, and their values zeroed in shared memory (0 x NaN is not 0).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "ptx.cuh"
+#include "serving.cuh"
+
+namespace mla {
+namespace ck {
+
+constexpr int kCtaRows = 64;               // query rows of one CTA
+constexpr int kBN = 128;                   // keys of a tile: two pages
+constexpr int kSlices = kDqk / 64;
+constexpr int kSliceBytes = 64 * 128;      // 64 rows or keys x 64 dims
+constexpr int kKSlices = 3;                // slices of a K stage
+constexpr int kKBytes = kKSlices * kSliceBytes;
+constexpr int kKStages = 3;
+constexpr int kVBytes = 4 * kSliceBytes;   // a page's 64 keys x this CTA's 256 dims
+constexpr int kVStages = 2;
+constexpr int kPBytes = 2 * kSliceBytes;   // 64 rows x 128 keys
+constexpr int kOffK = kSlices * kSliceBytes;
+constexpr int kOffV = kOffK + kKStages * kKBytes;
+constexpr int kOffP = kOffV + kVStages * kVBytes;
+constexpr int kOffBar = kOffP + kPBytes;
+
+enum : int {
+  Q_FULL = 0,
+  Q_EMPTY,                        // the unit's last Q K^T is done
+  K_FULL,                         // +stage
+  K_EMPTY = K_FULL + kKStages,    // +stage
+  V_FULL = K_EMPTY + kKStages,    // +stage
+  V_EMPTY = V_FULL + kVStages,    // +stage
+  S_FULL = V_EMPTY + kVStages,    // +buffer
+  P_FULL = S_FULL + 2,            // weights written, O rescaled (one arrival per softmax warp of both CTAs)
+  PV_DONE,                        // one completion a tile: P may be overwritten, O rescaled or read
+  TAIL,                           // a V page whose last rows are to be zeroed has landed
+  DRAIN,
+  kNumBars
+};
+constexpr int kOffMisc = kOffBar + kNumBars * 8;
+constexpr int kOffRow = (kOffMisc + 16 + 15) / 16 * 16;  // [2][4 parts][64 rows]: maxima of a tile, or sums
+constexpr int kSmemBytes = kOffRow + 2 * 4 * kCtaRows * 4;
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+static_assert(kKSlices * 3 == kSlices, "three K stages a tile");
+
+constexpr int kThreads = 384;
+constexpr int kWarpMma = 8, kWarpK = 9, kWarpQ = 11;  // 10: V
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemS = 256;  // two buffers of 64 columns
+constexpr float kTau = 8.0f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <bool kHalf>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (kHalf) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+// tcgen05.ld of 32 columns that also returns the maximum of this thread's 32 values.
+__device__ __forceinline__ void tmem_ld32_max(uint32_t taddr, float* f, float& mx) {
+  uint32_t(&r)[32] = *reinterpret_cast<uint32_t(*)[32]>(f);
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, %32, [%33];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
+        "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+        "=r"(r[30]), "=r"(r[31]), "=f"(mx)
+      : "r"(taddr));
+}
+
+// Arrive on a barrier of either CTA of the pair (address from mapa) after writes
+// to this CTA's own shared memory that fence.proxy.async has handed to its async
+// proxy, where an MMA issued by the other CTA reads them.
+__device__ __forceinline__ void arrive_pair(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+
+// ------------------------------------------------------------------ units
+
+struct Unit {
+  int row0;    // first query row in the packed q, of total_q * h_q
+  int rows;    // at most 128
+  int rel;     // row0's place among its request's rows
+  int req;
+  int len;     // keys that its last row sees
+  int limit0;  // causal: keys that a row of the request's token 0 sees (may be below 1)
+  int slot;    // first partial slot
+  int parts;   // pieces it is cut into (1: none; 0: no keys)
+};
+static_assert(sizeof(Unit) == 4 * kUnitInts, "two int4");
+
+__device__ __forceinline__ Unit load_unit(const int32_t* units, int u) {
+  const int4* e = reinterpret_cast<const int4*>(units + static_cast<long long>(u) * kUnitInts);
+  const int4 a = e[0], b = e[1];
+  return Unit{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+}
+
+__device__ __forceinline__ int pages_of(int len) { return (len + kTile - 1) / kTile; }
+__device__ __forceinline__ int tiles_of(int len) { return (len + kBN - 1) / kBN; }
+
+// A pair's run of tiles: from tile t0 of unit u0 to tile t1 of unit u1 (not included).
+struct Run {
+  int u0, t0, u1, t1, piece;  // piece: of u0, among those the unit is cut into
+};
+
+__device__ __forceinline__ Run load_run(const int32_t* sched, int pair) {
+  const int32_t* e = sched + pair * MLA_SCHED_INTS;
+  return Run{e[0], e[1], e[2], e[3], e[4]};
+}
+
+// The next unit of the run from u on, and its tiles lo .. hi - 1.
+struct Walk {
+  Unit unit;
+  int u, lo, hi;
+};
+
+__device__ __forceinline__ bool walk_to(const int32_t* units, const Run& r, int u, Walk& w) {
+  for (; u < r.u1 || (u == r.u1 && r.t1 > 0); ++u) {
+    w.unit = load_unit(units, u);
+    w.lo = u == r.u0 ? r.t0 : 0;
+    w.hi = u == r.u1 ? r.t1 : tiles_of(w.unit.len);
+    if (w.hi > w.lo) {
+      w.u = u;
+      return true;
+    }
+  }
+  return false;
+}
+
+// Page ids of a request's pages base .. base + 31, one a lane: -1 for one outside
+// the pool (reported; its keys are masked and page 0 is read in its place) or past
+// the unit's last key.
+__device__ __forceinline__ int page_window(const ChunkParams& p, const Unit& unit, int base, int lane) {
+  const int k = base + lane;
+  if (k >= pages_of(unit.len)) return -1;
+  const int page = k < p.max_pages ? p.block_table[static_cast<long long>(unit.req) * p.max_pages + k] : -1;
+  if (page >= 0 && page < p.num_pages) return page;
+  report(p.status, MLA_ERR_BAD_INDEX);
+  return -1;
+}
+
+// Whether the plan is that of the caller's offsets and lengths; the call's
+// results are those of the plan either way.
+__device__ __forceinline__ void check_plan(const ChunkParams& p) {
+  for (int i = blockIdx.x * 32 + (threadIdx.x & 31); i <= p.batch; i += gridDim.x * 32)
+    if ((p.cu != nullptr && p.made[i] != p.cu[i]) ||
+        (p.lens != nullptr && i < p.batch && p.made[p.batch + 1 + i] != p.lens[i]))
+      report(p.status, MLA_ERR_STALE_PLAN);
+}
+
+__device__ __forceinline__ void fail(volatile int* abort_flag, int32_t* status) {
+  *abort_flag = 1;
+  report(status, MLA_ERR_TIMEOUT);
+}
+
+constexpr uint64_t kStallWaitNs = 200000;  // wait budget of the stall-test instance, whose first K stage is never loaded
+
+template <bool kHalf, bool kStall = false>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    chunk_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+                 const __grid_constant__ CUtensorMap v_map, const ChunkParams p) {
+  constexpr uint64_t kWaitNs = kStall ? kStallWaitNs : MLA_WAIT_LIMIT_NS;
+  const uint32_t rank = cluster_ctarank();
+  extern __shared__ __align__(1024) uint8_t smem[];  // swizzle atoms need 1024-byte alignment
+  uint8_t* sQ = smem;
+  uint8_t* sK = smem + kOffK;
+  uint8_t* sV = smem + kOffV;
+  uint8_t* sP = smem + kOffP;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
+  float* sRow = reinterpret_cast<float*>(smem + kOffRow);
+
+  const int tid = threadIdx.x;
+  // by a shuffle: the compiler then knows that a warp takes one role, and keeps
+  // MMA operands in uniform registers
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+
+  if ((smem_u32(smem) & 1023u) != 0u) {  // not what was asked for (all CTAs alike)
+    if (tid == 0) report(p.status, MLA_ERR_UNSUPPORTED);
+    return;
+  }
+  if (tid == 0) {
+    *abort_flag = 0;
+    // the barriers that MMAs wait for are the even CTA's and count both CTAs' parts
+    mbar_init(&bars[Q_FULL], 2);
+    mbar_init(&bars[Q_EMPTY], 1);
+    for (int i = 0; i < kKStages; ++i) {
+      mbar_init(&bars[K_FULL + i], 2);
+      mbar_init(&bars[K_EMPTY + i], 1);
+    }
+    for (int i = 0; i < kVStages; ++i) {
+      mbar_init(&bars[V_FULL + i], 2);
+      mbar_init(&bars[V_EMPTY + i], 1);
+    }
+    mbar_init(&bars[S_FULL], 1);
+    mbar_init(&bars[S_FULL + 1], 1);
+    mbar_init(&bars[P_FULL], 2 * 8);
+    mbar_init(&bars[PV_DONE], 1);
+    mbar_init(&bars[TAIL], 1);
+    mbar_init(&bars[DRAIN], 1);
+    fence_mbar_init_cluster();
+  }
+  if (warp == kWarpMma) {
+    tmem2_alloc(tmem_slot, kTmemCols);
+    tmem2_relinquish();
+  }
+  if (warp == kWarpK && lane == 0) {
+    prefetch_tmap(&q_map);
+    prefetch_tmap(&k_map);
+    prefetch_tmap(&v_map);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  cluster_arrive();  // the other CTA's barriers are ready before anything arrives there
+  cluster_wait();
+  const uint32_t tmem = *tmem_slot;
+  pdl_launch_dependents();
+  const Run run = load_run(p.sched, blockIdx.x >> 1);
+  const int causal = p.head[kHeadCausal];
+  Walk w;
+
+  if (warp > kWarpMma) {
+    // ------------------------------------------------------------ loads: K, V or Q
+    bool ok = true;
+    const uint64_t pol_q = policy_evict_first(), pol_kv = policy_evict_last();
+    const uint32_t bar0 = mapa_shared(smem_u32(bars), 0);
+    auto expect = [&](int bar, uint32_t bytes) { mbar_arrive_expect_tx_remote_relaxed(bar0 + 8 * bar, bytes); };
+    uint32_t n = 0, tails = 0;  // stages (or units of Q) and tail pages so far
+    for (int u = run.u0; ok && walk_to(p.units, run, u, w); u = w.u + 1) {
+      if (warp == kWarpQ) {
+        if (lane == 0) {
+          if (n >= 1) ok = mbar_wait(&bars[Q_EMPTY], (n - 1) & 1, abort_flag, kWaitNs);
+          if (ok) {
+            expect(Q_FULL, kOffK);
+            tma_load_4d_pair(sQ, &q_map, bar0 + 8 * Q_FULL, 0, w.unit.row0 + kCtaRows * static_cast<int>(rank), 0, 0,
+                             pol_q);
+          }
+        }
+        ++n;
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        continue;
+      }
+      const int pages = pages_of(w.unit.len);
+      int ids = 0, base = -32;
+      for (int j = w.lo; j < w.hi && ok; ++j) {
+        if (2 * j - base >= 32) {
+          base = 2 * j;
+          ids = page_window(p, w.unit, base, lane);
+        }
+        if (warp == kWarpK) {
+          const int k = 2 * j + static_cast<int>(rank);
+          const int page = max(__shfl_sync(0xffffffffu, ids, k - base), 0);
+          if (lane == 0)
+            for (int c = 0; c < 3 && ok; ++c) {
+              const int s = static_cast<int>((n + c) % kKStages), r = static_cast<int>((n + c) / kKStages);
+              if (r >= 1) ok = mbar_wait(&bars[K_EMPTY + s], (r - 1) & 1, abort_flag, kWaitNs);
+              if (!ok || (kStall && rank == 0 && n + c == 0)) continue;
+              if (k < pages) {
+                expect(K_FULL + s, kKBytes);
+                tma_load_4d_pair(sK + s * kKBytes, &k_map, bar0 + 8 * (K_FULL + s), 0, 0, kKSlices * c, page, pol_kv);
+              } else {  // no such page: whatever the stage holds is masked
+                mbar_arrive_remote_relaxed(bar0 + 8 * (K_FULL + s));
+              }
+            }
+          n += 3;
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          continue;
+        }
+        for (int half = 0; half < 2 && ok; ++half) {
+          const int k = 2 * j + half;
+          if (k >= pages) break;  // its P V is left out
+          const int id = __shfl_sync(0xffffffffu, ids, k - base), page = max(id, 0);
+          const int keep = id < 0 ? 0 : w.unit.len - k * kTile;  // rows of the page that are keys
+          const int s = static_cast<int>(n % kVStages), r = static_cast<int>(n / kVStages);
+          uint8_t* dst = sV + s * kVBytes;
+          if (lane == 0) {
+            if (r >= 1) ok = mbar_wait(&bars[V_EMPTY + s], (r - 1) & 1, abort_flag, kWaitNs);
+            if (ok && keep < kTile) {  // onto this CTA's own barrier
+              mbar_arrive_expect_tx(&bars[TAIL], kVBytes);
+              tma_load_4d(dst, &v_map, &bars[TAIL], 0, 0, 4 * static_cast<int>(rank), page, pol_kv);
+            } else if (ok) {
+              expect(V_FULL + s, kVBytes);
+              tma_load_4d_pair(dst, &v_map, bar0 + 8 * (V_FULL + s), 0, 0, 4 * static_cast<int>(rank), page, pol_kv);
+            }
+          }
+          ++n;
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok || keep >= kTile) continue;
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars[TAIL], tails & 1, abort_flag, kWaitNs));
+          ++tails;
+          if (!ok) continue;
+          for (int b = 0; b < 4; ++b) {
+            uint4* z = reinterpret_cast<uint4*>(dst + b * kSliceBytes + keep * 128);
+            for (int i = lane; i < (kTile - keep) * 8; i += 32) z[i] = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) arrive_pair(bar0 + 8 * (V_FULL + s));
+        }
+      }
+    }
+    if (warp == kWarpQ) check_plan(p);
+    if (!ok && lane == 0) {
+      fail(abort_flag, p.status);
+      // copies in flight land (bounded) before this CTA may end
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 1000000ull) {
+      }
+    }
+    __syncwarp();
+  } else if (warp == kWarpMma) {
+    // ------------------------------------------------------------ MMAs
+    // The even CTA's warp issues for the pair, converged: its control flow and
+    // operands are the same in all lanes.
+    if (rank == 0) {
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      constexpr uint32_t idesc_qk = idesc_16bit_f32(128, kBN, false, kHalf);
+      constexpr uint32_t idesc_pv = idesc_16bit_f32(128, 256, true, kHalf);
+      const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t k_desc = sdesc_sw128(smem_u32(sK), 16, 1024);
+      const uint64_t v_desc = sdesc_sw128(smem_u32(sV), kSliceBytes, 1024);  // MN-major
+      const uint64_t p_desc = sdesc_sw128(smem_u32(sP), 16, 1024);
+      auto wait = [&](int bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait(&bars[bar], parity, abort_flag, kWaitNs));
+      };
+      bool ok = true;
+      uint32_t kn = 0, vn = 0, tn = 0, qn = 0;  // K and V stages, tiles and units so far
+      int before = 0;                           // pages of the tile whose P V is due
+      bool fresh = false;                       // that tile is its unit's first here
+      auto issue_pv = [&]() {
+        ok = ok && wait(P_FULL, (tn - 1) & 1);
+        for (int half = 0; half < before && ok; ++half, ++vn) {
+          const int vs = static_cast<int>(vn % kVStages);
+          ok = wait(V_FULL + vs, (vn / kVStages) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t vd = v_desc + static_cast<uint64_t>((vs * kVBytes) >> 4);
+          const uint64_t pd = p_desc + static_cast<uint64_t>((half * kSliceBytes) >> 4);
+          const bool first = fresh && half == 0;
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+#pragma unroll
+            for (int d = 0; d < 2; ++d)
+              umma2_f16_warp(tm + 128u * d, pd + static_cast<uint64_t>((kk * 32) >> 4),
+                             vd + static_cast<uint64_t>((2 * d * kSliceBytes + kk * 2048) >> 4), idesc_pv,
+                             (first && kk == 0) ? 0u : 1u);
+          umma2_commit_warp(&bars[V_EMPTY + vs]);
+        }
+        if (ok) umma2_commit_warp(&bars[PV_DONE]);
+      };
+      for (int u = run.u0; ok && walk_to(p.units, run, u, w); u = w.u + 1) {
+        const int pages = __shfl_sync(0xffffffffu, pages_of(w.unit.len), 0);
+        const int lo = __shfl_sync(0xffffffffu, w.lo, 0), hi = __shfl_sync(0xffffffffu, w.hi, 0);
+        ok = wait(Q_FULL, qn & 1);
+        ++qn;
+        for (int j = lo; j < hi && ok; ++j) {
+          const uint32_t s_col = tm + kTmemS + 64u * (tn & 1);
+#pragma unroll
+          for (int c = 0; c < 3; ++c, ++kn) {
+            const int ks = static_cast<int>(kn % kKStages);
+            if (ok) ok = wait(K_FULL + ks, (kn / kKStages) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t kd = k_desc + static_cast<uint64_t>((ks * kKBytes) >> 4);
+            const uint64_t qd = q_desc + static_cast<uint64_t>((c * kKBytes) >> 4);
+#pragma unroll
+            for (int s = 0; s < kKSlices; ++s)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma2_f16_warp(s_col, qd + static_cast<uint64_t>((s * kSliceBytes + kk * 32) >> 4),
+                               kd + static_cast<uint64_t>((s * kSliceBytes + kk * 32) >> 4), idesc_qk,
+                               (c == 0 && s == 0 && kk == 0) ? 0u : 1u);
+            umma2_commit_warp(&bars[K_EMPTY + ks]);
+          }
+          if (!ok) break;
+          umma2_commit_warp(&bars[S_FULL + (tn & 1)]);
+          if (j == hi - 1) umma2_commit_warp(&bars[Q_EMPTY]);
+          if (before > 0) issue_pv();
+          ++tn;
+          before = min(pages - 2 * j, 2);
+          fresh = j == lo;
+        }
+      }
+      if (ok && before > 0) issue_pv();
+      if (!ok && lane == 0) fail(abort_flag, p.status);
+      // every MMA is done with shared memory and TMEM before this CTA ends
+      umma2_commit_warp(&bars[DRAIN]);
+      mbar_wait(&bars[DRAIN], 0, nullptr, kWaitNs);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax + epilogue
+    // Warp quarter q (TMEM lanes 32 q ..): rows 32 (q & 1) .. of this CTA and page
+    // q >> 1 of the tile (or 256-dim half of the output); warps 4 .. 7 the second
+    // 32 keys (128 dims) of those.
+    const int q = warp & 3, kh = q >> 1, ch = warp >> 2, part = 2 * kh + ch;
+    const int r = 32 * (q & 1) + lane, row = kCtaRows * static_cast<int>(rank) + r;  // row: of the unit
+    const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
+    const uint32_t s_addr = tmem + lane_base + kTmemS + 32u * ch;
+    const uint32_t o_addr = tmem + lane_base + 128u * ch;
+    const uint32_t row_bar = 1 + (q & 1);  // the four warps of these 32 rows
+    const uint32_t p_full = mapa_shared(smem_u32(&bars[P_FULL]), 0);
+    const float c_log2 = p.scale_log2;
+    uint8_t* prow = sP + kh * kSliceBytes + r * 128;
+    const uint32_t swz = static_cast<uint32_t>(r & 7);
+    // What this thread has for its row, to be shared with the other three.  (Two
+    // buffers in turn, a barrier each time: a warp may be one turn ahead of one
+    // that still reads, not two.)
+    uint32_t turn = 0;
+    auto shared_row = [&](float v) {
+      float* buf = sRow + (turn & 1) * 4 * kCtaRows + r;
+      buf[part * kCtaRows] = v;
+      ++turn;
+      return buf;
+    };
+    bool ok = true;
+    uint32_t tn = 0;
+    for (int u = run.u0; ok && walk_to(p.units, run, u, w); u = w.u + 1) {
+      // keys this row sees (rows past the unit's last one: unmasked, not stored)
+      const int limit = row >= w.unit.rows ? 1 << 30
+                        : causal           ? min(w.unit.len, w.unit.limit0 + (w.unit.rel + row) / p.h_q)
+                                           : w.unit.len;
+      float ref = -INFINITY, l = 0.f;
+      int base = -32;
+      uint32_t bad = 0;  // pages of the window outside the pool
+      for (int j = w.lo; j < w.hi; ++j, ++tn) {
+        if (2 * j - base >= 32) {
+          base = 2 * j;
+          const int k = base + lane;
+          bool out = false;
+          if (k < pages_of(w.unit.len)) {
+            const int page = k < p.max_pages ? p.block_table[static_cast<long long>(w.unit.req) * p.max_pages + k] : -1;
+            out = page < 0 || page >= p.num_pages;
+          }
+          bad = __ballot_sync(0xffffffffu, out);
+        }
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(&bars[S_FULL + (tn & 1)], (tn >> 1) & 1, abort_flag, kWaitNs));
+        tc_fence_after();
+        float s[32], top;
+        tmem_ld32_max(s_addr + 64u * (tn & 1), s, top);
+        tmem_wait_ld();
+        int seen = limit - j * kBN - kTile * kh - 32 * ch;
+        if ((bad >> (2 * j + kh - base)) & 1u) seen = 0;
+        // (pages past the unit's last one have keys past every valid row's limit; rows past its last row are masked
+        // there too, for what the stage holds may be no number)
+        if (row >= w.unit.rows && (2 * j + kh) * kTile >= w.unit.len) seen = 0;
+        if (__any_sync(0xffffffffu, seen < 32)) {
+          const uint32_t keep = seen >= 32 ? ~0u : (seen <= 0 ? 0u : (1u << seen) - 1u);
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            if (!((keep >> i) & 1u)) s[i] = -INFINITY;
+            m4[i & 3] = fmaxf(m4[i & 3], s[i]);
+          }
+          top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        }
+        // the row's maximum over its four threads
+        const float* buf = shared_row(top);
+        ok = !named_bar_or(row_bar, 128, !ok);  // (a warp that gave up waiting takes the others along)
+        if (!ok) break;
+        const float mt = fmaxf(fmaxf(buf[0], buf[kCtaRows]), fmaxf(buf[2 * kCtaRows], buf[3 * kCtaRows])) * c_log2;
+        const float r_new = mt > ref + kTau ? mt : ref;
+        const float alpha = r_new == ref ? 1.f : ex2(ref - r_new);
+        ref = r_new;
+        const float mref = ref == -INFINITY ? 0.f : ref;
+        float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float2 cl = make_float2(c_log2, c_log2), nr = make_float2(-mref, -mref);
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float2 x = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]), cl, nr);
+          const float p0 = ex2(x.x), p1 = ex2(x.y);
+          pk[i] = pack2<kHalf>(p0, p1);
+          ls[i & 1] = __fadd2_rn(ls[i & 1], make_float2(p0, p1));
+        }
+        l = l * alpha + ((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y));
+        // P V of the tile before is done: P may be overwritten and O rescaled
+        if (tn >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&bars[PV_DONE], (tn - 1) & 1, abort_flag, kWaitNs));
+        if (j > w.lo && ok && __any_sync(0xffffffffu, alpha != 1.f)) {
+          tc_fence_after();
+#pragma unroll 1
+          for (uint32_t c0 = 0; c0 < 128; c0 += 16) {
+            uint32_t v[16];
+            tmem_ld16(o_addr + c0, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
+            tmem_st16(o_addr + c0, v);
+          }
+          tmem_wait_st();
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          *reinterpret_cast<uint4*>(prow + ((static_cast<uint32_t>(4 * ch + c) ^ swz) << 4)) =
+              make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_pair(p_full);
+      }
+      // the row's sum, in an order that all four share.  (A warp that gave up takes the others along.)
+      const float* sum = shared_row(l);
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars[PV_DONE], (tn - 1) & 1, abort_flag, kWaitNs));
+      ok = !named_bar_or(row_bar, 128, !ok);
+      if (!ok) break;
+      tc_fence_after();
+      l = (sum[0] + sum[kCtaRows]) + (sum[2 * kCtaRows] + sum[3 * kCtaRows]);
+      const float inv = l == 0.f ? 0.f : 1.f / l;  // 0: the row sees none of these keys
+      const bool direct = w.unit.parts == 1;
+      const int slot = w.unit.slot + (w.u == run.u0 ? run.piece : 0);
+      const long long first = direct ? w.unit.row0 : static_cast<long long>(slot) * kRowsPerBlock;
+      const int dim0 = 256 * kh + 128 * ch, q4 = lane & 3;
+      // 16 rows x 64 dims at a time.  The load leaves a row's values with four
+      // lanes, two of every eight each.
+#pragma unroll 1
+      for (int it = 0; it < 4; ++it) {
+        const int hh = it & 1, c0 = 64 * (it >> 1);
+        uint32_t v[32];
+        tmem_ld_16x64(o_addr + c0 + (static_cast<uint32_t>(16 * hh) << 16), v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int up = 0; up < 2; ++up) {
+          const int from = 16 * hh + 8 * up + (lane >> 2);  // lane that has this row's sum
+          const float iv = __shfl_sync(0xffffffffu, inv, from);
+          const int orow = row - lane + from;
+          const long long at = (first + orow) * kDv + dim0 + c0;
+          const bool store = orow < w.unit.rows;
+          if (!direct || p.out_type == MLA_DTYPE_FP32) {
+            float* dst = (direct ? static_cast<float*>(p.out) : p.o_accum) + at + 2 * q4;
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+              const float a = __uint_as_float(v[4 * n + 2 * up]), b = __uint_as_float(v[4 * n + 2 * up + 1]);
+              if (store)
+                *reinterpret_cast<float2*>(dst + 8 * n) =
+                    iv == 0.f ? make_float2(0.f, 0.f) : make_float2(a * iv, b * iv);
+            }
+            continue;
+          }
+          uint32_t x[8];
+#pragma unroll
+          for (int n = 0; n < 8; ++n) {
+            const float a = __uint_as_float(v[4 * n + 2 * up]) * iv, b = __uint_as_float(v[4 * n + 2 * up + 1]) * iv;
+            x[n] = iv == 0.f ? 0u : p.out_type == MLA_DTYPE_FP16 ? pack2<true>(a, b) : pack2<false>(a, b);
+          }
+          // word n of lane q4 -> word q4 of lane n, within four lanes and four
+          // words: each then holds whole 16-byte pieces, and a store of the warp
+          // covers 64 bytes of 8 rows
+#pragma unroll
+          for (int g = 0; g < 8; g += 4) {
+            uint32_t* y = x + g;
+            {
+              const bool odd = q4 & 1;
+              const uint32_t s0 = odd ? y[0] : y[1], s1 = odd ? y[2] : y[3];
+              const uint32_t r0 = __shfl_xor_sync(0xffffffffu, s0, 1), r1 = __shfl_xor_sync(0xffffffffu, s1, 1);
+              if (odd) {
+                y[0] = r0;
+                y[2] = r1;
+              } else {
+                y[1] = r0;
+                y[3] = r1;
+              }
+            }
+            {
+              const bool odd = q4 & 2;
+              const uint32_t s0 = odd ? y[0] : y[2], s1 = odd ? y[1] : y[3];
+              const uint32_t r0 = __shfl_xor_sync(0xffffffffu, s0, 2), r1 = __shfl_xor_sync(0xffffffffu, s1, 2);
+              if (odd) {
+                y[0] = r0;
+                y[1] = r1;
+              } else {
+                y[2] = r0;
+                y[3] = r1;
+              }
+            }
+            if (store)
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at + 8 * (g + q4)) =
+                  make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        }
+      }
+      if (part == 0 && row < w.unit.rows)
+        (direct ? p.lse : p.lse_accum)[first + row] = l == 0.f ? -INFINITY : (ref + __log2f(l)) * kLn2;
+      // O has been read: the next unit's first P V waits for this warp's P
+      tc_fence_before();
+    }
+    if (!ok && lane == 0) fail(abort_flag, p.status);
+  }
+
+  // ------------------------------------------------------------ teardown
+  tc_fence_before();
+  __syncthreads();
+  cluster_arrive();  // the other CTA loads, arrives and multiplies here no more
+  cluster_wait();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    tmem2_dealloc(tmem, kTmemCols);
+  }
+  cluster_arrive();  // neither CTA ends while the other gives TMEM back
+  cluster_wait();
+}
+
+// ------------------------------------------------------------------ combine
+
+// Rows of the units that were cut (their pieces merged) and of those without
+// keys (zeros):  out = sum_s e^(lse_s - m) O_s / Z, lse = m + ln Z.
+// A warp a row, 16 columns a lane; four pieces in flight.  Bound by the latency of
+// a few reads: the rows are at most 128 for each pair.
+__global__ void __launch_bounds__(128) chunk_combine_kernel(const ChunkParams p) {
+  constexpr int kAhead = 4;
+  const int lane = threadIdx.x & 31;
+  const long long rows = static_cast<long long>(p.head[kHeadFix]) * kRowsPerBlock;
+  pdl_wait_prior_grid();  // (also by blocks without work: a plan made next must not meet the kernel before)
+  for (long long i = blockIdx.x * 4ll + (threadIdx.x >> 5); i < rows; i += gridDim.x * 4ll) {
+    const Unit unit = load_unit(p.units, p.fix[i / kRowsPerBlock]);
+    const int r = static_cast<int>(i % kRowsPerBlock);
+    if (r >= unit.rows) continue;
+    const long long at = static_cast<long long>(unit.slot) * kRowsPerBlock + r;
+    float m = -INFINITY;
+    for (int s = lane; s < unit.parts; s += 32) m = fmaxf(m, p.lse_accum[at + s * kRowsPerBlock]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float4 acc[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float z = 0.f;
+    for (int s0 = 0; s0 < unit.parts; s0 += kAhead) {
+      float4 v[kAhead][4];
+      float e[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const bool in = s0 + k < unit.parts;
+        const long long a = at + (s0 + k) * kRowsPerBlock;
+        e[k] = in ? p.lse_accum[a] : -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          v[k][c] = in ? *reinterpret_cast<const float4*>(p.o_accum + a * kDv + 128 * c + 4 * lane)
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const float w = e[k] == -INFINITY ? 0.f : expf(e[k] - m);
+        z += w;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          acc[c].x = fmaf(w, v[k][c].x, acc[c].x);
+          acc[c].y = fmaf(w, v[k][c].y, acc[c].y);
+          acc[c].z = fmaf(w, v[k][c].z, acc[c].z);
+          acc[c].w = fmaf(w, v[k][c].w, acc[c].w);
+        }
+      }
+    }
+    const float inv = z == 0.f ? 0.f : 1.f / z;
+    const long long row = (static_cast<long long>(unit.row0) + r) * kDv + 4 * lane;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float4 o = make_float4(acc[c].x * inv, acc[c].y * inv, acc[c].z * inv, acc[c].w * inv);
+      const long long at_out = row + 128 * c;
+      if (p.out_type == MLA_DTYPE_FP32)
+        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at_out) = o;
+      else if (p.out_type == MLA_DTYPE_FP16)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at_out) =
+            make_uint2(pack2<true>(o.x, o.y), pack2<true>(o.z, o.w));
+      else
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at_out) =
+            make_uint2(pack2<false>(o.x, o.y), pack2<false>(o.z, o.w));
+    }
+    if (lane == 0) p.lse[unit.row0 + r] = z == 0.f ? -INFINITY : m + logf(z);
+  }
+}
+
+// ------------------------------------------------------------------ plan
+
+constexpr int kPlanThreads = 1024;
+
+// Sum over the block of one value a thread, exclusive; *total gets all of it.
+template <typename T>
+__device__ __forceinline__ T block_scan(T v, T* s_warp, T* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  T x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) s_warp[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    T y = s_warp[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const T z = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) y += z;
+    }
+    s_warp[lane] = y;
+  }
+  __syncthreads();
+  const T base = warp > 0 ? s_warp[warp - 1] : T(0);
+  *total = s_warp[31];
+  __syncthreads();
+  return base + x - v;
+}
+
+// Units of all requests, in order, and the cuts that give every pair the same
+// cost: a unit costs its tiles and kFixedCost more (its Q, its epilogue), pair i
+// begins where the sum reaches i / pairs of the whole.  A cut within a unit's
+// fixed part, or that would leave less than kLeastTiles on one side, moves to the
+// unit's border.  One block, made once for a batch.
+__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPlanParams p) {
+  __shared__ long long s_warp64[32];
+  __shared__ int s_warp[32];
+  __shared__ int broken;
+  __shared__ int cut_u[kMaxChunkParts + 1], cut_t[kMaxChunkParts + 1];
+  const int tid = threadIdx.x;
+  if (tid == 0) broken = 0;
+  __syncthreads();
+  for (int b = tid; b < p.batch; b += kPlanThreads) {
+    const int a = p.cu[b], e = p.cu[b + 1], n = p.lens[b];
+    p.made[b] = a;
+    if (b == p.batch - 1) p.made[p.batch] = e;
+    p.made[p.batch + 1 + b] = n;
+    if (a < 0 || e < a || e > p.total_q || n > kMaxChunkKeys) broken = 1;
+  }
+  __syncthreads();
+  if (broken) {  // offsets out of order could make requests overlap: nothing is done then
+    if (tid == 0) {
+      report(p.status, MLA_ERR_BAD_INDEX);
+      p.head[kHeadUnits] = 0;
+      p.head[kHeadCausal] = p.causal;
+      p.head[kHeadFix] = 0;
+    }
+    for (int i = tid; i < p.parts * MLA_SCHED_INTS; i += kPlanThreads) p.sched[i] = 0;
+    return;
+  }
+  // first unit of each request
+  int units = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    int n = 0;
+    if (b < p.batch) n = ((p.cu[b + 1] - p.cu[b]) * p.h_q + kRowsPerBlock - 1) / kRowsPerBlock;
+    int all;
+    const int at = block_scan(n, s_warp, &all);
+    if (b < p.batch) p.first[b] = units + at;
+    units += all;
+  }
+  if (tid == 0) {
+    p.head[kHeadUnits] = units;
+    p.head[kHeadCausal] = p.causal;
+    p.head[kHeadFix] = 0;
+  }
+  __syncthreads();
+  long long cost = 0;
+  for (int u0 = 0; u0 < units; u0 += kPlanThreads) {
+    const int u = u0 + tid;
+    long long mine = 0;
+    if (u < units) {
+      int lo = 0, hi = p.batch;  // first[lo] <= u: the last such request (those before it with none have the same first)
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (p.first[mid] <= u)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      const int tok0 = p.cu[lo], n = p.cu[lo + 1] - tok0, keys = max(p.lens[lo], 0);
+      const int rel = (u - p.first[lo]) * kRowsPerBlock, rows = min(n * p.h_q - rel, kRowsPerBlock);
+      const int limit0 = keys - n + 1;
+      const int len = p.causal ? max(limit0 + (rel + rows - 1) / p.h_q, 0) : keys;
+      int4* e = reinterpret_cast<int4*>(p.units + static_cast<long long>(u) * kUnitInts);
+      e[0] = make_int4(tok0 * p.h_q + rel, rows, rel, lo);
+      e[1] = make_int4(len, limit0, 0, len > 0 ? 1 : 0);
+      mine = len > 0 ? tiles_of(len) + kFixedCost : 0;
+      if (len == 0) p.fix[atomicAdd(&p.head[kHeadFix], 1)] = u;  // (in any order: no result depends on it)
+    }
+    long long all;
+    const long long at = block_scan(mine, s_warp64, &all);
+    if (u < units) p.prefix[u] = cost + at;
+    cost += all;
+  }
+  __syncthreads();
+  for (int i = tid; i <= p.parts; i += kPlanThreads) {
+    int u = units, t = 0;
+    if (i < p.parts && units > 0 && cost > 0) {
+      const long long x = cost * i / p.parts;
+      int lo = 0, hi = units;  // the last unit that begins at or before x
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (p.prefix[mid] <= x)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      u = lo;
+      const int tiles = tiles_of(p.units[static_cast<long long>(u) * kUnitInts + 4]);
+      const long long off = x - p.prefix[u];
+      t = static_cast<int>(min(max(off - kFixedCost, 0ll), static_cast<long long>(tiles)));
+      if (t < kLeastTiles) t = 0;
+      if (t > 0 && tiles - t < kLeastTiles) {
+        ++u;
+        t = 0;
+      }
+    }
+    cut_u[i] = u;
+    cut_t[i] = t;
+  }
+  __syncthreads();
+  // Cuts inside a unit, each counted once; the first of a unit opens its slots.
+  const bool in = tid < p.parts;
+  const bool inside = in && cut_t[tid] > 0 && (tid == 0 || cut_u[tid] != cut_u[tid - 1] || cut_t[tid] != cut_t[tid - 1]);
+  const bool opens = inside && (tid == 0 || cut_u[tid] != cut_u[tid - 1] || cut_t[tid - 1] == 0);
+  int all;
+  const int at = block_scan((inside ? 1 : 0) + (opens ? 1 : 0), s_warp, &all);
+  if (opens) {
+    int cuts = 1;
+    for (int i = tid + 1; i < p.parts && cut_u[i] == cut_u[tid]; ++i) cuts += cut_t[i] != cut_t[i - 1];
+    int32_t* e = p.units + static_cast<long long>(cut_u[tid]) * kUnitInts;
+    e[6] = at;
+    e[7] = cuts + 1;
+    p.fix[atomicAdd(&p.head[kHeadFix], 1)] = cut_u[tid];
+  }
+  if (in) {
+    int piece = 0;
+    if (cut_t[tid] > 0)
+      for (int i = tid; i >= 0 && cut_u[i] == cut_u[tid] && cut_t[i] > 0; --i)
+        piece += i == 0 || cut_u[i - 1] != cut_u[i] || cut_t[i - 1] != cut_t[i];
+    int4* e = reinterpret_cast<int4*>(p.sched + tid * MLA_SCHED_INTS);
+    e[0] = make_int4(cut_u[tid], cut_t[tid], cut_u[tid + 1], cut_t[tid + 1]);
+    e[1] = make_int4(piece, 0, 0, 0);
+  }
+}
+static_assert(kMaxChunkParts <= kPlanThreads, "a thread a cut");
+
+}  // namespace ck
+
+ChunkPlanLayout chunk_plan_layout(int batch, int total_q, int h_q, int parts) {
+  const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  ChunkPlanLayout z;
+  z.max_units = static_cast<int>(static_cast<long long>(total_q) * h_q / kRowsPerBlock) + batch;
+  const size_t units = static_cast<size_t>(z.max_units);
+  z.units = 256;
+  z.sched = z.units + up(units * kUnitInts * 4);
+  z.fix = z.sched + up(static_cast<size_t>(parts) * MLA_SCHED_INTS * 4);
+  z.prefix = z.fix + up(units * 4);
+  z.first = z.prefix + up(units * 8);
+  z.made = z.first + up(static_cast<size_t>(batch) * 4);
+  z.bytes = z.made + up((2 * static_cast<size_t>(batch) + 1) * 4);
+  return z;
+}
+
+cudaError_t launch_chunk_plan(const ChunkPlanParams& p, cudaStream_t st) {
+  ck::chunk_plan_kernel<<<1, ck::kPlanThreads, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+namespace {
+
+using ChunkKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, ChunkParams);
+ChunkKernel chunk_kernel_of(bool half, bool stall) {
+  return stall ? ck::chunk_kernel<false, true> : half ? ck::chunk_kernel<true> : ck::chunk_kernel<false>;
+}
+
+}  // namespace
+
+cudaError_t chunk_setup() {
+  for (int v = 0; v < 3; ++v) {
+    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(chunk_kernel_of(v == 1, v == 2)),
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, ck::kSmemBytes);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_chunk(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const ChunkParams& p,
+                         bool half, bool stall, int parts, cudaStream_t st) {
+  chunk_kernel_of(half, stall)<<<2 * parts, ck::kThreads, ck::kSmemBytes, st>>>(q, k, v, p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_chunk_combine(const ChunkParams& p, int parts, int sms, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min(parts * (kRowsPerBlock / 4), 16 * sms)), 1, 1);
+  cfg.blockDim = dim3(128, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, ck::chunk_combine_kernel, p);
+}
+
+}  // namespace mla

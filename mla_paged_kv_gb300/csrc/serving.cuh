@@ -68,6 +68,49 @@ struct AppendParams {
 };
 cudaError_t launch_append(const AppendParams& p, bool half, bool fp8, int sms, cudaStream_t stream);
 
+// A rotary table: each pair's step a position, in 2^-64 turns.
+constexpr int kMaxRopeDim = 256;
+struct RopeSteps {
+  unsigned long long step[kMaxRopeDim / 2];
+};
+cudaError_t launch_rope_table(const RopeSteps& f, int dim, float magnitude, long long first, int positions, float* out,
+                              int sms, cudaStream_t st);
+
+// Rotation (and norm) of heads: queries, and keys or none (heads = 0).
+struct RopeSide {
+  const uint16_t* x;
+  uint16_t* out;  // may be x
+  const uint16_t* weight;
+  long long x_token_stride, x_head_stride, out_token_stride, out_head_stride;
+  int heads;
+  int units;  // warps a token
+};
+struct RopeHeadsParams {
+  RopeSide side[2];
+  int total, batch, dim, rope, offset, interleaved;
+  int pairs, items, lanes;  // rope_heads_layout
+  float eps;
+  const int32_t *positions, *cu, *seqlens;
+  const float* cos_sin;  // NULL: no rotation
+  int max_pos;
+  int32_t* status;
+};
+constexpr int kMaxHeadDim = 1024;
+// The kernel's layout; passes: dims outside the rotary part are read and
+// written too.  False where the grid would be too large.
+bool rope_heads_layout(RopeHeadsParams* p, bool passes, int* per_lane, long long* blocks);
+cudaError_t launch_rope_heads(const RopeHeadsParams& p, bool half, int per_lane, long long blocks, cudaStream_t st);
+
+struct GatherParams {
+  const void* cache;
+  const int32_t *table, *cu, *starts;  // starts: NULL: 0
+  int max_pages, num_pages, batch, total;
+  uint16_t* out;
+  long long out_stride;
+  int32_t* status;
+};
+cudaError_t launch_gather(const GatherParams& p, bool fp8, int sms, cudaStream_t st);
+
 // The bookkeeping of a page pool.
 struct PageState {
   int32_t* refcount;
@@ -110,5 +153,41 @@ cudaError_t launch_prompt_plan(const int32_t* cu_q, const int32_t* cu_k, int bat
 cudaError_t prompt_setup();  // once per device: shared-memory opt-in
 cudaError_t launch_prompt(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PromptParams& p,
                           bool half, int d_qk, bool pair, bool stall, int sms, cudaStream_t st);
+
+// Attention of ragged chunks over a paged cache: the plan's parts, from its start.
+constexpr int kMaxChunkParts = 1024;
+constexpr int kMaxChunkKeys = 1 << 24;  // keys of a request
+constexpr int kFixedCost = 3;           // a unit's Q load and epilogue, in 128-key tiles
+constexpr int kLeastTiles = 1;          // of a unit's piece
+enum : int { kHeadUnits = 0, kHeadCausal = 1, kHeadFix = 2 };  // header: units, causal, units for the combine
+struct ChunkPlanLayout {
+  int max_units;
+  size_t units, sched, fix, prefix, first, made, bytes;
+};
+ChunkPlanLayout chunk_plan_layout(int batch, int total_q, int h_q, int parts);
+struct ChunkPlanParams {
+  const int32_t *cu, *lens;
+  int batch, total_q, h_q, causal, parts;
+  int32_t *head, *units, *sched, *fix, *first, *made;
+  long long* prefix;
+  int32_t* status;
+};
+struct ChunkParams {
+  const int32_t *head, *units, *sched, *fix, *made;  // of the plan
+  const int32_t *cu, *lens;                          // the caller's, to be compared with the plan's, or NULL
+  const int32_t* block_table;
+  int max_pages, num_pages, batch, h_q;
+  float scale_log2;
+  void* out;  // [total_q * h_q, 512]
+  int out_type;
+  float* lse;
+  float *o_accum, *lse_accum;  // [2 parts][128][512], [2 parts][128]
+  int32_t* status;
+};
+cudaError_t chunk_setup();  // once per device: shared-memory opt-in
+cudaError_t launch_chunk_plan(const ChunkPlanParams& p, cudaStream_t st);
+cudaError_t launch_chunk(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const ChunkParams& p,
+                         bool half, bool stall, int parts, cudaStream_t st);
+cudaError_t launch_chunk_combine(const ChunkParams& p, int parts, int sms, cudaStream_t st);
 
 }  // namespace mla

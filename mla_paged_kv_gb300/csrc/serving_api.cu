@@ -49,7 +49,7 @@ int serving_device(int* sms) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MLA_ERR_CUDA;
   std::lock_guard<std::mutex> lock(mu);
   if (!done[dev]) {
-    if (prompt_setup() != cudaSuccess || copy_pages_setup() != cudaSuccess) {
+    if (prompt_setup() != cudaSuccess || copy_pages_setup() != cudaSuccess || chunk_setup() != cudaSuccess) {
       cudaGetLastError();
       return MLA_ERR_CUDA;
     }
@@ -245,6 +245,85 @@ int shared_decode(const void* d_q, const void* d_kv, const int32_t* d_block_tabl
   if (rc != MLA_OK) return rc;
   return launched(launch_shared_combine(c.o_accum, c.lse_accum, c.units, c.split_offset, batch, s_q * h_q, d_out,
                                         out_type, d_lse, sms, st));
+}
+
+// Strides of a rope_heads operand: multiples of 8 elements (0 too: a broadcast
+// input), within 2^40.
+bool head_strides(long long total, int heads, long long ts, long long hs) {
+  const long long most = 1LL << 40;
+  return (total <= 1 || (ts % 8 == 0 && ts >= 0 && ts <= most)) &&
+         (heads <= 1 || (hs % 8 == 0 && hs >= 0 && hs <= most));
+}
+
+int chunk_sizes(int batch, int total_q, int h_q, int num_parts) {
+  if (batch < 1 || total_q < 0 || h_q < 1 || num_parts < 1) return MLA_ERR_INVALID_ARG;
+  if (static_cast<long long>(total_q) * h_q > kMaxInt || batch > (1 << 20) || num_parts > kMaxChunkParts)
+    return MLA_ERR_UNSUPPORTED;
+  return MLA_OK;
+}
+
+// mla_chunk_attention_fwd; stall: the instance of the timeout test.
+int chunk_attention(const void* d_q, const void* d_kv, const int32_t* d_block_table, int max_pages, int num_pages,
+                    int batch, int total_q, int h_q, int dtype, float softmax_scale, const int32_t* cu,
+                    const int32_t* lens, const void* d_plan, size_t plan_bytes, int num_parts, void* d_workspace,
+                    size_t workspace_bytes, void* d_out, int out_type, float* d_lse, int32_t* d_status, bool stall,
+                    mla_stream_t stream) {
+  if (!d_kv || !d_block_table || !d_plan || !d_workspace || !d_status) return MLA_ERR_INVALID_ARG;
+  if (total_q > 0 && (!d_q || !d_out || !d_lse)) return MLA_ERR_INVALID_ARG;
+  if (max_pages < 1 || num_pages < 1) return MLA_ERR_INVALID_ARG;
+  if (dtype != MLA_DTYPE_BF16 && dtype != MLA_DTYPE_FP16) return MLA_ERR_INVALID_ARG;
+  if (out_type != MLA_DTYPE_BF16 && out_type != MLA_DTYPE_FP32 && out_type != MLA_DTYPE_FP16)
+    return MLA_ERR_INVALID_ARG;
+  if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.f)) return MLA_ERR_INVALID_ARG;
+  if (!aligned(d_q, 16) || !aligned(d_kv, 16) || !aligned(d_plan, 16) || !aligned(d_workspace, 16) ||
+      !aligned(d_out, 16) || !aligned(d_block_table, 4) || !aligned(d_lse, 4) || !aligned(cu, 4) ||
+      !aligned(lens, 4) || !aligned(d_status, 4))
+    return MLA_ERR_INVALID_ARG;
+  int rc = chunk_sizes(batch, total_q, h_q, num_parts);
+  if (rc != MLA_OK) return rc;
+  if (max_pages > kMaxRowPages || num_pages > (1 << 30)) return MLA_ERR_UNSUPPORTED;
+  const ChunkPlanLayout z = chunk_plan_layout(batch, total_q, h_q, num_parts);
+  if (plan_bytes < z.bytes || workspace_bytes < mla_chunk_workspace_bytes(num_parts)) return MLA_ERR_INVALID_ARG;
+  int sms = 0;
+  rc = serving_device(&sms);
+  if (rc != MLA_OK || total_q == 0) return rc;
+  const char* plan = static_cast<const char*>(d_plan);
+  auto ints = [&](size_t at) { return reinterpret_cast<const int32_t*>(plan + at); };
+  ChunkParams p{};
+  p.head = ints(0);
+  p.units = ints(z.units);
+  p.sched = ints(z.sched);
+  p.fix = ints(z.fix);
+  p.made = ints(z.made);
+  p.cu = cu;
+  p.lens = lens;
+  p.block_table = d_block_table;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  p.batch = batch;
+  p.h_q = h_q;
+  p.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * 1.4426950408889634);
+  p.out = d_out;
+  p.out_type = out_type;
+  p.lse = d_lse;
+  p.o_accum = static_cast<float*>(d_workspace);
+  p.lse_accum = p.o_accum + 2ll * num_parts * MLA_ROWS_PER_BLOCK * MLA_D_V;
+  p.status = d_status;
+  // queries and cache rows as (64 dims of a slice, rows, slices): one box is
+  // several whole slices, each 64 rows of 128 swizzled bytes
+  CUtensorMap qm, km, vm;
+  const cuuint64_t q_dims[4] = {64, static_cast<cuuint64_t>(total_q) * h_q, MLA_D_QK / 64, 1};
+  const cuuint64_t q_strides[3] = {2 * MLA_D_QK, 128, 2 * MLA_D_QK};
+  const cuuint32_t q_box[4] = {64, 64, MLA_D_QK / 64, 1};
+  const cuuint64_t dims[4] = {64, MLA_PAGE_SIZE, MLA_D_QK / 64, static_cast<cuuint64_t>(num_pages)};
+  const cuuint64_t strides[3] = {2 * MLA_D_QK, 128, 2 * MLA_D_QK * MLA_PAGE_SIZE};
+  const cuuint32_t k_box[4] = {64, 64, 3, 1}, v_box[4] = {64, 64, 4, 1};
+  rc = encode_map16(&qm, d_q, 4, q_dims, q_strides, q_box);
+  if (rc == MLA_OK) rc = encode_map16(&km, d_kv, 4, dims, strides, k_box);
+  if (rc == MLA_OK) rc = encode_map16(&vm, d_kv, 4, dims, strides, v_box);
+  if (rc != MLA_OK) return rc;
+  rc = launched(launch_chunk(qm, km, vm, p, dtype == MLA_DTYPE_FP16, stall, num_parts, to_stream(stream)));
+  return rc != MLA_OK || stall ? rc : launched(launch_chunk_combine(p, num_parts, sms, to_stream(stream)));
 }
 
 }  // namespace
@@ -498,9 +577,239 @@ int mla_test_shared_prefix_timeout(const void* d_q, const void* d_kv, const int3
                        d_status, 1, stream);
 }
 
+int mla_rope_frequencies(int dim, double base, int scaling, double factor, double original, double low, double high,
+                         double* h_freq, double* h_magnitude) {
+  if (!h_freq || !h_magnitude || dim < 8 || dim % 8 != 0) return MLA_ERR_INVALID_ARG;
+  if (dim > kMaxRopeDim) return MLA_ERR_UNSUPPORTED;
+  if (scaling < MLA_ROPE_NONE || scaling > MLA_ROPE_WAVELENGTH) return MLA_ERR_INVALID_ARG;
+  if (!std::isfinite(base) || !(base > 1.0)) return MLA_ERR_INVALID_ARG;
+  if (scaling != MLA_ROPE_NONE && !(std::isfinite(factor) && factor >= 1.0)) return MLA_ERR_INVALID_ARG;
+  const bool parts = scaling == MLA_ROPE_YARN || scaling == MLA_ROPE_WAVELENGTH;
+  if (parts && !(std::isfinite(original) && original > 0.0 && std::isfinite(high) && low > 0.0 && low < high))
+    return MLA_ERR_INVALID_ARG;
+  constexpr double kTurn = 6.283185307179586476925;
+  if (scaling == MLA_ROPE_NTK) base *= std::pow(factor, dim / (dim - 2.0));
+  double from = 0.0, to = 0.0;
+  if (scaling == MLA_ROPE_YARN) {
+    auto pair_of = [&](double turns) { return dim * std::log(original / (turns * kTurn)) / (2.0 * std::log(base)); };
+    from = std::fmax(std::floor(pair_of(high)), 0.0);
+    to = std::fmin(std::ceil(pair_of(low)), dim - 1.0);
+  }
+  for (int i = 0; i < dim / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / dim);
+    double keep = 1.0;  // the share that is not stretched
+    if (scaling == MLA_ROPE_LINEAR) keep = 0.0;
+    if (scaling == MLA_ROPE_YARN) keep = 1.0 - std::fmin(std::fmax((i - from) / std::fmax(to - from, 0.001), 0.0), 1.0);
+    if (scaling == MLA_ROPE_WAVELENGTH)
+      keep = std::fmin(std::fmax((original * f / kTurn - low) / (high - low), 0.0), 1.0);
+    if (keep < 1.0) f = keep * f + (1.0 - keep) * f / factor;
+    h_freq[i] = f;
+  }
+  *h_magnitude = scaling == MLA_ROPE_YARN ? 0.1 * std::log(factor) + 1.0 : 1.0;
+  return MLA_OK;
+}
+
+int mla_rope_table(const double* h_freq, int dim, double magnitude, long long first_pos, int positions,
+                   float* d_cos_sin, mla_stream_t stream) {
+  if (!h_freq || dim < 8 || dim % 8 != 0 || !std::isfinite(magnitude) || first_pos < 0 || positions < 0)
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned(d_cos_sin, 16) || (positions > 0 && !d_cos_sin)) return MLA_ERR_INVALID_ARG;
+  if (dim > kMaxRopeDim || first_pos > kMaxInt + 1 - positions) return MLA_ERR_UNSUPPORTED;
+  RopeSteps steps{};
+  for (int i = 0; i < dim / 2; ++i) {
+    const double f = h_freq[i];
+    if (!(f >= 0.0 && f <= 1024.0)) return MLA_ERR_INVALID_ARG;
+    // turns a position, without the whole ones, in units of 2^-64
+    const double turns = f / 6.283185307179586476925;
+    const double part = std::ldexp(turns - std::floor(turns), 64);
+    steps.step[i] = part >= 18446744073709551615.0 ? 0ull : static_cast<unsigned long long>(part);
+  }
+  int sms = 0;
+  const int rc = device_ready(&sms);
+  if (rc != MLA_OK || positions == 0) return rc;
+  return launched(launch_rope_table(steps, dim, static_cast<float>(magnitude), first_pos, positions, d_cos_sin, sms,
+                                    to_stream(stream)));
+}
+
+int mla_rope_heads(const void* d_x, long long x_token_stride, long long x_head_stride, void* d_out,
+                   long long out_token_stride, long long out_head_stride, int heads, const void* d_x_weight,
+                   const void* d_k, long long k_token_stride, long long k_head_stride, void* d_k_out,
+                   long long k_out_token_stride, long long k_out_head_stride, int k_heads, const void* d_k_weight,
+                   int dim, int dtype, int total_tokens, int rope_dim, int rope_offset, int rope_interleaved,
+                   float norm_eps, const int32_t* d_positions, const int32_t* d_cu_seqlens,
+                   const int32_t* d_cache_seqlens, int batch, const float* d_cos_sin, int max_pos, int32_t* d_status,
+                   mla_stream_t stream) {
+  if (!d_status || total_tokens < 0 || heads < 1 || k_heads < 0 || dim < 8 || dim % 8 != 0) return MLA_ERR_INVALID_ARG;
+  if (total_tokens > 0 && (!d_x || !d_out || (k_heads > 0 && (!d_k || !d_k_out)))) return MLA_ERR_INVALID_ARG;
+  if (k_heads == 0 && (d_k || d_k_out || d_k_weight)) return MLA_ERR_INVALID_ARG;
+  if (dtype != MLA_DTYPE_BF16 && dtype != MLA_DTYPE_FP16) return MLA_ERR_INVALID_ARG;
+  if (rope_dim < 0 || rope_dim % 16 != 0 || rope_offset < 0 || rope_offset % 8 != 0 || rope_offset > dim - rope_dim)
+    return MLA_ERR_INVALID_ARG;
+  if ((d_x_weight || d_k_weight) && !(std::isfinite(norm_eps) && norm_eps >= 0.f)) return MLA_ERR_INVALID_ARG;
+  if (d_cos_sin) {
+    if (rope_dim < 16 || max_pos < 1) return MLA_ERR_INVALID_ARG;
+    if (!d_positions && (!d_cache_seqlens || batch < 1)) return MLA_ERR_INVALID_ARG;
+    if (d_positions && (d_cu_seqlens || d_cache_seqlens)) return MLA_ERR_INVALID_ARG;
+    if (!d_positions && !d_cu_seqlens && total_tokens % batch != 0) return MLA_ERR_INVALID_ARG;
+  } else if (rope_dim != 0 || d_positions || d_cu_seqlens || d_cache_seqlens || (!d_x_weight && !d_k_weight)) {
+    return MLA_ERR_INVALID_ARG;
+  }
+  if (!aligned(d_x, 16) || !aligned(d_out, 16) || !aligned(d_k, 16) || !aligned(d_k_out, 16) ||
+      !aligned(d_x_weight, 16) || !aligned(d_k_weight, 16) || !aligned(d_cos_sin, 16) || !aligned(d_positions, 4) ||
+      !aligned(d_cu_seqlens, 4) || !aligned(d_cache_seqlens, 4) || !aligned(d_status, 4))
+    return MLA_ERR_INVALID_ARG;
+  if (!head_strides(total_tokens, heads, x_token_stride, x_head_stride) ||
+      !head_strides(total_tokens, heads, out_token_stride, out_head_stride) ||
+      !head_strides(total_tokens, k_heads, k_token_stride, k_head_stride) ||
+      !head_strides(total_tokens, k_heads, k_out_token_stride, k_out_head_stride))
+    return MLA_ERR_INVALID_ARG;
+  // in place: each head onto itself
+  auto moved = [&](const void* from, const void* to, int n, long long t0, long long h0, long long t1, long long h1) {
+    return n > 0 && from == to && ((total_tokens > 1 && t0 != t1) || (n > 1 && h0 != h1));
+  };
+  if (moved(d_x, d_out, heads, x_token_stride, x_head_stride, out_token_stride, out_head_stride) ||
+      moved(d_k, d_k_out, k_heads, k_token_stride, k_head_stride, k_out_token_stride, k_out_head_stride))
+    return MLA_ERR_INVALID_ARG;
+  if (dim > kMaxHeadDim || rope_dim > kMaxRopeDim || total_tokens > (1 << 30) || heads > (1 << 20) ||
+      k_heads > (1 << 20))
+    return MLA_ERR_UNSUPPORTED;
+  RopeHeadsParams p{};
+  p.side[0] = RopeSide{static_cast<const uint16_t*>(d_x), static_cast<uint16_t*>(d_out),
+                       static_cast<const uint16_t*>(d_x_weight), x_token_stride, x_head_stride, out_token_stride,
+                       out_head_stride, heads, 0};
+  p.side[1] = RopeSide{static_cast<const uint16_t*>(d_k), static_cast<uint16_t*>(d_k_out),
+                       static_cast<const uint16_t*>(d_k_weight), k_token_stride, k_head_stride, k_out_token_stride,
+                       k_out_head_stride, k_heads, 0};
+  p.total = total_tokens;
+  p.batch = batch;
+  p.dim = dim;
+  p.rope = rope_dim;
+  p.offset = rope_offset;
+  p.interleaved = rope_interleaved ? 1 : 0;
+  p.eps = norm_eps;
+  p.positions = d_positions;
+  p.cu = d_cu_seqlens;
+  p.seqlens = d_cache_seqlens;
+  p.cos_sin = d_cos_sin;
+  p.max_pos = max_pos;
+  p.status = d_status;
+  // dims outside the rotary part stay where they are when nothing moves or scales them
+  const bool passes = d_x_weight || d_k_weight || d_x != d_out || d_k != d_k_out;
+  int per_lane = 0;
+  long long blocks = 0;
+  if (!rope_heads_layout(&p, passes, &per_lane, &blocks)) return MLA_ERR_UNSUPPORTED;
+  int sms = 0;
+  const int rc = device_ready(&sms);
+  if (rc != MLA_OK || total_tokens == 0) return rc;
+  return launched(launch_rope_heads(p, dtype == MLA_DTYPE_FP16, per_lane, blocks, to_stream(stream)));
+}
+
+int mla_cache_gather(const void* d_cache, int cache_dtype, int num_pages, const int32_t* d_block_table, int max_pages,
+                     const int32_t* d_cu_seqlens, const int32_t* d_starts, int batch, int total_rows, void* d_out,
+                     long long out_stride, int32_t* d_status, mla_stream_t stream) {
+  if (!d_cache || !d_block_table || !d_cu_seqlens || !d_status) return MLA_ERR_INVALID_ARG;
+  if (num_pages < 1 || max_pages < 1 || batch < 1 || total_rows < 0) return MLA_ERR_INVALID_ARG;
+  if (total_rows > 0 && !d_out) return MLA_ERR_INVALID_ARG;
+  if (cache_dtype != MLA_DTYPE_BF16 && cache_dtype != MLA_DTYPE_FP16 && cache_dtype != MLA_DTYPE_FP8_RECORD)
+    return MLA_ERR_INVALID_ARG;
+  if (out_stride % 8 != 0 || out_stride < MLA_D_QK || out_stride > (1LL << 40)) return MLA_ERR_INVALID_ARG;
+  if (!aligned(d_cache, 16) || !aligned(d_out, 16) || !aligned(d_block_table, 4) || !aligned(d_cu_seqlens, 4) ||
+      !aligned(d_starts, 4) || !aligned(d_status, 4))
+    return MLA_ERR_INVALID_ARG;
+  if (max_pages > kMaxRowPages || num_pages > (1 << 30) || total_rows > (1 << 30)) return MLA_ERR_UNSUPPORTED;
+  int sms = 0;
+  const int rc = device_ready(&sms);
+  if (rc != MLA_OK || total_rows == 0) return rc;
+  GatherParams p{};
+  p.cache = d_cache;
+  p.table = d_block_table;
+  p.cu = d_cu_seqlens;
+  p.starts = d_starts;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  p.batch = batch;
+  p.total = total_rows;
+  p.out = static_cast<uint16_t*>(d_out);
+  p.out_stride = out_stride;
+  p.status = d_status;
+  return launched(launch_gather(p, cache_dtype == MLA_DTYPE_FP8_RECORD, sms, to_stream(stream)));
+}
+
+int mla_chunk_num_parts(void) {
+  int sms = 0;
+  const int rc = device_ready(&sms);
+  return rc != MLA_OK ? -rc : sms / 2 < 1 ? 1 : sms / 2 > kMaxChunkParts ? kMaxChunkParts : sms / 2;
+}
+
+size_t mla_chunk_plan_bytes(int batch, int total_q, int h_q, int num_parts) {
+  return chunk_sizes(batch, total_q, h_q, num_parts) == MLA_OK ? chunk_plan_layout(batch, total_q, h_q, num_parts).bytes
+                                                               : 0;
+}
+
+size_t mla_chunk_workspace_bytes(int num_parts) {
+  return num_parts < 1 || num_parts > kMaxChunkParts
+             ? 0
+             : 2 * static_cast<size_t>(num_parts) * MLA_ROWS_PER_BLOCK * (MLA_D_V + 1) * 4;
+}
+
+int mla_chunk_get_plan(const int32_t* d_cu_seqlens_q, const int32_t* d_cache_seqlens, int batch, int total_q, int h_q,
+                       int causal, int num_parts, void* d_plan, size_t plan_bytes, int32_t* d_status,
+                       mla_stream_t stream) {
+  if (!d_cu_seqlens_q || !d_cache_seqlens || !d_plan || !d_status) return MLA_ERR_INVALID_ARG;
+  if (!aligned(d_cu_seqlens_q, 4) || !aligned(d_cache_seqlens, 4) || !aligned(d_plan, 16) || !aligned(d_status, 4))
+    return MLA_ERR_INVALID_ARG;
+  int rc = chunk_sizes(batch, total_q, h_q, num_parts);
+  if (rc != MLA_OK) return rc;
+  const ChunkPlanLayout z = chunk_plan_layout(batch, total_q, h_q, num_parts);
+  if (plan_bytes < z.bytes) return MLA_ERR_INVALID_ARG;
+  int sms = 0;
+  rc = device_ready(&sms);
+  if (rc != MLA_OK) return rc;
+  char* plan = static_cast<char*>(d_plan);
+  auto ints = [&](size_t at) { return reinterpret_cast<int32_t*>(plan + at); };
+  ChunkPlanParams p{};
+  p.cu = d_cu_seqlens_q;
+  p.lens = d_cache_seqlens;
+  p.batch = batch;
+  p.total_q = total_q;
+  p.h_q = h_q;
+  p.causal = causal ? 1 : 0;
+  p.parts = num_parts;
+  p.head = ints(0);
+  p.units = ints(z.units);
+  p.sched = ints(z.sched);
+  p.fix = ints(z.fix);
+  p.first = ints(z.first);
+  p.made = ints(z.made);
+  p.prefix = reinterpret_cast<long long*>(plan + z.prefix);
+  p.status = d_status;
+  return launched(launch_chunk_plan(p, to_stream(stream)));
+}
+
+int mla_chunk_attention_fwd(const void* d_q, const void* d_kv, const int32_t* d_block_table, int max_pages,
+                            int num_pages, int batch, int total_q, int h_q, int dtype, float softmax_scale,
+                            const int32_t* d_cu_seqlens_q, const int32_t* d_cache_seqlens, const void* d_plan,
+                            size_t plan_bytes, int num_parts, void* d_workspace, size_t workspace_bytes, void* d_out,
+                            int out_type, float* d_lse, int32_t* d_status, mla_stream_t stream) {
+  return chunk_attention(d_q, d_kv, d_block_table, max_pages, num_pages, batch, total_q, h_q, dtype, softmax_scale,
+                         d_cu_seqlens_q, d_cache_seqlens, d_plan, plan_bytes, num_parts, d_workspace, workspace_bytes,
+                         d_out, out_type, d_lse, d_status, false, stream);
+}
+
+int mla_test_chunk_timeout(const void* d_q, const void* d_kv, const int32_t* d_block_table, int max_pages,
+                           int num_pages, int batch, int total_q, int h_q, int dtype, float softmax_scale,
+                           const int32_t* d_cu_seqlens_q, const int32_t* d_cache_seqlens, const void* d_plan,
+                           size_t plan_bytes, int num_parts, void* d_workspace, size_t workspace_bytes, void* d_out,
+                           int out_type, float* d_lse, int32_t* d_status, mla_stream_t stream) {
+  if (dtype == MLA_DTYPE_FP16) return MLA_ERR_UNSUPPORTED;
+  return chunk_attention(d_q, d_kv, d_block_table, max_pages, num_pages, batch, total_q, h_q, dtype, softmax_scale,
+                         d_cu_seqlens_q, d_cache_seqlens, d_plan, plan_bytes, num_parts, d_workspace, workspace_bytes,
+                         d_out, out_type, d_lse, d_status, true, stream);
+}
+
 int mla_serving_call(int op, const void* args, size_t bytes) {
-  constexpr size_t kWords[] = {22, 11, 12, 10, 12, 10, 23, 21, 22, 25};  // by mla_call_t
-  if (!args || op < 0 || op > MLA_CALL_PROMPT_CHECKED || bytes != 8 * kWords[op]) return MLA_ERR_INVALID_ARG;
+  constexpr size_t kWords[] = {22, 11, 12, 10, 12, 10, 23, 21, 22, 25, 31, 13, 22};  // by mla_call_t
+  if (!args || op < 0 || op > MLA_CALL_CHUNK || bytes != 8 * kWords[op]) return MLA_ERR_INVALID_ARG;
   const char* a = static_cast<const char*>(args);
   auto word = [&](int i) {
     int64_t v;
@@ -551,6 +860,16 @@ int mla_serving_call(int op, const void* args, size_t bytes) {
       return mla_prompt_attention_checked_fwd(P(0), word(1), word(2), P(3), word(4), word(5), P(6), word(7), word(8),
                                               I(9), I(10), I(11), I(12), I(13), I(14), I(15), F(16), N(17), N(18),
                                               P(19), static_cast<size_t>(word(20)), P(21), R(22), N(23), S(24));
+    case MLA_CALL_ROPE_HEADS:
+      return mla_rope_heads(P(0), word(1), word(2), P(3), word(4), word(5), I(6), P(7), P(8), word(9), word(10), P(11),
+                            word(12), word(13), I(14), P(15), I(16), I(17), I(18), I(19), I(20), I(21), F(22), N(23),
+                            N(24), N(25), I(26), R(27), I(28), N(29), S(30));
+    case MLA_CALL_GATHER:
+      return mla_cache_gather(P(0), I(1), I(2), N(3), I(4), N(5), N(6), I(7), I(8), P(9), word(10), N(11), S(12));
+    case MLA_CALL_CHUNK:
+      return mla_chunk_attention_fwd(P(0), P(1), N(2), I(3), I(4), I(5), I(6), I(7), I(8), F(9), N(10), N(11), P(12),
+                                     static_cast<size_t>(word(13)), I(14), P(15), static_cast<size_t>(word(16)), P(17),
+                                     I(18), R(19), N(20), S(21));
     default: return MLA_ERR_INVALID_ARG;
   }
 }

@@ -30,7 +30,7 @@ import torch
 
 from . import (DTYPE_FP8_RECORD, _DTYPE_CODE, _F, _I, _P, _SZ, _check, check_status, load_library, MlaError)
 
-_LL = ctypes.c_longlong
+_LL, _D = ctypes.c_longlong, ctypes.c_double
 _DTYPE_CODE16 = {d: _DTYPE_CODE[d] for d in (torch.bfloat16, torch.float16)}
 
 SERVING_SIGS = {
@@ -56,17 +56,24 @@ SERVING_SIGS = {
                                           _P, _P, _P]),
     "mla_shared_prefix_decode_checked_fwd": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _SZ, _I, _P, _SZ,
                                                   _P, _I, _P, _P, _P]),
+    "mla_rope_frequencies": (_I, [_I, _D, _I, _D, _D, _D, _D, ctypes.POINTER(_D), ctypes.POINTER(_D)]),
+    "mla_rope_table": (_I, [ctypes.POINTER(_D), _I, _D, _LL, _I, _P, _P]),
+    "mla_rope_heads": (_I, [_P, _LL, _LL, _P, _LL, _LL, _I, _P, _P, _LL, _LL, _P, _LL, _LL, _I, _P, _I, _I, _I, _I, _I,
+                            _I, _F, _P, _P, _P, _I, _P, _I, _P, _P]),
+    "mla_cache_gather": (_I, [_P, _I, _I, _P, _I, _P, _P, _I, _I, _P, _LL, _P, _P]),
+    "mla_chunk_num_parts": (_I, []),
+    "mla_chunk_plan_bytes": (_SZ, [_I, _I, _I, _I]),
+    "mla_chunk_workspace_bytes": (_SZ, [_I]),
+    "mla_chunk_get_plan": (_I, [_P, _P, _I, _I, _I, _I, _I, _P, _SZ, _P, _P]),
+    "mla_chunk_attention_fwd": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _SZ, _I, _P, _SZ, _P, _I, _P,
+                                     _P, _P]),
     "mla_serving_call": (_I, [_I, ctypes.c_char_p, _SZ]),
 }
 for _hook, _of in (("mla_test_prompt_timeout", "mla_prompt_attention_fwd"),
-                   ("mla_test_shared_prefix_timeout", "mla_shared_prefix_decode_fwd")):
+                   ("mla_test_shared_prefix_timeout", "mla_shared_prefix_decode_fwd"),
+                   ("mla_test_chunk_timeout", "mla_chunk_attention_fwd")):
     SERVING_SIGS[_hook] = SERVING_SIGS[_of]
 SERVING_SYMBOLS = tuple(SERVING_SIGS)
-
-__all__ = [n for n in SERVING_SYMBOLS] + [
-    "SERVING_SYMBOLS", "cache_append", "cache_grow", "cache_fork", "cache_free", "cache_compact", "cache_copy_pages",
-    "PromptPlan", "plan_prompt", "prompt_attention", "SharedPrefixPlan", "plan_shared_prefix", "shared_prefix_decode",
-]
 
 
 def _refuse(t, dtype, dims, dev, name):
@@ -632,3 +639,10 @@ def shared_prefix_decode(q, kv, block_table, cache_seqlens, causal=False, softma
     if status is None:
         check_status(st, "mla_shared_prefix_decode_fwd")
     return out, lse
+
+
+# (the entry points that chunks.py binds are its own)
+__all__ = [n for n in SERVING_SYMBOLS if n in globals()] + [
+    "SERVING_SYMBOLS", "cache_append", "cache_grow", "cache_fork", "cache_free", "cache_compact", "cache_copy_pages",
+    "PromptPlan", "plan_prompt", "prompt_attention", "SharedPrefixPlan", "plan_shared_prefix", "shared_prefix_decode",
+]

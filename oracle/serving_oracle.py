@@ -193,3 +193,90 @@ def prompt_attention(q, k, v, cu_q, cu_k, causal, scale):
                 lse[rows, h] = top + np.log(z)
             reach[rows, h] = (scale * np.abs(q[rows, h]) @ np.abs(kk).T).max(1, initial=0.0)
     return out, lse, mix, reach
+
+
+# ------------------------------------------------------------------ chunks of new tokens
+
+
+def record_rows(rec):
+    """[n, 576] float64 values of FP8 records uint8 [n, 656]."""
+    rec = np.ascontiguousarray(rec)
+    scale = rec[:, 512:528].copy().view(np.float32).astype(np.float64)
+    rope = (rec[:, 528:].copy().view(np.uint16).astype(np.uint32) << 16).view(np.float32).astype(np.float64)
+    return np.concatenate([e4m3_value(rec[:, :512]) * np.repeat(scale, 128, axis=1), rope], 1)
+
+
+def request_keys(cache, table_row, length):
+    """Rows 0 .. length - 1 of a request in a pool [pages, 64, width], and whether each is on a page of the pool (else
+    page 0 stands in)."""
+    rows, seen = [], []
+    for p in range(length):
+        j = p // PAGE
+        page = int(table_row[j]) if j < len(table_row) else -1
+        good = 0 <= page < cache.shape[0]
+        seen.append(good)
+        rows.append(cache[page if good else 0, p % PAGE])
+    return np.array(rows).reshape(length, cache.shape[2]), np.array(seen, dtype=bool)
+
+
+def chunk_attention(q, keys, seen, cu, lens, causal, scale):
+    """As prompt_attention, for chunks over their requests' keys: keys[b] [len, 576] float64 and seen[b] [len] (a key
+    on a page outside the pool is masked)."""
+    q = np.asarray(q, dtype=np.float64)
+    out = np.full((*q.shape[:2], 512), np.nan)
+    mix, lse, reach = out.copy(), np.full(q.shape[:2], np.nan), np.full(q.shape[:2], np.nan)
+    for b in range(len(lens)):
+        n, total = cu[b + 1] - cu[b], max(lens[b], 0)
+        for i in range(n):
+            see = np.array(seen[b][:total])
+            if causal:
+                see = see & (np.arange(total) <= total - n + i)
+            k = keys[b][:total][see]
+            t = cu[b] + i
+            s = scale * q[t] @ k.T
+            top = s.max(1, initial=-np.inf)
+            e = np.exp(s - np.where(np.isfinite(top), top, 0.0)[:, None])
+            z = e.sum(1)
+            w = e / np.where(z > 0, z, 1.0)[:, None]
+            out[t], mix[t] = w @ k[:, :512], w @ np.abs(k[:, :512])
+            with np.errstate(divide="ignore"):
+                lse[t] = top + np.log(z)
+            reach[t] = (scale * np.abs(q[t]) @ np.abs(k).T).max(1, initial=0.0)
+    return out, lse, mix, reach
+
+
+def rope_frequencies(dim, base, scaling, factor, original, low, high):
+    """(frequencies, magnitude) of rotary positions, from their definitions."""
+    freq, magnitude = [], 1.0
+    for i in range(dim // 2):
+        f = base ** (-2.0 * i / dim)
+        if scaling == "linear":
+            f /= factor
+        elif scaling == "ntk":
+            f = (base * factor ** (dim / (dim - 2.0))) ** (-2.0 * i / dim)
+        elif scaling == "yarn":
+            place = [dim * np.log(original / (2 * np.pi * t)) / (2 * np.log(base)) for t in (high, low)]
+            a, b = max(np.floor(place[0]), 0), min(np.ceil(place[1]), dim - 1)
+            w = min(max((i - a) / max(b - a, 0.001), 0.0), 1.0)
+            f = w * f / factor + (1 - w) * f
+            magnitude = 0.1 * np.log(factor) + 1.0
+        elif scaling == "wavelength":
+            w = min(max((original * f / (2 * np.pi) - low) / (high - low), 0.0), 1.0)
+            f = (1 - w) * f / factor + w * f
+        freq.append(f)
+    return np.array(freq), float(magnitude)
+
+
+def rope_head(x, cos_sin_row, offset, interleaved, weight=None, eps=1e-6):
+    """One head [dim] in float64: norm (with weights), then dims offset .. offset + len(cos_sin_row) turned."""
+    y = np.array(x, dtype=np.float64)
+    if weight is not None:
+        y = y / np.sqrt(np.mean(y * y) + eps) * np.asarray(weight, dtype=np.float64)
+    if cos_sin_row is not None:
+        n = len(cos_sin_row) // 2
+        cos, sin = (np.asarray(v, dtype=np.float64) for v in (cos_sin_row[:n], cos_sin_row[n:]))
+        lo, hi = (slice(offset, offset + 2 * n, 2), slice(offset + 1, offset + 2 * n, 2)) if interleaved else \
+            (slice(offset, offset + n), slice(offset + n, offset + 2 * n))
+        a, b = y[lo].copy(), y[hi].copy()
+        y[lo], y[hi] = a * cos - b * sin, b * cos + a * sin
+    return y

@@ -1,0 +1,233 @@
+"""Attention of ragged chunks over a paged latent cache against 64-bit
+attention, element by element.
+
+Tolerances, from the arithmetic.  Each weight is rounded once to the cache's
+type: half a step, u = 2^-8 (bf16) or 2^-11 (fp16), moves the output by at most
+u * mix with mix = sum_j w_j |v_j|; rounding the output adds u |out| (2^-24 for
+fp32).  A score is a sum of 576 products in fp32: off by at most 576 * 2^-23 *
+reach, reach = max_j scale |q|.|k_j| (each add may lose one last place,
+truncation allowed for), and the exponential, the reference's rounding and the
+merge of pieces add 2^-20; both move weights, hence twice that on the output
+(numerator and sum).  lse moves by the score error plus 2^-19 (sum, log, merge)
+and one last place of its own value.  fp16 values below the smallest normal
+are off by at most 2^-25.
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import mla_paged_kv_gb300 as mla
+from oracle import serving_oracle as so
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP16 = torch.bfloat16, torch.float16
+U = {BF16: 2.0 ** -8, FP16: 2.0 ** -11, torch.float32: 2.0 ** -24}
+BAD_INDEX, STALE_PLAN = 5, 7
+SCALE = 1.0 / 24.0
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+class Case:
+    """Requests with `new` tokens behind `ctx` keys; slots behind their last keys, and pages of nobody, hold `rest`."""
+
+    def __init__(self, new, ctx, heads=2, dtype=BF16, seed=0, before=0, after=0, amp=1.0, rest=float("nan"), spare=3):
+        g = torch.Generator().manual_seed(seed)
+        self.new, self.lens = list(new), [a + b for a, b in zip(new, ctx)]
+        self.cu = [before + int(x) for x in np.concatenate([[0], np.cumsum(new)])]
+        need = [-(-max(n, 0) // 64) for n in self.lens]
+        pages = sum(need) + spare
+        perm = torch.randperm(pages, generator=g).tolist()
+        self.table = np.full((len(new), max(need) + 1), -1, dtype=np.int32)
+        self.cache = torch.full((pages, 64, 576), rest).to(dtype)
+        for b, n in enumerate(self.lens):
+            for j in range(need[b]):
+                page = perm.pop()
+                self.table[b, j] = page
+                k = min(64, n - 64 * j)
+                self.cache[page, :k] = torch.randn(k, 576, generator=g).to(dtype)
+        self.q = (amp * torch.randn(self.cu[-1] + after, heads, 576, generator=g)).to(dtype)
+
+    def keys(self):
+        rows = [so.request_keys(self.cache.double().numpy(), self.table[b], max(n, 0)) for b, n in enumerate(self.lens)]
+        return [r[0] for r in rows], [r[1] for r in rows]
+
+    def device(self):
+        return (self.q.cuda(), self.cache.cuda(), torch.from_numpy(self.table).cuda(), i32(self.lens), i32(self.cu))
+
+    def check(self, out, lse, causal, scale=SCALE, fill=None):
+        u, uo = U[self.q.dtype], U[out.dtype]
+        keys, seen = self.keys()
+        want, wlse, mix, reach = so.chunk_attention(self.q.double().numpy(), keys, seen, self.cu, self.lens, causal,
+                                                    scale)
+        o, l = out.double().cpu().numpy(), lse.double().cpu().numpy()
+        live = np.zeros(o.shape[0], dtype=bool)
+        live[self.cu[0]:self.cu[-1]] = True
+        if fill is not None:
+            assert np.all(o[~live] == fill) and np.all(l[~live] == fill), "rows of no chunk were written"
+        o, l, want, wlse, mix, reach = (x[live] for x in (o, l, want, wlse, mix, reach))
+        none = np.isneginf(wlse)
+        assert np.array_equal(np.isneginf(l), none) and not o[none].any()
+        score = 576 * 2.0 ** -23 * reach
+        half = self.q.dtype == FP16 or out.dtype == FP16
+        tol = (u + 2 * score + 2.0 ** -19)[..., None] * mix + uo * np.abs(want) + (2.0 ** -25 * 8 if half else 0)
+        assert np.isfinite(o).all() and np.all(np.abs(o - want) <= tol), np.max(np.abs(o - want) / tol)
+        l, wlse, score = l[~none], wlse[~none], score[~none]
+        assert np.all(np.abs(l - wlse) <= score + 2.0 ** -19 + 2.0 ** -23 * np.abs(wlse))
+
+    def run(self, causal=True, scale=SCALE, parts=None, out_fp32=False):
+        q, cache, table, lens, cu = self.device()
+        pl = None if parts is None else mla.plan_chunks(cu, lens, q.shape[0], q.shape[1], causal, num_parts=parts)
+        out, lse = mla.chunk_attention(q, cache, table, lens, cu, causal, scale, out_fp32, pl=pl)
+        self.check(out, lse, causal, scale)
+        return out, lse
+
+
+@pytest.mark.parametrize("keys", [1, 2, 31, 32, 33, 63, 64, 65, 96, 127, 128, 129, 191, 192, 193, 256, 257, 700])
+def test_one_token(keys):
+    Case([1], [keys - 1], seed=keys).run()
+
+
+@pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 63, 64, 65, 100])
+def test_one_chunk(n):
+    Case([n], [0], heads=4, seed=n).run()
+    Case([n], [n + 70], heads=3, seed=n + 1).run()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("out_fp32", [True, False])
+def test_types_and_masks(dtype, causal, out_fp32):
+    Case([5, 1, 33], [200, 64, 0], heads=8, dtype=dtype, seed=3).run(causal, out_fp32=out_fp32)
+
+
+@pytest.mark.parametrize("heads", [1, 5, 12, 16, 64, 128])
+def test_heads(heads):
+    """Blocks of 128 rows that begin and end inside a token among them."""
+    Case([7, 1, 4], [130, 5, 250], heads=heads, seed=heads).run()
+
+
+@pytest.mark.parametrize("parts", [1, 2, 3, 7, 76, 200])
+def test_cuts(parts):
+    """Units cut into up to as many pieces as they have tiles, and runs of many units."""
+    Case([3, 20, 1], [1500, 100, 900], heads=16, seed=parts).run(parts=parts)
+    Case([1], [3000], heads=16, seed=parts + 1).run(parts=parts)
+
+
+def test_many_requests():
+    new = [(5 * i) % 7 for i in range(60)]  # empty ones among them
+    Case(new, [(37 * i) % 300 for i in range(60)], heads=16, seed=5).run()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("parts", [None, 1])
+def test_rows_that_see_no_key(causal, parts):
+    """Chunks longer than their keys (the first tokens see none), and requests without keys."""
+    Case([40, 3, 2, 9], [-30, -3, 60, -9], heads=16, seed=7).run(causal, parts=parts)
+    Case([4, 2], [-4, -2], heads=16, seed=8).run(causal, parts=parts)
+
+
+@pytest.mark.parametrize("amp", [4.0, 30.0])
+def test_growing_maxima(amp):
+    """Scores that spread over hundreds of powers of two: the reference is raised again and again."""
+    for parts in (1, None):
+        Case([6, 40], [900, 500], heads=16, seed=11, amp=amp).run(parts=parts)
+
+
+def test_rows_of_no_chunk_are_left():
+    c = Case([3, 5], [100, 40], heads=16, seed=13, before=4, after=6)
+    q, cache, table, lens, cu = c.device()
+    for parts in (1, 76):
+        pl = mla.plan_chunks(cu, lens, q.shape[0], 16, num_parts=parts)
+        out = torch.full((q.shape[0], 16, 512), 7.0, dtype=BF16, device="cuda")
+        lse = torch.full((q.shape[0], 16), 7.0, device="cuda")
+        status = i32([0])
+        mla.mla_chunk_attention_fwd(q, cache, table, pl, out, lse, status)
+        assert int(status) == 0
+        c.check(out, lse, True, fill=7.0)
+
+
+@pytest.mark.parametrize("rest", [float("nan"), float("inf")])
+def test_what_lies_behind_the_last_key(rest):
+    """Slots behind a request's last key, and pages of nobody, hold no numbers; chunks end at every place of a tile."""
+    for n in (1, 60, 64, 70, 127, 190):
+        Case([2], [n], heads=64, seed=n, rest=rest).run()
+
+
+def test_bad_pages_are_masked_and_reported():
+    for heads, parts in ((16, None), (16, 1), (128, 2)):
+        c = Case([4, 3, 2], [300, 500, 100], heads=heads, seed=17)
+        c.table[0, 1], c.table[1, 0], c.table[1, 7] = -1, c.cache.shape[0], -5
+        c.table[2, :2] = 99999  # all keys of a request
+        q, cache, table, lens, cu = c.device()
+        status = i32([0])
+        pl = mla.plan_chunks(cu, lens, q.shape[0], heads, num_parts=parts)
+        out, lse = mla.chunk_attention(q, cache, table, lens, cu, pl=pl, status=status)
+        assert int(status) == BAD_INDEX
+        c.check(out, lse, True)
+
+
+def test_a_table_too_short_for_its_lengths():
+    c = Case([2, 2], [200, 30], heads=16, seed=19)
+    c.table = np.ascontiguousarray(c.table[:, :2])
+    q, cache, table, lens, cu = c.device()
+    status = i32([0])
+    out, lse = mla.chunk_attention(q, cache, table, lens, cu, status=status)
+    assert int(status) == BAD_INDEX
+    c.check(out, lse, True)
+
+
+def test_offsets_out_of_range():
+    c = Case([3, 3], [40, 50], heads=16, seed=23)
+    q, cache, table, lens, cu = c.device()
+    for bad, ln in (([0, 4, 3], c.lens), ([-1, 3, 6], c.lens), ([0, 3, 7], c.lens), (c.cu, [43, (1 << 24) + 1])):
+        status = i32([0])
+        pl = mla.plan_chunks(i32(bad), i32(ln), 6, 16, status=status)
+        assert int(status) == BAD_INDEX
+        out, lse = torch.full((6, 16, 512), 7.0, dtype=BF16, device="cuda"), torch.full((6, 16), 7.0, device="cuda")
+        status.zero_()
+        mla.mla_chunk_attention_fwd(q, cache, table, pl, out, lse, status)
+        assert int(status) == 0 and bool((out == 7.0).all()) and bool((lse == 7.0).all())
+        with pytest.raises(mla.MlaError):
+            mla.plan_chunks(i32(bad), i32(ln), 6, 16)
+
+
+def test_a_plan_of_others_is_reported():
+    c = Case([3, 5], [100, 40], heads=16, seed=29)
+    q, cache, table, lens, cu = c.device()
+    pl = mla.plan_chunks(cu, lens, 8, 16)
+    want = mla.chunk_attention(q, cache, table, lens, cu, pl=pl)
+    for cu2, lens2 in ((i32([0, 4, 8]), lens), (cu, lens + 1), (cu + 0, lens - i32([0, 1]))):
+        status = i32([0])
+        got = mla.chunk_attention(q, cache, table, lens2, cu2, pl=pl, status=status)
+        assert int(status) == STALE_PLAN
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])  # the plan's results
+        with pytest.raises(mla.MlaError):
+            mla.chunk_attention(q, cache, table, lens2, cu2, pl=pl)
+
+
+def test_calls_repeat_to_the_bit():
+    c = Case([30, 2, 1], [700, 1500, 90], heads=16, seed=31)
+    q, cache, table, lens, cu = c.device()
+    first = mla.chunk_attention(q, cache, table, lens, cu)
+    for _ in range(3):
+        again = mla.chunk_attention(q, cache, table, lens, cu)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def test_agrees_with_decode():
+    """One token each: the plain decode of the same batch, within both calls' roundings."""
+    c = Case([1] * 9, [70 * i for i in range(9)], heads=128, seed=37)
+    q, cache, table, lens, cu = c.device()
+    out, lse = mla.chunk_attention(q, cache, table, lens, cu, out_fp32=True)
+    c.check(out, lse, True)
+    # (the decode wants numbers behind the last key too)
+    ref, rlse = mla.decode(q[:, None], torch.nan_to_num(cache), table, lens, softmax_scale=SCALE)
+    assert float((out - ref[:, 0].float()).abs().max()) < 2.0 ** -6 * float(ref.abs().max())
+    assert float((lse - rlse[:, 0]).abs().max()) < 1e-3
