@@ -351,8 +351,9 @@ int mla_cache_gather(const void* d_cache, int cache_dtype, int num_pages, const 
  *   out = sum_j softmax_j(scale q . k_j) k_j[:512],  lse = ln sum_j exp(scale q . k_j)
  * A query that sees no key gets out = 0, lse = -inf.  Rows of the outputs outside
  * every chunk are left as they were.  Softmax weights are rounded to the cache's
- * type for the product with the values and divided by the sum of the unrounded
- * ones; statistics and sums are fp32.
+ * type (bf16 over FP8 records) for the product with the values and divided by the
+ * sum of the unrounded ones; statistics and sums are fp32.  Over FP8 records keys
+ * and values are code x scale rounded to bf16, what mla_cache_gather gives.
  *
  * num_parts: pairs of CTAs that share the work; mla_chunk_num_parts gives as many
  * as the device runs at once (>= 1, or a negative mla_status_t).  At most 1024. */
@@ -371,8 +372,9 @@ int mla_chunk_get_plan(const int32_t* d_cu_seqlens_q, const int32_t* d_cache_seq
                        int causal, int num_parts, void* d_plan, size_t plan_bytes, int32_t* d_status,
                        mla_stream_t stream);
 
-/*   d_q           [total_q, h_q, 576] of `dtype` (MLA_DTYPE_BF16 or _FP16)
- *   d_kv          [num_pages, 64, 576] of `dtype`
+/*   d_q           [total_q, h_q, 576] bf16 or fp16 (FP8 records: bf16)
+ *   d_kv          [num_pages, 64, 576] of q's type (`dtype`), or FP8 records
+ *                 [num_pages, 64, 656] (MLA_DTYPE_FP8_RECORD)
  *   d_block_table int32 [batch, max_pages]
  *   d_plan        from mla_chunk_get_plan with the same batch, total_q, h_q and
  *                 num_parts
@@ -412,7 +414,8 @@ int mla_test_shared_prefix_timeout(const void* d_q, const void* d_kv, const int3
                                    float softmax_scale, const void* d_plan, size_t plan_bytes, int num_parts,
                                    void* d_workspace, size_t workspace_bytes, void* d_out, int out_type, float* d_lse,
                                    int32_t* d_status, mla_stream_t stream);
-/* The same of mla_chunk_attention_fwd (bf16): its first K stage is never loaded. */
+/* The same of mla_chunk_attention_fwd (bf16, or FP8 records): its first K stage is
+ * never loaded. */
 int mla_test_chunk_timeout(const void* d_q, const void* d_kv, const int32_t* d_block_table, int max_pages,
                            int num_pages, int batch, int total_q, int h_q, int dtype, float softmax_scale,
                            const int32_t* d_cu_seqlens_q, const int32_t* d_cache_seqlens, const void* d_plan,

@@ -34,6 +34,7 @@
 //     are masked, and their values zeroed in shared memory (0 x NaN is not 0).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cuda_fp8.h>
 
 #include <algorithm>
 
@@ -79,8 +80,11 @@ constexpr int kSmemBytes = kOffRow + 2 * 4 * kCtaRows * 4;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 static_assert(kKSlices * 3 == kSlices, "three K stages a tile");
 
-constexpr int kThreads = 384;
-constexpr int kWarpMma = 8, kWarpK = 9, kWarpQ = 11;  // 10: V
+// Warps: 0 .. 7 softmax, then these.  16-bit caches: one warp each loads K and V
+// by TMA; FP8 records: four each convert them.
+constexpr int kWarpMma = 8, kWarpQ = 9, kWarpK = 10;
+constexpr int kConverters = 4;
+constexpr int threads_of(bool fp8) { return 32 * (kWarpK + (fp8 ? 2 * kConverters : 2)); }
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 256;  // two buffers of 64 columns
 constexpr float kTau = 8.0f;
@@ -203,10 +207,168 @@ __device__ __forceinline__ void fail(volatile int* abort_flag, int32_t* status) 
   report(status, MLA_ERR_TIMEOUT);
 }
 
+// ------------------------------------------------------------------ FP8 records
+
+// 16 codes times their scale as bf16, rounded once, into the two 16-byte chunks
+// from `chunk` on of a swizzled 128-byte row.
+__device__ __forceinline__ void store_codes(uint8_t* row, uint32_t chunk, uint32_t swz, const uint4& codes,
+                                            float scale) {
+  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+  uint32_t o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const __half2_raw h =
+        __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));  // (every E4M3 value is an fp16 value)
+    o[i] = pack2<false>(f.x * scale, f.y * scale);
+  }
+  *reinterpret_cast<uint4*>(row + ((chunk ^ swz) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+  *reinterpret_cast<uint4*>(row + (((chunk + 1) ^ swz) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+// What a converting lane has of a page: one key (16 a warp) and every other
+// 16-byte piece of its record, odd or even.  The two lanes of a key make whole
+// 32-byte sectors; the order of the keys over the lanes keeps the stores of eight
+// lanes in eight different bank groups (keys k, k+1, k+4, k+5 and two chunks).
+struct RecordLane {
+  int key;    // of the page
+  int piece;  // 0 or 1
+  uint32_t swz;
+};
+__device__ __forceinline__ RecordLane record_lane(int warp, int lane) {
+  const int k = (lane >> 1 & 1) | (lane >> 2 & 1) << 2 | (lane >> 3 & 1) << 1 | (lane >> 4 & 1) << 3;
+  return RecordLane{16 * warp + k, lane & 1, static_cast<uint32_t>(k & 7)};
+}
+
+__device__ __forceinline__ const uint8_t* record_at(const ChunkParams& p, int page, int key) {
+  return p.records + (static_cast<long long>(max(page, 0)) * kTile + key) * MLA_RECORD_BYTES;
+}
+
+// Converts K pages: three stages of 192 dims a tile, the third with the RoPE part.
+// A stage's pieces are in flight while the one before is converted.
+template <bool kStall>
+__device__ __forceinline__ bool convert_k(const ChunkParams& p, const Run& run, uint32_t rank, int warp, int lane,
+                                          uint8_t* sK, uint64_t* bars, uint32_t bar0, volatile int* abort_flag,
+                                          uint64_t wait_ns) {
+  const RecordLane me = record_lane(warp, lane);
+  Walk w;
+  uint32_t n = 0;  // stages so far
+  bool ok = true;
+  uint4 raw[8];
+  for (int u = run.u0; ok && walk_to(p.units, run, u, w); u = w.u + 1) {
+    const int pages = pages_of(w.unit.len);
+    int ids = 0, base = -32;
+    auto page_at = [&](int j) {  // this CTA's page of tile j
+      if (2 * j - base >= 32) {
+        base = 2 * j;
+        ids = page_window(p, w.unit, base, lane);
+      }
+      return __shfl_sync(0xffffffffu, ids, 2 * j + static_cast<int>(rank) - base);
+    };
+    auto load = [&](const uint8_t* rec, int c, int i) {  // piece i of stage c
+      if (c < 2) return i < 6 ? __ldcg(reinterpret_cast<const uint4*>(rec + 192 * c + 32 * i + 16 * me.piece)) : raw[i];
+      return i < 4 ? __ldcg(reinterpret_cast<const uint4*>(rec + 384 + 32 * i + 16 * me.piece))
+                   : __ldcg(reinterpret_cast<const uint4*>(rec + 528 + 32 * (i - 4) + 16 * me.piece));
+    };
+    const uint8_t* rec = record_at(p, page_at(w.lo), me.key);
+    float4 scale = __ldcg(reinterpret_cast<const float4*>(rec + 512));
+#pragma unroll
+    for (int i = 0; i < 6; ++i) raw[i] = load(rec, 0, i);
+    for (int j = w.lo; j < w.hi && ok; ++j) {
+      const bool have = 2 * j + static_cast<int>(rank) < pages;
+      const uint8_t* next = j + 1 < w.hi ? record_at(p, page_at(j + 1), me.key) : rec;
+      float4 next_scale = scale;
+#pragma unroll
+      for (int c = 0; c < 3; ++c, ++n) {
+        const int s = static_cast<int>(n % kKStages), r = static_cast<int>(n / kKStages);
+        if (ok && r >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&bars[K_EMPTY + s], (r - 1) & 1, abort_flag, wait_ns));
+        uint8_t* stage = sK + s * kKBytes + me.key * 128;
+        const uint8_t* from = c < 2 ? rec : next;
+        if (c == 2) next_scale = __ldcg(reinterpret_cast<const float4*>(next + 512));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (c == 2 || i < 6) {
+            const int dim = 192 * c + 32 * i + 16 * me.piece;  // of codes
+            if (have && c == 2 && i >= 4) {
+              const uint32_t chunk = static_cast<uint32_t>(2 * (i - 4) + me.piece);
+              *reinterpret_cast<uint4*>(stage + 2 * kSliceBytes + ((chunk ^ me.swz) << 4)) = raw[i];
+            } else if (have) {
+              const int g = (192 * c + 32 * i) / 128;
+              store_codes(stage + (dim / 64 - 3 * c) * kSliceBytes, static_cast<uint32_t>(dim % 64 / 8), me.swz, raw[i],
+                          g == 0 ? scale.x : g == 1 ? scale.y : g == 2 ? scale.z : scale.w);
+            }
+          }
+          raw[i] = load(from, (c + 1) % 3, i);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && ok && !(kStall && rank == 0 && n == 0)) arrive_pair(bar0 + 8 * (K_FULL + s));
+      }
+      rec = next;
+      scale = next_scale;
+    }
+  }
+  return ok;
+}
+
+// Converts V pages: this CTA's 256 dims of both pages of a tile; keys behind the
+// unit's last one (and pages outside the pool) as zeros.
+__device__ __forceinline__ bool convert_v(const ChunkParams& p, const Run& run, uint32_t rank, int warp, int lane,
+                                          uint8_t* sV, uint64_t* bars, uint32_t bar0, volatile int* abort_flag,
+                                          uint64_t wait_ns) {
+  const RecordLane me = record_lane(warp, lane);
+  Walk w;
+  uint32_t n = 0;
+  bool ok = true;
+  uint4 raw[8];
+  for (int u = run.u0; ok && walk_to(p.units, run, u, w); u = w.u + 1) {
+    const int pages = min(pages_of(w.unit.len), 2 * w.hi);
+    int ids = 0, base = -32;
+    auto page_at = [&](int k) {
+      if (k - base >= 32) {
+        base = k;
+        ids = page_window(p, w.unit, base, lane);
+      }
+      return __shfl_sync(0xffffffffu, ids, k - base);
+    };
+    int id = page_at(2 * w.lo);
+    const uint8_t* rec = record_at(p, id, me.key);
+    float2 scale = __ldcg(reinterpret_cast<const float2*>(rec + 512 + 8 * rank));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) raw[i] = __ldcg(reinterpret_cast<const uint4*>(rec + 256 * rank + 32 * i + 16 * me.piece));
+    for (int k = 2 * w.lo; k < pages && ok; ++k, ++n) {
+      const int s = static_cast<int>(n % kVStages), r = static_cast<int>(n / kVStages);
+      const bool live = id >= 0 && k * kTile + me.key < w.unit.len;
+      if (k + 1 < pages) id = page_at(k + 1);
+      const uint8_t* next = record_at(p, id, me.key);
+      const float2 next_scale = __ldcg(reinterpret_cast<const float2*>(next + 512 + 8 * rank));
+      if (r >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&bars[V_EMPTY + s], (r - 1) & 1, abort_flag, wait_ns));
+      uint8_t* stage = sV + s * kVBytes + me.key * 128;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        uint8_t* row = stage + i / 2 * kSliceBytes;
+        const uint32_t chunk = static_cast<uint32_t>(4 * (i & 1) + 2 * me.piece);
+        if (live) {
+          store_codes(row, chunk, me.swz, raw[i], i < 4 ? scale.x : scale.y);
+        } else {
+          *reinterpret_cast<uint4*>(row + ((chunk ^ me.swz) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(row + (((chunk + 1) ^ me.swz) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        raw[i] = __ldcg(reinterpret_cast<const uint4*>(next + 256 * rank + 32 * i + 16 * me.piece));
+      }
+      scale = next_scale;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && ok) arrive_pair(bar0 + 8 * (V_FULL + s));
+    }
+  }
+  return ok;
+}
+
 constexpr uint64_t kStallWaitNs = 200000;  // wait budget of the stall-test instance, whose first K stage is never loaded
 
-template <bool kHalf, bool kStall = false>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+template <bool kHalf, bool kFp8, bool kStall = false>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
     chunk_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                  const __grid_constant__ CUtensorMap v_map, const ChunkParams p) {
   constexpr uint64_t kWaitNs = kStall ? kStallWaitNs : MLA_WAIT_LIMIT_NS;
@@ -233,14 +395,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     *abort_flag = 0;
     // the barriers that MMAs wait for are the even CTA's and count both CTAs' parts
+    constexpr uint32_t kLoaders = 2 * (kFp8 ? kConverters : 1);
     mbar_init(&bars[Q_FULL], 2);
     mbar_init(&bars[Q_EMPTY], 1);
     for (int i = 0; i < kKStages; ++i) {
-      mbar_init(&bars[K_FULL + i], 2);
+      mbar_init(&bars[K_FULL + i], kLoaders);
       mbar_init(&bars[K_EMPTY + i], 1);
     }
     for (int i = 0; i < kVStages; ++i) {
-      mbar_init(&bars[V_FULL + i], 2);
+      mbar_init(&bars[V_FULL + i], kLoaders);
       mbar_init(&bars[V_EMPTY + i], 1);
     }
     mbar_init(&bars[S_FULL], 1);
@@ -255,10 +418,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tmem2_alloc(tmem_slot, kTmemCols);
     tmem2_relinquish();
   }
-  if (warp == kWarpK && lane == 0) {
+  if (warp == kWarpQ && lane == 0) {
     prefetch_tmap(&q_map);
-    prefetch_tmap(&k_map);
-    prefetch_tmap(&v_map);
+    if (!kFp8) {
+      prefetch_tmap(&k_map);
+      prefetch_tmap(&v_map);
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -271,8 +436,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int causal = p.head[kHeadCausal];
   Walk w;
 
-  if (warp > kWarpMma) {
-    // ------------------------------------------------------------ loads: K, V or Q
+  if (kFp8 && warp >= kWarpK) {
+    // ------------------------------------------------------------ FP8 records: K or V converted
+    const uint32_t bar0 = mapa_shared(smem_u32(bars), 0);
+    const bool ok = warp < kWarpK + kConverters ? convert_k<kStall>(p, run, rank, warp - kWarpK, lane, sK, bars, bar0,
+                                                                    abort_flag, kWaitNs)
+                                                : convert_v(p, run, rank, warp - kWarpK - kConverters, lane, sV, bars,
+                                                            bar0, abort_flag, kWaitNs);
+    if (!ok && lane == 0) fail(abort_flag, p.status);
+    __syncwarp();
+  } else if (warp > kWarpMma) {
+    // ------------------------------------------------------------ loads: Q, K or V
     bool ok = true;
     const uint64_t pol_q = policy_evict_first(), pol_kv = policy_evict_last();
     const uint32_t bar0 = mapa_shared(smem_u32(bars), 0);
@@ -906,15 +1080,16 @@ cudaError_t launch_chunk_plan(const ChunkPlanParams& p, cudaStream_t st) {
 namespace {
 
 using ChunkKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, ChunkParams);
-ChunkKernel chunk_kernel_of(bool half, bool stall) {
-  return stall ? ck::chunk_kernel<false, true> : half ? ck::chunk_kernel<true> : ck::chunk_kernel<false>;
+ChunkKernel chunk_kernel_of(bool half, bool fp8, bool stall) {
+  if (fp8) return stall ? ck::chunk_kernel<false, true, true> : ck::chunk_kernel<false, true>;
+  return stall ? ck::chunk_kernel<false, false, true> : half ? ck::chunk_kernel<true, false> : ck::chunk_kernel<false, false>;
 }
 
 }  // namespace
 
 cudaError_t chunk_setup() {
-  for (int v = 0; v < 3; ++v) {
-    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(chunk_kernel_of(v == 1, v == 2)),
+  for (int v = 0; v < 5; ++v) {
+    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(chunk_kernel_of(v == 4, v & 1, v == 2 || v == 3)),
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, ck::kSmemBytes);
     if (e != cudaSuccess) return e;
   }
@@ -923,7 +1098,8 @@ cudaError_t chunk_setup() {
 
 cudaError_t launch_chunk(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const ChunkParams& p,
                          bool half, bool stall, int parts, cudaStream_t st) {
-  chunk_kernel_of(half, stall)<<<2 * parts, ck::kThreads, ck::kSmemBytes, st>>>(q, k, v, p);
+  const bool fp8 = p.records != nullptr;
+  chunk_kernel_of(half, fp8, stall)<<<2 * parts, ck::threads_of(fp8), ck::kSmemBytes, st>>>(q, k, v, p);
   return cudaGetLastError();
 }
 

@@ -175,6 +175,7 @@ struct ChunkPlanParams {
 struct ChunkParams {
   const int32_t *head, *units, *sched, *fix, *made;  // of the plan
   const int32_t *cu, *lens;                          // the caller's, to be compared with the plan's, or NULL
+  const uint8_t* records;  // a cache of FP8 records, or NULL
   const int32_t* block_table;
   int max_pages, num_pages, batch, h_q;
   float scale_log2;

@@ -271,7 +271,8 @@ int chunk_attention(const void* d_q, const void* d_kv, const int32_t* d_block_ta
   if (!d_kv || !d_block_table || !d_plan || !d_workspace || !d_status) return MLA_ERR_INVALID_ARG;
   if (total_q > 0 && (!d_q || !d_out || !d_lse)) return MLA_ERR_INVALID_ARG;
   if (max_pages < 1 || num_pages < 1) return MLA_ERR_INVALID_ARG;
-  if (dtype != MLA_DTYPE_BF16 && dtype != MLA_DTYPE_FP16) return MLA_ERR_INVALID_ARG;
+  if (dtype != MLA_DTYPE_BF16 && dtype != MLA_DTYPE_FP16 && dtype != MLA_DTYPE_FP8_RECORD)
+    return MLA_ERR_INVALID_ARG;
   if (out_type != MLA_DTYPE_BF16 && out_type != MLA_DTYPE_FP32 && out_type != MLA_DTYPE_FP16)
     return MLA_ERR_INVALID_ARG;
   if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.f)) return MLA_ERR_INVALID_ARG;
@@ -297,6 +298,7 @@ int chunk_attention(const void* d_q, const void* d_kv, const int32_t* d_block_ta
   p.made = ints(z.made);
   p.cu = cu;
   p.lens = lens;
+  p.records = dtype == MLA_DTYPE_FP8_RECORD ? static_cast<const uint8_t*>(d_kv) : nullptr;
   p.block_table = d_block_table;
   p.max_pages = max_pages;
   p.num_pages = num_pages;
@@ -319,8 +321,12 @@ int chunk_attention(const void* d_q, const void* d_kv, const int32_t* d_block_ta
   const cuuint64_t strides[3] = {2 * MLA_D_QK, 128, 2 * MLA_D_QK * MLA_PAGE_SIZE};
   const cuuint32_t k_box[4] = {64, 64, 3, 1}, v_box[4] = {64, 64, 4, 1};
   rc = encode_map16(&qm, d_q, 4, q_dims, q_strides, q_box);
-  if (rc == MLA_OK) rc = encode_map16(&km, d_kv, 4, dims, strides, k_box);
-  if (rc == MLA_OK) rc = encode_map16(&vm, d_kv, 4, dims, strides, v_box);
+  if (p.records) {
+    km = vm = qm;  // not used
+  } else {
+    if (rc == MLA_OK) rc = encode_map16(&km, d_kv, 4, dims, strides, k_box);
+    if (rc == MLA_OK) rc = encode_map16(&vm, d_kv, 4, dims, strides, v_box);
+  }
   if (rc != MLA_OK) return rc;
   rc = launched(launch_chunk(qm, km, vm, p, dtype == MLA_DTYPE_FP16, stall, num_parts, to_stream(stream)));
   return rc != MLA_OK || stall ? rc : launched(launch_chunk_combine(p, num_parts, sms, to_stream(stream)));

@@ -10,7 +10,9 @@ truncation allowed for), and the exponential, the reference's rounding and the
 merge of pieces add 2^-20; both move weights, hence twice that on the output
 (numerator and sum).  lse moves by the score error plus 2^-19 (sum, log, merge)
 and one last place of its own value.  fp16 values below the smallest normal
-are off by at most 2^-25.
+are off by at most 2^-25.  Over FP8 records the keys and values are, by the
+call's definition, the fp32 products of codes and scales rounded to bf16: the
+restatement takes those, and the bounds are bf16's.
 """
 
 import math
@@ -37,7 +39,8 @@ def i32(v):
 class Case:
     """Requests with `new` tokens behind `ctx` keys; slots behind their last keys, and pages of nobody, hold `rest`."""
 
-    def __init__(self, new, ctx, heads=2, dtype=BF16, seed=0, before=0, after=0, amp=1.0, rest=float("nan"), spare=3):
+    def __init__(self, new, ctx, heads=2, dtype=BF16, seed=0, before=0, after=0, amp=1.0, rest=float("nan"), spare=3,
+                 fp8=False):
         g = torch.Generator().manual_seed(seed)
         self.new, self.lens = list(new), [a + b for a, b in zip(new, ctx)]
         self.cu = [before + int(x) for x in np.concatenate([[0], np.cumsum(new)])]
@@ -53,9 +56,19 @@ class Case:
                 k = min(64, n - 64 * j)
                 self.cache[page, :k] = torch.randn(k, 576, generator=g).to(dtype)
         self.q = (amp * torch.randn(self.cu[-1] + after, heads, 576, generator=g)).to(dtype)
+        self.values = self.cache.double().numpy()
+        if fp8:  # records of those rows; what is no number in a row becomes codes and scales that are none
+            c, r = self.cache[..., :512].float().reshape(pages, 64, 4, 128), self.cache[..., 512:]
+            scale = torch.nan_to_num(c).abs().amax(3).clamp(min=1e-3) / 448.0
+            scale = torch.where(torch.isfinite(c).all(3), scale, c[..., 0])
+            codes = torch.where(torch.isfinite(c), (c / scale[..., None]).clamp(-448, 448), c).to(torch.float8_e4m3fn)
+            self.cache = torch.cat([codes.view(torch.uint8).reshape(pages, 64, 512), scale.view(torch.uint8),
+                                    r.contiguous().view(torch.uint8)], 2).contiguous()
+            value = (codes.float() * scale[..., None]).to(BF16).reshape(pages, 64, 512)
+            self.values = torch.cat([value, r], 2).double().numpy()
 
     def keys(self):
-        rows = [so.request_keys(self.cache.double().numpy(), self.table[b], max(n, 0)) for b, n in enumerate(self.lens)]
+        rows = [so.request_keys(self.values, self.table[b], max(n, 0)) for b, n in enumerate(self.lens)]
         return [r[0] for r in rows], [r[1] for r in rows]
 
     def device(self):
@@ -89,15 +102,20 @@ class Case:
         return out, lse
 
 
+caches = pytest.mark.parametrize("fp8", [False, True])
+
+
+@caches
 @pytest.mark.parametrize("keys", [1, 2, 31, 32, 33, 63, 64, 65, 96, 127, 128, 129, 191, 192, 193, 256, 257, 700])
-def test_one_token(keys):
-    Case([1], [keys - 1], seed=keys).run()
+def test_one_token(keys, fp8):
+    Case([1], [keys - 1], seed=keys, fp8=fp8).run()
 
 
+@caches
 @pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 63, 64, 65, 100])
-def test_one_chunk(n):
-    Case([n], [0], heads=4, seed=n).run()
-    Case([n], [n + 70], heads=3, seed=n + 1).run()
+def test_one_chunk(n, fp8):
+    Case([n], [0], heads=4, seed=n, fp8=fp8).run()
+    Case([n], [n + 70], heads=3, seed=n + 1, fp8=fp8).run()
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP16])
@@ -105,39 +123,46 @@ def test_one_chunk(n):
 @pytest.mark.parametrize("out_fp32", [True, False])
 def test_types_and_masks(dtype, causal, out_fp32):
     Case([5, 1, 33], [200, 64, 0], heads=8, dtype=dtype, seed=3).run(causal, out_fp32=out_fp32)
+    if dtype == BF16:
+        Case([5, 1, 33], [200, 64, 0], heads=8, seed=4, fp8=True).run(causal, out_fp32=out_fp32)
 
 
+@caches
 @pytest.mark.parametrize("heads", [1, 5, 12, 16, 64, 128])
-def test_heads(heads):
+def test_heads(heads, fp8):
     """Blocks of 128 rows that begin and end inside a token among them."""
-    Case([7, 1, 4], [130, 5, 250], heads=heads, seed=heads).run()
+    Case([7, 1, 4], [130, 5, 250], heads=heads, seed=heads, fp8=fp8).run()
 
 
+@caches
 @pytest.mark.parametrize("parts", [1, 2, 3, 7, 76, 200])
-def test_cuts(parts):
+def test_cuts(parts, fp8):
     """Units cut into up to as many pieces as they have tiles, and runs of many units."""
-    Case([3, 20, 1], [1500, 100, 900], heads=16, seed=parts).run(parts=parts)
-    Case([1], [3000], heads=16, seed=parts + 1).run(parts=parts)
+    Case([3, 20, 1], [1500, 100, 900], heads=16, seed=parts, fp8=fp8).run(parts=parts)
+    Case([1], [3000], heads=16, seed=parts + 1, fp8=fp8).run(parts=parts)
 
 
-def test_many_requests():
+@caches
+def test_many_requests(fp8):
     new = [(5 * i) % 7 for i in range(60)]  # empty ones among them
-    Case(new, [(37 * i) % 300 for i in range(60)], heads=16, seed=5).run()
+    Case(new, [(37 * i) % 300 for i in range(60)], heads=16, seed=5, fp8=fp8).run()
 
 
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("parts", [None, 1])
-def test_rows_that_see_no_key(causal, parts):
+@caches
+def test_rows_that_see_no_key(causal, parts, fp8):
     """Chunks longer than their keys (the first tokens see none), and requests without keys."""
-    Case([40, 3, 2, 9], [-30, -3, 60, -9], heads=16, seed=7).run(causal, parts=parts)
-    Case([4, 2], [-4, -2], heads=16, seed=8).run(causal, parts=parts)
+    Case([40, 3, 2, 9], [-30, -3, 60, -9], heads=16, seed=7, fp8=fp8).run(causal, parts=parts)
+    Case([4, 2], [-4, -2], heads=16, seed=8, fp8=fp8).run(causal, parts=parts)
 
 
+@caches
 @pytest.mark.parametrize("amp", [4.0, 30.0])
-def test_growing_maxima(amp):
+def test_growing_maxima(amp, fp8):
     """Scores that spread over hundreds of powers of two: the reference is raised again and again."""
     for parts in (1, None):
-        Case([6, 40], [900, 500], heads=16, seed=11, amp=amp).run(parts=parts)
+        Case([6, 40], [900, 500], heads=16, seed=11, amp=amp, fp8=fp8).run(parts=parts)
 
 
 def test_rows_of_no_chunk_are_left():
@@ -153,16 +178,18 @@ def test_rows_of_no_chunk_are_left():
         c.check(out, lse, True, fill=7.0)
 
 
+@caches
 @pytest.mark.parametrize("rest", [float("nan"), float("inf")])
-def test_what_lies_behind_the_last_key(rest):
+def test_what_lies_behind_the_last_key(rest, fp8):
     """Slots behind a request's last key, and pages of nobody, hold no numbers; chunks end at every place of a tile."""
     for n in (1, 60, 64, 70, 127, 190):
-        Case([2], [n], heads=64, seed=n, rest=rest).run()
+        Case([2], [n], heads=64, seed=n, rest=rest, fp8=fp8).run()
 
 
-def test_bad_pages_are_masked_and_reported():
+@caches
+def test_bad_pages_are_masked_and_reported(fp8):
     for heads, parts in ((16, None), (16, 1), (128, 2)):
-        c = Case([4, 3, 2], [300, 500, 100], heads=heads, seed=17)
+        c = Case([4, 3, 2], [300, 500, 100], heads=heads, seed=17, fp8=fp8)
         c.table[0, 1], c.table[1, 0], c.table[1, 7] = -1, c.cache.shape[0], -5
         c.table[2, :2] = 99999  # all keys of a request
         q, cache, table, lens, cu = c.device()
@@ -173,8 +200,9 @@ def test_bad_pages_are_masked_and_reported():
         c.check(out, lse, True)
 
 
-def test_a_table_too_short_for_its_lengths():
-    c = Case([2, 2], [200, 30], heads=16, seed=19)
+@caches
+def test_a_table_too_short_for_its_lengths(fp8):
+    c = Case([2, 2], [200, 30], heads=16, seed=19, fp8=fp8)
     c.table = np.ascontiguousarray(c.table[:, :2])
     q, cache, table, lens, cu = c.device()
     status = i32([0])
@@ -212,8 +240,9 @@ def test_a_plan_of_others_is_reported():
             mla.chunk_attention(q, cache, table, lens2, cu2, pl=pl)
 
 
-def test_calls_repeat_to_the_bit():
-    c = Case([30, 2, 1], [700, 1500, 90], heads=16, seed=31)
+@caches
+def test_calls_repeat_to_the_bit(fp8):
+    c = Case([30, 2, 1], [700, 1500, 90], heads=16, seed=31, fp8=fp8)
     q, cache, table, lens, cu = c.device()
     first = mla.chunk_attention(q, cache, table, lens, cu)
     for _ in range(3):
@@ -231,3 +260,14 @@ def test_agrees_with_decode():
     ref, rlse = mla.decode(q[:, None], torch.nan_to_num(cache), table, lens, softmax_scale=SCALE)
     assert float((out - ref[:, 0].float()).abs().max()) < 2.0 ** -6 * float(ref.abs().max())
     assert float((lse - rlse[:, 0]).abs().max()) < 1e-3
+
+
+def test_records_are_the_rows_that_the_gather_gives():
+    """Over FP8 records the call is, to the bit, the one over a 16-bit cache of the gathered rows."""
+    c = Case([5, 2, 30], [130, 600, 64], heads=16, seed=41, fp8=True)
+    q, cache, table, lens, cu = c.device()
+    pages = torch.arange(cache.shape[0], dtype=torch.int32, device="cuda")
+    rows = mla.cache_gather(cache, pages[None], i32([0, 64 * cache.shape[0]]), 64 * cache.shape[0])
+    out, lse = mla.chunk_attention(q, cache, table, lens, cu)
+    want = mla.chunk_attention(q, rows.view(-1, 64, 576), table, lens, cu)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])

@@ -22,7 +22,7 @@ def i32(v):
 
 
 @pytest.mark.parametrize("new,ctx", [([3, 1, 5], [100, 40, 700]), ([40], [900])])
-@pytest.mark.parametrize("fp8", [False])
+@pytest.mark.parametrize("fp8", [False, True])
 def test_chunk_wait_runs_out_and_the_next_call_is_as_ever(new, ctx, fp8):
     g = torch.Generator().manual_seed(len(new))
     lens = [a + b for a, b in zip(new, ctx)]
