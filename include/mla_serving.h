@@ -357,6 +357,7 @@ int mla_cache_gather(const void* d_cache, int cache_dtype, int num_pages, const 
  *
  * num_parts: pairs of CTAs that share the work; mla_chunk_num_parts gives as many
  * as the device runs at once (>= 1, or a negative mla_status_t).  At most 1024. */
+#define MLA_CHUNK_PAGE_BYTES (64 * 576 * 2)
 int mla_chunk_num_parts(void);
 size_t mla_chunk_plan_bytes(int batch, int total_q, int h_q, int num_parts); /* 0: sizes out of range */
 size_t mla_chunk_workspace_bytes(int num_parts);
@@ -381,7 +382,11 @@ int mla_chunk_get_plan(const int32_t* d_cu_seqlens_q, const int32_t* d_cache_seq
  *   d_cu_seqlens_q, d_cache_seqlens  compared with the plan's on the device:
  *                 MLA_ERR_STALE_PLAN where one is another than the plan was made
  *                 for; the results are those of the plan.  NULL: not compared
- *   d_workspace   >= mla_chunk_workspace_bytes(num_parts)
+ *   d_workspace   >= mla_chunk_workspace_bytes(num_parts).  Over FP8 records every
+ *                 further MLA_CHUNK_PAGE_BYTES hold a page that is converted once
+ *                 for a request of several 128-row blocks; requests that do not
+ *                 fit are converted block by block (twice the time, other results
+ *                 none)
  *   d_out         [total_q, h_q, 512] of out_type (bf16, fp16 or fp32), d_lse fp32
  *                 [total_q, h_q]
  * A block-table entry outside the pool (or past max_pages) masks its 64 keys and

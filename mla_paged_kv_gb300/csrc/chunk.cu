@@ -83,7 +83,7 @@ static_assert(kKSlices * 3 == kSlices, "three K stages a tile");
 // Warps: 0 .. 7 softmax, then these.  16-bit caches: one warp each loads K and V
 // by TMA; FP8 records: four each convert them.
 constexpr int kWarpMma = 8, kWarpQ = 9, kWarpK = 10;
-constexpr int kConverters = 4;
+constexpr int kConverters = 8;
 constexpr int threads_of(bool fp8) { return 32 * (kWarpK + (fp8 ? 2 * kConverters : 2)); }
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 256;  // two buffers of 64 columns
@@ -140,13 +140,14 @@ struct Unit {
   int limit0;  // causal: keys that a row of the request's token 0 sees (may be below 1)
   int slot;    // first partial slot
   int parts;   // pieces it is cut into (1: none; 0: no keys)
+  int pages0;  // its request's first page among those converted once for all of its units, or -1
 };
-static_assert(sizeof(Unit) == 4 * kUnitInts, "two int4");
+static_assert(sizeof(Unit) <= 4 * kChunkUnitInts, "three int4");
 
 __device__ __forceinline__ Unit load_unit(const int32_t* units, int u) {
-  const int4* e = reinterpret_cast<const int4*>(units + static_cast<long long>(u) * kUnitInts);
+  const int4* e = reinterpret_cast<const int4*>(units + static_cast<long long>(u) * kChunkUnitInts);
   const int4 a = e[0], b = e[1];
-  return Unit{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  return Unit{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, e[2].x};
 }
 
 __device__ __forceinline__ int pages_of(int len) { return (len + kTile - 1) / kTile; }
@@ -209,54 +210,84 @@ __device__ __forceinline__ void fail(volatile int* abort_flag, int32_t* status) 
 
 // ------------------------------------------------------------------ FP8 records
 
-// 16 codes times their scale as bf16, rounded once, into the two 16-byte chunks
-// from `chunk` on of a swizzled 128-byte row.
+// Two E4M3 codes times their scale as bf16, rounded once.
+__device__ __forceinline__ uint32_t scaled2(uint32_t two, float scale) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));  // (every E4M3 value is an fp16 value)
+  return pack2<false>(f.x * scale, f.y * scale);
+}
+
+// 16 codes into the two 16-byte chunks from `chunk` on of a swizzled 128-byte row.
 __device__ __forceinline__ void store_codes(uint8_t* row, uint32_t chunk, uint32_t swz, const uint4& codes,
                                             float scale) {
   const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
   uint32_t o[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const __half2_raw h =
-        __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));  // (every E4M3 value is an fp16 value)
-    o[i] = pack2<false>(f.x * scale, f.y * scale);
-  }
+  for (int i = 0; i < 8; ++i) o[i] = scaled2(w[i >> 1] >> (16 * (i & 1)) & 0xffffu, scale);
   *reinterpret_cast<uint4*>(row + ((chunk ^ swz) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
   *reinterpret_cast<uint4*>(row + (((chunk + 1) ^ swz) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
-// What a converting lane has of a page: one key (16 a warp) and every other
-// 16-byte piece of its record, odd or even.  The two lanes of a key make whole
-// 32-byte sectors; the order of the keys over the lanes keeps the stores of eight
-// lanes in eight different bank groups (keys k, k+1, k+4, k+5 and two chunks).
+// What a converting lane has of a page: one key (8 a warp) and every fourth
+// 16-byte piece of its record: the same quarter of every 64-dim slice.  The four
+// lanes of a key read 64 bytes in a row, and the stores of eight lanes (two keys of
+// different parity) go to eight different bank groups.
 struct RecordLane {
-  int key;    // of the page
-  int piece;  // 0 or 1
+  int key;      // of the page
+  int quarter;  // of a slice
   uint32_t swz;
 };
 __device__ __forceinline__ RecordLane record_lane(int warp, int lane) {
-  const int k = (lane >> 1 & 1) | (lane >> 2 & 1) << 2 | (lane >> 3 & 1) << 1 | (lane >> 4 & 1) << 3;
-  return RecordLane{16 * warp + k, lane & 1, static_cast<uint32_t>(k & 7)};
+  const int key = 8 * warp + (lane >> 2);
+  return RecordLane{key, lane & 3, static_cast<uint32_t>(key & 7)};
 }
 
 __device__ __forceinline__ const uint8_t* record_at(const ChunkParams& p, int page, int key) {
   return p.records + (static_cast<long long>(max(page, 0)) * kTile + key) * MLA_RECORD_BYTES;
 }
 
-// Converts K pages: three stages of 192 dims a tile, the third with the RoPE part.
-// A stage's pieces are in flight while the one before is converted.
+// Whether the unit's request has been converted as a whole (chunk_convert_kernel).
+__device__ __forceinline__ bool converted(const ChunkParams& p, const Unit& unit) {
+  return unit.pages0 >= 0 && p.conv[unit.req + 1] <= p.room;
+}
+
+// Converts K pages: three stages of three slices a tile, the last slice the RoPE
+// part.  A piece of the next tile is loaded as soon as this tile's is converted, so
+// that a whole tile's loads are in flight (with a stage's alone the loads' latency
+// came with every stage: 3.5 us a tile).
 template <bool kStall>
 __device__ __forceinline__ bool convert_k(const ChunkParams& p, const Run& run, uint32_t rank, int warp, int lane,
-                                          uint8_t* sK, uint64_t* bars, uint32_t bar0, volatile int* abort_flag,
-                                          uint64_t wait_ns) {
+                                          uint8_t* sK, const CUtensorMap* map, uint64_t* bars, uint32_t bar0,
+                                          volatile int* abort_flag, uint64_t wait_ns) {
   const RecordLane me = record_lane(warp, lane);
   Walk w;
   uint32_t n = 0;  // stages so far
   bool ok = true;
-  uint4 raw[8];
+  const uint64_t pol = policy_evict_last();
+  uint4 raw[10];  // eight slices of codes, then the RoPE slice's two chunks
   for (int u = run.u0; ok && walk_to(p.units, run, u, w); u = w.u + 1) {
     const int pages = pages_of(w.unit.len);
+    if (converted(p, w.unit)) {
+      // its pages lie in the workspace: one TMA load a stage, and an arrival of every warp's
+      for (int j = w.lo; j < w.hi && ok; ++j) {
+        const int k = 2 * j + static_cast<int>(rank);
+        if (lane == 0)
+          for (int c = 0; c < 3 && ok; ++c) {
+            const int s = static_cast<int>((n + c) % kKStages), r = static_cast<int>((n + c) / kKStages);
+            if (r >= 1) ok = mbar_wait(&bars[K_EMPTY + s], (r - 1) & 1, abort_flag, wait_ns);
+            if (!ok || (kStall && rank == 0 && n + c == 0)) continue;
+            if (warp == 0 && k < pages) {
+              mbar_arrive_expect_tx_remote_relaxed(bar0 + 8 * (K_FULL + s), kKBytes);
+              tma_load_4d_pair(sK + s * kKBytes, map, bar0 + 8 * (K_FULL + s), 0, 0, kKSlices * c, w.unit.pages0 + k, pol);
+            } else {
+              mbar_arrive_remote_relaxed(bar0 + 8 * (K_FULL + s));
+            }
+          }
+        n += 3;
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+      }
+      continue;
+    }
     int ids = 0, base = -32;
     auto page_at = [&](int j) {  // this CTA's page of tile j
       if (2 * j - base >= 32) {
@@ -265,46 +296,42 @@ __device__ __forceinline__ bool convert_k(const ChunkParams& p, const Run& run, 
       }
       return __shfl_sync(0xffffffffu, ids, 2 * j + static_cast<int>(rank) - base);
     };
-    auto load = [&](const uint8_t* rec, int c, int i) {  // piece i of stage c
-      if (c < 2) return i < 6 ? __ldcg(reinterpret_cast<const uint4*>(rec + 192 * c + 32 * i + 16 * me.piece)) : raw[i];
-      return i < 4 ? __ldcg(reinterpret_cast<const uint4*>(rec + 384 + 32 * i + 16 * me.piece))
-                   : __ldcg(reinterpret_cast<const uint4*>(rec + 528 + 32 * (i - 4) + 16 * me.piece));
+    auto load = [&](const uint8_t* rec, int i) {
+      const uint8_t* at = i < 8 ? rec + 64 * i + 16 * me.quarter : rec + 528 + 32 * me.quarter + 16 * (i - 8);
+      return __ldcg(reinterpret_cast<const uint4*>(at));
     };
     const uint8_t* rec = record_at(p, page_at(w.lo), me.key);
     float4 scale = __ldcg(reinterpret_cast<const float4*>(rec + 512));
 #pragma unroll
-    for (int i = 0; i < 6; ++i) raw[i] = load(rec, 0, i);
+    for (int i = 0; i < 10; ++i) raw[i] = load(rec, i);
     for (int j = w.lo; j < w.hi && ok; ++j) {
       const bool have = 2 * j + static_cast<int>(rank) < pages;
-      const uint8_t* next = j + 1 < w.hi ? record_at(p, page_at(j + 1), me.key) : rec;
-      float4 next_scale = scale;
+      if (j + 1 < w.hi) rec = record_at(p, page_at(j + 1), me.key);
+      const float4 next_scale = __ldcg(reinterpret_cast<const float4*>(rec + 512));
 #pragma unroll
       for (int c = 0; c < 3; ++c, ++n) {
         const int s = static_cast<int>(n % kKStages), r = static_cast<int>(n / kKStages);
         if (ok && r >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&bars[K_EMPTY + s], (r - 1) & 1, abort_flag, wait_ns));
-        uint8_t* stage = sK + s * kKBytes + me.key * 128;
-        const uint8_t* from = c < 2 ? rec : next;
-        if (c == 2) next_scale = __ldcg(reinterpret_cast<const float4*>(next + 512));
+        uint8_t* row = sK + s * kKBytes + me.key * 128;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (c == 2 || i < 6) {
-            const int dim = 192 * c + 32 * i + 16 * me.piece;  // of codes
-            if (have && c == 2 && i >= 4) {
-              const uint32_t chunk = static_cast<uint32_t>(2 * (i - 4) + me.piece);
-              *reinterpret_cast<uint4*>(stage + 2 * kSliceBytes + ((chunk ^ me.swz) << 4)) = raw[i];
-            } else if (have) {
-              const int g = (192 * c + 32 * i) / 128;
-              store_codes(stage + (dim / 64 - 3 * c) * kSliceBytes, static_cast<uint32_t>(dim % 64 / 8), me.swz, raw[i],
-                          g == 0 ? scale.x : g == 1 ? scale.y : g == 2 ? scale.z : scale.w);
+        for (int i = 3 * c; i < 3 * c + 3; ++i, row += kSliceBytes) {
+          const uint32_t chunk = static_cast<uint32_t>(2 * me.quarter);
+          if (i < 8) {
+            const float sc = i < 2 ? scale.x : i < 4 ? scale.y : i < 6 ? scale.z : scale.w;
+            if (have) store_codes(row, chunk, me.swz, raw[i], sc);
+          } else {
+            if (have) {
+              *reinterpret_cast<uint4*>(row + ((chunk ^ me.swz) << 4)) = raw[8];
+              *reinterpret_cast<uint4*>(row + (((chunk + 1) ^ me.swz) << 4)) = raw[9];
             }
+            raw[9] = load(rec, 9);
           }
-          raw[i] = load(from, (c + 1) % 3, i);
+          raw[i] = load(rec, i);
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0 && ok && !(kStall && rank == 0 && n == 0)) arrive_pair(bar0 + 8 * (K_FULL + s));
       }
-      rec = next;
       scale = next_scale;
     }
   }
@@ -312,54 +339,84 @@ __device__ __forceinline__ bool convert_k(const ChunkParams& p, const Run& run, 
 }
 
 // Converts V pages: this CTA's 256 dims of both pages of a tile; keys behind the
-// unit's last one (and pages outside the pool) as zeros.
+// unit's last one (and pages outside the pool) as zeros.  Two pages' loads in
+// flight.
 __device__ __forceinline__ bool convert_v(const ChunkParams& p, const Run& run, uint32_t rank, int warp, int lane,
-                                          uint8_t* sV, uint64_t* bars, uint32_t bar0, volatile int* abort_flag,
-                                          uint64_t wait_ns) {
+                                          uint8_t* sV, const CUtensorMap* map, uint64_t* bars, uint32_t bar0,
+                                          volatile int* abort_flag, uint64_t wait_ns) {
   const RecordLane me = record_lane(warp, lane);
   Walk w;
   uint32_t n = 0;
   bool ok = true;
-  uint4 raw[8];
+  const uint64_t pol = policy_evict_last();
+  uint4 raw[2][4];
+  float2 scale[2];
+  bool live[2];
   for (int u = run.u0; ok && walk_to(p.units, run, u, w); u = w.u + 1) {
     const int pages = min(pages_of(w.unit.len), 2 * w.hi);
+    if (converted(p, w.unit)) {  // (rows behind the last key are zeros there)
+      for (int k = 2 * w.lo; k < pages && ok; ++k, ++n) {
+        const int s = static_cast<int>(n % kVStages), r = static_cast<int>(n / kVStages);
+        if (lane == 0) {
+          if (r >= 1) ok = mbar_wait(&bars[V_EMPTY + s], (r - 1) & 1, abort_flag, wait_ns);
+          if (ok && warp == 0) {
+            mbar_arrive_expect_tx_remote_relaxed(bar0 + 8 * (V_FULL + s), kVBytes);
+            tma_load_4d_pair(sV + s * kVBytes, map, bar0 + 8 * (V_FULL + s), 0, 0, 4 * static_cast<int>(rank),
+                             w.unit.pages0 + k, pol);
+          } else if (ok) {
+            mbar_arrive_remote_relaxed(bar0 + 8 * (V_FULL + s));
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+      }
+      continue;
+    }
     int ids = 0, base = -32;
-    auto page_at = [&](int k) {
+    auto fetch = [&](int k, int h) {  // page k's record: where it is, and whether its key counts
       if (k - base >= 32) {
         base = k;
         ids = page_window(p, w.unit, base, lane);
       }
-      return __shfl_sync(0xffffffffu, ids, k - base);
+      const int id = __shfl_sync(0xffffffffu, ids, k - base);
+      live[h] = id >= 0 && k * kTile + me.key < w.unit.len;
+      const uint8_t* rec = record_at(p, id, me.key);
+      scale[h] = __ldcg(reinterpret_cast<const float2*>(rec + 512 + 8 * rank));
+      return rec + 256 * rank + 16 * me.quarter;
     };
-    int id = page_at(2 * w.lo);
-    const uint8_t* rec = record_at(p, id, me.key);
-    float2 scale = __ldcg(reinterpret_cast<const float2*>(rec + 512 + 8 * rank));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) raw[i] = __ldcg(reinterpret_cast<const uint4*>(rec + 256 * rank + 32 * i + 16 * me.piece));
-    for (int k = 2 * w.lo; k < pages && ok; ++k, ++n) {
-      const int s = static_cast<int>(n % kVStages), r = static_cast<int>(n / kVStages);
-      const bool live = id >= 0 && k * kTile + me.key < w.unit.len;
-      if (k + 1 < pages) id = page_at(k + 1);
-      const uint8_t* next = record_at(p, id, me.key);
-      const float2 next_scale = __ldcg(reinterpret_cast<const float2*>(next + 512 + 8 * rank));
-      if (r >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&bars[V_EMPTY + s], (r - 1) & 1, abort_flag, wait_ns));
-      uint8_t* stage = sV + s * kVBytes + me.key * 128;
+    for (int h = 0; h < 2; ++h) {
+      if (2 * w.lo + h >= pages) continue;
+      const uint8_t* from = fetch(2 * w.lo + h, h);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint8_t* row = stage + i / 2 * kSliceBytes;
-        const uint32_t chunk = static_cast<uint32_t>(4 * (i & 1) + 2 * me.piece);
-        if (live) {
-          store_codes(row, chunk, me.swz, raw[i], i < 4 ? scale.x : scale.y);
-        } else {
-          *reinterpret_cast<uint4*>(row + ((chunk ^ me.swz) << 4)) = make_uint4(0u, 0u, 0u, 0u);
-          *reinterpret_cast<uint4*>(row + (((chunk + 1) ^ me.swz) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+      for (int i = 0; i < 4; ++i) raw[h][i] = __ldcg(reinterpret_cast<const uint4*>(from + 64 * i));
+    }
+    for (int k0 = 2 * w.lo; k0 < pages && ok; k0 += 2) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (k0 + h >= pages) continue;
+        const int s = static_cast<int>(n % kVStages), r = static_cast<int>(n / kVStages);
+        ++n;
+        const bool mine = live[h];
+        const float2 sc = scale[h];
+        const bool more = k0 + h + 2 < pages;
+        const uint8_t* from = more ? fetch(k0 + h + 2, h) : nullptr;
+        if (ok && r >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&bars[V_EMPTY + s], (r - 1) & 1, abort_flag, wait_ns));
+        uint8_t* row = sV + s * kVBytes + me.key * 128;
+        const uint32_t chunk = static_cast<uint32_t>(2 * me.quarter);
+#pragma unroll
+        for (int i = 0; i < 4; ++i, row += kSliceBytes) {
+          if (mine) {
+            store_codes(row, chunk, me.swz, raw[h][i], i < 2 ? sc.x : sc.y);
+          } else {
+            *reinterpret_cast<uint4*>(row + ((chunk ^ me.swz) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4*>(row + (((chunk + 1) ^ me.swz) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          if (more) raw[h][i] = __ldcg(reinterpret_cast<const uint4*>(from + 64 * i));
         }
-        raw[i] = __ldcg(reinterpret_cast<const uint4*>(next + 256 * rank + 32 * i + 16 * me.piece));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && ok) arrive_pair(bar0 + 8 * (V_FULL + s));
       }
-      scale = next_scale;
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0 && ok) arrive_pair(bar0 + 8 * (V_FULL + s));
     }
   }
   return ok;
@@ -420,10 +477,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
   }
   if (warp == kWarpQ && lane == 0) {
     prefetch_tmap(&q_map);
-    if (!kFp8) {
-      prefetch_tmap(&k_map);
-      prefetch_tmap(&v_map);
-    }
+    prefetch_tmap(&k_map);
+    prefetch_tmap(&v_map);
   }
   tc_fence_before();
   __syncthreads();
@@ -439,11 +494,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
   if (kFp8 && warp >= kWarpK) {
     // ------------------------------------------------------------ FP8 records: K or V converted
     const uint32_t bar0 = mapa_shared(smem_u32(bars), 0);
-    const bool ok = warp < kWarpK + kConverters ? convert_k<kStall>(p, run, rank, warp - kWarpK, lane, sK, bars, bar0,
-                                                                    abort_flag, kWaitNs)
-                                                : convert_v(p, run, rank, warp - kWarpK - kConverters, lane, sV, bars,
-                                                            bar0, abort_flag, kWaitNs);
-    if (!ok && lane == 0) fail(abort_flag, p.status);
+    pdl_wait_prior_grid();  // the pages that are converted before
+    const bool ok = warp < kWarpK + kConverters
+                        ? convert_k<kStall>(p, run, rank, warp - kWarpK, lane, sK, &k_map, bars, bar0, abort_flag, kWaitNs)
+                        : convert_v(p, run, rank, warp - kWarpK - kConverters, lane, sV, &v_map, bars, bar0, abort_flag,
+                                    kWaitNs);
+    if (!ok && lane == 0) {
+      fail(abort_flag, p.status);
+      // copies in flight land (bounded) before this CTA may end
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 1000000ull) {
+      }
+    }
     __syncwarp();
   } else if (warp > kWarpMma) {
     // ------------------------------------------------------------ loads: Q, K or V
@@ -825,6 +887,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
   cluster_wait();
 }
 
+// ------------------------------------------------------------------ convert
+
+// Pages of FP8 records as bf16 pages in the workspace, for requests of several
+// units: each of those would convert them again (3.0 us a tile against 1.5 from
+// 16-bit pages; a page converted here takes HBM 19 ns).  A block a page at a time,
+// eight rows a warp, half of them in flight; rows behind the last key, and pages
+// outside the pool (reported), as zeros.
+__global__ void __launch_bounds__(256) chunk_convert_kernel(const ChunkParams p, uint16_t* __restrict__ pages) {
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int total = min(p.conv[p.batch], p.room);
+  for (int i = blockIdx.x; i < total; i += gridDim.x) {
+    int lo = 0, hi = p.batch;  // conv[lo] <= i < conv[hi]
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
+      const int n = __popc(__ballot_sync(0xffffffffu, at < hi && p.conv[at] <= i));
+      lo += n * step;
+      hi = min(lo + step, hi);
+    }
+    if (p.conv[lo + 1] > p.room) return;  // only whole requests, and this is the last one
+    const int k = i - p.conv[lo], keys = p.made[p.batch + 1 + lo] - k * kTile;
+    const int page = k < p.max_pages ? p.block_table[static_cast<long long>(lo) * p.max_pages + k] : -1;
+    const bool good = page >= 0 && page < p.num_pages;
+    if (!good && threadIdx.x == 0) report(p.status, MLA_ERR_BAD_INDEX);
+    const int row0 = 8 * warp;
+    const uint8_t* rec = p.records + (static_cast<long long>(good ? page : 0) * kTile + row0) * MLA_RECORD_BYTES;
+    uint16_t* out = pages + (static_cast<long long>(i) * kTile + row0) * kDqk;
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+      uint2 code[4][2];
+      float scale[4][2];
+      uint4 rope[4];
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const uint8_t* r = rec + (4 * half + n) * MLA_RECORD_BYTES;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          code[n][h] = __ldcs(reinterpret_cast<const uint2*>(r + 256 * h) + lane);
+          scale[n][h] = __ldcs(reinterpret_cast<const float*>(r + 512) + 2 * h + (lane >> 4));
+        }
+        if (lane < 8) rope[n] = __ldcs(reinterpret_cast<const uint4*>(r + 528) + lane);
+      }
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const bool live = good && row0 + 4 * half + n < keys;
+        uint4* o = reinterpret_cast<uint4*>(out + (4 * half + n) * kDqk);
+        const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint2 c = code[n][h];
+          const float sc = scale[n][h];
+          o[32 * h + lane] = live ? make_uint4(scaled2(c.x & 0xffffu, sc), scaled2(c.x >> 16, sc),
+                                               scaled2(c.y & 0xffffu, sc), scaled2(c.y >> 16, sc))
+                                  : none;
+        }
+        if (lane < 8) o[64 + lane] = live ? rope[n] : none;
+      }
+    }
+  }
+}
+
 // ------------------------------------------------------------------ combine
 
 // Rows of the units that were cut (their pieces merged) and of those without
@@ -957,17 +1080,26 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPla
     for (int i = tid; i < p.parts * MLA_SCHED_INTS; i += kPlanThreads) p.sched[i] = 0;
     return;
   }
-  // first unit of each request
+  // first unit of each request, and its first page among those of requests that are converted as a whole
   int units = 0;
+  long long pages = 0;
   for (int b0 = 0; b0 < p.batch; b0 += kPlanThreads) {
     const int b = b0 + tid;
     int n = 0;
     if (b < p.batch) n = ((p.cu[b + 1] - p.cu[b]) * p.h_q + kRowsPerBlock - 1) / kRowsPerBlock;
     int all;
     const int at = block_scan(n, s_warp, &all);
-    if (b < p.batch) p.first[b] = units + at;
+    long long all_pages;
+    const long long page = block_scan(n >= kConvertUnits ? static_cast<long long>(pages_of(max(p.lens[b], 0))) : 0ll,
+                                      s_warp64, &all_pages);
+    if (b < p.batch) {
+      p.first[b] = units + at;
+      p.conv[b] = static_cast<int>(min(pages + page, static_cast<long long>(INT32_MAX)));
+    }
     units += all;
+    pages += all_pages;
   }
+  if (tid == 0) p.conv[p.batch] = static_cast<int>(min(pages, static_cast<long long>(INT32_MAX)));
   if (tid == 0) {
     p.head[kHeadUnits] = units;
     p.head[kHeadCausal] = p.causal;
@@ -991,9 +1123,10 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPla
       const int rel = (u - p.first[lo]) * kRowsPerBlock, rows = min(n * p.h_q - rel, kRowsPerBlock);
       const int limit0 = keys - n + 1;
       const int len = p.causal ? max(limit0 + (rel + rows - 1) / p.h_q, 0) : keys;
-      int4* e = reinterpret_cast<int4*>(p.units + static_cast<long long>(u) * kUnitInts);
+      int4* e = reinterpret_cast<int4*>(p.units + static_cast<long long>(u) * kChunkUnitInts);
       e[0] = make_int4(tok0 * p.h_q + rel, rows, rel, lo);
       e[1] = make_int4(len, limit0, 0, len > 0 ? 1 : 0);
+      e[2] = make_int4(p.conv[lo + 1] > p.conv[lo] ? p.conv[lo] : -1, 0, 0, 0);
       mine = len > 0 ? tiles_of(len) + kFixedCost : 0;
       if (len == 0) p.fix[atomicAdd(&p.head[kHeadFix], 1)] = u;  // (in any order: no result depends on it)
     }
@@ -1016,7 +1149,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPla
           hi = mid;
       }
       u = lo;
-      const int tiles = tiles_of(p.units[static_cast<long long>(u) * kUnitInts + 4]);
+      const int tiles = tiles_of(p.units[static_cast<long long>(u) * kChunkUnitInts + 4]);
       const long long off = x - p.prefix[u];
       t = static_cast<int>(min(max(off - kFixedCost, 0ll), static_cast<long long>(tiles)));
       if (t < kLeastTiles) t = 0;
@@ -1038,7 +1171,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPla
   if (opens) {
     int cuts = 1;
     for (int i = tid + 1; i < p.parts && cut_u[i] == cut_u[tid]; ++i) cuts += cut_t[i] != cut_t[i - 1];
-    int32_t* e = p.units + static_cast<long long>(cut_u[tid]) * kUnitInts;
+    int32_t* e = p.units + static_cast<long long>(cut_u[tid]) * kChunkUnitInts;
     e[6] = at;
     e[7] = cuts + 1;
     p.fix[atomicAdd(&p.head[kHeadFix], 1)] = cut_u[tid];
@@ -1063,11 +1196,12 @@ ChunkPlanLayout chunk_plan_layout(int batch, int total_q, int h_q, int parts) {
   z.max_units = static_cast<int>(static_cast<long long>(total_q) * h_q / kRowsPerBlock) + batch;
   const size_t units = static_cast<size_t>(z.max_units);
   z.units = 256;
-  z.sched = z.units + up(units * kUnitInts * 4);
+  z.sched = z.units + up(units * kChunkUnitInts * 4);
   z.fix = z.sched + up(static_cast<size_t>(parts) * MLA_SCHED_INTS * 4);
   z.prefix = z.fix + up(units * 4);
   z.first = z.prefix + up(units * 8);
-  z.made = z.first + up(static_cast<size_t>(batch) * 4);
+  z.conv = z.first + up(static_cast<size_t>(batch) * 4);
+  z.made = z.conv + up((static_cast<size_t>(batch) + 1) * 4);
   z.bytes = z.made + up((2 * static_cast<size_t>(batch) + 1) * 4);
   return z;
 }
@@ -1097,9 +1231,23 @@ cudaError_t chunk_setup() {
 }
 
 cudaError_t launch_chunk(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const ChunkParams& p,
-                         bool half, bool stall, int parts, cudaStream_t st) {
+                         bool half, bool stall, bool after_convert, int parts, cudaStream_t st) {
   const bool fp8 = p.records != nullptr;
-  chunk_kernel_of(half, fp8, stall)<<<2 * parts, ck::threads_of(fp8), ck::kSmemBytes, st>>>(q, k, v, p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * parts), 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(ck::threads_of(fp8)), 1, 1);
+  cfg.dynamicSmemBytes = ck::kSmemBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = after_convert ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, chunk_kernel_of(half, fp8, stall), q, k, v, p);
+}
+
+cudaError_t launch_chunk_convert(const ChunkParams& p, uint16_t* pages, int sms, cudaStream_t st) {
+  ck::chunk_convert_kernel<<<std::min(p.room, 8 * sms), 256, 0, st>>>(p, pages);
   return cudaGetLastError();
 }
 

@@ -159,23 +159,26 @@ constexpr int kMaxChunkParts = 1024;
 constexpr int kMaxChunkKeys = 1 << 24;  // keys of a request
 constexpr int kFixedCost = 3;           // a unit's Q load and epilogue, in 128-key tiles
 constexpr int kLeastTiles = 1;          // of a unit's piece
+constexpr int kChunkUnitInts = 12;
+constexpr int kConvertUnits = 2;        // units from which a request's FP8 pages are converted once for all
 enum : int { kHeadUnits = 0, kHeadCausal = 1, kHeadFix = 2 };  // header: units, causal, units for the combine
 struct ChunkPlanLayout {
   int max_units;
-  size_t units, sched, fix, prefix, first, made, bytes;
+  size_t units, sched, fix, prefix, first, conv, made, bytes;
 };
 ChunkPlanLayout chunk_plan_layout(int batch, int total_q, int h_q, int parts);
 struct ChunkPlanParams {
   const int32_t *cu, *lens;
   int batch, total_q, h_q, causal, parts;
-  int32_t *head, *units, *sched, *fix, *first, *made;
+  int32_t *head, *units, *sched, *fix, *first, *conv, *made;
   long long* prefix;
   int32_t* status;
 };
 struct ChunkParams {
-  const int32_t *head, *units, *sched, *fix, *made;  // of the plan
+  const int32_t *head, *units, *sched, *fix, *conv, *made;  // of the plan
   const int32_t *cu, *lens;                          // the caller's, to be compared with the plan's, or NULL
   const uint8_t* records;  // a cache of FP8 records, or NULL
+  int room;                // pages that the workspace holds converted
   const int32_t* block_table;
   int max_pages, num_pages, batch, h_q;
   float scale_log2;
@@ -188,7 +191,8 @@ struct ChunkParams {
 cudaError_t chunk_setup();  // once per device: shared-memory opt-in
 cudaError_t launch_chunk_plan(const ChunkPlanParams& p, cudaStream_t st);
 cudaError_t launch_chunk(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const ChunkParams& p,
-                         bool half, bool stall, int parts, cudaStream_t st);
+                         bool half, bool stall, bool after_convert, int parts, cudaStream_t st);
+cudaError_t launch_chunk_convert(const ChunkParams& p, uint16_t* pages, int sms, cudaStream_t st);
 cudaError_t launch_chunk_combine(const ChunkParams& p, int parts, int sms, cudaStream_t st);
 
 }  // namespace mla

@@ -1,5 +1,6 @@
 // C ABI of the serving operators (mla_serving.h): argument checks, tensor
 // maps and launches.  No device memory is allocated here.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -295,6 +296,7 @@ int chunk_attention(const void* d_q, const void* d_kv, const int32_t* d_block_ta
   p.units = ints(z.units);
   p.sched = ints(z.sched);
   p.fix = ints(z.fix);
+  p.conv = ints(z.conv);
   p.made = ints(z.made);
   p.cu = cu;
   p.lens = lens;
@@ -317,18 +319,31 @@ int chunk_attention(const void* d_q, const void* d_kv, const int32_t* d_block_ta
   const cuuint64_t q_dims[4] = {64, static_cast<cuuint64_t>(total_q) * h_q, MLA_D_QK / 64, 1};
   const cuuint64_t q_strides[3] = {2 * MLA_D_QK, 128, 2 * MLA_D_QK};
   const cuuint32_t q_box[4] = {64, 64, MLA_D_QK / 64, 1};
-  const cuuint64_t dims[4] = {64, MLA_PAGE_SIZE, MLA_D_QK / 64, static_cast<cuuint64_t>(num_pages)};
+  // FP8 records: the pages of the workspace behind the partial sums (none: a map that nothing is loaded through)
+  const void* pages = d_kv;
+  int map_pages = num_pages;
+  bool convert = false;
+  if (p.records) {
+    const size_t sums = mla_chunk_workspace_bytes(num_parts);
+    const size_t room = (workspace_bytes - sums) / (2 * MLA_D_QK * MLA_PAGE_SIZE);
+    p.room = static_cast<int>(std::min<size_t>(room, 1 << 30));
+    pages = p.room > 0 ? static_cast<const char*>(d_workspace) + sums : d_workspace;
+    map_pages = p.room > 0 ? p.room : 1;
+    // (a request of several row blocks has more rows than one)
+    convert = p.room > 0 && static_cast<long long>(total_q) * h_q > MLA_ROWS_PER_BLOCK;
+    if (!convert) p.room = 0;
+  }
+  const cuuint64_t dims[4] = {64, MLA_PAGE_SIZE, MLA_D_QK / 64, static_cast<cuuint64_t>(map_pages)};
   const cuuint64_t strides[3] = {2 * MLA_D_QK, 128, 2 * MLA_D_QK * MLA_PAGE_SIZE};
   const cuuint32_t k_box[4] = {64, 64, 3, 1}, v_box[4] = {64, 64, 4, 1};
   rc = encode_map16(&qm, d_q, 4, q_dims, q_strides, q_box);
-  if (p.records) {
-    km = vm = qm;  // not used
-  } else {
-    if (rc == MLA_OK) rc = encode_map16(&km, d_kv, 4, dims, strides, k_box);
-    if (rc == MLA_OK) rc = encode_map16(&vm, d_kv, 4, dims, strides, v_box);
-  }
+  if (rc == MLA_OK) rc = encode_map16(&km, pages, 4, dims, strides, k_box);
+  if (rc == MLA_OK) rc = encode_map16(&vm, pages, 4, dims, strides, v_box);
   if (rc != MLA_OK) return rc;
-  rc = launched(launch_chunk(qm, km, vm, p, dtype == MLA_DTYPE_FP16, stall, num_parts, to_stream(stream)));
+  if (convert)
+    rc = launched(launch_chunk_convert(p, static_cast<uint16_t*>(const_cast<void*>(pages)), sms, to_stream(stream)));
+  if (rc != MLA_OK) return rc;
+  rc = launched(launch_chunk(qm, km, vm, p, dtype == MLA_DTYPE_FP16, stall, convert, num_parts, to_stream(stream)));
   return rc != MLA_OK || stall ? rc : launched(launch_chunk_combine(p, num_parts, sms, to_stream(stream)));
 }
 
@@ -786,6 +801,7 @@ int mla_chunk_get_plan(const int32_t* d_cu_seqlens_q, const int32_t* d_cache_seq
   p.sched = ints(z.sched);
   p.fix = ints(z.fix);
   p.first = ints(z.first);
+  p.conv = ints(z.conv);
   p.made = ints(z.made);
   p.prefix = reinterpret_cast<long long*>(plan + z.prefix);
   p.status = d_status;

@@ -99,6 +99,14 @@ class Case:
         pl = None if parts is None else mla.plan_chunks(cu, lens, q.shape[0], q.shape[1], causal, num_parts=parts)
         out, lse = mla.chunk_attention(q, cache, table, lens, cu, causal, scale, out_fp32, pl=pl)
         self.check(out, lse, causal, scale)
+        if cache.dtype == torch.uint8:  # without room for converted pages, and with room for some: the same to the bit
+            pl = pl or mla.plan_chunks(cu, lens, q.shape[0], q.shape[1], causal)
+            base = pl.workspace
+            for room in (0, 3, 9):
+                pl.workspace = torch.zeros(base.numel() + room * mla.CHUNK_PAGE_BYTES, dtype=torch.uint8, device="cuda")
+                o, l, status = torch.full_like(out, 7.0), torch.full_like(lse, 7.0), i32([0])
+                mla.mla_chunk_attention_fwd(q, cache, table, pl, o, l, status, scale)
+                assert int(status) == 0 and torch.equal(o, out) and torch.equal(l, lse)
         return out, lse
 
 
