@@ -383,10 +383,10 @@ int mla_chunk_get_plan(const int32_t* d_cu_seqlens_q, const int32_t* d_cache_seq
  *                 MLA_ERR_STALE_PLAN where one is another than the plan was made
  *                 for; the results are those of the plan.  NULL: not compared
  *   d_workspace   >= mla_chunk_workspace_bytes(num_parts).  Over FP8 records every
- *                 further MLA_CHUNK_PAGE_BYTES hold a page that is converted once
- *                 for a request of several 128-row blocks; requests that do not
- *                 fit are converted block by block (twice the time, other results
- *                 none)
+ *                 further MLA_CHUNK_PAGE_BYTES hold a page of the requests, in
+ *                 order, converted once; requests that do not fit are converted by
+ *                 each 128-row block that reads them (two to three times slower, the
+ *                 same results)
  *   d_out         [total_q, h_q, 512] of out_type (bf16, fp16 or fp32), d_lse fp32
  *                 [total_q, h_q]
  * A block-table entry outside the pool (or past max_pages) masks its 64 keys and

@@ -42,6 +42,14 @@
 #include "ptx.cuh"
 #include "serving.cuh"
 
+// Timeline hooks: empty in the library; an instrumented build defines
+// MLA_TRACE(event, index) to record timestamps.
+#ifndef MLA_TRACE
+#define MLA_TRACE(ev, i) \
+  do {                   \
+  } while (0)
+#endif
+
 namespace mla {
 namespace ck {
 
@@ -141,43 +149,61 @@ struct Unit {
   int slot;    // first partial slot
   int parts;   // pieces it is cut into (1: none; 0: no keys)
   int pages0;  // its request's first page among those converted once for all of its units, or -1
+  int whole;   // 1: one pair's as a whole (pair u % pairs); 0: in the list that is cut
 };
 static_assert(sizeof(Unit) <= 4 * kChunkUnitInts, "three int4");
 
 __device__ __forceinline__ Unit load_unit(const int32_t* units, int u) {
   const int4* e = reinterpret_cast<const int4*>(units + static_cast<long long>(u) * kChunkUnitInts);
   const int4 a = e[0], b = e[1];
-  return Unit{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, e[2].x};
+  return Unit{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, e[2].x, e[2].y};
 }
 
 __device__ __forceinline__ int pages_of(int len) { return (len + kTile - 1) / kTile; }
 __device__ __forceinline__ int tiles_of(int len) { return (len + kBN - 1) / kBN; }
 
-// A pair's run of tiles: from tile t0 of unit u0 to tile t1 of unit u1 (not included).
+// A pair's work: the whole units among u = pair, pair + pairs, .. (in waves: the
+// pairs are then at neighbouring units at a time, which are the same requests' and
+// read the same keys), then its run of the units that are cut, from tile t0 of
+// entry u0 of their list to tile t1 of entry u1 (not included).
 struct Run {
-  int u0, t0, u1, t1, piece;  // piece: of u0, among those the unit is cut into
+  int u0, t0, u1, t1, piece;  // piece: of entry u0, among those it is cut into
+  int pair, pairs, units;
 };
 
-__device__ __forceinline__ Run load_run(const int32_t* sched, int pair) {
-  const int32_t* e = sched + pair * MLA_SCHED_INTS;
-  return Run{e[0], e[1], e[2], e[3], e[4]};
+__device__ __forceinline__ Run load_run(const ChunkParams& p) {
+  const int pair = blockIdx.x >> 1;
+  const int32_t* e = p.sched + pair * MLA_SCHED_INTS;
+  return Run{e[0], e[1], e[2], e[3], e[4], pair, static_cast<int>(gridDim.x >> 1), p.head[kHeadWhole]};
 }
 
-// The next unit of the run from u on, and its tiles lo .. hi - 1.
+// The units of a run one after another, and each one's tiles lo .. hi - 1.
 struct Walk {
   Unit unit;
-  int u, lo, hi;
+  int lo, hi;
+  int u;         // next unit to look at, then
+  int at;        // next entry of the list
+  bool first;    // the unit is the run's first entry: its pieces are counted from `piece`
 };
 
-__device__ __forceinline__ bool walk_to(const int32_t* units, const Run& r, int u, Walk& w) {
-  for (; u < r.u1 || (u == r.u1 && r.t1 > 0); ++u) {
-    w.unit = load_unit(units, u);
-    w.lo = u == r.u0 ? r.t0 : 0;
-    w.hi = u == r.u1 ? r.t1 : tiles_of(w.unit.len);
-    if (w.hi > w.lo) {
-      w.u = u;
-      return true;
-    }
+__device__ __forceinline__ Walk walk_begin(const Run& r) { return Walk{Unit{}, 0, 0, r.pair, r.u0, false}; }
+
+__device__ __forceinline__ bool walk_next(const ChunkParams& p, const Run& r, Walk& w) {
+  while (w.u < r.units) {
+    w.unit = load_unit(p.units, w.u);
+    w.u += r.pairs;
+    if (!w.unit.whole) continue;
+    w.lo = 0;
+    w.hi = tiles_of(w.unit.len);
+    return true;
+  }
+  while (w.at < r.u1 || (w.at == r.u1 && r.t1 > 0)) {
+    w.unit = load_unit(p.units, p.rest[w.at]);
+    w.first = w.at == r.u0;
+    w.lo = w.first ? r.t0 : 0;
+    w.hi = w.at == r.u1 ? r.t1 : tiles_of(w.unit.len);
+    ++w.at;
+    if (w.hi > w.lo) return true;
   }
   return false;
 }
@@ -260,12 +286,12 @@ __device__ __forceinline__ bool convert_k(const ChunkParams& p, const Run& run, 
                                           uint8_t* sK, const CUtensorMap* map, uint64_t* bars, uint32_t bar0,
                                           volatile int* abort_flag, uint64_t wait_ns) {
   const RecordLane me = record_lane(warp, lane);
-  Walk w;
+  Walk w = walk_begin(run);
   uint32_t n = 0;  // stages so far
   bool ok = true;
   const uint64_t pol = policy_evict_last();
   uint4 raw[10];  // eight slices of codes, then the RoPE slice's two chunks
-  for (int u = run.u0; ok && walk_to(p.units, run, u, w); u = w.u + 1) {
+  while (ok && walk_next(p, run, w)) {
     const int pages = pages_of(w.unit.len);
     if (converted(p, w.unit)) {
       // its pages lie in the workspace: one TMA load a stage, and an arrival of every warp's
@@ -345,14 +371,14 @@ __device__ __forceinline__ bool convert_v(const ChunkParams& p, const Run& run, 
                                           uint8_t* sV, const CUtensorMap* map, uint64_t* bars, uint32_t bar0,
                                           volatile int* abort_flag, uint64_t wait_ns) {
   const RecordLane me = record_lane(warp, lane);
-  Walk w;
+  Walk w = walk_begin(run);
   uint32_t n = 0;
   bool ok = true;
   const uint64_t pol = policy_evict_last();
   uint4 raw[2][4];
   float2 scale[2];
   bool live[2];
-  for (int u = run.u0; ok && walk_to(p.units, run, u, w); u = w.u + 1) {
+  while (ok && walk_next(p, run, w)) {
     const int pages = min(pages_of(w.unit.len), 2 * w.hi);
     if (converted(p, w.unit)) {  // (rows behind the last key are zeros there)
       for (int k = 2 * w.lo; k < pages && ok; ++k, ++n) {
@@ -441,6 +467,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
   float* sRow = reinterpret_cast<float*>(smem + kOffRow);
 
   const int tid = threadIdx.x;
+  if (tid == 0) MLA_TRACE(0, 0);
   // by a shuffle: the compiler then knows that a warp takes one role, and keeps
   // MMA operands in uniform registers
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -487,9 +514,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
   cluster_wait();
   const uint32_t tmem = *tmem_slot;
   pdl_launch_dependents();
-  const Run run = load_run(p.sched, blockIdx.x >> 1);
+  const Run run = load_run(p);
   const int causal = p.head[kHeadCausal];
-  Walk w;
+  if (tid == 0) MLA_TRACE(0, 1);
+  Walk w = walk_begin(run);
 
   if (kFp8 && warp >= kWarpK) {
     // ------------------------------------------------------------ FP8 records: K or V converted
@@ -514,7 +542,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
     const uint32_t bar0 = mapa_shared(smem_u32(bars), 0);
     auto expect = [&](int bar, uint32_t bytes) { mbar_arrive_expect_tx_remote_relaxed(bar0 + 8 * bar, bytes); };
     uint32_t n = 0, tails = 0;  // stages (or units of Q) and tail pages so far
-    for (int u = run.u0; ok && walk_to(p.units, run, u, w); u = w.u + 1) {
+    while (ok && walk_next(p, run, w)) {
       if (warp == kWarpQ) {
         if (lane == 0) {
           if (n >= 1) ok = mbar_wait(&bars[Q_EMPTY], (n - 1) & 1, abort_flag, kWaitNs);
@@ -617,10 +645,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
       bool fresh = false;                       // that tile is its unit's first here
       auto issue_pv = [&]() {
         ok = ok && wait(P_FULL, (tn - 1) & 1);
+        MLA_TRACE(3, tn - 1);
         for (int half = 0; half < before && ok; ++half, ++vn) {
           const int vs = static_cast<int>(vn % kVStages);
           ok = wait(V_FULL + vs, (vn / kVStages) & 1);
           if (!ok) break;
+          MLA_TRACE(4 + half, tn - 1);
           tc_fence_after();
           const uint64_t vd = v_desc + static_cast<uint64_t>((vs * kVBytes) >> 4);
           const uint64_t pd = p_desc + static_cast<uint64_t>((half * kSliceBytes) >> 4);
@@ -636,10 +666,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
         }
         if (ok) umma2_commit_warp(&bars[PV_DONE]);
       };
-      for (int u = run.u0; ok && walk_to(p.units, run, u, w); u = w.u + 1) {
+      while (ok && walk_next(p, run, w)) {
         const int pages = __shfl_sync(0xffffffffu, pages_of(w.unit.len), 0);
         const int lo = __shfl_sync(0xffffffffu, w.lo, 0), hi = __shfl_sync(0xffffffffu, w.hi, 0);
-        ok = wait(Q_FULL, qn & 1);
+        // between units the last P V goes first: the output waits for it, and Q K^T for the new Q
+        if (before > 0) issue_pv();
+        before = 0;
+        if (ok) ok = wait(Q_FULL, qn & 1);
+        MLA_TRACE(1, qn);
         ++qn;
         for (int j = lo; j < hi && ok; ++j) {
           const uint32_t s_col = tm + kTmemS + 64u * (tn & 1);
@@ -648,6 +682,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
             const int ks = static_cast<int>(kn % kKStages);
             if (ok) ok = wait(K_FULL + ks, (kn / kKStages) & 1);
             if (!ok) break;
+            if (c == 0) MLA_TRACE(2, tn);
+            if (c == 2) MLA_TRACE(6, tn);
             tc_fence_after();
             const uint64_t kd = k_desc + static_cast<uint64_t>((ks * kKBytes) >> 4);
             const uint64_t qd = q_desc + static_cast<uint64_t>((c * kKBytes) >> 4);
@@ -703,26 +739,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
     };
     bool ok = true;
     uint32_t tn = 0;
-    for (int u = run.u0; ok && walk_to(p.units, run, u, w); u = w.u + 1) {
-      // keys this row sees (rows past the unit's last one: unmasked, not stored)
-      const int limit = row >= w.unit.rows ? 1 << 30
-                        : causal           ? min(w.unit.len, w.unit.limit0 + (w.unit.rel + row) / p.h_q)
-                                           : w.unit.len;
+    // what the tile loop keeps of a unit: the keys this row sees (rows past the unit's last one: unmasked, not
+    // stored), the block table's row, and its pages outside the pool within the window from page `base` on
+    int limit, base;
+    uint32_t bad;
+    auto look = [&](int page) {
+      base = page;
+      const int k = base + lane;
+      bool out = false;
+      if (k < pages_of(w.unit.len)) {
+        const int id = k < p.max_pages ? p.block_table[static_cast<long long>(w.unit.req) * p.max_pages + k] : -1;
+        out = id < 0 || id >= p.num_pages;
+      }
+      bad = __ballot_sync(0xffffffffu, out);
+    };
+    auto enter = [&]() {
+      if (!walk_next(p, run, w)) return false;
+      limit = row >= w.unit.rows ? 1 << 30
+              : causal           ? min(w.unit.len, w.unit.limit0 + (w.unit.rel + row) / p.h_q)
+                                 : w.unit.len;
+      look(2 * w.lo);
+      return true;
+    };
+    bool more = enter();
+    while (more) {
       float ref = -INFINITY, l = 0.f;
-      int base = -32;
-      uint32_t bad = 0;  // pages of the window outside the pool
       for (int j = w.lo; j < w.hi; ++j, ++tn) {
-        if (2 * j - base >= 32) {
-          base = 2 * j;
-          const int k = base + lane;
-          bool out = false;
-          if (k < pages_of(w.unit.len)) {
-            const int page = k < p.max_pages ? p.block_table[static_cast<long long>(w.unit.req) * p.max_pages + k] : -1;
-            out = page < 0 || page >= p.num_pages;
-          }
-          bad = __ballot_sync(0xffffffffu, out);
-        }
+        if (2 * j - base >= 32) look(2 * j);
         ok = __all_sync(0xffffffffu, ok && mbar_wait(&bars[S_FULL + (tn & 1)], (tn >> 1) & 1, abort_flag, kWaitNs));
+        if (tid == 0) MLA_TRACE(7, tn);
         tc_fence_after();
         float s[32], top;
         tmem_ld32_max(s_addr + 64u * (tn & 1), s, top);
@@ -785,18 +830,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_pair(p_full);
+        if (tid == 0) MLA_TRACE(8, tn);
       }
+      // the next unit is looked at while the last P V runs
+      const bool direct = w.unit.parts == 1;
+      const int rows = w.unit.rows, slot = w.unit.slot + (w.first ? run.piece : 0);
+      const long long first = direct ? w.unit.row0 : static_cast<long long>(slot) * kRowsPerBlock;
+      if (ok) more = enter();
       // the row's sum, in an order that all four share.  (A warp that gave up takes the others along.)
       const float* sum = shared_row(l);
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars[PV_DONE], (tn - 1) & 1, abort_flag, kWaitNs));
       ok = !named_bar_or(row_bar, 128, !ok);
       if (!ok) break;
+      if (tid == 0) MLA_TRACE(10, tn);
       tc_fence_after();
       l = (sum[0] + sum[kCtaRows]) + (sum[2 * kCtaRows] + sum[3 * kCtaRows]);
       const float inv = l == 0.f ? 0.f : 1.f / l;  // 0: the row sees none of these keys
-      const bool direct = w.unit.parts == 1;
-      const int slot = w.unit.slot + (w.u == run.u0 ? run.piece : 0);
-      const long long first = direct ? w.unit.row0 : static_cast<long long>(slot) * kRowsPerBlock;
       const int dim0 = 256 * kh + 128 * ch, q4 = lane & 3;
       // 16 rows x 64 dims at a time.  The load leaves a row's values with four
       // lanes, two of every eight each.
@@ -812,7 +861,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
           const float iv = __shfl_sync(0xffffffffu, inv, from);
           const int orow = row - lane + from;
           const long long at = (first + orow) * kDv + dim0 + c0;
-          const bool store = orow < w.unit.rows;
+          const bool store = orow < rows;
           if (!direct || p.out_type == MLA_DTYPE_FP32) {
             float* dst = (direct ? static_cast<float*>(p.out) : p.o_accum) + at + 2 * q4;
 #pragma unroll
@@ -866,8 +915,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
           }
         }
       }
-      if (part == 0 && row < w.unit.rows)
+      if (part == 0 && row < rows)
         (direct ? p.lse : p.lse_accum)[first + row] = l == 0.f ? -INFINITY : (ref + __log2f(l)) * kLn2;
+      if (tid == 0) MLA_TRACE(9, tn);
       // O has been read: the next unit's first P V waits for this warp's P
       tc_fence_before();
     }
@@ -889,11 +939,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
 
 // ------------------------------------------------------------------ convert
 
-// Pages of FP8 records as bf16 pages in the workspace, for requests of several
-// units: each of those would convert them again (3.0 us a tile against 1.5 from
-// 16-bit pages; a page converted here takes HBM 19 ns).  A block a page at a time,
-// eight rows a warp, half of them in flight; rows behind the last key, and pages
-// outside the pool (reported), as zeros.
+// Pages of FP8 records as bf16 pages in the workspace, for the requests that fit:
+// every unit that reads them would convert them again, and take 3.8 us a tile where
+// 16-bit pages take 1.3 to 1.8 (a tile converted here costs HBM 35 ns; 43 requests, 3
+// of them chunks of up to 400 tokens, 16 heads: 111 us, 144 with single tokens'
+// requests left out, 205 without; 64 single tokens 116 and 110).  A block a page at
+// a time, eight rows a warp, half of them in flight; rows behind the last key, and
+// pages outside the pool (reported), as zeros.
 __global__ void __launch_bounds__(256) chunk_convert_kernel(const ChunkParams p, uint16_t* __restrict__ pages) {
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1049,11 +1101,13 @@ __device__ __forceinline__ T block_scan(T v, T* s_warp, T* total) {
   return base + x - v;
 }
 
-// Units of all requests, in order, and the cuts that give every pair the same
-// cost: a unit costs its tiles and kFixedCost more (its Q, its epilogue), pair i
-// begins where the sum reaches i / pairs of the whole.  A cut within a unit's
-// fixed part, or that would leave less than kLeastTiles on one side, moves to the
-// unit's border.  One block, made once for a batch.
+// Units of all requests, in order, and what each pair does of them.  A unit costs
+// its tiles and kFixedCost more (its Q, its epilogue).  Pair i takes units i, i +
+// pairs, .. as a whole while they fit its share of the whole cost; the others are
+// cut so that every pair's share is filled: the pair whose room is reached at x of
+// their sum begins there.  A cut within a unit's fixed part, or that would leave
+// less than kLeastTiles on one side, moves to the unit's border.  One block, made
+// once for a batch.
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPlanParams p) {
   __shared__ long long s_warp64[32];
   __shared__ int s_warp[32];
@@ -1073,14 +1127,14 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPla
   if (broken) {  // offsets out of order could make requests overlap: nothing is done then
     if (tid == 0) {
       report(p.status, MLA_ERR_BAD_INDEX);
-      p.head[kHeadUnits] = 0;
+      p.head[kHeadWhole] = 0;
       p.head[kHeadCausal] = p.causal;
       p.head[kHeadFix] = 0;
     }
     for (int i = tid; i < p.parts * MLA_SCHED_INTS; i += kPlanThreads) p.sched[i] = 0;
     return;
   }
-  // first unit of each request, and its first page among those of requests that are converted as a whole
+  // first unit of each request, and its first page among all requests'
   int units = 0;
   long long pages = 0;
   for (int b0 = 0; b0 < p.batch; b0 += kPlanThreads) {
@@ -1090,7 +1144,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPla
     int all;
     const int at = block_scan(n, s_warp, &all);
     long long all_pages;
-    const long long page = block_scan(n >= kConvertUnits ? static_cast<long long>(pages_of(max(p.lens[b], 0))) : 0ll,
+    const long long page = block_scan(n > 0 ? static_cast<long long>(pages_of(max(p.lens[b], 0))) : 0ll,
                                       s_warp64, &all_pages);
     if (b < p.batch) {
       p.first[b] = units + at;
@@ -1101,7 +1155,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPla
   }
   if (tid == 0) p.conv[p.batch] = static_cast<int>(min(pages, static_cast<long long>(INT32_MAX)));
   if (tid == 0) {
-    p.head[kHeadUnits] = units;
+    p.head[kHeadWhole] = units;
     p.head[kHeadCausal] = p.causal;
     p.head[kHeadFix] = 0;
   }
@@ -1130,36 +1184,80 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPla
       mine = len > 0 ? tiles_of(len) + kFixedCost : 0;
       if (len == 0) p.fix[atomicAdd(&p.head[kHeadFix], 1)] = u;  // (in any order: no result depends on it)
     }
+    if (u < units) p.cost[u] = static_cast<int>(mine);
     long long all;
-    const long long at = block_scan(mine, s_warp64, &all);
-    if (u < units) p.prefix[u] = cost + at;
+    block_scan(mine, s_warp64, &all);
     cost += all;
   }
   __syncthreads();
-  for (int i = tid; i <= p.parts; i += kPlanThreads) {
-    int u = units, t = 0;
-    if (i < p.parts && units > 0 && cost > 0) {
-      const long long x = cost * i / p.parts;
-      int lo = 0, hi = units;  // the last unit that begins at or before x
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (p.prefix[mid] <= x)
-          lo = mid;
-        else
-          hi = mid;
-      }
-      u = lo;
-      const int tiles = tiles_of(p.units[static_cast<long long>(u) * kChunkUnitInts + 4]);
-      const long long off = x - p.prefix[u];
-      t = static_cast<int>(min(max(off - kFixedCost, 0ll), static_cast<long long>(tiles)));
-      if (t < kLeastTiles) t = 0;
-      if (t > 0 && tiles - t < kLeastTiles) {
-        ++u;
-        t = 0;
-      }
+  // whole units: thread i for pair i
+  const long long share = (cost + p.parts - 1) / p.parts;
+  long long room = 0;
+  if (tid < p.parts) {
+    room = share;
+    constexpr int kAhead = 8;  // costs in flight: the loop is their latency
+    for (int u0 = tid; u0 < units; u0 += kAhead * p.parts) {
+      int c[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) c[k] = u0 + k * p.parts < units ? p.cost[u0 + k * p.parts] : 0;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (c[k] > 0 && c[k] <= room) {
+          room -= c[k];
+          p.cost[u0 + k * p.parts] = 0;
+          p.units[static_cast<long long>(u0 + k * p.parts) * kChunkUnitInts + 9] = 1;
+        }
     }
-    cut_u[i] = u;
-    cut_t[i] = t;
+  }
+  __syncthreads();
+  // the others, one after another, with the sum of the costs before each
+  int rest = 0;
+  long long sum = 0;
+  for (int u0 = 0; u0 < units; u0 += kPlanThreads) {
+    const int u = u0 + tid;
+    const long long mine = u < units ? p.cost[u] : 0;
+    int all;
+    long long all_cost;
+    const int at = block_scan(mine > 0 ? 1 : 0, s_warp, &all);
+    const long long before = block_scan(mine, s_warp64, &all_cost);
+    if (mine > 0) {
+      p.rest[rest + at] = u;
+      p.prefix[rest + at] = sum + before;
+    }
+    rest += all;
+    sum += all_cost;
+  }
+  __syncthreads();
+  {
+    long long all;
+    const long long x = block_scan(room, s_warp64, &all);
+    if (tid < p.parts) {
+      int e = rest, t = 0;
+      if (x < sum) {
+        int lo = 0, hi = rest;  // the last entry that begins at or before x
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) / 2;
+          if (p.prefix[mid] <= x)
+            lo = mid;
+          else
+            hi = mid;
+        }
+        e = lo;
+        const int tiles = tiles_of(p.units[static_cast<long long>(p.rest[e]) * kChunkUnitInts + 4]);
+        t = static_cast<int>(min(max(x - p.prefix[e] - kFixedCost, 0ll), static_cast<long long>(tiles)));
+        if (t < kLeastTiles) t = 0;
+        if (t > 0 && tiles - t < kLeastTiles) {
+          ++e;
+          t = 0;
+        }
+      }
+      cut_u[tid] = e;
+      cut_t[tid] = t;
+    }
+    if (tid == 0) {
+      cut_u[p.parts] = rest;
+      cut_t[p.parts] = 0;
+    }
   }
   __syncthreads();
   // Cuts inside a unit, each counted once; the first of a unit opens its slots.
@@ -1171,10 +1269,11 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPla
   if (opens) {
     int cuts = 1;
     for (int i = tid + 1; i < p.parts && cut_u[i] == cut_u[tid]; ++i) cuts += cut_t[i] != cut_t[i - 1];
-    int32_t* e = p.units + static_cast<long long>(cut_u[tid]) * kChunkUnitInts;
+    const int u = p.rest[cut_u[tid]];
+    int32_t* e = p.units + static_cast<long long>(u) * kChunkUnitInts;
     e[6] = at;
     e[7] = cuts + 1;
-    p.fix[atomicAdd(&p.head[kHeadFix], 1)] = cut_u[tid];
+    p.fix[atomicAdd(&p.head[kHeadFix], 1)] = u;
   }
   if (in) {
     int piece = 0;
@@ -1198,7 +1297,9 @@ ChunkPlanLayout chunk_plan_layout(int batch, int total_q, int h_q, int parts) {
   z.units = 256;
   z.sched = z.units + up(units * kChunkUnitInts * 4);
   z.fix = z.sched + up(static_cast<size_t>(parts) * MLA_SCHED_INTS * 4);
-  z.prefix = z.fix + up(units * 4);
+  z.rest = z.fix + up(units * 4);
+  z.cost = z.rest + up(units * 4);
+  z.prefix = z.cost + up(units * 4);
   z.first = z.prefix + up(units * 8);
   z.conv = z.first + up(static_cast<size_t>(batch) * 4);
   z.made = z.conv + up((static_cast<size_t>(batch) + 1) * 4);

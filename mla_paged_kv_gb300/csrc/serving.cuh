@@ -160,22 +160,25 @@ constexpr int kMaxChunkKeys = 1 << 24;  // keys of a request
 constexpr int kFixedCost = 3;           // a unit's Q load and epilogue, in 128-key tiles
 constexpr int kLeastTiles = 1;          // of a unit's piece
 constexpr int kChunkUnitInts = 12;
-constexpr int kConvertUnits = 2;        // units from which a request's FP8 pages are converted once for all
-enum : int { kHeadUnits = 0, kHeadCausal = 1, kHeadFix = 2 };  // header: units, causal, units for the combine
+#ifndef CU
+#define CU 2
+#endif
+constexpr int kConvertUnits = CU;        // units from which a request's FP8 pages are converted once for all
+enum : int { kHeadWhole = 0, kHeadCausal = 1, kHeadFix = 2 };  // header: units, causal, units for the combine
 struct ChunkPlanLayout {
   int max_units;
-  size_t units, sched, fix, prefix, first, conv, made, bytes;
+  size_t units, sched, fix, rest, cost, prefix, first, conv, made, bytes;
 };
 ChunkPlanLayout chunk_plan_layout(int batch, int total_q, int h_q, int parts);
 struct ChunkPlanParams {
   const int32_t *cu, *lens;
   int batch, total_q, h_q, causal, parts;
-  int32_t *head, *units, *sched, *fix, *first, *conv, *made;
+  int32_t *head, *units, *sched, *fix, *rest, *cost, *first, *conv, *made;
   long long* prefix;
   int32_t* status;
 };
 struct ChunkParams {
-  const int32_t *head, *units, *sched, *fix, *conv, *made;  // of the plan
+  const int32_t *head, *units, *sched, *fix, *rest, *conv, *made;  // of the plan
   const int32_t *cu, *lens;                          // the caller's, to be compared with the plan's, or NULL
   const uint8_t* records;  // a cache of FP8 records, or NULL
   int room;                // pages that the workspace holds converted

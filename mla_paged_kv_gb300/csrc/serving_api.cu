@@ -296,6 +296,7 @@ int chunk_attention(const void* d_q, const void* d_kv, const int32_t* d_block_ta
   p.units = ints(z.units);
   p.sched = ints(z.sched);
   p.fix = ints(z.fix);
+  p.rest = ints(z.rest);
   p.conv = ints(z.conv);
   p.made = ints(z.made);
   p.cu = cu;
@@ -800,6 +801,8 @@ int mla_chunk_get_plan(const int32_t* d_cu_seqlens_q, const int32_t* d_cache_seq
   p.units = ints(z.units);
   p.sched = ints(z.sched);
   p.fix = ints(z.fix);
+  p.rest = ints(z.rest);
+  p.cost = ints(z.cost);
   p.first = ints(z.first);
   p.conv = ints(z.conv);
   p.made = ints(z.made);
