@@ -307,7 +307,7 @@ int mla_rope_table(const double* h_freq, int dim, double magnitude, long long fi
  *              strides in elements, multiples of 8, the last dimension contiguous
  *   d_out, d_k_out  the same shapes, strides of their own; may be d_x and d_k
  *              themselves with the same strides (dims that are not changed are
- *              then not moved), else must not overlap any input
+ *              then not moved), else must share no element with any input
  *   dim        a multiple of 8, at most 1024; rope_dim a multiple of 16, at most
  *              256; rope_offset a multiple of 8
  *   d_x_weight, d_k_weight  [dim] of `dtype`, or NULL: no norm of that side

@@ -37,77 +37,99 @@ _ROPE_HEADS, _GATHER, _CHUNK = _words(10, "22qd8q"), _words(11, "13q"), _words(1
 # ------------------------------------------------------------------ rotary
 
 
+def _frequencies(dim, base, scaling, factor, original, low, high):
+    freq, size = (_D * max(dim // 2, 1))(), _D()
+    rc = load_library().mla_rope_frequencies(dim, base, scaling, factor, original, low, high, freq, size)
+    if rc:
+        _check(rc, "mla_rope_frequencies")
+    return freq, size.value
+
+
+def _table(freq, magnitude, first, out, stream):
+    dev = out.get_device()
+    ptr = _p(out, _FP32, 2, dev, "cos_sin")
+    positions, dim = out.shape
+    if len(freq) * 2 != dim:
+        raise ValueError("cos_sin must have two columns a frequency")
+    rc = load_library().mla_rope_table(freq, dim, magnitude, first, positions, ptr, _q(stream, dev))
+    if rc:
+        _check(rc, "mla_rope_table")
+
+
 def mla_rope_frequencies(dim, base, scaling, factor, original, low, high):
     """(frequencies, magnitude): dim / 2 floats, and what the table's values are multiplied by."""
-    freq, size = (_D * max(int(dim) // 2, 1))(), _D()
-    _check(load_library().mla_rope_frequencies(int(dim), float(base), int(scaling), float(factor), float(original),
-                                               float(low), float(high), freq, ctypes.byref(size)),
-           "mla_rope_frequencies")
-    return list(freq), size.value
+    freq, size = _frequencies(int(dim), float(base), int(scaling), float(factor), float(original), float(low),
+                              float(high))
+    return list(freq), size
 
 
 def mla_rope_table(freq, magnitude, first, cos_sin, stream=None):
     """The table of positions first .. first + cos_sin.shape[0] - 1 into cos_sin fp32 [positions, dim]."""
-    dev = cos_sin.get_device()
-    out = _p(cos_sin, _FP32, 2, dev, "cos_sin")
-    positions, dim = cos_sin.shape
-    if len(freq) * 2 != dim:
-        raise ValueError("cos_sin must have two columns a frequency")
-    _check(load_library().mla_rope_table((_D * len(freq))(*freq), dim, float(magnitude), int(first), positions, out,
-                                         _q(stream, dev)), "mla_rope_table")
+    _table((_D * len(freq))(*freq), float(magnitude), int(first), cos_sin, stream)
+
+
+def _scaling(scaling, high):
+    code = ROPE_SCALING.get(scaling)
+    if code is None:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALING)}")
+    return code, (4.0 if scaling == "wavelength" else 32.0) if high is None else high
 
 
 def rope_frequencies(dim=64, base=10000.0, scaling="none", factor=1.0, original=4096, low=1.0, high=None):
     """(frequencies, magnitude) of rotary positions whose context is stretched by factor: scaling "none", "linear",
     "ntk", "yarn" or "wavelength"; low and high are the turns over the original context (high defaults to 32 for
     "yarn", 4 for "wavelength")."""
-    if scaling not in ROPE_SCALING:
-        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALING)}")
-    if high is None:
-        high = 4.0 if scaling == "wavelength" else 32.0
-    return mla_rope_frequencies(dim, base, ROPE_SCALING[scaling], factor, original, low, high)
+    code, high = _scaling(scaling, high)
+    return mla_rope_frequencies(dim, base, code, factor, original, low, high)
 
 
 def rope_table(positions, dim=64, base=10000.0, scaling="none", factor=1.0, original=4096, low=1.0, high=None,
                magnitude=None, first=0, device="cuda"):
     """The fp32 table [positions, dim] that cache_append (dim 64) and rope_heads read: cosines, then sines, of the
     positions from first on.  magnitude (of the values) defaults to the scaling's own."""
-    freq, size = rope_frequencies(dim, base, scaling, factor, original, low, high)
-    out = torch.empty(positions, dim, dtype=_FP32, device=device)
-    mla_rope_table(freq, size if magnitude is None else magnitude, first, out)
+    code, high = _scaling(scaling, high)
+    freq, size = _frequencies(dim, base, code, factor, original, low, high)
+    out = torch.empty((positions, dim), dtype=_FP32, device=device)
+    _table(freq, size if magnitude is None else magnitude, first, out, None)
     return out
 
 
 def _heads(t, dtype, tokens, dim, dev, name):
-    """Address, strides and heads of a [tokens, heads, dim] tensor with a contiguous last dimension."""
+    """Address, strides and heads of a [tokens, heads, dim] tensor with a contiguous last dimension, and the address
+    behind it."""
+    stride, shape = t.stride(), t.shape
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    stride, shape = t.stride(), t.shape
-    if len(shape) != 3 or shape[0] != tokens or shape[2] != dim or (stride[2] != 1 and dim > 1):
+    if len(shape) != 3 or shape[0] != tokens or shape[2] != dim or stride[2] != 1:
         raise ValueError(f"{name} must be [{tokens}, heads, {dim}] with a contiguous last dimension")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be on cuda:{dev}, is on {t.device}")
-    return t.data_ptr(), stride[0], stride[1], shape[1]
+    ptr, heads = t.data_ptr(), shape[1]
+    return ptr, stride[0], stride[1], heads, ptr + 2 * ((tokens - 1) * stride[0] + (heads - 1) * stride[1] + dim)
 
 
-def _span(t):
-    """First byte of a strided tensor, and the one behind its last."""
-    if t.numel() == 0:
-        return 0, 0
-    at = t.data_ptr()
-    return at, at + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
+def _apart(a, b, tokens, dim):
+    """Whether two such tensors share no element: one behind the other, or side by side in rows (or heads) of equal
+    strides, as the parts of a packed projection are."""
+    if a[0] >= b[4] or b[0] >= a[4]:
+        return True
+    step = (b[0] - a[0]) // 2
+    for stride, one, other in ((a[1] if a[1] == b[1] else 0, (a[3] - 1) * a[2] + dim, (b[3] - 1) * b[2] + dim),
+                               (a[2] if a[1:3] == b[1:3] else 0, dim, dim)):
+        if stride > 0 and step % stride >= one and step % stride + other <= stride:
+            return True
+    return False
 
 
-def _check_apart(out, others, same):
-    """out must not overlap any of the others, but for `same`, which it may be exactly."""
-    if any(n > 1 and s < 1 for n, s in zip(out.shape, out.stride())):
+def _output(out, tokens, dim, others, same):
+    """An output's elements share no memory among themselves, nor with other tensors of the call but `same`, which it
+    may be as a whole (tensors as _heads gives them)."""
+    ptr, ts, hs, heads, end = out
+    if not ((heads == 1 or hs >= dim) and (tokens <= 1 or ts >= (heads - 1) * hs + dim)) and \
+            not ((tokens <= 1 or ts >= dim) and (heads == 1 or hs >= (tokens - 1) * ts + dim)):
         raise ValueError("an output must not have elements that share memory")
-    a, b = _span(out)
     for t in others:
-        if t is None or (t is same and t.data_ptr() == out.data_ptr() and t.stride() == out.stride()):
-            continue
-        c, d = _span(t)
-        if a < d and c < b:
+        if ptr < t[4] and t[0] < end and not (t is same and t[:4] == out[:4]) and not _apart(out, t, tokens, dim):
             raise ValueError("an output overlaps another tensor of the call")
 
 
@@ -124,22 +146,26 @@ def mla_rope_heads(x, out, cos_sin, status, cache_seqlens=None, cu_seqlens=None,
         raise ValueError("x must be [tokens, heads, dim]")
     dev = x.get_device()
     tokens, _, dim = x.shape
-    x_ptr, xt, xh, heads = _heads(x, dt, tokens, dim, dev, "x")
-    out_ptr, ot, oh, n = _heads(out, dt, tokens, dim, dev, "out")
-    if n != heads:
-        raise ValueError("out must have the heads of x")
-    k_ptr = ko_ptr = kt = kh = kot = koh = k_heads = 0
+    src = _heads(x, dt, tokens, dim, dev, "x")
+    dst = _heads(out, dt, tokens, dim, dev, "out")
+    heads = src[3]
+    if heads == 0 or dst[3] != heads:
+        raise ValueError("out must have the heads of x, at least one")
+    none = (0, 0, 0, 0, 0)
+    k_src = k_dst = none
     if k is not None:
-        k_ptr, kt, kh, k_heads = _heads(k, dt, tokens, dim, dev, "k")
         if k_out is None:
             raise ValueError("k needs k_out")
-        ko_ptr, kot, koh, n = _heads(k_out, dt, tokens, dim, dev, "k_out")
-        if n != k_heads or k_heads == 0:
+        k_src = _heads(k, dt, tokens, dim, dev, "k")
+        k_dst = _heads(k_out, dt, tokens, dim, dev, "k_out")
+        if k_src[3] == 0 or k_dst[3] != k_src[3]:
             raise ValueError("k_out must have the heads of k, at least one")
-        _check_apart(k_out, (x, k, out), k)
     elif k_out is not None or k_weight is not None:
         raise ValueError("k_out and k_weight need k")
-    _check_apart(out, (x, k), x)
+    if tokens:
+        _output(dst, tokens, dim, (src, k_src), src)
+        if k is not None:
+            _output(k_dst, tokens, dim, (src, k_src, dst), k_src)
     w_ptr = kw_ptr = 0
     if x_weight is not None:
         w_ptr = _p(x_weight, dt, 1, dev, "x_weight")
@@ -175,8 +201,8 @@ def mla_rope_heads(x, out, cos_sin, status, cache_seqlens=None, cu_seqlens=None,
         raise ValueError("cu_seqlens need cache_seqlens")
     if offset is None:
         offset = dim - rope
-    _call(_ROPE_HEADS, "mla_rope_heads", x_ptr, xt, xh, out_ptr, ot, oh, heads, w_ptr, k_ptr, kt, kh, ko_ptr, kot, koh,
-          k_heads, kw_ptr, dim, code, tokens, rope, offset, 1 if interleaved else 0, norm_eps, pos_ptr, cu_ptr,
+    _call(_ROPE_HEADS, "mla_rope_heads", *src[:3], *dst[:3], heads, w_ptr, *k_src[:3], *k_dst[:3], k_src[3], kw_ptr,
+          dim, code, tokens, rope, offset, 1 if interleaved else 0, norm_eps, pos_ptr, cu_ptr,
           lens_ptr, batch, cos_ptr, max_pos, _p(status, _INT32, 1, dev, "status"), _q(stream, dev))
 
 
@@ -233,8 +259,9 @@ def mla_cache_gather(cache, block_table, cu_seqlens, out, status, starts=None, s
     stride = out.stride()
     if len(stride) != 2 or out.shape[1] != 576 or stride[1] != 1 or out.get_device() != dev:
         raise ValueError(f"out must be [rows, 576] with contiguous rows, on cuda:{dev}")
-    _check_apart(out, (cache,), None)
-    rows = out.shape[0]
+    rows, at = out.shape[0], out.data_ptr()
+    if rows and at < ptr + cache.numel() * cache.element_size() and ptr < at + 2 * ((rows - 1) * stride[0] + 576):
+        raise ValueError("out overlaps the cache")
     _call(_GATHER, "mla_cache_gather", ptr, code, pages, table_ptr, max_pages, cu_ptr, starts_ptr, batch, rows,
           out.data_ptr(), stride[0] if rows > 1 else 576, _p(status, _INT32, 1, dev, "status"), _q(stream, dev))
 

@@ -22,27 +22,36 @@ namespace {
 // position 2^24, where an fp32 angle would be off by a radian.  The nearest
 // quarter turn comes off in integers too, so that sincospif sees at most a
 // quarter of a half turn, and values next to zero keep their leading bits.
-// Bound by the writes for many positions (163840 x 64: 42 MB), by the launch for
-// few; a thread takes four pairs, whose cosines and sines are a 16-byte store each.
+// A thread keeps four pairs and steps through positions, so that an angle is one
+// addition.  Bound by the writes for many positions (163840 x 64: 42 MB), by the
+// launch for few.
 __global__ void __launch_bounds__(256)
-    rope_table_kernel(const RopeSteps f, int dim, float magnitude, unsigned long long first, long long threads,
+    rope_table_kernel(const RopeSteps f, int dim, float magnitude, unsigned long long first, int positions,
                       float* __restrict__ out) {
-  const int quads = dim / 8;
-  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < threads; i += gridDim.x * 256ll) {
-    const long long p = i / quads;
-    const int q = static_cast<int>(i - p * quads);
+  const int quads = dim / 8, rows = 256 / quads;  // threads of a position, positions of a block at a time
+  const int q = threadIdx.x % quads, r = threadIdx.x / quads;
+  if (r >= rows) return;
+  const int step = gridDim.x * rows;
+  long long p = static_cast<long long>(blockIdx.x) * rows + r;
+  unsigned long long angle[4], turn[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    angle[k] = (first + static_cast<unsigned long long>(p)) * f.step[4 * q + k];
+    turn[k] = static_cast<unsigned long long>(step) * f.step[4 * q + k];
+  }
+  for (; p < positions; p += step) {
     float c[4], s[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const unsigned long long angle = (first + static_cast<unsigned long long>(p)) * f.step[4 * q + k];
-      const unsigned long long quarter = (angle + (1ull << 61)) >> 62;  // nearest, modulo 4
-      const float x = static_cast<float>(static_cast<long long>(angle - (quarter << 62))) * 0x1p-63f;  // half turns
+      const unsigned long long quarter = (angle[k] + (1ull << 61)) >> 62;  // nearest, modulo 4
+      const float x = static_cast<float>(static_cast<long long>(angle[k] - (quarter << 62))) * 0x1p-63f;  // half turns
       float sn, cs;
       sincospif(x, &sn, &cs);
       const bool swap = quarter & 1;
       const float a = swap ? sn : cs, b = swap ? cs : sn;
       c[k] = ((quarter + 1) & 2) ? -a * magnitude : a * magnitude;  // quarters 1 and 2
       s[k] = (quarter & 2) ? -b * magnitude : b * magnitude;        // quarters 2 and 3
+      angle[k] += turn[k];
     }
     float* row = out + p * dim + 4 * q;
     *reinterpret_cast<float4*>(row) = make_float4(c[0], c[1], c[2], c[3]);
@@ -71,21 +80,19 @@ __device__ __forceinline__ uint32_t pack2f(float a, float b) {
   }
 }
 
+// 8 elements as four pairs of fp32: the arithmetic runs on packed pairs.
 template <bool kHalf>
-__device__ __forceinline__ void widen(const uint4& v, float* f) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float2 a = unpack2<kHalf>(w[k]);
-    f[2 * k] = a.x;
-    f[2 * k + 1] = a.y;
-  }
+__device__ __forceinline__ void widen(const uint4& v, float2 (&f)[4]) {
+  f[0] = unpack2<kHalf>(v.x);
+  f[1] = unpack2<kHalf>(v.y);
+  f[2] = unpack2<kHalf>(v.z);
+  f[3] = unpack2<kHalf>(v.w);
 }
 
 template <bool kHalf>
-__device__ __forceinline__ uint4 narrow(const float* f) {
-  return make_uint4(pack2f<kHalf>(f[0], f[1]), pack2f<kHalf>(f[2], f[3]), pack2f<kHalf>(f[4], f[5]),
-                    pack2f<kHalf>(f[6], f[7]));
+__device__ __forceinline__ uint4 narrow(const float2 (&f)[4]) {
+  return make_uint4(pack2f<kHalf>(f[0].x, f[0].y), pack2f<kHalf>(f[1].x, f[1].y), pack2f<kHalf>(f[2].x, f[2].y),
+                    pack2f<kHalf>(f[3].x, f[3].y));
 }
 
 // y = x * rsqrt(mean(x^2) + eps) * w over a head's dims (with weights), then the
@@ -97,55 +104,61 @@ __device__ __forceinline__ uint4 narrow(const float* f) {
 // side by side), or two that only pass.  `lanes` lanes hold a head, kItems items
 // each, and a warp takes one token and as many heads as it has lanes for, kIter
 // times over: the position, found by a chain of small loads while the heads'
-// own are in flight, and the angles are read once for all of them.
-template <bool kHalf, int kItems, int kIter, bool kNorm>
+// own are in flight, and the angles are read once for all of them.  Issue comes
+// next after memory: layout and norm are template arguments, the arithmetic is
+// packed, and few registers leave many warps resident (24577 tokens x 40 heads x 128
+// dims with norm 86 us; 138 with one code for all and the items' values kept).
+// kTurn: items of a lane that may turn, its first ones.
+template <bool kHalf, int kItems, int kTurn, int kIter, bool kNorm, bool kInter>
 __global__ void __launch_bounds__(128) rope_heads_kernel(const RopeHeadsParams p) {
   const int lane = threadIdx.x & 31;
   const long long unit = blockIdx.x * 4ll + (threadIdx.x >> 5);
-  const int per_token = p.side[0].units + p.side[1].units;
-  const long long t64 = unit / per_token;
-  if (t64 >= p.total) return;  // uniform over the warp
-  const int t = static_cast<int>(t64);
-  int u = static_cast<int>(unit - t64 * per_token);
-  const bool second = u >= p.side[0].units;
-  const RopeSide& s = p.side[second];
-  if (second) u -= p.side[0].units;
-  const int slots = 32 / p.lanes, mine = lane & (p.lanes - 1);
-  const int head0 = u * slots * kIter + lane / p.lanes;
+  const int t = static_cast<int>(unit / p.units);
+  if (t >= p.total) return;  // uniform over the warp
+  const int slots = 32 >> p.lane_bits, mine = lane & ((1 << p.lane_bits) - 1);
+  // this lane's first head, of queries and then keys
+  const int head0 = static_cast<int>(unit - static_cast<long long>(t) * p.units) * slots * kIter + (lane >> p.lane_bits);
+  const int heads = p.side[0].heads + p.side[1].heads;
 
-  // Elements of an item's two pieces; -1: none.
+  // Where an item's two pieces lie in a head, and whether they are any of it.
   int at[kItems][2];
+  bool is[kItems][2], turns[kTurn];
 #pragma unroll
   for (int i = 0; i < kItems; ++i) {
-    const int item = mine + i * p.lanes;
-    if (item < p.pairs) {
-      at[i][0] = p.offset + (p.interleaved ? 16 * item : 8 * item);
-      at[i][1] = at[i][0] + (p.interleaved ? 8 : p.rope / 2);
+    const int item = mine + (i << p.lane_bits);
+    if (i < kTurn) turns[i] = item < p.pairs;
+    if (i < kTurn && turns[i]) {
+      at[i][0] = p.offset + (kInter ? 16 * item : 8 * item);
+      at[i][1] = at[i][0] + (kInter ? 8 : p.rope / 2);
+      is[i][0] = is[i][1] = true;
     } else {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         int e = 8 * (2 * (item - p.pairs) + k);
         if (e >= p.offset) e += p.rope;
-        at[i][k] = item < p.items && e < p.dim ? e : -1;
+        is[i][k] = item < p.items && e < p.dim;
+        at[i][k] = is[i][k] ? e : 0;
       }
     }
   }
   uint4 raw[kIter][kItems][2];
-  const uint16_t* x = s.x + t64 * s.x_token_stride;
 #pragma unroll
   for (int n = 0; n < kIter; ++n) {
     const int head = head0 + n * slots;
+    const bool second = head >= p.side[0].heads;
+    const RopeSide& s = p.side[second];
+    const uint16_t* x = s.x + static_cast<long long>(t) * s.x_token_stride +
+                        (head - (second ? p.side[0].heads : 0)) * s.x_head_stride;
 #pragma unroll
     for (int i = 0; i < kItems; ++i)
 #pragma unroll
       for (int k = 0; k < 2; ++k)
-        raw[n][i][k] = head < s.heads && at[i][k] >= 0
-                           ? *reinterpret_cast<const uint4*>(x + head * s.x_head_stride + at[i][k])
-                           : make_uint4(0u, 0u, 0u, 0u);
+        raw[n][i][k] = head < heads && is[i][k] ? *reinterpret_cast<const uint4*>(x + at[i][k]) : make_uint4(0u, 0u, 0u, 0u);
   }
 
+  const bool rotate = p.cos_sin != nullptr;
   int pos = 0;
-  if (p.cos_sin != nullptr) {
+  if (rotate) {
     if (p.positions != nullptr) {
       pos = p.positions[t];
     } else {
@@ -154,9 +167,16 @@ __global__ void __launch_bounds__(128) rope_heads_kernel(const RopeHeadsParams p
         const int each = p.total / p.batch;
         b = t / each;
         left = (b + 1) * each - t;
+        pos = p.seqlens[b] - left;
+      } else if (p.batch <= 32) {  // all requests at once: one trip to memory
+        const int b0 = min(lane, p.batch - 1);
+        const int first = p.cu[b0], last = p.cu[b0 + 1], len = p.seqlens[b0];
+        const uint32_t in = __ballot_sync(0xffffffffu, lane < p.batch && first <= t && t < last);
+        if (in == 0) return;  // of no sequence
+        pos = __shfl_sync(0xffffffffu, len - (last - t), 31 - __clz(in));
       } else {
-        if (t < p.cu[0] || t >= p.cu[p.batch]) return;  // of no sequence
-        int lo = 0, hi = p.batch;                       // cu[lo] <= t < cu[hi], 32 ways at a time
+        if (t < p.cu[0] || t >= p.cu[p.batch]) return;
+        int lo = 0, hi = p.batch;  // cu[lo] <= t < cu[hi], 32 ways at a time
         while (hi - lo > 1) {
           const int step = (hi - lo + 31) / 32, probe = lo + (lane + 1) * step;
           const int n = __popc(__ballot_sync(0xffffffffu, probe < hi && p.cu[probe] <= t));
@@ -165,103 +185,120 @@ __global__ void __launch_bounds__(128) rope_heads_kernel(const RopeHeadsParams p
         }
         b = lo;
         left = p.cu[b + 1] - t;
+        pos = p.seqlens[b] - left;
       }
-      pos = p.seqlens[b] - left;
     }
     if (pos < 0 || pos >= p.max_pos) {
       report(p.status, MLA_ERR_BAD_INDEX);
       return;
     }
   }
-  float cs[kItems][8], sn[kItems][8];
-  if (p.cos_sin != nullptr) {
+  // cosines and sines of an item's eight pairs, two at a time
+  float2 cs[kTurn][4], sn[kTurn][4];
+  if (rotate) {
     const float* row = p.cos_sin + static_cast<long long>(pos) * p.rope;
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-      const int item = mine + i * p.lanes;
-      if (item >= p.pairs) continue;
+    for (int i = 0; i < kTurn; ++i) {
+      if (!turns[i]) continue;
+      const int item = mine + (i << p.lane_bits);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        *reinterpret_cast<float4*>(cs[i] + 4 * k) = __ldg(reinterpret_cast<const float4*>(row + 8 * item) + k);
-        *reinterpret_cast<float4*>(sn[i] + 4 * k) =
+        *reinterpret_cast<float4*>(cs[i] + 2 * k) = __ldg(reinterpret_cast<const float4*>(row + 8 * item) + k);
+        *reinterpret_cast<float4*>(sn[i] + 2 * k) =
             __ldg(reinterpret_cast<const float4*>(row + p.rope / 2 + 8 * item) + k);
       }
     }
   }
-  uint16_t* out = s.out + t64 * s.out_token_stride;
 #pragma unroll
   for (int n = 0; n < kIter; ++n) {
     const int head = head0 + n * slots;
-    float rstd = 1.f;
+    const bool second = head >= p.side[0].heads;
+    const RopeSide& s = p.side[second];
+    uint16_t* out = s.out + static_cast<long long>(t) * s.out_token_stride +
+                    (head - (second ? p.side[0].heads : 0)) * s.out_head_stride;
+    const bool normed = kNorm && s.weight != nullptr;
+    float2 r2 = make_float2(1.f, 1.f);
     if constexpr (kNorm) {
-      if (s.weight != nullptr) {
-        float ss = 0.f;
+      float2 ss[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int i = 0; i < kItems; ++i)
+      for (int i = 0; i < kItems; ++i)
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float f[8];
-            widen<kHalf>(raw[n][i][k], f);
+        for (int k = 0; k < 2; ++k) {
+          float2 f[4];
+          widen<kHalf>(raw[n][i][k], f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(f[e], f[e], ss);
-          }
-        for (int o = p.lanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        rstd = 1.f / sqrtf(ss / static_cast<float>(p.dim) + p.eps);
-      }
+          for (int e = 0; e < 4; ++e) ss[e & 1] = __ffma2_rn(f[e], f[e], ss[e & 1]);
+        }
+      float sum = (ss[0].x + ss[0].y) + (ss[1].x + ss[1].y);
+      for (int o = 1 << p.lane_bits >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      const float r = rsqrtf(fmaf(sum, p.inv_dim, p.eps));
+      r2 = make_float2(r, r);
     }
-    if (head >= s.heads) continue;
+    if (head >= heads) continue;
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
-      float f[2][8];
-      widen<kHalf>(raw[n][i][0], f[0]);
-      widen<kHalf>(raw[n][i][1], f[1]);
-      if constexpr (kNorm) {
-        if (s.weight != nullptr) {
+      float2 f[2][4];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            if (at[i][k] < 0) continue;
-            float w[8];
-            widen<kHalf>(__ldg(reinterpret_cast<const uint4*>(s.weight + at[i][k])), w);
+      for (int k = 0; k < 2; ++k) {
+        widen<kHalf>(raw[n][i][k], f[k]);
+        if (normed) {
+          float2 g[4];
+          widen<kHalf>(__ldg(reinterpret_cast<const uint4*>(s.weight + at[i][k])), g);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[k][e] = f[k][e] * rstd * w[e];
-          }
+          for (int e = 0; e < 4; ++e) f[k][e] = __fmul2_rn(__fmul2_rn(f[k][e], r2), g[e]);
         }
       }
-      if (mine + i * p.lanes < p.pairs) {
-        // pair j of the item: elements j of both pieces, or (interleaved) 2j and 2j + 1 of the 16
+      // (products and sums in the order of cache_append's, so that a key turned there has the same bits)
+      if (i < kTurn && turns[i]) {
+        if constexpr (kInter) {  // pair j: element pair j of the item's eight
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float& a = p.interleaved ? f[j >> 2][2 * (j & 3)] : f[0][j];
-          float& b = p.interleaved ? f[j >> 2][2 * (j & 3) + 1] : f[1][j];
-          const float y = a * cs[i][j] - b * sn[i][j], z = b * cs[i][j] + a * sn[i][j];
-          a = y;
-          b = z;
+          for (int j = 0; j < 8; ++j) {
+            float2& a = f[j >> 2][j & 3];
+            const float c = (j & 1) ? cs[i][j >> 1].y : cs[i][j >> 1].x, w = (j & 1) ? sn[i][j >> 1].y : sn[i][j >> 1].x;
+            a = __ffma2_rn(a, make_float2(c, c), __fmul2_rn(make_float2(a.y, a.x), make_float2(-w, w)));
+          }
+        } else {  // pair j: element j of both pieces
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 a = f[0][j], b = f[1][j], c = cs[i][j], w = sn[i][j];
+            f[0][j] = __ffma2_rn(a, c, __fmul2_rn(make_float2(-b.x, -b.y), w));
+            f[1][j] = __ffma2_rn(b, c, __fmul2_rn(a, w));
+          }
         }
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k)
-        if (at[i][k] >= 0)
-          *reinterpret_cast<uint4*>(out + head * s.out_head_stride + at[i][k]) = narrow<kHalf>(f[k]);
+        if (is[i][k]) *reinterpret_cast<uint4*>(out + at[i][k]) = narrow<kHalf>(f[k]);
     }
   }
 }
 
-template <bool kHalf, int kItems, int kIter>
+template <bool kHalf, int kItems, int kTurn, int kIter>
 cudaError_t launch_heads(const RopeHeadsParams& p, bool norm, unsigned grid, cudaStream_t st) {
-  if (norm)
-    rope_heads_kernel<kHalf, kItems, kIter, true><<<grid, 128, 0, st>>>(p);
-  else
-    rope_heads_kernel<kHalf, kItems, kIter, false><<<grid, 128, 0, st>>>(p);
+  if (norm) {
+    if (p.interleaved)
+      rope_heads_kernel<kHalf, kItems, kTurn, kIter, true, true><<<grid, 128, 0, st>>>(p);
+    else
+      rope_heads_kernel<kHalf, kItems, kTurn, kIter, true, false><<<grid, 128, 0, st>>>(p);
+  } else if (p.interleaved) {
+    rope_heads_kernel<kHalf, kItems, kTurn, kIter, false, true><<<grid, 128, 0, st>>>(p);
+  } else {
+    rope_heads_kernel<kHalf, kItems, kTurn, kIter, false, false><<<grid, 128, 0, st>>>(p);
+  }
   return cudaGetLastError();
 }
 
 template <bool kHalf>
 cudaError_t launch_items(const RopeHeadsParams& p, int per_lane, bool norm, unsigned grid, cudaStream_t st) {
+  const bool one = p.pairs <= 1 << p.lane_bits;  // a lane's first item alone may turn
   switch (per_lane) {
-    case 1: return launch_heads<kHalf, 1, 4>(p, norm, grid, st);
-    case 2: return launch_heads<kHalf, 2, 2>(p, norm, grid, st);
-    case 3: return launch_heads<kHalf, 3, 1>(p, norm, grid, st);
-    default: return launch_heads<kHalf, 4, 1>(p, norm, grid, st);
+    case 1: return launch_heads<kHalf, 1, 1, 2>(p, norm, grid, st);
+    case 2:
+      return one ? launch_heads<kHalf, 2, 1, 2>(p, norm, grid, st) : launch_heads<kHalf, 2, 2, 2>(p, norm, grid, st);
+    case 3:
+      return one ? launch_heads<kHalf, 3, 1, 2>(p, norm, grid, st) : launch_heads<kHalf, 3, 3, 2>(p, norm, grid, st);
+    default:
+      return one ? launch_heads<kHalf, 4, 1, 1>(p, norm, grid, st) : launch_heads<kHalf, 4, 4, 1>(p, norm, grid, st);
   }
 }
 
@@ -269,10 +306,10 @@ cudaError_t launch_items(const RopeHeadsParams& p, int per_lane, bool norm, unsi
 
 cudaError_t launch_rope_table(const RopeSteps& f, int dim, float magnitude, long long first, int positions, float* out,
                               int sms, cudaStream_t st) {
-  const long long threads = static_cast<long long>(positions) * (dim / 8);
-  const long long blocks = std::min<long long>((threads + 255) / 256, 8ll * sms);
-  rope_table_kernel<<<static_cast<unsigned>(blocks), 256, 0, st>>>(f, dim, magnitude,
-                                                                   static_cast<unsigned long long>(first), threads, out);
+  const int rows = 256 / (dim / 8);
+  const long long blocks = std::min<long long>((positions + rows - 1ll) / rows, 8ll * sms);
+  rope_table_kernel<<<static_cast<unsigned>(blocks), 256, 0, st>>>(
+      f, dim, magnitude, static_cast<unsigned long long>(first), positions, out);
   return cudaGetLastError();
 }
 
@@ -284,17 +321,18 @@ bool rope_heads_layout(RopeHeadsParams* p, bool passes, int* per_lane, long long
   // 4 idle); among equals the fewest items a lane
   int best = 1 << 30;
   for (int n = 1; n <= 4; ++n) {
-    int lanes = 1;
-    while (lanes * n < p->items) lanes *= 2;
-    if (lanes <= 32 && lanes * n - p->items < best) {
-      best = lanes * n - p->items;
-      p->lanes = lanes;
+    int bits = 0;
+    while ((n << bits) < p->items) ++bits;
+    if (bits <= 5 && (n << bits) - p->items < best) {
+      best = (n << bits) - p->items;
+      p->lane_bits = bits;
       *per_lane = n;
     }
   }
-  const int iter = *per_lane == 1 ? 4 : *per_lane == 2 ? 2 : 1;
-  for (RopeSide& s : p->side) s.units = (s.heads + 32 / p->lanes * iter - 1) / (32 / p->lanes * iter);
-  *blocks = (static_cast<long long>(p->total) * (p->side[0].units + p->side[1].units) + 3) / 4;
+  p->inv_dim = 1.f / static_cast<float>(p->dim);
+  const int heads = (32 >> p->lane_bits) * (*per_lane < 4 ? 2 : 1);  // of a warp
+  p->units = (p->side[0].heads + p->side[1].heads + heads - 1) / heads;
+  *blocks = (static_cast<long long>(p->total) * p->units + 3) / 4;
   return best < (1 << 30) && *blocks < (1ll << 31);
 }
 

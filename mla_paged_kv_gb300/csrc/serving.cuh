@@ -83,13 +83,12 @@ struct RopeSide {
   const uint16_t* weight;
   long long x_token_stride, x_head_stride, out_token_stride, out_head_stride;
   int heads;
-  int units;  // warps a token
 };
 struct RopeHeadsParams {
   RopeSide side[2];
   int total, batch, dim, rope, offset, interleaved;
-  int pairs, items, lanes;  // rope_heads_layout
-  float eps;
+  int pairs, items, lane_bits, units;  // rope_heads_layout; units: warps a token
+  float eps, inv_dim;
   const int32_t *positions, *cu, *seqlens;
   const float* cos_sin;  // NULL: no rotation
   int max_pos;

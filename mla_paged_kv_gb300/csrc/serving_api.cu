@@ -698,10 +698,10 @@ int mla_rope_heads(const void* d_x, long long x_token_stride, long long x_head_s
   RopeHeadsParams p{};
   p.side[0] = RopeSide{static_cast<const uint16_t*>(d_x), static_cast<uint16_t*>(d_out),
                        static_cast<const uint16_t*>(d_x_weight), x_token_stride, x_head_stride, out_token_stride,
-                       out_head_stride, heads, 0};
+                       out_head_stride, heads};
   p.side[1] = RopeSide{static_cast<const uint16_t*>(d_k), static_cast<uint16_t*>(d_k_out),
                        static_cast<const uint16_t*>(d_k_weight), k_token_stride, k_head_stride, k_out_token_stride,
-                       k_out_head_stride, k_heads, 0};
+                       k_out_head_stride, k_heads};
   p.total = total_tokens;
   p.batch = batch;
   p.dim = dim;

@@ -192,8 +192,10 @@ def test_python_refuses_wrong_tensors():
     refuses(ValueError, x, table, lens, k_norm_weight=torch.zeros(64, dtype=torch.bfloat16))
     refuses(ValueError, x, table, lens, norm_weight=torch.zeros(32, dtype=torch.bfloat16))
     # outputs that overlap what is read, or themselves
-    both = torch.zeros(4, 2, 128, dtype=torch.bfloat16)
-    refuses(ValueError, both[..., :64], table, lens, out=both[..., 64:])
+    both = torch.zeros(5, 3, 128, dtype=torch.bfloat16)
+    refuses(ValueError, both[:4, :2, :64], table, lens, out=both[:4, :2, 8:72])
+    refuses(ValueError, both[:4, :2, :64], table, lens, out=both[:4, 1:, :64])
+    refuses(ValueError, both[:4, :2, :64], table, lens, out=both[1:, :2, :64])
     refuses(ValueError, x, table, lens, out=torch.zeros(4, 1, 64, dtype=torch.bfloat16).expand(4, 2, 64))
     refuses(ValueError, x, table, lens, k=x.clone(), k_out=x)
 

@@ -206,6 +206,27 @@ def test_in_place_and_strided():
     assert torch.equal(got, src[:, :1].expand(10, 12, 192))
 
 
+def test_packed_projection_in_place():
+    """Queries and keys side by side in one projection's rows, both turned where they lie; the values stay."""
+    h = Heads(9, 6, 64, 32, 2, norm=True, seed=21)
+    rows = torch.full((9, 10 * 64), 7.0, dtype=BF16, device="cuda")
+    q, k = rows[:, :384].view(9, 6, 64), rows[:, 384:512].view(9, 2, 64)
+    q.copy_(h.x)
+    k.copy_(h.k)
+    got = mla.rope_heads(q, h.table.cuda(), i32([30]), out=q, k=k, k_out=k, norm_weight=h.w.cuda(),
+                         k_norm_weight=h.kw.cuda(), norm_eps=EPS)
+    pos = list(range(21, 30))
+    h.check(got[0], h.x, h.w, pos, 32, False)
+    h.check(got[1], h.k, h.kw, pos, 32, False)
+    assert bool((rows[:, 512:] == 7.0).all())
+    # another part of the same heads as the output
+    both = torch.zeros(9, 6, 128, dtype=BF16, device="cuda")
+    both[..., :64] = h.x.cuda()
+    mla.rope_heads(both[..., :64], h.table.cuda(), i32([30]), out=both[..., 64:])
+    h.check(both[..., 64:], h.x, None, pos, 32, False)
+    assert torch.equal(both[..., :64].cpu(), h.x)
+
+
 @pytest.mark.parametrize("in_place", [False, True])
 def test_tokens_that_are_left(in_place):
     """Tokens of no request, and those whose position is not in the table (reported)."""
