@@ -352,12 +352,13 @@ int mla_cache_gather(const void* d_cache, int cache_dtype, int num_pages, const 
  * A query that sees no key gets out = 0, lse = -inf.  Rows of the outputs outside
  * every chunk are left as they were.  Softmax weights are rounded to the cache's
  * type (bf16 over FP8 records) for the product with the values and divided by the
- * sum of the unrounded ones; statistics and sums are fp32.  Over FP8 records keys
- * and values are code x scale rounded to bf16, what mla_cache_gather gives.
+ * sum of the unrounded ones; statistics and sums are fp32.  Over FP8 records a
+ * value is code x scale rounded to bf16, what mla_cache_gather gives, and a key
+ * that and its remainder in bf16, 16 bits of the product.
  *
  * num_parts: pairs of CTAs that share the work; mla_chunk_num_parts gives as many
  * as the device runs at once (>= 1, or a negative mla_status_t).  At most 1024. */
-#define MLA_CHUNK_PAGE_BYTES (64 * 576 * 2)
+#define MLA_CHUNK_PAGE_BYTES (64 * 1088 * 2)
 int mla_chunk_num_parts(void);
 size_t mla_chunk_plan_bytes(int batch, int total_q, int h_q, int num_parts); /* 0: sizes out of range */
 size_t mla_chunk_workspace_bytes(int num_parts);

@@ -26,7 +26,7 @@ import torch
 from . import DTYPE_FP8_RECORD, _DTYPE_CODE, _check, check_status, load_library, MlaError
 from .serving import (_D, _DTYPE_CODE16, _FP32, _INT32, _UINT8, _call, _p, _q, _status, _words)
 
-CHUNK_PAGE_BYTES = 64 * 576 * 2
+CHUNK_PAGE_BYTES = 64 * 1088 * 2  # of a page that a call over FP8 records converts (MLA_CHUNK_PAGE_BYTES)
 ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "wavelength": 4}
 
 __all__ = ["ROPE_SCALING", "CHUNK_PAGE_BYTES", "rope_frequencies", "rope_table", "rope_heads", "cache_gather", "ChunkPlan", "plan_chunks",
@@ -344,8 +344,8 @@ def _chunk(q, kv, block_table, pl, softmax_scale, status, stream, out=None, lse=
         raise ValueError("the plan was made for another batch")
     plan, ws, st = pl.plan, pl.workspace, _p(status, _INT32, 1, dev, "status")
     if out is None and code == DTYPE_FP8_RECORD and total_q * h_q > 128:
-        # room for the pages of requests of several row blocks, converted once (at most 1.2 GB)
-        room = min(batch * max_pages, pages, 1 << 14) * CHUNK_PAGE_BYTES
+        # room for the requests' pages, converted once (at most 1.1 GB)
+        room = min(batch * max_pages, 1 << 13) * CHUNK_PAGE_BYTES
         ws = torch.empty(mla_chunk_workspace_bytes(pl.num_parts) + room, dtype=_UINT8, device=q.device)
     plan_ptr, ws_ptr = _p(plan, _UINT8, 1, dev, "plan"), _p(ws, _UINT8, 1, dev, "workspace")
     queue = _q(stream, dev)

@@ -38,6 +38,7 @@
 
 #include <algorithm>
 
+#include "mla_serving.h"
 #include "common.cuh"
 #include "ptx.cuh"
 #include "serving.cuh"
@@ -58,6 +59,14 @@ constexpr int kBN = 128;                   // keys of a tile: two pages
 constexpr int kSlices = kDqk / 64;
 constexpr int kSliceBytes = 64 * 128;      // 64 rows or keys x 64 dims
 constexpr int kKSlices = 3;                // slices of a K stage
+// Over FP8 records a key is the sum of two bf16: the product of code and scale
+// rounded (its value, too), and what that leaves, 16 bits in all.  (Scores of the
+// first alone are off by 2^-9 of their products: lse by 1e-5 of itself, the output by
+// half its own rounding.)  Eight slices more a key, behind its nine.
+constexpr int kLowSlices = 8;
+constexpr int kPairRow = 64 * (kSlices + kLowSlices);  // elements of a converted row
+template <bool kFp8>
+constexpr int kChunks = kFp8 ? 6 : 3;      // K stages a tile
 constexpr int kKBytes = kKSlices * kSliceBytes;
 constexpr int kKStages = 3;
 constexpr int kVBytes = 4 * kSliceBytes;   // a page's 64 keys x this CTA's 256 dims
@@ -86,7 +95,7 @@ constexpr int kOffMisc = kOffBar + kNumBars * 8;
 constexpr int kOffRow = (kOffMisc + 16 + 15) / 16 * 16;  // [2][4 parts][64 rows]: maxima of a tile, or sums
 constexpr int kSmemBytes = kOffRow + 2 * 4 * kCtaRows * 4;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
-static_assert(kKSlices * 3 == kSlices, "three K stages a tile");
+static_assert(kKSlices * 3 == kSlices && kKSlices * 3 > kLowSlices && kPairRow * kTile * 2 == MLA_CHUNK_PAGE_BYTES, "K stages a tile");
 
 // Warps: 0 .. 7 softmax, then these.  16-bit caches: one warp each loads K and V
 // by TMA; FP8 records: four each convert them.
@@ -243,13 +252,28 @@ __device__ __forceinline__ uint32_t scaled2(uint32_t two, float scale) {
   return pack2<false>(f.x * scale, f.y * scale);
 }
 
+// What that leaves of the fp32 product, as bf16.
+__device__ __forceinline__ uint32_t rest2(uint32_t two, float scale) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  const float2 x = make_float2(f.x * scale, f.y * scale);
+  const __nv_bfloat162 hi = __floats2bfloat162_rn(x.x, x.y);
+  const float2 y = __bfloat1622float2(hi);
+  // (an infinite or missing product leaves nothing)
+  return pack2<false>(isfinite(y.x) ? x.x - y.x : 0.f, isfinite(y.y) ? x.y - y.y : 0.f);
+}
+
 // 16 codes into the two 16-byte chunks from `chunk` on of a swizzled 128-byte row.
+template <bool kRest>
 __device__ __forceinline__ void store_codes(uint8_t* row, uint32_t chunk, uint32_t swz, const uint4& codes,
                                             float scale) {
   const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
   uint32_t o[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) o[i] = scaled2(w[i >> 1] >> (16 * (i & 1)) & 0xffffu, scale);
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t two = w[i >> 1] >> (16 * (i & 1)) & 0xffffu;
+    o[i] = kRest ? rest2(two, scale) : scaled2(two, scale);
+  }
   *reinterpret_cast<uint4*>(row + ((chunk ^ swz) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
   *reinterpret_cast<uint4*>(row + (((chunk + 1) ^ swz) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
 }
@@ -277,8 +301,8 @@ __device__ __forceinline__ bool converted(const ChunkParams& p, const Unit& unit
   return unit.pages0 >= 0 && p.conv[unit.req + 1] <= p.room;
 }
 
-// Converts K pages: three stages of three slices a tile, the last slice the RoPE
-// part.  A piece of the next tile is loaded as soon as this tile's is converted, so
+// Converts K pages: six stages of three slices a tile, the ninth slice the RoPE part
+// and the 18th nothing.  A piece of the next tile is loaded as soon as this tile's is converted, so
 // that a whole tile's loads are in flight (with a stage's alone the loads' latency
 // came with every stage: 3.5 us a tile).
 template <bool kStall>
@@ -298,7 +322,7 @@ __device__ __forceinline__ bool convert_k(const ChunkParams& p, const Run& run, 
       for (int j = w.lo; j < w.hi && ok; ++j) {
         const int k = 2 * j + static_cast<int>(rank);
         if (lane == 0)
-          for (int c = 0; c < 3 && ok; ++c) {
+          for (int c = 0; c < kChunks<true> && ok; ++c) {
             const int s = static_cast<int>((n + c) % kKStages), r = static_cast<int>((n + c) / kKStages);
             if (r >= 1) ok = mbar_wait(&bars[K_EMPTY + s], (r - 1) & 1, abort_flag, wait_ns);
             if (!ok || (kStall && rank == 0 && n + c == 0)) continue;
@@ -309,7 +333,7 @@ __device__ __forceinline__ bool convert_k(const ChunkParams& p, const Run& run, 
               mbar_arrive_remote_relaxed(bar0 + 8 * (K_FULL + s));
             }
           }
-        n += 3;
+        n += kChunks<true>;
         ok = __shfl_sync(0xffffffffu, ok, 0);
       }
       continue;
@@ -335,24 +359,26 @@ __device__ __forceinline__ bool convert_k(const ChunkParams& p, const Run& run, 
       if (j + 1 < w.hi) rec = record_at(p, page_at(j + 1), me.key);
       const float4 next_scale = __ldcg(reinterpret_cast<const float4*>(rec + 512));
 #pragma unroll
-      for (int c = 0; c < 3; ++c, ++n) {
+      for (int c = 0; c < kChunks<true>; ++c, ++n) {
         const int s = static_cast<int>(n % kKStages), r = static_cast<int>(n / kKStages);
         if (ok && r >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&bars[K_EMPTY + s], (r - 1) & 1, abort_flag, wait_ns));
         uint8_t* row = sK + s * kKBytes + me.key * 128;
 #pragma unroll
-        for (int i = 3 * c; i < 3 * c + 3; ++i, row += kSliceBytes) {
+        for (int i = 3 * (c % 3); i < 3 * (c % 3) + 3; ++i, row += kSliceBytes) {
           const uint32_t chunk = static_cast<uint32_t>(2 * me.quarter);
+          const float sc = i < 2 ? scale.x : i < 4 ? scale.y : i < 6 ? scale.z : scale.w;
           if (i < 8) {
-            const float sc = i < 2 ? scale.x : i < 4 ? scale.y : i < 6 ? scale.z : scale.w;
-            if (have) store_codes(row, chunk, me.swz, raw[i], sc);
-          } else {
+            if (have && c < 3) store_codes<false>(row, chunk, me.swz, raw[i], sc);
+            if (have && c >= 3) store_codes<true>(row, chunk, me.swz, raw[i], sc);
+            if (c >= 3) raw[i] = load(rec, i);
+          } else if (c < 3) {
             if (have) {
               *reinterpret_cast<uint4*>(row + ((chunk ^ me.swz) << 4)) = raw[8];
               *reinterpret_cast<uint4*>(row + (((chunk + 1) ^ me.swz) << 4)) = raw[9];
             }
+            raw[8] = load(rec, 8);
             raw[9] = load(rec, 9);
           }
-          raw[i] = load(rec, i);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -432,7 +458,7 @@ __device__ __forceinline__ bool convert_v(const ChunkParams& p, const Run& run, 
 #pragma unroll
         for (int i = 0; i < 4; ++i, row += kSliceBytes) {
           if (mine) {
-            store_codes(row, chunk, me.swz, raw[h][i], i < 2 ? sc.x : sc.y);
+            store_codes<false>(row, chunk, me.swz, raw[h][i], i < 2 ? sc.x : sc.y);
           } else {
             *reinterpret_cast<uint4*>(row + ((chunk ^ me.swz) << 4)) = make_uint4(0u, 0u, 0u, 0u);
             *reinterpret_cast<uint4*>(row + (((chunk + 1) ^ me.swz) << 4)) = make_uint4(0u, 0u, 0u, 0u);
@@ -678,17 +704,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
         for (int j = lo; j < hi && ok; ++j) {
           const uint32_t s_col = tm + kTmemS + 64u * (tn & 1);
 #pragma unroll
-          for (int c = 0; c < 3; ++c, ++kn) {
+          for (int c = 0; c < kChunks<kFp8>; ++c, ++kn) {
             const int ks = static_cast<int>(kn % kKStages);
             if (ok) ok = wait(K_FULL + ks, (kn / kKStages) & 1);
             if (!ok) break;
             if (c == 0) MLA_TRACE(2, tn);
-            if (c == 2) MLA_TRACE(6, tn);
+            if (c == kChunks<kFp8> - 1) MLA_TRACE(6, tn);
             tc_fence_after();
             const uint64_t kd = k_desc + static_cast<uint64_t>((ks * kKBytes) >> 4);
-            const uint64_t qd = q_desc + static_cast<uint64_t>((c * kKBytes) >> 4);
+            const uint64_t qd = q_desc + static_cast<uint64_t>((c % 3 * kKBytes) >> 4);
 #pragma unroll
-            for (int s = 0; s < kKSlices; ++s)
+            for (int s = 0; s < (c == 5 ? kLowSlices % kKSlices : kKSlices); ++s)
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
                 umma2_f16_warp(s_col, qd + static_cast<uint64_t>((s * kSliceBytes + kk * 32) >> 4),
@@ -965,7 +991,7 @@ __global__ void __launch_bounds__(256) chunk_convert_kernel(const ChunkParams p,
     if (!good && threadIdx.x == 0) report(p.status, MLA_ERR_BAD_INDEX);
     const int row0 = 8 * warp;
     const uint8_t* rec = p.records + (static_cast<long long>(good ? page : 0) * kTile + row0) * MLA_RECORD_BYTES;
-    uint16_t* out = pages + (static_cast<long long>(i) * kTile + row0) * kDqk;
+    uint16_t* out = pages + (static_cast<long long>(i) * kTile + row0) * kPairRow;
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
       uint2 code[4][2];
@@ -984,7 +1010,7 @@ __global__ void __launch_bounds__(256) chunk_convert_kernel(const ChunkParams p,
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
         const bool live = good && row0 + 4 * half + n < keys;
-        uint4* o = reinterpret_cast<uint4*>(out + (4 * half + n) * kDqk);
+        uint4* o = reinterpret_cast<uint4*>(out + (4 * half + n) * kPairRow);
         const uint4 none = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -993,6 +1019,9 @@ __global__ void __launch_bounds__(256) chunk_convert_kernel(const ChunkParams p,
           o[32 * h + lane] = live ? make_uint4(scaled2(c.x & 0xffffu, sc), scaled2(c.x >> 16, sc),
                                                scaled2(c.y & 0xffffu, sc), scaled2(c.y >> 16, sc))
                                   : none;
+          o[72 + 32 * h + lane] = live ? make_uint4(rest2(c.x & 0xffffu, sc), rest2(c.x >> 16, sc),
+                                                    rest2(c.y & 0xffffu, sc), rest2(c.y >> 16, sc))
+                                       : none;
         }
         if (lane < 8) o[64 + lane] = live ? rope[n] : none;
       }

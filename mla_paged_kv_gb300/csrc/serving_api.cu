@@ -326,7 +326,7 @@ int chunk_attention(const void* d_q, const void* d_kv, const int32_t* d_block_ta
   bool convert = false;
   if (p.records) {
     const size_t sums = mla_chunk_workspace_bytes(num_parts);
-    const size_t room = (workspace_bytes - sums) / (2 * MLA_D_QK * MLA_PAGE_SIZE);
+    const size_t room = (workspace_bytes - sums) / MLA_CHUNK_PAGE_BYTES;
     p.room = static_cast<int>(std::min<size_t>(room, 1 << 30));
     pages = p.room > 0 ? static_cast<const char*>(d_workspace) + sums : d_workspace;
     map_pages = p.room > 0 ? p.room : 1;
@@ -334,8 +334,9 @@ int chunk_attention(const void* d_q, const void* d_kv, const int32_t* d_block_ta
     convert = p.room > 0 && static_cast<long long>(total_q) * h_q > MLA_ROWS_PER_BLOCK;
     if (!convert) p.room = 0;
   }
-  const cuuint64_t dims[4] = {64, MLA_PAGE_SIZE, MLA_D_QK / 64, static_cast<cuuint64_t>(map_pages)};
-  const cuuint64_t strides[3] = {2 * MLA_D_QK, 128, 2 * MLA_D_QK * MLA_PAGE_SIZE};
+  const cuuint64_t row = p.records ? MLA_CHUNK_PAGE_BYTES / MLA_PAGE_SIZE : 2 * MLA_D_QK;  // bytes
+  const cuuint64_t dims[4] = {64, MLA_PAGE_SIZE, row / 128, static_cast<cuuint64_t>(map_pages)};
+  const cuuint64_t strides[3] = {row, 128, row * MLA_PAGE_SIZE};
   const cuuint32_t k_box[4] = {64, 64, 3, 1}, v_box[4] = {64, 64, 4, 1};
   rc = encode_map16(&qm, d_q, 4, q_dims, q_strides, q_box);
   if (rc == MLA_OK) rc = encode_map16(&km, pages, 4, dims, strides, k_box);

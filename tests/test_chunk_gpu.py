@@ -10,9 +10,10 @@ truncation allowed for), and the exponential, the reference's rounding and the
 merge of pieces add 2^-20; both move weights, hence twice that on the output
 (numerator and sum).  lse moves by the score error plus 2^-19 (sum, log, merge)
 and one last place of its own value.  fp16 values below the smallest normal
-are off by at most 2^-25.  Over FP8 records the keys and values are, by the
-call's definition, the fp32 products of codes and scales rounded to bf16: the
-restatement takes those, and the bounds are bf16's.
+are off by at most 2^-25.  Over FP8 records a value is, by the call's definition,
+the fp32 product of code and scale rounded to bf16, and a key the sum of that and
+of its remainder in bf16: the restatement takes those, the bounds are bf16's, and
+a score's sum has the remainders' products too (1088 of them).
 """
 
 import math
@@ -64,21 +65,25 @@ class Case:
             codes = torch.where(torch.isfinite(c), (c / scale[..., None]).clamp(-448, 448), c).to(torch.float8_e4m3fn)
             self.cache = torch.cat([codes.view(torch.uint8).reshape(pages, 64, 512), scale.view(torch.uint8),
                                     r.contiguous().view(torch.uint8)], 2).contiguous()
-            value = (codes.float() * scale[..., None]).to(BF16).reshape(pages, 64, 512)
-            self.values = torch.cat([value, r], 2).double().numpy()
+            product = (codes.float() * scale[..., None]).reshape(pages, 64, 512)
+            value = product.to(BF16)
+            low = (product - value.float()).to(BF16)
+            self.values = torch.cat([value.double() + low.double(), r.double(), value.double()], 2).numpy()
 
     def keys(self):
+        """Keys, values and whether they are on a page of the pool, of each request."""
         rows = [so.request_keys(self.values, self.table[b], max(n, 0)) for b, n in enumerate(self.lens)]
-        return [r[0] for r in rows], [r[1] for r in rows]
+        return [r[0][:, :576] for r in rows], [r[0][:, -512:] if r[0].shape[1] > 576 else r[0][:, :512] for r in rows], \
+            [r[1] for r in rows]
 
     def device(self):
         return (self.q.cuda(), self.cache.cuda(), torch.from_numpy(self.table).cuda(), i32(self.lens), i32(self.cu))
 
     def check(self, out, lse, causal, scale=SCALE, fill=None):
         u, uo = U[self.q.dtype], U[out.dtype]
-        keys, seen = self.keys()
+        keys, values, seen = self.keys()
         want, wlse, mix, reach = so.chunk_attention(self.q.double().numpy(), keys, seen, self.cu, self.lens, causal,
-                                                    scale)
+                                                    scale, values)
         o, l = out.double().cpu().numpy(), lse.double().cpu().numpy()
         live = np.zeros(o.shape[0], dtype=bool)
         live[self.cu[0]:self.cu[-1]] = True
@@ -87,7 +92,7 @@ class Case:
         o, l, want, wlse, mix, reach = (x[live] for x in (o, l, want, wlse, mix, reach))
         none = np.isneginf(wlse)
         assert np.array_equal(np.isneginf(l), none) and not o[none].any()
-        score = 576 * 2.0 ** -23 * reach
+        score = (1088 if self.values.shape[2] > 576 else 576) * 2.0 ** -23 * reach
         half = self.q.dtype == FP16 or out.dtype == FP16
         tol = (u + 2 * score + 2.0 ** -19)[..., None] * mix + uo * np.abs(want) + (2.0 ** -25 * 8 if half else 0)
         assert np.isfinite(o).all() and np.all(np.abs(o - want) <= tol), np.max(np.abs(o - want) / tol)
@@ -270,12 +275,24 @@ def test_agrees_with_decode():
     assert float((lse - rlse[:, 0]).abs().max()) < 1e-3
 
 
-def test_records_are_the_rows_that_the_gather_gives():
-    """Over FP8 records the call is, to the bit, the one over a 16-bit cache of the gathered rows."""
+def test_records_against_the_rows_that_the_gather_gives():
+    """Over FP8 records scores have more bits than over a 16-bit cache of the gathered rows: lse is nearer the products'
+    own, by far; the outputs, whose values are the same, agree within what the keys' rounding moves weights by."""
     c = Case([5, 2, 30], [130, 600, 64], heads=16, seed=41, fp8=True)
     q, cache, table, lens, cu = c.device()
     pages = torch.arange(cache.shape[0], dtype=torch.int32, device="cuda")
     rows = mla.cache_gather(cache, pages[None], i32([0, 64 * cache.shape[0]]), 64 * cache.shape[0])
     out, lse = mla.chunk_attention(q, cache, table, lens, cu)
-    want = mla.chunk_attention(q, rows.view(-1, 64, 576), table, lens, cu)
-    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    coarse = mla.chunk_attention(q, rows.view(-1, 64, 576), table, lens, cu)
+    exact = c.cache[..., :512].contiguous().view(torch.float8_e4m3fn).double().reshape(-1, 64, 4, 128) * \
+        c.cache[..., 512:528].contiguous().view(torch.float32).double()[..., None]
+    exact = np.concatenate([exact.reshape(-1, 64, 512).numpy(), c.cache[..., 528:].contiguous().view(BF16).double().numpy()], 2)
+    keys = [so.request_keys(exact, c.table[b], n) for b, n in enumerate(c.lens)]
+    want, wlse, _, _ = so.chunk_attention(c.q.double().numpy(), [k[0] for k in keys], [k[1] for k in keys], c.cu, c.lens,
+                                          True, SCALE)
+
+    def off(x, y):
+        return float(np.linalg.norm(x.double().cpu().numpy() - y) / np.linalg.norm(y))
+
+    assert off(lse, wlse) < 1e-6 < 4e-6 < off(coarse[1], wlse)
+    assert off(out, want) < off(coarse[0], want) < 4e-3
