@@ -352,13 +352,16 @@ int mla_cache_gather(const void* d_cache, int cache_dtype, int num_pages, const 
  * A query that sees no key gets out = 0, lse = -inf.  Rows of the outputs outside
  * every chunk are left as they were.  Softmax weights are rounded to the cache's
  * type (bf16 over FP8 records) for the product with the values and divided by the
- * sum of the unrounded ones; statistics and sums are fp32.  Over FP8 records a
- * value is code x scale rounded to bf16, what mla_cache_gather gives, and a key
- * that and its remainder in bf16, 16 bits of the product.
+ * sum of the unrounded ones; statistics and sums are fp32.  Over FP8 records scores
+ * are those of the products code x scale: each group's codes times the query's, a
+ * query as two E4M3 numbers (exact down to 2^-9 of its largest latent element;
+ * smaller elements are off by 2^-17 of that one), times the scale in fp32.  Values
+ * are the products rounded to bf16.
  *
  * num_parts: pairs of CTAs that share the work; mla_chunk_num_parts gives as many
  * as the device runs at once (>= 1, or a negative mla_status_t).  At most 1024. */
-#define MLA_CHUNK_PAGE_BYTES (64 * 1088 * 2)
+#define MLA_CHUNK_PAGE_BYTES (64 * 512 * 2)
+#define MLA_CHUNK_QUERY_BYTES 1040
 int mla_chunk_num_parts(void);
 size_t mla_chunk_plan_bytes(int batch, int total_q, int h_q, int num_parts); /* 0: sizes out of range */
 size_t mla_chunk_workspace_bytes(int num_parts);
@@ -383,10 +386,11 @@ int mla_chunk_get_plan(const int32_t* d_cu_seqlens_q, const int32_t* d_cache_seq
  *   d_cu_seqlens_q, d_cache_seqlens  compared with the plan's on the device:
  *                 MLA_ERR_STALE_PLAN where one is another than the plan was made
  *                 for; the results are those of the plan.  NULL: not compared
- *   d_workspace   >= mla_chunk_workspace_bytes(num_parts).  Over FP8 records every
- *                 further MLA_CHUNK_PAGE_BYTES hold a page of the requests, in
- *                 order, converted once; requests that do not fit are converted by
- *                 each 128-row block that reads them (two to three times slower, the
+ *   d_workspace   >= mla_chunk_workspace_bytes(num_parts), over FP8 records and
+ *                 total_q * h_q times MLA_CHUNK_QUERY_BYTES.  There every further
+ *                 MLA_CHUNK_PAGE_BYTES hold the values of a page, converted once
+ *                 for requests of several 128-row blocks, in order; those that do
+ *                 not fit are converted by each block that reads them (slower, the
  *                 same results)
  *   d_out         [total_q, h_q, 512] of out_type (bf16, fp16 or fp32), d_lse fp32
  *                 [total_q, h_q]

@@ -26,11 +26,12 @@ import torch
 from . import DTYPE_FP8_RECORD, _DTYPE_CODE, _check, check_status, load_library, MlaError
 from .serving import (_D, _DTYPE_CODE16, _FP32, _INT32, _UINT8, _call, _p, _q, _status, _words)
 
-CHUNK_PAGE_BYTES = 64 * 1088 * 2  # of a page that a call over FP8 records converts (MLA_CHUNK_PAGE_BYTES)
+CHUNK_PAGE_BYTES = 64 * 512 * 2  # of a page whose values a call over FP8 records converts (MLA_CHUNK_PAGE_BYTES)
+CHUNK_QUERY_BYTES = 1040  # of a query head in the workspace of such a call (MLA_CHUNK_QUERY_BYTES)
 ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "wavelength": 4}
 
-__all__ = ["ROPE_SCALING", "CHUNK_PAGE_BYTES", "rope_frequencies", "rope_table", "rope_heads", "cache_gather", "ChunkPlan", "plan_chunks",
-           "chunk_attention"]
+__all__ = ["ROPE_SCALING", "CHUNK_PAGE_BYTES", "CHUNK_QUERY_BYTES", "rope_frequencies", "rope_table", "rope_heads",
+           "cache_gather", "ChunkPlan", "plan_chunks", "chunk_workspace", "chunk_attention"]
 
 _ROPE_HEADS, _GATHER, _CHUNK = _words(10, "22qd8q"), _words(11, "13q"), _words(12, "9qd12q")
 
@@ -343,10 +344,9 @@ def _chunk(q, kv, block_table, pl, softmax_scale, status, stream, out=None, lse=
     if pl.batch != batch or pl.total_q != total_q or pl.h_q != h_q:
         raise ValueError("the plan was made for another batch")
     plan, ws, st = pl.plan, pl.workspace, _p(status, _INT32, 1, dev, "status")
-    if out is None and code == DTYPE_FP8_RECORD and total_q * h_q > 128:
-        # room for the requests' pages, converted once (at most 1.1 GB)
-        room = min(batch * max_pages, 1 << 13) * CHUNK_PAGE_BYTES
-        ws = torch.empty(mla_chunk_workspace_bytes(pl.num_parts) + room, dtype=_UINT8, device=q.device)
+    if out is None and code == DTYPE_FP8_RECORD:
+        # room for values that are converted once for several row blocks (at most 0.5 GB)
+        ws = chunk_workspace(pl, min(batch * max_pages, 1 << 13) if total_q * h_q > 256 else 0)
     plan_ptr, ws_ptr = _p(plan, _UINT8, 1, dev, "plan"), _p(ws, _UINT8, 1, dev, "workspace")
     queue = _q(stream, dev)
     if out is None:
@@ -406,6 +406,13 @@ def plan_chunks(cu_seqlens_q, cache_seqlens, total_q, h_q, causal=True, num_part
     if status is None:
         check_status(st, "mla_chunk_get_plan")
     return ChunkPlan(plan, cache_seqlens.shape[0], int(total_q), int(h_q), parts, bool(causal), ws)
+
+
+def chunk_workspace(pl, pages=0):
+    """The workspace of a call over FP8 records, with room for the values of `pages` pages: pl.workspace, which
+    mla_chunk_attention_fwd takes, is that of calls over 16-bit caches (chunk_attention makes its own)."""
+    size = mla_chunk_workspace_bytes(pl.num_parts) + pl.total_q * pl.h_q * CHUNK_QUERY_BYTES + pages * CHUNK_PAGE_BYTES
+    return torch.empty(size, dtype=_UINT8, device=pl.plan.device)
 
 
 def chunk_attention(q, kv, block_table, cache_seqlens, cu_seqlens_q, causal=True, softmax_scale=None, out_fp32=False,

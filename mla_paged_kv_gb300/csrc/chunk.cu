@@ -59,14 +59,20 @@ constexpr int kBN = 128;                   // keys of a tile: two pages
 constexpr int kSlices = kDqk / 64;
 constexpr int kSliceBytes = 64 * 128;      // 64 rows or keys x 64 dims
 constexpr int kKSlices = 3;                // slices of a K stage
-// Over FP8 records a key is the sum of two bf16: the product of code and scale
-// rounded (its value, too), and what that leaves, 16 bits in all.  (Scores of the
-// first alone are off by 2^-9 of their products: lse by 1e-5 of itself, the output by
-// half its own rounding.)  Eight slices more a key, behind its nine.
-constexpr int kLowSlices = 8;
-constexpr int kPairRow = 64 * (kSlices + kLowSlices);  // elements of a converted row
-template <bool kFp8>
-constexpr int kChunks = kFp8 ? 6 : 3;      // K stages a tile
+// FP8 records.  Keys are multiplied as the codes they are: a bf16 query has eight
+// significant bits, which two E4M3 numbers hold (four bits, and the remainder's
+// four), so that Q K^T is two kind::f8f6f4 MMAs a group, at twice the rate, and K
+// needs no conversion.  Each 128-dim group has a sum of its own, which the softmax
+// threads multiply by the key's scale in fp32; the RoPE part (bf16) has the fifth.
+// A query is scaled by a power of two that brings its largest element to 128 .. 256:
+// elements down to 2^-9 of that one are exact, smaller ones are off by 2^-17 of it.
+// Values are code x scale rounded to bf16.
+constexpr int kParts = 5;                         // sums of a score: four groups, RoPE
+constexpr int kQueryRow = MLA_CHUNK_QUERY_BYTES;  // 512 codes, the remainders', 2^f and 2^-f as fp32, 8 bytes of nothing
+constexpr int kFp8Stages = 8;                     // of K: one 64-key x 128-byte part of a page each
+constexpr int kOffScales = kSlices * kSliceBytes + kFp8Stages * kSliceBytes;  // [2][4 groups][128 keys]
+static_assert(MLA_CHUNK_PAGE_BYTES == 2 * MLA_D_V * MLA_PAGE_SIZE && kQueryRow % 16 == 0 && kQueryRow >= 2 * MLA_D_V + 8,
+              "a page's values and a query in the workspace");
 constexpr int kKBytes = kKSlices * kSliceBytes;
 constexpr int kKStages = 3;
 constexpr int kVBytes = 4 * kSliceBytes;   // a page's 64 keys x this CTA's 256 dims
@@ -76,16 +82,23 @@ constexpr int kOffK = kSlices * kSliceBytes;
 constexpr int kOffV = kOffK + kKStages * kKBytes;
 constexpr int kOffP = kOffV + kVStages * kVBytes;
 constexpr int kOffBar = kOffP + kPBytes;
+static_assert(kOffScales + 2 * 4 * kBN * 4 <= kOffV, "the scales lie behind the K stages");
 
 enum : int {
   Q_FULL = 0,
   Q_EMPTY,                        // the unit's last Q K^T is done
   K_FULL,                         // +stage
-  K_EMPTY = K_FULL + kKStages,    // +stage
-  V_FULL = K_EMPTY + kKStages,    // +stage
+  K_EMPTY = K_FULL + kFp8Stages,    // +stage
+  V_FULL = K_EMPTY + kFp8Stages,    // +stage
   V_EMPTY = V_FULL + kVStages,    // +stage
   S_FULL = V_EMPTY + kVStages,    // +buffer
-  P_FULL = S_FULL + 2,            // weights written, O rescaled (one arrival per softmax warp of both CTAs)
+  // FP8 records: the tile's first sum, and all five, read by all softmax warps of both CTAs; then a tile's scales
+  // written (+ tile & 1), and read by this CTA's softmax warps
+  S_FIRST = S_FULL + 4,
+  S_ALL,
+  SCALE_FULL,
+  SCALE_EMPTY = SCALE_FULL + 2,
+  P_FULL = SCALE_EMPTY + 2,       // weights written, O rescaled (one arrival per softmax warp of both CTAs)
   PV_DONE,                        // one completion a tile: P may be overwritten, O rescaled or read
   TAIL,                           // a V page whose last rows are to be zeroed has landed
   DRAIN,
@@ -95,15 +108,16 @@ constexpr int kOffMisc = kOffBar + kNumBars * 8;
 constexpr int kOffRow = (kOffMisc + 16 + 15) / 16 * 16;  // [2][4 parts][64 rows]: maxima of a tile, or sums
 constexpr int kSmemBytes = kOffRow + 2 * 4 * kCtaRows * 4;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
-static_assert(kKSlices * 3 == kSlices && kKSlices * 3 > kLowSlices && kPairRow * kTile * 2 == MLA_CHUNK_PAGE_BYTES, "K stages a tile");
+static_assert(kKSlices * 3 == kSlices, "three K stages a tile");
 
-// Warps: 0 .. 7 softmax, then these.  16-bit caches: one warp each loads K and V
-// by TMA; FP8 records: four each convert them.
-constexpr int kWarpMma = 8, kWarpQ = 9, kWarpK = 10;
+// Warps: 0 .. 7 softmax (with 16 and 16 keys a thread FP8 records took 5% longer),
+// then one each for MMAs, Q (FP8 records: and scales) and K.  16-bit caches: one for
+// V; FP8 records: kConverters convert it.
+constexpr int kSoftmax = 8, kWarpMma = 8, kWarpQ = 9, kWarpK = 10, kWarpV = 11;
 constexpr int kConverters = 8;
-constexpr int threads_of(bool fp8) { return 32 * (kWarpK + (fp8 ? 2 * kConverters : 2)); }
+constexpr int threads_of(bool fp8) { return 32 * (kWarpV + (fp8 ? kConverters : 1)); }
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTmemS = 256;  // two buffers of 64 columns
+constexpr uint32_t kTmemS = 256;  // two buffers of 64 columns; four for the sums over FP8 records
 constexpr float kTau = 8.0f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -155,17 +169,20 @@ struct Unit {
   int req;
   int len;     // keys that its last row sees
   int limit0;  // causal: keys that a row of the request's token 0 sees (may be below 1)
+  int pages0;  // its request's first page among those converted once for all of its units, or -1
+  // of one of the plan's two schedules (16-bit caches, FP8 records)
   int slot;    // first partial slot
   int parts;   // pieces it is cut into (1: none; 0: no keys)
-  int pages0;  // its request's first page among those converted once for all of its units, or -1
-  int whole;   // 1: one pair's as a whole (pair u % pairs); 0: in the list that is cut
+  bool whole;  // one pair's as a whole (pair u % pairs); else in the list that is cut
 };
-static_assert(sizeof(Unit) <= 4 * kChunkUnitInts, "three int4");
+constexpr int kPages0 = 6, kSchedule = 8, kWhole = 1 << 16;  // ints of a unit; a schedule's: slot, parts (+ kWhole)
+static_assert(kSchedule + 4 == kChunkUnitInts && kMaxChunkParts < kWhole, "three int4");
 
-__device__ __forceinline__ Unit load_unit(const int32_t* units, int u) {
-  const int4* e = reinterpret_cast<const int4*>(units + static_cast<long long>(u) * kChunkUnitInts);
-  const int4 a = e[0], b = e[1];
-  return Unit{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, e[2].x, e[2].y};
+__device__ __forceinline__ Unit load_unit(const ChunkParams& p, int u) {
+  const int32_t* at = p.units + static_cast<long long>(u) * kChunkUnitInts;
+  const int4 a = reinterpret_cast<const int4*>(at)[0], b = reinterpret_cast<const int4*>(at)[1];
+  const int2 c = reinterpret_cast<const int2*>(at + kSchedule)[p.schedule];
+  return Unit{a.x, a.y, a.z, a.w, b.x, b.y, b.z, c.x, c.y & (kWhole - 1), c.y >= kWhole};
 }
 
 __device__ __forceinline__ int pages_of(int len) { return (len + kTile - 1) / kTile; }
@@ -199,7 +216,7 @@ __device__ __forceinline__ Walk walk_begin(const Run& r) { return Walk{Unit{}, 0
 
 __device__ __forceinline__ bool walk_next(const ChunkParams& p, const Run& r, Walk& w) {
   while (w.u < r.units) {
-    w.unit = load_unit(p.units, w.u);
+    w.unit = load_unit(p, w.u);
     w.u += r.pairs;
     if (!w.unit.whole) continue;
     w.lo = 0;
@@ -207,7 +224,7 @@ __device__ __forceinline__ bool walk_next(const ChunkParams& p, const Run& r, Wa
     return true;
   }
   while (w.at < r.u1 || (w.at == r.u1 && r.t1 > 0)) {
-    w.unit = load_unit(p.units, p.rest[w.at]);
+    w.unit = load_unit(p, p.rest[w.at]);
     w.first = w.at == r.u0;
     w.lo = w.first ? r.t0 : 0;
     w.hi = w.at == r.u1 ? r.t1 : tiles_of(w.unit.len);
@@ -252,28 +269,14 @@ __device__ __forceinline__ uint32_t scaled2(uint32_t two, float scale) {
   return pack2<false>(f.x * scale, f.y * scale);
 }
 
-// What that leaves of the fp32 product, as bf16.
-__device__ __forceinline__ uint32_t rest2(uint32_t two, float scale) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  const float2 x = make_float2(f.x * scale, f.y * scale);
-  const __nv_bfloat162 hi = __floats2bfloat162_rn(x.x, x.y);
-  const float2 y = __bfloat1622float2(hi);
-  // (an infinite or missing product leaves nothing)
-  return pack2<false>(isfinite(y.x) ? x.x - y.x : 0.f, isfinite(y.y) ? x.y - y.y : 0.f);
-}
-
-// 16 codes into the two 16-byte chunks from `chunk` on of a swizzled 128-byte row.
-template <bool kRest>
+// 16 codes times their scale into the two 16-byte chunks from `chunk` on of a
+// swizzled 128-byte row.
 __device__ __forceinline__ void store_codes(uint8_t* row, uint32_t chunk, uint32_t swz, const uint4& codes,
                                             float scale) {
   const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
   uint32_t o[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t two = w[i >> 1] >> (16 * (i & 1)) & 0xffffu;
-    o[i] = kRest ? rest2(two, scale) : scaled2(two, scale);
-  }
+  for (int i = 0; i < 8; ++i) o[i] = scaled2(w[i >> 1] >> (16 * (i & 1)) & 0xffffu, scale);
   *reinterpret_cast<uint4*>(row + ((chunk ^ swz) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
   *reinterpret_cast<uint4*>(row + (((chunk + 1) ^ swz) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
 }
@@ -301,95 +304,6 @@ __device__ __forceinline__ bool converted(const ChunkParams& p, const Unit& unit
   return unit.pages0 >= 0 && p.conv[unit.req + 1] <= p.room;
 }
 
-// Converts K pages: six stages of three slices a tile, the ninth slice the RoPE part
-// and the 18th nothing.  A piece of the next tile is loaded as soon as this tile's is converted, so
-// that a whole tile's loads are in flight (with a stage's alone the loads' latency
-// came with every stage: 3.5 us a tile).
-template <bool kStall>
-__device__ __forceinline__ bool convert_k(const ChunkParams& p, const Run& run, uint32_t rank, int warp, int lane,
-                                          uint8_t* sK, const CUtensorMap* map, uint64_t* bars, uint32_t bar0,
-                                          volatile int* abort_flag, uint64_t wait_ns) {
-  const RecordLane me = record_lane(warp, lane);
-  Walk w = walk_begin(run);
-  uint32_t n = 0;  // stages so far
-  bool ok = true;
-  const uint64_t pol = policy_evict_last();
-  uint4 raw[10];  // eight slices of codes, then the RoPE slice's two chunks
-  while (ok && walk_next(p, run, w)) {
-    const int pages = pages_of(w.unit.len);
-    if (converted(p, w.unit)) {
-      // its pages lie in the workspace: one TMA load a stage, and an arrival of every warp's
-      for (int j = w.lo; j < w.hi && ok; ++j) {
-        const int k = 2 * j + static_cast<int>(rank);
-        if (lane == 0)
-          for (int c = 0; c < kChunks<true> && ok; ++c) {
-            const int s = static_cast<int>((n + c) % kKStages), r = static_cast<int>((n + c) / kKStages);
-            if (r >= 1) ok = mbar_wait(&bars[K_EMPTY + s], (r - 1) & 1, abort_flag, wait_ns);
-            if (!ok || (kStall && rank == 0 && n + c == 0)) continue;
-            if (warp == 0 && k < pages) {
-              mbar_arrive_expect_tx_remote_relaxed(bar0 + 8 * (K_FULL + s), kKBytes);
-              tma_load_4d_pair(sK + s * kKBytes, map, bar0 + 8 * (K_FULL + s), 0, 0, kKSlices * c, w.unit.pages0 + k, pol);
-            } else {
-              mbar_arrive_remote_relaxed(bar0 + 8 * (K_FULL + s));
-            }
-          }
-        n += kChunks<true>;
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-      }
-      continue;
-    }
-    int ids = 0, base = -32;
-    auto page_at = [&](int j) {  // this CTA's page of tile j
-      if (2 * j - base >= 32) {
-        base = 2 * j;
-        ids = page_window(p, w.unit, base, lane);
-      }
-      return __shfl_sync(0xffffffffu, ids, 2 * j + static_cast<int>(rank) - base);
-    };
-    auto load = [&](const uint8_t* rec, int i) {
-      const uint8_t* at = i < 8 ? rec + 64 * i + 16 * me.quarter : rec + 528 + 32 * me.quarter + 16 * (i - 8);
-      return __ldcg(reinterpret_cast<const uint4*>(at));
-    };
-    const uint8_t* rec = record_at(p, page_at(w.lo), me.key);
-    float4 scale = __ldcg(reinterpret_cast<const float4*>(rec + 512));
-#pragma unroll
-    for (int i = 0; i < 10; ++i) raw[i] = load(rec, i);
-    for (int j = w.lo; j < w.hi && ok; ++j) {
-      const bool have = 2 * j + static_cast<int>(rank) < pages;
-      if (j + 1 < w.hi) rec = record_at(p, page_at(j + 1), me.key);
-      const float4 next_scale = __ldcg(reinterpret_cast<const float4*>(rec + 512));
-#pragma unroll
-      for (int c = 0; c < kChunks<true>; ++c, ++n) {
-        const int s = static_cast<int>(n % kKStages), r = static_cast<int>(n / kKStages);
-        if (ok && r >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&bars[K_EMPTY + s], (r - 1) & 1, abort_flag, wait_ns));
-        uint8_t* row = sK + s * kKBytes + me.key * 128;
-#pragma unroll
-        for (int i = 3 * (c % 3); i < 3 * (c % 3) + 3; ++i, row += kSliceBytes) {
-          const uint32_t chunk = static_cast<uint32_t>(2 * me.quarter);
-          const float sc = i < 2 ? scale.x : i < 4 ? scale.y : i < 6 ? scale.z : scale.w;
-          if (i < 8) {
-            if (have && c < 3) store_codes<false>(row, chunk, me.swz, raw[i], sc);
-            if (have && c >= 3) store_codes<true>(row, chunk, me.swz, raw[i], sc);
-            if (c >= 3) raw[i] = load(rec, i);
-          } else if (c < 3) {
-            if (have) {
-              *reinterpret_cast<uint4*>(row + ((chunk ^ me.swz) << 4)) = raw[8];
-              *reinterpret_cast<uint4*>(row + (((chunk + 1) ^ me.swz) << 4)) = raw[9];
-            }
-            raw[8] = load(rec, 8);
-            raw[9] = load(rec, 9);
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0 && ok && !(kStall && rank == 0 && n == 0)) arrive_pair(bar0 + 8 * (K_FULL + s));
-      }
-      scale = next_scale;
-    }
-  }
-  return ok;
-}
-
 // Converts V pages: this CTA's 256 dims of both pages of a tile; keys behind the
 // unit's last one (and pages outside the pool) as zeros.  Two pages' loads in
 // flight.
@@ -409,17 +323,12 @@ __device__ __forceinline__ bool convert_v(const ChunkParams& p, const Run& run, 
     if (converted(p, w.unit)) {  // (rows behind the last key are zeros there)
       for (int k = 2 * w.lo; k < pages && ok; ++k, ++n) {
         const int s = static_cast<int>(n % kVStages), r = static_cast<int>(n / kVStages);
-        if (lane == 0) {
-          if (r >= 1) ok = mbar_wait(&bars[V_EMPTY + s], (r - 1) & 1, abort_flag, wait_ns);
-          if (ok && warp == 0) {
-            mbar_arrive_expect_tx_remote_relaxed(bar0 + 8 * (V_FULL + s), kVBytes);
-            tma_load_4d_pair(sV + s * kVBytes, map, bar0 + 8 * (V_FULL + s), 0, 0, 4 * static_cast<int>(rank),
-                             w.unit.pages0 + k, pol);
-          } else if (ok) {
-            mbar_arrive_remote_relaxed(bar0 + 8 * (V_FULL + s));
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (r >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&bars[V_EMPTY + s], (r - 1) & 1, abort_flag, wait_ns));
+        if (ok && warp == 0)
+          tma_load_4d_pair_warp(sV + s * kVBytes, map, bar0 + 8 * (V_FULL + s), kVBytes, 0, 0, 4 * static_cast<int>(rank),
+                                w.unit.pages0 + k, pol);
+        else if (ok && lane == 0)
+          mbar_arrive_remote_relaxed(bar0 + 8 * (V_FULL + s));
       }
       continue;
     }
@@ -458,7 +367,7 @@ __device__ __forceinline__ bool convert_v(const ChunkParams& p, const Run& run, 
 #pragma unroll
         for (int i = 0; i < 4; ++i, row += kSliceBytes) {
           if (mine) {
-            store_codes<false>(row, chunk, me.swz, raw[h][i], i < 2 ? sc.x : sc.y);
+            store_codes(row, chunk, me.swz, raw[h][i], i < 2 ? sc.x : sc.y);
           } else {
             *reinterpret_cast<uint4*>(row + ((chunk ^ me.swz) << 4)) = make_uint4(0u, 0u, 0u, 0u);
             *reinterpret_cast<uint4*>(row + (((chunk + 1) ^ me.swz) << 4)) = make_uint4(0u, 0u, 0u, 0u);
@@ -474,12 +383,48 @@ __device__ __forceinline__ bool convert_v(const ChunkParams& p, const Run& run, 
   return ok;
 }
 
+// The scales of a unit's tiles, in turn in two buffers of [4 groups][128 keys]:
+// lane i has keys 4 i .. of a tile, the next tile's loads in flight.  (Pages outside
+// the pool or past the last one: page 0's, whose scores are masked.)
+__device__ __forceinline__ bool stage_scales(const ChunkParams& p, const Walk& w, int lane, uint8_t* smem,
+                                             uint64_t* bars, volatile int* abort_flag, uint64_t wait_ns,
+                                             uint32_t& n) {
+  float4 key[4];
+  int ids = 0, base = -32;
+  auto load = [&](int j) {
+    if (2 * j - base >= 32) {
+      base = 2 * j;
+      ids = page_window(p, w.unit, base, lane);
+    }
+    const int page = __shfl_sync(0xffffffffu, ids, 2 * j + (lane >> 4) - base);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      key[i] = __ldcg(reinterpret_cast<const float4*>(record_at(p, page, 4 * (lane & 15) + i) + kDv));
+  };
+  bool ok = true;
+  load(w.lo);
+  for (int j = w.lo; j < w.hi && ok; ++j, ++n) {
+    if (n >= 2)
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars[SCALE_EMPTY + (n & 1)], ((n >> 1) - 1) & 1, abort_flag, wait_ns));
+    float4* to = reinterpret_cast<float4*>(smem + kOffScales) + (n & 1) * kBN + lane;
+    to[0] = make_float4(key[0].x, key[1].x, key[2].x, key[3].x);
+    to[kBN / 4] = make_float4(key[0].y, key[1].y, key[2].y, key[3].y);
+    to[2 * kBN / 4] = make_float4(key[0].z, key[1].z, key[2].z, key[3].z);
+    to[3 * kBN / 4] = make_float4(key[0].w, key[1].w, key[2].w, key[3].w);
+    __syncwarp();
+    if (lane == 0 && ok) mbar_arrive(&bars[SCALE_FULL + (n & 1)]);
+    if (j + 1 < w.hi) load(j + 1);
+  }
+  return ok;
+}
+
 constexpr uint64_t kStallWaitNs = 200000;  // wait budget of the stall-test instance, whose first K stage is never loaded
 
 template <bool kHalf, bool kFp8, bool kStall = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
     chunk_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
-                 const __grid_constant__ CUtensorMap v_map, const ChunkParams p) {
+                 const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap rope_map,
+                 const ChunkParams p) {
   constexpr uint64_t kWaitNs = kStall ? kStallWaitNs : MLA_WAIT_LIMIT_NS;
   const uint32_t rank = cluster_ctarank();
   extern __shared__ __align__(1024) uint8_t smem[];  // swizzle atoms need 1024-byte alignment
@@ -505,20 +450,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
   if (tid == 0) {
     *abort_flag = 0;
     // the barriers that MMAs wait for are the even CTA's and count both CTAs' parts
-    constexpr uint32_t kLoaders = 2 * (kFp8 ? kConverters : 1);
     mbar_init(&bars[Q_FULL], 2);
     mbar_init(&bars[Q_EMPTY], 1);
-    for (int i = 0; i < kKStages; ++i) {
-      mbar_init(&bars[K_FULL + i], kLoaders);
+    for (int i = 0; i < (kFp8 ? kFp8Stages : kKStages); ++i) {
+      mbar_init(&bars[K_FULL + i], 2);
       mbar_init(&bars[K_EMPTY + i], 1);
     }
     for (int i = 0; i < kVStages; ++i) {
-      mbar_init(&bars[V_FULL + i], kLoaders);
+      mbar_init(&bars[V_FULL + i], 2 * (kFp8 ? 8 : 1));
       mbar_init(&bars[V_EMPTY + i], 1);
     }
-    mbar_init(&bars[S_FULL], 1);
-    mbar_init(&bars[S_FULL + 1], 1);
-    mbar_init(&bars[P_FULL], 2 * 8);
+    for (int i = 0; i < 4; ++i) mbar_init(&bars[S_FULL + i], 1);
+    mbar_init(&bars[S_FIRST], 2 * kSoftmax);
+    mbar_init(&bars[S_ALL], 2 * kSoftmax);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars[SCALE_FULL + i], 1);
+      mbar_init(&bars[SCALE_EMPTY + i], kSoftmax);
+    }
+    mbar_init(&bars[P_FULL], 2 * kSoftmax);
     mbar_init(&bars[PV_DONE], 1);
     mbar_init(&bars[TAIL], 1);
     mbar_init(&bars[DRAIN], 1);
@@ -545,14 +494,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
   if (tid == 0) MLA_TRACE(0, 1);
   Walk w = walk_begin(run);
 
-  if (kFp8 && warp >= kWarpK) {
-    // ------------------------------------------------------------ FP8 records: K or V converted
+  if (kFp8 && warp >= kWarpV) {
+    // ------------------------------------------------------------ FP8 records: V converted
     const uint32_t bar0 = mapa_shared(smem_u32(bars), 0);
     pdl_wait_prior_grid();  // the pages that are converted before
-    const bool ok = warp < kWarpK + kConverters
-                        ? convert_k<kStall>(p, run, rank, warp - kWarpK, lane, sK, &k_map, bars, bar0, abort_flag, kWaitNs)
-                        : convert_v(p, run, rank, warp - kWarpK - kConverters, lane, sV, &v_map, bars, bar0, abort_flag,
-                                    kWaitNs);
+    const bool ok = convert_v(p, run, rank, warp - kWarpV, lane, sV, &v_map, bars, bar0, abort_flag, kWaitNs);
     if (!ok && lane == 0) {
       fail(abort_flag, p.status);
       // copies in flight land (bounded) before this CTA may end
@@ -568,18 +514,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
     const uint32_t bar0 = mapa_shared(smem_u32(bars), 0);
     auto expect = [&](int bar, uint32_t bytes) { mbar_arrive_expect_tx_remote_relaxed(bar0 + 8 * bar, bytes); };
     uint32_t n = 0, tails = 0;  // stages (or units of Q) and tail pages so far
+    uint32_t scaled = 0;        // FP8 records: tiles whose scales are written
+    if (kFp8 && warp == kWarpQ) pdl_wait_prior_grid();  // the queries' codes
     while (ok && walk_next(p, run, w)) {
       if (warp == kWarpQ) {
-        if (lane == 0) {
-          if (n >= 1) ok = mbar_wait(&bars[Q_EMPTY], (n - 1) & 1, abort_flag, kWaitNs);
-          if (ok) {
-            expect(Q_FULL, kOffK);
-            tma_load_4d_pair(sQ, &q_map, bar0 + 8 * Q_FULL, 0, w.unit.row0 + kCtaRows * static_cast<int>(rank), 0, 0,
+        if (n >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&bars[Q_EMPTY], (n - 1) & 1, abort_flag, kWaitNs));
+        if (ok && lane == 0) {
+          expect(Q_FULL, kOffK);
+          const int row0 = w.unit.row0 + kCtaRows * static_cast<int>(rank);
+          tma_load_4d_pair(sQ, &q_map, bar0 + 8 * Q_FULL, 0, row0, 0, 0, pol_q);
+          if (kFp8)
+            tma_load_4d_pair(sQ + (kSlices - 1) * kSliceBytes, &rope_map, bar0 + 8 * Q_FULL, 0, row0, kSlices - 1, 0,
                              pol_q);
-          }
         }
         ++n;
-        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (kFp8 && ok) ok = stage_scales(p, w, lane, smem, bars, abort_flag, kWaitNs, scaled);
         continue;
       }
       const int pages = pages_of(w.unit.len);
@@ -592,20 +541,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
         if (warp == kWarpK) {
           const int k = 2 * j + static_cast<int>(rank);
           const int page = max(__shfl_sync(0xffffffffu, ids, k - base), 0);
-          if (lane == 0)
-            for (int c = 0; c < 3 && ok; ++c) {
-              const int s = static_cast<int>((n + c) % kKStages), r = static_cast<int>((n + c) / kKStages);
-              if (r >= 1) ok = mbar_wait(&bars[K_EMPTY + s], (r - 1) & 1, abort_flag, kWaitNs);
-              if (!ok || (kStall && rank == 0 && n + c == 0)) continue;
-              if (k < pages) {
-                expect(K_FULL + s, kKBytes);
-                tma_load_4d_pair(sK + s * kKBytes, &k_map, bar0 + 8 * (K_FULL + s), 0, 0, kKSlices * c, page, pol_kv);
-              } else {  // no such page: whatever the stage holds is masked
-                mbar_arrive_remote_relaxed(bar0 + 8 * (K_FULL + s));
-              }
+          constexpr int kStages = kFp8 ? kFp8Stages : kKStages, kLoads = kFp8 ? kParts : 3;
+          constexpr int kBytes = kFp8 ? kSliceBytes : kKBytes;
+          // (the whole warp, of which one lane issues)
+          for (int c = 0; c < kLoads && ok; ++c, ++n) {
+            const int s = static_cast<int>(n % kStages), r = static_cast<int>(n / kStages);
+            if (r >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&bars[K_EMPTY + s], (r - 1) & 1, abort_flag, kWaitNs));
+            if (!ok || (kStall && rank == 0 && n == 0)) continue;
+            if (k < pages) {
+              // FP8 records, in 16-bit units: 128 codes, the last time the 64 RoPE dims (from byte 528 on)
+              const int x = !kFp8 ? 0 : c < 4 ? 64 * c : 264, slice = kFp8 ? 0 : kKSlices * c;
+              tma_load_4d_pair_warp(sK + s * kBytes, &k_map, bar0 + 8 * (K_FULL + s), kBytes, x, 0, slice, page, pol_kv);
+            } else if (lane == 0) {  // no such page: whatever the stage holds is masked
+              mbar_arrive_remote_relaxed(bar0 + 8 * (K_FULL + s));
             }
-          n += 3;
-          ok = __shfl_sync(0xffffffffu, ok, 0);
+          }
           continue;
         }
         for (int half = 0; half < 2 && ok; ++half) {
@@ -615,18 +565,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
           const int keep = id < 0 ? 0 : w.unit.len - k * kTile;  // rows of the page that are keys
           const int s = static_cast<int>(n % kVStages), r = static_cast<int>(n / kVStages);
           uint8_t* dst = sV + s * kVBytes;
-          if (lane == 0) {
-            if (r >= 1) ok = mbar_wait(&bars[V_EMPTY + s], (r - 1) & 1, abort_flag, kWaitNs);
-            if (ok && keep < kTile) {  // onto this CTA's own barrier
-              mbar_arrive_expect_tx(&bars[TAIL], kVBytes);
-              tma_load_4d(dst, &v_map, &bars[TAIL], 0, 0, 4 * static_cast<int>(rank), page, pol_kv);
-            } else if (ok) {
-              expect(V_FULL + s, kVBytes);
-              tma_load_4d_pair(dst, &v_map, bar0 + 8 * (V_FULL + s), 0, 0, 4 * static_cast<int>(rank), page, pol_kv);
-            }
+          if (r >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&bars[V_EMPTY + s], (r - 1) & 1, abort_flag, kWaitNs));
+          if (ok && keep >= kTile) {
+            tma_load_4d_pair_warp(dst, &v_map, bar0 + 8 * (V_FULL + s), kVBytes, 0, 0, 4 * static_cast<int>(rank), page,
+                                  pol_kv);
+          } else if (ok && lane == 0) {  // onto this CTA's own barrier
+            mbar_arrive_expect_tx(&bars[TAIL], kVBytes);
+            tma_load_4d(dst, &v_map, &bars[TAIL], 0, 0, 4 * static_cast<int>(rank), page, pol_kv);
           }
           ++n;
-          ok = __shfl_sync(0xffffffffu, ok, 0);
           if (!ok || keep >= kTile) continue;
           ok = __all_sync(0xffffffffu, mbar_wait(&bars[TAIL], tails & 1, abort_flag, kWaitNs));
           ++tails;
@@ -657,6 +604,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
     if (rank == 0) {
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       constexpr uint32_t idesc_qk = idesc_16bit_f32(128, kBN, false, kHalf);
+      constexpr uint32_t idesc_codes = idesc_e4m3_f32(128, kBN);
       constexpr uint32_t idesc_pv = idesc_16bit_f32(128, 256, true, kHalf);
       const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024);
       const uint64_t k_desc = sdesc_sw128(smem_u32(sK), 16, 1024);
@@ -682,12 +630,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
           const uint64_t pd = p_desc + static_cast<uint64_t>((half * kSliceBytes) >> 4);
           const bool first = fresh && half == 0;
 #pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)
-#pragma unroll
-            for (int d = 0; d < 2; ++d)
-              umma2_f16_warp(tm + 128u * d, pd + static_cast<uint64_t>((kk * 32) >> 4),
-                             vd + static_cast<uint64_t>((2 * d * kSliceBytes + kk * 2048) >> 4), idesc_pv,
-                             (first && kk == 0) ? 0u : 1u);
+          for (int d = 0; d < 2; ++d)
+            umma2_f16_warp4<2, 128>(tm + 128u * d, pd, vd + static_cast<uint64_t>((2 * d * kSliceBytes) >> 4), idesc_pv,
+                                    first ? 0u : 1u);
           umma2_commit_warp(&bars[V_EMPTY + vs]);
         }
         if (ok) umma2_commit_warp(&bars[PV_DONE]);
@@ -702,30 +647,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
         MLA_TRACE(1, qn);
         ++qn;
         for (int j = lo; j < hi && ok; ++j) {
-          const uint32_t s_col = tm + kTmemS + 64u * (tn & 1);
+          if constexpr (kFp8) {
 #pragma unroll
-          for (int c = 0; c < kChunks<kFp8>; ++c, ++kn) {
-            const int ks = static_cast<int>(kn % kKStages);
-            if (ok) ok = wait(K_FULL + ks, (kn / kKStages) & 1);
-            if (!ok) break;
-            if (c == 0) MLA_TRACE(2, tn);
-            if (c == kChunks<kFp8> - 1) MLA_TRACE(6, tn);
-            tc_fence_after();
-            const uint64_t kd = k_desc + static_cast<uint64_t>((ks * kKBytes) >> 4);
-            const uint64_t qd = q_desc + static_cast<uint64_t>((c % 3 * kKBytes) >> 4);
+            for (int c = 0; c < kParts; ++c, ++kn) {  // a sum each, in four buffers
+              // the fifth waits until the softmax warps have begun with this tile: the P V that they wait for goes first
+              if (c == 4 && before > 0) issue_pv();
+              if (ok && c == 0 && tn >= 1) ok = wait(S_ALL, (tn - 1) & 1);
+              if (ok && c == 4) ok = wait(S_FIRST, tn & 1);
+              const int ks = static_cast<int>(kn % kFp8Stages);
+              if (ok) ok = wait(K_FULL + ks, (kn / kFp8Stages) & 1);
+              if (!ok) break;
+              if (c == 0) MLA_TRACE(2, tn);
+              if (c == kParts - 1) MLA_TRACE(6, tn);
+              tc_fence_after();
+              const uint32_t s_col = tm + kTmemS + 64u * (kn & 3);
+              const uint64_t kd = k_desc + static_cast<uint64_t>((ks * kSliceBytes) >> 4);
 #pragma unroll
-            for (int s = 0; s < (c == 5 ? kLowSlices % kKSlices : kKSlices); ++s)
+              for (int h = 0; h < (c < 4 ? 2 : 1); ++h) {  // codes, remainders
+                const int slice = c < 4 ? c + 4 * h : kSlices - 1;
+                const uint64_t qd = q_desc + static_cast<uint64_t>((slice * kSliceBytes) >> 4);
+                if (c < 4)
+                  umma2_f8_warp4<2, 2>(s_col, qd, kd, idesc_codes, h);
+                else
+                  umma2_f16_warp4<2, 2>(s_col, qd, kd, idesc_qk, 0u);
+              }
+              umma2_commit_warp(&bars[S_FULL + (kn & 3)]);
+              umma2_commit_warp(&bars[K_EMPTY + ks]);
+            }
+          } else {
+            const uint32_t s_col = tm + kTmemS + 64u * (tn & 1);
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                umma2_f16_warp(s_col, qd + static_cast<uint64_t>((s * kSliceBytes + kk * 32) >> 4),
-                               kd + static_cast<uint64_t>((s * kSliceBytes + kk * 32) >> 4), idesc_qk,
-                               (c == 0 && s == 0 && kk == 0) ? 0u : 1u);
-            umma2_commit_warp(&bars[K_EMPTY + ks]);
+            for (int c = 0; c < 3; ++c, ++kn) {
+              const int ks = static_cast<int>(kn % kKStages);
+              if (ok) ok = wait(K_FULL + ks, (kn / kKStages) & 1);
+              if (!ok) break;
+              if (c == 0) MLA_TRACE(2, tn);
+              if (c == 2) MLA_TRACE(6, tn);
+              tc_fence_after();
+              const uint64_t kd = k_desc + static_cast<uint64_t>((ks * kKBytes) >> 4);
+              const uint64_t qd = q_desc + static_cast<uint64_t>((c * kKBytes) >> 4);
+#pragma unroll
+              for (int s = 0; s < kKSlices; ++s)
+                umma2_f16_warp4<2, 2>(s_col, qd + static_cast<uint64_t>((s * kSliceBytes) >> 4),
+                                      kd + static_cast<uint64_t>((s * kSliceBytes) >> 4), idesc_qk,
+                                      (c == 0 && s == 0) ? 0u : 1u);
+              umma2_commit_warp(&bars[K_EMPTY + ks]);
+            }
           }
           if (!ok) break;
-          umma2_commit_warp(&bars[S_FULL + (tn & 1)]);
+          if (!kFp8) umma2_commit_warp(&bars[S_FULL + (tn & 1)]);
           if (j == hi - 1) umma2_commit_warp(&bars[Q_EMPTY]);
-          if (before > 0) issue_pv();
+          if (!kFp8 && before > 0) issue_pv();
           ++tn;
           before = min(pages - 2 * j, 2);
           fresh = j == lo;
@@ -749,8 +721,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
     const uint32_t s_addr = tmem + lane_base + kTmemS + 32u * ch;
     const uint32_t o_addr = tmem + lane_base + 128u * ch;
     const uint32_t row_bar = 1 + (q & 1);  // the four warps of these 32 rows
-    const uint32_t p_full = mapa_shared(smem_u32(&bars[P_FULL]), 0);
-    const float c_log2 = p.scale_log2;
+    const uint32_t p_full = mapa_shared(smem_u32(&bars[P_FULL]), 0), s_first = mapa_shared(smem_u32(&bars[S_FIRST]), 0);
     uint8_t* prow = sP + kh * kSliceBytes + r * 128;
     const uint32_t swz = static_cast<uint32_t>(r & 7);
     // What this thread has for its row, to be shared with the other three.  (Two
@@ -764,11 +735,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
       return buf;
     };
     bool ok = true;
-    uint32_t tn = 0;
+    uint32_t tn = 0, sn = 0;
     // what the tile loop keeps of a unit: the keys this row sees (rows past the unit's last one: unmasked, not
     // stored), the block table's row, and its pages outside the pool within the window from page `base` on
     int limit, base;
     uint32_t bad;
+    float c_log2 = p.scale_log2;  // FP8 records: times 2^-f, the scores being 2^f as large
+    float up = 1.f;               // 2^f of this row's query
+    float2 factor;                // of the unit that is entered: 2^f and 2^-f
+    const float* const sScale = reinterpret_cast<const float*>(smem + kOffScales) + kTile * kh + 32 * ch;
     auto look = [&](int page) {
       base = page;
       const int k = base + lane;
@@ -785,24 +760,73 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
               : causal           ? min(w.unit.len, w.unit.limit0 + (w.unit.rel + row) / p.h_q)
                                  : w.unit.len;
       look(2 * w.lo);
+      if constexpr (kFp8) {
+        // (the row after the unit's last one is another unit's, or none)
+        const int at = w.unit.row0 + min(row, w.unit.rows - 1);
+        factor = *reinterpret_cast<const float2*>(p.queries + static_cast<long long>(at) * kQueryRow + 2 * kDv);
+      }
       return true;
     };
+    if (kFp8) pdl_wait_prior_grid();  // the queries' factors
     bool more = enter();
     while (more) {
       float ref = -INFINITY, l = 0.f;
+      if constexpr (kFp8) {
+        up = factor.x;
+        c_log2 = p.scale_log2 * factor.y;
+      }
       for (int j = w.lo; j < w.hi; ++j, ++tn) {
-        if (2 * j - base >= 32) look(2 * j);
-        ok = __all_sync(0xffffffffu, ok && mbar_wait(&bars[S_FULL + (tn & 1)], (tn >> 1) & 1, abort_flag, kWaitNs));
-        if (tid == 0) MLA_TRACE(7, tn);
-        tc_fence_after();
-        float s[32], top;
-        tmem_ld32_max(s_addr + 64u * (tn & 1), s, top);
-        tmem_wait_ld();
         int seen = limit - j * kBN - kTile * kh - 32 * ch;
+        if (2 * j - base >= 32) look(2 * j);
         if ((bad >> (2 * j + kh - base)) & 1u) seen = 0;
         // (pages past the unit's last one have keys past every valid row's limit; rows past its last row are masked
         // there too, for what the stage holds may be no number)
         if (row >= w.unit.rows && (2 * j + kh) * kTile >= w.unit.len) seen = 0;
+        float s[32], top;
+        if constexpr (kFp8) {
+          const float* scales = sScale + (tn & 1) * 4 * kBN;
+          ok = ok && mbar_wait(&bars[SCALE_FULL + (tn & 1)], (tn >> 1) & 1, abort_flag, kWaitNs);
+#pragma unroll
+          for (int n = 0; n < kParts; ++n, ++sn) {
+            ok = __all_sync(0xffffffffu, ok && mbar_wait(&bars[S_FULL + (sn & 3)], (sn >> 2) & 1, abort_flag, kWaitNs));
+            if (tid == 0 && n == 0) MLA_TRACE(7, tn);
+            tc_fence_after();
+            uint32_t v[32];
+            tmem_ld32(s_addr + 64u * (sn & 3), v);
+            tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0 && n == 0) mbar_arrive_remote_relaxed(s_first);
+            if (lane == 0 && n == kParts - 1) {
+              mbar_arrive_remote_relaxed(s_first + 8 * (S_ALL - S_FIRST));
+              mbar_arrive(&bars[SCALE_EMPTY + (tn & 1)]);
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const float4 f = n == kParts - 1 ? make_float4(up, up, up, up)
+                                               : *reinterpret_cast<const float4*>(scales + kBN * n + i);
+              const float2 f2[2] = {make_float2(f.x, f.y), make_float2(f.z, f.w)};
+#pragma unroll
+              for (int k = i; k < i + 4; k += 2) {
+                const float2 y = make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+                const float2 z = n == 0 ? __fmul2_rn(y, f2[(k - i) >> 1])
+                                        : __ffma2_rn(y, f2[(k - i) >> 1], make_float2(s[k], s[k + 1]));
+                s[k] = z.x;
+                s[k + 1] = z.y;
+              }
+            }
+          }
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], s[i]);
+          top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        } else {
+          ok = __all_sync(0xffffffffu, ok && mbar_wait(&bars[S_FULL + (tn & 1)], (tn >> 1) & 1, abort_flag, kWaitNs));
+          if (tid == 0) MLA_TRACE(7, tn);
+          tc_fence_after();
+          tmem_ld32_max(s_addr + 64u * (tn & 1), s, top);
+          tmem_wait_ld();
+        }
         if (__any_sync(0xffffffffu, seen < 32)) {
           const uint32_t keep = seen >= 32 ? ~0u : (seen <= 0 ? 0u : (1u << seen) - 1u);
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -965,16 +989,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
 
 // ------------------------------------------------------------------ convert
 
-// Pages of FP8 records as bf16 pages in the workspace, for the requests that fit:
-// every unit that reads them would convert them again, and take 3.8 us a tile where
-// 16-bit pages take 1.3 to 1.8 (a tile converted here costs HBM 35 ns; 43 requests, 3
-// of them chunks of up to 400 tokens, 16 heads: 111 us, 144 with single tokens'
-// requests left out, 205 without; 64 single tokens 116 and 110).  A block a page at
-// a time, eight rows a warp, half of them in flight; rows behind the last key, and
-// pages outside the pool (reported), as zeros.
-__global__ void __launch_bounds__(256) chunk_convert_kernel(const ChunkParams p, uint16_t* __restrict__ pages) {
+// What a call over FP8 records prepares in the workspace.  Queries: 512 dims as E4M3
+// codes of q 2^f and of what they leave of it, 2^f bringing the row's largest element
+// to 128 .. 256 (f at most 40: a row of nothing but numbers below 2^-33 keeps fewer
+// bits).  A row that holds an infinity or a NaN is codes of NaN.  Pages: the values
+// of requests of kConvertUnits units and more that fit (every unit that reads them
+// would convert them again), rows behind the last key, and of pages outside the pool
+// (reported), as zeros.  A warp a query, a block a page at a time.
+__global__ void __launch_bounds__(256)
+    chunk_convert_kernel(const ChunkParams p, const uint16_t* __restrict__ q, uint16_t* __restrict__ pages) {
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (long long i = blockIdx.x * 8ll + warp; i < p.rows; i += gridDim.x * 8ll) {
+    const uint4* from = reinterpret_cast<const uint4*>(q + i * MLA_D_QK) + 2 * lane;
+    const uint4 a = __ldcs(from), b = __ldcs(from + 1);
+    const uint32_t two[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t most = 0;  // of the bits without the sign: infinities above numbers, NaN above those
+#pragma unroll
+    for (int k = 0; k < 8; ++k) most = max(most, max(two[k] & 0x7fffu, two[k] >> 16 & 0x7fffu));
+    most = __reduce_max_sync(0xffffffffu, most);
+    const bool finite = most < 0x7f80u;
+    // (a subnormal's exponent field is 0: f is 40 there too)
+    const int f = finite ? min(134 - static_cast<int>(most >> 7), 40) : 0;
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + f) << 23);
+    uint32_t code[4], rest[4];
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+      uint32_t c[2], r[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float2 x = make_float2(__uint_as_float(two[k + h] << 16) * up,
+                                     __uint_as_float(two[k + h] & 0xffff0000u) * up);
+        c[h] = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+        const __half2_raw raw = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c[h]), __NV_E4M3);
+        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&raw));
+        r[h] = __nv_cvt_float2_to_fp8x2(make_float2(x.x - y.x, x.y - y.y), __NV_SATFINITE, __NV_E4M3);
+      }
+      code[k >> 1] = finite ? c[0] | c[1] << 16 : 0x7f7f7f7fu;
+      rest[k >> 1] = finite ? r[0] | r[1] << 16 : 0u;
+    }
+    uint8_t* to = p.queries + i * kQueryRow;
+    reinterpret_cast<uint4*>(to)[lane] = make_uint4(code[0], code[1], code[2], code[3]);
+    reinterpret_cast<uint4*>(to + kDv)[lane] = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+    if (lane == 0)
+      *reinterpret_cast<float2*>(to + 2 * kDv) = make_float2(up, __uint_as_float(static_cast<uint32_t>(127 - f) << 23));
+  }
   const int total = min(p.conv[p.batch], p.room);
   for (int i = blockIdx.x; i < total; i += gridDim.x) {
     int lo = 0, hi = p.batch;  // conv[lo] <= i < conv[hi]
@@ -991,41 +1050,28 @@ __global__ void __launch_bounds__(256) chunk_convert_kernel(const ChunkParams p,
     if (!good && threadIdx.x == 0) report(p.status, MLA_ERR_BAD_INDEX);
     const int row0 = 8 * warp;
     const uint8_t* rec = p.records + (static_cast<long long>(good ? page : 0) * kTile + row0) * MLA_RECORD_BYTES;
-    uint16_t* out = pages + (static_cast<long long>(i) * kTile + row0) * kPairRow;
-#pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-      uint2 code[4][2];
-      float scale[4][2];
-      uint4 rope[4];
+    uint16_t* out = pages + (static_cast<long long>(i) * kTile + row0) * kDv;
+    uint2 code[8][2];
+    float scale[8][2];
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const uint8_t* r = rec + (4 * half + n) * MLA_RECORD_BYTES;
+    for (int n = 0; n < 8; ++n)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          code[n][h] = __ldcs(reinterpret_cast<const uint2*>(r + 256 * h) + lane);
-          scale[n][h] = __ldcs(reinterpret_cast<const float*>(r + 512) + 2 * h + (lane >> 4));
-        }
-        if (lane < 8) rope[n] = __ldcs(reinterpret_cast<const uint4*>(r + 528) + lane);
+      for (int h = 0; h < 2; ++h) {
+        const uint8_t* r = rec + n * MLA_RECORD_BYTES;
+        code[n][h] = __ldcs(reinterpret_cast<const uint2*>(r + 256 * h) + lane);
+        scale[n][h] = __ldcs(reinterpret_cast<const float*>(r + kDv) + 2 * h + (lane >> 4));
       }
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const bool live = good && row0 + 4 * half + n < keys;
-        uint4* o = reinterpret_cast<uint4*>(out + (4 * half + n) * kPairRow);
-        const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+    for (int n = 0; n < 8; ++n)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint2 c = code[n][h];
-          const float sc = scale[n][h];
-          o[32 * h + lane] = live ? make_uint4(scaled2(c.x & 0xffffu, sc), scaled2(c.x >> 16, sc),
-                                               scaled2(c.y & 0xffffu, sc), scaled2(c.y >> 16, sc))
-                                  : none;
-          o[72 + 32 * h + lane] = live ? make_uint4(rest2(c.x & 0xffffu, sc), rest2(c.x >> 16, sc),
-                                                    rest2(c.y & 0xffffu, sc), rest2(c.y >> 16, sc))
-                                       : none;
-        }
-        if (lane < 8) o[64 + lane] = live ? rope[n] : none;
+      for (int h = 0; h < 2; ++h) {
+        const uint2 c = code[n][h];
+        const float sc = scale[n][h];
+        reinterpret_cast<uint4*>(out + n * kDv)[32 * h + lane] =
+            good && row0 + n < keys ? make_uint4(scaled2(c.x & 0xffffu, sc), scaled2(c.x >> 16, sc),
+                                                 scaled2(c.y & 0xffffu, sc), scaled2(c.y >> 16, sc))
+                                    : make_uint4(0u, 0u, 0u, 0u);
       }
-    }
   }
 }
 
@@ -1038,10 +1084,10 @@ __global__ void __launch_bounds__(256) chunk_convert_kernel(const ChunkParams p,
 __global__ void __launch_bounds__(128) chunk_combine_kernel(const ChunkParams p) {
   constexpr int kAhead = 4;
   const int lane = threadIdx.x & 31;
-  const long long rows = static_cast<long long>(p.head[kHeadFix]) * kRowsPerBlock;
+  const long long rows = static_cast<long long>(p.head[kHeadFix + p.schedule]) * kRowsPerBlock;
   pdl_wait_prior_grid();  // (also by blocks without work: a plan made next must not meet the kernel before)
   for (long long i = blockIdx.x * 4ll + (threadIdx.x >> 5); i < rows; i += gridDim.x * 4ll) {
-    const Unit unit = load_unit(p.units, p.fix[i / kRowsPerBlock]);
+    const Unit unit = load_unit(p, p.fix[i / kRowsPerBlock]);
     const int r = static_cast<int>(i % kRowsPerBlock);
     if (r >= unit.rows) continue;
     const long long at = static_cast<long long>(unit.slot) * kRowsPerBlock + r;
@@ -1130,92 +1176,31 @@ __device__ __forceinline__ T block_scan(T v, T* s_warp, T* total) {
   return base + x - v;
 }
 
-// Units of all requests, in order, and what each pair does of them.  A unit costs
-// its tiles and kFixedCost more (its Q, its epilogue).  Pair i takes units i, i +
-// pairs, .. as a whole while they fit its share of the whole cost; the others are
-// cut so that every pair's share is filled: the pair whose room is reached at x of
-// their sum begins there.  A cut within a unit's fixed part, or that would leave
-// less than kLeastTiles on one side, moves to the unit's border.  One block, made
-// once for a batch.
-__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPlanParams p) {
-  __shared__ long long s_warp64[32];
-  __shared__ int s_warp[32];
-  __shared__ int broken;
-  __shared__ int cut_u[kMaxChunkParts + 1], cut_t[kMaxChunkParts + 1];
+// What each pair does of the units, for schedule v.  A unit costs its tiles (half
+// as much again over FP8 records that are not converted before: mixed batch 115 us,
+// 120 with the same, 121 with twice as much) and kFixedCost more (its
+// Q, its epilogue), in half tiles.  Pair i takes units i, i + pairs, .. as a whole
+// while they fit its share of the whole cost; the others are cut so that every pair's
+// share is filled: the pair whose room is reached at x of their sum begins there.  A
+// cut within a unit's fixed part moves to its border.
+__device__ __forceinline__ int tile_cost(int pages0, int v) { return v == 1 && pages0 < 0 ? 3 : 2; }
+
+__device__ void plan_schedule(const ChunkPlanParams& p, int v, int units, int* cut_u, int* cut_t, int* s_warp,
+                              long long* s_warp64) {
   const int tid = threadIdx.x;
-  if (tid == 0) broken = 0;
-  __syncthreads();
-  for (int b = tid; b < p.batch; b += kPlanThreads) {
-    const int a = p.cu[b], e = p.cu[b + 1], n = p.lens[b];
-    p.made[b] = a;
-    if (b == p.batch - 1) p.made[p.batch] = e;
-    p.made[p.batch + 1 + b] = n;
-    if (a < 0 || e < a || e > p.total_q || n > kMaxChunkKeys) broken = 1;
-  }
-  __syncthreads();
-  if (broken) {  // offsets out of order could make requests overlap: nothing is done then
-    if (tid == 0) {
-      report(p.status, MLA_ERR_BAD_INDEX);
-      p.head[kHeadWhole] = 0;
-      p.head[kHeadCausal] = p.causal;
-      p.head[kHeadFix] = 0;
-    }
-    for (int i = tid; i < p.parts * MLA_SCHED_INTS; i += kPlanThreads) p.sched[i] = 0;
-    return;
-  }
-  // first unit of each request, and its first page among all requests'
-  int units = 0;
-  long long pages = 0;
-  for (int b0 = 0; b0 < p.batch; b0 += kPlanThreads) {
-    const int b = b0 + tid;
-    int n = 0;
-    if (b < p.batch) n = ((p.cu[b + 1] - p.cu[b]) * p.h_q + kRowsPerBlock - 1) / kRowsPerBlock;
-    int all;
-    const int at = block_scan(n, s_warp, &all);
-    long long all_pages;
-    const long long page = block_scan(n > 0 ? static_cast<long long>(pages_of(max(p.lens[b], 0))) : 0ll,
-                                      s_warp64, &all_pages);
-    if (b < p.batch) {
-      p.first[b] = units + at;
-      p.conv[b] = static_cast<int>(min(pages + page, static_cast<long long>(INT32_MAX)));
-    }
-    units += all;
-    pages += all_pages;
-  }
-  if (tid == 0) p.conv[p.batch] = static_cast<int>(min(pages, static_cast<long long>(INT32_MAX)));
-  if (tid == 0) {
-    p.head[kHeadWhole] = units;
-    p.head[kHeadCausal] = p.causal;
-    p.head[kHeadFix] = 0;
-  }
-  __syncthreads();
+  const ChunkSchedule& out = p.schedule[v];
+  auto unit_int = [&](int u, int i) -> int32_t& { return p.units[static_cast<long long>(u) * kChunkUnitInts + i]; };
   long long cost = 0;
   for (int u0 = 0; u0 < units; u0 += kPlanThreads) {
     const int u = u0 + tid;
-    long long mine = 0;
+    int mine = 0;
     if (u < units) {
-      int lo = 0, hi = p.batch;  // first[lo] <= u: the last such request (those before it with none have the same first)
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (p.first[mid] <= u)
-          lo = mid;
-        else
-          hi = mid;
-      }
-      const int tok0 = p.cu[lo], n = p.cu[lo + 1] - tok0, keys = max(p.lens[lo], 0);
-      const int rel = (u - p.first[lo]) * kRowsPerBlock, rows = min(n * p.h_q - rel, kRowsPerBlock);
-      const int limit0 = keys - n + 1;
-      const int len = p.causal ? max(limit0 + (rel + rows - 1) / p.h_q, 0) : keys;
-      int4* e = reinterpret_cast<int4*>(p.units + static_cast<long long>(u) * kChunkUnitInts);
-      e[0] = make_int4(tok0 * p.h_q + rel, rows, rel, lo);
-      e[1] = make_int4(len, limit0, 0, len > 0 ? 1 : 0);
-      e[2] = make_int4(p.conv[lo + 1] > p.conv[lo] ? p.conv[lo] : -1, 0, 0, 0);
-      mine = len > 0 ? tiles_of(len) + kFixedCost : 0;
-      if (len == 0) p.fix[atomicAdd(&p.head[kHeadFix], 1)] = u;  // (in any order: no result depends on it)
+      const int tiles = tiles_of(unit_int(u, 4));
+      mine = tiles > 0 ? tiles * tile_cost(unit_int(u, kPages0), v) + kFixedCost : 0;
+      p.cost[u] = mine;
     }
-    if (u < units) p.cost[u] = static_cast<int>(mine);
     long long all;
-    block_scan(mine, s_warp64, &all);
+    block_scan(static_cast<long long>(mine), s_warp64, &all);
     cost += all;
   }
   __syncthreads();
@@ -1234,7 +1219,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPla
         if (c[k] > 0 && c[k] <= room) {
           room -= c[k];
           p.cost[u0 + k * p.parts] = 0;
-          p.units[static_cast<long long>(u0 + k * p.parts) * kChunkUnitInts + 9] = 1;
+          unit_int(u0 + k * p.parts, kSchedule + 2 * v + 1) = 1 + kWhole;
         }
     }
   }
@@ -1250,7 +1235,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPla
     const int at = block_scan(mine > 0 ? 1 : 0, s_warp, &all);
     const long long before = block_scan(mine, s_warp64, &all_cost);
     if (mine > 0) {
-      p.rest[rest + at] = u;
+      out.rest[rest + at] = u;
       p.prefix[rest + at] = sum + before;
     }
     rest += all;
@@ -1272,10 +1257,9 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPla
             hi = mid;
         }
         e = lo;
-        const int tiles = tiles_of(p.units[static_cast<long long>(p.rest[e]) * kChunkUnitInts + 4]);
-        t = static_cast<int>(min(max(x - p.prefix[e] - kFixedCost, 0ll), static_cast<long long>(tiles)));
-        if (t < kLeastTiles) t = 0;
-        if (t > 0 && tiles - t < kLeastTiles) {
+        const int u = out.rest[e], tiles = tiles_of(unit_int(u, 4)), per = tile_cost(unit_int(u, kPages0), v);
+        t = static_cast<int>(min(max(x - p.prefix[e] - kFixedCost, 0ll) / per, static_cast<long long>(tiles)));
+        if (t == tiles) {
           ++e;
           t = 0;
         }
@@ -1298,20 +1282,102 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPla
   if (opens) {
     int cuts = 1;
     for (int i = tid + 1; i < p.parts && cut_u[i] == cut_u[tid]; ++i) cuts += cut_t[i] != cut_t[i - 1];
-    const int u = p.rest[cut_u[tid]];
-    int32_t* e = p.units + static_cast<long long>(u) * kChunkUnitInts;
-    e[6] = at;
-    e[7] = cuts + 1;
-    p.fix[atomicAdd(&p.head[kHeadFix], 1)] = u;
+    const int u = out.rest[cut_u[tid]];
+    unit_int(u, kSchedule + 2 * v) = at;
+    unit_int(u, kSchedule + 2 * v + 1) = cuts + 1;
+    out.fix[atomicAdd(&p.head[kHeadFix + v], 1)] = u;
   }
   if (in) {
     int piece = 0;
     if (cut_t[tid] > 0)
       for (int i = tid; i >= 0 && cut_u[i] == cut_u[tid] && cut_t[i] > 0; --i)
         piece += i == 0 || cut_u[i - 1] != cut_u[i] || cut_t[i - 1] != cut_t[i];
-    int4* e = reinterpret_cast<int4*>(p.sched + tid * MLA_SCHED_INTS);
+    int4* e = reinterpret_cast<int4*>(out.sched + tid * MLA_SCHED_INTS);
     e[0] = make_int4(cut_u[tid], cut_t[tid], cut_u[tid + 1], cut_t[tid + 1]);
     e[1] = make_int4(piece, 0, 0, 0);
+  }
+}
+
+// The plan: units of all requests, in order, and both schedules.  One block, made
+// once for a batch.
+__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPlanParams p) {
+  __shared__ long long s_warp64[32];
+  __shared__ int s_warp[32];
+  __shared__ int broken;
+  __shared__ int cut_u[kMaxChunkParts + 1], cut_t[kMaxChunkParts + 1];
+  const int tid = threadIdx.x;
+  if (tid == 0) broken = 0;
+  __syncthreads();
+  for (int b = tid; b < p.batch; b += kPlanThreads) {
+    const int a = p.cu[b], e = p.cu[b + 1], n = p.lens[b];
+    p.made[b] = a;
+    if (b == p.batch - 1) p.made[p.batch] = e;
+    p.made[p.batch + 1 + b] = n;
+    if (a < 0 || e < a || e > p.total_q || n > kMaxChunkKeys) broken = 1;
+  }
+  __syncthreads();
+  if (broken) {  // offsets out of order could make requests overlap: nothing is done then
+    if (tid == 0) {
+      report(p.status, MLA_ERR_BAD_INDEX);
+      p.head[kHeadWhole] = 0;
+      p.head[kHeadCausal] = p.causal;
+      p.head[kHeadFix] = p.head[kHeadFix + 1] = 0;
+    }
+    for (int v = 0; v < 2; ++v)
+      for (int i = tid; i < p.parts * MLA_SCHED_INTS; i += kPlanThreads) p.schedule[v].sched[i] = 0;
+    return;
+  }
+  // first unit of each request, and its first page among those of requests that are
+  // converted as a whole
+  int units = 0;
+  long long pages = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    int n = 0;
+    if (b < p.batch) n = ((p.cu[b + 1] - p.cu[b]) * p.h_q + kRowsPerBlock - 1) / kRowsPerBlock;
+    int all;
+    const int at = block_scan(n, s_warp, &all);
+    long long all_pages;
+    const long long page = block_scan(n >= kConvertUnits ? static_cast<long long>(pages_of(max(p.lens[b], 0))) : 0ll,
+                                      s_warp64, &all_pages);
+    if (b < p.batch) {
+      p.first[b] = units + at;
+      p.conv[b] = static_cast<int>(min(pages + page, static_cast<long long>(INT32_MAX)));
+    }
+    units += all;
+    pages += all_pages;
+  }
+  if (tid == 0) p.conv[p.batch] = static_cast<int>(min(pages, static_cast<long long>(INT32_MAX)));
+  if (tid == 0) {
+    p.head[kHeadWhole] = units;
+    p.head[kHeadCausal] = p.causal;
+    p.head[kHeadFix] = p.head[kHeadFix + 1] = 0;
+  }
+  __syncthreads();
+  for (int u = tid; u < units; u += kPlanThreads) {
+    int lo = 0, hi = p.batch;  // first[lo] <= u: the last such request (those before it with none have the same first)
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (p.first[mid] <= u)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    const int tok0 = p.cu[lo], n = p.cu[lo + 1] - tok0, keys = max(p.lens[lo], 0);
+    const int rel = (u - p.first[lo]) * kRowsPerBlock, rows = min(n * p.h_q - rel, kRowsPerBlock);
+    const int limit0 = keys - n + 1;
+    const int len = p.causal ? max(limit0 + (rel + rows - 1) / p.h_q, 0) : keys;
+    int4* e = reinterpret_cast<int4*>(p.units + static_cast<long long>(u) * kChunkUnitInts);
+    e[0] = make_int4(tok0 * p.h_q + rel, rows, rel, lo);
+    e[1] = make_int4(len, limit0, p.conv[lo + 1] > p.conv[lo] ? p.conv[lo] : -1, 0);
+    e[2] = make_int4(0, len > 0 ? 1 : 0, 0, len > 0 ? 1 : 0);
+    if (len == 0)
+      for (int v = 0; v < 2; ++v) p.schedule[v].fix[atomicAdd(&p.head[kHeadFix + v], 1)] = u;  // (in any order: no result depends on it)
+  }
+  __syncthreads();
+  for (int v = 0; v < 2; ++v) {
+    plan_schedule(p, v, units, cut_u, cut_t, s_warp, s_warp64);
+    __syncthreads();
   }
 }
 static_assert(kMaxChunkParts <= kPlanThreads, "a thread a cut");
@@ -1324,10 +1390,14 @@ ChunkPlanLayout chunk_plan_layout(int batch, int total_q, int h_q, int parts) {
   z.max_units = static_cast<int>(static_cast<long long>(total_q) * h_q / kRowsPerBlock) + batch;
   const size_t units = static_cast<size_t>(z.max_units);
   z.units = 256;
-  z.sched = z.units + up(units * kChunkUnitInts * 4);
-  z.fix = z.sched + up(static_cast<size_t>(parts) * MLA_SCHED_INTS * 4);
-  z.rest = z.fix + up(units * 4);
-  z.cost = z.rest + up(units * 4);
+  size_t at = z.units + up(units * kChunkUnitInts * 4);
+  for (auto& c : z.schedule) {
+    c.sched = at;
+    c.fix = c.sched + up(static_cast<size_t>(parts) * MLA_SCHED_INTS * 4);
+    c.rest = c.fix + up(units * 4);
+    at = c.rest + up(units * 4);
+  }
+  z.cost = at;
   z.prefix = z.cost + up(units * 4);
   z.first = z.prefix + up(units * 8);
   z.conv = z.first + up(static_cast<size_t>(batch) * 4);
@@ -1343,7 +1413,7 @@ cudaError_t launch_chunk_plan(const ChunkPlanParams& p, cudaStream_t st) {
 
 namespace {
 
-using ChunkKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, ChunkParams);
+using ChunkKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, ChunkParams);
 ChunkKernel chunk_kernel_of(bool half, bool fp8, bool stall) {
   if (fp8) return stall ? ck::chunk_kernel<false, true, true> : ck::chunk_kernel<false, true>;
   return stall ? ck::chunk_kernel<false, false, true> : half ? ck::chunk_kernel<true, false> : ck::chunk_kernel<false, false>;
@@ -1360,8 +1430,8 @@ cudaError_t chunk_setup() {
   return cudaSuccess;
 }
 
-cudaError_t launch_chunk(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const ChunkParams& p,
-                         bool half, bool stall, bool after_convert, int parts, cudaStream_t st) {
+cudaError_t launch_chunk(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& rope,
+                         const ChunkParams& p, bool half, bool stall, int parts, cudaStream_t st) {
   const bool fp8 = p.records != nullptr;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * parts), 1, 1);
@@ -1372,12 +1442,13 @@ cudaError_t launch_chunk(const CUtensorMap& q, const CUtensorMap& k, const CUten
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = after_convert ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, chunk_kernel_of(half, fp8, stall), q, k, v, p);
+  cfg.numAttrs = fp8 ? 1 : 0;  // after chunk_convert_kernel
+  return cudaLaunchKernelEx(&cfg, chunk_kernel_of(half, fp8, stall), q, k, v, rope, p);
 }
 
-cudaError_t launch_chunk_convert(const ChunkParams& p, uint16_t* pages, int sms, cudaStream_t st) {
-  ck::chunk_convert_kernel<<<std::min(p.room, 8 * sms), 256, 0, st>>>(p, pages);
+cudaError_t launch_chunk_convert(const ChunkParams& p, const uint16_t* q, uint16_t* pages, int sms, cudaStream_t st) {
+  const long long blocks = std::max((p.rows + 7) / 8, static_cast<long long>(p.room));
+  ck::chunk_convert_kernel<<<static_cast<int>(std::min(blocks, 8ll * sms)), 256, 0, st>>>(p, q, pages);
   return cudaGetLastError();
 }
 

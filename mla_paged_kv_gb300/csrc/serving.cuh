@@ -156,31 +156,37 @@ cudaError_t launch_prompt(const CUtensorMap& q, const CUtensorMap& k, const CUte
 // Attention of ragged chunks over a paged cache: the plan's parts, from its start.
 constexpr int kMaxChunkParts = 1024;
 constexpr int kMaxChunkKeys = 1 << 24;  // keys of a request
-constexpr int kFixedCost = 3;           // a unit's Q load and epilogue, in 128-key tiles
-constexpr int kLeastTiles = 1;          // of a unit's piece
+constexpr int kFixedCost = 6;            // a unit's Q load and epilogue, in half tiles of 128 keys
 constexpr int kChunkUnitInts = 12;
-#ifndef CU
-#define CU 2
-#endif
-constexpr int kConvertUnits = CU;        // units from which a request's FP8 pages are converted once for all
-enum : int { kHeadWhole = 0, kHeadCausal = 1, kHeadFix = 2 };  // header: units, causal, units for the combine
+constexpr int kConvertUnits = 3;         // units from which a request's FP8 pages are converted once for all
+enum : int { kHeadWhole = 0, kHeadCausal = 1, kHeadFix = 2 };  // header: units, causal, units for the combine (2)
 struct ChunkPlanLayout {
   int max_units;
-  size_t units, sched, fix, rest, cost, prefix, first, conv, made, bytes;
+  size_t units, cost, prefix, first, conv, made, bytes;
+  struct {
+    size_t sched, fix, rest;
+  } schedule[2];  // for 16-bit caches, and FP8 records
 };
 ChunkPlanLayout chunk_plan_layout(int batch, int total_q, int h_q, int parts);
+struct ChunkSchedule {
+  int32_t *sched, *fix, *rest;
+};
 struct ChunkPlanParams {
   const int32_t *cu, *lens;
   int batch, total_q, h_q, causal, parts;
-  int32_t *head, *units, *sched, *fix, *rest, *cost, *first, *conv, *made;
+  int32_t *head, *units, *cost, *first, *conv, *made;
   long long* prefix;
+  ChunkSchedule schedule[2];
   int32_t* status;
 };
 struct ChunkParams {
   const int32_t *head, *units, *sched, *fix, *rest, *conv, *made;  // of the plan
+  int schedule;                                                    // 0, or 1: FP8 records
   const int32_t *cu, *lens;                          // the caller's, to be compared with the plan's, or NULL
   const uint8_t* records;  // a cache of FP8 records, or NULL
   int room;                // pages that the workspace holds converted
+  uint8_t* queries;        // [total_q * h_q][MLA_CHUNK_QUERY_BYTES], behind them
+  long long rows;          // total_q * h_q
   const int32_t* block_table;
   int max_pages, num_pages, batch, h_q;
   float scale_log2;
@@ -192,9 +198,9 @@ struct ChunkParams {
 };
 cudaError_t chunk_setup();  // once per device: shared-memory opt-in
 cudaError_t launch_chunk_plan(const ChunkPlanParams& p, cudaStream_t st);
-cudaError_t launch_chunk(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const ChunkParams& p,
-                         bool half, bool stall, bool after_convert, int parts, cudaStream_t st);
-cudaError_t launch_chunk_convert(const ChunkParams& p, uint16_t* pages, int sms, cudaStream_t st);
+cudaError_t launch_chunk(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& rope,
+                         const ChunkParams& p, bool half, bool stall, int parts, cudaStream_t st);
+cudaError_t launch_chunk_convert(const ChunkParams& p, const uint16_t* q, uint16_t* pages, int sms, cudaStream_t st);
 cudaError_t launch_chunk_combine(const ChunkParams& p, int parts, int sms, cudaStream_t st);
 
 }  // namespace mla

@@ -285,7 +285,10 @@ int chunk_attention(const void* d_q, const void* d_kv, const int32_t* d_block_ta
   if (rc != MLA_OK) return rc;
   if (max_pages > kMaxRowPages || num_pages > (1 << 30)) return MLA_ERR_UNSUPPORTED;
   const ChunkPlanLayout z = chunk_plan_layout(batch, total_q, h_q, num_parts);
-  if (plan_bytes < z.bytes || workspace_bytes < mla_chunk_workspace_bytes(num_parts)) return MLA_ERR_INVALID_ARG;
+  const size_t sums = mla_chunk_workspace_bytes(num_parts);
+  const long long rows = static_cast<long long>(total_q) * h_q;
+  const size_t queries = dtype == MLA_DTYPE_FP8_RECORD ? static_cast<size_t>(rows) * MLA_CHUNK_QUERY_BYTES : 0;
+  if (plan_bytes < z.bytes || workspace_bytes < sums + queries) return MLA_ERR_INVALID_ARG;
   int sms = 0;
   rc = serving_device(&sms);
   if (rc != MLA_OK || total_q == 0) return rc;
@@ -294,9 +297,10 @@ int chunk_attention(const void* d_q, const void* d_kv, const int32_t* d_block_ta
   ChunkParams p{};
   p.head = ints(0);
   p.units = ints(z.units);
-  p.sched = ints(z.sched);
-  p.fix = ints(z.fix);
-  p.rest = ints(z.rest);
+  p.schedule = dtype == MLA_DTYPE_FP8_RECORD;
+  p.sched = ints(z.schedule[p.schedule].sched);
+  p.fix = ints(z.schedule[p.schedule].fix);
+  p.rest = ints(z.schedule[p.schedule].rest);
   p.conv = ints(z.conv);
   p.made = ints(z.made);
   p.cu = cu;
@@ -316,36 +320,45 @@ int chunk_attention(const void* d_q, const void* d_kv, const int32_t* d_block_ta
   p.status = d_status;
   // queries and cache rows as (64 dims of a slice, rows, slices): one box is
   // several whole slices, each 64 rows of 128 swizzled bytes
-  CUtensorMap qm, km, vm;
-  const cuuint64_t q_dims[4] = {64, static_cast<cuuint64_t>(total_q) * h_q, MLA_D_QK / 64, 1};
+  CUtensorMap qm, km, vm, rm;
+  const cuuint64_t q_dims[4] = {64, static_cast<cuuint64_t>(rows), MLA_D_QK / 64, 1};
   const cuuint64_t q_strides[3] = {2 * MLA_D_QK, 128, 2 * MLA_D_QK};
-  const cuuint32_t q_box[4] = {64, 64, MLA_D_QK / 64, 1};
-  // FP8 records: the pages of the workspace behind the partial sums (none: a map that nothing is loaded through)
-  const void* pages = d_kv;
-  int map_pages = num_pages;
-  bool convert = false;
-  if (p.records) {
-    const size_t sums = mla_chunk_workspace_bytes(num_parts);
-    const size_t room = (workspace_bytes - sums) / MLA_CHUNK_PAGE_BYTES;
-    p.room = static_cast<int>(std::min<size_t>(room, 1 << 30));
-    pages = p.room > 0 ? static_cast<const char*>(d_workspace) + sums : d_workspace;
-    map_pages = p.room > 0 ? p.room : 1;
-    // (a request of several row blocks has more rows than one)
-    convert = p.room > 0 && static_cast<long long>(total_q) * h_q > MLA_ROWS_PER_BLOCK;
-    if (!convert) p.room = 0;
+  const cuuint32_t q_box[4] = {64, 64, MLA_D_QK / 64, 1}, v_box[4] = {64, 64, 4, 1};
+  const cuuint64_t total_pages = static_cast<cuuint64_t>(num_pages);
+  if (!p.records) {
+    const cuuint64_t dims[4] = {64, MLA_PAGE_SIZE, MLA_D_QK / 64, total_pages};
+    const cuuint64_t strides[3] = {2 * MLA_D_QK, 128, 2 * MLA_D_QK * MLA_PAGE_SIZE};
+    const cuuint32_t k_box[4] = {64, 64, 3, 1};
+    rc = encode_map16(&qm, d_q, 4, q_dims, q_strides, q_box);
+    if (rc == MLA_OK) rc = encode_map16(&km, d_kv, 4, dims, strides, k_box);
+    if (rc == MLA_OK) rc = encode_map16(&vm, d_kv, 4, dims, strides, v_box);
+    rm = qm;  // (not used)
+  } else {
+    // in the workspace: the sums, pages (as many as fit), the queries
+    char* base = static_cast<char*>(d_workspace) + sums;
+    p.room = static_cast<int>(std::min<size_t>((workspace_bytes - sums - queries) / MLA_CHUNK_PAGE_BYTES, 1 << 30));
+    p.queries = reinterpret_cast<uint8_t*>(base + static_cast<size_t>(p.room) * MLA_CHUNK_PAGE_BYTES);
+    p.rows = rows;
+    // codes and RoPE dims in 16-bit units: a box of 64 is 128 bytes
+    const cuuint64_t dims[4] = {MLA_RECORD_BYTES / 2, MLA_PAGE_SIZE, 1, total_pages};
+    const cuuint64_t strides[3] = {MLA_RECORD_BYTES, 128, MLA_RECORD_BYTES * MLA_PAGE_SIZE};
+    const cuuint32_t box[4] = {64, 64, 1, 1};
+    const cuuint64_t c_dims[4] = {64, static_cast<cuuint64_t>(rows), 8, 1};
+    const cuuint64_t c_strides[3] = {MLA_CHUNK_QUERY_BYTES, 128, MLA_CHUNK_QUERY_BYTES};
+    const cuuint32_t c_box[4] = {64, 64, 8, 1};
+    // (no pages: a map of what is there, that nothing is loaded through)
+    const cuuint64_t v_dims[4] = {64, MLA_PAGE_SIZE, 8, static_cast<cuuint64_t>(p.room > 0 ? p.room : 1)};
+    const cuuint64_t v_strides[3] = {2 * MLA_D_V, 128, 2 * MLA_D_V * MLA_PAGE_SIZE};
+    rc = encode_map16(&qm, p.queries, 4, c_dims, c_strides, c_box);
+    if (rc == MLA_OK) rc = encode_map16(&km, d_kv, 4, dims, strides, box);
+    if (rc == MLA_OK) rc = encode_map16(&vm, p.room > 0 ? base : d_workspace, 4, v_dims, v_strides, v_box);
+    if (rc == MLA_OK) rc = encode_map16(&rm, d_q, 4, q_dims, q_strides, box);
+    if (rc == MLA_OK)
+      rc = launched(launch_chunk_convert(p, static_cast<const uint16_t*>(d_q), reinterpret_cast<uint16_t*>(base), sms,
+                                         to_stream(stream)));
   }
-  const cuuint64_t row = p.records ? MLA_CHUNK_PAGE_BYTES / MLA_PAGE_SIZE : 2 * MLA_D_QK;  // bytes
-  const cuuint64_t dims[4] = {64, MLA_PAGE_SIZE, row / 128, static_cast<cuuint64_t>(map_pages)};
-  const cuuint64_t strides[3] = {row, 128, row * MLA_PAGE_SIZE};
-  const cuuint32_t k_box[4] = {64, 64, 3, 1}, v_box[4] = {64, 64, 4, 1};
-  rc = encode_map16(&qm, d_q, 4, q_dims, q_strides, q_box);
-  if (rc == MLA_OK) rc = encode_map16(&km, pages, 4, dims, strides, k_box);
-  if (rc == MLA_OK) rc = encode_map16(&vm, pages, 4, dims, strides, v_box);
   if (rc != MLA_OK) return rc;
-  if (convert)
-    rc = launched(launch_chunk_convert(p, static_cast<uint16_t*>(const_cast<void*>(pages)), sms, to_stream(stream)));
-  if (rc != MLA_OK) return rc;
-  rc = launched(launch_chunk(qm, km, vm, p, dtype == MLA_DTYPE_FP16, stall, convert, num_parts, to_stream(stream)));
+  rc = launched(launch_chunk(qm, km, vm, rm, p, dtype == MLA_DTYPE_FP16, stall, num_parts, to_stream(stream)));
   return rc != MLA_OK || stall ? rc : launched(launch_chunk_combine(p, num_parts, sms, to_stream(stream)));
 }
 
@@ -800,9 +813,8 @@ int mla_chunk_get_plan(const int32_t* d_cu_seqlens_q, const int32_t* d_cache_seq
   p.parts = num_parts;
   p.head = ints(0);
   p.units = ints(z.units);
-  p.sched = ints(z.sched);
-  p.fix = ints(z.fix);
-  p.rest = ints(z.rest);
+  for (int v = 0; v < 2; ++v)
+    p.schedule[v] = ChunkSchedule{ints(z.schedule[v].sched), ints(z.schedule[v].fix), ints(z.schedule[v].rest)};
   p.cost = ints(z.cost);
   p.first = ints(z.first);
   p.conv = ints(z.conv);

@@ -11,9 +11,8 @@ merge of pieces add 2^-20; both move weights, hence twice that on the output
 (numerator and sum).  lse moves by the score error plus 2^-19 (sum, log, merge)
 and one last place of its own value.  fp16 values below the smallest normal
 are off by at most 2^-25.  Over FP8 records a value is, by the call's definition,
-the fp32 product of code and scale rounded to bf16, and a key the sum of that and
-of its remainder in bf16: the restatement takes those, the bounds are bf16's, and
-a score's sum has the remainders' products too (1088 of them).
+the product of code and scale rounded to bf16, and a score that of the products:
+the restatement takes those, and the bounds are bf16's.
 """
 
 import math
@@ -65,10 +64,9 @@ class Case:
             codes = torch.where(torch.isfinite(c), (c / scale[..., None]).clamp(-448, 448), c).to(torch.float8_e4m3fn)
             self.cache = torch.cat([codes.view(torch.uint8).reshape(pages, 64, 512), scale.view(torch.uint8),
                                     r.contiguous().view(torch.uint8)], 2).contiguous()
-            product = (codes.float() * scale[..., None]).reshape(pages, 64, 512)
-            value = product.to(BF16)
-            low = (product - value.float()).to(BF16)
-            self.values = torch.cat([value.double() + low.double(), r.double(), value.double()], 2).numpy()
+            key = (codes.double() * scale.double()[..., None]).reshape(pages, 64, 512)
+            value = (codes.float() * scale[..., None]).to(BF16).double().reshape(pages, 64, 512)
+            self.values = torch.cat([key, r.double(), value], 2).numpy()
 
     def keys(self):
         """Keys, values and whether they are on a page of the pool, of each request."""
@@ -79,7 +77,7 @@ class Case:
     def device(self):
         return (self.q.cuda(), self.cache.cuda(), torch.from_numpy(self.table).cuda(), i32(self.lens), i32(self.cu))
 
-    def check(self, out, lse, causal, scale=SCALE, fill=None):
+    def check(self, out, lse, causal, scale=SCALE, fill=None, split=False):
         u, uo = U[self.q.dtype], U[out.dtype]
         keys, values, seen = self.keys()
         want, wlse, mix, reach = so.chunk_attention(self.q.double().numpy(), keys, seen, self.cu, self.lens, causal,
@@ -92,23 +90,25 @@ class Case:
         o, l, want, wlse, mix, reach = (x[live] for x in (o, l, want, wlse, mix, reach))
         none = np.isneginf(wlse)
         assert np.array_equal(np.isneginf(l), none) and not o[none].any()
-        score = (1088 if self.values.shape[2] > 576 else 576) * 2.0 ** -23 * reach
+        score = 576 * 2.0 ** -23 * reach
+        if split:
+            most = np.abs(self.q.double().numpy()[live][..., :512]).max(2)
+            score = score + 2.0 ** -17 * scale * most * max(np.abs(k[:, :512]).sum(1).max() for k in keys)
         half = self.q.dtype == FP16 or out.dtype == FP16
         tol = (u + 2 * score + 2.0 ** -19)[..., None] * mix + uo * np.abs(want) + (2.0 ** -25 * 8 if half else 0)
         assert np.isfinite(o).all() and np.all(np.abs(o - want) <= tol), np.max(np.abs(o - want) / tol)
         l, wlse, score = l[~none], wlse[~none], score[~none]
         assert np.all(np.abs(l - wlse) <= score + 2.0 ** -19 + 2.0 ** -23 * np.abs(wlse))
 
-    def run(self, causal=True, scale=SCALE, parts=None, out_fp32=False):
+    def run(self, causal=True, scale=SCALE, parts=None, out_fp32=False, split=False):
         q, cache, table, lens, cu = self.device()
         pl = None if parts is None else mla.plan_chunks(cu, lens, q.shape[0], q.shape[1], causal, num_parts=parts)
         out, lse = mla.chunk_attention(q, cache, table, lens, cu, causal, scale, out_fp32, pl=pl)
-        self.check(out, lse, causal, scale)
+        self.check(out, lse, causal, scale, split=split)
         if cache.dtype == torch.uint8:  # without room for converted pages, and with room for some: the same to the bit
             pl = pl or mla.plan_chunks(cu, lens, q.shape[0], q.shape[1], causal)
-            base = pl.workspace
             for room in (0, 3, 9):
-                pl.workspace = torch.zeros(base.numel() + room * mla.CHUNK_PAGE_BYTES, dtype=torch.uint8, device="cuda")
+                pl.workspace = mla.chunk_workspace(pl, room)
                 o, l, status = torch.full_like(out, 7.0), torch.full_like(lse, 7.0), i32([0])
                 mla.mla_chunk_attention_fwd(q, cache, table, pl, o, l, status, scale)
                 assert int(status) == 0 and torch.equal(o, out) and torch.equal(l, lse)
@@ -176,6 +176,43 @@ def test_growing_maxima(amp, fp8):
     """Scores that spread over hundreds of powers of two: the reference is raised again and again."""
     for parts in (1, None):
         Case([6, 40], [900, 500], heads=16, seed=11, amp=amp, fp8=fp8).run(parts=parts)
+
+
+@pytest.mark.parametrize("spread", [0, 6, 14])
+def test_queries_of_any_size_over_records(spread):
+    """Over FP8 records a query is two E4M3 numbers an element, scaled by its largest one: elements below 2^-9 of that
+    are off by 2^-17 of it at most, and so a score by that times the key's absolute sum (`split`).  Rows from 2^-60 to
+    2^5, elements of a row within `spread` powers of two and one that is far above the others."""
+    c = Case([9, 3], [130, 300], heads=16, seed=spread, fp8=True)
+    g = torch.Generator().manual_seed(spread)
+    q = c.q.float()
+    q[..., :512] *= 2.0 ** -torch.randint(0, spread + 1, q[..., :512].shape, generator=g).float()
+    q[:, 3, 77] *= 64
+    for h, e in enumerate([-60, -35, -34, -20, -3, 5]):
+        q[:, h] *= 2.0 ** e
+    q[:, 7] = 0
+    q[:, 8, :512] = 0
+    q[:, 9, 512:] = 0
+    c.q = q.to(BF16)
+    c.run(split=True)
+
+
+@caches
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), -float("inf")])
+def test_a_query_that_is_no_number_stays_with_its_row(what, fp8):
+    c = Case([5, 40], [100, 200], heads=16, seed=5, fp8=fp8)
+    want = c.run()
+    for head, dim in ((2, 100), (9, 511), (15, 570)):
+        c.q[3, head, dim] = what
+    q, cache, table, lens, cu = c.device()
+    out, lse = mla.chunk_attention(q, cache, table, lens, cu, True, SCALE)
+    for head in range(16):
+        if head in (2, 9, 15):
+            assert not bool(torch.isfinite(out[3, head]).all())
+        else:
+            assert torch.equal(out[3, head], want[0][3, head]) and torch.equal(lse[3, head], want[1][3, head])
+    keep = [t for t in range(45) if t != 3]
+    assert torch.equal(out[keep], want[0][keep]) and torch.equal(lse[keep], want[1][keep])
 
 
 def test_rows_of_no_chunk_are_left():
@@ -276,8 +313,8 @@ def test_agrees_with_decode():
 
 
 def test_records_against_the_rows_that_the_gather_gives():
-    """Over FP8 records scores have more bits than over a 16-bit cache of the gathered rows: lse is nearer the products'
-    own, by far; the outputs, whose values are the same, agree within what the keys' rounding moves weights by."""
+    """Over FP8 records scores are the products' own; over a 16-bit cache of the gathered rows (the same values) keys are
+    rounded, and lse and outputs are further from them."""
     c = Case([5, 2, 30], [130, 600, 64], heads=16, seed=41, fp8=True)
     q, cache, table, lens, cu = c.device()
     pages = torch.arange(cache.shape[0], dtype=torch.int32, device="cuda")

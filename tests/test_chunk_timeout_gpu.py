@@ -35,6 +35,8 @@ def test_chunk_wait_runs_out_and_the_next_call_is_as_ever(new, ctx, fp8):
     table = torch.arange(60, dtype=torch.int32, device="cuda").view(len(new), -1).contiguous()
     cu = i32([sum(new[:i]) for i in range(len(new) + 1)])
     pl = mla.plan_chunks(cu, i32(lens), sum(new), 16)
+    if fp8:
+        pl.workspace = mla.chunk_workspace(pl)
     want = mla.chunk_attention(q, cache, table, i32(lens), cu, pl=pl)
     out, lse, status = torch.zeros_like(want[0]), torch.zeros_like(want[1]), i32([0])
     for _ in range(2):
