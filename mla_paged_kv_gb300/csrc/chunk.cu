@@ -1323,6 +1323,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPla
       p.head[kHeadCausal] = p.causal;
       p.head[kHeadFix] = p.head[kHeadFix + 1] = 0;
     }
+    for (int b = tid; b <= p.batch; b += kPlanThreads) p.conv[b] = 0;
     for (int v = 0; v < 2; ++v)
       for (int i = tid; i < p.parts * MLA_SCHED_INTS; i += kPlanThreads) p.schedule[v].sched[i] = 0;
     return;

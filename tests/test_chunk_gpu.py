@@ -276,6 +276,25 @@ def test_offsets_out_of_range():
             mla.plan_chunks(i32(bad), i32(ln), 6, 16)
 
 
+def test_an_empty_plan_over_records_converts_nothing():
+    """A plan of offsets out of range, made where other numbers lay: no page and no query is looked at by it."""
+    c = Case([200, 300], [40, 50], heads=16, seed=24, fp8=True)
+    q, cache, table, lens, _ = c.device()
+    parts = mla.mla_chunk_num_parts()
+    plan = torch.full((mla.mla_chunk_plan_bytes(2, 500, 16, parts),), 0x3F, dtype=torch.uint8, device="cuda")
+    status = i32([0])
+    mla.mla_chunk_get_plan(i32([0, 300, 200]), lens, 500, 16, True, parts, plan, status)
+    assert int(status) == BAD_INDEX
+    pl = mla.ChunkPlan(plan, 2, 500, 16, parts, True, None)
+    pl.workspace = mla.chunk_workspace(pl, 9).zero_()
+    out, lse = torch.full((500, 16, 512), 7.0, dtype=BF16, device="cuda"), torch.full((500, 16), 7.0, device="cuda")
+    status.zero_()
+    mla.mla_chunk_attention_fwd(q, cache, table, pl, out, lse, status)
+    assert int(status) == 0 and bool((out == 7.0).all()) and bool((lse == 7.0).all())
+    base = mla.mla_chunk_workspace_bytes(parts)
+    assert not bool(pl.workspace[base:base + 9 * mla.CHUNK_PAGE_BYTES].any())
+
+
 def test_a_plan_of_others_is_reported():
     c = Case([3, 5], [100, 40], heads=16, seed=29)
     q, cache, table, lens, cu = c.device()
