@@ -351,12 +351,14 @@ int mla_cache_gather(const void* d_cache, int cache_dtype, int num_pages, const 
  *   out = sum_j softmax_j(scale q . k_j) k_j[:512],  lse = ln sum_j exp(scale q . k_j)
  * A query that sees no key gets out = 0, lse = -inf.  Rows of the outputs outside
  * every chunk are left as they were.  Softmax weights are rounded to the cache's
- * type (bf16 over FP8 records) for the product with the values and divided by the
+ * type (fp16 over FP8 records) for the product with the values and divided by the
  * sum of the unrounded ones; statistics and sums are fp32.  Over FP8 records scores
  * are those of the products code x scale: each group's codes times the query's, a
  * query as two E4M3 numbers (exact down to 2^-9 of its largest latent element;
  * smaller elements are off by 2^-17 of that one), times the scale in fp32.  Values
- * are the products rounded to bf16.
+ * are the products with 11 significant bits of scale and product, where a group's
+ * scale is above 2^-13 of its key's largest (fewer below) and that one is within
+ * 2^-61 .. 2^68.
  *
  * num_parts: pairs of CTAs that share the work; mla_chunk_num_parts gives as many
  * as the device runs at once (>= 1, or a negative mla_status_t).  At most 1024. */

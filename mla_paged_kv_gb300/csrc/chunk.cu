@@ -37,6 +37,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <climits>
 
 #include "mla_serving.h"
 #include "common.cuh"
@@ -66,11 +67,15 @@ constexpr int kKSlices = 3;                // slices of a K stage
 // threads multiply by the key's scale in fp32; the RoPE part (bf16) has the fifth.
 // A query is scaled by a power of two that brings its largest element to 128 .. 256:
 // elements down to 2^-9 of that one are exact, smaller ones are off by 2^-17 of it.
-// Values are code x scale rounded to bf16.
+// Values are code x (scale / 2^E) in fp16, E a key's own multiple of 8 that leaves its
+// largest scale at 1/2 .. 128, and weights are those of the products times 2^E, fp16
+// too: with values and weights in bf16 the output was off by half as much again as
+// its own rounding.  A tile whose keys all have the same E, as a normalised cache's
+// do, takes it as one term of the exponent.
 constexpr int kParts = 5;                         // sums of a score: four groups, RoPE
 constexpr int kQueryRow = MLA_CHUNK_QUERY_BYTES;  // 512 codes, the remainders', 2^f and 2^-f as fp32, 8 bytes of nothing
 constexpr int kFp8Stages = 8;                     // of K: one 64-key x 128-byte part of a page each
-constexpr int kOffScales = kSlices * kSliceBytes + kFp8Stages * kSliceBytes;  // [2][4 groups][128 keys]
+constexpr int kOffScales = kSlices * kSliceBytes + kFp8Stages * kSliceBytes;  // [2][4 groups, E][128 keys]
 static_assert(MLA_CHUNK_PAGE_BYTES == 2 * MLA_D_V * MLA_PAGE_SIZE && kQueryRow % 16 == 0 && kQueryRow >= 2 * MLA_D_V + 8,
               "a page's values and a query in the workspace");
 constexpr int kKBytes = kKSlices * kSliceBytes;
@@ -82,7 +87,9 @@ constexpr int kOffK = kSlices * kSliceBytes;
 constexpr int kOffV = kOffK + kKStages * kKBytes;
 constexpr int kOffP = kOffV + kVStages * kVBytes;
 constexpr int kOffBar = kOffP + kPBytes;
-static_assert(kOffScales + 2 * 4 * kBN * 4 <= kOffV, "the scales lie behind the K stages");
+constexpr int kOffTileE = kOffScales + 2 * 5 * kBN * 4;  // [2]: E of a tile's keys, or kMixed; 2^-E
+static_assert(kOffTileE + 16 <= kOffV, "the scales lie behind the K stages");
+constexpr float kMixed = 1000.f;
 
 enum : int {
   Q_FULL = 0,
@@ -112,9 +119,11 @@ static_assert(kKSlices * 3 == kSlices, "three K stages a tile");
 
 // Warps: 0 .. 7 softmax (with 16 and 16 keys a thread FP8 records took 5% longer),
 // then one each for MMAs, Q (FP8 records: and scales) and K.  16-bit caches: one for
-// V; FP8 records: kConverters convert it.
+// V; FP8 records: kConverters convert it (eight of them instead of four leave the
+// softmax threads 96 registers: 4% longer).
 constexpr int kSoftmax = 8, kWarpMma = 8, kWarpQ = 9, kWarpK = 10, kWarpV = 11;
-constexpr int kConverters = 8;
+constexpr int kConverters = 4;
+constexpr int kLaneKeys = 8 / kConverters;  // keys of a page that a converting lane has, 8 kConverters apart
 constexpr int threads_of(bool fp8) { return 32 * (kWarpV + (fp8 ? kConverters : 1)); }
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 256;  // two buffers of 64 columns; four for the sums over FP8 records
@@ -262,31 +271,42 @@ __device__ __forceinline__ void fail(volatile int* abort_flag, int32_t* status) 
 
 // ------------------------------------------------------------------ FP8 records
 
-// Two E4M3 codes times their scale as bf16, rounded once.
-__device__ __forceinline__ uint32_t scaled2(uint32_t two, float scale) {
+// E of a key: 8 k - 10, its largest scale being in 2^(8 k - 11) .. 2^(8 k - 3).  Within
+// -66 .. 62, so that weights of keys that far apart stay floats: scales below 2^-61
+// keep fewer bits, from 2^69 on values overflow.
+__device__ __forceinline__ int key_exponent(const float4& scale) {
+  const float most = fmaxf(fmaxf(fabsf(scale.x), fabsf(scale.y)), fmaxf(fabsf(scale.z), fabsf(scale.w)));
+  const int e = static_cast<int>(__float_as_uint(most) >> 23) - 127;
+  return ((min(max(e, -61), 61) + 11) >> 3) * 8 - 10;
+}
+
+__device__ __forceinline__ float two_to(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
+// 16 codes times their key's scale / 2^E, as fp16, into the two 16-byte chunks from
+// `chunk` on of a swizzled 128-byte row.
+__device__ __forceinline__ uint32_t scaled2(uint32_t two, __half2 scale) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));  // (every E4M3 value is an fp16 value)
-  return pack2<false>(f.x * scale, f.y * scale);
+  const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&h), scale);
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// 16 codes times their scale into the two 16-byte chunks from `chunk` on of a
-// swizzled 128-byte row.
+__device__ __forceinline__ uint4 scaled8(uint32_t a, uint32_t b, __half2 scale) {
+  return make_uint4(scaled2(a & 0xffffu, scale), scaled2(a >> 16, scale), scaled2(b & 0xffffu, scale),
+                    scaled2(b >> 16, scale));
+}
+
 __device__ __forceinline__ void store_codes(uint8_t* row, uint32_t chunk, uint32_t swz, const uint4& codes,
-                                            float scale) {
-  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-  uint32_t o[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) o[i] = scaled2(w[i >> 1] >> (16 * (i & 1)) & 0xffffu, scale);
-  *reinterpret_cast<uint4*>(row + ((chunk ^ swz) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-  *reinterpret_cast<uint4*>(row + (((chunk + 1) ^ swz) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+                                            __half2 scale) {
+  *reinterpret_cast<uint4*>(row + ((chunk ^ swz) << 4)) = scaled8(codes.x, codes.y, scale);
+  *reinterpret_cast<uint4*>(row + (((chunk + 1) ^ swz) << 4)) = scaled8(codes.z, codes.w, scale);
 }
 
-// What a converting lane has of a page: one key (8 a warp) and every fourth
-// 16-byte piece of its record: the same quarter of every 64-dim slice.  The four
+// What a converting lane has of a page: kLaneKeys keys (8 a warp at a time) and every
+// fourth 16-byte piece of their records: the same quarter of every 64-dim slice.  The four
 // lanes of a key read 64 bytes in a row, and the stores of eight lanes (two keys of
 // different parity) go to eight different bank groups.
 struct RecordLane {
-  int key;      // of the page
+  int key;      // of the page, the first
   int quarter;  // of a slice
   uint32_t swz;
 };
@@ -315,9 +335,9 @@ __device__ __forceinline__ bool convert_v(const ChunkParams& p, const Run& run, 
   uint32_t n = 0;
   bool ok = true;
   const uint64_t pol = policy_evict_last();
-  uint4 raw[2][4];
-  float2 scale[2];
-  bool live[2];
+  uint4 raw[2][kLaneKeys][4];
+  float4 key_scale[2][kLaneKeys];
+  int left[2];  // keys of the page that count, less the lane's first one
   while (ok && walk_next(p, run, w)) {
     const int pages = min(pages_of(w.unit.len), 2 * w.hi);
     if (converted(p, w.unit)) {  // (rows behind the last key are zeros there)
@@ -333,23 +353,29 @@ __device__ __forceinline__ bool convert_v(const ChunkParams& p, const Run& run, 
       continue;
     }
     int ids = 0, base = -32;
-    auto fetch = [&](int k, int h) {  // page k's record: where it is, and whether its key counts
+    const uint8_t* from;
+    auto find = [&](int k, int h) {  // page k: where this lane's first key is, and how many count
       if (k - base >= 32) {
         base = k;
         ids = page_window(p, w.unit, base, lane);
       }
       const int id = __shfl_sync(0xffffffffu, ids, k - base);
-      live[h] = id >= 0 && k * kTile + me.key < w.unit.len;
-      const uint8_t* rec = record_at(p, id, me.key);
-      scale[h] = __ldcg(reinterpret_cast<const float2*>(rec + 512 + 8 * rank));
-      return rec + 256 * rank + 16 * me.quarter;
+      left[h] = id < 0 ? 0 : w.unit.len - k * kTile - me.key;
+      from = record_at(p, id, me.key);
+    };
+    auto load = [&](int h, int y, int i) {  // the lane's key y: a quarter of slice i
+      const uint8_t* rec = from + y * (8 * kConverters * MLA_RECORD_BYTES);
+      if (i == 0) key_scale[h][y] = __ldcg(reinterpret_cast<const float4*>(rec + kDv));
+      raw[h][y][i] = __ldcg(reinterpret_cast<const uint4*>(rec + 256 * rank + 16 * me.quarter + 64 * i));
     };
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (2 * w.lo + h >= pages) continue;
-      const uint8_t* from = fetch(2 * w.lo + h, h);
+      find(2 * w.lo + h, h);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) raw[h][i] = __ldcg(reinterpret_cast<const uint4*>(from + 64 * i));
+      for (int y = 0; y < kLaneKeys; ++y)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) load(h, y, i);
     }
     for (int k0 = 2 * w.lo; k0 < pages && ok; k0 += 2) {
 #pragma unroll
@@ -357,22 +383,28 @@ __device__ __forceinline__ bool convert_v(const ChunkParams& p, const Run& run, 
         if (k0 + h >= pages) continue;
         const int s = static_cast<int>(n % kVStages), r = static_cast<int>(n / kVStages);
         ++n;
-        const bool mine = live[h];
-        const float2 sc = scale[h];
+        const int mine = left[h];
         const bool more = k0 + h + 2 < pages;
-        const uint8_t* from = more ? fetch(k0 + h + 2, h) : nullptr;
+        if (more) find(k0 + h + 2, h);
         if (ok && r >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&bars[V_EMPTY + s], (r - 1) & 1, abort_flag, wait_ns));
-        uint8_t* row = sV + s * kVBytes + me.key * 128;
         const uint32_t chunk = static_cast<uint32_t>(2 * me.quarter);
 #pragma unroll
-        for (int i = 0; i < 4; ++i, row += kSliceBytes) {
-          if (mine) {
-            store_codes(row, chunk, me.swz, raw[h][i], i < 2 ? sc.x : sc.y);
-          } else {
-            *reinterpret_cast<uint4*>(row + ((chunk ^ me.swz) << 4)) = make_uint4(0u, 0u, 0u, 0u);
-            *reinterpret_cast<uint4*>(row + (((chunk + 1) ^ me.swz) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+        for (int y = 0; y < kLaneKeys; ++y) {
+          const float4 sc = key_scale[h][y];
+          const float down = two_to(-key_exponent(sc));
+          const __half2 scale[2] = {__float2half2_rn((rank == 0 ? sc.x : sc.z) * down),
+                                    __float2half2_rn((rank == 0 ? sc.y : sc.w) * down)};
+          uint8_t* row = sV + s * kVBytes + (me.key + 8 * kConverters * y) * 128;
+#pragma unroll
+          for (int i = 0; i < 4; ++i, row += kSliceBytes) {
+            if (mine > 8 * kConverters * y) {
+              store_codes(row, chunk, me.swz, raw[h][y][i], scale[i >> 1]);
+            } else {
+              *reinterpret_cast<uint4*>(row + ((chunk ^ me.swz) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+              *reinterpret_cast<uint4*>(row + (((chunk + 1) ^ me.swz) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            if (more) load(h, y, i);
           }
-          if (more) raw[h][i] = __ldcg(reinterpret_cast<const uint4*>(from + 64 * i));
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -385,18 +417,20 @@ __device__ __forceinline__ bool convert_v(const ChunkParams& p, const Run& run, 
 
 // The scales of a unit's tiles, in turn in two buffers of [4 groups][128 keys]:
 // lane i has keys 4 i .. of a tile, the next tile's loads in flight.  (Pages outside
-// the pool or past the last one: page 0's, whose scores are masked.)
+// the pool or past the last one: page 0's, whose scores are masked.)  With them each
+// key's E and the tile's.
 __device__ __forceinline__ bool stage_scales(const ChunkParams& p, const Walk& w, int lane, uint8_t* smem,
                                              uint64_t* bars, volatile int* abort_flag, uint64_t wait_ns,
                                              uint32_t& n) {
   float4 key[4];
-  int ids = 0, base = -32;
+  int ids = 0, base = -32, live = 0;  // live: this lane's keys that are any
   auto load = [&](int j) {
     if (2 * j - base >= 32) {
       base = 2 * j;
       ids = page_window(p, w.unit, base, lane);
     }
     const int page = __shfl_sync(0xffffffffu, ids, 2 * j + (lane >> 4) - base);
+    live = page < 0 ? 0 : w.unit.len - j * kBN - 4 * lane;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       key[i] = __ldcg(reinterpret_cast<const float4*>(record_at(p, page, 4 * (lane & 15) + i) + kDv));
@@ -406,7 +440,24 @@ __device__ __forceinline__ bool stage_scales(const ChunkParams& p, const Walk& w
   for (int j = w.lo; j < w.hi && ok; ++j, ++n) {
     if (n >= 2)
       ok = __all_sync(0xffffffffu, mbar_wait(&bars[SCALE_EMPTY + (n & 1)], ((n >> 1) - 1) & 1, abort_flag, wait_ns));
-    float4* to = reinterpret_cast<float4*>(smem + kOffScales) + (n & 1) * kBN + lane;
+    int e[4], least = INT_MAX, most = INT_MIN;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      e[i] = key_exponent(key[i]);
+      if (i < live) {
+        least = min(least, e[i]);
+        most = max(most, e[i]);
+      }
+    }
+    least = __reduce_min_sync(0xffffffffu, least);
+    most = __reduce_max_sync(0xffffffffu, most);
+    float4* to = reinterpret_cast<float4*>(smem + kOffScales) + (n & 1) * (5 * kBN / 4) + lane;
+    to[4 * kBN / 4] = make_float4(static_cast<float>(e[0]), static_cast<float>(e[1]), static_cast<float>(e[2]),
+                                  static_cast<float>(e[3]));
+    const int all = least == most ? least : 0;  // (no key at all: whatever)
+    if (lane == 0)
+      reinterpret_cast<float2*>(smem + kOffTileE)[n & 1] =
+          make_float2(least < most ? kMixed : static_cast<float>(all), two_to(-all));
     to[0] = make_float4(key[0].x, key[1].x, key[2].x, key[3].x);
     to[kBN / 4] = make_float4(key[0].y, key[1].y, key[2].y, key[3].y);
     to[2 * kBN / 4] = make_float4(key[0].z, key[1].z, key[2].z, key[3].z);
@@ -457,7 +508,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
       mbar_init(&bars[K_EMPTY + i], 1);
     }
     for (int i = 0; i < kVStages; ++i) {
-      mbar_init(&bars[V_FULL + i], 2 * (kFp8 ? 8 : 1));
+      mbar_init(&bars[V_FULL + i], 2 * (kFp8 ? kConverters : 1));
       mbar_init(&bars[V_EMPTY + i], 1);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&bars[S_FULL + i], 1);
@@ -607,7 +658,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       constexpr uint32_t idesc_qk = idesc_16bit_f32(128, kBN, false, kHalf);
       constexpr uint32_t idesc_codes = idesc_e4m3_f32(128, kBN);
-      constexpr uint32_t idesc_pv = idesc_16bit_f32(128, 256, true, kHalf);
+      constexpr uint32_t idesc_pv = idesc_16bit_f32(128, 256, true, kHalf || kFp8);
       const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024);
       const uint64_t k_desc = sdesc_sw128(smem_u32(sK), 16, 1024);
       const uint64_t v_desc = sdesc_sw128(smem_u32(sV), kSliceBytes, 1024);  // MN-major
@@ -785,11 +836,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
         // there too, for what the stage holds may be no number)
         if (row >= w.unit.rows && (2 * j + kh) * kTile >= w.unit.len) seen = 0;
         float s[32], top;
+        float2 tile_e = make_float2(0.f, 1.f);
         if constexpr (kFp8) {
-          const float* scales = sScale + (tn & 1) * 4 * kBN;
+          const float* scales = sScale + (tn & 1) * 5 * kBN;
           ok = ok && mbar_wait(&bars[SCALE_FULL + (tn & 1)], (tn >> 1) & 1, abort_flag, kWaitNs);
 #pragma unroll
           for (int n = 0; n < kParts; ++n, ++sn) {
+            if (n == kParts - 1) tile_e = reinterpret_cast<const float2*>(smem + kOffTileE)[tn & 1];
             ok = __all_sync(0xffffffffu, ok && mbar_wait(&bars[S_FULL + (sn & 3)], (sn >> 2) & 1, abort_flag, kWaitNs));
             if (tid == 0 && n == 0) MLA_TRACE(7, tn);
             tc_fence_after();
@@ -801,7 +854,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
             if (lane == 0 && n == 0) mbar_arrive_remote_relaxed(s_first);
             if (lane == 0 && n == kParts - 1) {
               mbar_arrive_remote_relaxed(s_first + 8 * (S_ALL - S_FIRST));
-              mbar_arrive(&bars[SCALE_EMPTY + (tn & 1)]);
             }
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
@@ -839,26 +891,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
           }
           top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         }
+        // (FP8 records: of scores to which the keys' E are added, one by one or as one for all)
+        float c = c_log2, add = 0.f, down = 1.f;  // down: 2^-add
+        bool mixed = false;
+        const float* key_e = sScale + (tn & 1) * 5 * kBN + 4 * kBN;
+        if constexpr (kFp8) {
+          add = tile_e.x;
+          down = tile_e.y;
+          mixed = add == kMixed;
+          if (mixed) {
+            top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              s[i] = fmaf(s[i], c, key_e[i]);
+              top = fmaxf(top, s[i]);
+            }
+            c = down = 1.f;
+            add = 0.f;
+          }
+        }
         // the row's maximum over its four threads
         const float* buf = shared_row(top);
         ok = !named_bar_or(row_bar, 128, !ok);  // (a warp that gave up waiting takes the others along)
         if (!ok) break;
-        const float mt = fmaxf(fmaxf(buf[0], buf[kCtaRows]), fmaxf(buf[2 * kCtaRows], buf[3 * kCtaRows])) * c_log2;
+        const float mt = fmaf(fmaxf(fmaxf(buf[0], buf[kCtaRows]), fmaxf(buf[2 * kCtaRows], buf[3 * kCtaRows])), c, add);
         const float r_new = mt > ref + kTau ? mt : ref;
         const float alpha = r_new == ref ? 1.f : ex2(ref - r_new);
         ref = r_new;
         const float mref = ref == -INFINITY ? 0.f : ref;
         float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        const float2 cl = make_float2(c_log2, c_log2), nr = make_float2(-mref, -mref);
+        const float2 cl = make_float2(c, c), nr = make_float2(add - mref, add - mref);
         uint32_t pk[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const float2 x = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]), cl, nr);
           const float p0 = ex2(x.x), p1 = ex2(x.y);
-          pk[i] = pack2<kHalf>(p0, p1);
+          pk[i] = pack2<kHalf || kFp8>(p0, p1);
           ls[i & 1] = __fadd2_rn(ls[i & 1], make_float2(p0, p1));
         }
-        l = l * alpha + ((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y));
+        float sum_p = (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
+        if constexpr (kFp8) {  // without the 2^E
+          sum_p *= down;
+          if (mixed) {
+            sum_p = 0.f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sum_p = fmaf(ex2(s[i] - mref), two_to(-static_cast<int>(key_e[i])), sum_p);
+          }
+          __syncwarp();  // every lane has read the scales
+          if (lane == 0) mbar_arrive(&bars[SCALE_EMPTY + (tn & 1)]);
+        }
+        l = l * alpha + sum_p;
         // P V of the tile before is done: P may be overwritten and O rescaled
         if (tn >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&bars[PV_DONE], (tn - 1) & 1, abort_flag, kWaitNs));
         if (j > w.lo && ok && __any_sync(0xffffffffu, alpha != 1.f)) {
@@ -1055,26 +1137,25 @@ __global__ void __launch_bounds__(256)
     const uint8_t* rec = p.records + (static_cast<long long>(good ? page : 0) * kTile + row0) * MLA_RECORD_BYTES;
     uint16_t* out = pages + (static_cast<long long>(i) * kTile + row0) * kDv;
     uint2 code[8][2];
-    float scale[8][2];
+    float4 scale[8];
 #pragma unroll
-    for (int n = 0; n < 8; ++n)
+    for (int n = 0; n < 8; ++n) {
+      const uint8_t* r = rec + n * MLA_RECORD_BYTES;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) code[n][h] = __ldcs(reinterpret_cast<const uint2*>(r + 256 * h) + lane);
+      scale[n] = __ldcs(reinterpret_cast<const float4*>(r + kDv));
+    }
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      const float down = two_to(-key_exponent(scale[n]));
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint8_t* r = rec + n * MLA_RECORD_BYTES;
-        code[n][h] = __ldcs(reinterpret_cast<const uint2*>(r + 256 * h) + lane);
-        scale[n][h] = __ldcs(reinterpret_cast<const float*>(r + kDv) + 2 * h + (lane >> 4));
-      }
-#pragma unroll
-    for (int n = 0; n < 8; ++n)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint2 c = code[n][h];
-        const float sc = scale[n][h];
+        const float mine = h == 0 ? (lane < 16 ? scale[n].x : scale[n].y) : (lane < 16 ? scale[n].z : scale[n].w);
         reinterpret_cast<uint4*>(out + n * kDv)[32 * h + lane] =
-            good && row0 + n < keys ? make_uint4(scaled2(c.x & 0xffffu, sc), scaled2(c.x >> 16, sc),
-                                                 scaled2(c.y & 0xffffu, sc), scaled2(c.y >> 16, sc))
+            good && row0 + n < keys ? scaled8(code[n][h].x, code[n][h].y, __float2half2_rn(mine * down))
                                     : make_uint4(0u, 0u, 0u, 0u);
       }
+    }
   }
 }
 

@@ -219,9 +219,9 @@ def request_keys(cache, table_row, length):
     return np.array(rows).reshape(length, cache.shape[2]), np.array(seen, dtype=bool)
 
 
-def chunk_attention(q, keys, seen, cu, lens, causal, scale, values=None):
-    """As prompt_attention, for chunks over their requests' keys: keys[b] [len, 576] float64, values[b] [len, 512] (the
-    keys' first 512 dims if not given) and seen[b] [len] (a key on a page outside the pool is masked)."""
+def chunk_attention(q, keys, seen, cu, lens, causal, scale):
+    """As prompt_attention, for chunks over their requests' keys: keys[b] [len, 576] float64 (the first 512 dims the value)
+    and seen[b] [len] (a key on a page outside the pool is masked)."""
     q = np.asarray(q, dtype=np.float64)
     out = np.full((*q.shape[:2], 512), np.nan)
     mix, lse, reach = out.copy(), np.full(q.shape[:2], np.nan), np.full(q.shape[:2], np.nan)
@@ -232,7 +232,7 @@ def chunk_attention(q, keys, seen, cu, lens, causal, scale, values=None):
             if causal:
                 see = see & (np.arange(total) <= total - n + i)
             k = keys[b][:total][see]
-            v = k[:, :512] if values is None else values[b][:total][see]
+            v = k[:, :512]
             t = cu[b] + i
             s = scale * q[t] @ k.T
             top = s.max(1, initial=-np.inf)

@@ -10,9 +10,11 @@ truncation allowed for), and the exponential, the reference's rounding and the
 merge of pieces add 2^-20; both move weights, hence twice that on the output
 (numerator and sum).  lse moves by the score error plus 2^-19 (sum, log, merge)
 and one last place of its own value.  fp16 values below the smallest normal
-are off by at most 2^-25.  Over FP8 records a value is, by the call's definition,
-the product of code and scale rounded to bf16, and a score that of the products:
-the restatement takes those, and the bounds are bf16's.
+are off by at most 2^-25.  Over FP8 records weights are fp16 (2^-11; those below
+2^-14 of the largest are off by 2^-25 of it: 2^-25 sum_j |v_j| on the output), and a
+value is off by the rounding of its scale and of the product, 2^-11 each.  Both are
+taken without a power of two, 2^E, that the key's largest scale has in common with
+those within a factor of 256: what is below the smallest normal is so after that.
 """
 
 import math
@@ -65,23 +67,22 @@ class Case:
             self.cache = torch.cat([codes.view(torch.uint8).reshape(pages, 64, 512), scale.view(torch.uint8),
                                     r.contiguous().view(torch.uint8)], 2).contiguous()
             key = (codes.double() * scale.double()[..., None]).reshape(pages, 64, 512)
-            value = (codes.float() * scale[..., None]).to(BF16).double().reshape(pages, 64, 512)
-            self.values = torch.cat([key, r.double(), value], 2).numpy()
+            self.values = torch.cat([key, r.double()], 2).numpy()
+            self.scale = scale
 
     def keys(self):
-        """Keys, values and whether they are on a page of the pool, of each request."""
+        """Keys, and whether they are on a page of the pool, of each request."""
         rows = [so.request_keys(self.values, self.table[b], max(n, 0)) for b, n in enumerate(self.lens)]
-        return [r[0][:, :576] for r in rows], [r[0][:, -512:] if r[0].shape[1] > 576 else r[0][:, :512] for r in rows], \
-            [r[1] for r in rows]
+        return [r[0] for r in rows], [r[1] for r in rows]
 
     def device(self):
         return (self.q.cuda(), self.cache.cuda(), torch.from_numpy(self.table).cuda(), i32(self.lens), i32(self.cu))
 
     def check(self, out, lse, causal, scale=SCALE, fill=None, split=False):
         u, uo = U[self.q.dtype], U[out.dtype]
-        keys, values, seen = self.keys()
+        keys, seen = self.keys()
         want, wlse, mix, reach = so.chunk_attention(self.q.double().numpy(), keys, seen, self.cu, self.lens, causal,
-                                                    scale, values)
+                                                    scale)
         o, l = out.double().cpu().numpy(), lse.double().cpu().numpy()
         live = np.zeros(o.shape[0], dtype=bool)
         live[self.cu[0]:self.cu[-1]] = True
@@ -95,7 +96,15 @@ class Case:
             most = np.abs(self.q.double().numpy()[live][..., :512]).max(2)
             score = score + 2.0 ** -17 * scale * most * max(np.abs(k[:, :512]).sum(1).max() for k in keys)
         half = self.q.dtype == FP16 or out.dtype == FP16
-        tol = (u + 2 * score + 2.0 ** -19)[..., None] * mix + uo * np.abs(want) + (2.0 ** -25 * 8 if half else 0)
+        tiny = 2.0 ** -25 * 8 if half else 0
+        if self.cache.dtype == torch.uint8:
+            u = 3 * 2.0 ** -11
+            most = torch.nan_to_num(self.scale.double().abs().amax(2), posinf=1.0).clamp(2.0 ** -61, 2.0 ** 61)
+            power = 2.0 ** (8 * torch.floor((torch.floor(torch.log2(most)) + 11) / 8) - 10)[..., None].numpy()
+            power = [so.request_keys(power, self.table[b], max(n, 0))[0] for b, n in enumerate(self.lens)]
+            tiny += max([2.0 ** -25 * e.max() * (8 + (np.abs(np.nan_to_num(k[:, :512])) / e).sum(0).max())
+                         for k, e in zip(keys, power) if len(k)], default=0)
+        tol = (u + 2 * score + 2.0 ** -19)[..., None] * mix + uo * np.abs(want) + tiny
         assert np.isfinite(o).all() and np.all(np.abs(o - want) <= tol), np.max(np.abs(o - want) / tol)
         l, wlse, score = l[~none], wlse[~none], score[~none]
         assert np.all(np.abs(l - wlse) <= score + 2.0 ** -19 + 2.0 ** -23 * np.abs(wlse))
@@ -195,6 +204,24 @@ def test_queries_of_any_size_over_records(spread):
     q[:, 9, 512:] = 0
     c.q = q.to(BF16)
     c.run(split=True)
+
+
+@pytest.mark.parametrize("parts", [None, 1])
+def test_scales_far_apart(parts):
+    """Keys (and groups of a key) whose scales are far from each other, in tiles of their own and side by side."""
+    c = Case([9, 40, 200], [130, 300, 500], heads=16, seed=77, fp8=True, amp=0.5)
+    g = torch.Generator().manual_seed(78)
+    far = 2.0 ** torch.tensor([-50.0, -30.0, -12.0, -6.0, 0.0, 3.0])
+    size = far[torch.randint(0, 6, c.scale.shape[:2], generator=g)][..., None].expand(-1, -1, 4).clone()
+    size[::3] = 2.0 ** -9  # pages of keys that are alike
+    size[1::3] *= 2.0 ** -torch.randint(0, 5, size[1::3].shape, generator=g).float()
+    c.scale = c.scale * size
+    rows, code = c.cache.clone(), c.cache[..., :512].contiguous().view(torch.float8_e4m3fn)
+    rows[..., 512:528] = c.scale.contiguous().view(torch.uint8)
+    key = (code.double().reshape(-1, 64, 4, 128) * c.scale.double()[..., None]).reshape(-1, 64, 512)
+    c.cache, c.values = rows, np.concatenate([key.numpy(), c.values[..., 512:]], 2)
+    c.run(parts=parts)
+    c.run(False, parts=parts, out_fp32=True)
 
 
 @caches

@@ -28,15 +28,15 @@ def as_case(q, cache, table, lens, cu):
     """The attention over what the device holds, for Case.check."""
     c = object.__new__(Case)
     c.q, c.table, c.lens, c.cu = q.cpu(), table.cpu().numpy(), list(lens), list(cu)
-    rows = cache.cpu()
+    rows = c.cache = cache.cpu()
     if cache.dtype != torch.uint8:
         c.values = rows.double().numpy()
     else:
         code = rows[..., :512].contiguous().view(torch.float8_e4m3fn).reshape(-1, 64, 4, 128)
         scale = rows[..., 512:528].contiguous().view(torch.float32)[..., None]
         key = (code.double() * scale.double()).reshape(-1, 64, 512)
-        value = (code.float() * scale).to(BF16).double().reshape(-1, 64, 512)
-        c.values = torch.cat([key, rows[..., 528:].contiguous().view(BF16).double(), value], 2).numpy()
+        c.scale = scale[..., 0]
+        c.values = torch.cat([key, rows[..., 528:].contiguous().view(BF16).double()], 2).numpy()
     return c
 
 
