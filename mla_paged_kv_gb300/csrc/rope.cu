@@ -14,17 +14,51 @@ namespace {
 
 // ------------------------------------------------------------------ table
 
+constexpr double kPi = 3.14159265358979323846;
+__host__ __device__ constexpr double pi_to(int n) { return n == 0 ? 1.0 : kPi * pi_to(n - 1); }
+__host__ __device__ constexpr double factorial(int n) { return n < 2 ? 1.0 : n * factorial(n - 1); }
+// The coefficient of x^n in the series of sin(pi x) (n odd) or cos(pi x) (n even), twice.
+template <int n>
+__device__ __forceinline__ float2 series() {
+  constexpr float c = static_cast<float>(((n >> 1) & 1 ? -1.0 : 1.0) * pi_to(n) / factorial(n));
+  return make_float2(c, c);
+}
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// For |x| <= 1/4.
+__device__ __forceinline__ float2 sin_pi(float2 x) {
+  constexpr float kHigh = static_cast<float>(kPi), kLow = static_cast<float>(kPi - static_cast<double>(kHigh));
+  const float2 t = __fmul2_rn(x, x);
+  float2 y = __ffma2_rn(t, series<9>(), series<7>());
+  y = __ffma2_rn(t, y, series<5>());
+  y = __ffma2_rn(t, y, series<3>());
+  y = __ffma2_rn(t, y, both(kLow));
+  return __ffma2_rn(x, both(kHigh), __fmul2_rn(x, y));
+}
+__device__ __forceinline__ float2 cos_pi(float2 x) {
+  const float2 t = __fmul2_rn(x, x);
+  float2 y = __ffma2_rn(t, series<10>(), series<8>());
+  y = __ffma2_rn(t, y, series<6>());
+  y = __ffma2_rn(t, y, series<4>());
+  y = __ffma2_rn(t, y, series<2>());
+  return __ffma2_rn(t, y, both(1.f));
+}
+
 // cos_sin[p] = magnitude * (cos(p f_0) .. , sin(p f_0) ..).
 //
 // Angles in whole turns of 2^64 steps: step_i = round(f_i / 2 pi * 2^64), and
 // p * step_i modulo 2^64 is the angle modulo a turn with no rounding at all: what
 // is left of the frequency's own rounding (2^-53 of it) is below 2^-31 turns at
 // position 2^24, where an fp32 angle would be off by a radian.  The nearest
-// quarter turn comes off in integers too, so that sincospif sees at most a
-// quarter of a half turn, and values next to zero keep their leading bits.
-// A thread keeps four pairs and steps through positions, so that an angle is one
-// addition.  Bound by the writes for many positions (163840 x 64: 42 MB), by the
-// launch for few.
+// quarter turn comes off in integers too; what is left, at most an eighth of a turn
+// to either side, is converted high and low word apart, so that values next to zero
+// keep their leading bits, and the Taylor series of sin(pi x) and cos(pi x) to x^9
+// and x^10 leave 2^-29 of it there.
+// A thread keeps four pairs, two at a time in packed arithmetic, and steps through
+// positions, so that an angle is one addition.  Bound by the launch for few positions
+// (4096 x 64: 4.2 us), for many by issue, with half of it left to the writes (160000 x
+// 64: 41 MB in 10.4 us; 14.5 with the library's sincospif).
 __global__ void __launch_bounds__(256)
     rope_table_kernel(const RopeSteps f, int dim, float magnitude, unsigned long long first, int positions,
                       float* __restrict__ out) {
@@ -42,16 +76,26 @@ __global__ void __launch_bounds__(256)
   for (; p < positions; p += step) {
     float c[4], s[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const unsigned long long quarter = (angle[k] + (1ull << 61)) >> 62;  // nearest, modulo 4
-      const float x = static_cast<float>(static_cast<long long>(angle[k] - (quarter << 62))) * 0x1p-63f;  // half turns
-      float sn, cs;
-      sincospif(x, &sn, &cs);
-      const bool swap = quarter & 1;
-      const float a = swap ? sn : cs, b = swap ? cs : sn;
-      c[k] = ((quarter + 1) & 2) ? -a * magnitude : a * magnitude;  // quarters 1 and 2
-      s[k] = (quarter & 2) ? -b * magnitude : b * magnitude;        // quarters 2 and 3
-      angle[k] += turn[k];
+    for (int k = 0; k < 4; k += 2) {
+      uint32_t quarter[2];  // nearest, modulo 4
+      float2 x;             // half turns past it
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t high = static_cast<uint32_t>(angle[k + h] >> 32), low = static_cast<uint32_t>(angle[k + h]);
+        quarter[h] = (high + (1u << 29)) >> 30;
+        const int rest = static_cast<int>(high - (quarter[h] << 30));
+        (h ? x.y : x.x) = fmaf(static_cast<float>(low), 0x1p-63f, static_cast<float>(rest) * 0x1p-31f);
+        angle[k + h] += turn[k + h];
+      }
+      const float2 sn = sin_pi(x), cs = cos_pi(x);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float a = h ? cs.y : cs.x, b = h ? sn.y : sn.x;
+        const bool swap = quarter[h] & 1;
+        // quarters 1 and 2, and 2 and 3, are negative
+        c[k + h] = __uint_as_float(__float_as_uint(swap ? b : a) ^ ((quarter[h] + 1) & 2) << 30) * magnitude;
+        s[k + h] = __uint_as_float(__float_as_uint(swap ? a : b) ^ (quarter[h] & 2) << 30) * magnitude;
+      }
     }
     float* row = out + p * dim + 4 * q;
     *reinterpret_cast<float4*>(row) = make_float4(c[0], c[1], c[2], c[3]);
@@ -107,7 +151,7 @@ __device__ __forceinline__ uint4 narrow(const float2 (&f)[4]) {
 // own are in flight, and the angles are read once for all of them.  Issue comes
 // next after memory: layout and norm are template arguments, the arithmetic is
 // packed, and few registers leave many warps resident (24577 tokens x 40 heads x 128
-// dims with norm 86 us; 138 with one code for all and the items' values kept).
+// dims with norm 89 us, 5.8 TB/s; 138 with one code for all and the items' values kept).
 // kTurn: items of a lane that may turn, its first ones.
 template <bool kHalf, int kItems, int kTurn, int kIter, bool kNorm, bool kInter>
 __global__ void __launch_bounds__(128) rope_heads_kernel(const RopeHeadsParams p) {

@@ -108,7 +108,7 @@ struct GatherParams {
   long long out_stride;
   int32_t* status;
 };
-cudaError_t launch_gather(const GatherParams& p, bool fp8, int sms, cudaStream_t st);
+cudaError_t launch_gather(const GatherParams& p, bool fp8, cudaStream_t st);
 
 // The bookkeeping of a page pool.
 struct PageState {

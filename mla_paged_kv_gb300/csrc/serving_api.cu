@@ -768,7 +768,7 @@ int mla_cache_gather(const void* d_cache, int cache_dtype, int num_pages, const 
   p.out = static_cast<uint16_t*>(d_out);
   p.out_stride = out_stride;
   p.status = d_status;
-  return launched(launch_gather(p, cache_dtype == MLA_DTYPE_FP8_RECORD, sms, to_stream(stream)));
+  return launched(launch_gather(p, cache_dtype == MLA_DTYPE_FP8_RECORD, to_stream(stream)));
 }
 
 int mla_chunk_num_parts(void) {
