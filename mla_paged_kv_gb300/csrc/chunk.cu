@@ -1297,7 +1297,7 @@ __device__ void plan_schedule(const ChunkPlanParams& p, int v, int units, int* c
     if (u < units) {
       const int tiles = tiles_of(unit_int(u, 4));
       mine = tiles > 0 ? tiles * tile_cost(unit_int(u, kPages0), v) + kFixedCost : 0;
-      p.cost[u] = mine;
+      out.cost[u] = mine;
     }
     long long all;
     block_scan(static_cast<long long>(mine), s_warp64, &all);
@@ -1313,12 +1313,12 @@ __device__ void plan_schedule(const ChunkPlanParams& p, int v, int units, int* c
     for (int u0 = tid; u0 < units; u0 += kAhead * p.parts) {
       int c[kAhead];
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) c[k] = u0 + k * p.parts < units ? p.cost[u0 + k * p.parts] : 0;
+      for (int k = 0; k < kAhead; ++k) c[k] = u0 + k * p.parts < units ? out.cost[u0 + k * p.parts] : 0;
 #pragma unroll
       for (int k = 0; k < kAhead; ++k)
         if (c[k] > 0 && c[k] <= room) {
           room -= c[k];
-          p.cost[u0 + k * p.parts] = 0;
+          out.cost[u0 + k * p.parts] = 0;
           unit_int(u0 + k * p.parts, kSchedule + 2 * v + 1) = 1 + kWhole;
         }
     }
@@ -1329,14 +1329,14 @@ __device__ void plan_schedule(const ChunkPlanParams& p, int v, int units, int* c
   long long sum = 0;
   for (int u0 = 0; u0 < units; u0 += kPlanThreads) {
     const int u = u0 + tid;
-    const long long mine = u < units ? p.cost[u] : 0;
+    const long long mine = u < units ? out.cost[u] : 0;
     int all;
     long long all_cost;
     const int at = block_scan(mine > 0 ? 1 : 0, s_warp, &all);
     const long long before = block_scan(mine, s_warp64, &all_cost);
     if (mine > 0) {
       out.rest[rest + at] = u;
-      p.prefix[rest + at] = sum + before;
+      out.prefix[rest + at] = sum + before;
     }
     rest += all;
     sum += all_cost;
@@ -1351,14 +1351,14 @@ __device__ void plan_schedule(const ChunkPlanParams& p, int v, int units, int* c
         int lo = 0, hi = rest;  // the last entry that begins at or before x
         while (hi - lo > 1) {
           const int mid = (lo + hi) / 2;
-          if (p.prefix[mid] <= x)
+          if (out.prefix[mid] <= x)
             lo = mid;
           else
             hi = mid;
         }
         e = lo;
         const int u = out.rest[e], tiles = tiles_of(unit_int(u, 4)), per = tile_cost(unit_int(u, kPages0), v);
-        t = static_cast<int>(min(max(x - p.prefix[e] - kFixedCost, 0ll) / per, static_cast<long long>(tiles)));
+        t = static_cast<int>(min(max(x - out.prefix[e] - kFixedCost, 0ll) / per, static_cast<long long>(tiles)));
         if (t == tiles) {
           ++e;
           t = 0;
@@ -1398,14 +1398,15 @@ __device__ void plan_schedule(const ChunkPlanParams& p, int v, int units, int* c
   }
 }
 
-// The plan: units of all requests, in order, and both schedules.  One block, made
-// once for a batch.
+// The plan: units of all requests, in order, and both schedules, a block each (what
+// they have in common both find and write alike).  Made once for a batch: 64 requests
+// x up to 6 tokens x 128 heads 11 us, the latency of a few passes over the units.
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPlanParams p) {
   __shared__ long long s_warp64[32];
   __shared__ int s_warp[32];
   __shared__ int broken;
   __shared__ int cut_u[kMaxChunkParts + 1], cut_t[kMaxChunkParts + 1];
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, v = blockIdx.x;
   if (tid == 0) broken = 0;
   __syncthreads();
   for (int b = tid; b < p.batch; b += kPlanThreads) {
@@ -1421,11 +1422,10 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPla
       report(p.status, MLA_ERR_BAD_INDEX);
       p.head[kHeadWhole] = 0;
       p.head[kHeadCausal] = p.causal;
-      p.head[kHeadFix] = p.head[kHeadFix + 1] = 0;
+      p.head[kHeadFix + v] = 0;
     }
     for (int b = tid; b <= p.batch; b += kPlanThreads) p.conv[b] = 0;
-    for (int v = 0; v < 2; ++v)
-      for (int i = tid; i < p.parts * MLA_SCHED_INTS; i += kPlanThreads) p.schedule[v].sched[i] = 0;
+    for (int i = tid; i < p.parts * MLA_SCHED_INTS; i += kPlanThreads) p.schedule[v].sched[i] = 0;
     return;
   }
   // first unit of each request, and its first page among those of requests that are
@@ -1452,7 +1452,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPla
   if (tid == 0) {
     p.head[kHeadWhole] = units;
     p.head[kHeadCausal] = p.causal;
-    p.head[kHeadFix] = p.head[kHeadFix + 1] = 0;
+    p.head[kHeadFix + v] = 0;
   }
   __syncthreads();
   for (int u = tid; u < units; u += kPlanThreads) {
@@ -1471,15 +1471,11 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPla
     int4* e = reinterpret_cast<int4*>(p.units + static_cast<long long>(u) * kChunkUnitInts);
     e[0] = make_int4(tok0 * p.h_q + rel, rows, rel, lo);
     e[1] = make_int4(len, limit0, p.conv[lo + 1] > p.conv[lo] ? p.conv[lo] : -1, 0);
-    e[2] = make_int4(0, len > 0 ? 1 : 0, 0, len > 0 ? 1 : 0);
-    if (len == 0)
-      for (int v = 0; v < 2; ++v) p.schedule[v].fix[atomicAdd(&p.head[kHeadFix + v], 1)] = u;  // (in any order: no result depends on it)
+    reinterpret_cast<int2*>(e + 2)[v] = make_int2(0, len > 0 ? 1 : 0);
+    if (len == 0) p.schedule[v].fix[atomicAdd(&p.head[kHeadFix + v], 1)] = u;  // (in any order: no result depends on it)
   }
   __syncthreads();
-  for (int v = 0; v < 2; ++v) {
-    plan_schedule(p, v, units, cut_u, cut_t, s_warp, s_warp64);
-    __syncthreads();
-  }
+  plan_schedule(p, v, units, cut_u, cut_t, s_warp, s_warp64);
 }
 static_assert(kMaxChunkParts <= kPlanThreads, "a thread a cut");
 
@@ -1496,11 +1492,11 @@ ChunkPlanLayout chunk_plan_layout(int batch, int total_q, int h_q, int parts) {
     c.sched = at;
     c.fix = c.sched + up(static_cast<size_t>(parts) * MLA_SCHED_INTS * 4);
     c.rest = c.fix + up(units * 4);
-    at = c.rest + up(units * 4);
+    c.cost = c.rest + up(units * 4);
+    c.prefix = c.cost + up(units * 4);
+    at = c.prefix + up(units * 8);
   }
-  z.cost = at;
-  z.prefix = z.cost + up(units * 4);
-  z.first = z.prefix + up(units * 8);
+  z.first = at;
   z.conv = z.first + up(static_cast<size_t>(batch) * 4);
   z.made = z.conv + up((static_cast<size_t>(batch) + 1) * 4);
   z.bytes = z.made + up((2 * static_cast<size_t>(batch) + 1) * 4);
@@ -1508,7 +1504,7 @@ ChunkPlanLayout chunk_plan_layout(int batch, int total_q, int h_q, int parts) {
 }
 
 cudaError_t launch_chunk_plan(const ChunkPlanParams& p, cudaStream_t st) {
-  ck::chunk_plan_kernel<<<1, ck::kPlanThreads, 0, st>>>(p);
+  ck::chunk_plan_kernel<<<2, ck::kPlanThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 

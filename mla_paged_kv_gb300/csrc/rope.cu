@@ -151,7 +151,7 @@ __device__ __forceinline__ uint4 narrow(const float2 (&f)[4]) {
 // own are in flight, and the angles are read once for all of them.  Issue comes
 // next after memory: layout and norm are template arguments, the arithmetic is
 // packed, and few registers leave many warps resident (24577 tokens x 40 heads x 128
-// dims with norm 89 us, 5.8 TB/s; 138 with one code for all and the items' values kept).
+// dims with norm 94 us, 5.5 TB/s; 138 with one code for all and the items' values kept).
 // kTurn: items of a lane that may turn, its first ones.
 template <bool kHalf, int kItems, int kTurn, int kIter, bool kNorm, bool kInter>
 __global__ void __launch_bounds__(128) rope_heads_kernel(const RopeHeadsParams p) {

@@ -162,20 +162,20 @@ constexpr int kConvertUnits = 3;         // units from which a request's FP8 pag
 enum : int { kHeadWhole = 0, kHeadCausal = 1, kHeadFix = 2 };  // header: units, causal, units for the combine (2)
 struct ChunkPlanLayout {
   int max_units;
-  size_t units, cost, prefix, first, conv, made, bytes;
+  size_t units, first, conv, made, bytes;
   struct {
-    size_t sched, fix, rest;
+    size_t sched, fix, rest, cost, prefix;
   } schedule[2];  // for 16-bit caches, and FP8 records
 };
 ChunkPlanLayout chunk_plan_layout(int batch, int total_q, int h_q, int parts);
 struct ChunkSchedule {
-  int32_t *sched, *fix, *rest;
+  int32_t *sched, *fix, *rest, *cost;
+  long long* prefix;
 };
 struct ChunkPlanParams {
   const int32_t *cu, *lens;
   int batch, total_q, h_q, causal, parts;
-  int32_t *head, *units, *cost, *first, *conv, *made;
-  long long* prefix;
+  int32_t *head, *units, *first, *conv, *made;
   ChunkSchedule schedule[2];
   int32_t* status;
 };

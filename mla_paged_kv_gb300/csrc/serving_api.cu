@@ -814,12 +814,11 @@ int mla_chunk_get_plan(const int32_t* d_cu_seqlens_q, const int32_t* d_cache_seq
   p.head = ints(0);
   p.units = ints(z.units);
   for (int v = 0; v < 2; ++v)
-    p.schedule[v] = ChunkSchedule{ints(z.schedule[v].sched), ints(z.schedule[v].fix), ints(z.schedule[v].rest)};
-  p.cost = ints(z.cost);
+    p.schedule[v] = ChunkSchedule{ints(z.schedule[v].sched), ints(z.schedule[v].fix), ints(z.schedule[v].rest),
+                                  ints(z.schedule[v].cost), reinterpret_cast<long long*>(plan + z.schedule[v].prefix)};
   p.first = ints(z.first);
   p.conv = ints(z.conv);
   p.made = ints(z.made);
-  p.prefix = reinterpret_cast<long long*>(plan + z.prefix);
   p.status = d_status;
   return launched(launch_chunk_plan(p, to_stream(stream)));
 }
