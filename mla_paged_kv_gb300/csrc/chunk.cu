@@ -1178,30 +1178,28 @@ __global__ void __launch_bounds__(256)
 
 // Rows of the units that were cut (their pieces merged) and of those without
 // keys (zeros):  out = sum_s e^(lse_s - m) O_s / Z, lse = m + ln Z.
-// A warp a row, 16 columns a lane; four pieces in flight.  Bound by the latency of
-// a few reads: the rows are at most 128 for each pair.
+// A warp a row, 16 columns a lane; four pieces in flight, their lse beside them.
+// Bound by latency, the rows being at most 128 for each pair: about 5 us behind the
+// attention of 64 requests x up to 6 drafts x 128 heads (6.5 with pieces loaded after
+// the maximum of their lse, and units found after the wait).
 __global__ void __launch_bounds__(128) chunk_combine_kernel(const ChunkParams p) {
   constexpr int kAhead = 4;
   const int lane = threadIdx.x & 31;
-  pdl_wait_prior_grid();  // (also by blocks without work: a plan made next must not meet the kernel before)
-  pdl_launch_dependents();  // the next call's kernel sets up under this one (64 requests x up to 6 drafts x 128 heads, calls in a row: 148 -> 145 us)
+  // what the plan says does not wait for the kernel before
   const long long rows = static_cast<long long>(p.head[kHeadFix + p.schedule]) * kRowsPerBlock;
-  for (long long i = blockIdx.x * 4ll + (threadIdx.x >> 5); i < rows; i += gridDim.x * 4ll) {
-    const Unit unit = load_unit(p, p.fix[i / kRowsPerBlock]);
+  const long long first = blockIdx.x * 4ll + (threadIdx.x >> 5);
+  Unit unit{};
+  if (first < rows) unit = load_unit(p, p.fix[first / kRowsPerBlock]);
+  pdl_wait_prior_grid();  // (also by blocks without work: a plan made next must not meet the kernel before)
+  pdl_launch_dependents();  // the next call's kernel sets up under this one (the same case, calls in a row: 148 -> 145 us)
+  for (long long i = first; i < rows; i += gridDim.x * 4ll) {
+    if (i != first) unit = load_unit(p, p.fix[i / kRowsPerBlock]);
     const int r = static_cast<int>(i % kRowsPerBlock);
     if (r >= unit.rows) continue;
     const long long at = static_cast<long long>(unit.slot) * kRowsPerBlock + r;
-    float m = -INFINITY;
-    for (int s = lane; s < unit.parts; s += 32) m = fmaxf(m, p.lse_accum[at + s * kRowsPerBlock]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float4 acc[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-    float z = 0.f;
-    for (int s0 = 0; s0 < unit.parts; s0 += kAhead) {
-      float4 v[kAhead][4];
-      float e[kAhead];
+    float4 v[kAhead][4];
+    float e[kAhead];
+    auto load = [&](int s0) {
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         const bool in = s0 + k < unit.parts;
@@ -1212,6 +1210,23 @@ __global__ void __launch_bounds__(128) chunk_combine_kernel(const ChunkParams p)
           v[k][c] = in ? *reinterpret_cast<const float4*>(p.o_accum + a * kDv + 128 * c + 4 * lane)
                        : make_float4(0.f, 0.f, 0.f, 0.f);
       }
+    };
+    load(0);
+    float m = -INFINITY;
+    if (unit.parts > kAhead) {
+      for (int s = lane; s < unit.parts; s += 32) m = fmaxf(m, p.lse_accum[at + s * kRowsPerBlock]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    } else {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) m = fmaxf(m, e[k]);
+    }
+    float4 acc[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float z = 0.f;
+    for (int s0 = 0; s0 < unit.parts; s0 += kAhead) {
+      if (s0 > 0) load(s0);
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         const float w = e[k] == -INFINITY ? 0.f : expf(e[k] - m);
