@@ -1,8 +1,10 @@
 /*
  * mla_serving.h -- C ABI of the operators around the decode of
  * mla_paged_kv.h: what fills a paged latent cache, what shares, frees and
- * moves its pages, attention over the prompts that fill it, and the decode
- * that reads a prefix many requests share once for all of them.
+ * moves its pages, attention over the prompts that fill it, the decode
+ * that reads a prefix many requests share once for all of them, and what takes
+ * chunks of new tokens through it: rotary tables, the rotation of heads, rows
+ * read back, and attention of ragged chunks over their requests' pages.
  *
  * The conventions are those of mla_paged_kv.h (types, status codes, the
  * stream, caller-owned memory, asynchronous calls, errors before any launch
