@@ -57,7 +57,7 @@ __device__ __forceinline__ float2 cos_pi(float2 x) {
 // and x^10 leave 2^-29 of it there.
 // A thread keeps four pairs, two at a time in packed arithmetic, and steps through
 // positions, so that an angle is one addition.  Bound by the launch for few positions
-// (4096 x 64: 4.2 us), for many by issue, with half of it left to the writes (160000 x
+// (4096 x 64: 4.2 us), for many by issue, with half of it left to the writes (163840 x
 // 64: 41 MB in 10.4 us; 14.5 with the library's sincospif).
 __global__ void __launch_bounds__(256)
     rope_table_kernel(const RopeSteps f, int dim, float magnitude, unsigned long long first, int positions,
