@@ -397,7 +397,7 @@ int mla_chunk_get_plan(const int32_t* d_cu_seqlens_q, const int32_t* d_cache_seq
  *                 not fit are converted by each block that reads them (slower, the
  *                 same results)
  *   d_out         [total_q, h_q, 512] of out_type (bf16, fp16 or fp32), d_lse fp32
- *                 [total_q, h_q]
+ *                 [total_q, h_q]; no output or workspace may overlap an input
  * A block-table entry outside the pool (or past max_pages) masks its 64 keys and
  * is reported, MLA_ERR_BAD_INDEX.  Slots of a page behind a request's last key may
  * hold anything; keys that any of its queries sees must be finite for all of them. */

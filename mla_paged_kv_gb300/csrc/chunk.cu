@@ -44,7 +44,7 @@
 // FP8 records: below.  1.9 us a tile, bound by the softmax threads' chain (five sums
 // of a score from TMEM and their scales from shared memory, 0.2 us each); tiles whose
 // values no other unit shares, 2.4 us, by their conversion.  43 requests, 3 chunks of
-// up to 400 tokens among single ones, 16 heads over up to 3400 keys: 113 us.
+// up to 400 tokens among single ones, 16 heads over up to 3400 keys: 114 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -552,8 +552,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
   cluster_arrive();  // the other CTA's barriers are ready before anything arrives there
   cluster_wait();
   const uint32_t tmem = *tmem_slot;
-  // the kernel before is done from here on (FP8 records: the conversion's own wait; only some roles need its results)
-  if constexpr (!kFp8) pdl_wait_prior_grid();
+  pdl_wait_prior_grid();  // the kernel before is done from here on
   pdl_launch_dependents();
   const Run run = load_run(p);
   const int causal = p.head[kHeadCausal];
@@ -563,7 +562,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
   if (kFp8 && warp >= kWarpV) {
     // ------------------------------------------------------------ FP8 records: V converted
     const uint32_t bar0 = mapa_shared(smem_u32(bars), 0);
-    pdl_wait_prior_grid();  // the pages that are converted before
     const bool ok = convert_v(p, run, rank, warp - kWarpV, lane, sV, &v_map, bars, bar0, abort_flag, kWaitNs);
     if (!ok && lane == 0) {
       fail(abort_flag, p.status);
@@ -581,7 +579,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
     auto expect = [&](int bar, uint32_t bytes) { mbar_arrive_expect_tx_remote_relaxed(bar0 + 8 * bar, bytes); };
     uint32_t n = 0, tails = 0;  // stages (or units of Q) and tail pages so far
     uint32_t scaled = 0;        // FP8 records: tiles whose scales are written
-    if (kFp8 && warp == kWarpQ) pdl_wait_prior_grid();  // the queries' codes
     while (ok && walk_next(p, run, w)) {
       if (warp == kWarpQ) {
         if (n >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&bars[Q_EMPTY], (n - 1) & 1, abort_flag, kWaitNs));
@@ -833,7 +830,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
       }
       return true;
     };
-    if (kFp8) pdl_wait_prior_grid();  // the queries' factors
     bool more = enter();
     while (more) {
       float ref = -INFINITY, l = 0.f;
@@ -1185,7 +1181,7 @@ __global__ void __launch_bounds__(256)
 __global__ void __launch_bounds__(128) chunk_combine_kernel(const ChunkParams p) {
   constexpr int kAhead = 4;
   const int lane = threadIdx.x & 31;
-  // what the plan says does not wait for the kernel before
+  // what the plan says does not wait for the kernel before, which has waited for the plan
   const long long rows = static_cast<long long>(p.head[kHeadFix + p.schedule]) * kRowsPerBlock;
   const long long first = blockIdx.x * 4ll + (threadIdx.x >> 5);
   Unit unit{};

@@ -282,6 +282,47 @@ def test_pages_that_several_rows_and_places_share(fp8):
     c.check(out, lse, True)
 
 
+def test_one_plan_for_caches_of_every_kind():
+    cases = [Case([70, 1, 3, 140], [200, 900, 64, 0], heads=H, seed=97, dtype=FP16 if k == 1 else BF16, fp8=k == 2)
+             for k in range(3)]
+    on = [c.device() for c in cases]
+    pl = mla.plan_chunks(on[0][4], on[0][3], 214, H)
+    for _ in range(2):
+        for c, (q, cache, table, lens, cu) in zip(cases, on):
+            out, lse = mla.chunk_attention(q, cache, table, lens, cu, pl=pl)
+            c.check(out, lse, True)
+            alone = mla.chunk_attention(q, cache, table, lens, cu)
+            assert torch.equal(out, alone[0]) and torch.equal(lse, alone[1])
+
+
+@caches
+def test_calls_back_to_back(fp8):
+    """Each call's first kernel begins while the call before ends: what a call reads is what the one before wrote."""
+    c = Case([9, 1, 60], [300, 700, 64], heads=H, seed=98, fp8=fp8)
+    q, cache, table, lens, cu = c.device()
+    pl, status = mla.plan_chunks(cu, lens, 70, H), i32([0])
+    pl.workspace = mla.chunk_workspace(pl, 4)
+    outs = [(torch.zeros(70, H, 512, dtype=BF16, device="cuda"), torch.zeros(70, H, device="cuda")) for _ in range(2)]
+
+    def chain(wait):
+        x = q.clone()
+        for i in range(12):
+            out, lse = outs[i % 2]
+            mla.mla_chunk_attention_fwd(x, cache, table, pl, out, lse, status)
+            if wait:
+                torch.cuda.synchronize()
+            x[..., :512] = out
+            mla.mla_chunk_attention_fwd(x, cache, table, pl, out, lse, status)
+            if wait:
+                torch.cuda.synchronize()
+        return [t.clone() for pair in outs for t in pair]
+
+    want = chain(True)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(chain(False), want))
+    assert int(status) == 0
+
+
 @caches
 def test_nothing_to_do(fp8):
     c = Case([2], [100], heads=H, seed=96, fp8=fp8)
