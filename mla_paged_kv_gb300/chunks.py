@@ -46,13 +46,8 @@ def _frequencies(dim, base, scaling, factor, original, low, high):
     return freq, size.value
 
 
-def _table(freq, magnitude, first, out, stream):
-    dev = out.get_device()
-    ptr = _p(out, _FP32, 2, dev, "cos_sin")
-    positions, dim = out.shape
-    if len(freq) * 2 != dim:
-        raise ValueError("cos_sin must have two columns a frequency")
-    rc = load_library().mla_rope_table(freq, dim, magnitude, first, positions, ptr, _q(stream, dev))
+def _table(freq, dim, magnitude, first, positions, out, dev, stream):
+    rc = load_library().mla_rope_table(freq, dim, magnitude, first, positions, out.data_ptr(), _q(stream, dev))
     if rc:
         _check(rc, "mla_rope_table")
 
@@ -66,7 +61,12 @@ def mla_rope_frequencies(dim, base, scaling, factor, original, low, high):
 
 def mla_rope_table(freq, magnitude, first, cos_sin, stream=None):
     """The table of positions first .. first + cos_sin.shape[0] - 1 into cos_sin fp32 [positions, dim]."""
-    _table((_D * len(freq))(*freq), float(magnitude), int(first), cos_sin, stream)
+    dev = cos_sin.get_device()
+    _p(cos_sin, _FP32, 2, dev, "cos_sin")
+    positions, dim = cos_sin.shape
+    if len(freq) * 2 != dim:
+        raise ValueError("cos_sin must have two columns a frequency")
+    _table((_D * len(freq))(*freq), dim, float(magnitude), int(first), positions, cos_sin, dev, stream)
 
 
 def _scaling(scaling, high):
@@ -91,7 +91,7 @@ def rope_table(positions, dim=64, base=10000.0, scaling="none", factor=1.0, orig
     code, high = _scaling(scaling, high)
     freq, size = _frequencies(dim, base, code, factor, original, low, high)
     out = torch.empty((positions, dim), dtype=_FP32, device=device)
-    _table(freq, size if magnitude is None else magnitude, first, out, None)
+    _table(freq, dim, size if magnitude is None else magnitude, first, positions, out, out.get_device(), None)
     return out
 
 
@@ -134,11 +134,28 @@ def _output(out, tokens, dim, others, same):
             raise ValueError("an output overlaps another tensor of the call")
 
 
+def _fresh(t, tokens, dim):
+    """A new tensor of the shape of t, which _heads has passed, and what that says of it."""
+    heads = t.shape[1]
+    out = torch.empty((tokens, heads, dim), dtype=t.dtype, device=t.device)
+    ptr, row = out.data_ptr(), heads * dim
+    return out, (ptr, row, dim, heads, ptr + 2 * tokens * row)
+
+
 def mla_rope_heads(x, out, cos_sin, status, cache_seqlens=None, cu_seqlens=None, positions=None, k=None, k_out=None,
                    x_weight=None, k_weight=None, norm_eps=1e-6, offset=None, interleaved=False, stream=None):
     """x [tokens, heads, dim] (and k [tokens, k_heads, dim]), bf16 or fp16, into out (k_out), which may be x (k)
     itself; strides free, multiples of 8.  cos_sin fp32 [positions, rope_dim] turns dims offset .. offset + rope_dim
     (default: the last ones) of every head at positions [tokens], or at those of cache_append; None: norm only."""
+    if out is None or (k is not None and k_out is None):
+        raise ValueError("x needs out, and k needs k_out")
+    _rope(x, out, cos_sin, status, cache_seqlens, cu_seqlens, positions, k, k_out, x_weight, k_weight, norm_eps, offset,
+          interleaved, stream)
+
+
+def _rope(x, out, cos_sin, status, cache_seqlens, cu_seqlens, positions, k, k_out, x_weight, k_weight, norm_eps, offset,
+          interleaved, stream):
+    """The checks and the call of mla_rope_heads; allocates out and k_out if not given, and returns them."""
     dt = x.dtype
     code = _DTYPE_CODE16.get(dt)
     if code is None:
@@ -148,25 +165,30 @@ def mla_rope_heads(x, out, cos_sin, status, cache_seqlens=None, cu_seqlens=None,
     dev = x.get_device()
     tokens, _, dim = x.shape
     src = _heads(x, dt, tokens, dim, dev, "x")
-    dst = _heads(out, dt, tokens, dim, dev, "out")
     heads = src[3]
-    if heads == 0 or dst[3] != heads:
-        raise ValueError("out must have the heads of x, at least one")
     none = (0, 0, 0, 0, 0)
     k_src = k_dst = none
     if k is not None:
-        if k_out is None:
-            raise ValueError("k needs k_out")
         k_src = _heads(k, dt, tokens, dim, dev, "k")
-        k_dst = _heads(k_out, dt, tokens, dim, dev, "k_out")
-        if k_src[3] == 0 or k_dst[3] != k_src[3]:
-            raise ValueError("k_out must have the heads of k, at least one")
     elif k_out is not None or k_weight is not None:
         raise ValueError("k_out and k_weight need k")
-    if tokens:
-        _output(dst, tokens, dim, (src, k_src), src)
-        if k is not None:
-            _output(k_dst, tokens, dim, (src, k_src, dst), k_src)
+    if out is None:
+        out, dst = _fresh(x, tokens, dim)
+    else:
+        dst = _heads(out, dt, tokens, dim, dev, "out")
+        if tokens:
+            _output(dst, tokens, dim, (src, k_src), src)
+    if heads == 0 or dst[3] != heads:
+        raise ValueError("out must have the heads of x, at least one")
+    if k is not None:
+        if k_out is None:
+            k_out, k_dst = _fresh(k, tokens, dim)
+        else:
+            k_dst = _heads(k_out, dt, tokens, dim, dev, "k_out")
+            if tokens:
+                _output(k_dst, tokens, dim, (src, k_src, dst), k_src)
+        if k_src[3] == 0 or k_dst[3] != k_src[3]:
+            raise ValueError("k_out must have the heads of k, at least one")
     w_ptr = kw_ptr = 0
     if x_weight is not None:
         w_ptr = _p(x_weight, dt, 1, dev, "x_weight")
@@ -205,6 +227,7 @@ def mla_rope_heads(x, out, cos_sin, status, cache_seqlens=None, cu_seqlens=None,
     _call(_ROPE_HEADS, "mla_rope_heads", *src[:3], *dst[:3], heads, w_ptr, *k_src[:3], *k_dst[:3], k_src[3], kw_ptr,
           dim, code, tokens, rope, offset, 1 if interleaved else 0, norm_eps, pos_ptr, cu_ptr,
           lens_ptr, batch, cos_ptr, max_pos, _p(status, _INT32, 1, dev, "status"), _q(stream, dev))
+    return out, k_out
 
 
 def rope_heads(x, cos_sin, cache_seqlens=None, cu_seqlens=None, positions=None, out=None, k=None, k_out=None,
@@ -212,12 +235,8 @@ def rope_heads(x, cos_sin, cache_seqlens=None, cu_seqlens=None, positions=None, 
     """Rotate part of each head of x (and of k), each optionally RMS-normalised first; returns out, with k (out,
     k_out).  out and k_out default to new tensors; x and k themselves turn them in place."""
     st = _status(status, x)
-    if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    mla_rope_heads(x, out, cos_sin, st, cache_seqlens, cu_seqlens, positions, k, k_out, norm_weight, k_norm_weight,
-                   norm_eps, offset, interleaved)
+    out, k_out = _rope(x, out, cos_sin, st, cache_seqlens, cu_seqlens, positions, k, k_out, norm_weight, k_norm_weight,
+                       norm_eps, offset, interleaved, None)
     if status is None:
         check_status(st, "mla_rope_heads")
     return out if k is None else (out, k_out)
@@ -242,6 +261,13 @@ def _cache(cache, dev, name):
 def mla_cache_gather(cache, block_table, cu_seqlens, out, status, starts=None, stream=None):
     """Rows of the cache into out [total, 576] (the cache's type; bf16 of FP8 records), row stride free: row t of
     request b, cu_seqlens[b] <= t < cu_seqlens[b + 1], from position starts[b] (0) + t - cu_seqlens[b]."""
+    if out is None:
+        raise ValueError("out is needed")
+    _rows(cache, block_table, cu_seqlens, out, 0, starts, status, stream)
+
+
+def _rows(cache, block_table, cu_seqlens, out, rows, starts, status, stream):
+    """The checks and the call of mla_cache_gather; allocates out, of `rows` rows, if not given, and returns it."""
     dev = cache.get_device()
     ptr, code, pages = _cache(cache, dev, "cache")
     table_ptr = _p(block_table, _INT32, 2, dev, "block_table")
@@ -254,29 +280,33 @@ def mla_cache_gather(cache, block_table, cu_seqlens, out, status, starts=None, s
         starts_ptr = _p(starts, _INT32, 1, dev, "starts")
         if starts.shape[0] != batch:
             raise ValueError("starts must have one entry a request")
-    want = torch.bfloat16 if cache.dtype is _UINT8 else cache.dtype
-    if out.dtype is not want:
-        raise TypeError(f"out must be {want}, got {out.dtype}")
-    stride = out.stride()
-    if len(stride) != 2 or out.shape[1] != 576 or stride[1] != 1 or out.get_device() != dev:
-        raise ValueError(f"out must be [rows, 576] with contiguous rows, on cuda:{dev}")
-    rows, at = out.shape[0], out.data_ptr()
-    if rows and at < ptr + cache.numel() * cache.element_size() and ptr < at + 2 * ((rows - 1) * stride[0] + 576):
-        raise ValueError("out overlaps the cache")
+    want, step = torch.bfloat16 if code == DTYPE_FP8_RECORD else cache.dtype, 576
+    if out is None:
+        out = torch.empty((rows, 576), dtype=want, device=cache.device)
+        at = out.data_ptr()
+    else:
+        if out.dtype is not want:
+            raise TypeError(f"out must be {want}, got {out.dtype}")
+        stride = out.stride()
+        if len(stride) != 2 or out.shape[1] != 576 or stride[1] != 1 or out.get_device() != dev:
+            raise ValueError(f"out must be [rows, 576] with contiguous rows, on cuda:{dev}")
+        rows, at = out.shape[0], out.data_ptr()
+        if rows > 1:
+            step = stride[0]
+        if rows and at < ptr + cache.numel() * cache.element_size() and ptr < at + 2 * ((rows - 1) * step + 576):
+            raise ValueError("out overlaps the cache")
     _call(_GATHER, "mla_cache_gather", ptr, code, pages, table_ptr, max_pages, cu_ptr, starts_ptr, batch, rows,
-          out.data_ptr(), stride[0] if rows > 1 else 576, _p(status, _INT32, 1, dev, "status"), _q(stream, dev))
+          at, step, _p(status, _INT32, 1, dev, "status"), _q(stream, dev))
+    return out
 
 
 def cache_gather(cache, block_table, cu_seqlens, total=None, starts=None, out=None, status=None):
     """Rows of a paged cache as packed rows [total, 576] (see mla_cache_gather).  total defaults to the last offset,
     which reads it from the GPU."""
     st = _status(status, cache)
-    if out is None:
-        if total is None:
-            total = int(cu_seqlens[-1])
-        dt = torch.bfloat16 if cache.dtype is _UINT8 else cache.dtype
-        out = torch.empty(total, 576, dtype=dt, device=cache.device)
-    mla_cache_gather(cache, block_table, cu_seqlens, out, st, starts)
+    if out is None and total is None:
+        total = int(cu_seqlens[-1])
+    out = _rows(cache, block_table, cu_seqlens, out, total, starts, st, None)
     if status is None:
         check_status(st, "mla_cache_gather")
     return out

@@ -83,7 +83,8 @@ def test_chunk_plan_refusals(change, want):
     (dict(dt=1), INVALID), (dict(dt=4), INVALID), (dict(ot=3), INVALID), (dict(scale=0.0), INVALID),
     (dict(scale=float("nan")), INVALID), (dict(pbytes=64), INVALID), (dict(wbytes=64), INVALID),
     (dict(pages=0), INVALID), (dict(width=0), INVALID), (dict(q=OFF8), INVALID), (dict(kv=OFF8), INVALID),
-    (dict(cu=ODD), INVALID), (dict(lens=ODD), INVALID), (dict(width=(1 << 18) + 1), UNSUPPORTED)])
+    (dict(cu=ODD), INVALID), (dict(lens=ODD), INVALID), (dict(width=(1 << 18) + 1), UNSUPPORTED),
+    (dict(dt=3, wbytes=2 * 4 * 128 * 513 * 4 + 160 * 1040 - 1), INVALID)])
 @pytest.mark.parametrize("name", ["mla_chunk_attention_fwd", "mla_test_chunk_timeout"])
 def test_chunk_refusals(name, change, want):
     assert getattr(mla.load_library(), name)(*{**CHUNK, **change}.values()) == want
