@@ -44,7 +44,7 @@
 // FP8 records: below.  1.9 us a tile, bound by the softmax threads' chain (five sums
 // of a score from TMEM and their scales from shared memory, 0.2 us each); tiles whose
 // values no other unit shares, 2.4 us, by their conversion.  43 requests, 3 chunks of
-// up to 400 tokens among single ones, 16 heads over up to 3400 keys: 114 us.
+// up to 400 tokens among single ones, 16 heads over up to 3400 keys: 112 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -830,6 +830,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
       }
       return true;
     };
+    const int dim0 = 256 * kh + 128 * ch;
+    // 8 words of a row (of 16 it + 8 up + lane / 4): word n of lane q4 -> word q4 of
+    // lane n, within four lanes and four words: each then holds whole 16-byte pieces,
+    // and a store of the warp covers 64 bytes of 8 rows
+    auto store16 = [&](uint32_t (&x)[8], int it, int up, long long first, int rows) {
+      const int q4 = lane & 3, orow = row - lane + 16 * (it & 1) + 8 * up + (lane >> 2);
+      uint16_t* dst = static_cast<uint16_t*>(p.out) + (first + orow) * kDv + dim0 + 64 * (it >> 1) + 8 * q4;
+#pragma unroll
+      for (int g = 0; g < 8; g += 4) {
+        uint32_t* y = x + g;
+        {
+          const bool odd = q4 & 1;
+          const uint32_t s0 = odd ? y[0] : y[1], s1 = odd ? y[2] : y[3];
+          const uint32_t r0 = __shfl_xor_sync(0xffffffffu, s0, 1), r1 = __shfl_xor_sync(0xffffffffu, s1, 1);
+          if (odd) {
+            y[0] = r0;
+            y[2] = r1;
+          } else {
+            y[1] = r0;
+            y[3] = r1;
+          }
+        }
+        {
+          const bool odd = q4 & 2;
+          const uint32_t s0 = odd ? y[0] : y[2], s1 = odd ? y[1] : y[3];
+          const uint32_t r0 = __shfl_xor_sync(0xffffffffu, s0, 2), r1 = __shfl_xor_sync(0xffffffffu, s1, 2);
+          if (odd) {
+            y[0] = r0;
+            y[1] = r1;
+          } else {
+            y[2] = r0;
+            y[3] = r1;
+          }
+        }
+        if (orow < rows) *reinterpret_cast<uint4*>(dst + 8 * g) = make_uint4(y[0], y[1], y[2], y[3]);
+      }
+    };
     bool more = enter();
     while (more) {
       float ref = -INFINITY, l = 0.f;
@@ -989,72 +1026,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
       tc_fence_after();
       l = (sum[0] + sum[kCtaRows]) + (sum[2 * kCtaRows] + sum[3 * kCtaRows]);
       const float inv = l == 0.f ? 0.f : 1.f / l;  // 0: the row sees none of these keys
-      const int dim0 = 256 * kh + 128 * ch, q4 = lane & 3;
       // 16 rows x 64 dims at a time.  The load leaves a row's values with four
       // lanes, two of every eight each.
-#pragma unroll 1
-      for (int it = 0; it < 4; ++it) {
-        const int hh = it & 1, c0 = 64 * (it >> 1);
-        uint32_t v[32];
-        tmem_ld_16x64(o_addr + c0 + (static_cast<uint32_t>(16 * hh) << 16), v);
+      const bool wide = !direct || p.out_type == MLA_DTYPE_FP32, half_out = p.out_type == MLA_DTYPE_FP16;
+      auto load = [&](int it, uint32_t (&v)[32]) {
+        tmem_ld_16x64(o_addr + 64 * (it >> 1) + (static_cast<uint32_t>(16 * (it & 1)) << 16), v);
         tmem_wait_ld();
+      };
+      if (wide) {
+#pragma unroll 1
+        for (int it = 0; it < 4; ++it) {
+          uint32_t v[32];
+          load(it, v);
 #pragma unroll
-        for (int up = 0; up < 2; ++up) {
-          const int from = 16 * hh + 8 * up + (lane >> 2);  // lane that has this row's sum
-          const float iv = __shfl_sync(0xffffffffu, inv, from);
-          const int orow = row - lane + from;
-          const long long at = (first + orow) * kDv + dim0 + c0;
-          const bool store = orow < rows;
-          if (!direct || p.out_type == MLA_DTYPE_FP32) {
-            float* dst = (direct ? static_cast<float*>(p.out) : p.o_accum) + at + 2 * q4;
+          for (int up = 0; up < 2; ++up) {
+            const int from = 16 * (it & 1) + 8 * up + (lane >> 2);  // lane that has this row's sum
+            const float iv = __shfl_sync(0xffffffffu, inv, from);
+            const int orow = row - lane + from;
+            float* dst = (direct ? static_cast<float*>(p.out) : p.o_accum) + (first + orow) * kDv + dim0 +
+                         64 * (it >> 1) + 2 * (lane & 3);
 #pragma unroll
             for (int n = 0; n < 8; ++n) {
               const float a = __uint_as_float(v[4 * n + 2 * up]), b = __uint_as_float(v[4 * n + 2 * up + 1]);
-              if (store)
+              if (orow < rows)
                 *reinterpret_cast<float2*>(dst + 8 * n) =
                     iv == 0.f ? make_float2(0.f, 0.f) : make_float2(a * iv, b * iv);
             }
-            continue;
           }
-          uint32_t x[8];
+        }
+      } else {
+#pragma unroll 1
+        for (int it = 0; it < 4; ++it) {
+          uint32_t v[32];
+          load(it, v);
 #pragma unroll
-          for (int n = 0; n < 8; ++n) {
-            const float a = __uint_as_float(v[4 * n + 2 * up]) * iv, b = __uint_as_float(v[4 * n + 2 * up + 1]) * iv;
-            x[n] = iv == 0.f ? 0u : p.out_type == MLA_DTYPE_FP16 ? pack2<true>(a, b) : pack2<false>(a, b);
-          }
-          // word n of lane q4 -> word q4 of lane n, within four lanes and four
-          // words: each then holds whole 16-byte pieces, and a store of the warp
-          // covers 64 bytes of 8 rows
+          for (int up = 0; up < 2; ++up) {
+            const float iv = __shfl_sync(0xffffffffu, inv, 16 * (it & 1) + 8 * up + (lane >> 2));  // of that row's lane
+            uint32_t x[8];
 #pragma unroll
-          for (int g = 0; g < 8; g += 4) {
-            uint32_t* y = x + g;
-            {
-              const bool odd = q4 & 1;
-              const uint32_t s0 = odd ? y[0] : y[1], s1 = odd ? y[2] : y[3];
-              const uint32_t r0 = __shfl_xor_sync(0xffffffffu, s0, 1), r1 = __shfl_xor_sync(0xffffffffu, s1, 1);
-              if (odd) {
-                y[0] = r0;
-                y[2] = r1;
-              } else {
-                y[1] = r0;
-                y[3] = r1;
-              }
+            for (int n = 0; n < 8; ++n) {
+              const float a = __uint_as_float(v[4 * n + 2 * up]) * iv, b = __uint_as_float(v[4 * n + 2 * up + 1]) * iv;
+              x[n] = iv == 0.f ? 0u : half_out ? pack2<true>(a, b) : pack2<false>(a, b);
             }
-            {
-              const bool odd = q4 & 2;
-              const uint32_t s0 = odd ? y[0] : y[2], s1 = odd ? y[1] : y[3];
-              const uint32_t r0 = __shfl_xor_sync(0xffffffffu, s0, 2), r1 = __shfl_xor_sync(0xffffffffu, s1, 2);
-              if (odd) {
-                y[0] = r0;
-                y[1] = r1;
-              } else {
-                y[2] = r0;
-                y[3] = r1;
-              }
-            }
-            if (store)
-              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at + 8 * (g + q4)) =
-                  make_uint4(y[0], y[1], y[2], y[3]);
+            store16(x, it, up, first, rows);
           }
         }
       }
