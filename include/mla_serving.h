@@ -393,7 +393,7 @@ int mla_chunk_get_plan(const int32_t* d_cu_seqlens_q, const int32_t* d_cache_seq
  *   d_workspace   >= mla_chunk_workspace_bytes(num_parts), over FP8 records and
  *                 total_q * h_q times MLA_CHUNK_QUERY_BYTES.  There every further
  *                 MLA_CHUNK_PAGE_BYTES hold the values of a page, converted once
- *                 for requests of several 128-row blocks, in order; those that do
+ *                 for requests of three 128-row blocks and more, in order; those that do
  *                 not fit are converted by each block that reads them (slower, the
  *                 same results)
  *   d_out         [total_q, h_q, 512] of out_type (bf16, fp16 or fp32), d_lse fp32

@@ -375,8 +375,8 @@ def _chunk(q, kv, block_table, pl, softmax_scale, status, stream, out=None, lse=
         raise ValueError("the plan was made for another batch")
     plan, ws, st = pl.plan, pl.workspace, _p(status, _INT32, 1, dev, "status")
     if out is None and code == DTYPE_FP8_RECORD:
-        # room for values that are converted once for several row blocks (at most 0.5 GB)
-        ws = chunk_workspace(pl, min(batch * max_pages, 1 << 13) if total_q * h_q > 256 else 0)
+        # room for values that are converted once for three row blocks and more (at most 0.5 GB)
+        ws = chunk_workspace(pl, min(min(batch, total_q * h_q // 257) * max_pages, 1 << 13))
     plan_ptr, ws_ptr = _p(plan, _UINT8, 1, dev, "plan"), _p(ws, _UINT8, 1, dev, "workspace")
     queue = _q(stream, dev)
     if out is None:

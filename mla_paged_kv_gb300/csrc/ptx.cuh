@@ -434,7 +434,7 @@ __device__ __forceinline__ void umma2_f16_warp(uint32_t d_tmem, uint64_t a_desc,
       : "memory");
 }
 
-// Four of them that go on by A and B (16-byte units) in their descriptors: one
+// Four MMAs that go on by A and B (16-byte units) in their descriptors: one
 // election, and no instruction between them that the compiler places.
 template <int A, int B>
 __device__ __forceinline__ void umma2_f16_warp4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
@@ -527,8 +527,9 @@ __device__ __forceinline__ void mbar_arrive_expect_tx_remote_relaxed(uint32_t ba
                : "memory");
 }
 
-// The two above by the elected lane of a converged warp: operands that are the same
-// in all lanes stay in uniform registers (a loop of one lane's took 0.4 us a load).
+// The arrival above, with the bytes to expect, and a load onto that barrier, by the
+// elected lane of a converged warp: operands that are the same in all lanes stay in
+// uniform registers (a loop of one lane's took 0.4 us a load).
 __device__ __forceinline__ void tma_load_4d_pair_warp(void* dst, const CUtensorMap* map, uint32_t bar_cluster,
                                                       uint32_t bytes, int c0, int c1, int c2, int c3,
                                                       uint64_t policy) {
