@@ -354,13 +354,18 @@ int mla_cache_gather(const void* d_cache, int cache_dtype, int num_pages, const 
  * A query that sees no key gets out = 0, lse = -inf.  Rows of the outputs outside
  * every chunk are left as they were.  Softmax weights are rounded to the cache's
  * type (fp16 over FP8 records) for the product with the values and divided by the
- * sum of the unrounded ones; statistics and sums are fp32.  Over FP8 records scores
+ * sum of the unrounded ones; statistics and sums are fp32.  In fp16 the row's largest
+ * weight is held as 2^7 .. 2^15: weights below 2^-21 of it keep fewer bits, at worst
+ * (the largest at 2^7) off by 2^-32 of it, and those below 2^-32 of it are 0 beside a
+ * sum that has them.  Over FP8 records scores
  * are those of the products code x scale: each group's codes times the query's, a
  * query as two E4M3 numbers (exact down to 2^-9 of its largest latent element;
  * smaller elements are off by 2^-17 of that one), times the scale in fp32.  Values
  * are the products with 11 significant bits of scale and product, where a group's
  * scale is above 2^-13 of its key's largest (fewer below) and that one is within
- * 2^-61 .. 2^68.
+ * 2^-61 .. 2^68.  Values there are held without a power of two, 2^E, that largest scales
+ * within a factor of 256 have in common, and weights with it: what is said of the
+ * largest weight holds for the largest product with 2^E.
  *
  * num_parts: pairs of CTAs that share the work; mla_chunk_num_parts gives as many
  * as the device runs at once (>= 1, or a negative mla_status_t).  At most 1024. */

@@ -27,9 +27,10 @@
 //   * One warp issues  Q K^T (t+1)  P V (t):  the softmax of tile t+1 runs under
 //     P V (t) and Q K^T (t+2), that of t under Q K^T (t+1).
 //   * Four threads hold a row's 128 scores, 32 each, and share their maxima in
-//     shared memory.  The reference r is raised only when the maximum grows by
-//     more than 2^8 (then O is rescaled, rarely).  Weights are rounded to the
-//     cache's type for P V and divided by the sum of the unrounded ones.
+//     shared memory.  The reference r (2^7 below the maximum where weights are
+//     fp16) is raised only when the maximum grows by more than 2^8 (then O is
+//     rescaled, rarely).  Weights are rounded to the cache's type for P V and divided
+//     by the sum of the unrounded ones.
 //   * Rows of a page behind the unit's last key may hold anything: their scores
 //     are masked, and their values zeroed in shared memory (0 x NaN is not 0).
 //
@@ -140,7 +141,15 @@ constexpr int kLaneKeys = 8 / kConverters;  // keys of a page that a converting 
 constexpr int threads_of(bool fp8) { return 32 * (kWarpV + (fp8 ? kConverters : 1)); }
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 256;  // two buffers of 64 columns; four for the sums over FP8 records
-constexpr float kTau = 8.0f;
+constexpr float kTau = 8.0f;  // the reference is raised when the maximum is 2^kTau above the one it was last set by
+// Weights in fp16 are held 2^7 as large, 2^15 at most: what lies 2^21 below a row's
+// largest is still a normal number, and lost are those below 2^-32 of it.  (With the
+// largest near 1 they were lost below 2^-25, while the sum l kept them: the output of
+// 131072 keys that lie 2^25 below one of values near 0 was 0.  Raising the reference at
+// 2^4 would leave room for 2^11: scores with a deviation of 4, 64 requests x 4 tokens x
+// 128 heads, 155 us instead of 152, FP8 records 255 instead of 250.)
+template <bool kF16>
+constexpr float kLift = kF16 ? 7.0f : 0.0f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -867,6 +876,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
         if (orow < rows) *reinterpret_cast<uint4*>(dst + 8 * g) = make_uint4(y[0], y[1], y[2], y[3]);
       }
     };
+    constexpr float lift = kLift<kHalf || kFp8>;
     bool more = enter();
     while (more) {
       float ref = -INFINITY, l = 0.f;
@@ -961,7 +971,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
         ok = !named_bar_or(row_bar, 128, !ok);  // (a warp that gave up waiting takes the others along)
         if (!ok) break;
         const float mt = fmaf(fmaxf(fmaxf(buf[0], buf[kCtaRows]), fmaxf(buf[2 * kCtaRows], buf[3 * kCtaRows])), c, add);
-        const float r_new = mt > ref + kTau ? mt : ref;
+        const float r_new = mt > ref + (kTau + lift) ? mt - lift : ref;
         const float alpha = r_new == ref ? 1.f : ex2(ref - r_new);
         ref = r_new;
         const float mref = ref == -INFINITY ? 0.f : ref;
@@ -1073,7 +1083,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
         }
       }
       if (part == 0 && row < rows)
-        (direct ? p.lse : p.lse_accum)[first + row] = l == 0.f ? -INFINITY : (ref + __log2f(l)) * kLn2;
+        (direct ? p.lse : p.lse_accum)[first + row] =
+            l == 0.f ? -INFINITY : (ref + lift + __log2f(l * two_to(-static_cast<int>(lift)))) * kLn2;
       if (tid == 0) MLA_TRACE(9, tn);
       // O has been read: the next unit's first P V waits for this warp's P
       tc_fence_before();
