@@ -20,6 +20,7 @@ a cached context as rows, to be expanded into heads for ``prompt_attention``.
 from __future__ import annotations
 
 import ctypes
+import math
 
 import torch
 
@@ -110,16 +111,35 @@ def _heads(t, dtype, tokens, dim, dev, name):
 
 
 def _apart(a, b, tokens, dim):
-    """Whether two such tensors share no element: one behind the other, or side by side in rows (or heads) of equal
-    strides, as the parts of a packed projection are."""
+    """Whether two such tensors share no element.  (Exact for equal strides; others have to lie one behind the other, or
+    side by side in what their strides are multiples of.)"""
     if a[0] >= b[4] or b[0] >= a[4]:
         return True
-    step = (b[0] - a[0]) // 2
-    for stride, one, other in ((a[1] if a[1] == b[1] else 0, (a[3] - 1) * a[2] + dim, (b[3] - 1) * b[2] + dim),
-                               (a[2] if a[1:3] == b[1:3] else 0, dim, dim)):
-        if stride > 0 and step % stride >= one and step % stride + other <= stride:
+    step, ts, hs = (b[0] - a[0]) // 2, a[1], a[2]
+    # side by side in every token's rows, as the parts of a packed projection are
+    if ts == b[1] > 0 and step % ts >= (a[3] - 1) * hs + dim and step % ts + (b[3] - 1) * b[2] + dim <= ts:
+        return True
+    # .. in what all strides repeat, as parts of the same heads are
+    cell = math.gcd(ts, hs, b[1], b[2])
+    if cell and dim <= step % cell <= cell - dim:
+        return True
+    if b[1:3] != (ts, hs) or ts <= 0 or hs <= 0:
+        return False
+    # .. or in rows that hold something else behind the heads (what follows would find it too: 0.3 ms for 128 heads)
+    for by, n, m in ((step, a[3], b[3]), (-step, b[3], a[3])):
+        head, place = divmod(by % ts, hs)
+        if dim <= place <= hs - dim and max(n, head + m) * hs <= ts:
             return True
-    return False
+    # every distance between a token and head of a and one of b, step + i ts + n hs: the fewer of them one by one, the
+    # two nearest of the others
+    i, n = (ts, 1 - tokens, tokens - 1), (hs, 1 - a[3], b[3] - 1)
+    few, many = (i, n) if 2 * tokens < a[3] + b[3] else (n, i)
+    for k in range(few[1], few[2] + 1):
+        at = step + k * few[0]
+        j = min(max(-at // many[0], many[1]), many[2])
+        if abs(at + j * many[0]) < dim or (j < many[2] and abs(at + (j + 1) * many[0]) < dim):
+            return False
+    return True
 
 
 def _output(out, tokens, dim, others, same):
