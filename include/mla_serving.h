@@ -307,7 +307,9 @@ int mla_rope_table(const double* h_freq, int dim, double magnitude, long long fi
  * d_cache_seqlens are NULL.
  *   d_x, d_k   [total_tokens, heads, dim] of `dtype` (MLA_DTYPE_BF16 or _FP16);
  *              strides in elements, multiples of 8, the last dimension contiguous
- *   d_out, d_k_out  the same shapes, strides of their own; may be d_x and d_k
+ *              (0: one read for all)
+ *   d_out, d_k_out  the same shapes, strides of their own, at least dim (no element
+ *              may be written twice); may be d_x and d_k
  *              themselves with the same strides (dims that are not changed are
  *              then not moved), else must share no element with any input
  *   dim        a multiple of 8, at most 1024; rope_dim a multiple of 16, at most

@@ -734,6 +734,12 @@ int mla_rope_heads(const void* d_x, long long x_token_stride, long long x_head_s
   int per_lane = 0;
   long long blocks = 0;
   if (!rope_heads_layout(&p, passes, &per_lane, &blocks)) return MLA_ERR_UNSUPPORTED;
+  // an output's tokens, and heads, are at least a head apart (inputs may be read with a stride of 0)
+  auto stacked = [&](int n, long long ts, long long hs) {
+    return (n > 0 && total_tokens > 1 && ts < dim) || (n > 1 && hs < dim);
+  };
+  if (stacked(heads, out_token_stride, out_head_stride) || stacked(k_heads, k_out_token_stride, k_out_head_stride))
+    return MLA_ERR_INVALID_ARG;
   int sms = 0;
   const int rc = device_ready(&sms);
   if (rc != MLA_OK || total_tokens == 0) return rc;

@@ -10,6 +10,7 @@ import torch
 
 import mla_paged_kv_gb300 as mla
 from mla_paged_kv_gb300.chunks import _apart, _output
+from tests.test_chunks_abi import HEADS, INVALID
 
 DIM = 8
 
@@ -95,3 +96,11 @@ def test_layouts_of_projections_are_taken():
     assert not refused(wide[:1, :, :64], wide[:1, :, 64:]) and not refused(wide[:2, :, :64], wide[3:, :, :64])
     one = buf(5, 1, 64).expand(5, 3, 64)  # a head that is read for all
     assert not refused(one, buf(5, 3, 64))
+
+
+@pytest.mark.parametrize("change", [dict(ot=0), dict(oh=0), dict(oh=56), dict(kot=0), dict(koh=0), dict(koh=32),
+                                    dict(ot=32, oh=4096)])
+def test_the_entry_point_refuses_outputs_on_top_of_each_other(change):
+    """(Inputs may be: a stride of 0 reads one head for all.)"""
+    args = {**HEADS, **change}
+    assert mla.load_library().mla_rope_heads(*args.values()) == INVALID
