@@ -396,7 +396,10 @@ int mla_chunk_get_plan(const int32_t* d_cu_seqlens_q, const int32_t* d_cache_seq
  *                 num_parts
  *   d_cu_seqlens_q, d_cache_seqlens  compared with the plan's on the device:
  *                 MLA_ERR_STALE_PLAN where one is another than the plan was made
- *                 for; the results are those of the plan.  NULL: not compared
+ *                 for; the results are those of the plan.  MLA_ERR_BAD_INDEX
+ *                 where they are but were out of range then: the plan is empty
+ *                 and nothing is written.  NULL: not compared, and such a plan
+ *                 is reported by mla_chunk_get_plan alone
  *   d_workspace   >= mla_chunk_workspace_bytes(num_parts), over FP8 records and
  *                 total_q * h_q times MLA_CHUNK_QUERY_BYTES.  There every further
  *                 MLA_CHUNK_PAGE_BYTES hold the values of a page, converted once

@@ -433,7 +433,8 @@ def mla_chunk_attention_fwd(q, kv, block_table, pl, out, lse, status, softmax_sc
                             cache_seqlens=None, stream=None):
     """q [total_q, h_q, 576] and kv [pages, 64, 576], both bf16 or both fp16, or a bf16 q over FP8 records (uint8
     [pages, 64, 656]); pl a ChunkPlan; out [total_q, h_q, 512] bf16, fp16 or fp32, lse fp32 [total_q, h_q].  Offsets
-    and lengths that are given are compared with the plan's: others are MLA_ERR_STALE_PLAN in status."""
+    and lengths that are given are compared with the plan's: others are MLA_ERR_STALE_PLAN in status, the same but out of
+    range MLA_ERR_BAD_INDEX."""
     _chunk(q, kv, block_table, pl, softmax_scale, status, stream, out, lse, None, cu_seqlens_q, cache_seqlens)
 
 
@@ -471,7 +472,8 @@ def chunk_attention(q, kv, block_table, cache_seqlens, cu_seqlens_q, causal=True
     to 1 / sqrt(576), as decode's does: a model with prompt heads of 192 dims gives 192 ** -0.5.
 
     A plan holds the offsets and lengths it was made for.  With pl they are compared with cu_seqlens_q and
-    cache_seqlens on the device, and a plan of others is MLA_ERR_STALE_PLAN."""
+    cache_seqlens on the device: a plan of others is MLA_ERR_STALE_PLAN, one that is empty because they are out of range
+    MLA_ERR_BAD_INDEX (outputs are then not written)."""
     st = _status(status, q)
     cu, lens = cu_seqlens_q, cache_seqlens
     if pl is None:  # a plan made here is that of the offsets

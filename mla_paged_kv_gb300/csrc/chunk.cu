@@ -277,9 +277,11 @@ __device__ __forceinline__ int page_window(const ChunkParams& p, const Unit& uni
   return -1;
 }
 
-// Whether the plan is that of the caller's offsets and lengths; the call's
-// results are those of the plan either way.
+// Whether the plan is that of the caller's offsets and lengths, and these are in
+// range; the call's results are those of the plan either way.
 __device__ __forceinline__ void check_plan(const ChunkParams& p) {
+  if ((p.cu != nullptr || p.lens != nullptr) && blockIdx.x == 0 && (threadIdx.x & 31) == 0 && p.head[kHeadBroken] != 0)
+    report(p.status, MLA_ERR_BAD_INDEX);
   for (int i = blockIdx.x * 32 + (threadIdx.x & 31); i <= p.batch; i += gridDim.x * 32)
     if ((p.cu != nullptr && p.made[i] != p.cu[i]) ||
         (p.lens != nullptr && i < p.batch && p.made[p.batch + 1 + i] != p.lens[i]))
@@ -1459,6 +1461,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPla
       p.head[kHeadWhole] = 0;
       p.head[kHeadCausal] = p.causal;
       p.head[kHeadFix + v] = 0;
+      p.head[kHeadBroken] = 1;
     }
     for (int b = tid; b <= p.batch; b += kPlanThreads) p.conv[b] = 0;
     for (int i = tid; i < p.parts * MLA_SCHED_INTS; i += kPlanThreads) p.schedule[v].sched[i] = 0;
@@ -1489,6 +1492,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkPla
     p.head[kHeadWhole] = units;
     p.head[kHeadCausal] = p.causal;
     p.head[kHeadFix + v] = 0;
+    p.head[kHeadBroken] = 0;
   }
   __syncthreads();
   for (int u = tid; u < units; u += kPlanThreads) {

@@ -159,7 +159,8 @@ constexpr int kMaxChunkKeys = 1 << 24;  // keys of a request
 constexpr int kFixedCost = 6;            // a unit's Q load and epilogue, in half tiles of 128 keys
 constexpr int kChunkUnitInts = 12;
 constexpr int kConvertUnits = 3;         // units from which a request's FP8 pages are converted once for all
-enum : int { kHeadWhole = 0, kHeadCausal = 1, kHeadFix = 2 };  // header: units, causal, units for the combine (2)
+// header: units, causal, units for the combine (2), whether an offset or length was out of range (no units then)
+enum : int { kHeadWhole = 0, kHeadCausal = 1, kHeadFix = 2, kHeadBroken = 4 };
 struct ChunkPlanLayout {
   int max_units;
   size_t units, first, conv, made, bytes;
