@@ -435,11 +435,15 @@ def mla_chunk_attention_fwd(q, kv, block_table, pl, out, lse, status, softmax_sc
     [pages, 64, 656]); pl a ChunkPlan; out [total_q, h_q, 512] bf16, fp16 or fp32, lse fp32 [total_q, h_q].  Offsets
     and lengths that are given are compared with the plan's: others are MLA_ERR_STALE_PLAN in status, the same but out of
     range MLA_ERR_BAD_INDEX."""
+    if out is None or lse is None:
+        raise ValueError("out and lse are needed")
     _chunk(q, kv, block_table, pl, softmax_scale, status, stream, out, lse, None, cu_seqlens_q, cache_seqlens)
 
 
 def mla_test_chunk_timeout(q, kv, block_table, pl, out, lse, status, softmax_scale=1.0 / 24.0, stream=None):
     """Test hook: mla_chunk_attention_fwd whose first K stage is never loaded (status: MLA_ERR_TIMEOUT)."""
+    if out is None or lse is None:
+        raise ValueError("out and lse are needed")
     _chunk(q, kv, block_table, pl, softmax_scale, status, stream, out, lse, hook=True)
 
 
