@@ -286,8 +286,10 @@ int mla_rope_frequencies(int dim, double base, int scaling, double factor, doubl
  *   d_cos_sin[p] = magnitude (cos p f_0 .. cos p f_(dim/2-1), sin p f_0 ..)
  * fp32 [positions, dim], 16-byte aligned, as mla_cache_append (dim 64) and
  * mla_rope_heads read it.  h_freq in host memory, 0 <= f <= 2^10, read before the
- * call returns.  Angles are exact to 2^-52 of themselves at any position below
- * 2^31 (first_pos + positions is at most that), and values to a few ulp. */
+ * call returns.  Angles are off by at most 2^-52 of themselves and 2^-64 turns a
+ * position (a frequency's turns are cut there), at any position below 2^31
+ * (first_pos + positions is at most that); values are within 2^-21 of the cosine
+ * and sine of that angle, and next to their zeros within 2^-52 of the magnitude. */
 int mla_rope_table(const double* h_freq, int dim, double magnitude, long long first_pos, int positions,
                    float* d_cos_sin, mla_stream_t stream);
 

@@ -47,14 +47,15 @@ __device__ __forceinline__ float2 cos_pi(float2 x) {
 
 // cos_sin[p] = magnitude * (cos(p f_0) .. , sin(p f_0) ..).
 //
-// Angles in whole turns of 2^64 steps: step_i = round(f_i / 2 pi * 2^64), and
-// p * step_i modulo 2^64 is the angle modulo a turn with no rounding at all: what
-// is left of the frequency's own rounding (2^-53 of it) is below 2^-31 turns at
-// position 2^24, where an fp32 angle would be off by a radian.  The nearest
-// quarter turn comes off in integers too; what is left, at most an eighth of a turn
-// to either side, is converted high and low word apart, so that values next to zero
-// keep their leading bits, and the Taylor series of sin(pi x) and cos(pi x) to x^9
-// and x^10 leave 2^-29 of it there.
+// Angles in whole turns of 2^64 steps: step_i is the fraction of f_i / 2 pi, in 64-bit
+// arithmetic (off by 2^-52 of it) and cut behind 2^-64, and p * step_i modulo 2^64 is
+// the angle modulo a turn with no rounding.  It is off by 2^-52 of the whole angle and
+// 2^-64 turns a position: below 2^-30 turns at position 2^24 for f = 1, where an fp32
+// angle would be off by a radian, and below 2^-23 at the last position, 2^31.  The
+// nearest quarter turn comes off in integers too; what is left, at most an eighth of a
+// turn to either side, is converted high and low word apart, so that values next to
+// zero keep their leading bits (to 2^-52), and the Taylor series of sin(pi x) and
+// cos(pi x) to x^9 and x^10 leave 2^-28 of it there.
 // A thread keeps four pairs, two at a time in packed arithmetic, and steps through
 // positions, so that an angle is one addition.  Bound by the launch for few positions
 // (4096 x 64: 4.2 us), for many by issue, with half of it left to the writes (163840 x
