@@ -35,17 +35,20 @@
 //     are masked, and their values zeroed in shared memory (0 x NaN is not 0).
 //
 // Bound by the tensor pipe over 16-bit caches: busy 92% of the cycles of 3 chunks of
-// up to 300 tokens x 128 heads over 8000 keys (592 us, 1886 TFLOP/s), 80% of 64
-// requests' up to 6 drafts over up to 4096 keys (145 us; a unit's output, 2 us, and
-// the first loads, 5 us, are not under anything).  Both products feed it from shared
+// up to 300 tokens x 128 heads over 8000 keys (580 us, 1930 TFLOP/s), 80% of 64
+// requests' up to 6 drafts over up to 4096 keys (148 us; a unit's output, 2 us, and
+// the first scores, 6 us, are not under anything).  Both products feed it from shared
 // memory, whose 128 bytes a cycle Q K^T takes to the full (4 KB an MMA of 32 cycles),
-// so that loads and weights stored at the same time cost it cycles: 1.45 us a tile
+// so that loads and weights stored at the same time cost it cycles: 1.35 us a tile
 // where the MMAs alone are 1.15.
 //
-// FP8 records: below.  1.9 us a tile, bound by the softmax threads' chain (five sums
+// FP8 records: below.  1.8 us a tile, bound by the softmax threads' chain (five sums
 // of a score from TMEM and their scales from shared memory, 0.2 us each); tiles whose
-// values no other unit shares, 2.4 us, by their conversion.  43 requests, 3 chunks of
-// up to 400 tokens among single ones, 16 heads over up to 3400 keys: 112 us.
+// values no other unit shares, 2.4 us among others and 2.8 where all are such, by
+// their conversion.  43 requests, 3 chunks of up to 400 tokens among single ones, 16
+// heads over up to 3400 keys: 112 us, of which the slowest pair has 100 (first scores
+// 5, 41 tiles a pair 74, changes of units 9, the last output 4, pairs that end 7
+// apart) and the kernels before and behind it the rest.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -1116,8 +1119,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
 // of requests of kConvertUnits units and more that fit, rows behind the last key, and
 // of pages outside the pool (reported), as zeros.  A warp a query, a block a page at
 // a time.  Every unit that reads a page would convert it again, for 2.4 us a tile
-// instead of 1.9: with no room for pages the mixed batch above takes 142 us, 3 chunks
-// x 128 heads over 8000 keys 1080 instead of 740; from 2, 3 or 5 units on is the same.
+// instead of 1.8: with no room for pages the mixed batch above takes 142 us, 3 chunks
+// x 128 heads over 8000 keys 1080 instead of 740.  Why from three units on: 64 requests
+// x 2 tokens x 128 heads (two units) over 4096 keys take 148 us, 166 with their pages
+// converted before; x 3 tokens 199, and 213 without; 200 x 2 over 1000 keys 145 and 162.
 __global__ void __launch_bounds__(256)
     chunk_convert_kernel(const ChunkParams p, const uint16_t* __restrict__ q, uint16_t* __restrict__ pages) {
   pdl_wait_prior_grid();
